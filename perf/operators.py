@@ -138,7 +138,8 @@ def _codes(kind, x):
         return x.to(F16), None
     x = x.float().unflatten(-1, (-1, 32))
     hi, lo = x.amax(-1), x.amin(-1)
-    d = torch.maximum(hi, -lo) / (127.0 if kind == "Q8_0" else 8.0)
+    # (A tensor divisor: torch multiplies by the reciprocal of a number.)
+    d = torch.maximum(hi, -lo) / torch.full((), 127.0 if kind == "Q8_0" else 8.0, device=x.device)
     h = d.to(F16).clamp(max=65504.0)
     up = (h.float() < d) & (h < 65504.0)
     h = (h.view(torch.int16) + up.to(torch.int16)).view(F16)  # rounded up: no code leaves its range
