@@ -10,7 +10,9 @@ it raises instead of falling back to anything else.
 
 ``gemv``, ``gemm``, ``matmul``, ``moe`` and ``dequant`` are conveniences that
 allocate their outputs (and the expert workspace) with torch and call the
-``qmm_*`` functions.
+``qmm_*`` functions; so are ``rope``, ``kv_write``, ``kv_append``, ``kv_read``
+and ``attn_decode``, the operators between a layer's projections, over a paged
+key/value cache of ``kv_pages`` tensors.
 """
 from __future__ import annotations
 
@@ -46,6 +48,7 @@ def load_library(path: str = LIBRARY) -> ctypes.CDLL:
                            "(hipcc --offload-arch=gfx950) first")
     lib = ctypes.CDLL(path)
     P, I, I64, SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
+    F, F64 = ctypes.c_float, ctypes.c_double
     sig = {
         "qmm_gemv": (I, [I, P, P, P, I64, I64]),
         "qmm_gemv_ex": (I, [I, P, P, I, P, I64, I64, I64, P]),
@@ -68,6 +71,16 @@ def load_library(path: str = LIBRARY) -> ctypes.CDLL:
         "qmm_gemv_i8_noalloc": (I, [I, P, P, I, P, I64, I64, I64, P]),
         "qmm_moe_packed": (I, [I, P, I64, P, I64, P, I, I, P, I64, I64, I64, P, SZ, P]),
         "qmm_gemv_i8_workspace_bytes": (SZ, [I64, I64]),
+        "qmm_kv_page_bytes": (I64, [I, I64, I64, I64]),
+        "qmm_rope_freqs": (I, [P, P, I64, F64, P, F64, I64, F64, F64]),
+        "qmm_rope": (I, [P, I64, I, F, P, P, I, I64, P, I, I64, I64, I64, I64, P]),
+        "qmm_kv_write": (I, [I, I, P, P, I64, I64, I64, I64, P, I64, P, I64, I, P, I64, P]),
+        "qmm_kv_append": (I, [P, I64, I, F, P, P, I64, I64, P, I, I64, I, I, P, P, I64, I64, I64, I64, P, I64, P,
+                              I64, I, P, I64, P]),
+        "qmm_kv_read": (I, [I, I, P, P, I64, I64, I64, I64, P, I64, P, P, I, P]),
+        "qmm_attn_decode": (I, [I, I, P, P, I64, I64, I64, I64, P, I, I64, I64, P, I64, P, I64, F, I64, P, P, P, SZ,
+                                P]),
+        "qmm_attn_decode_workspace_bytes": (SZ, [I64, I64, I64, I64]),
         "qmm_row_bytes": (I64, [I, I64]),
         "qmm_block_geometry": (I, [I, ctypes.POINTER(I), ctypes.POINTER(I)]),
         "qmm_kind_from_name": (I, [ctypes.c_char_p]),
@@ -546,4 +559,257 @@ def dequant(kind, W, n_elems: int | None = None, stream=None):
     n = (W.numel() // bb) * be if n_elems is None else n_elems
     out = torch.empty(n, dtype=torch.float32, device=W.device)
     qmm_dequant(kind, W, out, n, stream)
+    return out
+
+
+# ---------------------------------------------------------------------------
+# Rotary positions, the paged key/value cache and attention over it.  The
+# functions mirror the C entry points but take their sizes from the tensors:
+# rows are [T, heads, head_dim] with packed heads and any row stride (slices of
+# one projection's output), pages are uint8 [n_pages, page_bytes].
+# ---------------------------------------------------------------------------
+CACHE_KINDS = {"F16": 1, "Q8_0": 8, "Q4_0": 2}
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+
+
+def cache_kind_id(kind) -> int:
+    if isinstance(kind, str):
+        if kind not in CACHE_KINDS:
+            raise QmmError(2, f"cache kind {kind} is none of {', '.join(CACHE_KINDS)}")
+        return CACHE_KINDS[kind]
+    return int(kind)
+
+
+def _layout_id(layout) -> int:
+    if isinstance(layout, str):
+        if layout not in ROPE_LAYOUTS:
+            raise QmmError(5, f"rope layout {layout} is none of {', '.join(ROPE_LAYOUTS)}")
+        return ROPE_LAYOUTS[layout]
+    return int(layout)
+
+
+def _rows_arg(x, what: str) -> tuple[int, int, int, int]:
+    """T, heads, head_dim and row stride of [T, heads, head_dim] rows."""
+    if x.dim() != 3:
+        raise ValueError(f"{what} must be [rows, heads, head_dim], got {tuple(x.shape)}")
+    T, H, D = x.shape
+    st, sh, sd = x.stride()
+    if (D > 1 and sd != 1) or (H > 1 and sh != D):
+        raise ValueError(f"the heads of a row of {what} must be packed, got strides {x.stride()}")
+    return T, H, D, st if T > 1 else H * D
+
+
+def _ints(t, count: int, what: str):
+    import torch
+    if t.dtype != torch.int32:
+        raise TypeError(f"{what} must be int32, got {t.dtype}")
+    if not t.is_contiguous() or t.numel() != count:
+        raise ValueError(f"{what} must hold {count} contiguous elements, got {tuple(t.shape)}")
+
+
+def _pages_arg(pages, kind: int, page_size: int, n_kv: int, head_dim: int, what: str) -> int:
+    """Number of pages of a page tensor."""
+    pb = int(load_library().qmm_kv_page_bytes(kind, page_size, n_kv, head_dim))
+    if pages.element_size() != 1 or pages.dim() != 2 or not pages.is_contiguous():
+        raise TypeError(f"{what} must be a contiguous byte tensor [n_pages, page_bytes]")
+    if pb > 0 and pages.shape[1] != pb:
+        raise ValueError(f"{what} has pages of {pages.shape[1]} bytes, page_size={page_size}, n_kv={n_kv} and "
+                         f"head_dim={head_dim} need {pb}")
+    return pages.shape[0]
+
+
+class _on:
+    """Makes the operands' device the current one for the call, refusing
+    operands on different devices or on the host, and gives the stream (by
+    default that device's current one)."""
+
+    def __init__(self, *tensors):
+        self.index = tensors[0].device.index
+        for t in tensors:
+            if t is not None and (t.device.type != "cuda" or t.device.index != self.index):
+                raise ValueError(f"operands must be on one GPU, got {t.device} with {tensors[0].device}")
+
+    def __enter__(self):
+        import torch
+        self.before = torch.cuda.current_device()
+        if self.before != self.index:
+            torch.cuda.set_device(self.index)
+        return self
+
+    def stream(self, stream) -> int:
+        return _stream(stream)
+
+    def __exit__(self, *exc):
+        if self.before != self.index:
+            import torch
+            torch.cuda.set_device(self.before)
+
+
+def kv_page_bytes(kind, page_size: int, n_kv: int, head_dim: int) -> int:
+    return int(load_library().qmm_kv_page_bytes(cache_kind_id(kind), page_size, n_kv, head_dim))
+
+
+def kv_pages(kind, n_pages: int, page_size: int, n_kv: int, head_dim: int, device="cuda"):
+    """An empty page tensor, uint8 [n_pages, page_bytes] (not initialized)."""
+    import torch
+    pb = kv_page_bytes(kind, page_size, n_kv, head_dim)
+    if pb < 0:
+        raise QmmError(5, f"no pages of kind {kind}, page_size={page_size}, n_kv={n_kv}, head_dim={head_dim}")
+    return torch.empty((n_pages, pb), dtype=torch.uint8, device=device)
+
+
+def rope_freqs(n_rot: int, base: float = 10000.0, factors=None, factor: float = 1.0, orig_ctx: int = 0,
+               beta_fast: float = 32.0, beta_slow: float = 1.0, device="cuda"):
+    """(freqs, mscale): f64 radians per position of the n_rot / 2 pairs on the
+    device and the factor on the rotated elements.  factors: per-pair divisors
+    (a sequence or f32 tensor of n_rot / 2)."""
+    import torch
+    out = torch.empty(max(n_rot // 2, 1), dtype=torch.float64)
+    m = ctypes.c_float(1.0)
+    fac = None
+    if factors is not None:
+        fac = torch.as_tensor(factors, dtype=torch.float32).cpu().contiguous()
+        if fac.numel() != n_rot // 2:
+            raise ValueError(f"factors holds {fac.numel()} elements, needs {n_rot // 2}")
+    _check(load_library().qmm_rope_freqs(out.data_ptr(), ctypes.byref(m), n_rot, base,
+                                         0 if fac is None else fac.data_ptr(), factor, orig_ctx, beta_fast, beta_slow))
+    return out.to(device), float(m.value)
+
+
+def _freqs_arg(freqs) -> int:
+    import torch
+    if freqs.dtype != torch.float64 or not freqs.is_contiguous() or freqs.dim() != 1:
+        raise TypeError(f"freqs must be a contiguous float64 vector, got {freqs.dtype} {tuple(freqs.shape)}")
+    return 2 * freqs.shape[0]
+
+
+def rope(x, positions, freqs, layout="half", mscale: float = 1.0, out=None, out_dtype=None, stream=None):
+    """x [T, H, head_dim] with the first 2 * len(freqs) elements of each head
+    turned by positions [T] int32; out may be x."""
+    import torch
+    T, H, D, xs = _rows_arg(x, "x")
+    _ints(positions, T, "positions")
+    if out is None:
+        out = torch.empty((T, H, D), dtype=out_dtype or x.dtype, device=x.device)
+    To, Ho, Do, ys = _rows_arg(out, "out")
+    if (To, Ho, Do) != (T, H, D):
+        raise ValueError(f"out is {tuple(out.shape)}, x is {tuple(x.shape)}")
+    with _on(x, positions, freqs, out) as dev:
+        _check(load_library().qmm_rope(freqs.data_ptr(), _freqs_arg(freqs), _layout_id(layout), mscale,
+                                       positions.data_ptr(), x.data_ptr(), _dtype_code(x), xs, out.data_ptr(),
+                                       _dtype_code(out), ys, T, H, D, dev.stream(stream)))
+    return out
+
+
+def _kv_args(k, v, slots):
+    T, n_kv, D, ks = _rows_arg(k, "k")
+    Tv, Hv, Dv, vs = _rows_arg(v, "v")
+    if (Tv, Hv, Dv) != (T, n_kv, D):
+        raise ValueError(f"k is {tuple(k.shape)}, v is {tuple(v.shape)}")
+    if k.dtype != v.dtype:
+        raise TypeError(f"k is {k.dtype}, v is {v.dtype}")
+    _ints(slots, T, "slots")
+    return T, n_kv, D, ks, vs
+
+
+def _cache_args(k_pages, v_pages, k_kind, v_kind, page_size: int, n_kv: int, D: int):
+    kk, vk = cache_kind_id(k_kind), cache_kind_id(v_kind)
+    n = _pages_arg(k_pages, kk, page_size, n_kv, D, "k_pages")
+    if _pages_arg(v_pages, vk, page_size, n_kv, D, "v_pages") != n:
+        raise ValueError(f"k_pages holds {n} pages, v_pages {v_pages.shape[0]}")
+    return kk, vk, k_pages.data_ptr(), v_pages.data_ptr(), n, page_size, n_kv, D
+
+
+def kv_write(k, v, slots, k_pages, v_pages, k_kind, v_kind, page_size: int, stream=None):
+    """Writes the tokens' keys and values [T, n_kv, head_dim] to slots [T] int32."""
+    T, n_kv, D, ks, vs = _kv_args(k, v, slots)
+    cache = _cache_args(k_pages, v_pages, k_kind, v_kind, page_size, n_kv, D)
+    with _on(k, v, slots, k_pages, v_pages) as dev:
+        _check(load_library().qmm_kv_write(*cache, k.data_ptr(), ks, v.data_ptr(), vs, _dtype_code(k),
+                                           slots.data_ptr(), T, dev.stream(stream)))
+
+
+def kv_append(q, k, v, positions, slots, k_pages, v_pages, k_kind, v_kind, page_size: int, freqs, layout="half",
+              mscale: float = 1.0, out=None, out_dtype=None, stream=None):
+    """Rotates q [T, n_q, head_dim] (returned; out may be q) and k, and writes
+    k and v to their slots, in one launch."""
+    import torch
+    T, n_kv, D, ks, vs = _kv_args(k, v, slots)
+    Tq, n_q, Dq, qs = _rows_arg(q, "q")
+    if (Tq, Dq) != (T, D):
+        raise ValueError(f"q is {tuple(q.shape)}, k is {tuple(k.shape)}")
+    if q.dtype != k.dtype:
+        raise TypeError(f"q is {q.dtype}, k is {k.dtype}")
+    _ints(positions, T, "positions")
+    cache = _cache_args(k_pages, v_pages, k_kind, v_kind, page_size, n_kv, D)
+    if out is None:
+        out = torch.empty((T, n_q, D), dtype=out_dtype or q.dtype, device=q.device)
+    To, Ho, Do, os_ = _rows_arg(out, "out")
+    if (To, Ho, Do) != (T, n_q, D):
+        raise ValueError(f"out is {tuple(out.shape)}, q is {tuple(q.shape)}")
+    with _on(q, k, v, positions, slots, k_pages, v_pages, freqs, out) as dev:
+        _check(load_library().qmm_kv_append(freqs.data_ptr(), _freqs_arg(freqs), _layout_id(layout), mscale,
+                                            positions.data_ptr(), q.data_ptr(), qs, n_q, out.data_ptr(),
+                                            _dtype_code(out), os_, *cache, k.data_ptr(), ks, v.data_ptr(), vs,
+                                            _dtype_code(k), slots.data_ptr(), T, dev.stream(stream)))
+    return out
+
+
+def kv_read(slots, k_pages, v_pages, k_kind, v_kind, page_size: int, n_kv: int, head_dim: int, dtype=None, k_out=None,
+            v_out=None, stream=None):
+    """(k, v) [T, n_kv, head_dim] of the tokens at slots [T] int32, f16 by
+    default; zeros for skipped slots (outside the cache)."""
+    import torch
+    T = slots.numel()
+    _ints(slots, T, "slots")
+    shape = (T, n_kv, head_dim)
+    if (k_out is None) != (v_out is None):
+        raise ValueError("k_out and v_out go together")
+    if k_out is None:
+        k_out, v_out = torch.empty((2, *shape), dtype=dtype or torch.float16, device=slots.device).unbind(0)
+    for t in (k_out, v_out):
+        if tuple(t.shape) != shape or not t.is_contiguous() or t.dtype != k_out.dtype:
+            raise ValueError(f"k_out and v_out must be contiguous {shape} of one type")
+    cache = _cache_args(k_pages, v_pages, k_kind, v_kind, page_size, n_kv, head_dim)
+    with _on(slots, k_pages, v_pages, k_out, v_out) as dev:
+        _check(load_library().qmm_kv_read(*cache, slots.data_ptr(), T, k_out.data_ptr(), v_out.data_ptr(),
+                                          _dtype_code(k_out), dev.stream(stream)))
+    return k_out, v_out
+
+
+def qmm_attn_decode_workspace_bytes(B: int, n_q: int, n_kv: int, head_dim: int) -> int:
+    return int(load_library().qmm_attn_decode_workspace_bytes(B, n_q, n_kv, head_dim))
+
+
+def attn_decode(q, k_pages, v_pages, block_table, seq_lens, k_kind, v_kind, page_size: int, n_kv: int, scale=None,
+                window: int = 0, sinks=None, out=None, stream=None, workspace=None):
+    """out [B, n_q, head_dim]: attention of one new token per sequence, q [B,
+    n_q, head_dim], over the pages named by block_table [B, max_pages] int32 for
+    seq_lens [B] int32 tokens.  scale defaults to head_dim^-0.5; window > 0
+    keeps the last `window` tokens; sinks [n_q] f32 adds a logit without a
+    value per head."""
+    import torch
+    B, n_q, D, qs = _rows_arg(q, "q")
+    _ints(seq_lens, B, "seq_lens")
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError(f"block_table must be [{B}, max_pages], got {tuple(block_table.shape)}")
+    max_pages = block_table.shape[1]
+    _ints(block_table, B * max_pages, "block_table")
+    if sinks is not None and (sinks.dtype != torch.float32 or not sinks.is_contiguous() or sinks.numel() != n_q):
+        raise ValueError(f"sinks must be {n_q} contiguous float32 values")
+    cache = _cache_args(k_pages, v_pages, k_kind, v_kind, page_size, n_kv, D)
+    if out is None:
+        out = torch.empty((B, n_q, D), dtype=q.dtype, device=q.device)
+    elif tuple(out.shape) != (B, n_q, D) or not out.is_contiguous() or out.dtype != q.dtype:
+        raise ValueError(f"out must be contiguous {(B, n_q, D)} of q's type")
+    if workspace is None:
+        nbytes = qmm_attn_decode_workspace_bytes(B, n_q, n_kv, D)
+        workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=q.device)
+    with _on(q, k_pages, v_pages, block_table, seq_lens, sinks, out, workspace) as dev:
+        _check(load_library().qmm_attn_decode(*cache, q.data_ptr(), _dtype_code(q), qs, n_q, block_table.data_ptr(),
+                                              max_pages, seq_lens.data_ptr(), B,
+                                              D ** -0.5 if scale is None else scale, window,
+                                              0 if sinks is None else sinks.data_ptr(), out.data_ptr(),
+                                              workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                              dev.stream(stream)))
     return out

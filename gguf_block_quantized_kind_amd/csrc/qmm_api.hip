@@ -1,5 +1,6 @@
 // qmm_api.hip -- the exported C ABI: argument checks in the documented
 // order, then dispatch to the launchers.  Nothing here allocates.
+#include <math.h>
 #include <stdarg.h>
 #include <string.h>
 
@@ -415,6 +416,246 @@ QMM_EXPORT int qmm_moe_packed(int kind, const void *P, int64_t E, const int32_t 
   return hip_status(qmm::launch_moe(kind, (const uint8_t *)P, E, ids, topk, X, x_dtype == QMM_F16, x_per_slot, Y, M,
                                     N, K, workspace, (hipStream_t)stream, true),
                     "moe_packed launch");
+}
+
+// ---------------------------------------------------------------------------
+// Rotary positions, the paged key/value cache, attention over it
+// ---------------------------------------------------------------------------
+namespace {
+
+bool cache_kind(int kind) { return kind == QMM_CACHE_F16 || kind == QMM_Q8_0 || kind == QMM_Q4_0; }
+
+// Zero dimensions, kinds, head_dim against the block: the shared first checks
+// of the cache calls.  `rows` is T or B.
+int check_cache_shape(const qmm::KvCache &c, int64_t rows) {
+  if (c.n_pages <= 0 || c.page_size <= 0 || c.n_kv <= 0 || c.head_dim <= 0 || rows <= 0)
+    return fail(QMM_ERR_EMPTY_SHAPE, "empty shape: n_pages=%lld page_size=%lld n_kv=%lld head_dim=%lld rows=%lld",
+                (long long)c.n_pages, (long long)c.page_size, (long long)c.n_kv, (long long)c.head_dim,
+                (long long)rows);
+  for (int kind : {c.k_kind, c.v_kind})
+    if (!cache_kind(kind))
+      return fail(QMM_ERR_UNSUPPORTED_KIND, "cache kind %d is none of F16 (%d), Q8_0 (%d), Q4_0 (%d)", kind,
+                  QMM_CACHE_F16, QMM_Q8_0, QMM_Q4_0);
+  if (c.head_dim % 32 != 0)
+    return fail(QMM_ERR_K_NOT_BLOCK_ALIGNED, "head_dim=%lld is not a whole number of 32-element blocks",
+                (long long)c.head_dim);
+  return QMM_OK;
+}
+
+bool head_dim_supported(int64_t d) { return d == 64 || d == 96 || d == 128 || d == 192 || d == 256; }
+
+int check_cache(const qmm::KvCache &c) {
+  if (!head_dim_supported(c.head_dim))
+    return fail(QMM_ERR_BAD_ARG, "head_dim=%lld is none of 64, 96, 128, 192, 256", (long long)c.head_dim);
+  if (c.page_size % 32 != 0 || c.page_size > 65536)
+    return fail(QMM_ERR_BAD_ARG, "page_size=%lld is not a multiple of 32 up to 65536", (long long)c.page_size);
+  if (c.n_kv > 1024 || c.n_pages > INT32_MAX || c.n_pages * c.page_size > INT32_MAX)
+    return fail(QMM_ERR_BAD_ARG, "n_kv=%lld or n_pages=%lld exceeds the supported range", (long long)c.n_kv,
+                (long long)c.n_pages);
+  if (!c.k_pages || !c.v_pages) return fail(QMM_ERR_BAD_ARG, "k_pages or v_pages is NULL");
+  if (!aligned(c.k_pages, 16) || !aligned(c.v_pages, 16))
+    return fail(QMM_ERR_BAD_ARG, "k_pages or v_pages is not 16-byte aligned");
+  return QMM_OK;
+}
+
+// Rows of H heads: pointer, alignment, stride.
+int check_rows(const void *x, int dtype, int64_t stride, int64_t row, int64_t T, const char *what) {
+  int st = check_act(x, dtype, what);
+  if (st) return st;
+  if (stride < row || stride > ((int64_t)1 << 40) / T)
+    return fail(QMM_ERR_BAD_ARG, "the row stride %lld of %s is below its %lld elements or out of range",
+                (long long)stride, what, (long long)row);
+  return QMM_OK;
+}
+
+// The rotation of q into q_out.
+int check_rope(const qmm::KvWrite &w, int64_t H, int64_t D) {
+  if (w.n_rot <= 0 || w.n_rot % 2 != 0 || w.n_rot > D)
+    return fail(QMM_ERR_BAD_ARG, "n_rot=%lld is not an even number of elements within head_dim=%lld",
+                (long long)w.n_rot, (long long)D);
+  if (!w.freqs || !w.pos || !aligned(w.freqs, 8) || !aligned(w.pos, 4))
+    return fail(QMM_ERR_BAD_ARG, "freqs or pos is NULL or misaligned");
+  int st = check_rows(w.q, w.f16 ? QMM_F16 : QMM_F32, w.q_stride, H * D, w.T, "the rows to rotate");
+  if (st) return st;
+  if ((st = check_rows(w.q_out, w.q_out_f16 ? QMM_F16 : QMM_F32, w.q_out_stride, H * D, w.T, "the rotated rows")))
+    return st;
+  if (w.q == w.q_out && (w.f16 != w.q_out_f16 || w.q_stride != w.q_out_stride))
+    return fail(QMM_ERR_BAD_ARG, "rotating in place needs equal types and strides");
+  return QMM_OK;
+}
+
+int kv_write_checked(const qmm::KvCache &c, qmm::KvWrite &w, int dtype, int q_out_dtype, int layout, void *stream) {
+  if (w.rope && w.n_q <= 0) return fail(QMM_ERR_EMPTY_SHAPE, "empty shape: n_q=%lld", (long long)w.n_q);
+  int st = check_cache_shape(c, w.T);
+  if (st) return st;
+  if ((st = check_dtype(dtype))) return st;
+  if (w.rope && (st = check_dtype(q_out_dtype))) return st;
+  if ((st = check_cache(c))) return st;
+  if (w.T > INT32_MAX || (w.rope && w.n_q > 65536) || w.T * (c.n_kv + (w.rope ? w.n_q : 0)) * c.head_dim > INT32_MAX)
+    return fail(QMM_ERR_BAD_ARG, "T=%lld tokens exceed the supported range", (long long)w.T);
+  const int64_t row = c.n_kv * c.head_dim;
+  if ((st = check_rows(w.k, dtype, w.k_stride, row, w.T, "k"))) return st;
+  if ((st = check_rows(w.v, dtype, w.v_stride, row, w.T, "v"))) return st;
+  if (!w.slots || !aligned(w.slots, 4)) return fail(QMM_ERR_BAD_ARG, "slots is NULL or misaligned");
+  w.f16 = dtype == QMM_F16;
+  if (w.rope) {
+    w.q_out_f16 = q_out_dtype == QMM_F16;
+    if (layout != QMM_ROPE_HALF && layout != QMM_ROPE_INTERLEAVED)
+      return fail(QMM_ERR_BAD_ARG, "layout %d is neither QMM_ROPE_HALF nor QMM_ROPE_INTERLEAVED", layout);
+    w.interleaved = layout == QMM_ROPE_INTERLEAVED;
+    if ((st = check_rope(w, w.n_q, c.head_dim))) return st;
+  }
+  return hip_status(qmm::launch_kv_write(c, w, (hipStream_t)stream), w.rope ? "kv_append launch" : "kv_write launch");
+}
+
+}  // namespace
+
+QMM_EXPORT int64_t qmm_kv_page_bytes(int kind, int64_t page_size, int64_t n_kv, int64_t head_dim) {
+  if (!cache_kind(kind) || page_size <= 0 || page_size % 32 != 0 || page_size > 65536 || n_kv <= 0 || n_kv > 1024 ||
+      !head_dim_supported(head_dim))
+    return -1;
+  return qmm::kv_page_bytes(kind, page_size, n_kv, head_dim);
+}
+
+QMM_EXPORT int qmm_rope_freqs(double *freqs, float *mscale, int64_t n_rot, double base, const float *factors,
+                              double factor, int64_t orig_ctx, double beta_fast, double beta_slow) {
+  if (n_rot <= 0) return fail(QMM_ERR_EMPTY_SHAPE, "empty shape: n_rot=%lld", (long long)n_rot);
+  if (n_rot % 2 != 0 || n_rot > 65536 || !freqs) return fail(QMM_ERR_BAD_ARG, "n_rot=%lld is odd or out of range, or freqs is NULL", (long long)n_rot);
+  if (!(base > 1.0) || !isfinite(base)) return fail(QMM_ERR_BAD_ARG, "base=%g is not above 1", base);
+  if (!(factor >= 1.0) || !isfinite(factor)) return fail(QMM_ERR_BAD_ARG, "factor=%g is not at least 1", factor);
+  if (orig_ctx < 0) return fail(QMM_ERR_BAD_ARG, "orig_ctx=%lld is negative", (long long)orig_ctx);
+  const bool yarn = orig_ctx > 0 && factor > 1.0;
+  if (yarn && !(beta_slow > 0.0 && beta_fast > beta_slow))
+    return fail(QMM_ERR_BAD_ARG, "YaRN needs beta_fast > beta_slow > 0, got %g and %g", beta_fast, beta_slow);
+  const double n = (double)n_rot;
+  double low = 0.0, high = 1.0;
+  if (yarn) {
+    const double per_turn = n / (2.0 * log(base)), turns = (double)orig_ctx / (2.0 * M_PI);
+    low = fmax(floor(per_turn * log(turns / beta_fast)), 0.0);
+    high = fmin(ceil(per_turn * log(turns / beta_slow)), n - 1.0);
+  }
+  for (int64_t i = 0; i < n_rot / 2; ++i) {
+    double f = pow(base, -2.0 * (double)i / n);
+    if (factors) f /= (double)factors[i];
+    if (yarn) {
+      const double ramp = fmin(fmax(((double)i - low) / fmax(high - low, 0.001), 0.0), 1.0);
+      f = f * (1.0 - ramp) + f / factor * ramp;
+    } else {
+      f /= factor;
+    }
+    freqs[i] = f;
+  }
+  if (mscale) *mscale = yarn ? (float)(0.1 * log(factor) + 1.0) : 1.0f;
+  return ok();
+}
+
+QMM_EXPORT int qmm_rope(const double *freqs, int64_t n_rot, int layout, float mscale, const int32_t *pos,
+                        const void *x, int x_dtype, int64_t x_stride, void *y, int y_dtype, int64_t y_stride,
+                        int64_t T, int64_t H, int64_t head_dim, void *stream) {
+  if (T <= 0 || H <= 0 || head_dim <= 0)
+    return fail(QMM_ERR_EMPTY_SHAPE, "empty shape: T=%lld H=%lld head_dim=%lld", (long long)T, (long long)H,
+                (long long)head_dim);
+  int st = check_dtype(x_dtype);
+  if (st) return st;
+  if ((st = check_dtype(y_dtype))) return st;
+  if (layout != QMM_ROPE_HALF && layout != QMM_ROPE_INTERLEAVED)
+    return fail(QMM_ERR_BAD_ARG, "layout %d is neither QMM_ROPE_HALF nor QMM_ROPE_INTERLEAVED", layout);
+  if (head_dim % 2 != 0 || head_dim > 65536 || H > 65536 || T > INT32_MAX || T * H * head_dim > (int64_t)1 << 32)
+    return fail(QMM_ERR_BAD_ARG, "head_dim=%lld is odd, or T=%lld, H=%lld exceed the supported range",
+                (long long)head_dim, (long long)T, (long long)H);
+  qmm::KvWrite w{};
+  w.q = x, w.q_stride = x_stride, w.q_out = y, w.q_out_stride = y_stride;
+  w.f16 = x_dtype == QMM_F16, w.q_out_f16 = y_dtype == QMM_F16;
+  w.pos = pos, w.T = T, w.n_q = H, w.freqs = freqs, w.n_rot = n_rot;
+  w.interleaved = layout == QMM_ROPE_INTERLEAVED, w.mscale = mscale;
+  if ((st = check_rope(w, H, head_dim))) return st;
+  return hip_status(qmm::launch_rope(w, H, head_dim, (hipStream_t)stream), "rope launch");
+}
+
+QMM_EXPORT int qmm_kv_write(int k_kind, int v_kind, void *k_pages, void *v_pages, int64_t n_pages, int64_t page_size,
+                            int64_t n_kv, int64_t head_dim, const void *k, int64_t k_stride, const void *v,
+                            int64_t v_stride, int dtype, const int32_t *slots, int64_t T, void *stream) {
+  const qmm::KvCache c{k_kind, v_kind, k_pages, v_pages, n_pages, page_size, n_kv, head_dim};
+  qmm::KvWrite w{};
+  w.k = k, w.v = v, w.k_stride = k_stride, w.v_stride = v_stride, w.slots = slots, w.T = T;
+  return kv_write_checked(c, w, dtype, dtype, QMM_ROPE_HALF, stream);
+}
+
+QMM_EXPORT int qmm_kv_append(const double *freqs, int64_t n_rot, int layout, float mscale, const int32_t *pos,
+                             const void *q, int64_t q_stride, int64_t n_q, void *q_out, int q_out_dtype,
+                             int64_t q_out_stride, int k_kind, int v_kind, void *k_pages, void *v_pages,
+                             int64_t n_pages, int64_t page_size, int64_t n_kv, int64_t head_dim, const void *k,
+                             int64_t k_stride, const void *v, int64_t v_stride, int dtype, const int32_t *slots,
+                             int64_t T, void *stream) {
+  const qmm::KvCache c{k_kind, v_kind, k_pages, v_pages, n_pages, page_size, n_kv, head_dim};
+  qmm::KvWrite w{};
+  w.k = k, w.v = v, w.k_stride = k_stride, w.v_stride = v_stride, w.slots = slots, w.T = T;
+  w.q = q, w.q_stride = q_stride, w.n_q = n_q, w.q_out = q_out, w.q_out_stride = q_out_stride;
+  w.rope = 1, w.freqs = freqs, w.n_rot = n_rot, w.mscale = mscale, w.pos = pos;
+  return kv_write_checked(c, w, dtype, q_out_dtype, layout, stream);
+}
+
+QMM_EXPORT int qmm_kv_read(int k_kind, int v_kind, const void *k_pages, const void *v_pages, int64_t n_pages,
+                           int64_t page_size, int64_t n_kv, int64_t head_dim, const int32_t *slots, int64_t T,
+                           void *k_out, void *v_out, int dtype, void *stream) {
+  const qmm::KvCache c{k_kind, v_kind, (void *)k_pages, (void *)v_pages, n_pages, page_size, n_kv, head_dim};
+  int st = check_cache_shape(c, T);
+  if (st) return st;
+  if ((st = check_dtype(dtype))) return st;
+  if ((st = check_cache(c))) return st;
+  if (T > INT32_MAX || T * n_kv * head_dim > INT32_MAX)
+    return fail(QMM_ERR_BAD_ARG, "T=%lld tokens exceed the supported range", (long long)T);
+  if (!slots || !aligned(slots, 4)) return fail(QMM_ERR_BAD_ARG, "slots is NULL or misaligned");
+  if (!k_out || !v_out || !aligned(k_out, 16) || !aligned(v_out, 16))
+    return fail(QMM_ERR_BAD_ARG, "k_out or v_out is NULL or not 16-byte aligned");
+  return hip_status(qmm::launch_kv_read(c, slots, T, k_out, v_out, dtype == QMM_F16, (hipStream_t)stream),
+                    "kv_read launch");
+}
+
+namespace {
+// Largest grids (HIP: fewer than 2^32 threads) and counts of the attention
+// call.
+bool attn_sizes_ok(int64_t B, int64_t n_q, int64_t n_kv) {
+  return B <= 65536 && n_q <= 65536 && n_kv <= 1024 && n_q % n_kv == 0 && B * n_q <= ((int64_t)1 << 23);
+}
+}  // namespace
+
+QMM_EXPORT size_t qmm_attn_decode_workspace_bytes(int64_t B, int64_t n_q, int64_t n_kv, int64_t head_dim) {
+  if (B <= 0 || n_q <= 0 || n_kv <= 0 || !head_dim_supported(head_dim) || !attn_sizes_ok(B, n_q, n_kv)) return 0;
+  return qmm::attn_workspace_bytes(B, n_q, n_kv, head_dim);
+}
+
+QMM_EXPORT int qmm_attn_decode(int k_kind, int v_kind, const void *k_pages, const void *v_pages, int64_t n_pages,
+                               int64_t page_size, int64_t n_kv, int64_t head_dim, const void *q, int dtype,
+                               int64_t q_stride, int64_t n_q, const int32_t *block_table, int64_t max_pages,
+                               const int32_t *seq_lens, int64_t B, float scale, int64_t window, const float *sinks,
+                               void *out, void *workspace, size_t workspace_bytes, void *stream) {
+  const qmm::KvCache c{k_kind, v_kind, (void *)k_pages, (void *)v_pages, n_pages, page_size, n_kv, head_dim};
+  if (n_q <= 0 || max_pages <= 0)
+    return fail(QMM_ERR_EMPTY_SHAPE, "empty shape: n_q=%lld max_pages=%lld", (long long)n_q, (long long)max_pages);
+  int st = check_cache_shape(c, B);
+  if (st) return st;
+  if ((st = check_dtype(dtype))) return st;
+  if ((st = check_cache(c))) return st;
+  if (!attn_sizes_ok(B, n_q, n_kv))
+    return fail(QMM_ERR_BAD_ARG, "n_q=%lld is not a multiple of n_kv=%lld, or they or B=%lld exceed the supported range",
+                (long long)n_q, (long long)n_kv, (long long)B);
+  if (max_pages > INT32_MAX || max_pages * page_size > INT32_MAX)
+    return fail(QMM_ERR_BAD_ARG, "max_pages=%lld exceeds the supported range", (long long)max_pages);
+  if (!isfinite(scale)) return fail(QMM_ERR_BAD_ARG, "scale is not finite");
+  if (window < 0) return fail(QMM_ERR_BAD_ARG, "window=%lld is negative", (long long)window);
+  if ((st = check_rows(q, dtype, q_stride, n_q * head_dim, B, "q"))) return st;
+  if (!block_table || !seq_lens || !aligned(block_table, 4) || !aligned(seq_lens, 4))
+    return fail(QMM_ERR_BAD_ARG, "block_table or seq_lens is NULL or misaligned");
+  if (sinks && !aligned(sinks, 4)) return fail(QMM_ERR_BAD_ARG, "sinks is misaligned");
+  if (!out || !aligned(out, 16)) return fail(QMM_ERR_BAD_ARG, "out is NULL or not 16-byte aligned");
+  const size_t need = qmm::attn_workspace_bytes(B, n_q, n_kv, head_dim);
+  if (!workspace || workspace_bytes < need || !aligned(workspace, 16))
+    return fail(QMM_ERR_WORKSPACE, "workspace needs %zu bytes (16-byte aligned), got %zu", need,
+                workspace ? workspace_bytes : (size_t)0);
+  const qmm::AttnDecode d{q,     q_stride, dtype == QMM_F16, n_q,   B,   block_table, max_pages,
+                          seq_lens, scale, window,           sinks, out, workspace};
+  return hip_status(qmm::launch_attn_decode(c, d, (hipStream_t)stream), "attn_decode launch");
 }
 
 QMM_EXPORT int qmm_dequant(int kind, const void *W, float *out, int64_t n_elems, void *stream) {

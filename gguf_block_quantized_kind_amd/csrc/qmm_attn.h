@@ -1,0 +1,544 @@
+// qmm_attn.h -- attention of one new token per sequence over the paged cache
+// of qmm_kv.h: the matrix-core kernel, by key kind, value kind, head size and
+// query type.
+//
+//   s_t = scale * q . k_t,   out = sum_t e^{s_t} v_t / (sum_t e^{s_t} + e^sink)
+//
+// over the tokens lo <= t < len of a sequence, lo = max(0, len - window).
+//
+// Work.  The tokens of a (sequence, key head) are cut into splits of whole
+// 32-token groups; a workgroup of four waves takes one split, its waves every
+// fourth group.  The G = n_q / n_kv query heads that share the key head are
+// the columns of the matrix-core products (16 at a time), so the cache is
+// read once per key head.  The number of groups per split follows from the
+// lengths themselves, which every workgroup reads: the host need not know
+// them, and the call can be captured.
+//
+// Products, per group (layouts in qmm_kv.h):
+//   scores   D[token][head] = K . Q^T.  F16 keys are the operand as they are.
+//            Codes enter as f16 subnormals, u * 2^-24 with u the stored
+//            unsigned code (one v_perm or AND per two codes; a high nibble
+//            stays in place as 16 u, its query element divided by 16), the
+//            offset as the accumulator's start value -offset * sum q (Q4_0
+//            beside f32 queries: signed integers, as the values); each
+//            block's product is scaled by the token's f32 block scale.
+//   values   D[element][head] += V^T . P^T.  Codes enter as exact signed
+//            integers in f16; the block scale goes into the weight, p * d,
+//            rounded once to f16.
+// f32 queries are split into two f16 terms (exact to about 2^-22), and so are
+// the weights p and p * d; f16 queries and their weights take one term.
+//
+// The softmax keeps a running reference R per head instead of the running
+// maximum: R is the maximum of (group maximum of s + exponent of the group's
+// largest value scale) - 14, so that p * d = 2^(s - R) * d reaches 2^14..2^15
+// for the strongest tokens and stays clear of f16's subnormals for tokens down
+// to 2^-28 of them, whatever the size of the values.
+#pragma once
+
+#include "qmm_internal.h"
+#include "qmm_kv.h"
+
+namespace qmm {
+namespace attn {
+
+using kv::C_F16;
+using kv::C_Q4_0;
+using kv::C_Q8_0;
+
+typedef _Float16 half8 __attribute__((ext_vector_type(8)));
+typedef _Float16 half2v __attribute__((ext_vector_type(2)));
+typedef float floatx4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+constexpr float kFloor = -1e30f;  // R of no tokens
+constexpr int kWaves = 4;
+constexpr int kMinGroups = 4;  // groups per split at least: one per wave
+
+struct Args {
+  const uint8_t *kp, *vp;
+  int64_t k_page_bytes, v_page_bytes, n_pages;
+  int page_groups;  // 32-token groups per page
+  int n_kv, n_q, G, tiles, heads;  // tiles of `heads` = min(G, 16) query heads
+  const void *q;
+  int64_t q_stride;
+  const int32_t *table;
+  int64_t max_pages;
+  const int32_t *lens;
+  int B;
+  float scale2;  // scale * log2(e)
+  int64_t window;
+  const float *sinks;
+  void *out;
+  float *part;  // [item][heads][D] then [item][heads][2] (reference, sum)
+  int64_t items;
+  int target;  // workgroups the splits aim at
+};
+
+// The groups [g0, g0 + n) of sequence b that hold attended tokens [lo, len).
+struct Span {
+  int lo, len, g0, n;
+};
+__device__ __forceinline__ Span span_of(const Args &a, int b) {
+  const int64_t most = a.max_pages * a.page_groups * kv::kGroup;
+  int len = b < a.B ? max(a.lens[b], 0) : 0;
+  if (len > most) len = (int)most;
+  const int lo = a.window > 0 && len > a.window ? len - (int)a.window : 0;
+  const int g0 = lo / kv::kGroup;
+  return Span{lo, len, g0, len > 0 ? (int)(((int64_t)len + kv::kGroup - 1) / kv::kGroup) - g0 : 0};
+}
+
+__device__ __forceinline__ int64_t wave_sum(int64_t v) {
+#pragma unroll
+  for (int k = 1; k < 64; k <<= 1) v += __shfl_xor(v, k, 64);
+  return v;
+}
+
+// Groups per split: the attended groups of the whole batch over the target
+// number of workgroups.
+__device__ __forceinline__ int groups_per_split(const Args &a, int lane) {
+  int64_t total = 0;
+  for (int b0 = 0; b0 < a.B; b0 += 64) total += span_of(a, b0 + lane).n;
+  total = wave_sum(total) * a.n_kv * a.tiles;
+  const int64_t c = (total + a.target - 1) / a.target;
+  return (int)max(c, (int64_t)kMinGroups);
+}
+
+// Splits are numbered through the batch (at least one per sequence, so that
+// every output row is written).  first_split: the number of splits before
+// sequence `want_b`, or, with want_b < 0, the sequence that split `unit`
+// belongs to (-1 past the last) and its first split.
+struct Found {
+  int b;
+  int64_t first;
+};
+__device__ __forceinline__ Found find_split(const Args &a, int lane, int c, int64_t unit, int want_b) {
+  int64_t before = 0;
+  for (int b0 = 0; b0 < a.B; b0 += 64) {
+    const int n = span_of(a, b0 + lane).n;
+    const int splits = b0 + lane < a.B ? max(1, (n + c - 1) / c) : 0;
+    int incl = splits;
+#pragma unroll
+    for (int k = 1; k < 64; k <<= 1) {
+      const int v = __shfl_up(incl, k, 64);
+      if (lane >= k) incl += v;
+    }
+    const bool hit = want_b < 0 ? unit < before + incl : b0 + lane == want_b;
+    const uint64_t mask = __ballot(hit);
+    if (mask) {
+      const int l = __ffsll((unsigned long long)mask) - 1;
+      return Found{b0 + l, before + __shfl(incl - splits, l, 64)};
+    }
+    before += __shfl(incl, 63, 64);
+  }
+  return Found{-1, before};
+}
+
+// Query element that K entry k of lane group G holds, of 32 (qmm_kv.h; Q4_0
+// bytes are taken in the order 0, 2, 1, 3 with low and high nibbles of a pair
+// of bytes side by side), and whether its code stands 16 times too high.
+template <int KK>
+__device__ __forceinline__ int k_element(int G, int k) {
+  if constexpr (KK != C_Q4_0) return 8 * G + k;
+  const int y = (k & 1) * 2 + (k >> 2);
+  return 4 * G + y + (k & 2 ? 16 : 0);
+}
+
+__device__ __forceinline__ half8 as_h8(u32x4 v) { return __builtin_bit_cast(half8, v); }
+__device__ __forceinline__ uint32_t pk(float a, float b) {
+  return __builtin_bit_cast(uint32_t, half2v{(_Float16)a, (_Float16)b});
+}
+__device__ __forceinline__ uint32_t pk_add(uint32_t a, _Float16 b) {
+  const half2v v = __builtin_bit_cast(half2v, a) + half2v{b, b};
+  return __builtin_bit_cast(uint32_t, v);
+}
+__device__ __forceinline__ uint32_t pk_fma(uint32_t a, _Float16 m, _Float16 b) {
+  const half2v v = __builtin_elementwise_fma(__builtin_bit_cast(half2v, a), half2v{m, m}, half2v{b, b});
+  return __builtin_bit_cast(uint32_t, v);
+}
+
+// Bytes of one block as a lane reads them.
+template <int KIND> struct Raw { u32x4 w; };  // Q8_0
+template <> struct Raw<C_F16> { u32x4 w[2]; };
+template <> struct Raw<C_Q4_0> { u32x2 w; };
+
+template <int KIND>
+__device__ __forceinline__ void load_block(const uint8_t *block, int lane, Raw<KIND> &r) {
+  if constexpr (KIND == C_F16) {
+    r.w[0] = *(const u32x4 *)(block + lane * 16);
+    r.w[1] = *(const u32x4 *)(block + 1024 + lane * 16);
+  } else if constexpr (KIND == C_Q8_0) {
+    r.w = *(const u32x4 *)(block + lane * 16);
+  } else {
+    r.w = *(const u32x2 *)(block + lane * 8);
+  }
+}
+
+// Eight bytes of Q8_0, or the nibbles of four bytes of Q4_0 in the order of
+// k_element, as exact signed integers in f16: the code under the mantissa of
+// 1024 (a high nibble 16 times too high), the offset taken off by one packed
+// operation.
+__device__ __forceinline__ half8 signed_bytes(uint32_t a, uint32_t b) {
+  const uint32_t k = 0x64646464;  // 1024 + u
+  return as_h8(u32x4{pk_add(__builtin_amdgcn_perm(k, a, 0x04010400), -1152.0f16),
+                     pk_add(__builtin_amdgcn_perm(k, a, 0x04030402), -1152.0f16),
+                     pk_add(__builtin_amdgcn_perm(k, b, 0x04010400), -1152.0f16),
+                     pk_add(__builtin_amdgcn_perm(k, b, 0x04030402), -1152.0f16)});
+}
+__device__ __forceinline__ uint32_t signed_low(uint32_t a) { return pk_add((a & 0x000f000f) | 0x64006400, -1032.0f16); }
+__device__ __forceinline__ uint32_t signed_high(uint32_t a) {  // (1024 + 16 u) / 16 - 72
+  return pk_fma((a & 0x00f000f0) | 0x64006400, 0.0625f16, -72.0f16);
+}
+
+// Whether codes of keys enter as f16 subnormals.  The matrix cores align the
+// products of one step by the operands' exponent fields, so a subnormal code u
+// keeps only about 24 - 10 + log2(u) bits: fine beside f16 queries, too few
+// for Q4_0 beside f32 ones (measured: outputs off by 5e-6 instead of 3e-7).
+template <int KK, bool SPLIT>
+constexpr bool kSubnormalKeys = KK == C_Q8_0 || (KK == C_Q4_0 && !SPLIT);
+
+// Key operand of tile m: halves, codes * 2^-24 (Q4_0 high nibbles 2^-20), or
+// signed codes.
+template <int KK, bool SPLIT>
+__device__ __forceinline__ half8 key_operand(const Raw<KK> &r, int m) {
+  if constexpr (KK == C_F16) return as_h8(r.w[m]);
+  if constexpr (KK == C_Q4_0 && SPLIT) {
+    const uint32_t a = r.w[m], b = a >> 8;
+    return as_h8(u32x4{signed_low(a), signed_high(a), signed_low(b), signed_high(b)});
+  }
+  if constexpr (KK == C_Q8_0) {
+    const uint32_t a = r.w[2 * m], b = r.w[2 * m + 1];
+    return as_h8(u32x4{__builtin_amdgcn_perm(0, a, 0x0c010c00), __builtin_amdgcn_perm(0, a, 0x0c030c02),
+                       __builtin_amdgcn_perm(0, b, 0x0c010c00), __builtin_amdgcn_perm(0, b, 0x0c030c02)});
+  } else if constexpr (KK == C_Q4_0) {
+    const uint32_t a = r.w[m], b = a >> 8;
+    return as_h8(u32x4{a & 0x000f000f, a & 0x00f000f0, b & 0x000f000f, b & 0x00f000f0});
+  }
+}
+
+// Value operand of tile x: halves, or exact signed codes.  Token order of the
+// eight K entries: natural, for Q4_0 0 2 1 3 4 6 5 7.
+template <int VK>
+__device__ __forceinline__ half8 value_operand(const Raw<VK> &r, int x) {
+  if constexpr (VK == C_F16) return as_h8(r.w[x]);
+  if constexpr (VK == C_Q8_0) return signed_bytes(r.w[2 * x], r.w[2 * x + 1]);
+  if constexpr (VK == C_Q4_0) {
+    const uint32_t a = r.w[0], b = r.w[1];
+    if (x == 0) return as_h8(u32x4{signed_low(a), signed_low(a >> 8), signed_low(b), signed_low(b >> 8)});
+    return as_h8(u32x4{signed_high(a), signed_high(a >> 8), signed_high(b), signed_high(b >> 8)});
+  }
+}
+template <int VK>
+__device__ __forceinline__ constexpr int v_token(int k) {
+  if (VK != C_Q4_0) return k;
+  const int p = k & 3;
+  return (k & 4) + (p == 1 ? 2 : p == 2 ? 1 : p);
+}
+
+template <int KK, int VK, int NB, typename QT>
+__global__ __launch_bounds__(64 * kWaves) void attn_kernel(Args a) {
+  constexpr int D = NB * 32;
+  constexpr bool SPLIT = sizeof(QT) == 4;  // two f16 terms
+  constexpr bool SUB = kSubnormalKeys<KK, SPLIT>;
+  constexpr int kPitch = D + 4;
+  extern __shared__ float lds[];  // [2][heads][kPitch], then [wave][heads][2]
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int j = lane & 15, G = lane >> 4;
+
+  // Which split this workgroup has.
+  const int nh = a.n_kv * a.tiles;
+  const int64_t unit = (int64_t)blockIdx.x / nh;
+  const int hh = (int)(blockIdx.x - unit * nh), kvh = hh % a.n_kv, tile = hh / a.n_kv;
+  const int c = groups_per_split(a, lane);
+  const Found f = find_split(a, lane, c, unit, -1);
+  if (f.b < 0) return;
+  const int b = __builtin_amdgcn_readfirstlane(f.b);
+  const Span sp = span_of(a, b);
+  const int splits = max(1, (sp.n + c - 1) / c), each = (sp.n + splits - 1) / splits;
+  const int mine = (int)(unit - f.first);
+  const int gs = __builtin_amdgcn_readfirstlane(sp.g0 + min(mine * each, sp.n));
+  const int ge = __builtin_amdgcn_readfirstlane(sp.g0 + min((mine + 1) * each, sp.n));
+
+  // This tile's query heads: column j is head kvh * G + tile * 16 + j.
+  const int heads = min(a.heads, a.G - tile * 16);
+  const int head0 = kvh * a.G + tile * 16;
+  const QT *q = (const QT *)a.q + (int64_t)b * a.q_stride + (int64_t)(head0 + min(j, heads - 1)) * D;
+
+  // The query scaled by a power of two to 2^14 .. 2^15, in one or two terms,
+  // and what undoes it.
+  half8 qh[NB], ql[SPLIT ? NB : 1];
+  float qoff[SUB ? NB : 1];
+  float qscale;
+  {
+    float big = 0.0f;
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) big = fmaxf(big, fabsf((float)q[n * 32 + k_element<KK>(G, k)]));
+    big = fmaxf(big, __shfl_xor(big, 16, 64));
+    big = fmaxf(big, __shfl_xor(big, 32, 64));
+    const int e = big > 0.0f && big < __builtin_inff() ? 14 - ilogbf(big) : 0;
+    qscale = ldexpf(a.scale2, -e + (SUB ? 24 : 0));
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      float sum = 0.0f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const bool high = KK == C_Q4_0 && SUB && (k & 2);
+        const float v = ldexpf((float)q[n * 32 + k_element<KK>(G, k)], high ? e - 4 : e);
+        const _Float16 h = (_Float16)v;
+        qh[n][k] = h;
+        float got = (float)h;
+        if constexpr (SPLIT) {
+          const _Float16 l = (_Float16)(v - got);
+          ql[n][k] = l;
+          got += (float)l;
+        }
+        sum += high ? 16.0f * got : got;
+      }
+      if constexpr (SUB) {
+        sum += __shfl_xor(sum, 16, 64);
+        sum += __shfl_xor(sum, 32, 64);
+        qoff[n] = sum * (KK == C_Q8_0 ? -128.0f : -8.0f) * 0x1p-24f;
+      }
+    }
+  }
+
+  floatx4 acc[NB][2];
+#pragma unroll
+  for (int n = 0; n < NB; ++n) acc[n][0] = acc[n][1] = floatx4{0, 0, 0, 0};
+  float R = kFloor, sum = 0.0f;
+
+  constexpr int kKG = kv::group_bytes(KK, NB), kVG = kv::group_bytes(VK, NB);
+  constexpr int kKB = kv::block_code_bytes(KK), kVB = kv::block_code_bytes(VK);
+  for (int g = gs + wave; g < ge; g += kWaves) {
+    const int page = a.table[(int64_t)b * a.max_pages + g / a.page_groups];
+    if (page < 0 || page >= a.n_pages) continue;
+    const int in_page = kvh * a.page_groups + g % a.page_groups;
+    const uint8_t *kg = a.kp + page * a.k_page_bytes + (int64_t)in_page * kKG;
+    const uint8_t *vg = a.vp + page * a.v_page_bytes + (int64_t)in_page * kVG;
+    Raw<KK> kr[NB];
+    Raw<VK> vr[NB];
+    half8 kd[KK == C_F16 ? 1 : NB], vd[VK == C_F16 ? 1 : NB];
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      load_block<KK>(kg + n * kKB, lane, kr[n]);
+      if constexpr (KK != C_F16) kd[n] = *(const half8 *)(kg + NB * kKB + n * 64 + G * 16);
+    }
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      load_block<VK>(vg + n * kVB, lane, vr[n]);
+      if constexpr (VK != C_F16) vd[n] = *(const half8 *)(vg + NB * kVB + n * 64 + G * 16);
+    }
+
+    // Scores of tokens 8G + k, head j.
+    float s[8];
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      floatx4 t = {0, 0, 0, 0};
+#pragma unroll
+      for (int n = 0; n < NB; ++n) {
+        const half8 k = key_operand<KK, SPLIT>(kr[n], m);
+        floatx4 u;
+        if constexpr (KK == C_F16) u = t;
+        else if constexpr (SUB) u = floatx4{qoff[n], qoff[n], qoff[n], qoff[n]};
+        else u = floatx4{0, 0, 0, 0};
+        u = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, qh[n], u, 0, 0, 0);
+        if constexpr (SPLIT) u = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, ql[n], u, 0, 0, 0);
+        if constexpr (KK == C_F16) t = u;
+        else
+#pragma unroll
+          for (int r = 0; r < 4; ++r) t[r] = __builtin_fmaf((float)kd[n][4 * m + r], u[r], t[r]);
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) s[4 * m + r] = t[r] * qscale;
+    }
+
+    // Tokens outside [lo, len) of the first and last group: whatever their
+    // bytes hold, they weigh nothing.
+    const int t0 = g * kv::kGroup;
+    if (t0 < sp.lo || t0 > sp.len - kv::kGroup) {
+      bool in[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int t = t0 + 8 * G + k;
+        in[k] = t >= sp.lo && t < sp.len;
+        if (!in[k]) s[k] = -__builtin_inff();
+      }
+#pragma unroll
+      for (int n = 0; n < NB; ++n) {
+        if constexpr (VK == C_F16) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              vr[n].w[x][k] &= (in[2 * k] ? 0xffffu : 0u) | (in[2 * k + 1] ? 0xffff0000u : 0u);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) vd[n][k] = in[k] ? vd[n][k] : (_Float16)0.0f;
+        }
+      }
+    }
+
+    float top = s[0];
+#pragma unroll
+    for (int k = 1; k < 8; ++k) top = fmaxf(top, s[k]);
+    top = fmaxf(top, __shfl_xor(top, 16, 64));
+    top = fmaxf(top, __shfl_xor(top, 32, 64));
+    if constexpr (VK == C_F16) {
+      top -= 14.0f;
+    } else {
+      _Float16 big = (_Float16)0.0f;
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) big = __builtin_fmaxf16(big, __builtin_fabsf16(vd[n][k]));
+      float bf = (float)big;
+      bf = fmaxf(bf, __shfl_xor(bf, 16, 64));
+      bf = fmaxf(bf, __shfl_xor(bf, 32, 64));
+      // 2^e <= bf < 2^(e + 1); f16 scales are 0 or at least 2^-24.
+      const int e = (int)(__builtin_bit_cast(uint32_t, fmaxf(bf, 0x1p-24f)) >> 23) - 127;
+      top += (float)(e - 14);
+    }
+    const float Rn = fmaxf(R, top);
+    const float alpha = __builtin_amdgcn_exp2f(R - Rn);
+    R = Rn;
+    float p[8], ps = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      p[k] = __builtin_amdgcn_exp2f(s[k] - Rn);
+      ps += p[k];
+    }
+    sum = __builtin_fmaf(sum, alpha, ps);
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) acc[n][x] *= alpha;
+
+    half8 ph, pl;
+    if constexpr (VK == C_F16) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        ph[k] = (_Float16)p[k];
+        if constexpr (SPLIT) pl[k] = (_Float16)(p[k] - (float)ph[k]);
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      if constexpr (VK != C_F16) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) ph[k] = (_Float16)(p[v_token<VK>(k)] * (float)vd[n][v_token<VK>(k)]);
+        if constexpr (SPLIT) {
+          // The second term is what the first one, as it was rounded, leaves:
+          // the compiler must not recompute that rounding in another way.
+          asm("" : "+v"(ph));
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            pl[k] = (_Float16)__builtin_fmaf(p[v_token<VK>(k)], (float)vd[n][v_token<VK>(k)], -(float)ph[k]);
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const half8 v = value_operand<VK>(vr[n], x);
+        acc[n][x] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, ph, acc[n][x], 0, 0, 0);
+        if constexpr (SPLIT) acc[n][x] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, pl, acc[n][x], 0, 0, 0);
+      }
+    }
+  }
+  sum += __shfl_xor(sum, 16, 64);
+  sum += __shfl_xor(sum, 32, 64);
+
+  // The four waves' parts, joined through LDS: references and sums first, then
+  // the accumulators on the common reference, waves 2 and 3 handing theirs to
+  // waves 0 and 1.
+  float *ml = lds + 2 * a.heads * kPitch;
+  if (G == 0 && j < heads) {
+    ml[(wave * a.heads + j) * 2] = R;
+    ml[(wave * a.heads + j) * 2 + 1] = sum;
+  }
+  __syncthreads();
+  if (j < heads) {
+    float Rm = kFloor;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) Rm = fmaxf(Rm, ml[(w * a.heads + j) * 2]);
+    const float f = __builtin_amdgcn_exp2f(R - Rm);
+    float *o = lds + ((wave & 1) * a.heads + j) * kPitch + 4 * G;
+    if (wave >= 2) {
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) *(floatx4 *)(o + n * 32 + x * 16) = acc[n][x] * f;
+    }
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) acc[n][x] *= f;
+  }
+  __syncthreads();
+  if (wave < 2 && j < heads) {
+    float *o = lds + (wave * a.heads + j) * kPitch + 4 * G;
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) *(floatx4 *)(o + n * 32 + x * 16) += acc[n][x];
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < heads * D; i += 64 * kWaves) {
+    const int h = i / D, d = i - h * D;
+    float Rm = kFloor, l = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) Rm = fmaxf(Rm, ml[(w * a.heads + h) * 2]);
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w)
+      l = __builtin_fmaf(__builtin_amdgcn_exp2f(ml[(w * a.heads + h) * 2] - Rm), ml[(w * a.heads + h) * 2 + 1], l);
+    const float o = lds[h * kPitch + d] + lds[(a.heads + h) * kPitch + d];
+    if (splits == 1) {
+      if (a.sinks) l += __builtin_amdgcn_exp2f(fminf(a.sinks[head0 + h] * 1.44269504f - Rm, 120.0f));
+      ((QT *)a.out)[((int64_t)b * a.n_q + head0 + h) * D + d] = (QT)(l > 0.0f || l != l ? o / l : 0.0f);
+    } else {
+      a.part[((int64_t)blockIdx.x * a.heads + h) * D + d] = o;
+      if (d == 0) {
+        float *m = a.part + a.items * a.heads * D + ((int64_t)blockIdx.x * a.heads + h) * 2;
+        m[0] = Rm;
+        m[1] = l;
+      }
+    }
+  }
+}
+
+template <int KK, int VK, int NB, typename QT>
+static hipError_t run(const Args &a, hipStream_t s) {
+  const unsigned lds = (2 * (NB * 32 + 4) + 2 * kWaves) * a.heads * sizeof(float);  // at most 34 KiB
+  hipLaunchKernelGGL((attn_kernel<KK, VK, NB, QT>), dim3((unsigned)a.items), dim3(64 * kWaves), lds, s, a);
+  return hipGetLastError();
+}
+
+template <int KK, int VK, typename QT>
+static hipError_t run_nb(const Args &a, int NB, hipStream_t s) {
+  switch (NB) {
+    case 2: return run<KK, VK, 2, QT>(a, s);
+    case 3: return run<KK, VK, 3, QT>(a, s);
+    case 4: return run<KK, VK, 4, QT>(a, s);
+    case 6: return run<KK, VK, 6, QT>(a, s);
+    case 8: return run<KK, VK, 8, QT>(a, s);
+  }
+  return hipErrorInvalidValue;
+}
+
+template <int KK, int VK>
+static hipError_t run_kinds(const Args &a, int NB, int f16, hipStream_t s) {
+  return f16 ? run_nb<KK, VK, _Float16>(a, NB, s) : run_nb<KK, VK, float>(a, NB, s);
+}
+
+hipError_t launch_f16_f16(const Args &, int NB, int f16, hipStream_t);
+hipError_t launch_f16_q8(const Args &, int NB, int f16, hipStream_t);
+hipError_t launch_f16_q4(const Args &, int NB, int f16, hipStream_t);
+hipError_t launch_q8_f16(const Args &, int NB, int f16, hipStream_t);
+hipError_t launch_q8_q8(const Args &, int NB, int f16, hipStream_t);
+hipError_t launch_q8_q4(const Args &, int NB, int f16, hipStream_t);
+hipError_t launch_q4_f16(const Args &, int NB, int f16, hipStream_t);
+hipError_t launch_q4_q8(const Args &, int NB, int f16, hipStream_t);
+hipError_t launch_q4_q4(const Args &, int NB, int f16, hipStream_t);
+
+}  // namespace attn
+}  // namespace qmm

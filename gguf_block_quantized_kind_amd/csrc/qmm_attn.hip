@@ -1,0 +1,92 @@
+// qmm_attn.hip -- single-token attention over the paged cache: workspace,
+// dispatch by kinds, and the join of a sequence's splits.
+#include "qmm_attn.h"
+
+namespace qmm {
+namespace attn {
+
+// One workgroup per (sequence, query head): the splits' parts, weighted by
+// 2^(R_i - max R), over the weighted sums (plus the sink's share).  Sequences
+// of one split were finished by the attention kernel.
+template <typename QT>
+__global__ __launch_bounds__(256) void join_kernel(Args a, int D) {
+  const int lane = threadIdx.x & 63;
+  const int b = blockIdx.x / a.n_q, hq = blockIdx.x - b * a.n_q;
+  const int c = groups_per_split(a, lane);
+  const Span sp = span_of(a, b);
+  const int splits = (sp.n + c - 1) / c;
+  if (splits <= 1) return;
+  const Found f = find_split(a, lane, c, 0, b);
+  const int kvh = hq / a.G, in = hq - kvh * a.G, tile = in / 16, h = in - tile * 16;
+  const int nh = a.n_kv * a.tiles;
+  const int64_t item0 = f.first * nh + tile * a.n_kv + kvh;
+  const float *ml = a.part + a.items * a.heads * D;
+  float Rm = kFloor;
+  for (int i = 0; i < splits; ++i) Rm = fmaxf(Rm, ml[((item0 + (int64_t)i * nh) * a.heads + h) * 2]);
+  const int d = threadIdx.x;
+  if (d >= D) return;
+  float o = 0.0f, l = 0.0f;
+  for (int i = 0; i < splits; ++i) {
+    const int64_t at = (item0 + (int64_t)i * nh) * a.heads + h;
+    const float w = __builtin_amdgcn_exp2f(ml[at * 2] - Rm);
+    o = __builtin_fmaf(w, a.part[at * D + d], o);
+    l = __builtin_fmaf(w, ml[at * 2 + 1], l);
+  }
+  if (a.sinks) l += __builtin_amdgcn_exp2f(fminf(a.sinks[hq] * 1.44269504f - Rm, 120.0f));
+  ((QT *)a.out)[((int64_t)b * a.n_q + hq) * D + d] = (QT)(l > 0.0f || l != l ? o / l : 0.0f);
+}
+
+// Splits aim at this many workgroups.
+constexpr int kTarget = 1024;
+
+static int64_t items_of(int64_t B, int64_t n_q, int64_t n_kv) {
+  const int64_t tiles = (n_q / n_kv + 15) / 16;
+  return kTarget + B * n_kv * tiles;
+}
+
+}  // namespace attn
+
+size_t attn_workspace_bytes(int64_t B, int64_t n_q, int64_t n_kv, int64_t head_dim) {
+  const int64_t G = n_q / n_kv, heads = G < 16 ? G : 16;
+  return (size_t)(attn::items_of(B, n_q, n_kv) * heads * (head_dim + 2) * 4);
+}
+
+hipError_t launch_attn_decode(const KvCache &kc, const AttnDecode &d, hipStream_t s) {
+  using namespace attn;
+  Args a{};
+  a.kp = (const uint8_t *)kc.k_pages, a.vp = (const uint8_t *)kc.v_pages;
+  a.k_page_bytes = kv_page_bytes(kc.k_kind, kc.page_size, kc.n_kv, kc.head_dim);
+  a.v_page_bytes = kv_page_bytes(kc.v_kind, kc.page_size, kc.n_kv, kc.head_dim);
+  a.n_pages = kc.n_pages;
+  a.page_groups = (int)(kc.page_size / kv::kGroup);
+  a.n_kv = (int)kc.n_kv, a.n_q = (int)d.n_q, a.G = a.n_q / a.n_kv;
+  a.tiles = (a.G + 15) / 16, a.heads = a.G < 16 ? a.G : 16;
+  a.q = d.q, a.q_stride = d.q_stride;
+  a.table = d.table, a.max_pages = d.max_pages, a.lens = d.lens, a.B = (int)d.B;
+  a.scale2 = d.scale * 1.44269504088896f;
+  a.window = d.window, a.sinks = d.sinks, a.out = d.out;
+  a.part = (float *)d.workspace;
+  a.items = items_of(d.B, d.n_q, kc.n_kv);
+  a.target = kTarget;
+  const int NB = (int)(kc.head_dim / 32);
+  hipError_t e = hipErrorInvalidValue;
+#define QMM_CASE(K, V, F) \
+  if (kc.k_kind == K && kc.v_kind == V) e = F(a, NB, d.f16, s);
+  QMM_CASE(C_F16, C_F16, launch_f16_f16)
+  QMM_CASE(C_F16, C_Q8_0, launch_f16_q8)
+  QMM_CASE(C_F16, C_Q4_0, launch_f16_q4)
+  QMM_CASE(C_Q8_0, C_F16, launch_q8_f16)
+  QMM_CASE(C_Q8_0, C_Q8_0, launch_q8_q8)
+  QMM_CASE(C_Q8_0, C_Q4_0, launch_q8_q4)
+  QMM_CASE(C_Q4_0, C_F16, launch_q4_f16)
+  QMM_CASE(C_Q4_0, C_Q8_0, launch_q4_q8)
+  QMM_CASE(C_Q4_0, C_Q4_0, launch_q4_q4)
+#undef QMM_CASE
+  if (e != hipSuccess) return e;
+  const dim3 grid((unsigned)(a.B * a.n_q));
+  if (d.f16) hipLaunchKernelGGL(join_kernel<_Float16>, grid, dim3(256), 0, s, a, (int)kc.head_dim);
+  else hipLaunchKernelGGL(join_kernel<float>, grid, dim3(256), 0, s, a, (int)kc.head_dim);
+  return hipGetLastError();
+}
+
+}  // namespace qmm

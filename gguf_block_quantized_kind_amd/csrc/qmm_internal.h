@@ -140,4 +140,49 @@ hipError_t launch_moe_t1(int kind, const uint8_t *W, const void *X, int x_f16, f
 hipError_t launch_moe_mfma(int kind, const uint8_t *W, const void *X, int x_f16, float *Y, int mt, int64_t N,
                            int64_t K, const MoeRoute &rt, int items, hipStream_t s, bool packed = false);
 
+// The paged key/value cache (qmm_kv.h) and what reads and writes it.  Kinds
+// are GGUF type ids: 1 (F16), 8 (Q8_0), 2 (Q4_0).
+struct KvCache {
+  int k_kind, v_kind;
+  void *k_pages, *v_pages;
+  int64_t n_pages, page_size, n_kv, head_dim;
+};
+// New tokens: k and v rows [T][n_kv][head_dim] (row strides in elements) to
+// the tokens' slots, k rotated first if rope is set; q rows [T][n_q][head_dim]
+// rotated into q_out.  launch_rope takes the rotation and q alone (n_q and
+// head_dim as arguments).
+struct KvWrite {
+  const void *q, *k, *v;
+  void *q_out;
+  int64_t q_stride, k_stride, v_stride, q_out_stride;
+  int f16, q_out_f16;  // q, k, v (else f32); q_out
+  const int32_t *pos, *slots;
+  int64_t T, n_q;
+  int rope;
+  const double *freqs;
+  int64_t n_rot;
+  int interleaved;
+  float mscale;
+};
+struct AttnDecode {
+  const void *q;
+  int64_t q_stride;
+  int f16;
+  int64_t n_q, B;
+  const int32_t *table;
+  int64_t max_pages;
+  const int32_t *lens;
+  float scale;
+  int64_t window;
+  const float *sinks;
+  void *out, *workspace;
+};
+int64_t kv_page_bytes(int kind, int64_t page_size, int64_t n_kv, int64_t head_dim);
+hipError_t launch_rope(const KvWrite &w, int64_t H, int64_t D, hipStream_t s);
+hipError_t launch_kv_write(const KvCache &c, const KvWrite &w, hipStream_t s);
+hipError_t launch_kv_read(const KvCache &c, const int32_t *slots, int64_t T, void *k_out, void *v_out, int f16,
+                          hipStream_t s);
+size_t attn_workspace_bytes(int64_t B, int64_t n_q, int64_t n_kv, int64_t head_dim);
+hipError_t launch_attn_decode(const KvCache &c, const AttnDecode &d, hipStream_t s);
+
 }  // namespace qmm

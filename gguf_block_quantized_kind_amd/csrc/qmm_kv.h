@@ -1,0 +1,157 @@
+// qmm_kv.h -- the paged key/value cache: where its bytes lie, and the block
+// quantizer and rotation shared by the kernels that write it.
+//
+// A page holds page_size tokens of n_kv heads; page_size is a multiple of 32
+// and the unit is a group of 32 consecutive tokens of one head:
+//
+//   page = [head][page_size / 32 groups], group = codes, then scales
+//   codes  NB = head_dim / 32 blocks of 32 elements x 32 tokens, each laid
+//          out as the lanes of v_mfma_f32_16x16x32_f16 read it (below)
+//   scales (Q8_0, Q4_0) f16 [NB][32 tokens]
+//
+// so a group is 32 * qmm_row_bytes-like bytes (2, 34/32 or 18/32 bytes per
+// element) and every byte of it is read by whole 8- or 16-byte lane loads.
+//
+// In a key block the matrix-core rows are tokens and its K dimension the
+// elements; in a value block the rows are elements and K the tokens.  Lane
+// (i, G) of a wave (i = lane % 16, G = lane / 16) holds, of row i, the K
+// entries 8G .. 8G + 7 (Q4_0 keys: the elements 4G .. 4G + 3 and 16 + those,
+// two to a byte).  There are two row tiles per block:
+//   keys    tile m, row i = token 8 (i / 4) + 4 m + i % 4, so that the rows
+//           4G + r of a lane's score registers are tokens 8G + 4m + r: the
+//           eight tokens whose weights the same lane supplies as the K
+//           entries of the value product, with no movement between lanes;
+//   values  tile x, row j = element 16 x + j.
+//   F16     [tile][G][row][8] halves           1024 bytes per tile
+//   Q8_0    [G][row][tile][8] bytes, code + 128
+//   Q4_0    keys [G][row][tile][4] bytes, byte y = elements 4G + y (low
+//           nibble) and 16 + 4G + y (high); values [G][row][8 tokens] bytes,
+//           elements row (low) and 16 + row (high); codes 0 .. 15 = value / d + 8
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace qmm {
+namespace kv {
+
+// Cache kinds by GGUF type id.
+enum CacheKind : int { C_F16 = 1, C_Q4_0 = 2, C_Q8_0 = 8 };
+
+constexpr int kGroup = 32;  // tokens per group
+
+// Bytes of one block (32 elements x 32 tokens) without its scales, and of a
+// group of NB blocks with them.
+__host__ __device__ constexpr int block_code_bytes(int kind) {
+  return kind == C_F16 ? 2048 : kind == C_Q8_0 ? 1024 : 512;
+}
+__host__ __device__ constexpr int group_bytes(int kind, int NB) {
+  return NB * (block_code_bytes(kind) + (kind == C_F16 ? 0 : 64));
+}
+
+// Byte of (block b, token r of the group, element c of the block) in a group;
+// Q4_0: the byte holding it (nibble c / 16).
+template <int KIND, bool IS_V>
+__device__ __forceinline__ int code_offset(int b, int r, int c) {
+  const int base = b * block_code_bytes(KIND);
+  if constexpr (!IS_V) {
+    const int i = 4 * (r >> 3) + (r & 3), m = (r >> 2) & 1;
+    if constexpr (KIND == C_F16) return base + ((m * 4 + (c >> 3)) * 16 + i) * 16 + (c & 7) * 2;
+    if constexpr (KIND == C_Q8_0) return base + (((c >> 3) * 16 + i) * 2 + m) * 8 + (c & 7);
+    return base + ((((c & 15) >> 2) * 16 + i) * 2 + m) * 4 + (c & 3);
+  } else {
+    const int G = r >> 3, e = r & 7;
+    if constexpr (KIND == C_F16) return base + (((c >> 4) * 4 + G) * 16 + (c & 15)) * 16 + e * 2;
+    if constexpr (KIND == C_Q8_0) return base + ((G * 16 + (c & 15)) * 2 + (c >> 4)) * 8 + e;
+    return base + (G * 16 + (c & 15)) * 8 + e;
+  }
+}
+__device__ __forceinline__ int scale_offset(int kind, int NB, int b, int r) {
+  return NB * block_code_bytes(kind) + (b * kGroup + r) * 2;
+}
+
+// The smallest f16 not below d >= 0, at most 65504 (rounding the step up keeps
+// every code in its range, so the error of a code is at most half a step).
+__device__ __forceinline__ _Float16 f16_up(float d) {
+  _Float16 h = (_Float16)fminf(d, 65504.0f);
+  if ((float)h < d && (float)h < 65504.0f)
+    h = __builtin_bit_cast(_Float16, (uint16_t)(__builtin_bit_cast(uint16_t, h) + 1));
+  return h;
+}
+
+// The scale of a block from its largest and smallest element; `bits` is the
+// largest bit pattern of |x|, which tells an infinity or NaN: such a block
+// gets a NaN scale and reads back as NaN throughout.
+template <int KIND>
+__device__ __forceinline__ _Float16 block_scale(float hi, float lo, uint32_t bits) {
+  if (bits >= 0x7f800000u) return __builtin_bit_cast(_Float16, (uint16_t)0x7e00);
+  _Float16 h = f16_up(fabsf(fmaxf(hi, -lo)) / (KIND == C_Q8_0 ? 127.0f : 8.0f));
+  if (KIND == C_Q4_0 && hi >= -lo && h != (_Float16)0.0f) h = -h;  // the extreme element becomes code 0: -8 d
+  return h;
+}
+
+// The stored code of x under scale h: the nearest integer to the correctly
+// rounded x / h, ties to even.
+template <int KIND>
+__device__ __forceinline__ uint32_t encode(float x, _Float16 h) {
+  const float d = (float)h;
+  float q = (d == 0.0f || d != d) ? 0.0f : rintf(x / d);
+  if constexpr (KIND == C_Q8_0) return (uint32_t)((int)fminf(fmaxf(q, -127.0f), 127.0f) + 128);
+  return (uint32_t)(int)fminf(fmaxf(q + 8.0f, 0.0f), 15.0f);
+}
+
+// cos and sin of pos * freq (radians per position), each within about 1e-7.
+// The angle is reduced in 64 bits to an eighth of a turn: a 32-bit angle at
+// position 10^6 would already be off by 0.06.  The rest is the Taylor series
+// on |x| <= pi / 4, whose first omitted terms are below 2e-9.
+__device__ __forceinline__ void rotation(int pos, double freq, float &c, float &s) {
+  double t = (double)pos * freq * 0.15915494309189533577;  // turns
+  t -= rint(t);
+  const double q = rint(4.0 * t);
+  const float x = (float)((t - 0.25 * q) * 6.283185307179586477);
+  const float z = x * x;
+  float sp = __builtin_fmaf(z, 2.7557319e-6f, -1.9841270e-4f);
+  sp = __builtin_fmaf(z, sp, 8.3333333e-3f);
+  sp = __builtin_fmaf(z, sp, -1.6666667e-1f);
+  sp = __builtin_fmaf(z * x, sp, x);
+  float cp = __builtin_fmaf(z, -2.7557319e-7f, 2.4801587e-5f);
+  cp = __builtin_fmaf(z, cp, -1.3888889e-3f);
+  cp = __builtin_fmaf(z, cp, 4.1666667e-2f);
+  cp = __builtin_fmaf(z, cp, -0.5f);
+  cp = __builtin_fmaf(z, cp, 1.0f);
+  const int k = (int)q & 3;
+  const float a = (k & 1) ? sp : cp, b = (k & 1) ? cp : sp;
+  c = (k == 1 || k == 2) ? -a : a;
+  s = (k & 2) ? -b : b;
+}
+
+struct Rope {
+  const double *freqs;  // n_rot / 2 radians per position
+  int n_rot;
+  int interleaved;
+  float mscale;
+};
+
+// Row t of x[T][H][D] starts at t * stride elements.
+struct Rows {
+  const void *x;
+  int64_t stride;
+  int f16;
+};
+template <typename T>
+__device__ __forceinline__ float at(const void *x, int64_t i) { return (float)((const T *)x)[i]; }
+
+struct Cache {
+  uint8_t *k_pages, *v_pages;
+  int64_t n_slots;  // n_pages * page_size
+  int page_size, n_kv, NB;
+};
+
+// First byte of the group of (slot, head).
+__device__ __forceinline__ int64_t group_at(const Cache &c, int kind, int slot, int head) {
+  const int page = slot / c.page_size, g = (slot - page * c.page_size) / kGroup, groups = c.page_size / kGroup;
+  return (((int64_t)page * c.n_kv + head) * groups + g) * group_bytes(kind, c.NB);
+}
+
+}  // namespace kv
+}  // namespace qmm

@@ -366,6 +366,154 @@ int qmm_gemv_i8_noalloc(int kind, const void *P, const void *x, int x_dtype, flo
  * blocks (QMM_ERR_K_NOT_BLOCK_ALIGNED), NULL pointers (QMM_ERR_BAD_ARG). */
 int qmm_dequant(int kind, const void *W, float *out, int64_t n_elems, void *stream);
 
+/* ------------------------------------------------------------------------
+ * The attention side of a decode step: rotary positions, a paged key/value
+ * cache held in block formats, and attention of one new token per sequence
+ * over it.  Model semantics beyond the pages, like qmm_moe_ffn; these are the
+ * operators between the projections that the products above compute.
+ *
+ * The cache of a layer is two arrays of pages, one for keys and one for
+ * values, each page holding page_size tokens of n_kv heads of head_dim
+ * elements in one of three kinds (the two arrays may differ):
+ *   QMM_CACHE_F16   2 bytes an element, rounded to nearest (|x| <= 65504)
+ *   QMM_Q8_0        32-element blocks, value d * c, c in [-127, 127]:
+ *                   d = the smallest f16 >= max|x| / 127 (at most 65504),
+ *                   c = RNE(x / d)
+ *   QMM_Q4_0        value d * (c - 8), c in [0, 15]: |d| = the smallest f16 >=
+ *                   max|x| / 8 with the sign that makes the largest element
+ *                   (the positive one at a tie) code 0, c = RNE(x / d) + 8,
+ *                   at most 15
+ * with f32 quotients; |value - x| <= |d| / 2 except where a Q4_0 code was cut
+ * to 15 (up to |d|).  A block holding an infinity or a NaN reads back as NaN.
+ * page_size is a multiple of 32 (at most 65536) and head_dim one of 64, 96,
+ * 128, 192, 256.  A page is qmm_kv_page_bytes(...) bytes, 16-byte aligned, and
+ * holds [n_kv][page_size / 32] groups of 32 tokens; a group is its codes
+ * followed by its f16 scales (none for F16) as [head_dim / 32][32 tokens].
+ * The codes of block b (elements 32b + c) of the group's token r (base =
+ * b * 2048 bytes for F16, 1024 Q8_0, 512 Q4_0; i = 4 (r / 8) + r % 4,
+ * m = (r / 4) % 2, integer division):
+ *   keys    F16   half  at ((4m + c/8) * 16 + i) * 16 + 2 (c % 8)
+ *           Q8_0  c+128 at ((16 (c/8) + i) * 2 + m) * 8 + c % 8
+ *           Q4_0  byte  at ((16 (c%16/4) + i) * 2 + m) * 4 + c % 4, elements
+ *                 below 16 in the low nibble
+ *   values  F16   half  at ((4 (c/16) + r/8) * 16 + c % 16) * 16 + 2 (r % 8)
+ *           Q8_0  c+128 at ((16 (r/8) + c % 16) * 2 + c/16) * 8 + r % 8
+ *           Q4_0  byte  at (16 (r/8) + c % 16) * 8 + r % 8, same nibbles
+ * A page need not be initialized: bytes of tokens that no call has written
+ * are never given weight, whatever they hold.
+ *
+ * A slot names a token's place: slot = page * page_size + offset, int32,
+ * with n_pages * page_size below 2^31.  A slot outside [0, n_pages *
+ * page_size) marks a token to skip (padding): nothing is written for it, and
+ * it reads as zeros.  Two tokens of one call must
+ * not name the same slot (that slot's contents are then unspecified).
+ *
+ * Row strides are in elements: row t of a [T][H][head_dim] operand starts at
+ * t * stride, its heads packed (stride >= H * head_dim), so that the q, k and
+ * v parts of one projection's output need no copies.
+ * --------------------------------------------------------------------- */
+#define QMM_CACHE_F16 1
+int64_t qmm_kv_page_bytes(int kind, int64_t page_size, int64_t n_kv, int64_t head_dim); /* -1: refused */
+
+/* How the pairs of the rotated part of a head lie: (i, i + n_rot/2) or
+ * (2i, 2i + 1). */
+enum qmm_rope_layout { QMM_ROPE_HALF = 0, QMM_ROPE_INTERLEAVED = 1 };
+
+/* Angles per position of the n_rot / 2 pairs, on the HOST (no GPU work; the
+ * caller copies them to the device once): freqs[i] = base^(-2i / n_rot),
+ * divided by factors[i] if factors is not NULL (the per-pair factors some
+ * GGUF files carry), then for factor > 1
+ *   orig_ctx = 0   divided by factor (positions interpolated linearly);
+ *   orig_ctx > 0   YaRN: with dim(n) = n_rot ln(orig_ctx / (2 pi n)) /
+ *                  (2 ln base), low = max(floor(dim(beta_fast)), 0), high =
+ *                  min(ceil(dim(beta_slow)), n_rot - 1) and ramp = clamp((i -
+ *                  low) / max(high - low, 0.001), 0, 1), the mean of freqs[i]
+ *                  (weight 1 - ramp) and freqs[i] / factor (ramp).
+ * *mscale (if not NULL) becomes 0.1 ln(factor) + 1 for YaRN, else 1.
+ * Errors: n_rot <= 0 QMM_ERR_EMPTY_SHAPE; odd n_rot, NULL freqs, base <= 1,
+ * factor < 1 (or not finite), negative orig_ctx, or YaRN without
+ * beta_fast > beta_slow > 0 QMM_ERR_BAD_ARG. */
+int qmm_rope_freqs(double *freqs, float *mscale, int64_t n_rot, double base, const float *factors, double factor,
+                   int64_t orig_ctx, double beta_fast, double beta_slow);
+
+/* Rotary positions: y = x with, in every head of row t, pair (a, b) number i
+ * turned by phi = pos[t] * freqs[i] (freqs: n_rot / 2 f64 on the device):
+ *   y_a = mscale (x_a cos phi - x_b sin phi)
+ *   y_b = mscale (x_a sin phi + x_b cos phi);
+ * elements n_rot .. head_dim - 1 are copied.  The angle is reduced in 64
+ * bits, so far positions lose nothing; cos, sin and the products are f32
+ * (within 2^-21 mscale (|x_a| + |x_b|), before the rounding to f16).  x is [T][H][head_dim] f32 or f16, y
+ * f32 or f16, head_dim and n_rot even, n_rot <= head_dim.  y may be x itself
+ * (same stride and type); any other overlap is not allowed.
+ * Errors: a zero dimension, dtype, then pointers, alignment, strides, layout,
+ * n_rot and T * H * head_dim > 2^32 as QMM_ERR_BAD_ARG. */
+int qmm_rope(const double *freqs, int64_t n_rot, int layout, float mscale, const int32_t *pos, const void *x,
+             int x_dtype, int64_t x_stride, void *y, int y_dtype, int64_t y_stride, int64_t T, int64_t H,
+             int64_t head_dim, void *stream);
+
+/* Writes T tokens' keys and values ([T][n_kv][head_dim], both of `dtype`) into
+ * the cache at their slots.  Errors: a zero dimension, unsupported kinds,
+ * head_dim not a multiple of 32 (QMM_ERR_K_NOT_BLOCK_ALIGNED), dtype, then
+ * QMM_ERR_BAD_ARG for any other head_dim or page_size, n_kv > 1024, T * n_kv *
+ * head_dim >= 2^31, NULL or misaligned pointers and short strides. */
+int qmm_kv_write(int k_kind, int v_kind, void *k_pages, void *v_pages, int64_t n_pages, int64_t page_size,
+                 int64_t n_kv, int64_t head_dim, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                 int dtype, const int32_t *slots, int64_t T, void *stream);
+
+/* qmm_rope on q and k and qmm_kv_write of the rotated k and of v, in one
+ * launch: what a decode step does between the projections and the
+ * attention.  q is [T][n_q][head_dim] of `dtype`, q_out of q_out_dtype (it may
+ * be q itself, as in qmm_rope); the rotated k is quantized from f32.  Tokens
+ * with a skipped slot still get their q rows.  Errors as qmm_kv_write (with T *
+ * (n_q + n_kv) * head_dim below 2^31) and qmm_rope. */
+int qmm_kv_append(const double *freqs, int64_t n_rot, int layout, float mscale, const int32_t *pos, const void *q,
+                  int64_t q_stride, int64_t n_q, void *q_out, int q_out_dtype, int64_t q_out_stride, int k_kind,
+                  int v_kind, void *k_pages, void *v_pages, int64_t n_pages, int64_t page_size, int64_t n_kv,
+                  int64_t head_dim, const void *k, int64_t k_stride, const void *v, int64_t v_stride, int dtype,
+                  const int32_t *slots, int64_t T, void *stream);
+
+/* Reads T tokens back: k_out and v_out [T][n_kv][head_dim], contiguous, f32
+ * (exact) or f16 (the value rounded once).  Errors as qmm_kv_write. */
+int qmm_kv_read(int k_kind, int v_kind, const void *k_pages, const void *v_pages, int64_t n_pages, int64_t page_size,
+                int64_t n_kv, int64_t head_dim, const int32_t *slots, int64_t T, void *k_out, void *v_out, int dtype,
+                void *stream);
+
+/* Attention of one new token per sequence: for sequence b and query head h,
+ * with key head h / (n_q / n_kv),
+ *   s_t = scale * q . k_t,  out = sum_t e^{s_t} v_t / (sum_t e^{s_t} + e^{sinks[h]})
+ * over the tokens max(0, len - window) <= t < len, len = seq_lens[b] (window 0:
+ * all of them; sinks NULL: no such term).  Token t lies in page
+ * block_table[b * max_pages + t / page_size] at offset t % page_size.  The new
+ * token's own key and value are part of the cache (qmm_kv_append first).  q is
+ * [B][n_q][head_dim] f32 or f16 with a row stride, out [B][n_q][head_dim],
+ * contiguous, of the same type.  A sequence without tokens (length 0 or
+ * below) gives zeros; lengths are cut to max_pages * page_size; tokens whose
+ * page number lies outside [0, n_pages) count as absent.
+ * Numerics: keys and values are exact (codes as integers, block scales in
+ * f32 or folded into the weight); scores, softmax and sums are f32.  f16 q is
+ * exact and the weights are rounded once to f16; f32 q and weights are carried
+ * as two f16 terms (relative 2^-21).  With w_t the exact weights,
+ *   |out - exact| <= (r + 2 max_t e_t) sum_t w_t |v_t|  (+ f16 out's rounding)
+ * where r = 2^-11 + 2^-18 for f16 and 2^-18 for f32, and e_t = c (scale * sum
+ * over 32-element blocks of (sum |q|) (max |k_t|) + max |s| + 40) with c =
+ * 2^-17 for f16 and 2^-20 for f32 bounds a score's error.  The order of every sum is fixed: a call repeated gives the
+ * same bits.
+ * n_q is a multiple of n_kv.  workspace: qmm_attn_decode_workspace_bytes(B,
+ * n_q, n_kv, head_dim) bytes, 16-byte aligned, overwritten (it need not be
+ * initialized); calls sharing it must not overlap.  Nothing depends on the
+ * host's knowledge of the lengths, so a captured call replays with others.
+ * Errors: a zero dimension, kinds and head_dim as qmm_kv_write, dtype, then
+ * QMM_ERR_BAD_ARG (n_q not a multiple of n_kv, B * n_q > 2^23, max_pages *
+ * page_size >= 2^31, scale not finite, window < 0, pointers, alignment, stride), then QMM_ERR_WORKSPACE. */
+int qmm_attn_decode(int k_kind, int v_kind, const void *k_pages, const void *v_pages, int64_t n_pages,
+                    int64_t page_size, int64_t n_kv, int64_t head_dim, const void *q, int dtype, int64_t q_stride,
+                    int64_t n_q, const int32_t *block_table, int64_t max_pages, const int32_t *seq_lens, int64_t B,
+                    float scale, int64_t window, const float *sinks, void *out, void *workspace,
+                    size_t workspace_bytes, void *stream);
+/* 0 for a non-positive argument, n_q not a multiple of n_kv or sizes
+ * qmm_attn_decode refuses. */
+size_t qmm_attn_decode_workspace_bytes(int64_t B, int64_t n_q, int64_t n_kv, int64_t head_dim);
+
 /* Geometry and names.  qmm_row_bytes is the expected row length of
  * ferrox-cuda mul_mm.rs validate_shape ((K / block_elems) * block_bytes),
  * -1 for a bad kind or K not a whole number of blocks.  qmm_block_geometry
