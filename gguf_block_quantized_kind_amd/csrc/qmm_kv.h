@@ -90,12 +90,29 @@ __device__ __forceinline__ _Float16 block_scale(float hi, float lo, uint32_t bit
   return h;
 }
 
-// The stored code of x under scale h: the nearest integer to the correctly
-// rounded x / h, ties to even.
-template <int KIND>
-__device__ __forceinline__ uint32_t encode(float x, _Float16 h) {
+// The bits of |x|: above 0x7f7fffff for an infinity or NaN.  (A function: a bit
+// cast of a vector's element in place reads the vector's first element.)
+__device__ __forceinline__ uint32_t magnitude_bits(float x) { return __builtin_bit_cast(uint32_t, x) & 0x7fffffffu; }
+
+// A block's step and its reciprocal, each correctly rounded (both 0 where
+// every code is that of zero: a zero or NaN scale).
+struct Step {
+  float d, inv;
+};
+__device__ __forceinline__ Step step_of(_Float16 h) {
   const float d = (float)h;
-  float q = (d == 0.0f || d != d) ? 0.0f : rintf(x / d);
+  const bool none = d == 0.0f || d != d;
+  return Step{none ? 0.0f : d, none ? 0.0f : 1.0f / d};
+}
+
+// The stored code of x: the nearest integer to the correctly rounded x / d,
+// ties to even.  With inv the correctly rounded 1 / d, one residual step makes
+// the quotient correctly rounded (Markstein, IBM J. Res. Dev. 34, 1990): three
+// operations an element instead of a division's dozen.
+template <int KIND>
+__device__ __forceinline__ uint32_t encode(float x, Step st) {
+  const float q0 = x * st.inv;
+  const float q = st.inv == 0.0f ? 0.0f : rintf(__builtin_fmaf(__builtin_fmaf(-st.d, q0, x), st.inv, q0));
   if constexpr (KIND == C_Q8_0) return (uint32_t)((int)fminf(fmaxf(q, -127.0f), 127.0f) + 128);
   return (uint32_t)(int)fminf(fmaxf(q + 8.0f, 0.0f), 15.0f);
 }
@@ -132,15 +149,6 @@ struct Rope {
   float mscale;
 };
 
-// Row t of x[T][H][D] starts at t * stride elements.
-struct Rows {
-  const void *x;
-  int64_t stride;
-  int f16;
-};
-template <typename T>
-__device__ __forceinline__ float at(const void *x, int64_t i) { return (float)((const T *)x)[i]; }
-
 struct Cache {
   uint8_t *k_pages, *v_pages;
   int64_t n_slots;  // n_pages * page_size
@@ -151,6 +159,102 @@ struct Cache {
 __device__ __forceinline__ int64_t group_at(const Cache &c, int kind, int slot, int head) {
   const int page = slot / c.page_size, g = (slot - page * c.page_size) / kGroup, groups = c.page_size / kGroup;
   return (((int64_t)page * c.n_kv + head) * groups + g) * group_bytes(kind, c.NB);
+}
+
+// Rotation of whole rows, V pairs of every head of a range per thread: the
+// angle costs about sixty operations (half of them 64-bit), so each is used
+// for as many heads as leave the grid full.
+struct Rotate {
+  const void *x;
+  void *y;
+  int64_t x_stride, y_stride;
+  const int32_t *pos;
+  int64_t T;
+  int H, D, per;       // heads per thread
+  int chunks, ranges;  // D / 2 / V, ceil(H / per)
+  Rope rope;
+};
+template <typename T, int V>
+struct Vec {
+  typedef T type __attribute__((ext_vector_type(V)));
+};
+template <typename T>
+struct Vec<T, 1> {
+  struct type {
+    T v;
+    __device__ __forceinline__ T &operator[](int) { return v; }
+  };
+};
+template <typename T, typename O, int V>
+__device__ __forceinline__ void rotate_rows(const Rotate &r, int64_t i) {
+  using X = typename Vec<T, V>::type;
+  using Y = typename Vec<O, V>::type;
+  const int per_token = r.chunks * r.ranges;
+  const int64_t t = i / per_token;
+  if (t >= r.T) return;
+  const int rest = (int)(i - t * per_token), range = rest / r.chunks, p = (rest - range * r.chunks) * V;
+  const int half = r.rope.n_rot >> 1;
+  const bool turned = p < half, split = turned && !r.rope.interleaved;
+  // Elements [da, da + V) and [db, db + V): the two members of V pairs, or (interleaved, passing) 2 V neighbours.
+  const int da = split ? p : 2 * p, db = split ? p + half : 2 * p + V;
+  float c[V], s[V];
+#pragma unroll
+  for (int k = 0; k < V; ++k) {
+    c[k] = 1.0f;
+    s[k] = 0.0f;
+    if (turned) {
+      rotation(r.pos[t], r.rope.freqs[p + k], c[k], s[k]);
+      c[k] *= r.rope.mscale;
+      s[k] *= r.rope.mscale;
+    }
+  }
+  const int h1 = min(r.H, (range + 1) * r.per);
+  const T *x = (const T *)r.x + t * r.x_stride;
+  O *y = (O *)r.y + t * r.y_stride;
+  for (int h = range * r.per; h < h1; ++h) {
+    X a, b;
+    __builtin_memcpy(&a, __builtin_assume_aligned(x + (int64_t)h * r.D + da, sizeof(X)), sizeof(X));
+    __builtin_memcpy(&b, __builtin_assume_aligned(x + (int64_t)h * r.D + db, sizeof(X)), sizeof(X));
+    Y u, v;
+    if (!turned) {
+#pragma unroll
+      for (int k = 0; k < V; ++k) u[k] = (O)(float)a[k], v[k] = (O)(float)b[k];
+    } else if (split) {
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        u[k] = (O)((float)a[k] * c[k] - (float)b[k] * s[k]);
+        v[k] = (O)((float)a[k] * s[k] + (float)b[k] * c[k]);
+      }
+    } else if constexpr (V == 1) {
+      u[0] = (O)((float)a[0] * c[0] - (float)b[0] * s[0]);
+      v[0] = (O)((float)a[0] * s[0] + (float)b[0] * c[0]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < V; k += 2) {
+        u[k] = (O)((float)a[k] * c[k / 2] - (float)a[k + 1] * s[k / 2]);
+        u[k + 1] = (O)((float)a[k] * s[k / 2] + (float)a[k + 1] * c[k / 2]);
+        v[k] = (O)((float)b[k] * c[(V + k) / 2] - (float)b[k + 1] * s[(V + k) / 2]);
+        v[k + 1] = (O)((float)b[k] * s[(V + k) / 2] + (float)b[k + 1] * c[(V + k) / 2]);
+      }
+    }
+    __builtin_memcpy(__builtin_assume_aligned(y + (int64_t)h * r.D + da, sizeof(Y)), &u, sizeof(Y));
+    __builtin_memcpy(__builtin_assume_aligned(y + (int64_t)h * r.D + db, sizeof(Y)), &v, sizeof(Y));
+  }
+}
+
+// Fills in the split of T rows of H heads; four pairs a thread where every
+// vector they make is aligned, else one.
+inline bool plan_rotate(Rotate &r, int x_bytes, int y_bytes, int64_t &threads) {
+  const int v = 4;
+  const bool wide = r.D % (2 * v) == 0 && r.rope.n_rot % (2 * v) == 0 && r.x_stride % v == 0 && r.y_stride % v == 0 &&
+                    (uintptr_t)r.x % (v * x_bytes) == 0 && (uintptr_t)r.y % (v * y_bytes) == 0;
+  r.chunks = r.D / 2 / (wide ? v : 1);
+  // Heads per thread: one until the grid holds eight waves per SIMD.
+  const int64_t one = r.T * r.chunks * r.H, full = (int64_t)256 * 4 * 8 * 64;
+  r.per = (int)(one / full < 1 ? 1 : one / full > r.H ? r.H : one / full);
+  r.ranges = (r.H + r.per - 1) / r.per;
+  threads = r.T * r.chunks * r.ranges;
+  return wide;
 }
 
 }  // namespace kv

@@ -1,158 +1,369 @@
 // qmm_kv.hip -- writing new tokens into the paged key/value cache (quantized
 // to its kind, with or without the rotation of the keys and queries) and
 // reading tokens back.  Layout and quantizer: qmm_kv.h.
+//
+// Both kernels give a workgroup a window of 32 tokens of one head's keys or
+// values and pass it through LDS, because rows lie along the elements and
+// cache units across tokens:
+//   write  rows -> LDS (f32; rotated there), block scales, then every thread
+//          encodes the elements of one cache unit and stores it: 16, 8 or 4
+//          bytes of one key token, or eight tokens of an element pair of the
+//          values.
+//   read   the reverse; keys need no LDS, a unit of theirs being a run of one
+//          row's elements.
+// Value units hold eight consecutive tokens.  The window's tokens are taken in
+// octets that start where the first token's slot is a multiple of eight, so a
+// prompt's tokens fill whole units wherever it starts; an octet whose slots
+// are not eight consecutive aligned ones (other sequences, skipped tokens, the
+// window's ends) goes byte by byte.
 #include "qmm_internal.h"
 #include "qmm_kv.h"
 
 namespace qmm {
 namespace kv {
 
-// One rotated element d of a row: x[d] with its partner of the pair.
-template <typename T>
-__device__ __forceinline__ float rotated(const Rope &rp, const T *x, int d, int pos) {
-  const float v = (float)x[d];
-  if (d >= rp.n_rot) return v;
-  const int half = rp.n_rot >> 1;
-  const bool second = rp.interleaved ? (d & 1) : d >= half;
-  const int pair = rp.interleaved ? d >> 1 : second ? d - half : d;
-  const int other = rp.interleaved ? d ^ 1 : second ? d - half : d + half;
-  float c, s;
-  rotation(pos, rp.freqs[pair], c, s);
-  c *= rp.mscale;
-  s *= rp.mscale;
-  const float u = (float)x[other];
-  return second ? u * s + v * c : v * c - u * s;
+typedef float floatx4 __attribute__((ext_vector_type(4)));
+typedef _Float16 half4 __attribute__((ext_vector_type(4)));
+typedef _Float16 half8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+constexpr int kWindow = 32;
+constexpr int kOctets = kWindow / 8 + 1;
+
+// Where the window's tokens lie.
+struct Window {
+  int64_t base[kWindow];  // first byte of the token's group
+  int slot[kWindow];      // -1: skipped or past the end
+  int r[kWindow];         // token of its group
+  int whole[kOctets];     // the octet is one aligned unit
+  int phase;              // octet o covers tokens 8 o - phase + [0, 8)
+};
+
+__device__ __forceinline__ void find_window(Window &w, const Cache &c, const int32_t *slots, int64_t t0, int nt, int kind,
+                                            int head) {
+  const int tid = threadIdx.x;
+  if (tid < kWindow) {
+    int slot = tid < nt ? slots[t0 + tid] : -1;
+    if (slot >= c.n_slots) slot = -1;
+    slot = max(slot, -1);
+    w.slot[tid] = slot;
+    w.base[tid] = slot < 0 ? 0 : group_at(c, kind, slot, head);
+    w.r[tid] = slot < 0 ? 0 : (slot % c.page_size) % kGroup;
+    if (tid == 0) w.phase = slot < 0 ? 0 : slot % 8;
+  }
+  __syncthreads();
+  if (tid < kOctets) {
+    const int t = 8 * tid - w.phase;
+    bool whole = t >= 0 && t + 8 <= kWindow && w.slot[max(t, 0)] >= 0 && w.slot[max(t, 0)] % 8 == 0;
+    for (int e = 1; e < 8 && whole; ++e) whole = w.slot[t + e] == w.slot[t] + e;
+    w.whole[tid] = whole;
+  }
 }
 
-// One block of 32 elements per half wave: lane c holds element c.
-template <int KIND, bool IS_V>
-__device__ __forceinline__ void store_block(uint8_t *group, int NB, int b, int r, int c, float x) {
-  uint8_t *p = group + code_offset<KIND, IS_V>(b, r, c);
-  if constexpr (KIND == C_F16) {
-    *(_Float16 *)p = (_Float16)x;
-  } else {
-    float hi = x, lo = x;
-    uint32_t bits = __builtin_bit_cast(uint32_t, x) & 0x7fffffffu;
+template <typename T>
+__device__ __forceinline__ floatx4 load4(const T *x, bool vec) {
+  if (vec) {
+    typename Vec<T, 4>::type v;
+    __builtin_memcpy(&v, __builtin_assume_aligned(x, 4 * sizeof(T)), sizeof v);
+    return floatx4{(float)v[0], (float)v[1], (float)v[2], (float)v[3]};
+  }
+  return floatx4{(float)x[0], (float)x[1], (float)x[2], (float)x[3]};
+}
+
+__device__ __forceinline__ uint32_t pack_h(float a, float b) {
+  return (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)a) | (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)b) << 16;
+}
+
+// One head's keys or values of a window: rows x + t * stride.
+template <int KIND, bool IS_V, typename T, bool ROPE>
+__device__ __forceinline__ void write_window(const Cache &c, uint8_t *pages, const T *x, int64_t stride, bool vec, int nt,
+                                             const int32_t *pos, const Rope &rope, const Window &w, float *rows,
+                                             Step *steps) {
+  const int tid = threadIdx.x, NB = c.NB, D = NB * 32, pitch = D + 4;
+  for (int i = tid; i < nt * (D / 4); i += 256) {
+    const int t = i / (D / 4), d = (i - t * (D / 4)) * 4;
+    if (w.slot[t] >= 0) *(floatx4 *)(rows + t * pitch + d) = load4(x + t * stride + d, vec);
+  }
+  __syncthreads();
+  if constexpr (ROPE) {
+    const int half = rope.n_rot >> 1;
+    for (int i = tid; i < nt * half; i += 256) {
+      const int t = i / half, p = i - t * half;
+      if (w.slot[t] < 0) continue;
+      float *a = rows + t * pitch + (rope.interleaved ? 2 * p : p), *b = a + (rope.interleaved ? 1 : half);
+      float co, si;
+      rotation(pos[t], rope.freqs[p], co, si);
+      co *= rope.mscale;
+      si *= rope.mscale;
+      const float u = *a, v = *b;
+      *a = u * co - v * si;
+      *b = u * si + v * co;
+    }
+    __syncthreads();
+  }
+  if constexpr (KIND != C_F16) {
+    // Four lanes per (token, block), eight elements each.
+    for (int i = tid; i < NB * kWindow * 4; i += 256) {
+      const int t = (i >> 2) & (kWindow - 1), b = i >> 7;
+      if (w.slot[t] < 0) continue;
+      const float *e = rows + t * pitch + b * 32 + (i & 3) * 8;
+      const floatx4 u = *(const floatx4 *)e, v = *(const floatx4 *)(e + 4);
+      float hi = u[0], lo = u[0];
+      uint32_t bits = 0;
 #pragma unroll
-    for (int k = 16; k; k >>= 1) {
-      hi = fmaxf(hi, __shfl_xor(hi, k, 32));
-      lo = fminf(lo, __shfl_xor(lo, k, 32));
-      bits = max(bits, (uint32_t)__shfl_xor((int)bits, k, 32));
+      for (int k = 0; k < 4; ++k) {
+        hi = fmaxf(hi, fmaxf(u[k], v[k]));
+        lo = fminf(lo, fminf(u[k], v[k]));
+        bits = max(bits, max(magnitude_bits(u[k]), magnitude_bits(v[k])));
+      }
+#pragma unroll
+      for (int k = 1; k < 4; k <<= 1) {
+        hi = fmaxf(hi, __shfl_xor(hi, k, 4));
+        lo = fminf(lo, __shfl_xor(lo, k, 4));
+        bits = max(bits, (uint32_t)__shfl_xor((int)bits, k, 4));
+      }
+      if ((i & 3) == 0) {
+        const _Float16 h = block_scale<KIND>(hi, lo, bits);
+        steps[b * kWindow + t] = step_of(h);
+        *(_Float16 *)(pages + w.base[t] + scale_offset(KIND, NB, b, w.r[t])) = h;
+      }
     }
-    const _Float16 h = block_scale<KIND>(hi, lo, bits);
-    uint32_t q = encode<KIND>(x, h);
-    if constexpr (KIND == C_Q4_0) {
-      q |= (uint32_t)__shfl_xor((int)q, 16, 32) << 4;
-      if (c < 16) *p = (uint8_t)q;
-    } else {
-      *p = (uint8_t)q;
+    __syncthreads();
+  }
+  if constexpr (!IS_V) {
+    for (int i = tid; i < NB * 4 * kWindow; i += 256) {
+      const int t = i & (kWindow - 1), G = (i >> 5) & 3, b = i >> 7;
+      if (w.slot[t] < 0) continue;
+      const float *e = rows + t * pitch + b * 32;
+      uint8_t *p = pages + w.base[t] + code_offset<KIND, false>(b, w.r[t], KIND == C_Q4_0 ? 4 * G : 8 * G);
+      const floatx4 u = *(const floatx4 *)(e + (KIND == C_Q4_0 ? 4 * G : 8 * G));
+      const floatx4 v = *(const floatx4 *)(e + (KIND == C_Q4_0 ? 16 + 4 * G : 8 * G + 4));
+      if constexpr (KIND == C_F16) {
+        *(u32x4 *)p = u32x4{pack_h(u[0], u[1]), pack_h(u[2], u[3]), pack_h(v[0], v[1]), pack_h(v[2], v[3])};
+      } else {
+        const Step st = steps[b * kWindow + t];
+        uint32_t lo = 0, hi = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          lo |= encode<KIND>(u[k], st) << (8 * k);
+          hi |= encode<KIND>(v[k], st) << (8 * k);
+        }
+        if constexpr (KIND == C_Q8_0) *(u32x2 *)p = u32x2{lo, hi};
+        else *(uint32_t *)p = lo | hi << 4;
+      }
     }
-    if (c == 0) *(_Float16 *)(group + scale_offset(KIND, NB, b, r)) = h;
+  } else {
+    for (int i = tid; i < NB * kOctets * 16; i += 256) {
+      const int j = i & 15, o = (i >> 4) % kOctets, b = (i >> 4) / kOctets;
+      const int t0 = 8 * o - w.phase;
+      if (w.whole[o]) {
+        const float *e = rows + t0 * pitch + b * 32 + j;
+        uint8_t *p = pages + w.base[t0] + code_offset<KIND, true>(b, w.r[t0], j);
+        if constexpr (KIND == C_F16) {
+          u32x4 a, v;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            a[k] = pack_h(e[2 * k * pitch], e[(2 * k + 1) * pitch]);
+            v[k] = pack_h(e[2 * k * pitch + 16], e[(2 * k + 1) * pitch + 16]);
+          }
+          *(u32x4 *)p = a;
+          *(u32x4 *)(p + 1024) = v;
+        } else {
+          u32x4 q = {0, 0, 0, 0};
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const Step st = steps[b * kWindow + t0 + k];
+            q[k >> 2] |= encode<KIND>(e[k * pitch], st) << (8 * (k & 3));
+            q[2 + (k >> 2)] |= encode<KIND>(e[k * pitch + 16], st) << (8 * (k & 3));
+          }
+          if constexpr (KIND == C_Q8_0) *(u32x4 *)p = q;
+          else *(u32x2 *)p = u32x2{q[0] | q[2] << 4, q[1] | q[3] << 4};
+        }
+      } else {
+        for (int t = max(t0, 0); t < min(t0 + 8, nt); ++t) {
+          if (w.slot[t] < 0) continue;
+          const float *e = rows + t * pitch + b * 32 + j;
+          uint8_t *p = pages + w.base[t];
+          if constexpr (KIND == C_F16) {
+            *(_Float16 *)(p + code_offset<KIND, true>(b, w.r[t], j)) = (_Float16)e[0];
+            *(_Float16 *)(p + code_offset<KIND, true>(b, w.r[t], j + 16)) = (_Float16)e[16];
+          } else {
+            const Step st = steps[b * kWindow + t];
+            const uint32_t lo = encode<KIND>(e[0], st), hi = encode<KIND>(e[16], st);
+            if constexpr (KIND == C_Q8_0) {
+              p[code_offset<KIND, true>(b, w.r[t], j)] = (uint8_t)lo;
+              p[code_offset<KIND, true>(b, w.r[t], j + 16)] = (uint8_t)hi;
+            } else {
+              p[code_offset<KIND, true>(b, w.r[t], j)] = (uint8_t)(lo | hi << 4);
+            }
+          }
+        }
+      }
+    }
   }
 }
 
 struct WriteArgs {
   Cache cache;
-  const void *k, *v, *q;
-  int64_t k_stride, v_stride, q_stride;
-  void *q_out;
-  int64_t q_out_stride;
+  const void *k, *v;
+  int64_t k_stride, v_stride;
+  int k_vec, v_vec;
   const int32_t *pos, *slots;
+  int64_t T;
   int64_t kv_wgs;  // workgroups of the cache part; the rest rotate q
-  int64_t kv_blocks, q_pairs;
-  int n_q;
   Rope rope;
+  Rotate q;
 };
 
-// Per-token write: a half wave owns one block of 32 elements of one token's
-// key or value head.  The reads are whole rows; the codes go out as single
-// bytes (a token's bytes lie apart in the group).
-template <int KK, int VK, typename T, typename QO, bool ROPE>
+// V: pairs per thread of the q rotation (0: no rotation).
+template <int KK, int VK, typename T, typename QO, int V>
 __global__ __launch_bounds__(256) void kv_write_kernel(WriteArgs a) {
-  const int NB = a.cache.NB, D = NB * 32;
-  if ((int64_t)blockIdx.x < a.kv_wgs) {
-    const int64_t task = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (task >= a.kv_blocks) return;  // a whole half wave
-    const int c = threadIdx.x & 31;
-    const int per = a.cache.n_kv * 2 * NB;
-    const int64_t t = task / per;
-    int rest = (int)(task - t * per);
-    const int is_v = rest / (a.cache.n_kv * NB);
-    rest -= is_v * a.cache.n_kv * NB;
-    const int head = rest / NB, b = rest - head * NB;
-    const int slot = a.slots[t];
-    if (slot < 0 || slot >= a.cache.n_slots) return;
-    const int r = (slot % a.cache.page_size) % kGroup;
-    if (is_v) {
-      const T *x = (const T *)a.v + t * a.v_stride + head * D;
-      store_block<VK, true>(a.cache.v_pages + group_at(a.cache, VK, slot, head), NB, b, r, c, (float)x[b * 32 + c]);
-    } else {
-      const T *x = (const T *)a.k + t * a.k_stride + head * D;
-      const float y = ROPE ? rotated(a.rope, x, b * 32 + c, a.pos[t]) : (float)x[b * 32 + c];
-      store_block<KK, false>(a.cache.k_pages + group_at(a.cache, KK, slot, head), NB, b, r, c, y);
-    }
-  } else if constexpr (ROPE) {
-    const int64_t p = ((int64_t)blockIdx.x - a.kv_wgs) * 256 + threadIdx.x;
-    if (p >= a.q_pairs) return;
-    const int64_t row = p / (D / 2);  // t * n_q + head
-    const int i = (int)(p - row * (D / 2)), half = a.rope.n_rot >> 1;
-    const int64_t t = row / a.n_q;
-    const int head = (int)(row - t * a.n_q);
-    const T *x = (const T *)a.q + t * a.q_stride + (int64_t)head * D;
-    QO *y = (QO *)a.q_out + t * a.q_out_stride + (int64_t)head * D;
-    const bool turned = i < half;
-    const int da = turned ? (a.rope.interleaved ? 2 * i : i) : 2 * i;
-    const int db = turned && !a.rope.interleaved ? i + half : da + 1;
-    const float u = (float)x[da], v = (float)x[db];
-    float c = 1.0f, s = 0.0f;
-    if (turned) {
-      rotation(a.pos[t], a.rope.freqs[i], c, s);
-      c *= a.rope.mscale;
-      s *= a.rope.mscale;
-    }
-    y[da] = (QO)(turned ? u * c - v * s : u);
-    y[db] = (QO)(turned ? u * s + v * c : v);
+  if ((int64_t)blockIdx.x >= a.kv_wgs) {
+    if constexpr (V > 0) rotate_rows<T, QO, V>(a.q, ((int64_t)blockIdx.x - a.kv_wgs) * 256 + threadIdx.x);
+    return;
   }
-}
-
-template <int KIND, bool IS_V>
-__device__ __forceinline__ float load_element(const uint8_t *group, int NB, int b, int r, int c) {
-  const uint8_t *p = group + code_offset<KIND, IS_V>(b, r, c);
-  if constexpr (KIND == C_F16) return (float)*(const _Float16 *)p;
-  const float d = (float)*(const _Float16 *)(group + scale_offset(KIND, NB, b, r));
-  if constexpr (KIND == C_Q8_0) return d * (float)((int)*p - 128);
-  return d * (float)(((int)*p >> (c >> 4) * 4 & 15) - 8);
+  __shared__ Window w;
+  extern __shared__ float rows[];  // [kWindow][D + 4], then steps [NB][kWindow]
+  const int D = a.cache.NB * 32;
+  Step *steps = (Step *)(rows + kWindow * (D + 4));
+  const int n = a.cache.n_kv;
+  const int64_t win = (int64_t)blockIdx.x / (2 * n);
+  const int rest = (int)(blockIdx.x - win * 2 * n), is_v = rest >= n, head = is_v ? rest - n : rest;
+  const int64_t t0 = win * kWindow;
+  const int nt = (int)min((int64_t)kWindow, a.T - t0);
+  find_window(w, a.cache, a.slots, t0, nt, is_v ? VK : KK, head);
+  __syncthreads();
+  if (is_v)
+    write_window<VK, true, T, false>(a.cache, a.cache.v_pages, (const T *)a.v + t0 * a.v_stride + head * D, a.v_stride,
+                                     a.v_vec, nt, nullptr, a.rope, w, rows, steps);
+  else
+    write_window<KK, false, T, (V > 0)>(a.cache, a.cache.k_pages, (const T *)a.k + t0 * a.k_stride + head * D, a.k_stride,
+                                        a.k_vec, nt, a.pos + t0, a.rope, w, rows, steps);
 }
 
 struct ReadArgs {
   Cache cache;
   const int32_t *slots;
   void *k_out, *v_out;
-  int64_t blocks;
+  int64_t T;
 };
+
+template <typename O>
+__device__ __forceinline__ void store4(O *p, floatx4 v) {
+  if constexpr (sizeof(O) == 2) *(half4 *)p = half4{(_Float16)v[0], (_Float16)v[1], (_Float16)v[2], (_Float16)v[3]};
+  else *(floatx4 *)p = v;
+}
+
+template <int KIND>
+__device__ __forceinline__ float value(uint32_t code, float d) {
+  return d * (float)((int)code - (KIND == C_Q8_0 ? 128 : 8));
+}
+
+template <int KIND, typename O>
+__device__ __forceinline__ void read_keys(const Cache &c, O *out, int64_t out_stride, int nt, const Window &w) {
+  const int NB = c.NB, pieces = NB * 4;
+  for (int i = threadIdx.x; i < nt * pieces; i += 256) {
+    const int t = i / pieces, p = i - t * pieces, b = p >> 2, G = p & 3;
+    O *o = out + t * out_stride + b * 32 + (KIND == C_Q4_0 ? 4 * G : 8 * G);
+    floatx4 u = {0, 0, 0, 0}, v = u;
+    if (w.slot[t] >= 0) {
+      const uint8_t *g = c.k_pages + w.base[t];
+      const uint8_t *at = g + code_offset<KIND, false>(b, w.r[t], KIND == C_Q4_0 ? 4 * G : 8 * G);
+      if constexpr (KIND == C_F16) {
+        const half8 h = *(const half8 *)at;
+        u = floatx4{(float)h[0], (float)h[1], (float)h[2], (float)h[3]};
+        v = floatx4{(float)h[4], (float)h[5], (float)h[6], (float)h[7]};
+      } else {
+        const float d = (float)*(const _Float16 *)(g + scale_offset(KIND, NB, b, w.r[t]));
+        uint32_t lo, hi;
+        if constexpr (KIND == C_Q8_0) {
+          const u32x2 q = *(const u32x2 *)at;
+          lo = q[0], hi = q[1];
+        } else {
+          const uint32_t q = *(const uint32_t *)at;
+          lo = q & 0x0f0f0f0f, hi = q >> 4 & 0x0f0f0f0f;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          u[k] = value<KIND>(lo >> (8 * k) & 255, d);
+          v[k] = value<KIND>(hi >> (8 * k) & 255, d);
+        }
+      }
+    }
+    store4(o, u);
+    store4(o + (KIND == C_Q4_0 ? 16 : 4), v);
+  }
+}
+
+template <int KIND, typename O>
+__device__ __forceinline__ void read_values(const Cache &c, O *out, int64_t out_stride, int nt, const Window &w, O *rows) {
+  const int NB = c.NB, D = NB * 32, pitch = D + 16 / (int)sizeof(O);
+  for (int i = threadIdx.x; i < NB * kOctets * 16; i += 256) {
+    const int j = i & 15, o = (i >> 4) % kOctets, b = (i >> 4) / kOctets;
+    const int t0 = 8 * o - w.phase;
+    if (w.whole[o]) {
+      const uint8_t *g = c.v_pages + w.base[t0], *p = g + code_offset<KIND, true>(b, w.r[t0], j);
+      O *e = rows + t0 * pitch + b * 32 + j;
+      if constexpr (KIND == C_F16) {
+        const half8 u = *(const half8 *)p, v = *(const half8 *)(p + 1024);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) e[k * pitch] = (O)(float)u[k], e[k * pitch + 16] = (O)(float)v[k];
+      } else {
+        const half8 d = *(const half8 *)(g + scale_offset(KIND, NB, b, w.r[t0]));
+        u32x4 q;
+        if constexpr (KIND == C_Q8_0) {
+          q = *(const u32x4 *)p;
+        } else {
+          const u32x2 n = *(const u32x2 *)p;
+          q = u32x4{n[0] & 0x0f0f0f0f, n[1] & 0x0f0f0f0f, n[0] >> 4 & 0x0f0f0f0f, n[1] >> 4 & 0x0f0f0f0f};
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          e[k * pitch] = (O)value<KIND>(q[k >> 2] >> (8 * (k & 3)) & 255, (float)d[k]);
+          e[k * pitch + 16] = (O)value<KIND>(q[2 + (k >> 2)] >> (8 * (k & 3)) & 255, (float)d[k]);
+        }
+      }
+    } else {
+      for (int t = max(t0, 0); t < min(t0 + 8, nt); ++t) {
+        float u = 0.0f, v = 0.0f;
+        if (w.slot[t] >= 0) {
+          const uint8_t *g = c.v_pages + w.base[t], *p = g + code_offset<KIND, true>(b, w.r[t], j);
+          if constexpr (KIND == C_F16) {
+            u = (float)*(const _Float16 *)p, v = (float)*(const _Float16 *)(p + 1024);
+          } else {
+            const float d = (float)*(const _Float16 *)(g + scale_offset(KIND, NB, b, w.r[t]));
+            if constexpr (KIND == C_Q8_0) u = value<KIND>(p[0], d), v = value<KIND>(p[8], d);
+            else u = value<KIND>(p[0] & 15, d), v = value<KIND>(p[0] >> 4, d);
+          }
+        }
+        rows[t * pitch + b * 32 + j] = (O)u;
+        rows[t * pitch + b * 32 + j + 16] = (O)v;
+      }
+    }
+  }
+  __syncthreads();
+  constexpr int per = 16 / sizeof(O);
+  for (int i = threadIdx.x; i < nt * (D / per); i += 256) {
+    const int t = i / (D / per), d = (i - t * (D / per)) * per;
+    *(u32x4 *)(out + t * out_stride + d) = *(const u32x4 *)(rows + t * pitch + d);
+  }
+}
 
 template <int KK, int VK, typename O>
 __global__ __launch_bounds__(256) void kv_read_kernel(ReadArgs a) {
-  const int64_t task = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (task >= a.blocks) return;
-  const int NB = a.cache.NB, c = threadIdx.x & 31;
-  const int per = a.cache.n_kv * 2 * NB;
-  const int64_t t = task / per;
-  int rest = (int)(task - t * per);
-  const int is_v = rest / (a.cache.n_kv * NB);
-  rest -= is_v * a.cache.n_kv * NB;
-  const int head = rest / NB, b = rest - head * NB;
-  const int slot = a.slots[t];
-  const int64_t o = (t * a.cache.n_kv + head) * (NB * 32) + b * 32 + c;
-  if (slot < 0 || slot >= a.cache.n_slots) {
-    ((O *)(is_v ? a.v_out : a.k_out))[o] = (O)0.0f;
-    return;
-  }
-  const int r = (slot % a.cache.page_size) % kGroup;
-  if (is_v)
-    ((O *)a.v_out)[o] = (O)load_element<VK, true>(a.cache.v_pages + group_at(a.cache, VK, slot, head), NB, b, r, c);
-  else
-    ((O *)a.k_out)[o] = (O)load_element<KK, false>(a.cache.k_pages + group_at(a.cache, KK, slot, head), NB, b, r, c);
+  __shared__ Window w;
+  extern __shared__ u32x4 tile[];  // values: [kWindow][D + 16 bytes]
+  const int D = a.cache.NB * 32, n = a.cache.n_kv;
+  const int64_t win = (int64_t)blockIdx.x / (2 * n);
+  const int rest = (int)(blockIdx.x - win * 2 * n), is_v = rest >= n, head = is_v ? rest - n : rest;
+  const int64_t t0 = win * kWindow;
+  const int nt = (int)min((int64_t)kWindow, a.T - t0);
+  find_window(w, a.cache, a.slots, t0, nt, is_v ? VK : KK, head);
+  __syncthreads();
+  O *out = (O *)(is_v ? a.v_out : a.k_out) + (t0 * n + head) * D;
+  if (is_v) read_values<VK, O>(a.cache, out, (int64_t)n * D, nt, w, (O *)tile);
+  else read_keys<KK, O>(a.cache, out, (int64_t)n * D, nt, w);
 }
 
 static Cache make_cache(const KvCache &k) {
@@ -160,43 +371,48 @@ static Cache make_cache(const KvCache &k) {
                (int)(k.head_dim / 32)};
 }
 
-template <int KK, int VK>
-static hipError_t write_kinds(const KvCache &kc, const KvWrite &w, hipStream_t s) {
+template <int KK, int VK, typename T, typename QO>
+static hipError_t write_types(const KvCache &kc, const KvWrite &w, hipStream_t s) {
   WriteArgs a{};
   a.cache = make_cache(kc);
-  a.k = w.k, a.v = w.v, a.q = w.q;
-  a.k_stride = w.k_stride, a.v_stride = w.v_stride, a.q_stride = w.q_stride;
-  a.q_out = w.q_out, a.q_out_stride = w.q_out_stride;
-  a.pos = w.pos, a.slots = w.slots;
-  a.kv_blocks = w.T * kc.n_kv * 2 * a.cache.NB;
-  a.kv_wgs = (a.kv_blocks + 7) / 8;
-  a.n_q = (int)w.n_q;
-  a.q_pairs = w.rope ? w.T * w.n_q * (kc.head_dim / 2) : 0;
-  if (w.rope) a.rope = Rope{w.freqs, (int)w.n_rot, w.interleaved, w.mscale};
-  const dim3 grid((unsigned)(a.kv_wgs + (a.q_pairs + 255) / 256));
-#define QMM_LAUNCH(T, QO, R) hipLaunchKernelGGL((kv_write_kernel<KK, VK, T, QO, R>), grid, dim3(256), 0, s, a)
-  if (!w.rope) {
-    if (w.f16) QMM_LAUNCH(_Float16, _Float16, false);
-    else QMM_LAUNCH(float, float, false);
-  } else if (w.f16) {
-    if (w.q_out_f16) QMM_LAUNCH(_Float16, _Float16, true);
-    else QMM_LAUNCH(_Float16, float, true);
-  } else {
-    if (w.q_out_f16) QMM_LAUNCH(float, _Float16, true);
-    else QMM_LAUNCH(float, float, true);
+  a.k = w.k, a.v = w.v;
+  a.k_stride = w.k_stride, a.v_stride = w.v_stride;
+  a.k_vec = w.k_stride % 4 == 0 && (uintptr_t)w.k % (4 * sizeof(T)) == 0;
+  a.v_vec = w.v_stride % 4 == 0 && (uintptr_t)w.v % (4 * sizeof(T)) == 0;
+  a.pos = w.pos, a.slots = w.slots, a.T = w.T;
+  a.kv_wgs = (w.T + kWindow - 1) / kWindow * 2 * kc.n_kv;
+  int64_t threads = 0;
+  bool wide = false;
+  if (w.rope) {
+    a.rope = Rope{w.freqs, (int)w.n_rot, w.interleaved, w.mscale};
+    a.q.x = w.q, a.q.y = w.q_out, a.q.x_stride = w.q_stride, a.q.y_stride = w.q_out_stride;
+    a.q.pos = w.pos, a.q.T = w.T, a.q.H = (int)w.n_q, a.q.D = (int)kc.head_dim, a.q.rope = a.rope;
+    wide = plan_rotate(a.q, sizeof(T), sizeof(QO), threads);
   }
-#undef QMM_LAUNCH
+  const dim3 grid((unsigned)(a.kv_wgs + (threads + 255) / 256));
+  const unsigned lds = kWindow * ((kc.head_dim + 4) * sizeof(float) + a.cache.NB * sizeof(Step));
+  if (!w.rope) hipLaunchKernelGGL((kv_write_kernel<KK, VK, T, QO, 0>), grid, dim3(256), lds, s, a);
+  else if (wide) hipLaunchKernelGGL((kv_write_kernel<KK, VK, T, QO, 4>), grid, dim3(256), lds, s, a);
+  else hipLaunchKernelGGL((kv_write_kernel<KK, VK, T, QO, 1>), grid, dim3(256), lds, s, a);
   return hipGetLastError();
+}
+
+template <int KK, int VK>
+static hipError_t write_kinds(const KvCache &kc, const KvWrite &w, hipStream_t s) {
+  if (!w.rope) return w.f16 ? write_types<KK, VK, _Float16, _Float16>(kc, w, s) : write_types<KK, VK, float, float>(kc, w, s);
+  if (w.f16)
+    return w.q_out_f16 ? write_types<KK, VK, _Float16, _Float16>(kc, w, s) : write_types<KK, VK, _Float16, float>(kc, w, s);
+  return w.q_out_f16 ? write_types<KK, VK, float, _Float16>(kc, w, s) : write_types<KK, VK, float, float>(kc, w, s);
 }
 
 template <int KK, int VK>
 static hipError_t read_kinds(const KvCache &kc, const int32_t *slots, int64_t T, void *k_out, void *v_out, int f16,
                              hipStream_t s) {
-  ReadArgs a{make_cache(kc), slots, k_out, v_out, 0};
-  a.blocks = T * kc.n_kv * 2 * a.cache.NB;
-  const dim3 grid((unsigned)((a.blocks + 7) / 8));
-  if (f16) hipLaunchKernelGGL((kv_read_kernel<KK, VK, _Float16>), grid, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((kv_read_kernel<KK, VK, float>), grid, dim3(256), 0, s, a);
+  ReadArgs a{make_cache(kc), slots, k_out, v_out, T};
+  const dim3 grid((unsigned)((T + kWindow - 1) / kWindow * 2 * kc.n_kv));
+  const unsigned lds = kWindow * (kc.head_dim * (f16 ? 2 : 4) + 16);
+  if (f16) hipLaunchKernelGGL((kv_read_kernel<KK, VK, _Float16>), grid, dim3(256), lds, s, a);
+  else hipLaunchKernelGGL((kv_read_kernel<KK, VK, float>), grid, dim3(256), lds, s, a);
   return hipGetLastError();
 }
 
