@@ -43,7 +43,10 @@ def compile_flags() -> list[str]:
 # ordinary VGPRs: with accumulation registers the allocator rotates its
 # loop-carried accumulators through copies on every iteration.  (The GEMV
 # mixes inline assembly with its matrix-core code and keeps the default.)
-FILE_FLAGS = {"qmm_gemm.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+# The attention kernels do too: their score products go straight to the VALU.
+VGPR_FORM = ["-mllvm", "-amdgpu-mfma-vgpr-form"]
+FILE_FLAGS = {"qmm_gemm.hip": VGPR_FORM,
+              **{f"qmm_attn_{k}_{v}.hip": VGPR_FORM for k in ("f16", "q8", "q4") for v in ("f16", "q8", "q4")}}
 
 
 def sources() -> list[str]:

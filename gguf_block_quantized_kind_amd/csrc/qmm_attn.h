@@ -47,6 +47,7 @@ using kv::C_Q8_0;
 
 typedef _Float16 half8 __attribute__((ext_vector_type(8)));
 typedef _Float16 half2v __attribute__((ext_vector_type(2)));
+typedef uint16_t ushort2v __attribute__((ext_vector_type(2)));
 typedef float floatx4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -88,31 +89,43 @@ __device__ __forceinline__ Span span_of(const Args &a, int b) {
   return Span{lo, len, g0, len > 0 ? (int)(((int64_t)len + kv::kGroup - 1) / kv::kGroup) - g0 : 0};
 }
 
-__device__ __forceinline__ int64_t wave_sum(int64_t v) {
-#pragma unroll
-  for (int k = 1; k < 64; k <<= 1) v += __shfl_xor(v, k, 64);
-  return v;
+// Reductions over the four lane groups G of a column (lanes j, 16 + j, 32 + j,
+// 48 + j), every lane receiving the result: each swap exchanges rows of 16 or
+// 32 lanes between two copies of the value.
+__device__ __forceinline__ float max_over_groups(float v) {
+  auto a = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v), false, false);
+  v = fmaxf(__builtin_bit_cast(float, (uint32_t)a[0]), __builtin_bit_cast(float, (uint32_t)a[1]));
+  auto b = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v), false, false);
+  return fmaxf(__builtin_bit_cast(float, (uint32_t)b[0]), __builtin_bit_cast(float, (uint32_t)b[1]));
 }
-
-// Groups per split: the attended groups of the whole batch over the target
-// number of workgroups.
-__device__ __forceinline__ int groups_per_split(const Args &a, int lane) {
-  int64_t total = 0;
-  for (int b0 = 0; b0 < a.B; b0 += 64) total += span_of(a, b0 + lane).n;
-  total = wave_sum(total) * a.n_kv * a.tiles;
-  const int64_t c = (total + a.target - 1) / a.target;
-  return (int)max(c, (int64_t)kMinGroups);
+__device__ __forceinline__ float sum_over_groups(float v) {
+  auto a = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v), false, false);
+  v = __builtin_bit_cast(float, (uint32_t)a[0]) + __builtin_bit_cast(float, (uint32_t)a[1]);
+  auto b = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v), false, false);
+  return __builtin_bit_cast(float, (uint32_t)b[0]) + __builtin_bit_cast(float, (uint32_t)b[1]);
 }
 
 // Splits are numbered through the batch (at least one per sequence, so that
-// every output row is written).  first_split: the number of splits before
-// sequence `want_b`, or, with want_b < 0, the sequence that split `unit`
-// belongs to (-1 past the last) and its first split.
+// every output row is written).  The groups per split are the attended groups
+// of the whole batch over the target number of workgroups, at least one group
+// per wave.
 struct Found {
-  int b;
-  int64_t first;
+  int b, c;       // sequence (-1: past the last split), groups per split
+  int64_t first;  // its first split
 };
-__device__ __forceinline__ Found find_split(const Args &a, int lane, int c, int64_t unit, int want_b) {
+// want_b < 0: the sequence that split `unit` belongs to; else sequence want_b.
+__device__ __forceinline__ Found find_split(const Args &a, int lane, int64_t unit, int want_b) {
+  const int64_t nh = (int64_t)a.n_kv * a.tiles;
+  if (a.B == 1) {  // no scan
+    const int n = span_of(a, 0).n;
+    const int c = (int)max((n * nh + a.target - 1) / a.target, (int64_t)kMinGroups);
+    return Found{want_b < 0 && unit >= max(1, (n + c - 1) / c) ? -1 : 0, c, 0};
+  }
+  int64_t total = 0;
+  for (int b0 = 0; b0 < a.B; b0 += 64) total += span_of(a, b0 + lane).n;
+#pragma unroll
+  for (int k = 1; k < 64; k <<= 1) total += __shfl_xor(total, k, 64);
+  const int c = (int)max((total * nh + a.target - 1) / a.target, (int64_t)kMinGroups);
   int64_t before = 0;
   for (int b0 = 0; b0 < a.B; b0 += 64) {
     const int n = span_of(a, b0 + lane).n;
@@ -127,27 +140,17 @@ __device__ __forceinline__ Found find_split(const Args &a, int lane, int c, int6
     const uint64_t mask = __ballot(hit);
     if (mask) {
       const int l = __ffsll((unsigned long long)mask) - 1;
-      return Found{b0 + l, before + __shfl(incl - splits, l, 64)};
+      return Found{b0 + l, c, before + __shfl(incl - splits, l, 64)};
     }
     before += __shfl(incl, 63, 64);
   }
-  return Found{-1, before};
+  return Found{-1, c, before};
 }
 
-// Query element that K entry k of lane group G holds, of 32 (qmm_kv.h; Q4_0
-// bytes are taken in the order 0, 2, 1, 3 with low and high nibbles of a pair
-// of bytes side by side), and whether its code stands 16 times too high.
-template <int KK>
-__device__ __forceinline__ int k_element(int G, int k) {
-  if constexpr (KK != C_Q4_0) return 8 * G + k;
-  const int y = (k & 1) * 2 + (k >> 2);
-  return 4 * G + y + (k & 2 ? 16 : 0);
-}
-
+__device__ __forceinline__ ushort2v as_us2(uint32_t v) { return __builtin_bit_cast(ushort2v, v); }
+__device__ __forceinline__ uint32_t as_u(ushort2v v) { return __builtin_bit_cast(uint32_t, v); }
+__device__ __forceinline__ half2v as_h2(uint32_t v) { return __builtin_bit_cast(half2v, v); }
 __device__ __forceinline__ half8 as_h8(u32x4 v) { return __builtin_bit_cast(half8, v); }
-__device__ __forceinline__ uint32_t pk(float a, float b) {
-  return __builtin_bit_cast(uint32_t, half2v{(_Float16)a, (_Float16)b});
-}
 __device__ __forceinline__ uint32_t pk_add(uint32_t a, _Float16 b) {
   const half2v v = __builtin_bit_cast(half2v, a) + half2v{b, b};
   return __builtin_bit_cast(uint32_t, v);
@@ -174,8 +177,7 @@ __device__ __forceinline__ void load_block(const uint8_t *block, int lane, Raw<K
   }
 }
 
-// Eight bytes of Q8_0, or the nibbles of four bytes of Q4_0 in the order of
-// k_element, as exact signed integers in f16: the code under the mantissa of
+// Eight bytes of Q8_0, or the nibbles of pairs of Q4_0 bytes, as exact signed integers in f16: the code under the mantissa of
 // 1024 (a high nibble 16 times too high), the offset taken off by one packed
 // operation.
 __device__ __forceinline__ half8 signed_bytes(uint32_t a, uint32_t b) {
@@ -185,10 +187,18 @@ __device__ __forceinline__ half8 signed_bytes(uint32_t a, uint32_t b) {
                      pk_add(__builtin_amdgcn_perm(k, b, 0x04010400), -1152.0f16),
                      pk_add(__builtin_amdgcn_perm(k, b, 0x04030402), -1152.0f16)});
 }
-__device__ __forceinline__ uint32_t signed_low(uint32_t a) { return pk_add((a & 0x000f000f) | 0x64006400, -1032.0f16); }
-__device__ __forceinline__ uint32_t signed_high(uint32_t a) {  // (1024 + 16 u) / 16 - 72
-  return pk_fma((a & 0x00f000f0) | 0x64006400, 0.0625f16, -72.0f16);
-}
+// The constants sit in registers so that mask and exponent are one v_and_or
+// (an instruction takes one scalar operand, and these literals need two).
+struct Nibbles {
+  uint32_t k, low, high;
+  __device__ __forceinline__ Nibbles() : k(0x64006400), low(0x000f000f), high(0x00f000f0) {
+    asm("" : "+v"(k), "+s"(low), "+s"(high));
+  }
+  __device__ __forceinline__ uint32_t signed_low(uint32_t a) const { return pk_add((a & low) | k, -1032.0f16); }
+  __device__ __forceinline__ uint32_t signed_high(uint32_t a) const {  // (1024 + 16 u) / 16 - 72
+    return pk_fma((a & high) | k, 0.0625f16, -72.0f16);
+  }
+};
 
 // Whether codes of keys enter as f16 subnormals.  The matrix cores align the
 // products of one step by the operands' exponent fields, so a subnormal code u
@@ -200,11 +210,11 @@ constexpr bool kSubnormalKeys = KK == C_Q8_0 || (KK == C_Q4_0 && !SPLIT);
 // Key operand of tile m: halves, codes * 2^-24 (Q4_0 high nibbles 2^-20), or
 // signed codes.
 template <int KK, bool SPLIT>
-__device__ __forceinline__ half8 key_operand(const Raw<KK> &r, int m) {
+__device__ __forceinline__ half8 key_operand(const Raw<KK> &r, int m, const Nibbles &nb) {
   if constexpr (KK == C_F16) return as_h8(r.w[m]);
   if constexpr (KK == C_Q4_0 && SPLIT) {
     const uint32_t a = r.w[m], b = a >> 8;
-    return as_h8(u32x4{signed_low(a), signed_high(a), signed_low(b), signed_high(b)});
+    return as_h8(u32x4{nb.signed_low(a), nb.signed_high(a), nb.signed_low(b), nb.signed_high(b)});
   }
   if constexpr (KK == C_Q8_0) {
     const uint32_t a = r.w[2 * m], b = r.w[2 * m + 1];
@@ -219,13 +229,13 @@ __device__ __forceinline__ half8 key_operand(const Raw<KK> &r, int m) {
 // Value operand of tile x: halves, or exact signed codes.  Token order of the
 // eight K entries: natural, for Q4_0 0 2 1 3 4 6 5 7.
 template <int VK>
-__device__ __forceinline__ half8 value_operand(const Raw<VK> &r, int x) {
+__device__ __forceinline__ half8 value_operand(const Raw<VK> &r, int x, const Nibbles &nb) {
   if constexpr (VK == C_F16) return as_h8(r.w[x]);
   if constexpr (VK == C_Q8_0) return signed_bytes(r.w[2 * x], r.w[2 * x + 1]);
   if constexpr (VK == C_Q4_0) {
     const uint32_t a = r.w[0], b = r.w[1];
-    if (x == 0) return as_h8(u32x4{signed_low(a), signed_low(a >> 8), signed_low(b), signed_low(b >> 8)});
-    return as_h8(u32x4{signed_high(a), signed_high(a >> 8), signed_high(b), signed_high(b >> 8)});
+    if (x == 0) return as_h8(u32x4{nb.signed_low(a), nb.signed_low(a >> 8), nb.signed_low(b), nb.signed_low(b >> 8)});
+    return as_h8(u32x4{nb.signed_high(a), nb.signed_high(a >> 8), nb.signed_high(b), nb.signed_high(b >> 8)});
   }
 }
 template <int VK>
@@ -233,6 +243,22 @@ __device__ __forceinline__ constexpr int v_token(int k) {
   if (VK != C_Q4_0) return k;
   const int p = k & 3;
   return (k & 4) + (p == 1 ? 2 : p == 2 ? 1 : p);
+}
+
+// The query elements of the eight K entries of lane group G, of a block of 32
+// (qmm_kv.h; Q4_0 bytes are taken in the order 0, 2, 1, 3, low and high nibbles
+// of a pair of bytes side by side), as floats.
+template <int KK, typename QT>
+__device__ __forceinline__ void load_q(const QT *q, int G, float (&v)[8]) {
+  typedef QT q4 __attribute__((ext_vector_type(4)));
+  q4 a, b;
+  __builtin_memcpy(&a, q + (KK == C_Q4_0 ? 4 * G : 8 * G), sizeof a);
+  __builtin_memcpy(&b, q + (KK == C_Q4_0 ? 16 + 4 * G : 8 * G + 4), sizeof b);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int y = (k & 1) * 2 + (k >> 2);
+    v[k] = KK == C_Q4_0 ? (float)(k & 2 ? b[y] : a[y]) : (float)(k < 4 ? a[k] : b[k - 4]);
+  }
 }
 
 template <int KK, int VK, int NB, typename QT>
@@ -249,10 +275,9 @@ __global__ __launch_bounds__(64 * kWaves) void attn_kernel(Args a) {
   const int nh = a.n_kv * a.tiles;
   const int64_t unit = (int64_t)blockIdx.x / nh;
   const int hh = (int)(blockIdx.x - unit * nh), kvh = hh % a.n_kv, tile = hh / a.n_kv;
-  const int c = groups_per_split(a, lane);
-  const Found f = find_split(a, lane, c, unit, -1);
+  const Found f = find_split(a, lane, unit, -1);
   if (f.b < 0) return;
-  const int b = __builtin_amdgcn_readfirstlane(f.b);
+  const int b = __builtin_amdgcn_readfirstlane(f.b), c = __builtin_amdgcn_readfirstlane(f.c);
   const Span sp = span_of(a, b);
   const int splits = max(1, (sp.n + c - 1) / c), each = (sp.n + splits - 1) / splits;
   const int mine = (int)(unit - f.first);
@@ -262,44 +287,93 @@ __global__ __launch_bounds__(64 * kWaves) void attn_kernel(Args a) {
   // This tile's query heads: column j is head kvh * G + tile * 16 + j.
   const int heads = min(a.heads, a.G - tile * 16);
   const int head0 = kvh * a.G + tile * 16;
-  const QT *q = (const QT *)a.q + (int64_t)b * a.q_stride + (int64_t)(head0 + min(j, heads - 1)) * D;
+
+  // Group g's bytes.  A page outside the cache stands for absent tokens: page
+  // 0 is read in its place and given no weight.
+  constexpr int kKG = kv::group_bytes(KK, NB), kVG = kv::group_bytes(VK, NB);
+  constexpr int kKB = kv::block_code_bytes(KK), kVB = kv::block_code_bytes(VK);
+  const int32_t *table = a.table + (int64_t)b * a.max_pages;
+  Raw<KK> kr[NB];
+  Raw<VK> vr[NB];
+  half8 kd[KK == C_F16 ? 1 : NB], vd[VK == C_F16 ? 1 : NB];
+  auto load_keys = [&](int page, int in_page) {
+    const uint8_t *p = a.kp + page * a.k_page_bytes + (int64_t)in_page * kKG;
+#pragma unroll
+    for (int n = 0; n < NB; ++n) load_block<KK>(p + n * kKB, lane, kr[n]);
+    if constexpr (KK != C_F16) {
+#pragma unroll
+      for (int n = 0; n < NB; ++n) kd[n] = *(const half8 *)(p + NB * kKB + n * 64 + G * 16);
+    }
+  };
+  auto load_values = [&](int page, int in_page) {
+    const uint8_t *p = a.vp + page * a.v_page_bytes + (int64_t)in_page * kVG;
+    if constexpr (VK != C_F16) {
+#pragma unroll
+      for (int n = 0; n < NB; ++n) vd[n] = *(const half8 *)(p + NB * kVB + n * 64 + G * 16);
+    }
+#pragma unroll
+    for (int n = 0; n < NB; ++n) load_block<VK>(p + n * kVB, lane, vr[n]);
+  };
+  auto usable = [&](int page) { return page >= 0 && page < a.n_pages; };
+  // This wave's groups: g, then every fourth; (pi, gi) is page and group in it
+  // of the next one, whose page number is read an iteration ahead.
+  int g = gs + wave, page = 0, pi = g / a.page_groups, gi = g - pi * a.page_groups;
+  bool there = false;
+  if (g < ge) {
+    page = table[pi];
+    there = usable(page);
+    page = there ? page : 0;
+    load_keys(page, kvh * a.page_groups + gi);
+    load_values(page, kvh * a.page_groups + gi);
+  }
 
   // The query scaled by a power of two to 2^14 .. 2^15, in one or two terms,
-  // and what undoes it.
+  // and what undoes it; the sign of the scale goes into the query, so that
+  // the largest product is the largest score.  (f16 queries beside f16 keys
+  // need no scaling: their products are exact.)
   half8 qh[NB], ql[SPLIT ? NB : 1];
-  float qoff[SUB ? NB : 1];
-  float qscale;
+  floatx4 qoff[SUB ? NB : 1];
+  float qscale = a.scale2 == 0.0f ? 1.0f : fabsf(a.scale2);
   {
-    float big = 0.0f;
+    const QT *q = (const QT *)a.q + (int64_t)b * a.q_stride + (int64_t)(head0 + min(j, heads - 1)) * D;
+    const float sign = a.scale2 > 0.0f ? 1.0f : a.scale2 < 0.0f ? -1.0f : 0.0f;
+    float up = sign;
+    float v[NB][8];
 #pragma unroll
-    for (int n = 0; n < NB; ++n)
+    for (int n = 0; n < NB; ++n) load_q<KK>(q + n * 32, G, v[n]);
+    if constexpr (KK != C_F16 || SPLIT) {
+      float big = 0.0f;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) big = fmaxf(big, fabsf((float)q[n * 32 + k_element<KK>(G, k)]));
-    big = fmaxf(big, __shfl_xor(big, 16, 64));
-    big = fmaxf(big, __shfl_xor(big, 32, 64));
-    const int e = big > 0.0f && big < __builtin_inff() ? 14 - ilogbf(big) : 0;
-    qscale = ldexpf(a.scale2, -e + (SUB ? 24 : 0));
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) big = fmaxf(big, fabsf(v[n][k]));
+      big = max_over_groups(big);
+      // 2^e brings big to [2^14, 2^15); the exponents kept where 2^e and 2^-e are normal.
+      int e = 14 + 127 - (int)(__builtin_bit_cast(uint32_t, big) >> 23);
+      e = big > 0.0f && big < __builtin_inff() ? min(max(e, -112), 125) : 0;
+      up *= __builtin_bit_cast(float, (uint32_t)(127 + e) << 23);
+      qscale *= __builtin_bit_cast(float, (uint32_t)(127 - e) << 23) * (SUB ? 0x1p24f : 1.0f);
+    }
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
       float sum = 0.0f;
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const bool high = KK == C_Q4_0 && SUB && (k & 2);
-        const float v = ldexpf((float)q[n * 32 + k_element<KK>(G, k)], high ? e - 4 : e);
-        const _Float16 h = (_Float16)v;
+        const float w = v[n][k] * (high ? up * 0.0625f : up);
+        const _Float16 h = (_Float16)w;
         qh[n][k] = h;
         float got = (float)h;
         if constexpr (SPLIT) {
-          const _Float16 l = (_Float16)(v - got);
+          const _Float16 l = (_Float16)(w - got);
           ql[n][k] = l;
           got += (float)l;
         }
         sum += high ? 16.0f * got : got;
       }
       if constexpr (SUB) {
-        sum += __shfl_xor(sum, 16, 64);
-        sum += __shfl_xor(sum, 32, 64);
-        qoff[n] = sum * (KK == C_Q8_0 ? -128.0f : -8.0f) * 0x1p-24f;
+        const float off = sum_over_groups(sum) * (KK == C_Q8_0 ? -128.0f : -8.0f) * 0x1p-24f;
+        qoff[n] = floatx4{off, off, off, off};
       }
     }
   }
@@ -308,40 +382,29 @@ __global__ __launch_bounds__(64 * kWaves) void attn_kernel(Args a) {
 #pragma unroll
   for (int n = 0; n < NB; ++n) acc[n][0] = acc[n][1] = floatx4{0, 0, 0, 0};
   float R = kFloor, sum = 0.0f;
+  const Nibbles nb;
 
-  constexpr int kKG = kv::group_bytes(KK, NB), kVG = kv::group_bytes(VK, NB);
-  constexpr int kKB = kv::block_code_bytes(KK), kVB = kv::block_code_bytes(VK);
-  for (int g = gs + wave; g < ge; g += kWaves) {
-    const int page = a.table[(int64_t)b * a.max_pages + g / a.page_groups];
-    if (page < 0 || page >= a.n_pages) continue;
-    const int in_page = kvh * a.page_groups + g % a.page_groups;
-    const uint8_t *kg = a.kp + page * a.k_page_bytes + (int64_t)in_page * kKG;
-    const uint8_t *vg = a.vp + page * a.v_page_bytes + (int64_t)in_page * kVG;
-    Raw<KK> kr[NB];
-    Raw<VK> vr[NB];
-    half8 kd[KK == C_F16 ? 1 : NB], vd[VK == C_F16 ? 1 : NB];
-#pragma unroll
-    for (int n = 0; n < NB; ++n) {
-      load_block<KK>(kg + n * kKB, lane, kr[n]);
-      if constexpr (KK != C_F16) kd[n] = *(const half8 *)(kg + NB * kKB + n * 64 + G * 16);
+  while (g < ge) {
+    // The next group (the same again after the last: its loads are issued
+    // whatever follows, so that no wait is widened by a branch).
+    const bool more = g + kWaves < ge;
+    if (more) {
+      gi += kWaves;
+      while (gi >= a.page_groups) gi -= a.page_groups, ++pi;
     }
-#pragma unroll
-    for (int n = 0; n < NB; ++n) {
-      load_block<VK>(vg + n * kVB, lane, vr[n]);
-      if constexpr (VK != C_F16) vd[n] = *(const half8 *)(vg + NB * kVB + n * 64 + G * 16);
-    }
+    int next = table[pi];
 
-    // Scores of tokens 8G + k, head j.
+    // Products of tokens 8G + k with head j, without the query's scale.
     float s[8];
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
       floatx4 t = {0, 0, 0, 0};
 #pragma unroll
       for (int n = 0; n < NB; ++n) {
-        const half8 k = key_operand<KK, SPLIT>(kr[n], m);
+        const half8 k = key_operand<KK, SPLIT>(kr[n], m, nb);
         floatx4 u;
         if constexpr (KK == C_F16) u = t;
-        else if constexpr (SUB) u = floatx4{qoff[n], qoff[n], qoff[n], qoff[n]};
+        else if constexpr (SUB) u = qoff[n];
         else u = floatx4{0, 0, 0, 0};
         u = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, qh[n], u, 0, 0, 0);
         if constexpr (SPLIT) u = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, ql[n], u, 0, 0, 0);
@@ -351,18 +414,21 @@ __global__ __launch_bounds__(64 * kWaves) void attn_kernel(Args a) {
           for (int r = 0; r < 4; ++r) t[r] = __builtin_fmaf((float)kd[n][4 * m + r], u[r], t[r]);
       }
 #pragma unroll
-      for (int r = 0; r < 4; ++r) s[4 * m + r] = t[r] * qscale;
+      for (int r = 0; r < 4; ++r) s[4 * m + r] = t[r];
     }
+    const bool there_next = usable(next);
+    next = there_next ? next : 0;
+    load_keys(next, kvh * a.page_groups + gi);
 
     // Tokens outside [lo, len) of the first and last group: whatever their
     // bytes hold, they weigh nothing.
     const int t0 = g * kv::kGroup;
-    if (t0 < sp.lo || t0 > sp.len - kv::kGroup) {
+    if (t0 < sp.lo || t0 > sp.len - kv::kGroup || !there) {
       bool in[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const int t = t0 + 8 * G + k;
-        in[k] = t >= sp.lo && t < sp.len;
+        in[k] = there && t >= sp.lo && t < sp.len;
         if (!in[k]) s[k] = -__builtin_inff();
       }
 #pragma unroll
@@ -380,40 +446,46 @@ __global__ __launch_bounds__(64 * kWaves) void attn_kernel(Args a) {
       }
     }
 
+    // The reference: per lane (its eight tokens) the largest score and the
+    // exponent of the largest value scale, then over the lanes of the column.
     float top = s[0];
 #pragma unroll
     for (int k = 1; k < 8; ++k) top = fmaxf(top, s[k]);
-    top = fmaxf(top, __shfl_xor(top, 16, 64));
-    top = fmaxf(top, __shfl_xor(top, 32, 64));
+    top *= qscale;
     if constexpr (VK == C_F16) {
       top -= 14.0f;
     } else {
-      _Float16 big = (_Float16)0.0f;
+      // Magnitudes of halves compare as integers (Q8_0 scales have no sign).
+      ushort2v part[4] = {{0, 0}, {0, 0}, {0, 0}, {0, 0}};
+#pragma unroll
+      for (int n = 0; n < NB; ++n) {
+        const u32x4 w = __builtin_bit_cast(u32x4, vd[n]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          part[k] = __builtin_elementwise_max(part[k], as_us2(VK == C_Q4_0 ? w[k] & 0x7fff7fffu : w[k]));
+      }
+      const half2v big = as_h2(as_u(__builtin_elementwise_max(__builtin_elementwise_max(part[0], part[1]),
+                                                              __builtin_elementwise_max(part[2], part[3]))));
+      // 2^e <= scale < 2^(e + 1); f16 scales are 0 or at least 2^-24.
+      const float bf = fmaxf(fmaxf((float)big[0], (float)big[1]), 0x1p-24f);
+      top += (float)((int)(__builtin_bit_cast(uint32_t, bf) >> 23) - 127 - 14);
+    }
+    top = max_over_groups(top);
+    if (__any(top > R)) {  // rare after the first groups
+      const float Rn = fmaxf(R, top), alpha = __builtin_amdgcn_exp2f(R - Rn);
+      R = Rn;
+      sum *= alpha;
 #pragma unroll
       for (int n = 0; n < NB; ++n)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) big = __builtin_fmaxf16(big, __builtin_fabsf16(vd[n][k]));
-      float bf = (float)big;
-      bf = fmaxf(bf, __shfl_xor(bf, 16, 64));
-      bf = fmaxf(bf, __shfl_xor(bf, 32, 64));
-      // 2^e <= bf < 2^(e + 1); f16 scales are 0 or at least 2^-24.
-      const int e = (int)(__builtin_bit_cast(uint32_t, fmaxf(bf, 0x1p-24f)) >> 23) - 127;
-      top += (float)(e - 14);
+        for (int x = 0; x < 2; ++x) acc[n][x] *= alpha;
     }
-    const float Rn = fmaxf(R, top);
-    const float alpha = __builtin_amdgcn_exp2f(R - Rn);
-    R = Rn;
-    float p[8], ps = 0.0f;
+    float p[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      p[k] = __builtin_amdgcn_exp2f(s[k] - Rn);
-      ps += p[k];
+      p[k] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[k], qscale, -R));
+      sum += p[k];
     }
-    sum = __builtin_fmaf(sum, alpha, ps);
-#pragma unroll
-    for (int n = 0; n < NB; ++n)
-#pragma unroll
-      for (int x = 0; x < 2; ++x) acc[n][x] *= alpha;
 
     half8 ph, pl;
     if constexpr (VK == C_F16) {
@@ -427,7 +499,8 @@ __global__ __launch_bounds__(64 * kWaves) void attn_kernel(Args a) {
     for (int n = 0; n < NB; ++n) {
       if constexpr (VK != C_F16) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) ph[k] = (_Float16)(p[v_token<VK>(k)] * (float)vd[n][v_token<VK>(k)]);
+        for (int k = 0; k < 8; ++k)  // one v_fma_mix each
+          ph[k] = (_Float16)__builtin_fmaf(p[v_token<VK>(k)], (float)vd[n][v_token<VK>(k)], 0.0f);
         if constexpr (SPLIT) {
           // The second term is what the first one, as it was rounded, leaves:
           // the compiler must not recompute that rounding in another way.
@@ -439,14 +512,16 @@ __global__ __launch_bounds__(64 * kWaves) void attn_kernel(Args a) {
       }
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        const half8 v = value_operand<VK>(vr[n], x);
+        const half8 v = value_operand<VK>(vr[n], x, nb);
         acc[n][x] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, ph, acc[n][x], 0, 0, 0);
         if constexpr (SPLIT) acc[n][x] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, pl, acc[n][x], 0, 0, 0);
       }
     }
+    load_values(next, kvh * a.page_groups + gi);
+    there = there_next;
+    g += kWaves;
   }
-  sum += __shfl_xor(sum, 16, 64);
-  sum += __shfl_xor(sum, 32, 64);
+  sum = sum_over_groups(sum);
 
   // The four waves' parts, joined through LDS: references and sums first, then
   // the accumulators on the common reference, waves 2 and 3 handing theirs to

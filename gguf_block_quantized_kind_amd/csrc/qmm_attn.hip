@@ -7,33 +7,63 @@ namespace attn {
 
 // One workgroup per (sequence, query head): the splits' parts, weighted by
 // 2^(R_i - max R), over the weighted sums (plus the sink's share).  Sequences
-// of one split were finished by the attention kernel.
+// of one split were finished by the attention kernel.  Weights and sums come
+// from all threads at once, the parts from 1024 / D groups of D / 4 lanes, so
+// that a sequence of a thousand splits costs no chain of a thousand loads.
 template <typename QT>
 __global__ __launch_bounds__(256) void join_kernel(Args a, int D) {
-  const int lane = threadIdx.x & 63;
+  constexpr int kChunk = 1024;
+  __shared__ float weight[kChunk];
+  __shared__ float red[8];
+  __shared__ floatx4 part[256];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int b = blockIdx.x / a.n_q, hq = blockIdx.x - b * a.n_q;
-  const int c = groups_per_split(a, lane);
-  const Span sp = span_of(a, b);
-  const int splits = (sp.n + c - 1) / c;
+  const Found f = find_split(a, lane, 0, b);
+  const int splits = (span_of(a, b).n + f.c - 1) / f.c;
   if (splits <= 1) return;
-  const Found f = find_split(a, lane, c, 0, b);
   const int kvh = hq / a.G, in = hq - kvh * a.G, tile = in / 16, h = in - tile * 16;
-  const int nh = a.n_kv * a.tiles;
-  const int64_t item0 = f.first * nh + tile * a.n_kv + kvh;
+  const int64_t nh = (int64_t)a.n_kv * a.tiles, item0 = f.first * nh + tile * a.n_kv + kvh;
   const float *ml = a.part + a.items * a.heads * D;
+
   float Rm = kFloor;
-  for (int i = 0; i < splits; ++i) Rm = fmaxf(Rm, ml[((item0 + (int64_t)i * nh) * a.heads + h) * 2]);
-  const int d = threadIdx.x;
-  if (d >= D) return;
-  float o = 0.0f, l = 0.0f;
-  for (int i = 0; i < splits; ++i) {
-    const int64_t at = (item0 + (int64_t)i * nh) * a.heads + h;
-    const float w = __builtin_amdgcn_exp2f(ml[at * 2] - Rm);
-    o = __builtin_fmaf(w, a.part[at * D + d], o);
-    l = __builtin_fmaf(w, ml[at * 2 + 1], l);
+  for (int i = tid; i < splits; i += 256) Rm = fmaxf(Rm, ml[((item0 + i * nh) * a.heads + h) * 2]);
+#pragma unroll
+  for (int k = 1; k < 64; k <<= 1) Rm = fmaxf(Rm, __shfl_xor(Rm, k, 64));
+  if (lane == 0) red[wave] = Rm;
+  __syncthreads();
+  Rm = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+
+  const int lanes = D / 4, ways = 256 / lanes, way = tid / lanes, d4 = tid - way * lanes;
+  floatx4 o = {0, 0, 0, 0};
+  float l = 0.0f;
+  for (int i0 = 0; i0 < splits; i0 += kChunk) {
+    const int n = min(kChunk, splits - i0);
+    if (i0) __syncthreads();
+    for (int i = tid; i < n; i += 256) {
+      const float *m = ml + ((item0 + (i0 + i) * nh) * a.heads + h) * 2;
+      const float w = __builtin_amdgcn_exp2f(m[0] - Rm);
+      weight[i] = w;
+      l = __builtin_fmaf(w, m[1], l);
+    }
+    __syncthreads();
+    if (way < ways) {
+      const float *p = a.part + ((item0 + i0 * nh) * a.heads + h) * D + 4 * d4;
+      const int64_t step = nh * a.heads * D;
+#pragma unroll 4
+      for (int i = way; i < n; i += ways) o += weight[i] * *(const floatx4 *)(p + i * step);
+    }
   }
+#pragma unroll
+  for (int k = 1; k < 64; k <<= 1) l += __shfl_xor(l, k, 64);
+  if (lane == 0) red[4 + wave] = l;
+  part[tid] = o;
+  __syncthreads();
+  if (tid >= D) return;
+  l = (red[4] + red[5]) + (red[6] + red[7]);
+  float v = 0.0f;
+  for (int k = 0; k < ways; ++k) v += ((const float *)part)[k * D + tid];
   if (a.sinks) l += __builtin_amdgcn_exp2f(fminf(a.sinks[hq] * 1.44269504f - Rm, 120.0f));
-  ((QT *)a.out)[((int64_t)b * a.n_q + hq) * D + d] = (QT)(l > 0.0f || l != l ? o / l : 0.0f);
+  ((QT *)a.out)[((int64_t)b * a.n_q + hq) * D + tid] = (QT)(l > 0.0f || l != l ? v / l : 0.0f);
 }
 
 // Splits aim at this many workgroups.
