@@ -55,6 +55,7 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 constexpr float kFloor = -1e30f;  // R of no tokens
 constexpr int kWaves = 4;
 constexpr int kMinGroups = 4;  // groups per split at least: one per wave
+constexpr int kTarget = 1024;  // workgroups the splits aim at
 
 struct Args {
   const uint8_t *kp, *vp;
@@ -71,9 +72,9 @@ struct Args {
   int64_t window;
   const float *sinks;
   void *out;
-  float *part;  // [item][heads][D] then [item][heads][2] (reference, sum)
+  float *part;     // [item][heads][D], then [item][heads][2]: reference and sum
+  int32_t *plan;   // [B][2]: a sequence's first split and number of splits, for the join
   int64_t items;
-  int target;  // workgroups the splits aim at
 };
 
 // The groups [g0, g0 + n) of sequence b that hold attended tokens [lo, len).
@@ -105,44 +106,59 @@ __device__ __forceinline__ float sum_over_groups(float v) {
   return __builtin_bit_cast(float, (uint32_t)b[0]) + __builtin_bit_cast(float, (uint32_t)b[1]);
 }
 
+// Inclusive sum over the lanes of a wave, without LDS: within rows of 16, then
+// each row's last lane into the rows after it.
+__device__ __forceinline__ uint32_t scan(uint32_t v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, true);  // row_shr:1
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);  // row_bcast:15 into rows 1, 3
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);  // row_bcast:31 into rows 2, 3
+  return v;
+}
+
 // Splits are numbered through the batch (at least one per sequence, so that
 // every output row is written).  The groups per split are the attended groups
 // of the whole batch over the target number of workgroups, at least one group
-// per wave.
+// per wave.  find_split: the sequence (-1: past the last) that split `unit`
+// belongs to, its first split and the groups per split.
 struct Found {
-  int b, c;       // sequence (-1: past the last split), groups per split
-  int64_t first;  // its first split
+  int b, c;
+  uint32_t first;
 };
-// want_b < 0: the sequence that split `unit` belongs to; else sequence want_b.
-__device__ __forceinline__ Found find_split(const Args &a, int lane, int64_t unit, int want_b) {
-  const int64_t nh = (int64_t)a.n_kv * a.tiles;
-  if (a.B == 1) {  // no scan
-    const int n = span_of(a, 0).n;
-    const int c = (int)max((n * nh + a.target - 1) / a.target, (int64_t)kMinGroups);
-    return Found{want_b < 0 && unit >= max(1, (n + c - 1) / c) ? -1 : 0, c, 0};
-  }
-  int64_t total = 0;
-  for (int b0 = 0; b0 < a.B; b0 += 64) total += span_of(a, b0 + lane).n;
-#pragma unroll
-  for (int k = 1; k < 64; k <<= 1) total += __shfl_xor(total, k, 64);
-  const int c = (int)max((total * nh + a.target - 1) / a.target, (int64_t)kMinGroups);
-  int64_t before = 0;
-  for (int b0 = 0; b0 < a.B; b0 += 64) {
-    const int n = span_of(a, b0 + lane).n;
-    const int splits = b0 + lane < a.B ? max(1, (n + c - 1) / c) : 0;
-    int incl = splits;
-#pragma unroll
-    for (int k = 1; k < 64; k <<= 1) {
-      const int v = __shfl_up(incl, k, 64);
-      if (lane >= k) incl += v;
+__device__ __forceinline__ Found find_split(const Args &a, int lane, uint32_t unit) {
+  const uint32_t nh = (uint32_t)(a.n_kv * a.tiles);
+  int n = span_of(a, lane).n;
+  uint64_t total;
+  if (a.B == 1) {
+    total = (uint32_t)__builtin_amdgcn_readfirstlane(n);
+  } else {
+    total = 0;
+    for (int b0 = 0;;) {  // (at most 2^26 groups a sequence: one less keeps 64 of them below 2^32)
+      total += (uint32_t)__builtin_amdgcn_readlane((int)scan((uint32_t)min(n, (1 << 26) - 1)), 63);
+      b0 += 64;
+      if (b0 >= a.B) break;
+      n = span_of(a, b0 + lane).n;
     }
-    const bool hit = want_b < 0 ? unit < before + incl : b0 + lane == want_b;
-    const uint64_t mask = __ballot(hit);
+    if (a.B > 64) n = span_of(a, lane).n;
+  }
+  const int c = max((int)((total * nh + (kTarget - 1)) / kTarget), kMinGroups);
+  if (a.B == 1) {
+    n = __builtin_amdgcn_readfirstlane(n);
+    return Found{unit < (uint32_t)max(1, (n + c - 1) / c) ? 0 : -1, c, 0};
+  }
+  uint32_t before = 0;
+  for (int b0 = 0; b0 < a.B; b0 += 64) {
+    if (b0) n = span_of(a, b0 + lane).n;
+    const uint32_t splits = b0 + lane < a.B ? (uint32_t)max(1, (n + c - 1) / c) : 0;
+    const uint32_t incl = scan(splits);
+    const uint64_t mask = __ballot(unit - before < incl);
     if (mask) {
       const int l = __ffsll((unsigned long long)mask) - 1;
-      return Found{b0 + l, c, before + __shfl(incl - splits, l, 64)};
+      return Found{b0 + l, c, before + (uint32_t)__builtin_amdgcn_readlane((int)(incl - splits), l)};
     }
-    before += __shfl(incl, 63, 64);
+    before += (uint32_t)__builtin_amdgcn_readlane((int)incl, 63);
   }
   return Found{-1, c, before};
 }
@@ -272,15 +288,18 @@ __global__ __launch_bounds__(64 * kWaves) void attn_kernel(Args a) {
   const int j = lane & 15, G = lane >> 4;
 
   // Which split this workgroup has.
-  const int nh = a.n_kv * a.tiles;
-  const int64_t unit = (int64_t)blockIdx.x / nh;
+  const uint32_t nh = (uint32_t)(a.n_kv * a.tiles), unit = blockIdx.x / nh;
   const int hh = (int)(blockIdx.x - unit * nh), kvh = hh % a.n_kv, tile = hh / a.n_kv;
-  const Found f = find_split(a, lane, unit, -1);
+  const Found f = find_split(a, lane, unit);
   if (f.b < 0) return;
   const int b = __builtin_amdgcn_readfirstlane(f.b), c = __builtin_amdgcn_readfirstlane(f.c);
   const Span sp = span_of(a, b);
   const int splits = max(1, (sp.n + c - 1) / c), each = (sp.n + splits - 1) / splits;
   const int mine = (int)(unit - f.first);
+  if (mine == 0 && hh == 0 && threadIdx.x == 0) {
+    a.plan[2 * b] = (int32_t)f.first;
+    a.plan[2 * b + 1] = splits;
+  }
   const int gs = __builtin_amdgcn_readfirstlane(sp.g0 + min(mine * each, sp.n));
   const int ge = __builtin_amdgcn_readfirstlane(sp.g0 + min((mine + 1) * each, sp.n));
 

@@ -18,11 +18,10 @@ __global__ __launch_bounds__(256) void join_kernel(Args a, int D) {
   __shared__ floatx4 part[256];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int b = blockIdx.x / a.n_q, hq = blockIdx.x - b * a.n_q;
-  const Found f = find_split(a, lane, 0, b);
-  const int splits = (span_of(a, b).n + f.c - 1) / f.c;
+  const int first = a.plan[2 * b], splits = a.plan[2 * b + 1];
   if (splits <= 1) return;
   const int kvh = hq / a.G, in = hq - kvh * a.G, tile = in / 16, h = in - tile * 16;
-  const int64_t nh = (int64_t)a.n_kv * a.tiles, item0 = f.first * nh + tile * a.n_kv + kvh;
+  const int64_t nh = (int64_t)a.n_kv * a.tiles, item0 = first * nh + tile * a.n_kv + kvh;
   const float *ml = a.part + a.items * a.heads * D;
 
   float Rm = kFloor;
@@ -66,9 +65,6 @@ __global__ __launch_bounds__(256) void join_kernel(Args a, int D) {
   ((QT *)a.out)[((int64_t)b * a.n_q + hq) * D + tid] = (QT)(l > 0.0f || l != l ? v / l : 0.0f);
 }
 
-// Splits aim at this many workgroups.
-constexpr int kTarget = 1024;
-
 static int64_t items_of(int64_t B, int64_t n_q, int64_t n_kv) {
   const int64_t tiles = (n_q / n_kv + 15) / 16;
   return kTarget + B * n_kv * tiles;
@@ -78,7 +74,7 @@ static int64_t items_of(int64_t B, int64_t n_q, int64_t n_kv) {
 
 size_t attn_workspace_bytes(int64_t B, int64_t n_q, int64_t n_kv, int64_t head_dim) {
   const int64_t G = n_q / n_kv, heads = G < 16 ? G : 16;
-  return (size_t)(attn::items_of(B, n_q, n_kv) * heads * (head_dim + 2) * 4);
+  return (size_t)(attn::items_of(B, n_q, n_kv) * heads * (head_dim + 2) * 4 + B * 8);
 }
 
 hipError_t launch_attn_decode(const KvCache &kc, const AttnDecode &d, hipStream_t s) {
@@ -97,7 +93,7 @@ hipError_t launch_attn_decode(const KvCache &kc, const AttnDecode &d, hipStream_
   a.window = d.window, a.sinks = d.sinks, a.out = d.out;
   a.part = (float *)d.workspace;
   a.items = items_of(d.B, d.n_q, kc.n_kv);
-  a.target = kTarget;
+  a.plan = (int32_t *)(a.part + a.items * a.heads * (kc.head_dim + 2));
   const int NB = (int)(kc.head_dim / 32);
   hipError_t e = hipErrorInvalidValue;
 #define QMM_CASE(K, V, F) \

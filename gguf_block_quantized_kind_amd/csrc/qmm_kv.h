@@ -95,7 +95,8 @@ __device__ __forceinline__ _Float16 block_scale(float hi, float lo, uint32_t bit
 __device__ __forceinline__ uint32_t magnitude_bits(float x) { return __builtin_bit_cast(uint32_t, x) & 0x7fffffffu; }
 
 // A block's step and its reciprocal, each correctly rounded (both 0 where
-// every code is that of zero: a zero or NaN scale).
+// every code is that of zero: a zero or NaN scale, whose elements are taken as
+// zeros).
 struct Step {
   float d, inv;
 };
@@ -105,16 +106,16 @@ __device__ __forceinline__ Step step_of(_Float16 h) {
   return Step{none ? 0.0f : d, none ? 0.0f : 1.0f / d};
 }
 
-// The stored code of x: the nearest integer to the correctly rounded x / d,
+// The stored code of x (an integer in f32; the caller's conversion to a byte
+// cuts it at 0 and 255): the nearest integer to the correctly rounded x / d,
 // ties to even.  With inv the correctly rounded 1 / d, one residual step makes
 // the quotient correctly rounded (Markstein, IBM J. Res. Dev. 34, 1990): three
 // operations an element instead of a division's dozen.
 template <int KIND>
-__device__ __forceinline__ uint32_t encode(float x, Step st) {
+__device__ __forceinline__ float encode(float x, Step st) {
   const float q0 = x * st.inv;
-  const float q = st.inv == 0.0f ? 0.0f : rintf(__builtin_fmaf(__builtin_fmaf(-st.d, q0, x), st.inv, q0));
-  if constexpr (KIND == C_Q8_0) return (uint32_t)((int)fminf(fmaxf(q, -127.0f), 127.0f) + 128);
-  return (uint32_t)(int)fminf(fmaxf(q + 8.0f, 0.0f), 15.0f);
+  const float q = rintf(__builtin_fmaf(__builtin_fmaf(-st.d, q0, x), st.inv, q0));
+  return KIND == C_Q8_0 ? fmaxf(q, -127.0f) + 128.0f : fminf(q + 8.0f, 15.0f);
 }
 
 // cos and sin of pos * freq (radians per position), each within about 1e-7.
@@ -240,6 +241,13 @@ __device__ __forceinline__ void rotate_rows(const Rotate &r, int64_t i) {
     __builtin_memcpy(__builtin_assume_aligned(y + (int64_t)h * r.D + da, sizeof(Y)), &u, sizeof(Y));
     __builtin_memcpy(__builtin_assume_aligned(y + (int64_t)h * r.D + db, sizeof(Y)), &v, sizeof(Y));
   }
+}
+
+// The same by q_out's type and the width, known at run time.
+template <typename T>
+__device__ __forceinline__ void rotate_any(const Rotate &r, int out_f16, int wide, int64_t i) {
+  if (out_f16) wide ? rotate_rows<T, _Float16, 4>(r, i) : rotate_rows<T, _Float16, 1>(r, i);
+  else wide ? rotate_rows<T, float, 4>(r, i) : rotate_rows<T, float, 1>(r, i);
 }
 
 // Fills in the split of T rows of H heads; four pairs a thread where every

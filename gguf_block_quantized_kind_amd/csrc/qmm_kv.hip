@@ -16,6 +16,8 @@
 // prompt's tokens fill whole units wherever it starts; an octet whose slots
 // are not eight consecutive aligned ones (other sequences, skipped tokens, the
 // window's ends) goes byte by byte.
+#include <type_traits>
+
 #include "qmm_internal.h"
 #include "qmm_kv.h"
 
@@ -75,128 +77,118 @@ __device__ __forceinline__ uint32_t pack_h(float a, float b) {
   return (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)a) | (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)b) << 16;
 }
 
-// One head's keys or values of a window: rows x + t * stride.
-template <int KIND, bool IS_V, typename T, bool ROPE>
-__device__ __forceinline__ void write_window(const Cache &c, uint8_t *pages, const T *x, int64_t stride, bool vec, int nt,
-                                             const int32_t *pos, const Rope &rope, const Window &w, float *rows,
-                                             Step *steps) {
-  const int tid = threadIdx.x, NB = c.NB, D = NB * 32, pitch = D + 4;
-  for (int i = tid; i < nt * (D / 4); i += 256) {
-    const int t = i / (D / 4), d = (i - t * (D / 4)) * 4;
-    if (w.slot[t] >= 0) *(floatx4 *)(rows + t * pitch + d) = load4(x + t * stride + d, vec);
-  }
-  __syncthreads();
-  if constexpr (ROPE) {
-    const int half = rope.n_rot >> 1;
-    for (int i = tid; i < nt * half; i += 256) {
-      const int t = i / half, p = i - t * half;
-      if (w.slot[t] < 0) continue;
-      float *a = rows + t * pitch + (rope.interleaved ? 2 * p : p), *b = a + (rope.interleaved ? 1 : half);
-      float co, si;
-      rotation(pos[t], rope.freqs[p], co, si);
-      co *= rope.mscale;
-      si *= rope.mscale;
-      const float u = *a, v = *b;
-      *a = u * co - v * si;
-      *b = u * si + v * co;
+// One byte of a code at place k of w.
+__device__ __forceinline__ uint32_t put(uint32_t w, int k, float code) {
+  return __builtin_amdgcn_cvt_pk_u8_f32(code, k, w);
+}
+
+// The block scales of a window's rows, four lanes per (token, block) with
+// eight elements each: stored in the cache, and as steps for the encoding.
+template <int KIND, int NB>
+__device__ __forceinline__ void write_scales(uint8_t *pages, const Window &w, float *rows, Step *steps) {
+  constexpr int pitch = NB * 32 + 4;
+#pragma unroll
+  for (int i0 = 0; i0 < NB * kWindow * 4; i0 += 256) {
+    const int i = i0 + threadIdx.x, t = (i >> 2) & (kWindow - 1), b = i >> 7;
+    if (b >= NB || w.slot[t] < 0) continue;  // (all four lanes)
+    float *e = rows + t * pitch + b * 32 + (i & 3) * 8;
+    const floatx4 u = *(const floatx4 *)e, v = *(const floatx4 *)(e + 4);
+    float hi = u[0], lo = u[0];
+    uint32_t bits = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      hi = fmaxf(hi, fmaxf(u[k], v[k]));
+      lo = fminf(lo, fminf(u[k], v[k]));
+      bits = max(bits, max(magnitude_bits(u[k]), magnitude_bits(v[k])));
     }
-    __syncthreads();
+#pragma unroll
+    for (int k = 1; k < 4; k <<= 1) {
+      hi = fmaxf(hi, __shfl_xor(hi, k, 4));
+      lo = fminf(lo, __shfl_xor(lo, k, 4));
+      bits = max(bits, (uint32_t)__shfl_xor((int)bits, k, 4));
+    }
+    const _Float16 h = block_scale<KIND>(hi, lo, bits);
+    if (bits >= 0x7f800000u) *(floatx4 *)e = *(floatx4 *)(e + 4) = floatx4{0, 0, 0, 0};
+    if ((i & 3) == 0) {
+      steps[b * kWindow + t] = step_of(h);
+      *(_Float16 *)(pages + w.base[t] + scale_offset(KIND, NB, b, w.r[t])) = h;
+    }
   }
-  if constexpr (KIND != C_F16) {
-    // Four lanes per (token, block), eight elements each.
-    for (int i = tid; i < NB * kWindow * 4; i += 256) {
-      const int t = (i >> 2) & (kWindow - 1), b = i >> 7;
-      if (w.slot[t] < 0) continue;
-      const float *e = rows + t * pitch + b * 32 + (i & 3) * 8;
-      const floatx4 u = *(const floatx4 *)e, v = *(const floatx4 *)(e + 4);
-      float hi = u[0], lo = u[0];
-      uint32_t bits = 0;
+}
+
+template <int KIND, int NB>
+__device__ __forceinline__ void write_keys(uint8_t *pages, const Window &w, const float *rows, const Step *steps) {
+  constexpr int pitch = NB * 32 + 4;
+#pragma unroll
+  for (int i0 = 0; i0 < NB * 4 * kWindow; i0 += 256) {
+    const int i = i0 + threadIdx.x, t = i & (kWindow - 1), G = (i >> 5) & 3, b = i >> 7;
+    if (b >= NB || w.slot[t] < 0) continue;
+    const float *e = rows + t * pitch + b * 32;
+    uint8_t *p = pages + w.base[t] + code_offset<KIND, false>(b, w.r[t], KIND == C_Q4_0 ? 4 * G : 8 * G);
+    const floatx4 u = *(const floatx4 *)(e + (KIND == C_Q4_0 ? 4 * G : 8 * G));
+    const floatx4 v = *(const floatx4 *)(e + (KIND == C_Q4_0 ? 16 + 4 * G : 8 * G + 4));
+    if constexpr (KIND == C_F16) {
+      *(u32x4 *)p = u32x4{pack_h(u[0], u[1]), pack_h(u[2], u[3]), pack_h(v[0], v[1]), pack_h(v[2], v[3])};
+    } else {
+      const Step st = steps[b * kWindow + t];
+      uint32_t lo = 0, hi = 0;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        hi = fmaxf(hi, fmaxf(u[k], v[k]));
-        lo = fminf(lo, fminf(u[k], v[k]));
-        bits = max(bits, max(magnitude_bits(u[k]), magnitude_bits(v[k])));
+        lo = put(lo, k, encode<KIND>(u[k], st));
+        hi = put(hi, k, encode<KIND>(v[k], st));
       }
-#pragma unroll
-      for (int k = 1; k < 4; k <<= 1) {
-        hi = fmaxf(hi, __shfl_xor(hi, k, 4));
-        lo = fminf(lo, __shfl_xor(lo, k, 4));
-        bits = max(bits, (uint32_t)__shfl_xor((int)bits, k, 4));
-      }
-      if ((i & 3) == 0) {
-        const _Float16 h = block_scale<KIND>(hi, lo, bits);
-        steps[b * kWindow + t] = step_of(h);
-        *(_Float16 *)(pages + w.base[t] + scale_offset(KIND, NB, b, w.r[t])) = h;
-      }
+      if constexpr (KIND == C_Q8_0) *(u32x2 *)p = u32x2{lo, hi};
+      else *(uint32_t *)p = lo | hi << 4;
     }
-    __syncthreads();
   }
-  if constexpr (!IS_V) {
-    for (int i = tid; i < NB * 4 * kWindow; i += 256) {
-      const int t = i & (kWindow - 1), G = (i >> 5) & 3, b = i >> 7;
-      if (w.slot[t] < 0) continue;
-      const float *e = rows + t * pitch + b * 32;
-      uint8_t *p = pages + w.base[t] + code_offset<KIND, false>(b, w.r[t], KIND == C_Q4_0 ? 4 * G : 8 * G);
-      const floatx4 u = *(const floatx4 *)(e + (KIND == C_Q4_0 ? 4 * G : 8 * G));
-      const floatx4 v = *(const floatx4 *)(e + (KIND == C_Q4_0 ? 16 + 4 * G : 8 * G + 4));
+}
+
+template <int KIND, int NB>
+__device__ __forceinline__ void write_values(uint8_t *pages, int nt, const Window &w, const float *rows,
+                                             const Step *steps) {
+  constexpr int pitch = NB * 32 + 4;
+  for (int i = threadIdx.x; i < kOctets * NB * 16; i += 256) {
+    const int j = i & 15, b = (i >> 4) % NB, o = (i >> 4) / NB;
+    const int t0 = 8 * o - w.phase;
+    if (w.whole[o]) {
+      const float *e = rows + t0 * pitch + b * 32 + j;
+      uint8_t *p = pages + w.base[t0] + code_offset<KIND, true>(b, w.r[t0], j);
       if constexpr (KIND == C_F16) {
-        *(u32x4 *)p = u32x4{pack_h(u[0], u[1]), pack_h(u[2], u[3]), pack_h(v[0], v[1]), pack_h(v[2], v[3])};
-      } else {
-        const Step st = steps[b * kWindow + t];
-        uint32_t lo = 0, hi = 0;
+        u32x4 a, v;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          lo |= encode<KIND>(u[k], st) << (8 * k);
-          hi |= encode<KIND>(v[k], st) << (8 * k);
+          a[k] = pack_h(e[2 * k * pitch], e[(2 * k + 1) * pitch]);
+          v[k] = pack_h(e[2 * k * pitch + 16], e[(2 * k + 1) * pitch + 16]);
         }
-        if constexpr (KIND == C_Q8_0) *(u32x2 *)p = u32x2{lo, hi};
-        else *(uint32_t *)p = lo | hi << 4;
-      }
-    }
-  } else {
-    for (int i = tid; i < NB * kOctets * 16; i += 256) {
-      const int j = i & 15, o = (i >> 4) % kOctets, b = (i >> 4) / kOctets;
-      const int t0 = 8 * o - w.phase;
-      if (w.whole[o]) {
-        const float *e = rows + t0 * pitch + b * 32 + j;
-        uint8_t *p = pages + w.base[t0] + code_offset<KIND, true>(b, w.r[t0], j);
-        if constexpr (KIND == C_F16) {
-          u32x4 a, v;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            a[k] = pack_h(e[2 * k * pitch], e[(2 * k + 1) * pitch]);
-            v[k] = pack_h(e[2 * k * pitch + 16], e[(2 * k + 1) * pitch + 16]);
-          }
-          *(u32x4 *)p = a;
-          *(u32x4 *)(p + 1024) = v;
-        } else {
-          u32x4 q = {0, 0, 0, 0};
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const Step st = steps[b * kWindow + t0 + k];
-            q[k >> 2] |= encode<KIND>(e[k * pitch], st) << (8 * (k & 3));
-            q[2 + (k >> 2)] |= encode<KIND>(e[k * pitch + 16], st) << (8 * (k & 3));
-          }
-          if constexpr (KIND == C_Q8_0) *(u32x4 *)p = q;
-          else *(u32x2 *)p = u32x2{q[0] | q[2] << 4, q[1] | q[3] << 4};
-        }
+        *(u32x4 *)p = a;
+        *(u32x4 *)(p + 1024) = v;
       } else {
-        for (int t = max(t0, 0); t < min(t0 + 8, nt); ++t) {
-          if (w.slot[t] < 0) continue;
-          const float *e = rows + t * pitch + b * 32 + j;
-          uint8_t *p = pages + w.base[t];
-          if constexpr (KIND == C_F16) {
-            *(_Float16 *)(p + code_offset<KIND, true>(b, w.r[t], j)) = (_Float16)e[0];
-            *(_Float16 *)(p + code_offset<KIND, true>(b, w.r[t], j + 16)) = (_Float16)e[16];
+        uint32_t q[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const Step st = steps[b * kWindow + t0 + k];
+          q[k >> 2] = put(q[k >> 2], k & 3, encode<KIND>(e[k * pitch], st));
+          q[2 + (k >> 2)] = put(q[2 + (k >> 2)], k & 3, encode<KIND>(e[k * pitch + 16], st));
+        }
+        if constexpr (KIND == C_Q8_0) *(u32x4 *)p = u32x4{q[0], q[1], q[2], q[3]};
+        else *(u32x2 *)p = u32x2{q[0] | q[2] << 4, q[1] | q[3] << 4};
+      }
+    } else {
+      for (int t = max(t0, 0); t < min(t0 + 8, nt); ++t) {
+        if (w.slot[t] < 0) continue;
+        const float *e = rows + t * pitch + b * 32 + j;
+        uint8_t *p = pages + w.base[t];
+        if constexpr (KIND == C_F16) {
+          *(_Float16 *)(p + code_offset<KIND, true>(b, w.r[t], j)) = (_Float16)e[0];
+          *(_Float16 *)(p + code_offset<KIND, true>(b, w.r[t], j + 16)) = (_Float16)e[16];
+        } else {
+          const Step st = steps[b * kWindow + t];
+          const uint32_t q = put(put(0, 0, encode<KIND>(e[0], st)), 1, encode<KIND>(e[16], st));
+          if constexpr (KIND == C_Q8_0) {
+            p[code_offset<KIND, true>(b, w.r[t], j)] = (uint8_t)q;
+            p[code_offset<KIND, true>(b, w.r[t], j + 16)] = (uint8_t)(q >> 8);
           } else {
-            const Step st = steps[b * kWindow + t];
-            const uint32_t lo = encode<KIND>(e[0], st), hi = encode<KIND>(e[16], st);
-            if constexpr (KIND == C_Q8_0) {
-              p[code_offset<KIND, true>(b, w.r[t], j)] = (uint8_t)lo;
-              p[code_offset<KIND, true>(b, w.r[t], j + 16)] = (uint8_t)hi;
-            } else {
-              p[code_offset<KIND, true>(b, w.r[t], j)] = (uint8_t)(lo | hi << 4);
-            }
+            p[code_offset<KIND, true>(b, w.r[t], j)] = (uint8_t)(q | q >> 4);
           }
         }
       }
@@ -206,6 +198,7 @@ __device__ __forceinline__ void write_window(const Cache &c, uint8_t *pages, con
 
 struct WriteArgs {
   Cache cache;
+  int k_kind, v_kind;
   const void *k, *v;
   int64_t k_stride, v_stride;
   int k_vec, v_vec;
@@ -214,36 +207,68 @@ struct WriteArgs {
   int64_t kv_wgs;  // workgroups of the cache part; the rest rotate q
   Rope rope;
   Rotate q;
+  int q_out_f16, q_wide;
 };
 
-// V: pairs per thread of the q rotation (0: no rotation).
-template <int KK, int VK, typename T, typename QO, int V>
+template <typename T, int NB, bool ROPE>
 __global__ __launch_bounds__(256) void kv_write_kernel(WriteArgs a) {
   if ((int64_t)blockIdx.x >= a.kv_wgs) {
-    if constexpr (V > 0) rotate_rows<T, QO, V>(a.q, ((int64_t)blockIdx.x - a.kv_wgs) * 256 + threadIdx.x);
+    if constexpr (ROPE) rotate_any<T>(a.q, a.q_out_f16, a.q_wide, ((int64_t)blockIdx.x - a.kv_wgs) * 256 + threadIdx.x);
     return;
   }
+  constexpr int D = NB * 32, pitch = D + 4;
   __shared__ Window w;
-  extern __shared__ float rows[];  // [kWindow][D + 4], then steps [NB][kWindow]
-  const int D = a.cache.NB * 32;
-  Step *steps = (Step *)(rows + kWindow * (D + 4));
-  const int n = a.cache.n_kv;
-  const int64_t win = (int64_t)blockIdx.x / (2 * n);
+  __shared__ float rows[kWindow * pitch];
+  __shared__ Step steps[NB * kWindow];
+  const int tid = threadIdx.x, n = a.cache.n_kv;
+  const int64_t win = (int64_t)((uint32_t)blockIdx.x / (uint32_t)(2 * n));
   const int rest = (int)(blockIdx.x - win * 2 * n), is_v = rest >= n, head = is_v ? rest - n : rest;
-  const int64_t t0 = win * kWindow;
+  const int kind = is_v ? a.v_kind : a.k_kind;
+  const int64_t t0 = win * kWindow, stride = is_v ? a.v_stride : a.k_stride;
   const int nt = (int)min((int64_t)kWindow, a.T - t0);
-  find_window(w, a.cache, a.slots, t0, nt, is_v ? VK : KK, head);
+
+  // Rows, slots and the first rotations' angles in one round of loads.
+  const T *x = (const T *)(is_v ? a.v : a.k) + t0 * stride + head * D;
+  const bool vec = is_v ? a.v_vec : a.k_vec;
+#pragma unroll
+  for (int i0 = 0; i0 < kWindow * (D / 4); i0 += 256) {
+    const int i = i0 + tid, t = i / (D / 4), d = (i % (D / 4)) * 4;
+    if (t < nt) *(floatx4 *)(rows + t * pitch + d) = load4(x + t * stride + d, vec);
+  }
+  const int half = ROPE ? a.rope.n_rot >> 1 : 0;
+  float co = 1.0f, si = 0.0f;
+  if (ROPE && !is_v && tid < nt * half) rotation(a.pos[t0 + tid / half], a.rope.freqs[tid % half], co, si);
+  find_window(w, a.cache, a.slots, t0, nt, kind, head);
   __syncthreads();
-  if (is_v)
-    write_window<VK, true, T, false>(a.cache, a.cache.v_pages, (const T *)a.v + t0 * a.v_stride + head * D, a.v_stride,
-                                     a.v_vec, nt, nullptr, a.rope, w, rows, steps);
-  else
-    write_window<KK, false, T, (V > 0)>(a.cache, a.cache.k_pages, (const T *)a.k + t0 * a.k_stride + head * D, a.k_stride,
-                                        a.k_vec, nt, a.pos + t0, a.rope, w, rows, steps);
+  if (ROPE && !is_v) {
+    for (int i = tid; i < nt * half; i += 256) {
+      const int t = i / half, p = i - t * half;
+      if (i >= 256) rotation(a.pos[t0 + t], a.rope.freqs[p], co, si);
+      float *u = rows + t * pitch + (a.rope.interleaved ? 2 * p : p), *v = u + (a.rope.interleaved ? 1 : half);
+      const float c = co * a.rope.mscale, s = si * a.rope.mscale, xa = *u, xb = *v;
+      *u = xa * c - xb * s;
+      *v = xa * s + xb * c;
+    }
+    __syncthreads();
+  }
+  uint8_t *pages = is_v ? a.cache.v_pages : a.cache.k_pages;
+  auto go = [&](auto k) {
+    constexpr int KIND = decltype(k)::value;
+    if constexpr (KIND != C_F16) {
+      write_scales<KIND, NB>(pages, w, rows, steps);
+      __syncthreads();
+    }
+    if (is_v) write_values<KIND, NB>(pages, nt, w, rows, steps);
+    else write_keys<KIND, NB>(pages, w, rows, steps);
+  };
+  if (kind == C_Q8_0) go(std::integral_constant<int, C_Q8_0>{});
+  else if (kind == C_Q4_0) go(std::integral_constant<int, C_Q4_0>{});
+  else go(std::integral_constant<int, C_F16>{});
 }
 
 struct ReadArgs {
   Cache cache;
+  int k_kind, v_kind;
   const int32_t *slots;
   void *k_out, *v_out;
   int64_t T;
@@ -255,16 +280,20 @@ __device__ __forceinline__ void store4(O *p, floatx4 v) {
   else *(floatx4 *)p = v;
 }
 
-template <int KIND>
-__device__ __forceinline__ float value(uint32_t code, float d) {
-  return d * (float)((int)code - (KIND == C_Q8_0 ? 128 : 8));
+// d * (code - offset), exactly: the value fits f32 and the offset's product
+// comes in by the same rounding.  Byte k of w, `zero` = -offset * d.
+__device__ __forceinline__ float value(uint32_t w, int k, float d, float zero) {
+  return __builtin_fmaf((float)(w >> (8 * k) & 255u), d, zero);
 }
+template <int KIND>
+constexpr float kOffset = KIND == C_Q8_0 ? -128.0f : -8.0f;
 
-template <int KIND, typename O>
+template <int KIND, int NB, typename O>
 __device__ __forceinline__ void read_keys(const Cache &c, O *out, int64_t out_stride, int nt, const Window &w) {
-  const int NB = c.NB, pieces = NB * 4;
-  for (int i = threadIdx.x; i < nt * pieces; i += 256) {
-    const int t = i / pieces, p = i - t * pieces, b = p >> 2, G = p & 3;
+#pragma unroll
+  for (int i0 = 0; i0 < kWindow * NB * 4; i0 += 256) {
+    const int i = i0 + threadIdx.x, t = i / (NB * 4), p = i % (NB * 4), b = p >> 2, G = p & 3;
+    if (t >= nt) continue;
     O *o = out + t * out_stride + b * 32 + (KIND == C_Q4_0 ? 4 * G : 8 * G);
     floatx4 u = {0, 0, 0, 0}, v = u;
     if (w.slot[t] >= 0) {
@@ -275,7 +304,7 @@ __device__ __forceinline__ void read_keys(const Cache &c, O *out, int64_t out_st
         u = floatx4{(float)h[0], (float)h[1], (float)h[2], (float)h[3]};
         v = floatx4{(float)h[4], (float)h[5], (float)h[6], (float)h[7]};
       } else {
-        const float d = (float)*(const _Float16 *)(g + scale_offset(KIND, NB, b, w.r[t]));
+        const float d = (float)*(const _Float16 *)(g + scale_offset(KIND, NB, b, w.r[t])), z = kOffset<KIND> * d;
         uint32_t lo, hi;
         if constexpr (KIND == C_Q8_0) {
           const u32x2 q = *(const u32x2 *)at;
@@ -286,8 +315,8 @@ __device__ __forceinline__ void read_keys(const Cache &c, O *out, int64_t out_st
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          u[k] = value<KIND>(lo >> (8 * k) & 255, d);
-          v[k] = value<KIND>(hi >> (8 * k) & 255, d);
+          u[k] = value(lo, k, d, z);
+          v[k] = value(hi, k, d, z);
         }
       }
     }
@@ -296,11 +325,11 @@ __device__ __forceinline__ void read_keys(const Cache &c, O *out, int64_t out_st
   }
 }
 
-template <int KIND, typename O>
+template <int KIND, int NB, typename O>
 __device__ __forceinline__ void read_values(const Cache &c, O *out, int64_t out_stride, int nt, const Window &w, O *rows) {
-  const int NB = c.NB, D = NB * 32, pitch = D + 16 / (int)sizeof(O);
-  for (int i = threadIdx.x; i < NB * kOctets * 16; i += 256) {
-    const int j = i & 15, o = (i >> 4) % kOctets, b = (i >> 4) / kOctets;
+  constexpr int D = NB * 32, pitch = D + 16 / (int)sizeof(O);
+  for (int i = threadIdx.x; i < kOctets * NB * 16; i += 256) {
+    const int j = i & 15, b = (i >> 4) % NB, o = (i >> 4) / NB;
     const int t0 = 8 * o - w.phase;
     if (w.whole[o]) {
       const uint8_t *g = c.v_pages + w.base[t0], *p = g + code_offset<KIND, true>(b, w.r[t0], j);
@@ -310,7 +339,7 @@ __device__ __forceinline__ void read_values(const Cache &c, O *out, int64_t out_
 #pragma unroll
         for (int k = 0; k < 8; ++k) e[k * pitch] = (O)(float)u[k], e[k * pitch + 16] = (O)(float)v[k];
       } else {
-        const half8 d = *(const half8 *)(g + scale_offset(KIND, NB, b, w.r[t0]));
+        const half8 h = *(const half8 *)(g + scale_offset(KIND, NB, b, w.r[t0]));
         u32x4 q;
         if constexpr (KIND == C_Q8_0) {
           q = *(const u32x4 *)p;
@@ -320,8 +349,9 @@ __device__ __forceinline__ void read_values(const Cache &c, O *out, int64_t out_
         }
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          e[k * pitch] = (O)value<KIND>(q[k >> 2] >> (8 * (k & 3)) & 255, (float)d[k]);
-          e[k * pitch + 16] = (O)value<KIND>(q[2 + (k >> 2)] >> (8 * (k & 3)) & 255, (float)d[k]);
+          const float d = (float)h[k], z = kOffset<KIND> * d;
+          e[k * pitch] = (O)value(q[k >> 2], k & 3, d, z);
+          e[k * pitch + 16] = (O)value(q[2 + (k >> 2)], k & 3, d, z);
         }
       }
     } else {
@@ -332,9 +362,9 @@ __device__ __forceinline__ void read_values(const Cache &c, O *out, int64_t out_
           if constexpr (KIND == C_F16) {
             u = (float)*(const _Float16 *)p, v = (float)*(const _Float16 *)(p + 1024);
           } else {
-            const float d = (float)*(const _Float16 *)(g + scale_offset(KIND, NB, b, w.r[t]));
-            if constexpr (KIND == C_Q8_0) u = value<KIND>(p[0], d), v = value<KIND>(p[8], d);
-            else u = value<KIND>(p[0] & 15, d), v = value<KIND>(p[0] >> 4, d);
+            const float d = (float)*(const _Float16 *)(g + scale_offset(KIND, NB, b, w.r[t])), z = kOffset<KIND> * d;
+            if constexpr (KIND == C_Q8_0) u = value(p[0], 0, d, z), v = value(p[8], 0, d, z);
+            else u = value(p[0] & 15, 0, d, z), v = value(p[0] >> 4, 0, d, z);
           }
         }
         rows[t * pitch + b * 32 + j] = (O)u;
@@ -344,26 +374,35 @@ __device__ __forceinline__ void read_values(const Cache &c, O *out, int64_t out_
   }
   __syncthreads();
   constexpr int per = 16 / sizeof(O);
-  for (int i = threadIdx.x; i < nt * (D / per); i += 256) {
-    const int t = i / (D / per), d = (i - t * (D / per)) * per;
-    *(u32x4 *)(out + t * out_stride + d) = *(const u32x4 *)(rows + t * pitch + d);
+#pragma unroll
+  for (int i0 = 0; i0 < kWindow * (D / per); i0 += 256) {
+    const int i = i0 + threadIdx.x, t = i / (D / per), d = (i % (D / per)) * per;
+    if (t < nt) *(u32x4 *)(out + t * out_stride + d) = *(const u32x4 *)(rows + t * pitch + d);
   }
 }
 
-template <int KK, int VK, typename O>
+template <typename O, int NB>
 __global__ __launch_bounds__(256) void kv_read_kernel(ReadArgs a) {
+  constexpr int D = NB * 32;
   __shared__ Window w;
-  extern __shared__ u32x4 tile[];  // values: [kWindow][D + 16 bytes]
-  const int D = a.cache.NB * 32, n = a.cache.n_kv;
-  const int64_t win = (int64_t)blockIdx.x / (2 * n);
+  __shared__ u32x4 tile[kWindow * (D * sizeof(O) + 16) / 16];
+  const int n = a.cache.n_kv;
+  const int64_t win = (int64_t)((uint32_t)blockIdx.x / (uint32_t)(2 * n));
   const int rest = (int)(blockIdx.x - win * 2 * n), is_v = rest >= n, head = is_v ? rest - n : rest;
+  const int kind = is_v ? a.v_kind : a.k_kind;
   const int64_t t0 = win * kWindow;
   const int nt = (int)min((int64_t)kWindow, a.T - t0);
-  find_window(w, a.cache, a.slots, t0, nt, is_v ? VK : KK, head);
+  find_window(w, a.cache, a.slots, t0, nt, kind, head);
   __syncthreads();
   O *out = (O *)(is_v ? a.v_out : a.k_out) + (t0 * n + head) * D;
-  if (is_v) read_values<VK, O>(a.cache, out, (int64_t)n * D, nt, w, (O *)tile);
-  else read_keys<KK, O>(a.cache, out, (int64_t)n * D, nt, w);
+  auto go = [&](auto k) {
+    constexpr int KIND = decltype(k)::value;
+    if (is_v) read_values<KIND, NB, O>(a.cache, out, (int64_t)n * D, nt, w, (O *)tile);
+    else read_keys<KIND, NB, O>(a.cache, out, (int64_t)n * D, nt, w);
+  };
+  if (kind == C_Q8_0) go(std::integral_constant<int, C_Q8_0>{});
+  else if (kind == C_Q4_0) go(std::integral_constant<int, C_Q4_0>{});
+  else go(std::integral_constant<int, C_F16>{});
 }
 
 static Cache make_cache(const KvCache &k) {
@@ -371,10 +410,11 @@ static Cache make_cache(const KvCache &k) {
                (int)(k.head_dim / 32)};
 }
 
-template <int KK, int VK, typename T, typename QO>
-static hipError_t write_types(const KvCache &kc, const KvWrite &w, hipStream_t s) {
+template <typename T, int NB>
+static hipError_t run_write(const KvCache &kc, const KvWrite &w, hipStream_t s) {
   WriteArgs a{};
   a.cache = make_cache(kc);
+  a.k_kind = kc.k_kind, a.v_kind = kc.v_kind;
   a.k = w.k, a.v = w.v;
   a.k_stride = w.k_stride, a.v_stride = w.v_stride;
   a.k_vec = w.k_stride % 4 == 0 && (uintptr_t)w.k % (4 * sizeof(T)) == 0;
@@ -382,59 +422,51 @@ static hipError_t write_types(const KvCache &kc, const KvWrite &w, hipStream_t s
   a.pos = w.pos, a.slots = w.slots, a.T = w.T;
   a.kv_wgs = (w.T + kWindow - 1) / kWindow * 2 * kc.n_kv;
   int64_t threads = 0;
-  bool wide = false;
   if (w.rope) {
     a.rope = Rope{w.freqs, (int)w.n_rot, w.interleaved, w.mscale};
     a.q.x = w.q, a.q.y = w.q_out, a.q.x_stride = w.q_stride, a.q.y_stride = w.q_out_stride;
     a.q.pos = w.pos, a.q.T = w.T, a.q.H = (int)w.n_q, a.q.D = (int)kc.head_dim, a.q.rope = a.rope;
-    wide = plan_rotate(a.q, sizeof(T), sizeof(QO), threads);
+    a.q_out_f16 = w.q_out_f16;
+    a.q_wide = plan_rotate(a.q, sizeof(T), w.q_out_f16 ? 2 : 4, threads);
   }
   const dim3 grid((unsigned)(a.kv_wgs + (threads + 255) / 256));
-  const unsigned lds = kWindow * ((kc.head_dim + 4) * sizeof(float) + a.cache.NB * sizeof(Step));
-  if (!w.rope) hipLaunchKernelGGL((kv_write_kernel<KK, VK, T, QO, 0>), grid, dim3(256), lds, s, a);
-  else if (wide) hipLaunchKernelGGL((kv_write_kernel<KK, VK, T, QO, 4>), grid, dim3(256), lds, s, a);
-  else hipLaunchKernelGGL((kv_write_kernel<KK, VK, T, QO, 1>), grid, dim3(256), lds, s, a);
+  if (w.rope) hipLaunchKernelGGL((kv_write_kernel<T, NB, true>), grid, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((kv_write_kernel<T, NB, false>), grid, dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
-template <int KK, int VK>
-static hipError_t write_kinds(const KvCache &kc, const KvWrite &w, hipStream_t s) {
-  if (!w.rope) return w.f16 ? write_types<KK, VK, _Float16, _Float16>(kc, w, s) : write_types<KK, VK, float, float>(kc, w, s);
-  if (w.f16)
-    return w.q_out_f16 ? write_types<KK, VK, _Float16, _Float16>(kc, w, s) : write_types<KK, VK, _Float16, float>(kc, w, s);
-  return w.q_out_f16 ? write_types<KK, VK, float, _Float16>(kc, w, s) : write_types<KK, VK, float, float>(kc, w, s);
-}
-
-template <int KK, int VK>
-static hipError_t read_kinds(const KvCache &kc, const int32_t *slots, int64_t T, void *k_out, void *v_out, int f16,
-                             hipStream_t s) {
-  ReadArgs a{make_cache(kc), slots, k_out, v_out, T};
+template <int NB>
+static hipError_t run_read(const KvCache &kc, const int32_t *slots, int64_t T, void *k_out, void *v_out, int f16,
+                           hipStream_t s) {
+  const ReadArgs a{make_cache(kc), kc.k_kind, kc.v_kind, slots, k_out, v_out, T};
   const dim3 grid((unsigned)((T + kWindow - 1) / kWindow * 2 * kc.n_kv));
-  const unsigned lds = kWindow * (kc.head_dim * (f16 ? 2 : 4) + 16);
-  if (f16) hipLaunchKernelGGL((kv_read_kernel<KK, VK, _Float16>), grid, dim3(256), lds, s, a);
-  else hipLaunchKernelGGL((kv_read_kernel<KK, VK, float>), grid, dim3(256), lds, s, a);
+  if (f16) hipLaunchKernelGGL((kv_read_kernel<_Float16, NB>), grid, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((kv_read_kernel<float, NB>), grid, dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
 }  // namespace kv
 
-#define QMM_KV_KINDS(F)                                                                            \
-  F(1, 1) F(1, 8) F(1, 2) F(8, 1) F(8, 8) F(8, 2) F(2, 1) F(2, 8) F(2, 2)
-
 hipError_t launch_kv_write(const KvCache &c, const KvWrite &w, hipStream_t s) {
-#define QMM_CASE(K, V) \
-  if (c.k_kind == K && c.v_kind == V) return kv::write_kinds<K, V>(c, w, s);
-  QMM_KV_KINDS(QMM_CASE)
+  switch (c.head_dim / 32) {
+#define QMM_CASE(NB) \
+  case NB:           \
+    return w.f16 ? kv::run_write<_Float16, NB>(c, w, s) : kv::run_write<float, NB>(c, w, s);
+    QMM_CASE(2) QMM_CASE(3) QMM_CASE(4) QMM_CASE(6) QMM_CASE(8)
 #undef QMM_CASE
+  }
   return hipErrorInvalidValue;
 }
 
 hipError_t launch_kv_read(const KvCache &c, const int32_t *slots, int64_t T, void *k_out, void *v_out, int f16,
                           hipStream_t s) {
-#define QMM_CASE(K, V) \
-  if (c.k_kind == K && c.v_kind == V) return kv::read_kinds<K, V>(c, slots, T, k_out, v_out, f16, s);
-  QMM_KV_KINDS(QMM_CASE)
+  switch (c.head_dim / 32) {
+#define QMM_CASE(NB) \
+  case NB:           \
+    return kv::run_read<NB>(c, slots, T, k_out, v_out, f16, s);
+    QMM_CASE(2) QMM_CASE(3) QMM_CASE(4) QMM_CASE(6) QMM_CASE(8)
 #undef QMM_CASE
+  }
   return hipErrorInvalidValue;
 }
 
