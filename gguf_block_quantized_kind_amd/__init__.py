@@ -17,6 +17,7 @@ key/value cache of ``kv_pages`` tensors.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -588,11 +589,20 @@ def _layout_id(layout) -> int:
     return int(layout)
 
 
+# These calls run once per layer and token, where the host's time is what a
+# small step waits for: sizes that are functions of their arguments alone are
+# looked up once, and the checks below read each tensor property once.
+@functools.lru_cache(maxsize=256)
+def _page_bytes(kind: int, page_size: int, n_kv: int, head_dim: int) -> int:
+    return int(load_library().qmm_kv_page_bytes(kind, page_size, n_kv, head_dim))
+
+
 def _rows_arg(x, what: str) -> tuple[int, int, int, int]:
     """T, heads, head_dim and row stride of [T, heads, head_dim] rows."""
-    if x.dim() != 3:
-        raise ValueError(f"{what} must be [rows, heads, head_dim], got {tuple(x.shape)}")
-    T, H, D = x.shape
+    shape = x.shape
+    if len(shape) != 3:
+        raise ValueError(f"{what} must be [rows, heads, head_dim], got {tuple(shape)}")
+    T, H, D = shape
     st, sh, sd = x.stride()
     if (D > 1 and sd != 1) or (H > 1 and sh != D):
         raise ValueError(f"the heads of a row of {what} must be packed, got strides {x.stride()}")
@@ -601,7 +611,7 @@ def _rows_arg(x, what: str) -> tuple[int, int, int, int]:
 
 def _ints(t, count: int, what: str):
     import torch
-    if t.dtype != torch.int32:
+    if t.dtype is not torch.int32:
         raise TypeError(f"{what} must be int32, got {t.dtype}")
     if not t.is_contiguous() or t.numel() != count:
         raise ValueError(f"{what} must hold {count} contiguous elements, got {tuple(t.shape)}")
@@ -609,44 +619,39 @@ def _ints(t, count: int, what: str):
 
 def _pages_arg(pages, kind: int, page_size: int, n_kv: int, head_dim: int, what: str) -> int:
     """Number of pages of a page tensor."""
-    pb = int(load_library().qmm_kv_page_bytes(kind, page_size, n_kv, head_dim))
-    if pages.element_size() != 1 or pages.dim() != 2 or not pages.is_contiguous():
+    shape = pages.shape
+    if len(shape) != 2 or pages.element_size() != 1 or not pages.is_contiguous():
         raise TypeError(f"{what} must be a contiguous byte tensor [n_pages, page_bytes]")
-    if pb > 0 and pages.shape[1] != pb:
-        raise ValueError(f"{what} has pages of {pages.shape[1]} bytes, page_size={page_size}, n_kv={n_kv} and "
+    pb = _page_bytes(kind, page_size, n_kv, head_dim)
+    if pb > 0 and shape[1] != pb:
+        raise ValueError(f"{what} has pages of {shape[1]} bytes, page_size={page_size}, n_kv={n_kv} and "
                          f"head_dim={head_dim} need {pb}")
-    return pages.shape[0]
+    return shape[0]
 
 
-class _on:
-    """Makes the operands' device the current one for the call, refusing
-    operands on different devices or on the host, and gives the stream (by
-    default that device's current one)."""
-
-    def __init__(self, *tensors):
-        self.index = tensors[0].device.index
-        for t in tensors:
-            if t is not None and (t.device.type != "cuda" or t.device.index != self.index):
-                raise ValueError(f"operands must be on one GPU, got {t.device} with {tensors[0].device}")
-
-    def __enter__(self):
-        import torch
-        self.before = torch.cuda.current_device()
-        if self.before != self.index:
-            torch.cuda.set_device(self.index)
-        return self
-
-    def stream(self, stream) -> int:
-        return _stream(stream)
-
-    def __exit__(self, *exc):
-        if self.before != self.index:
-            import torch
-            torch.cuda.set_device(self.before)
+def _call(name: str, stream, tensors, *args):
+    """Calls a C entry point on the operands' device (made the current one for
+    the call), refusing operands on the host or on different devices; its last
+    argument is the stream, by default that device's current one."""
+    import torch
+    index = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and (t.get_device() != index or index < 0):
+            raise ValueError(f"operands must be on one GPU, got {t.device} with {tensors[0].device}")
+    s = torch._C._cuda_getCurrentRawStream(index) if stream is None else int(stream.cuda_stream)
+    fn = getattr(load_library(), name)
+    before = torch._C._cuda_getDevice()
+    if before == index:
+        status = fn(*args, s)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, s)
+    if status:
+        _check(status)
 
 
 def kv_page_bytes(kind, page_size: int, n_kv: int, head_dim: int) -> int:
-    return int(load_library().qmm_kv_page_bytes(cache_kind_id(kind), page_size, n_kv, head_dim))
+    return _page_bytes(cache_kind_id(kind), page_size, n_kv, head_dim)
 
 
 def kv_pages(kind, n_pages: int, page_size: int, n_kv: int, head_dim: int, device="cuda"):
@@ -678,35 +683,39 @@ def rope_freqs(n_rot: int, base: float = 10000.0, factors=None, factor: float = 
 
 def _freqs_arg(freqs) -> int:
     import torch
-    if freqs.dtype != torch.float64 or not freqs.is_contiguous() or freqs.dim() != 1:
+    if freqs.dtype is not torch.float64 or freqs.dim() != 1 or not freqs.is_contiguous():
         raise TypeError(f"freqs must be a contiguous float64 vector, got {freqs.dtype} {tuple(freqs.shape)}")
     return 2 * freqs.shape[0]
+
+
+def _out_arg(out, shape, dtype, like) -> tuple:
+    """`out`, allocated if None, and its row stride."""
+    import torch
+    if out is None:
+        return torch.empty(shape, dtype=dtype or like.dtype, device=like.device), shape[1] * shape[2]
+    T, H, D, stride = _rows_arg(out, "out")
+    if (T, H, D) != shape:
+        raise ValueError(f"out is {tuple(out.shape)}, needs {shape}")
+    return out, stride
 
 
 def rope(x, positions, freqs, layout="half", mscale: float = 1.0, out=None, out_dtype=None, stream=None):
     """x [T, H, head_dim] with the first 2 * len(freqs) elements of each head
     turned by positions [T] int32; out may be x."""
-    import torch
     T, H, D, xs = _rows_arg(x, "x")
     _ints(positions, T, "positions")
-    if out is None:
-        out = torch.empty((T, H, D), dtype=out_dtype or x.dtype, device=x.device)
-    To, Ho, Do, ys = _rows_arg(out, "out")
-    if (To, Ho, Do) != (T, H, D):
-        raise ValueError(f"out is {tuple(out.shape)}, x is {tuple(x.shape)}")
-    with _on(x, positions, freqs, out) as dev:
-        _check(load_library().qmm_rope(freqs.data_ptr(), _freqs_arg(freqs), _layout_id(layout), mscale,
-                                       positions.data_ptr(), x.data_ptr(), _dtype_code(x), xs, out.data_ptr(),
-                                       _dtype_code(out), ys, T, H, D, dev.stream(stream)))
+    out, ys = _out_arg(out, (T, H, D), out_dtype, x)
+    _call("qmm_rope", stream, (x, positions, freqs, out), freqs.data_ptr(), _freqs_arg(freqs), _layout_id(layout), mscale,
+          positions.data_ptr(), x.data_ptr(), _dtype_code(x), xs, out.data_ptr(), _dtype_code(out), ys, T, H, D)
     return out
 
 
 def _kv_args(k, v, slots):
     T, n_kv, D, ks = _rows_arg(k, "k")
     Tv, Hv, Dv, vs = _rows_arg(v, "v")
-    if (Tv, Hv, Dv) != (T, n_kv, D):
+    if Tv != T or Hv != n_kv or Dv != D:
         raise ValueError(f"k is {tuple(k.shape)}, v is {tuple(v.shape)}")
-    if k.dtype != v.dtype:
+    if k.dtype is not v.dtype:
         raise TypeError(f"k is {k.dtype}, v is {v.dtype}")
     _ints(slots, T, "slots")
     return T, n_kv, D, ks, vs
@@ -724,34 +733,26 @@ def kv_write(k, v, slots, k_pages, v_pages, k_kind, v_kind, page_size: int, stre
     """Writes the tokens' keys and values [T, n_kv, head_dim] to slots [T] int32."""
     T, n_kv, D, ks, vs = _kv_args(k, v, slots)
     cache = _cache_args(k_pages, v_pages, k_kind, v_kind, page_size, n_kv, D)
-    with _on(k, v, slots, k_pages, v_pages) as dev:
-        _check(load_library().qmm_kv_write(*cache, k.data_ptr(), ks, v.data_ptr(), vs, _dtype_code(k),
-                                           slots.data_ptr(), T, dev.stream(stream)))
+    _call("qmm_kv_write", stream, (k, v, slots, k_pages, v_pages), *cache, k.data_ptr(), ks, v.data_ptr(), vs,
+          _dtype_code(k), slots.data_ptr(), T)
 
 
 def kv_append(q, k, v, positions, slots, k_pages, v_pages, k_kind, v_kind, page_size: int, freqs, layout="half",
               mscale: float = 1.0, out=None, out_dtype=None, stream=None):
     """Rotates q [T, n_q, head_dim] (returned; out may be q) and k, and writes
     k and v to their slots, in one launch."""
-    import torch
     T, n_kv, D, ks, vs = _kv_args(k, v, slots)
     Tq, n_q, Dq, qs = _rows_arg(q, "q")
-    if (Tq, Dq) != (T, D):
+    if Tq != T or Dq != D:
         raise ValueError(f"q is {tuple(q.shape)}, k is {tuple(k.shape)}")
-    if q.dtype != k.dtype:
+    if q.dtype is not k.dtype:
         raise TypeError(f"q is {q.dtype}, k is {k.dtype}")
     _ints(positions, T, "positions")
     cache = _cache_args(k_pages, v_pages, k_kind, v_kind, page_size, n_kv, D)
-    if out is None:
-        out = torch.empty((T, n_q, D), dtype=out_dtype or q.dtype, device=q.device)
-    To, Ho, Do, os_ = _rows_arg(out, "out")
-    if (To, Ho, Do) != (T, n_q, D):
-        raise ValueError(f"out is {tuple(out.shape)}, q is {tuple(q.shape)}")
-    with _on(q, k, v, positions, slots, k_pages, v_pages, freqs, out) as dev:
-        _check(load_library().qmm_kv_append(freqs.data_ptr(), _freqs_arg(freqs), _layout_id(layout), mscale,
-                                            positions.data_ptr(), q.data_ptr(), qs, n_q, out.data_ptr(),
-                                            _dtype_code(out), os_, *cache, k.data_ptr(), ks, v.data_ptr(), vs,
-                                            _dtype_code(k), slots.data_ptr(), T, dev.stream(stream)))
+    out, os_ = _out_arg(out, (T, n_q, D), out_dtype, q)
+    _call("qmm_kv_append", stream, (q, k, v, positions, slots, k_pages, v_pages, freqs, out), freqs.data_ptr(),
+          _freqs_arg(freqs), _layout_id(layout), mscale, positions.data_ptr(), q.data_ptr(), qs, n_q, out.data_ptr(),
+          _dtype_code(out), os_, *cache, k.data_ptr(), ks, v.data_ptr(), vs, _dtype_code(k), slots.data_ptr(), T)
     return out
 
 
@@ -766,17 +767,20 @@ def kv_read(slots, k_pages, v_pages, k_kind, v_kind, page_size: int, n_kv: int, 
     if (k_out is None) != (v_out is None):
         raise ValueError("k_out and v_out go together")
     if k_out is None:
-        k_out, v_out = torch.empty((2, *shape), dtype=dtype or torch.float16, device=slots.device).unbind(0)
-    for t in (k_out, v_out):
-        if tuple(t.shape) != shape or not t.is_contiguous() or t.dtype != k_out.dtype:
-            raise ValueError(f"k_out and v_out must be contiguous {shape} of one type")
+        dtype = dtype or torch.float16
+        k_out = torch.empty(shape, dtype=dtype, device=slots.device)
+        v_out = torch.empty(shape, dtype=dtype, device=slots.device)
+    else:
+        for t in (k_out, v_out):
+            if tuple(t.shape) != shape or not t.is_contiguous() or t.dtype is not k_out.dtype:
+                raise ValueError(f"k_out and v_out must be contiguous {shape} of one type")
     cache = _cache_args(k_pages, v_pages, k_kind, v_kind, page_size, n_kv, head_dim)
-    with _on(slots, k_pages, v_pages, k_out, v_out) as dev:
-        _check(load_library().qmm_kv_read(*cache, slots.data_ptr(), T, k_out.data_ptr(), v_out.data_ptr(),
-                                          _dtype_code(k_out), dev.stream(stream)))
+    _call("qmm_kv_read", stream, (slots, k_pages, v_pages, k_out, v_out), *cache, slots.data_ptr(), T, k_out.data_ptr(),
+          v_out.data_ptr(), _dtype_code(k_out))
     return k_out, v_out
 
 
+@functools.lru_cache(maxsize=1024)
 def qmm_attn_decode_workspace_bytes(B: int, n_q: int, n_kv: int, head_dim: int) -> int:
     return int(load_library().qmm_attn_decode_workspace_bytes(B, n_q, n_kv, head_dim))
 
@@ -791,25 +795,27 @@ def attn_decode(q, k_pages, v_pages, block_table, seq_lens, k_kind, v_kind, page
     import torch
     B, n_q, D, qs = _rows_arg(q, "q")
     _ints(seq_lens, B, "seq_lens")
-    if block_table.dim() != 2 or block_table.shape[0] != B:
-        raise ValueError(f"block_table must be [{B}, max_pages], got {tuple(block_table.shape)}")
-    max_pages = block_table.shape[1]
+    shape = block_table.shape
+    if len(shape) != 2 or shape[0] != B:
+        raise ValueError(f"block_table must be [{B}, max_pages], got {tuple(shape)}")
+    max_pages = shape[1]
     _ints(block_table, B * max_pages, "block_table")
-    if sinks is not None and (sinks.dtype != torch.float32 or not sinks.is_contiguous() or sinks.numel() != n_q):
+    if sinks is not None and (sinks.dtype is not torch.float32 or not sinks.is_contiguous() or sinks.numel() != n_q):
         raise ValueError(f"sinks must be {n_q} contiguous float32 values")
     cache = _cache_args(k_pages, v_pages, k_kind, v_kind, page_size, n_kv, D)
     if out is None:
         out = torch.empty((B, n_q, D), dtype=q.dtype, device=q.device)
-    elif tuple(out.shape) != (B, n_q, D) or not out.is_contiguous() or out.dtype != q.dtype:
+    elif tuple(out.shape) != (B, n_q, D) or not out.is_contiguous() or out.dtype is not q.dtype:
         raise ValueError(f"out must be contiguous {(B, n_q, D)} of q's type")
     if workspace is None:
         nbytes = qmm_attn_decode_workspace_bytes(B, n_q, n_kv, D)
         workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=q.device)
-    with _on(q, k_pages, v_pages, block_table, seq_lens, sinks, out, workspace) as dev:
-        _check(load_library().qmm_attn_decode(*cache, q.data_ptr(), _dtype_code(q), qs, n_q, block_table.data_ptr(),
-                                              max_pages, seq_lens.data_ptr(), B,
-                                              D ** -0.5 if scale is None else scale, window,
-                                              0 if sinks is None else sinks.data_ptr(), out.data_ptr(),
-                                              workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                              dev.stream(stream)))
+    else:
+        nbytes = workspace.numel() * workspace.element_size()
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+    _call("qmm_attn_decode", stream, (q, k_pages, v_pages, block_table, seq_lens, sinks, out, workspace), *cache,
+          q.data_ptr(), _dtype_code(q), qs, n_q, block_table.data_ptr(), max_pages, seq_lens.data_ptr(), B,
+          D ** -0.5 if scale is None else scale, window, 0 if sinks is None else sinks.data_ptr(), out.data_ptr(),
+          workspace.data_ptr(), nbytes)
     return out
