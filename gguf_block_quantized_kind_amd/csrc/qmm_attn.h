@@ -277,13 +277,26 @@ __device__ __forceinline__ void load_q(const QT *q, int G, float (&v)[8]) {
   }
 }
 
+// Parts of a workgroup's join that lie in LDS at once.
+__host__ __device__ inline int lds_parts(int heads) { return heads <= 8 ? kWaves : 2; }
+
+// Four elements of the result: the sums o over the weights' sum l (both on
+// reference R) with the sink's share; zeros where nothing was attended.
+template <typename QT>
+__device__ __forceinline__ void store_out(QT *out, floatx4 o, float l, float R, const float *sinks, int head) {
+  if (sinks) l += __builtin_amdgcn_exp2f(fminf(sinks[head] * 1.44269504f - R, 120.0f));
+  const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+  typedef QT q4 __attribute__((ext_vector_type(4)));
+  *(q4 *)out = q4{(QT)(o[0] * inv), (QT)(o[1] * inv), (QT)(o[2] * inv), (QT)(o[3] * inv)};
+}
+
 template <int KK, int VK, int NB, typename QT>
 __global__ __launch_bounds__(64 * kWaves) void attn_kernel(Args a) {
   constexpr int D = NB * 32;
   constexpr bool SPLIT = sizeof(QT) == 4;  // two f16 terms
   constexpr bool SUB = kSubnormalKeys<KK, SPLIT>;
   constexpr int kPitch = D + 4;
-  extern __shared__ float lds[];  // [2][heads][kPitch], then [wave][heads][2]
+  extern __shared__ float lds[];  // [part][heads][kPitch], then [part][heads][2]
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int j = lane & 15, G = lane >> 4;
 
@@ -542,57 +555,60 @@ __global__ __launch_bounds__(64 * kWaves) void attn_kernel(Args a) {
   }
   sum = sum_over_groups(sum);
 
-  // The four waves' parts, joined through LDS: references and sums first, then
-  // the accumulators on the common reference, waves 2 and 3 handing theirs to
-  // waves 0 and 1.
-  float *ml = lds + 2 * a.heads * kPitch;
-  if (G == 0 && j < heads) {
-    ml[(wave * a.heads + j) * 2] = R;
-    ml[(wave * a.heads + j) * 2 + 1] = sum;
-  }
-  __syncthreads();
-  if (j < heads) {
-    float Rm = kFloor;
+  // The four waves' parts, joined through LDS with their references.  Where the
+  // heads are too many for four parts in LDS, waves 2 and 3 first hand theirs
+  // to waves 0 and 1.
+  const int parts = lds_parts(a.heads);
+  float *ml = lds + parts * a.heads * kPitch;  // [part][heads][2]
+  auto put_part = [&](int w) {
+    if (j >= heads) return;
+    float *o = lds + (w * a.heads + j) * kPitch + 4 * G;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) Rm = fmaxf(Rm, ml[(w * a.heads + j) * 2]);
-    const float f = __builtin_amdgcn_exp2f(R - Rm);
-    float *o = lds + ((wave & 1) * a.heads + j) * kPitch + 4 * G;
-    if (wave >= 2) {
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) *(floatx4 *)(o + n * 32 + x * 16) = acc[n][x];
+    if (G == 0) {
+      ml[(w * a.heads + j) * 2] = R;
+      ml[(w * a.heads + j) * 2 + 1] = sum;
+    }
+  };
+  if (parts == 2) {
+    if (wave >= 2) put_part(wave - 2);
+    __syncthreads();
+    if (wave < 2 && j < heads) {
+      const float Ro = ml[(wave * a.heads + j) * 2], Rn = fmaxf(R, Ro);
+      const float f = __builtin_amdgcn_exp2f(R - Rn), fo = __builtin_amdgcn_exp2f(Ro - Rn);
+      const float *o = lds + (wave * a.heads + j) * kPitch + 4 * G;
 #pragma unroll
       for (int n = 0; n < NB; ++n)
 #pragma unroll
-        for (int x = 0; x < 2; ++x) *(floatx4 *)(o + n * 32 + x * 16) = acc[n][x] * f;
+        for (int x = 0; x < 2; ++x) acc[n][x] = acc[n][x] * f + *(const floatx4 *)(o + n * 32 + x * 16) * fo;
+      sum = sum * f + ml[(wave * a.heads + j) * 2 + 1] * fo;
+      R = Rn;
     }
-#pragma unroll
-    for (int n = 0; n < NB; ++n)
-#pragma unroll
-      for (int x = 0; x < 2; ++x) acc[n][x] *= f;
+    __syncthreads();
+    if (wave < 2) put_part(wave);
+  } else {
+    put_part(wave);
   }
   __syncthreads();
-  if (wave < 2 && j < heads) {
-    float *o = lds + (wave * a.heads + j) * kPitch + 4 * G;
-#pragma unroll
-    for (int n = 0; n < NB; ++n)
-#pragma unroll
-      for (int x = 0; x < 2; ++x) *(floatx4 *)(o + n * 32 + x * 16) += acc[n][x];
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < heads * D; i += 64 * kWaves) {
-    const int h = i / D, d = i - h * D;
+  for (int i = threadIdx.x; i < heads * (D / 4); i += 64 * kWaves) {
+    const int h = i / (D / 4), d = i % (D / 4) * 4;
     float Rm = kFloor, l = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) Rm = fmaxf(Rm, ml[(w * a.heads + h) * 2]);
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w)
-      l = __builtin_fmaf(__builtin_amdgcn_exp2f(ml[(w * a.heads + h) * 2] - Rm), ml[(w * a.heads + h) * 2 + 1], l);
-    const float o = lds[h * kPitch + d] + lds[(a.heads + h) * kPitch + d];
+    for (int w = 0; w < parts; ++w) Rm = fmaxf(Rm, ml[(w * a.heads + h) * 2]);
+    floatx4 o = {0, 0, 0, 0};
+    for (int w = 0; w < parts; ++w) {
+      const float f = __builtin_amdgcn_exp2f(ml[(w * a.heads + h) * 2] - Rm);
+      l = __builtin_fmaf(f, ml[(w * a.heads + h) * 2 + 1], l);
+      o += *(const floatx4 *)(lds + (w * a.heads + h) * kPitch + d) * f;
+    }
     if (splits == 1) {
-      if (a.sinks) l += __builtin_amdgcn_exp2f(fminf(a.sinks[head0 + h] * 1.44269504f - Rm, 120.0f));
-      ((QT *)a.out)[((int64_t)b * a.n_q + head0 + h) * D + d] = (QT)(l > 0.0f || l != l ? o / l : 0.0f);
+      store_out((QT *)a.out + ((int64_t)b * a.n_q + head0 + h) * D + d, o, l, Rm, a.sinks, head0 + h);
     } else {
-      a.part[((int64_t)blockIdx.x * a.heads + h) * D + d] = o;
+      const int64_t part = (int64_t)blockIdx.x * a.heads + h;
+      *(floatx4 *)(a.part + part * D + d) = o;
       if (d == 0) {
-        float *m = a.part + a.items * a.heads * D + ((int64_t)blockIdx.x * a.heads + h) * 2;
+        float *m = a.part + a.items * a.heads * D + part * 2;
         m[0] = Rm;
         m[1] = l;
       }
@@ -602,7 +618,7 @@ __global__ __launch_bounds__(64 * kWaves) void attn_kernel(Args a) {
 
 template <int KK, int VK, int NB, typename QT>
 static hipError_t run(const Args &a, hipStream_t s) {
-  const unsigned lds = (2 * (NB * 32 + 4) + 2 * kWaves) * a.heads * sizeof(float);  // at most 34 KiB
+  const unsigned lds = lds_parts(a.heads) * (NB * 32 + 4 + 2) * a.heads * sizeof(float);  // at most 34 KiB
   hipLaunchKernelGGL((attn_kernel<KK, VK, NB, QT>), dim3((unsigned)a.items), dim3(64 * kWaves), lds, s, a);
   return hipGetLastError();
 }

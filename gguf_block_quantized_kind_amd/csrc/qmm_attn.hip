@@ -5,19 +5,21 @@
 namespace qmm {
 namespace attn {
 
-// One workgroup per (sequence, query head): the splits' parts, weighted by
+// One workgroup per H query heads of a sequence: the splits' parts, weighted by
 // 2^(R_i - max R), over the weighted sums (plus the sink's share).  Sequences
-// of one split were finished by the attention kernel.  Weights and sums come
-// from all threads at once, the parts from 1024 / D groups of D / 4 lanes, so
-// that a sequence of a thousand splits costs no chain of a thousand loads.
-template <typename QT>
+// of one split were finished by the attention kernel.  256 / H threads of a
+// head compute its weights and sums together and read its parts in ways of
+// D / 4 lanes, so that a sequence of a thousand splits costs no chain of a
+// thousand loads.  H = 1 spreads few heads with many splits over the GPU, H = 4
+// makes fewer workgroups of many heads with few splits.
+template <typename QT, int H>
 __global__ __launch_bounds__(256) void join_kernel(Args a, int D) {
-  constexpr int kChunk = 1024;
-  __shared__ float weight[kChunk];
-  __shared__ float red[8];
+  constexpr int kThreads = 256 / H, kChunk = 1024 / H;
+  __shared__ float weight[H][kChunk];
+  __shared__ float red[H][8];
   __shared__ floatx4 part[256];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int b = blockIdx.x / a.n_q, hq = blockIdx.x - b * a.n_q;
+  const int sub = threadIdx.x / kThreads, tid = threadIdx.x % kThreads, lane = tid & 63, wave = tid >> 6;
+  const int per_b = (a.n_q + H - 1) / H, b = blockIdx.x / per_b, hq = min((blockIdx.x - b * per_b) * H + sub, a.n_q - 1);
   const int first = a.plan[2 * b], splits = a.plan[2 * b + 1];
   if (splits <= 1) return;
   const int kvh = hq / a.G, in = hq - kvh * a.G, tile = in / 16, h = in - tile * 16;
@@ -25,23 +27,25 @@ __global__ __launch_bounds__(256) void join_kernel(Args a, int D) {
   const float *ml = a.part + a.items * a.heads * D;
 
   float Rm = kFloor;
-  for (int i = tid; i < splits; i += 256) Rm = fmaxf(Rm, ml[((item0 + i * nh) * a.heads + h) * 2]);
+  for (int i = tid; i < splits; i += kThreads) Rm = fmaxf(Rm, ml[((item0 + i * nh) * a.heads + h) * 2]);
 #pragma unroll
   for (int k = 1; k < 64; k <<= 1) Rm = fmaxf(Rm, __shfl_xor(Rm, k, 64));
-  if (lane == 0) red[wave] = Rm;
-  __syncthreads();
-  Rm = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  if constexpr (kThreads > 64) {
+    if (lane == 0) red[sub][wave] = Rm;
+    __syncthreads();
+    Rm = fmaxf(fmaxf(red[sub][0], red[sub][1]), fmaxf(red[sub][2], red[sub][3]));
+  }
 
-  const int lanes = D / 4, ways = 256 / lanes, way = tid / lanes, d4 = tid - way * lanes;
+  const int lanes = D / 4, ways = kThreads / lanes, way = tid / lanes, d4 = tid - way * lanes;
   floatx4 o = {0, 0, 0, 0};
   float l = 0.0f;
   for (int i0 = 0; i0 < splits; i0 += kChunk) {
     const int n = min(kChunk, splits - i0);
     if (i0) __syncthreads();
-    for (int i = tid; i < n; i += 256) {
+    for (int i = tid; i < n; i += kThreads) {
       const float *m = ml + ((item0 + (i0 + i) * nh) * a.heads + h) * 2;
       const float w = __builtin_amdgcn_exp2f(m[0] - Rm);
-      weight[i] = w;
+      weight[sub][i] = w;
       l = __builtin_fmaf(w, m[1], l);
     }
     __syncthreads();
@@ -49,20 +53,26 @@ __global__ __launch_bounds__(256) void join_kernel(Args a, int D) {
       const float *p = a.part + ((item0 + i0 * nh) * a.heads + h) * D + 4 * d4;
       const int64_t step = nh * a.heads * D;
 #pragma unroll 4
-      for (int i = way; i < n; i += ways) o += weight[i] * *(const floatx4 *)(p + i * step);
+      for (int i = way; i < n; i += ways) o += weight[sub][i] * *(const floatx4 *)(p + i * step);
     }
   }
 #pragma unroll
   for (int k = 1; k < 64; k <<= 1) l += __shfl_xor(l, k, 64);
-  if (lane == 0) red[4 + wave] = l;
-  part[tid] = o;
+  if constexpr (kThreads > 64) {
+    if (lane == 0) red[sub][4 + wave] = l;
+  }
+  part[threadIdx.x] = o;
   __syncthreads();
-  if (tid >= D) return;
-  l = (red[4] + red[5]) + (red[6] + red[7]);
-  float v = 0.0f;
-  for (int k = 0; k < ways; ++k) v += ((const float *)part)[k * D + tid];
-  if (a.sinks) l += __builtin_amdgcn_exp2f(fminf(a.sinks[hq] * 1.44269504f - Rm, 120.0f));
-  ((QT *)a.out)[((int64_t)b * a.n_q + hq) * D + tid] = (QT)(l > 0.0f || l != l ? v / l : 0.0f);
+  if (tid >= lanes) return;
+  if constexpr (kThreads > 64) l = (red[sub][4] + red[sub][5]) + (red[sub][6] + red[sub][7]);
+  for (int k = 1; k < ways; ++k) o += part[sub * kThreads + k * lanes + tid];
+  store_out((QT *)a.out + ((int64_t)b * a.n_q + hq) * D + 4 * tid, o, l, Rm, a.sinks, hq);
+}
+
+template <typename QT>
+static void launch_join(const Args &a, int D, hipStream_t s) {
+  if (a.B * a.n_q < 1024) hipLaunchKernelGGL((join_kernel<QT, 1>), dim3((unsigned)(a.B * a.n_q)), dim3(256), 0, s, a, D);
+  else hipLaunchKernelGGL((join_kernel<QT, 4>), dim3((unsigned)(a.B * ((a.n_q + 3) / 4))), dim3(256), 0, s, a, D);
 }
 
 static int64_t items_of(int64_t B, int64_t n_q, int64_t n_kv) {
@@ -109,9 +119,8 @@ hipError_t launch_attn_decode(const KvCache &kc, const AttnDecode &d, hipStream_
   QMM_CASE(C_Q4_0, C_Q4_0, launch_q4_q4)
 #undef QMM_CASE
   if (e != hipSuccess) return e;
-  const dim3 grid((unsigned)(a.B * a.n_q));
-  if (d.f16) hipLaunchKernelGGL(join_kernel<_Float16>, grid, dim3(256), 0, s, a, (int)kc.head_dim);
-  else hipLaunchKernelGGL(join_kernel<float>, grid, dim3(256), 0, s, a, (int)kc.head_dim);
+  if (d.f16) launch_join<_Float16>(a, (int)kc.head_dim, s);
+  else launch_join<float>(a, (int)kc.head_dim, s);
   return hipGetLastError();
 }
 

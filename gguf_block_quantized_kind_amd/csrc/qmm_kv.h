@@ -79,15 +79,19 @@ __device__ __forceinline__ _Float16 f16_up(float d) {
   return h;
 }
 
-// The scale of a block from its largest and smallest element; `bits` is the
-// largest bit pattern of |x|, which tells an infinity or NaN: such a block
-// gets a NaN scale and reads back as NaN throughout.
+// The scale of a block from the bits of its largest |x| and (Q4_0) its largest
+// x.  An infinity or NaN shows in the bits: such a block gets a NaN scale and
+// reads back as NaN throughout.
 template <int KIND>
-__device__ __forceinline__ _Float16 block_scale(float hi, float lo, uint32_t bits) {
+__device__ __forceinline__ _Float16 block_scale(float hi, uint32_t bits) {
   if (bits >= 0x7f800000u) return __builtin_bit_cast(_Float16, (uint16_t)0x7e00);
-  _Float16 h = f16_up(fabsf(fmaxf(hi, -lo)) / (KIND == C_Q8_0 ? 127.0f : 8.0f));
-  if (KIND == C_Q4_0 && hi >= -lo && h != (_Float16)0.0f) h = -h;  // the extreme element becomes code 0: -8 d
-  return h;
+  const float big = __builtin_bit_cast(float, bits);
+  if constexpr (KIND == C_Q8_0) {  // big / 127, correctly rounded as in encode
+    const float inv = 1.0f / 127.0f, q = big * inv;
+    return f16_up(__builtin_fmaf(__builtin_fmaf(-127.0f, q, big), inv, q));
+  }
+  const _Float16 h = f16_up(big * 0.125f);
+  return hi == big && big != 0.0f ? -h : h;  // the extreme element becomes code 0: -8 d
 }
 
 // The bits of |x|: above 0x7f7fffff for an infinity or NaN.  (A function: a bit
@@ -153,14 +157,9 @@ struct Rope {
 struct Cache {
   uint8_t *k_pages, *v_pages;
   int64_t n_slots;  // n_pages * page_size
-  int page_size, n_kv, NB;
+  int page_size, page_shift;  // shift: log2 of a power of two, else -1
+  int n_kv, NB;
 };
-
-// First byte of the group of (slot, head).
-__device__ __forceinline__ int64_t group_at(const Cache &c, int kind, int slot, int head) {
-  const int page = slot / c.page_size, g = (slot - page * c.page_size) / kGroup, groups = c.page_size / kGroup;
-  return (((int64_t)page * c.n_kv + head) * groups + g) * group_bytes(kind, c.NB);
-}
 
 // Rotation of whole rows, V pairs of every head of a range per thread: the
 // angle costs about sixty operations (half of them 64-bit), so each is used
