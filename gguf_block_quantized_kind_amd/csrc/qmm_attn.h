@@ -35,6 +35,9 @@
 // to 2^-28 of them, whatever the size of the values.
 #pragma once
 
+#include <algorithm>
+#include <atomic>
+
 #include "qmm_internal.h"
 #include "qmm_kv.h"
 
@@ -55,7 +58,8 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 constexpr float kFloor = -1e30f;  // R of no tokens
 constexpr int kWaves = 4;
 constexpr int kMinGroups = 4;  // groups per split at least: one per wave
-constexpr int kTarget = 1024;  // workgroups the splits aim at
+constexpr int kMaxSlots = 1280;  // most workgroups counted on at once (five on each of 256 compute units)
+constexpr float kOverhead = 8.0f;  // a workgroup's start and end, in groups' time
 
 struct Args {
   const uint8_t *kp, *vp;
@@ -72,9 +76,10 @@ struct Args {
   int64_t window;
   const float *sinks;
   void *out;
-  float *part;     // [item][heads][D], then [item][heads][2]: reference and sum
-  int32_t *plan;   // [B][2]: a sequence's first split and number of splits, for the join
-  int64_t items;
+  float *part;    // [item][heads][D], then [item][heads][2]: reference and sum
+  int32_t *plan;  // [B][2]: a sequence's first split and number of splits, for the join
+  int64_t items;  // workgroups launched
+  int slots;      // workgroups the GPU holds at once
 };
 
 // The groups [g0, g0 + n) of sequence b that hold attended tokens [lo, len).
@@ -119,34 +124,51 @@ __device__ __forceinline__ uint32_t scan(uint32_t v) {
 }
 
 // Splits are numbered through the batch (at least one per sequence, so that
-// every output row is written).  The groups per split are the attended groups
-// of the whole batch over the target number of workgroups, at least one group
-// per wave.  find_split: the sequence (-1: past the last) that split `unit`
-// belongs to, its first split and the groups per split.
+// every output row is written).  find_split: the sequence (-1: past the last)
+// that split `unit` belongs to, its first split and the groups per split.
+//
+// Groups per split, c.  Either all splits run at once: the smallest c whose
+// splits fit the slots, costing c + overhead; or there are two rounds of them
+// (of which the second overlaps the first's ends, by half a split on
+// average), c = total / (2 slots), costing total / slots + 2 overheads + c / 2.
+// Equal lengths take the first, very unequal ones the second.
 struct Found {
   int b, c;
   uint32_t first;
 };
+__device__ __forceinline__ int per_split(int64_t groups, int64_t splits) {
+  return (int)min(max((groups + splits - 1) / splits, (int64_t)kMinGroups), (int64_t)1 << 26);
+}
 __device__ __forceinline__ Found find_split(const Args &a, int lane, uint32_t unit) {
-  const uint32_t nh = (uint32_t)(a.n_kv * a.tiles);
+  const int nh = a.n_kv * a.tiles;
   int n = span_of(a, lane).n;
-  uint64_t total;
-  if (a.B == 1) {
-    total = (uint32_t)__builtin_amdgcn_readfirstlane(n);
-  } else {
-    total = 0;
-    for (int b0 = 0;;) {  // (at most 2^26 groups a sequence: one less keeps 64 of them below 2^32)
-      total += (uint32_t)__builtin_amdgcn_readlane((int)scan((uint32_t)min(n, (1 << 26) - 1)), 63);
-      b0 += 64;
-      if (b0 >= a.B) break;
-      n = span_of(a, b0 + lane).n;
-    }
-    if (a.B > 64) n = span_of(a, lane).n;
-  }
-  const int c = max((int)((total * nh + (kTarget - 1)) / kTarget), kMinGroups);
   if (a.B == 1) {
     n = __builtin_amdgcn_readfirstlane(n);
+    const int c = per_split(n, max(a.slots / nh, 1));
     return Found{unit < (uint32_t)max(1, (n + c - 1) / c) ? 0 : -1, c, 0};
+  }
+  uint64_t total = 0;
+  for (int b0 = 0;;) {  // (at most 2^26 groups a sequence: one less keeps 64 of them below 2^32)
+    total += (uint32_t)__builtin_amdgcn_readlane((int)scan((uint32_t)min(n, (1 << 26) - 1)), 63);
+    b0 += 64;
+    if (b0 >= a.B) break;
+    n = span_of(a, b0 + lane).n;
+  }
+  if (a.B > 64) n = span_of(a, lane).n;
+  total *= nh;
+  auto count = [&](int c) { return lane < a.B ? (uint32_t)max(1, (n + c - 1) / c) : 0; };
+  int c = per_split(total, 2 * a.slots);
+  if (a.B <= 64 && a.B * nh <= a.slots) {
+    int once = per_split(total, a.slots);
+#pragma unroll 1
+    for (int i = 0; i < 3; ++i) {
+      const int items = __builtin_amdgcn_readlane((int)scan(count(once)), 63) * nh;
+      if (items <= a.slots) break;
+      once = (int)((int64_t)once * items / a.slots) + 1;
+    }
+    // (If they still do not all fit, the cost is near enough.)
+    const float even = (float)total / (float)a.slots;
+    if ((float)once <= even + kOverhead + 0.5f * (float)c) c = once;
   }
   uint32_t before = 0;
   for (int b0 = 0; b0 < a.B; b0 += 64) {
@@ -616,15 +638,30 @@ __global__ __launch_bounds__(64 * kWaves) void attn_kernel(Args a) {
   }
 }
 
+// How many workgroups the GPU holds is looked up once per instantiation (with
+// the most LDS a call uses).
 template <int KK, int VK, int NB, typename QT>
-static hipError_t run(const Args &a, hipStream_t s) {
-  const unsigned lds = lds_parts(a.heads) * (NB * 32 + 4 + 2) * a.heads * sizeof(float);  // at most 34 KiB
-  hipLaunchKernelGGL((attn_kernel<KK, VK, NB, QT>), dim3((unsigned)a.items), dim3(64 * kWaves), lds, s, a);
+static hipError_t run(Args &a, hipStream_t s) {
+  static std::atomic<int> per_cu{0};
+  auto lds = [](int heads) { return (unsigned)(lds_parts(heads) * (NB * 32 + 4 + 2) * heads * sizeof(float)); };  // <= 34 KiB
+  int n = per_cu.load(std::memory_order_relaxed);
+  if (n == 0) {
+    hipError_t e = hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, attn_kernel<KK, VK, NB, QT>, 64 * kWaves,
+                                                                std::max(lds(8), lds(16)));
+    if (e != hipSuccess) return e;
+    n = std::max(n, 1);
+    per_cu.store(n, std::memory_order_relaxed);
+  }
+  a.slots = std::min(n * device_cus(), kMaxSlots);
+  // Splits of the longest sequences the page table can hold, and of any batch.
+  const int64_t nh = a.n_kv * a.tiles, most = a.max_pages * a.page_groups;
+  a.items = std::min(2 * a.slots + a.B * nh, a.B * nh * ((most + kMinGroups - 1) / kMinGroups));
+  hipLaunchKernelGGL((attn_kernel<KK, VK, NB, QT>), dim3((unsigned)a.items), dim3(64 * kWaves), lds(a.heads), s, a);
   return hipGetLastError();
 }
 
 template <int KK, int VK, typename QT>
-static hipError_t run_nb(const Args &a, int NB, hipStream_t s) {
+static hipError_t run_nb(Args &a, int NB, hipStream_t s) {
   switch (NB) {
     case 2: return run<KK, VK, 2, QT>(a, s);
     case 3: return run<KK, VK, 3, QT>(a, s);
@@ -636,19 +673,19 @@ static hipError_t run_nb(const Args &a, int NB, hipStream_t s) {
 }
 
 template <int KK, int VK>
-static hipError_t run_kinds(const Args &a, int NB, int f16, hipStream_t s) {
+static hipError_t run_kinds(Args &a, int NB, int f16, hipStream_t s) {
   return f16 ? run_nb<KK, VK, _Float16>(a, NB, s) : run_nb<KK, VK, float>(a, NB, s);
 }
 
-hipError_t launch_f16_f16(const Args &, int NB, int f16, hipStream_t);
-hipError_t launch_f16_q8(const Args &, int NB, int f16, hipStream_t);
-hipError_t launch_f16_q4(const Args &, int NB, int f16, hipStream_t);
-hipError_t launch_q8_f16(const Args &, int NB, int f16, hipStream_t);
-hipError_t launch_q8_q8(const Args &, int NB, int f16, hipStream_t);
-hipError_t launch_q8_q4(const Args &, int NB, int f16, hipStream_t);
-hipError_t launch_q4_f16(const Args &, int NB, int f16, hipStream_t);
-hipError_t launch_q4_q8(const Args &, int NB, int f16, hipStream_t);
-hipError_t launch_q4_q4(const Args &, int NB, int f16, hipStream_t);
+hipError_t launch_f16_f16(Args &, int NB, int f16, hipStream_t);
+hipError_t launch_f16_q8(Args &, int NB, int f16, hipStream_t);
+hipError_t launch_f16_q4(Args &, int NB, int f16, hipStream_t);
+hipError_t launch_q8_f16(Args &, int NB, int f16, hipStream_t);
+hipError_t launch_q8_q8(Args &, int NB, int f16, hipStream_t);
+hipError_t launch_q8_q4(Args &, int NB, int f16, hipStream_t);
+hipError_t launch_q4_f16(Args &, int NB, int f16, hipStream_t);
+hipError_t launch_q4_q8(Args &, int NB, int f16, hipStream_t);
+hipError_t launch_q4_q4(Args &, int NB, int f16, hipStream_t);
 
 }  // namespace attn
 }  // namespace qmm

@@ -75,16 +75,13 @@ static void launch_join(const Args &a, int D, hipStream_t s) {
   else hipLaunchKernelGGL((join_kernel<QT, 4>), dim3((unsigned)(a.B * ((a.n_q + 3) / 4))), dim3(256), 0, s, a, D);
 }
 
-static int64_t items_of(int64_t B, int64_t n_q, int64_t n_kv) {
-  const int64_t tiles = (n_q / n_kv + 15) / 16;
-  return kTarget + B * n_kv * tiles;
-}
+static size_t plan_bytes(int64_t B) { return (size_t)((B * 8 + 15) / 16 * 16); }
 
 }  // namespace attn
 
 size_t attn_workspace_bytes(int64_t B, int64_t n_q, int64_t n_kv, int64_t head_dim) {
-  const int64_t G = n_q / n_kv, heads = G < 16 ? G : 16;
-  return (size_t)(attn::items_of(B, n_q, n_kv) * heads * (head_dim + 2) * 4 + B * 8);
+  const int64_t G = n_q / n_kv, heads = G < 16 ? G : 16, items = 2 * attn::kMaxSlots + B * n_kv * ((G + 15) / 16);
+  return attn::plan_bytes(B) + (size_t)(items * heads * (head_dim + 2) * 4);
 }
 
 hipError_t launch_attn_decode(const KvCache &kc, const AttnDecode &d, hipStream_t s) {
@@ -101,9 +98,8 @@ hipError_t launch_attn_decode(const KvCache &kc, const AttnDecode &d, hipStream_
   a.table = d.table, a.max_pages = d.max_pages, a.lens = d.lens, a.B = (int)d.B;
   a.scale2 = d.scale * 1.44269504088896f;
   a.window = d.window, a.sinks = d.sinks, a.out = d.out;
-  a.part = (float *)d.workspace;
-  a.items = items_of(d.B, d.n_q, kc.n_kv);
-  a.plan = (int32_t *)(a.part + a.items * a.heads * (kc.head_dim + 2));
+  a.plan = (int32_t *)d.workspace;
+  a.part = (float *)((uint8_t *)d.workspace + plan_bytes(d.B));
   const int NB = (int)(kc.head_dim / 32);
   hipError_t e = hipErrorInvalidValue;
 #define QMM_CASE(K, V, F) \

@@ -4,6 +4,6 @@
 
 namespace qmm {
 namespace attn {
-hipError_t launch_q8_q4(const Args &a, int NB, int f16, hipStream_t s) { return run_kinds<C_Q8_0, C_Q4_0>(a, NB, f16, s); }
+hipError_t launch_q8_q4(Args &a, int NB, int f16, hipStream_t s) { return run_kinds<C_Q8_0, C_Q4_0>(a, NB, f16, s); }
 }  // namespace attn
 }  // namespace qmm
