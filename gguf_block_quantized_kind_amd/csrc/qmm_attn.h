@@ -346,7 +346,9 @@ __global__ __launch_bounds__(64 * kWaves) void attn_kernel(Args a) {
   // 0 is read in its place and given no weight.
   constexpr int kKG = kv::group_bytes(KK, NB), kVG = kv::group_bytes(VK, NB);
   constexpr int kKB = kv::block_code_bytes(KK), kVB = kv::block_code_bytes(VK);
-  const int32_t *table = a.table + (int64_t)b * a.max_pages;
+  // (Page numbers come through scalar loads: a vector load of one would wait
+  // for every key and value load before it.)
+  const auto *table = (const __attribute__((address_space(4))) int32_t *)(a.table + (int64_t)b * a.max_pages);
   Raw<KK> kr[NB];
   Raw<VK> vr[NB];
   half8 kd[KK == C_F16 ? 1 : NB], vd[VK == C_F16 ? 1 : NB];
@@ -369,16 +371,27 @@ __global__ __launch_bounds__(64 * kWaves) void attn_kernel(Args a) {
     for (int n = 0; n < NB; ++n) load_block<VK>(p + n * kVB, lane, vr[n]);
   };
   auto usable = [&](int page) { return page >= 0 && page < a.n_pages; };
-  // This wave's groups: g, then every fourth; (pi, gi) is page and group in it
-  // of the next one, whose page number is read an iteration ahead.
-  int g = gs + wave, page = 0, pi = g / a.page_groups, gi = g - pi * a.page_groups;
+  // This wave's groups: g, then every fourth.  (pi, gi) is the page table's
+  // entry and the group in its page of the group two steps ahead (past the end
+  // the last one again), whose page number is read that early.
+  int g = gs + wave, page = 0, in_page = 0, pi = 0, gi = 0, gn = g, page_next = 0, in_next = 0;
   bool there = false;
+  auto advance = [&] {
+    if (gn + kWaves < ge) {
+      gn += kWaves;
+      gi += kWaves;
+      while (gi >= a.page_groups) gi -= a.page_groups, ++pi;
+    }
+  };
   if (g < ge) {
-    page = table[pi];
+    pi = g / a.page_groups, gi = g - pi * a.page_groups;
+    page = table[pi], in_page = kvh * a.page_groups + gi;
+    advance();
+    page_next = table[pi], in_next = kvh * a.page_groups + gi;
     there = usable(page);
     page = there ? page : 0;
-    load_keys(page, kvh * a.page_groups + gi);
-    load_values(page, kvh * a.page_groups + gi);
+    load_keys(page, in_page);
+    load_values(page, in_page);
   }
 
   // The query scaled by a power of two to 2^14 .. 2^15, in one or two terms,
@@ -439,14 +452,11 @@ __global__ __launch_bounds__(64 * kWaves) void attn_kernel(Args a) {
   const Nibbles nb;
 
   while (g < ge) {
-    // The next group (the same again after the last: its loads are issued
+    // The next group's keys load as soon as this one's are used, its values
+    // likewise (after the last group once more the last: the loads are issued
     // whatever follows, so that no wait is widened by a branch).
-    const bool more = g + kWaves < ge;
-    if (more) {
-      gi += kWaves;
-      while (gi >= a.page_groups) gi -= a.page_groups, ++pi;
-    }
-    int next = table[pi];
+    advance();
+    const int page_after = table[pi], in_after = kvh * a.page_groups + gi;
 
     // Products of tokens 8G + k with head j, without the query's scale.
     float s[8];
@@ -470,9 +480,9 @@ __global__ __launch_bounds__(64 * kWaves) void attn_kernel(Args a) {
 #pragma unroll
       for (int r = 0; r < 4; ++r) s[4 * m + r] = t[r];
     }
-    const bool there_next = usable(next);
-    next = there_next ? next : 0;
-    load_keys(next, kvh * a.page_groups + gi);
+    const bool there_next = usable(page_next);
+    const int next = there_next ? page_next : 0;
+    load_keys(next, in_next);
 
     // Tokens outside [lo, len) of the first and last group: whatever their
     // bytes hold, they weigh nothing.
@@ -571,8 +581,9 @@ __global__ __launch_bounds__(64 * kWaves) void attn_kernel(Args a) {
         if constexpr (SPLIT) acc[n][x] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, pl, acc[n][x], 0, 0, 0);
       }
     }
-    load_values(next, kvh * a.page_groups + gi);
+    load_values(next, in_next);
     there = there_next;
+    page_next = page_after, in_next = in_after;
     g += kWaves;
   }
   sum = sum_over_groups(sum);
