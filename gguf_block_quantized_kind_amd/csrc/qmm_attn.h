@@ -136,16 +136,27 @@ struct Found {
   int b, c;
   uint32_t first;
 };
-__device__ __forceinline__ int per_split(int64_t groups, int64_t splits) {
-  return (int)min(max((groups + splits - 1) / splits, (int64_t)kMinGroups), (int64_t)1 << 26);
+// At least groups / splits (in f32, rounded up past its errors).
+__device__ __forceinline__ int per_split(float groups, float splits) {
+  return (int)fminf(fmaxf(groups / splits * (1.0f + 0x1p-20f) + 1.0f, (float)kMinGroups), 0x1p26f);
+}
+// ceil(n / c) for 0 <= n <= 2^26, c >= 4: a quotient in f32 is within two of it.
+__device__ __forceinline__ int splits_of(int n, int c, float inv) {
+  int q = (int)((float)n * inv);
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    const int r = q * c - n;  // (within a few c of 0: no overflow)
+    q += r < 0 ? 1 : r >= c ? -1 : 0;
+  }
+  return max(q, 1);
 }
 __device__ __forceinline__ Found find_split(const Args &a, int lane, uint32_t unit) {
   const int nh = a.n_kv * a.tiles;
   int n = span_of(a, lane).n;
   if (a.B == 1) {
     n = __builtin_amdgcn_readfirstlane(n);
-    const int c = per_split(n, max(a.slots / nh, 1));
-    return Found{unit < (uint32_t)max(1, (n + c - 1) / c) ? 0 : -1, c, 0};
+    const int most = max(a.slots / nh, 1), c = max((n + most - 1) / most, kMinGroups);
+    return Found{unit < (uint32_t)splits_of(n, c, 1.0f / (float)c) ? 0 : -1, c, 0};
   }
   uint64_t total = 0;
   for (int b0 = 0;;) {  // (at most 2^26 groups a sequence: one less keeps 64 of them below 2^32)
@@ -155,25 +166,26 @@ __device__ __forceinline__ Found find_split(const Args &a, int lane, uint32_t un
     n = span_of(a, b0 + lane).n;
   }
   if (a.B > 64) n = span_of(a, lane).n;
-  total *= nh;
-  auto count = [&](int c) { return lane < a.B ? (uint32_t)max(1, (n + c - 1) / c) : 0; };
-  int c = per_split(total, 2 * a.slots);
+  const float groups = (float)total * (float)nh, slots = (float)a.slots;
+  int c = per_split(groups, 2.0f * slots);
   if (a.B <= 64 && a.B * nh <= a.slots) {
-    int once = per_split(total, a.slots);
+    int once = per_split(groups, slots);
 #pragma unroll 1
     for (int i = 0; i < 3; ++i) {
-      const int items = __builtin_amdgcn_readlane((int)scan(count(once)), 63) * nh;
+      const uint32_t splits = lane < a.B ? (uint32_t)splits_of(n, once, 1.0f / (float)once) : 0;
+      const int items = __builtin_amdgcn_readlane((int)scan(splits), 63) * nh;
       if (items <= a.slots) break;
-      once = (int)((int64_t)once * items / a.slots) + 1;
+      once = (int)((float)once * ((float)items / slots)) + 1;
     }
     // (If they still do not all fit, the cost is near enough.)
-    const float even = (float)total / (float)a.slots;
-    if ((float)once <= even + kOverhead + 0.5f * (float)c) c = once;
+    if ((float)once <= groups / slots + kOverhead + 0.5f * (float)c) c = once;
   }
+  c = __builtin_amdgcn_readfirstlane(c);
+  const float inv = 1.0f / (float)c;
   uint32_t before = 0;
   for (int b0 = 0; b0 < a.B; b0 += 64) {
     if (b0) n = span_of(a, b0 + lane).n;
-    const uint32_t splits = b0 + lane < a.B ? (uint32_t)max(1, (n + c - 1) / c) : 0;
+    const uint32_t splits = b0 + lane < a.B ? (uint32_t)splits_of(n, c, inv) : 0;
     const uint32_t incl = scan(splits);
     const uint64_t mask = __ballot(unit - before < incl);
     if (mask) {
@@ -329,7 +341,7 @@ __global__ __launch_bounds__(64 * kWaves) void attn_kernel(Args a) {
   if (f.b < 0) return;
   const int b = __builtin_amdgcn_readfirstlane(f.b), c = __builtin_amdgcn_readfirstlane(f.c);
   const Span sp = span_of(a, b);
-  const int splits = max(1, (sp.n + c - 1) / c), each = (sp.n + splits - 1) / splits;
+  const int splits = __builtin_amdgcn_readfirstlane(splits_of(sp.n, c, 1.0f / (float)c)), each = (sp.n + splits - 1) / splits;
   const int mine = (int)(unit - f.first);
   if (mine == 0 && hh == 0 && threadIdx.x == 0) {
     a.plan[2 * b] = (int32_t)f.first;
