@@ -92,8 +92,24 @@ def load_library(path: str = LIBRARY) -> ctypes.CDLL:
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
         fn.restype, fn.argtypes = res, args
+    _bind_calls(lib)
     _lib = lib
     return lib
+
+
+# The entry points a decode step calls once per layer, through _qmm_call (built
+# with the library) instead of ctypes: name -> function.
+_calls = {}
+
+
+def _bind_calls(lib):
+    try:
+        from . import _qmm_call
+    except ImportError as e:
+        raise RuntimeError("the _qmm_call module is not built; run __graft_entry__.build() first") from e
+    for name in ("qmm_rope", "qmm_kv_write", "qmm_kv_append", "qmm_kv_read", "qmm_attn_decode"):
+        _qmm_call.bind(name, ctypes.cast(getattr(lib, name), ctypes.c_void_p).value)
+        _calls[name] = getattr(_qmm_call, name)
 
 
 def _check(status: int):
@@ -639,7 +655,10 @@ def _call(name: str, stream, tensors, *args):
         if t is not None and (t.get_device() != index or index < 0):
             raise ValueError(f"operands must be on one GPU, got {t.device} with {tensors[0].device}")
     s = torch._C._cuda_getCurrentRawStream(index) if stream is None else int(stream.cuda_stream)
-    fn = getattr(load_library(), name)
+    fn = _calls.get(name)
+    if fn is None:
+        load_library()
+        fn = _calls[name]
     before = torch._C._cuda_getDevice()
     if before == index:
         status = fn(*args, s)

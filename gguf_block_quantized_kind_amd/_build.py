@@ -11,6 +11,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -21,6 +22,9 @@ LIBRARY = os.path.join(HERE, "libqmm.so")
 # library; not part of the matmul C ABI).
 PROBE_SOURCE = os.path.join(CSRC, "probe", "qmm_stream_read.hip")
 PROBE_LIBRARY = os.path.join(HERE, "libqmm_probe.so")
+# The CPython calls of the entry points made once per layer (host code only).
+CALL_SOURCE = os.path.join(CSRC, "bind", "qmm_call.c")
+CALL_MODULE = os.path.join(HERE, "_qmm_call" + sysconfig.get_config_var("EXT_SUFFIX"))
 OBJDIR = os.path.join(ROOT, "_build")
 ARCH = "gfx950"
 
@@ -76,6 +80,7 @@ def build(jobs: int = 8, verbose: bool = False) -> str:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIBRARY)
     build_probe(cc)
+    build_call()
     return LIBRARY
 
 
@@ -86,6 +91,16 @@ def build_probe(cc: str) -> str:
         raise RuntimeError(f"hipcc failed on {PROBE_SOURCE}:\n{r.stderr}")
     os.replace(tmp, PROBE_LIBRARY)
     return PROBE_LIBRARY
+
+
+def build_call() -> str:
+    tmp = CALL_MODULE + ".tmp"
+    r = subprocess.run(["gcc", "-O2", "-shared", "-fPIC", "-Wall", "-I", sysconfig.get_paths()["include"], CALL_SOURCE, "-o", tmp],
+                       capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"gcc failed on {CALL_SOURCE}:\n{r.stderr}")
+    os.replace(tmp, CALL_MODULE)
+    return CALL_MODULE
 
 
 if __name__ == "__main__":

@@ -26,6 +26,14 @@ __global__ __launch_bounds__(256) void join_kernel(Args a, int D) {
   const int64_t nh = (int64_t)a.n_kv * a.tiles, item0 = first * nh + tile * a.n_kv + kvh;
   const float *ml = a.part + a.items * a.heads * D;
 
+  // The first parts load beside the references, whose weights they wait for.
+  const int lanes = D / 4, ways = kThreads / lanes, way = tid / lanes, d4 = tid - way * lanes;
+  const float *parts = a.part + (item0 * a.heads + h) * D + 4 * d4;
+  const int64_t step = nh * a.heads * D;
+  const bool early = way < ways && way < splits;
+  floatx4 o = {0, 0, 0, 0};
+  if (early) o = *(const floatx4 *)(parts + way * step);
+
   float Rm = kFloor;
   for (int i = tid; i < splits; i += kThreads) Rm = fmaxf(Rm, ml[((item0 + i * nh) * a.heads + h) * 2]);
 #pragma unroll
@@ -36,8 +44,6 @@ __global__ __launch_bounds__(256) void join_kernel(Args a, int D) {
     Rm = fmaxf(fmaxf(red[sub][0], red[sub][1]), fmaxf(red[sub][2], red[sub][3]));
   }
 
-  const int lanes = D / 4, ways = kThreads / lanes, way = tid / lanes, d4 = tid - way * lanes;
-  floatx4 o = {0, 0, 0, 0};
   float l = 0.0f;
   for (int i0 = 0; i0 < splits; i0 += kChunk) {
     const int n = min(kChunk, splits - i0);
@@ -49,11 +55,10 @@ __global__ __launch_bounds__(256) void join_kernel(Args a, int D) {
       l = __builtin_fmaf(w, m[1], l);
     }
     __syncthreads();
+    if (i0 == 0 && early) o *= weight[sub][way];
     if (way < ways) {
-      const float *p = a.part + ((item0 + i0 * nh) * a.heads + h) * D + 4 * d4;
-      const int64_t step = nh * a.heads * D;
 #pragma unroll 4
-      for (int i = way; i < n; i += ways) o += weight[sub][i] * *(const floatx4 *)(p + i * step);
+      for (int i = way + (i0 ? 0 : ways); i < n; i += ways) o += weight[sub][i] * *(const floatx4 *)(parts + (i0 + i) * step);
     }
   }
 #pragma unroll
