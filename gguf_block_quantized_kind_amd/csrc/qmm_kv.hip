@@ -74,6 +74,15 @@ __device__ __forceinline__ int64_t lane_of(int64_t v, int lane) {
   return (int64_t)(uint32_t)__shfl((int)v, lane, 64) | (int64_t)__shfl((int)(v >> 32), lane, 64) << 32;
 }
 
+// The lane number, whose uses the compiler does not move out of the loop over
+// the heads: kept addresses of every kind's path would cost registers, and so
+// waves.
+__device__ __forceinline__ int fresh_lane() {
+  int lane = threadIdx.x & 63;
+  asm volatile("" : "+v"(lane));
+  return lane;
+}
+
 // LDS written by some lanes of the wave is read by others after this.
 __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
@@ -122,7 +131,7 @@ __device__ __forceinline__ Spot spot_of(const Places &p, int lane) {
 template <int KIND, int NB>
 __device__ __forceinline__ void write_scales(uint8_t *head, const Spot &at, const Eight &g, float *rows, Step *steps) {
   constexpr int pitch = NB * 32 + 4;
-  const int lane = threadIdx.x & 63, t = (lane >> 2) & 7;
+  const int lane = fresh_lane(), t = (lane >> 2) & 7;
   if (!(g.mask >> t & 1)) return;  // (all four lanes)
 #pragma unroll 1
   for (int b0 = 0; b0 < NB; b0 += 2) {
@@ -155,7 +164,7 @@ template <int KIND, int NB>
 __device__ __forceinline__ void write_keys(uint8_t *head, const Spot &at, const Eight &g, const float *rows,
                                            const Step *steps) {
   constexpr int pitch = NB * 32 + 4;
-  const int lane = threadIdx.x & 63, t = lane & 7, r = at.r;  // `at`: of token lane % 8
+  const int lane = fresh_lane(), t = lane & 7, r = at.r;  // `at`: of token lane % 8
   uint8_t *token = head + at.base;
   if (!(g.mask >> t & 1)) return;
 #pragma unroll 1
@@ -186,7 +195,7 @@ template <int KIND, int NB>
 __device__ __forceinline__ void write_values(uint8_t *head, const Places &p, const Spot &first, const Eight &g,
                                              const float *rows, const Step *steps) {
   constexpr int pitch = NB * 32 + 4;
-  const int lane = threadIdx.x & 63, j = lane & 15;
+  const int lane = fresh_lane(), j = lane & 15;
   if (g.whole) {
     const int r = first.r;
     uint8_t *octet = head + first.base;
@@ -270,10 +279,8 @@ __device__ __forceinline__ void load_rows(floatx4 (&v)[NB], const T *x, int64_t 
   }
 }
 
-// (Five waves per SIMD fit without spilling; held to six, the 32768-token write
-// takes 86 us instead of 71.)
 template <typename T, int NB, bool ROPE>
-__global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(5))) void kv_write_kernel(WriteArgs a) {
+__global__ __launch_bounds__(64 * kWaves) void kv_write_kernel(WriteArgs a) {
   if ((int64_t)blockIdx.x >= a.kv_wgs) {
     if constexpr (ROPE) rotate_any<T>(a.q, a.q_out_f16, a.q_wide, ((int64_t)blockIdx.x - a.kv_wgs) * 256 + threadIdx.x);
     return;
