@@ -608,6 +608,22 @@ def _layout_id(layout) -> int:
 # These calls run once per layer and token, where the host's time is what a
 # small step waits for: sizes that are functions of their arguments alone are
 # looked up once, and the checks below read each tensor property once.
+_torch = None        # set by the first call
+_DTYPE_CODES = {}
+
+
+def _load_torch():
+    global _torch
+    import torch
+    _DTYPE_CODES.update({torch.float32: QMM_F32, torch.float16: QMM_F16})
+    _torch = torch
+    return torch
+
+
+def _code(t) -> int:
+    return _DTYPE_CODES.get(t.dtype, 99)  # 99: refused by the library as a bad dtype
+
+
 @functools.lru_cache(maxsize=256)
 def _page_bytes(kind: int, page_size: int, n_kv: int, head_dim: int) -> int:
     return int(load_library().qmm_kv_page_bytes(kind, page_size, n_kv, head_dim))
@@ -626,10 +642,9 @@ def _rows_arg(x, what: str) -> tuple[int, int, int, int]:
 
 
 def _ints(t, count: int, what: str):
-    import torch
-    if t.dtype is not torch.int32:
+    if t.dtype is not (_torch or _load_torch()).int32:
         raise TypeError(f"{what} must be int32, got {t.dtype}")
-    if not t.is_contiguous() or t.numel() != count:
+    if t.numel() != count or not t.is_contiguous():
         raise ValueError(f"{what} must hold {count} contiguous elements, got {tuple(t.shape)}")
 
 
@@ -649,10 +664,10 @@ def _call(name: str, stream, tensors, *args):
     """Calls a C entry point on the operands' device (made the current one for
     the call), refusing operands on the host or on different devices; its last
     argument is the stream, by default that device's current one."""
-    import torch
+    torch = _torch
     index = tensors[0].get_device()
     for t in tensors:
-        if t is not None and (t.get_device() != index or index < 0):
+        if t is not None and t.get_device() != index or index < 0:
             raise ValueError(f"operands must be on one GPU, got {t.device} with {tensors[0].device}")
     s = torch._C._cuda_getCurrentRawStream(index) if stream is None else int(stream.cuda_stream)
     fn = _calls.get(name)
@@ -701,17 +716,23 @@ def rope_freqs(n_rot: int, base: float = 10000.0, factors=None, factor: float = 
 
 
 def _freqs_arg(freqs) -> int:
-    import torch
-    if freqs.dtype is not torch.float64 or freqs.dim() != 1 or not freqs.is_contiguous():
+    if freqs.dtype is not _torch.float64 or freqs.dim() != 1 or not freqs.is_contiguous():
         raise TypeError(f"freqs must be a contiguous float64 vector, got {freqs.dtype} {tuple(freqs.shape)}")
-    return 2 * freqs.shape[0]
+    return 2 * freqs.numel()
 
 
-def _out_arg(out, shape, dtype, like) -> tuple:
+def _new(shape, dtype, like, stream):
+    """An operand allocated for the call, kept from reuse while `stream` has it."""
+    t = _torch.empty(shape, dtype=dtype, device=like.device)
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
+def _out_arg(out, shape, dtype, like, stream) -> tuple:
     """`out`, allocated if None, and its row stride."""
-    import torch
     if out is None:
-        return torch.empty(shape, dtype=dtype or like.dtype, device=like.device), shape[1] * shape[2]
+        return _new(shape, dtype or like.dtype, like, stream), shape[1] * shape[2]
     T, H, D, stride = _rows_arg(out, "out")
     if (T, H, D) != shape:
         raise ValueError(f"out is {tuple(out.shape)}, needs {shape}")
@@ -723,9 +744,9 @@ def rope(x, positions, freqs, layout="half", mscale: float = 1.0, out=None, out_
     turned by positions [T] int32; out may be x."""
     T, H, D, xs = _rows_arg(x, "x")
     _ints(positions, T, "positions")
-    out, ys = _out_arg(out, (T, H, D), out_dtype, x)
+    out, ys = _out_arg(out, (T, H, D), out_dtype, x, stream)
     _call("qmm_rope", stream, (x, positions, freqs, out), freqs.data_ptr(), _freqs_arg(freqs), _layout_id(layout), mscale,
-          positions.data_ptr(), x.data_ptr(), _dtype_code(x), xs, out.data_ptr(), _dtype_code(out), ys, T, H, D)
+          positions.data_ptr(), x.data_ptr(), _code(x), xs, out.data_ptr(), _code(out), ys, T, H, D)
     return out
 
 
@@ -741,7 +762,7 @@ def _kv_args(k, v, slots):
 
 
 def _cache_args(k_pages, v_pages, k_kind, v_kind, page_size: int, n_kv: int, D: int):
-    kk, vk = cache_kind_id(k_kind), cache_kind_id(v_kind)
+    kk, vk = CACHE_KINDS.get(k_kind) or cache_kind_id(k_kind), CACHE_KINDS.get(v_kind) or cache_kind_id(v_kind)
     n = _pages_arg(k_pages, kk, page_size, n_kv, D, "k_pages")
     if _pages_arg(v_pages, vk, page_size, n_kv, D, "v_pages") != n:
         raise ValueError(f"k_pages holds {n} pages, v_pages {v_pages.shape[0]}")
@@ -753,7 +774,7 @@ def kv_write(k, v, slots, k_pages, v_pages, k_kind, v_kind, page_size: int, stre
     T, n_kv, D, ks, vs = _kv_args(k, v, slots)
     cache = _cache_args(k_pages, v_pages, k_kind, v_kind, page_size, n_kv, D)
     _call("qmm_kv_write", stream, (k, v, slots, k_pages, v_pages), *cache, k.data_ptr(), ks, v.data_ptr(), vs,
-          _dtype_code(k), slots.data_ptr(), T)
+          _code(k), slots.data_ptr(), T)
 
 
 def kv_append(q, k, v, positions, slots, k_pages, v_pages, k_kind, v_kind, page_size: int, freqs, layout="half",
@@ -768,10 +789,10 @@ def kv_append(q, k, v, positions, slots, k_pages, v_pages, k_kind, v_kind, page_
         raise TypeError(f"q is {q.dtype}, k is {k.dtype}")
     _ints(positions, T, "positions")
     cache = _cache_args(k_pages, v_pages, k_kind, v_kind, page_size, n_kv, D)
-    out, os_ = _out_arg(out, (T, n_q, D), out_dtype, q)
+    out, os_ = _out_arg(out, (T, n_q, D), out_dtype, q, stream)
     _call("qmm_kv_append", stream, (q, k, v, positions, slots, k_pages, v_pages, freqs, out), freqs.data_ptr(),
           _freqs_arg(freqs), _layout_id(layout), mscale, positions.data_ptr(), q.data_ptr(), qs, n_q, out.data_ptr(),
-          _dtype_code(out), os_, *cache, k.data_ptr(), ks, v.data_ptr(), vs, _dtype_code(k), slots.data_ptr(), T)
+          _code(out), os_, *cache, k.data_ptr(), ks, v.data_ptr(), vs, _code(k), slots.data_ptr(), T)
     return out
 
 
@@ -779,7 +800,7 @@ def kv_read(slots, k_pages, v_pages, k_kind, v_kind, page_size: int, n_kv: int, 
             v_out=None, stream=None):
     """(k, v) [T, n_kv, head_dim] of the tokens at slots [T] int32, f16 by
     default; zeros for skipped slots (outside the cache)."""
-    import torch
+    torch = _torch or _load_torch()
     T = slots.numel()
     _ints(slots, T, "slots")
     shape = (T, n_kv, head_dim)
@@ -787,15 +808,14 @@ def kv_read(slots, k_pages, v_pages, k_kind, v_kind, page_size: int, n_kv: int, 
         raise ValueError("k_out and v_out go together")
     if k_out is None:
         dtype = dtype or torch.float16
-        k_out = torch.empty(shape, dtype=dtype, device=slots.device)
-        v_out = torch.empty(shape, dtype=dtype, device=slots.device)
+        k_out, v_out = _new(shape, dtype, slots, stream), _new(shape, dtype, slots, stream)
     else:
         for t in (k_out, v_out):
             if tuple(t.shape) != shape or not t.is_contiguous() or t.dtype is not k_out.dtype:
                 raise ValueError(f"k_out and v_out must be contiguous {shape} of one type")
     cache = _cache_args(k_pages, v_pages, k_kind, v_kind, page_size, n_kv, head_dim)
     _call("qmm_kv_read", stream, (slots, k_pages, v_pages, k_out, v_out), *cache, slots.data_ptr(), T, k_out.data_ptr(),
-          v_out.data_ptr(), _dtype_code(k_out))
+          v_out.data_ptr(), _code(k_out))
     return k_out, v_out
 
 
@@ -811,7 +831,7 @@ def attn_decode(q, k_pages, v_pages, block_table, seq_lens, k_kind, v_kind, page
     seq_lens [B] int32 tokens.  scale defaults to head_dim^-0.5; window > 0
     keeps the last `window` tokens; sinks [n_q] f32 adds a logit without a
     value per head."""
-    import torch
+    torch = _torch or _load_torch()
     B, n_q, D, qs = _rows_arg(q, "q")
     _ints(seq_lens, B, "seq_lens")
     shape = block_table.shape
@@ -823,18 +843,18 @@ def attn_decode(q, k_pages, v_pages, block_table, seq_lens, k_kind, v_kind, page
         raise ValueError(f"sinks must be {n_q} contiguous float32 values")
     cache = _cache_args(k_pages, v_pages, k_kind, v_kind, page_size, n_kv, D)
     if out is None:
-        out = torch.empty((B, n_q, D), dtype=q.dtype, device=q.device)
+        out = _new((B, n_q, D), q.dtype, q, stream)
     elif tuple(out.shape) != (B, n_q, D) or not out.is_contiguous() or out.dtype is not q.dtype:
         raise ValueError(f"out must be contiguous {(B, n_q, D)} of q's type")
     if workspace is None:
         nbytes = qmm_attn_decode_workspace_bytes(B, n_q, n_kv, D)
-        workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=q.device)
+        workspace = _new(max(nbytes, 1), torch.uint8, q, stream)
     else:
         nbytes = workspace.numel() * workspace.element_size()
         if not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous")
     _call("qmm_attn_decode", stream, (q, k_pages, v_pages, block_table, seq_lens, sinks, out, workspace), *cache,
-          q.data_ptr(), _dtype_code(q), qs, n_q, block_table.data_ptr(), max_pages, seq_lens.data_ptr(), B,
+          q.data_ptr(), _code(q), qs, n_q, block_table.data_ptr(), max_pages, seq_lens.data_ptr(), B,
           D ** -0.5 if scale is None else scale, window, 0 if sinks is None else sinks.data_ptr(), out.data_ptr(),
           workspace.data_ptr(), nbytes)
     return out

@@ -315,11 +315,17 @@ __device__ __forceinline__ void load_q(const QT *q, int G, float (&v)[8]) {
 __host__ __device__ inline int lds_parts(int heads) { return heads <= 8 ? kWaves : 2; }
 
 // Four elements of the result: the sums o over the weights' sum l (both on
-// reference R) with the sink's share; zeros where nothing was attended.
+// reference R), with the sink's share on the larger of the two references;
+// zeros where nothing was attended.
 template <typename QT>
 __device__ __forceinline__ void store_out(QT *out, floatx4 o, float l, float R, const float *sinks, int head) {
-  if (sinks) l += __builtin_amdgcn_exp2f(fminf(sinks[head] * 1.44269504f - R, 120.0f));
-  const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+  float f = 1.0f;
+  if (sinks) {
+    const float sink = sinks[head] * 1.44269504f, Rn = fmaxf(R, sink);
+    f = __builtin_amdgcn_exp2f(R - Rn);
+    l = __builtin_fmaf(l, f, __builtin_amdgcn_exp2f(sink - Rn));
+  }
+  const float inv = l > 0.0f || l != l ? f / l : 0.0f;
   typedef QT q4 __attribute__((ext_vector_type(4)));
   *(q4 *)out = q4{(QT)(o[0] * inv), (QT)(o[1] * inv), (QT)(o[2] * inv), (QT)(o[3] * inv)};
 }
@@ -330,7 +336,7 @@ __global__ __launch_bounds__(64 * kWaves) void attn_kernel(Args a) {
   constexpr bool SPLIT = sizeof(QT) == 4;  // two f16 terms
   constexpr bool SUB = kSubnormalKeys<KK, SPLIT>;
   constexpr int kPitch = D + 4;
-  extern __shared__ float lds[];  // [part][heads][kPitch], then [part][heads][2]
+  extern __shared__ __attribute__((aligned(16))) float lds[];  // [part][heads][kPitch], then [part][heads][2]
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int j = lane & 15, G = lane >> 4;
 
@@ -429,9 +435,10 @@ __global__ __launch_bounds__(64 * kWaves) void attn_kernel(Args a) {
       big = max_over_groups(big);
       // 2^e brings big to [2^14, 2^15); the exponents kept where 2^e and 2^-e are normal.
       int e = 14 + 127 - (int)(__builtin_bit_cast(uint32_t, big) >> 23);
-      e = big > 0.0f && big < __builtin_inff() ? min(max(e, -112), 125) : 0;
+      e = big > 0.0f && big < __builtin_inff() ? min(max(e, -113), 125) : 0;
       up *= __builtin_bit_cast(float, (uint32_t)(127 + e) << 23);
-      qscale *= __builtin_bit_cast(float, (uint32_t)(127 - e) << 23) * (SUB ? 0x1p24f : 1.0f);
+      qscale *= __builtin_bit_cast(float, (uint32_t)(127 - e) << 23);
+      if constexpr (SUB) qscale *= 0x1p24f;
     }
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
@@ -540,8 +547,19 @@ __global__ __launch_bounds__(64 * kWaves) void attn_kernel(Args a) {
         for (int k = 0; k < 4; ++k)
           part[k] = __builtin_elementwise_max(part[k], as_us2(VK == C_Q4_0 ? w[k] & 0x7fff7fffu : w[k]));
       }
-      const half2v big = as_h2(as_u(__builtin_elementwise_max(__builtin_elementwise_max(part[0], part[1]),
-                                                              __builtin_elementwise_max(part[2], part[3]))));
+      ushort2v most = __builtin_elementwise_max(__builtin_elementwise_max(part[0], part[1]),
+                                                __builtin_elementwise_max(part[2], part[3]));
+      // A NaN scale (a block that held an infinity or NaN) leaves the other
+      // blocks' reference alone.
+      if (__any(max(most[0], most[1]) >= 0x7c00)) {
+        most = ushort2v{0, 0};
+        for (int n = 0; n < NB; ++n)
+          for (int k = 0; k < 8; ++k) {
+            const uint16_t m = __builtin_bit_cast(uint16_t, (_Float16)vd[n][k]) & 0x7fff;
+            if (m < 0x7c00) most[0] = max(most[0], m);
+          }
+      }
+      const half2v big = as_h2(as_u(most));
       // 2^e <= scale < 2^(e + 1); f16 scales are 0 or at least 2^-24.
       const float bf = fmaxf(fmaxf((float)big[0], (float)big[1]), 0x1p-24f);
       top += (float)((int)(__builtin_bit_cast(uint32_t, bf) >> 23) - 127 - 14);

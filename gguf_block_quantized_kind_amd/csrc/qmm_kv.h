@@ -189,10 +189,10 @@ template <typename T, typename O, int V>
 __device__ __forceinline__ void rotate_rows(const Rotate &r, int64_t i) {
   using X = typename Vec<T, V>::type;
   using Y = typename Vec<O, V>::type;
-  const int per_token = r.chunks * r.ranges;
-  const int64_t t = i / per_token;
+  const uint32_t per_token = (uint32_t)(r.chunks * r.ranges), t32 = (uint32_t)i / per_token;  // (fewer than 2^32 threads)
+  const int64_t t = t32;
   if (t >= r.T) return;
-  const int rest = (int)(i - t * per_token), range = rest / r.chunks, p = (rest - range * r.chunks) * V;
+  const int rest = (int)((uint32_t)i - t32 * per_token), range = rest / r.chunks, p = (rest - range * r.chunks) * V;
   const int half = r.rope.n_rot >> 1;
   const bool turned = p < half, split = turned && !r.rope.interleaved;
   // Elements [da, da + V) and [db, db + V): the two members of V pairs, or (interleaved, passing) 2 V neighbours.

@@ -286,7 +286,7 @@ __global__ __launch_bounds__(64 * kWaves) void kv_write_kernel(WriteArgs a) {
     return;
   }
   constexpr int D = NB * 32, pitch = D + 4;
-  __shared__ float lds_rows[kWaves][8 * pitch];
+  __shared__ __attribute__((aligned(16))) float lds_rows[kWaves][8 * pitch];
   __shared__ Step lds_steps[kWaves][NB * 8];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   float *rows = lds_rows[wave];

@@ -375,6 +375,68 @@ def test_cache_beyond_32_bit_offsets():
             check(got[b, h], w, tol + half_step(w, "f16"), f"far {b} {h}")
 
 
+@pytest.mark.parametrize("kk,vk", [("F16", "F16"), ("Q8_0", "Q8_0"), ("Q4_0", "Q4_0")])
+@pytest.mark.parametrize("dt", ["f16", "f32"])
+@pytest.mark.parametrize("scale", [-0.2, 0.0])
+def test_attn_negative_and_zero_scale(kk, vk, dt, scale):
+    c = Case(kk, vk, 64, 32, 2, [90, 1, 400])
+    q = c.g.normal(size=(3, 6, 64)).astype(NP[dt])
+    check(c.run(dev(q), scale=scale).cpu().numpy(), *c.want(q, dt, scale=scale), f"scale={scale}")
+
+
+@pytest.mark.parametrize("kk,vk", [("F16", "F16"), ("Q8_0", "Q8_0"), ("Q4_0", "Q4_0")])
+def test_attn_extreme_queries_and_sinks(kk, vk):
+    """f32 queries near the ends of their range, and results far below one through sinks: relative to themselves."""
+    c = Case(kk, vk, 64, 32, 1, [70, 300])
+    q = c.g.normal(size=(2, 2, 64)).astype(np.float32)
+    for size in (1e-36, 1e36):
+        check(c.run(dev(q * np.float32(size)), scale=0.125 / size).cpu().numpy(),
+              *c.want(q * np.float32(size), "f32", scale=0.125 / size), f"{size}")
+    c.v = (c.v * 2.0 ** -12).astype(np.float32)
+    slots = np.concatenate([c.table[b, np.arange(n) // 32] * 32 + np.arange(n) % 32 for b, n in enumerate(c.lens)])
+    qmm.kv_write(dev(c.k), dev(c.v), dev(slots.astype(np.int32)), c.kp, c.vp, kk, vk, 32)
+    c.vx = oa.dequantize(vk, *oa.quantize(vk, c.v))
+    sinks = np.array([55.0, 60.0], np.float32)
+    check(c.run(dev(q), sinks=dev(sinks)).cpu().numpy(), *c.want(q, "f32", sinks=sinks), "far below one")
+
+
+@pytest.mark.parametrize("vk", ["F16", "Q8_0", "Q4_0"])
+def test_attn_nonfinite_value_stays_in_its_elements(vk):
+    """A NaN in an attended value reaches the elements that share its place (its block of a quantized kind) and no
+    others."""
+    c = Case("Q8_0", vk, 96, 32, 2, [200, 40])
+    row, el = 77, 40                                           # sequence 0, key head 1, block 1
+    c.v[row, 1, el] = np.nan
+    slots = np.concatenate([c.table[b, np.arange(n) // 32] * 32 + np.arange(n) % 32 for b, n in enumerate(c.lens)])
+    qmm.kv_write(dev(c.k), dev(c.v), dev(slots.astype(np.int32)), c.kp, c.vp, "Q8_0", vk, 32)
+    q = c.g.normal(size=(2, 4, 96)).astype(np.float16)
+    got = c.run(dev(q)).cpu().numpy().astype(np.float64)
+    hit = np.zeros(got.shape, bool)
+    hit[0, 2:, el if vk == "F16" else slice(32, 64)] = True
+    assert np.array_equal(np.isnan(got), hit)
+    c.vx[np.isnan(c.vx)] = 0
+    want, tol = c.want(q, "f16")
+    got[hit] = want[hit] = 0
+    check(got, want, tol, "the other elements")
+
+
+def test_two_streams_at_once():
+    """Calls on two streams, each with its own workspace, and the stream argument with outputs allocated by the call."""
+    cases = [Case("Q8_0", "Q4_0", 128, 64, 2, [3000, 100]), Case("F16", "F16", 64, 32, 1, [5000])]
+    qs = [dev(c.g.normal(size=(len(c.lens), 4, c.D)).astype(np.float16)) for c in cases]
+    want = [c.run(q) for c, q in zip(cases, qs)]
+    streams = [torch.cuda.Stream() for _ in cases]
+    tables = [(dev(c.table), dev(np.array(c.lens, np.int32))) for c in cases]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, (c, q) in enumerate(zip(cases, qs)):
+            got[i].append(qmm.attn_decode(q, c.kp, c.vp, *tables[i], c.kk, c.vk, c.P, c.n_kv, stream=streams[i]))
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        assert all(torch.equal(x, want[i]) for x in got[i])
+
+
 # -- the operators together ----------------------------------------------------------
 def test_decode_steps_through_a_layer(oracle_mod):
     """Prompt, then decode steps: q, k, v from a Q4_0 projection (qmm_matmul), append, attention, output projection.
