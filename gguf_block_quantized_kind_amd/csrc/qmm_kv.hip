@@ -17,6 +17,15 @@
 // those of its tokens that no octet covers (other sequences' single tokens,
 // the ends of a prompt), byte by byte.  A prompt's tokens so fill whole units
 // from any start.
+//
+// What bounds it: memory traffic when there is much of it, and a wave's chain of
+// loads and LDS rounds when there is not.  Measured, 32768 tokens of 8 heads of
+// 128 in Q4_0: f32 rows written (306 MB) in 72 us, 4.3 TB/s, read back as f16
+// (172 MB) in 37 us, 4.6 TB/s; 5003 tokens, Q8_0 keys and Q4_0 values, written
+// from f16 (29 MB) in 15 us and read as f32 (49 MB) in 12; one token of 8 heads
+// appended with 32 query heads 5.5 us.  A half wave per block of a token with
+// byte stores took 420 and 230 us for the first two; windows of 32 tokens per
+// workgroup, synchronized three times, 82 and 51.
 #include <algorithm>
 #include <type_traits>
 
