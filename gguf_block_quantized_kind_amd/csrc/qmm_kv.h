@@ -147,6 +147,21 @@ __device__ __forceinline__ void rotation(int pos, double freq, float &c, float &
   s = (k & 2) ? -b : b;
 }
 
+// The members of a rotated pair, by the same operations wherever they are
+// computed, rounded to f32 before any narrower type: a result does not depend
+// on the alignment of its row.  (Without the barrier the compiler rounds some
+// of them from the exact sum to f16.)
+__device__ __forceinline__ float in_f32(float x) {
+  asm("" : "+v"(x));
+  return x;
+}
+__device__ __forceinline__ float turned_a(float u, float v, float c, float s) {
+  return in_f32(__builtin_fmaf(u, c, -(v * s)));
+}
+__device__ __forceinline__ float turned_b(float u, float v, float c, float s) {
+  return in_f32(__builtin_fmaf(u, s, v * c));
+}
+
 struct Rope {
   const double *freqs;  // n_rot / 2 radians per position
   int n_rot;
@@ -222,19 +237,19 @@ __device__ __forceinline__ void rotate_rows(const Rotate &r, int64_t i) {
     } else if (split) {
 #pragma unroll
       for (int k = 0; k < V; ++k) {
-        u[k] = (O)((float)a[k] * c[k] - (float)b[k] * s[k]);
-        v[k] = (O)((float)a[k] * s[k] + (float)b[k] * c[k]);
+        u[k] = (O)turned_a((float)a[k], (float)b[k], c[k], s[k]);
+        v[k] = (O)turned_b((float)a[k], (float)b[k], c[k], s[k]);
       }
     } else if constexpr (V == 1) {
-      u[0] = (O)((float)a[0] * c[0] - (float)b[0] * s[0]);
-      v[0] = (O)((float)a[0] * s[0] + (float)b[0] * c[0]);
+      u[0] = (O)turned_a((float)a[0], (float)b[0], c[0], s[0]);
+      v[0] = (O)turned_b((float)a[0], (float)b[0], c[0], s[0]);
     } else {
 #pragma unroll
       for (int k = 0; k < V; k += 2) {
-        u[k] = (O)((float)a[k] * c[k / 2] - (float)a[k + 1] * s[k / 2]);
-        u[k + 1] = (O)((float)a[k] * s[k / 2] + (float)a[k + 1] * c[k / 2]);
-        v[k] = (O)((float)b[k] * c[(V + k) / 2] - (float)b[k + 1] * s[(V + k) / 2]);
-        v[k + 1] = (O)((float)b[k] * s[(V + k) / 2] + (float)b[k + 1] * c[(V + k) / 2]);
+        u[k] = (O)turned_a((float)a[k], (float)a[k + 1], c[k / 2], s[k / 2]);
+        u[k + 1] = (O)turned_b((float)a[k], (float)a[k + 1], c[k / 2], s[k / 2]);
+        v[k] = (O)turned_a((float)b[k], (float)b[k + 1], c[(V + k) / 2], s[(V + k) / 2]);
+        v[k + 1] = (O)turned_b((float)b[k], (float)b[k + 1], c[(V + k) / 2], s[(V + k) / 2]);
       }
     }
     __builtin_memcpy(__builtin_assume_aligned(y + (int64_t)h * r.D + da, sizeof(Y)), &u, sizeof(Y));

@@ -348,8 +348,8 @@ __global__ __launch_bounds__(64 * kWaves) void kv_write_kernel(WriteArgs a) {
           s *= a.rope.mscale;
           float *u = rows + t * pitch + (a.rope.interleaved ? 2 * q : q), *v = u + (a.rope.interleaved ? 1 : half);
           const float xa = *u, xb = *v;
-          *u = xa * c - xb * s;
-          *v = xa * s + xb * c;
+          *u = turned_a(xa, xb, c, s);
+          *v = turned_b(xa, xb, c, s);
         }
         wave_sync();
       }

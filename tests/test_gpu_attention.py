@@ -151,6 +151,54 @@ def test_kv_write_bytes_and_read(kk, vk, dt, D, P, H, case):
             assert same, (s, od)
 
 
+@pytest.mark.parametrize("kk,vk", [("Q8_0", "Q4_0"), ("F16", "Q8_0"), ("Q4_0", "F16")])
+def test_kv_large_calls_equal_small_ones(kk, vk):
+    """Sizes whose waves take several heads each: the same bytes and values as calls of 777 tokens."""
+    P, H, D, T = 64, 8, 64, 70001
+    n_pages = T // P + 3
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+    x = torch.randn((T, 2 * H, D), generator=g, device="cuda").half()
+    order = torch.randperm(n_pages, generator=g, device="cuda").int()
+    t = torch.arange(T, device="cuda") + 13
+    slots = order[t // P] * P + (t % P).int()
+    slots[5000] = -1
+    pages = [[torch.full((n_pages, oa.page_bytes(k, P, H, D)), 0x33, dtype=torch.uint8, device="cuda") for k in (kk, vk)]
+             for _ in range(2)]
+    qmm.kv_write(x[:, :H], x[:, H:], slots, *pages[0], kk, vk, P)
+    for i in range(0, T, 777):
+        qmm.kv_write(x[i:i + 777, :H], x[i:i + 777, H:], slots[i:i + 777], *pages[1], kk, vk, P)
+    assert torch.equal(pages[0][0], pages[1][0]) and torch.equal(pages[0][1], pages[1][1])
+    k, v = qmm.kv_read(slots, *pages[0], kk, vk, P, H, D)
+    for i in range(0, T, 777):
+        a, b = qmm.kv_read(slots[i:i + 777], *pages[0], kk, vk, P, H, D)
+        assert torch.equal(a, k[i:i + 777]) and torch.equal(b, v[i:i + 777])
+
+
+@pytest.mark.parametrize("dt", ["f16", "f32"])
+def test_odd_strides_and_offsets(dt):
+    """Rows at odd element offsets and strides give what packed rows give, in every operator."""
+    T, nq, H, D, P = 37, 4, 2, 128, 32
+    g = wl.rng("attn", f"odd{dt}")
+    x = g.normal(size=(T, nq + 2 * H, D)).astype(NP[dt])
+    row = (nq + 2 * H) * D + 3
+    buf = torch.zeros(T * row + 1, dtype=getattr(torch, {"f16": "float16", "f32": "float32"}[dt]), device="cuda")
+    odd = buf[1:].view(T, row)[:, :row - 3].unflatten(1, (nq + 2 * H, D))
+    odd.copy_(dev(x))
+    pos, slots = dev(np.arange(T, dtype=np.int32) * 999), dev(g.permutation(4 * P)[:T].astype(np.int32))
+    freqs, m = qmm.rope_freqs(D)
+    got = []
+    for y in (dev(x), odd):
+        kp, vp = qmm.kv_pages("Q8_0", 4, P, H, D), qmm.kv_pages("Q4_0", 4, P, H, D)
+        kp.zero_()
+        vp.zero_()
+        q = qmm.kv_append(y[:, :nq], y[:, nq:nq + H], y[:, nq + H:], pos, slots, kp, vp, "Q8_0", "Q4_0", P, freqs, mscale=m)
+        r = qmm.rope(y, pos, freqs, "interleaved")
+        table, lens = dev(np.arange(4, dtype=np.int32).reshape(1, 4).repeat(T, 0)), dev(np.arange(T, dtype=np.int32) * 3)
+        got.append((kp, vp, q, r, qmm.attn_decode(y[:, :nq], kp, vp, table, lens, "Q8_0", "Q4_0", P, H)))
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
 def test_kv_write_nonfinite_blocks():
     g = wl.rng("kv", "nonfinite")
     x = g.normal(size=(3, 2, 64)).astype(np.float32)
