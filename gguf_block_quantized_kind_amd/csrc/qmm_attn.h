@@ -98,7 +98,8 @@ struct Args {
   const float *sinks;
   void *out;
   float *part;    // [item][heads][D], then [item][heads][2]: reference and sum
-  int32_t *plan;  // [B][2]: a sequence's first split and number of splits, for the join
+  int32_t *plan;   // [B][2]: a sequence's first split and number of splits, for the join
+  int32_t *units;  // more than 64 sequences: number of splits, then each split's sequence
   int64_t items;  // workgroups launched
   int slots;      // workgroups the GPU holds at once
 };
@@ -146,16 +147,19 @@ __device__ __forceinline__ uint32_t scan(uint32_t v) {
 
 // Splits are numbered through the batch (at least one per sequence, so that
 // every output row is written).  find_split: the sequence (-1: past the last)
-// that split `unit` belongs to, its first split and the groups per split.
+// that split `unit` belongs to, its first split and their number.
 //
 // Groups per split, c.  Either all splits run at once: the smallest c whose
 // splits fit the slots, costing c + overhead; or there are two rounds of them
 // (of which the second overlaps the first's ends, by half a split on
 // average), c = total / (2 slots), costing total / slots + 2 overheads + c / 2.
 // Equal lengths take the first, very unequal ones the second.
+//
+// Up to 64 sequences every wave works this out by itself, one lane each; more
+// are planned by plan_kernel, once, before.
+constexpr int kLanes = 64;
 struct Found {
-  int b, c;
-  uint32_t first;
+  int b, first, splits;
 };
 // At least groups / splits (in f32, rounded up past its errors).
 __device__ __forceinline__ int per_split(float groups, float splits) {
@@ -171,51 +175,43 @@ __device__ __forceinline__ int splits_of(int n, int c, float inv) {
   }
   return max(q, 1);
 }
+// Two rounds of splits, or `once`, where all run at once: the cheaper.
+__device__ __forceinline__ int choose(int once, int twice, float groups, float slots) {
+  return (float)once <= groups / slots + kOverhead + 0.5f * (float)twice ? once : twice;
+}
+__device__ __forceinline__ int fewer(int c, float items, float slots) { return (int)((float)c * (items / slots)) + 1; }
+
 __device__ __forceinline__ Found find_split(const Args &a, int lane, uint32_t unit) {
   const int nh = a.n_kv * a.tiles;
   int n = span_of(a, lane).n;
   if (a.B == 1) {
     n = __builtin_amdgcn_readfirstlane(n);
     const int most = max(a.slots / nh, 1), c = max((n + most - 1) / most, kMinGroups);
-    return Found{unit < (uint32_t)splits_of(n, c, 1.0f / (float)c) ? 0 : -1, c, 0};
+    const int splits = splits_of(n, c, 1.0f / (float)c);
+    return Found{unit < (uint32_t)splits ? 0 : -1, 0, splits};
   }
-  uint64_t total = 0;
-  for (int b0 = 0;;) {  // (at most 2^26 groups a sequence: one less keeps 64 of them below 2^32)
-    total += (uint32_t)__builtin_amdgcn_readlane((int)scan((uint32_t)min(n, (1 << 26) - 1)), 63);
-    b0 += 64;
-    if (b0 >= a.B) break;
-    n = span_of(a, b0 + lane).n;
-  }
-  if (a.B > 64) n = span_of(a, lane).n;
+  // (At most 2^26 groups a sequence: one less keeps 64 of them below 2^32.)
+  const uint32_t total = (uint32_t)__builtin_amdgcn_readlane((int)scan((uint32_t)min(n, (1 << 26) - 1)), 63);
   const float groups = (float)total * (float)nh, slots = (float)a.slots;
   int c = per_split(groups, 2.0f * slots);
-  if (a.B <= 64 && a.B * nh <= a.slots) {
+  if (a.B * nh <= a.slots) {
     int once = per_split(groups, slots);
 #pragma unroll 1
     for (int i = 0; i < 3; ++i) {
       const uint32_t splits = lane < a.B ? (uint32_t)splits_of(n, once, 1.0f / (float)once) : 0;
       const int items = __builtin_amdgcn_readlane((int)scan(splits), 63) * nh;
       if (items <= a.slots) break;
-      once = (int)((float)once * ((float)items / slots)) + 1;
+      once = fewer(once, (float)items, slots);
     }
-    // (If they still do not all fit, the cost is near enough.)
-    if ((float)once <= groups / slots + kOverhead + 0.5f * (float)c) c = once;
+    c = choose(once, c, groups, slots);  // (if they still do not all fit, the cost is near enough)
   }
   c = __builtin_amdgcn_readfirstlane(c);
-  const float inv = 1.0f / (float)c;
-  uint32_t before = 0;
-  for (int b0 = 0; b0 < a.B; b0 += 64) {
-    if (b0) n = span_of(a, b0 + lane).n;
-    const uint32_t splits = b0 + lane < a.B ? (uint32_t)splits_of(n, c, inv) : 0;
-    const uint32_t incl = scan(splits);
-    const uint64_t mask = __ballot(unit - before < incl);
-    if (mask) {
-      const int l = __ffsll((unsigned long long)mask) - 1;
-      return Found{b0 + l, c, before + (uint32_t)__builtin_amdgcn_readlane((int)(incl - splits), l)};
-    }
-    before += (uint32_t)__builtin_amdgcn_readlane((int)incl, 63);
-  }
-  return Found{-1, c, before};
+  const uint32_t splits = lane < a.B ? (uint32_t)splits_of(n, c, 1.0f / (float)c) : 0;
+  const uint32_t incl = scan(splits);
+  const uint64_t mask = __ballot(unit < incl);
+  if (!mask) return Found{-1, 0, 0};
+  const int l = __ffsll((unsigned long long)mask) - 1;
+  return Found{l, __builtin_amdgcn_readlane((int)(incl - splits), l), __builtin_amdgcn_readlane((int)splits, l)};
 }
 
 __device__ __forceinline__ ushort2v as_us2(uint32_t v) { return __builtin_bit_cast(ushort2v, v); }
@@ -364,16 +360,22 @@ __global__ __launch_bounds__(64 * kWaves) void attn_kernel(Args a) {
   // Which split this workgroup has.
   const uint32_t nh = (uint32_t)(a.n_kv * a.tiles), unit = blockIdx.x / nh;
   const int hh = (int)(blockIdx.x - unit * nh), kvh = hh % a.n_kv, tile = hh / a.n_kv;
-  const Found f = find_split(a, lane, unit);
-  if (f.b < 0) return;
-  const int b = __builtin_amdgcn_readfirstlane(f.b), c = __builtin_amdgcn_readfirstlane(f.c);
-  const Span sp = span_of(a, b);
-  const int splits = __builtin_amdgcn_readfirstlane(splits_of(sp.n, c, 1.0f / (float)c)), each = (sp.n + splits - 1) / splits;
-  const int mine = (int)(unit - f.first);
-  if (mine == 0 && hh == 0 && threadIdx.x == 0) {
-    a.plan[2 * b] = (int32_t)f.first;
-    a.plan[2 * b + 1] = splits;
+  Found f;
+  if (a.B <= kLanes) {
+    f = find_split(a, lane, unit);
+    if (f.b < 0) return;
+    if ((int)unit == f.first && hh == 0 && threadIdx.x == 0) {
+      a.plan[2 * f.b] = f.first;
+      a.plan[2 * f.b + 1] = f.splits;
+    }
+  } else {
+    if (unit >= (uint32_t)a.units[0]) return;
+    f.b = a.units[1 + unit];
+    f.first = a.plan[2 * f.b], f.splits = a.plan[2 * f.b + 1];
   }
+  const int b = __builtin_amdgcn_readfirstlane(f.b), splits = __builtin_amdgcn_readfirstlane(f.splits);
+  const Span sp = span_of(a, b);
+  const int each = (sp.n + splits - 1) / splits, mine = (int)unit - f.first;
   const int gs = __builtin_amdgcn_readfirstlane(sp.g0 + min(mine * each, sp.n));
   const int ge = __builtin_amdgcn_readfirstlane(sp.g0 + min((mine + 1) * each, sp.n));
 
@@ -700,6 +702,8 @@ __global__ __launch_bounds__(64 * kWaves) void attn_kernel(Args a) {
   }
 }
 
+hipError_t launch_plan(const Args &a, hipStream_t s);
+
 // How many workgroups the GPU holds is looked up once per instantiation (with
 // the most LDS a call uses).
 template <int KK, int VK, int NB, typename QT>
@@ -718,6 +722,10 @@ static hipError_t run(Args &a, hipStream_t s) {
   // Splits of the longest sequences the page table can hold, and of any batch.
   const int64_t nh = a.n_kv * a.tiles, most = a.max_pages * a.page_groups;
   a.items = std::min(2 * a.slots + a.B * nh, a.B * nh * ((most + kMinGroups - 1) / kMinGroups));
+  if (a.B > kLanes) {
+    const hipError_t e = launch_plan(a, s);
+    if (e != hipSuccess) return e;
+  }
   hipLaunchKernelGGL((attn_kernel<KK, VK, NB, QT>), dim3((unsigned)a.items), dim3(64 * kWaves), lds(a.heads), s, a);
   return hipGetLastError();
 }

@@ -5,6 +5,67 @@
 namespace qmm {
 namespace attn {
 
+// The splits of more than 64 sequences, by one workgroup: as find_split, with
+// sums in 64 bits.
+__global__ __launch_bounds__(1024) void plan_kernel(Args a) {
+  __shared__ double dsum[16];
+  __shared__ uint32_t usum[16];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  auto block_sum = [&](double v) {
+#pragma unroll
+    for (int k = 1; k < 64; k <<= 1) v += __shfl_xor(v, k, 64);
+    if (lane == 0) dsum[wave] = v;
+    __syncthreads();
+    v = 0.0;
+    for (int w = 0; w < 16; ++w) v += dsum[w];
+    __syncthreads();
+    return v;
+  };
+  const int nh = a.n_kv * a.tiles;
+  const float slots = (float)a.slots;
+  double v = 0.0;
+  for (int b = tid; b < a.B; b += 1024) v += (double)span_of(a, b).n;
+  const float groups = (float)(block_sum(v) * nh);
+  int c = per_split(groups, 2.0f * slots);
+  if ((int64_t)a.B * nh <= a.slots) {
+    int once = per_split(groups, slots);
+    for (int i = 0; i < 3; ++i) {
+      v = 0.0;
+      for (int b = tid; b < a.B; b += 1024) v += (double)splits_of(span_of(a, b).n, once, 1.0f / (float)once);
+      const float items = (float)(block_sum(v) * nh);
+      if (items <= slots) break;
+      once = fewer(once, items, slots);
+    }
+    c = choose(once, c, groups, slots);
+  }
+  const float inv = 1.0f / (float)c;
+  uint32_t before = 0;
+  for (int b0 = 0; b0 < a.B; b0 += 1024) {
+    const int b = b0 + tid;
+    const uint32_t splits = b < a.B ? (uint32_t)splits_of(span_of(a, b).n, c, inv) : 0;
+    const uint32_t incl = scan(splits);
+    if (lane == 63) usum[wave] = incl;
+    __syncthreads();
+    uint32_t first = before + incl - splits;
+    for (int w = 0; w < 16; ++w) {
+      if (w < wave) first += usum[w];
+      before += usum[w];
+    }
+    if (b < a.B) {
+      a.plan[2 * b] = (int32_t)first;
+      a.plan[2 * b + 1] = (int32_t)splits;
+      for (uint32_t i = 0; i < splits; ++i) a.units[1 + first + i] = b;
+    }
+    __syncthreads();
+  }
+  if (tid == 0) a.units[0] = (int32_t)before;
+}
+
+hipError_t launch_plan(const Args &a, hipStream_t s) {
+  hipLaunchKernelGGL(plan_kernel, dim3(1), dim3(1024), 0, s, a);
+  return hipGetLastError();
+}
+
 // One workgroup per H query heads of a sequence: the splits' parts, weighted by
 // 2^(R_i - max R), over the weighted sums (plus the sink's share).  Sequences
 // of one split were finished by the attention kernel.  256 / H threads of a
@@ -81,7 +142,11 @@ static void launch_join(const Args &a, int D, hipStream_t s) {
   else hipLaunchKernelGGL((join_kernel<QT, 4>), dim3((unsigned)(a.B * ((a.n_q + 3) / 4))), dim3(256), 0, s, a, D);
 }
 
-static size_t plan_bytes(int64_t B) { return (size_t)((B * 8 + 15) / 16 * 16); }
+// The plan and, beyond 64 sequences, the splits' sequences: at most 2 slots /
+// heads + one a sequence of them (per_split).
+static size_t plan_bytes(int64_t B) {
+  return (size_t)((B * 8 + (B > kLanes ? (1 + 2 * kMaxSlots + B) * 4 : 0) + 15) / 16 * 16);
+}
 
 }  // namespace attn
 
@@ -105,6 +170,7 @@ hipError_t launch_attn_decode(const KvCache &kc, const AttnDecode &d, hipStream_
   a.scale2 = d.scale * 1.44269504088896f;
   a.window = d.window, a.sinks = d.sinks, a.out = d.out;
   a.plan = (int32_t *)d.workspace;
+  a.units = a.plan + 2 * d.B;
   a.part = (float *)((uint8_t *)d.workspace + plan_bytes(d.B));
   const int NB = (int)(kc.head_dim / 32);
   hipError_t e = hipErrorInvalidValue;

@@ -334,9 +334,10 @@ def test_attn_window(window, kk, vk):
     check(c.run(dev(q), window=window).cpu().numpy(), *c.want(q, "f16", window=window), f"window={window}")
 
 
-@pytest.mark.parametrize("B", [1, 63, 64, 65, 130, 300])
+@pytest.mark.parametrize("B", [1, 2, 63, 64, 65, 130, 300, 1500])
 def test_attn_many_sequences(B):
-    """Counts of sequences around the 64 that one pass over the lengths covers, most of them short, one long."""
+    """Counts of sequences around the 64 that a wave plans and the 1024 that a workgroup plans at a time, most of them
+    short, one long."""
     g = wl.rng("attn", f"many{B}")
     lens = [int(x) for x in g.integers(0, 70, B)]
     lens[B // 2] = 3000
