@@ -723,7 +723,7 @@ def _freqs_arg(freqs) -> int:
 
 def _new(shape, dtype, like, stream):
     """An operand allocated for the call, kept from reuse while `stream` has it."""
-    t = _torch.empty(shape, dtype=dtype, device=like.device)
+    t = like.new_empty(shape) if dtype is like.dtype else like.new_empty(shape, dtype=dtype)
     if stream is not None:
         t.record_stream(stream)
     return t

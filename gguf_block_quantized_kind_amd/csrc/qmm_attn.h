@@ -108,14 +108,17 @@ struct Args {
 struct Span {
   int lo, len, g0, n;
 };
-__device__ __forceinline__ Span span_of(const Args &a, int b) {
+__device__ __forceinline__ int length_of(const Args &a, int b) {
   const int64_t most = a.max_pages * a.page_groups * kv::kGroup;
-  int len = b < a.B ? max(a.lens[b], 0) : 0;
-  if (len > most) len = (int)most;
+  const int len = b < a.B ? max(a.lens[b], 0) : 0;
+  return len > most ? (int)most : len;
+}
+__device__ __forceinline__ Span span_at(const Args &a, int len) {
   const int lo = a.window > 0 && len > a.window ? len - (int)a.window : 0;
   const int g0 = lo / kv::kGroup;
   return Span{lo, len, g0, len > 0 ? (int)(((int64_t)len + kv::kGroup - 1) / kv::kGroup) - g0 : 0};
 }
+__device__ __forceinline__ Span span_of(const Args &a, int b) { return span_at(a, length_of(a, b)); }
 
 // Reductions over the four lane groups G of a column (lanes j, 16 + j, 32 + j,
 // 48 + j), every lane receiving the result: each swap exchanges rows of 16 or
@@ -159,7 +162,7 @@ __device__ __forceinline__ uint32_t scan(uint32_t v) {
 // are planned by plan_kernel, once, before.
 constexpr int kLanes = 64;
 struct Found {
-  int b, first, splits;
+  int b, first, splits, len;
 };
 // At least groups / splits (in f32, rounded up past its errors).
 __device__ __forceinline__ int per_split(float groups, float splits) {
@@ -182,13 +185,13 @@ __device__ __forceinline__ int choose(int once, int twice, float groups, float s
 __device__ __forceinline__ int fewer(int c, float items, float slots) { return (int)((float)c * (items / slots)) + 1; }
 
 __device__ __forceinline__ Found find_split(const Args &a, int lane, uint32_t unit) {
-  const int nh = a.n_kv * a.tiles;
-  int n = span_of(a, lane).n;
+  const int nh = a.n_kv * a.tiles, len = length_of(a, lane);
+  int n = span_at(a, len).n;
   if (a.B == 1) {
     n = __builtin_amdgcn_readfirstlane(n);
     const int most = max(a.slots / nh, 1), c = max((n + most - 1) / most, kMinGroups);
     const int splits = splits_of(n, c, 1.0f / (float)c);
-    return Found{unit < (uint32_t)splits ? 0 : -1, 0, splits};
+    return Found{unit < (uint32_t)splits ? 0 : -1, 0, splits, __builtin_amdgcn_readfirstlane(len)};
   }
   // (At most 2^26 groups a sequence: one less keeps 64 of them below 2^32.)
   const uint32_t total = (uint32_t)__builtin_amdgcn_readlane((int)scan((uint32_t)min(n, (1 << 26) - 1)), 63);
@@ -209,9 +212,10 @@ __device__ __forceinline__ Found find_split(const Args &a, int lane, uint32_t un
   const uint32_t splits = lane < a.B ? (uint32_t)splits_of(n, c, 1.0f / (float)c) : 0;
   const uint32_t incl = scan(splits);
   const uint64_t mask = __ballot(unit < incl);
-  if (!mask) return Found{-1, 0, 0};
+  if (!mask) return Found{-1, 0, 0, 0};
   const int l = __ffsll((unsigned long long)mask) - 1;
-  return Found{l, __builtin_amdgcn_readlane((int)(incl - splits), l), __builtin_amdgcn_readlane((int)splits, l)};
+  return Found{l, __builtin_amdgcn_readlane((int)(incl - splits), l), __builtin_amdgcn_readlane((int)splits, l),
+               __builtin_amdgcn_readlane(len, l)};
 }
 
 __device__ __forceinline__ ushort2v as_us2(uint32_t v) { return __builtin_bit_cast(ushort2v, v); }
@@ -371,10 +375,10 @@ __global__ __launch_bounds__(64 * kWaves) void attn_kernel(Args a) {
   } else {
     if (unit >= (uint32_t)a.units[0]) return;
     f.b = a.units[1 + unit];
-    f.first = a.plan[2 * f.b], f.splits = a.plan[2 * f.b + 1];
+    f.first = a.plan[2 * f.b], f.splits = a.plan[2 * f.b + 1], f.len = length_of(a, f.b);
   }
   const int b = __builtin_amdgcn_readfirstlane(f.b), splits = __builtin_amdgcn_readfirstlane(f.splits);
-  const Span sp = span_of(a, b);
+  const Span sp = span_at(a, __builtin_amdgcn_readfirstlane(f.len));
   const int each = (sp.n + splits - 1) / splits, mine = (int)unit - f.first;
   const int gs = __builtin_amdgcn_readfirstlane(sp.g0 + min(mine * each, sp.n));
   const int ge = __builtin_amdgcn_readfirstlane(sp.g0 + min((mine + 1) * each, sp.n));
