@@ -76,7 +76,8 @@ typedef float floatx4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
-constexpr float kFloor = -1e30f;  // R of no tokens
+constexpr float kFloor = -3e38f;  // R of no tokens
+constexpr float kFar = 0x1p20f;  // scores whose products are rounded by more than 2^-5
 constexpr int kWaves = 4;
 constexpr int kMinGroups = 4;  // groups per split at least: one per wave
 constexpr int kMaxSlots = 1280;  // most workgroups counted on at once (five on each of 256 compute units)
@@ -466,6 +467,10 @@ __global__ __launch_bounds__(64 * kWaves) void attn_kernel(Args a) {
       up *= __builtin_bit_cast(float, (uint32_t)(127 + e) << 23);
       qscale *= __builtin_bit_cast(float, (uint32_t)(127 - e) << 23);
       if constexpr (SUB) qscale *= 0x1p24f;
+      // Products lie below 2^42 and differ by 2^-32 or more: past these limits
+      // all scores are 0, or all but the largest far below it, as without
+      // them, and none overflows.
+      qscale = fminf(fmaxf(qscale, 0x1p-126f), 0x1p80f);
     }
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
@@ -562,9 +567,8 @@ __global__ __launch_bounds__(64 * kWaves) void attn_kernel(Args a) {
 #pragma unroll
     for (int k = 1; k < 8; ++k) top = fmaxf(top, s[k]);
     top *= qscale;
-    if constexpr (VK == C_F16) {
-      top -= 14.0f;
-    } else {
+    float below = 14.0f;  // 14 - the exponent of the largest value scale
+    if constexpr (VK != C_F16) {
       // Magnitudes of halves compare as integers (Q8_0 scales have no sign).
       ushort2v part[4] = {{0, 0}, {0, 0}, {0, 0}, {0, 0}};
 #pragma unroll
@@ -589,8 +593,11 @@ __global__ __launch_bounds__(64 * kWaves) void attn_kernel(Args a) {
       const half2v big = as_h2(as_u(most));
       // 2^e <= scale < 2^(e + 1); f16 scales are 0 or at least 2^-24.
       const float bf = fmaxf(fmaxf((float)big[0], (float)big[1]), 0x1p-24f);
-      top += (float)((int)(__builtin_bit_cast(uint32_t, bf) >> 23) - 127 - 14);
+      below = (float)(127 + 14 - (int)(__builtin_bit_cast(uint32_t, bf) >> 23));
     }
+    // (Among scores whose f32 neighbours lie further apart than `below` means,
+    // the reference is the score itself: weights up to 1, not 2^14.)
+    top = fabsf(top) < kFar ? top - below : top;
     top = max_over_groups(top);
     if (__any(top > R)) {  // rare after the first groups
       const float Rn = fmaxf(R, top), alpha = __builtin_amdgcn_exp2f(R - Rn);
@@ -602,11 +609,17 @@ __global__ __launch_bounds__(64 * kWaves) void attn_kernel(Args a) {
         for (int x = 0; x < 2; ++x) acc[n][x] *= alpha;
     }
     float p[8];
+    if (__any(fabsf(R) >= kFar)) {
+      // The score rounded as the reference was: what the product's rounding
+      // leaves, itself large here, must not become a weight.
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      p[k] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[k], qscale, -R));
-      sum += p[k];
+      for (int k = 0; k < 8; ++k) p[k] = __builtin_amdgcn_exp2f(kv::in_f32(s[k] * qscale) - R);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) p[k] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[k], qscale, -R));
     }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sum += p[k];
 
     half8 ph, pl;
     if constexpr (VK == C_F16) {

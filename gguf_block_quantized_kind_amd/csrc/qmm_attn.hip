@@ -73,7 +73,7 @@ hipError_t launch_plan(const Args &a, hipStream_t s) {
 // D / 4 lanes, so that a sequence of a thousand splits costs no chain of a
 // thousand loads.  H = 1 spreads few heads with many splits over the GPU (32
 // heads of 96 splits 5 us), H = 4 makes fewer workgroups of many heads with few
-// splits (3072 heads of 3 splits 7.5 -> 4.7 us).
+// splits (48 sequences of 64 heads, 3 splits: 7.5 -> 4.7 us).
 template <typename QT, int H>
 __global__ __launch_bounds__(256) void join_kernel(Args a, int D) {
   constexpr int kThreads = 256 / H, kChunk = 1024 / H;

@@ -449,6 +449,35 @@ def test_attn_extreme_queries_and_sinks(kk, vk):
     check(c.run(dev(q), sinks=dev(sinks)).cpu().numpy(), *c.want(q, "f32", sinks=sinks), "far below one")
 
 
+@pytest.mark.parametrize("kk,vk", PAIRS)
+@pytest.mark.parametrize("dt,size", [("f16", 2.0 ** 12), ("f32", 2.0 ** 16), ("f32", 2.0 ** 60), ("f32", 2.0 ** 100)])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_attn_far_scores_pick_one_token(kk, vk, dt, size, sign):
+    """Scores whose f32 neighbours are far apart: all the weight is on the largest (the next one lies below it by more
+    than both errors and 100), which has the exact weight 1."""
+    c = Case(kk, vk, 64, 64, 1, [1, 40, 150, 333], spread=300.0)
+    q = (c.g.normal(size=(4, 3, 64)) * size).astype(NP[dt])
+    got = c.run(dev(q), scale=sign * 0.125).cpu().numpy()
+    want = np.zeros(q.shape)
+    for b in range(4):
+        k, v = c.kx[c.first[b]:c.first[b + 1], 0], c.vx[c.first[b]:c.first[b + 1], 0]
+        for h in range(3):
+            s = sign * 0.125 * (k @ q[b, h].astype(np.float64))
+            e = 2.0 ** -17 * (0.125 * np.abs(q[b, h].astype(np.float64)).reshape(2, 32).sum(-1)
+                              @ np.abs(k).reshape(-1, 2, 32).max(-1).T + np.abs(s) + 40)
+            top = np.argmax(s)
+            assert np.all(np.delete(s + e, top) + 100 < s[top] - e[top])
+            want[b, h] = v[top]
+    check(got, want, 2.0 ** (-11 if dt == "f16" else -18) * np.abs(want) + half_step(want, dt), "out")
+
+
+@pytest.mark.parametrize("kk,vk", [("F16", "F16"), ("Q8_0", "Q8_0"), ("Q4_0", "Q4_0")])
+def test_attn_vanishing_scores(kk, vk):
+    c = Case(kk, vk, 64, 64, 1, [1, 0, 40, 150])
+    q = (c.g.normal(size=(4, 3, 64)) * 2.0 ** -115).astype(np.float32)
+    check(c.run(dev(q), scale=2.0 ** -40).cpu().numpy(), *c.want(q, "f32", scale=2.0 ** -40), "out")
+
+
 @pytest.mark.parametrize("vk", ["F16", "Q8_0", "Q4_0"])
 def test_attn_nonfinite_value_stays_in_its_elements(vk):
     """A NaN in an attended value reaches the elements that share its place (its block of a quantized kind) and no
