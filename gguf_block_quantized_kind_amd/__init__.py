@@ -722,10 +722,14 @@ def _freqs_arg(freqs) -> int:
 
 
 def _new(shape, dtype, like, stream):
-    """An operand allocated for the call, kept from reuse while `stream` has it."""
-    t = like.new_empty(shape) if dtype is like.dtype else like.new_empty(shape, dtype=dtype)
-    if stream is not None:
-        t.record_stream(stream)
+    """An operand allocated for the call, of `stream`'s memory if it runs there
+    (the current stream's free memory may still be in use by its pending work),
+    kept from reuse until both streams are done with it."""
+    if stream is None:
+        return like.new_empty(shape) if dtype is like.dtype else like.new_empty(shape, dtype=dtype)
+    with _torch.cuda.stream(stream):
+        t = like.new_empty(shape, dtype=dtype)
+    t.record_stream(_torch.cuda.current_stream(like.device))
     return t
 
 

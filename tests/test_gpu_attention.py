@@ -516,6 +516,23 @@ def test_two_streams_at_once():
 
 
 # -- the operators together ----------------------------------------------------------
+def test_outputs_of_a_call_on_another_stream_are_its_own():
+    """Memory that the current stream's pending work still writes is not handed to a call on another stream."""
+    T, H, D = 1000, 7, 128
+    x = dev(wl.rng("stream", "own").normal(size=(T, H, D)).astype(np.float32))
+    pos, (freqs, m) = dev(np.arange(T, dtype=np.int32)), qmm.rope_freqs(D)
+    want = qmm.rope(x, pos, freqs, mscale=m).clone()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    late = torch.empty_like(x)
+    torch.cuda._sleep(50_000_000)
+    late.fill_(5.0)
+    del late
+    got = qmm.rope(x, pos, freqs, mscale=m, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+
+
 def test_decode_steps_through_a_layer(oracle_mod):
     """Prompt, then decode steps: q, k, v from a Q4_0 projection (qmm_matmul), append, attention, output projection.
     Each part against its definition on the previous part's actual output."""
