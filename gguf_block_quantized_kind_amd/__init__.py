@@ -17,7 +17,6 @@ key/value cache of ``kv_pages`` tensors.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -92,24 +91,8 @@ def load_library(path: str = LIBRARY) -> ctypes.CDLL:
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
         fn.restype, fn.argtypes = res, args
-    _bind_calls(lib)
     _lib = lib
     return lib
-
-
-# The entry points a decode step calls once per layer, through _qmm_call (built
-# with the library) instead of ctypes: name -> function.
-_calls = {}
-
-
-def _bind_calls(lib):
-    try:
-        from . import _qmm_call
-    except ImportError as e:
-        raise RuntimeError("the _qmm_call module is not built; run __graft_entry__.build() first") from e
-    for name in ("qmm_rope", "qmm_kv_write", "qmm_kv_append", "qmm_kv_read", "qmm_attn_decode"):
-        _qmm_call.bind(name, ctypes.cast(getattr(lib, name), ctypes.c_void_p).value)
-        _calls[name] = getattr(_qmm_call, name)
 
 
 def _check(status: int):
@@ -605,87 +588,46 @@ def _layout_id(layout) -> int:
     return int(layout)
 
 
-# These calls run once per layer and token, where the host's time is what a
-# small step waits for: sizes that are functions of their arguments alone are
-# looked up once, and the checks below read each tensor property once.
-_torch = None        # set by the first call
-_DTYPE_CODES = {}
+# Checks, allocation and the C calls on tensors are in the _qmm_call module
+# (built with the library): these calls run once per layer and token, where the
+# host's time is what a small step waits for.
+_ops = None
 
 
-def _load_torch():
-    global _torch
+def _load_ops():
+    global _ops
+    import torch  # noqa: F401  (whose libraries the module uses)
+    try:
+        from . import _qmm_call
+    except ImportError as e:
+        raise RuntimeError("the _qmm_call module is not built; run __graft_entry__.build() first") from e
+    lib = load_library()
+    names = ("qmm_rope", "qmm_kv_write", "qmm_kv_append", "qmm_kv_read", "qmm_attn_decode",
+             "qmm_attn_decode_workspace_bytes", "qmm_kv_page_bytes")
+    _qmm_call.setup({n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names}, _check, cache_kind_id,
+                    _layout_id)
+    _ops = _qmm_call
+    return _ops
+
+
+def _on(stream, like, fn, *args):
+    """fn(*args) on `stream`.  What it allocates is of that stream's memory (the
+    current stream's free memory may still be in use by its pending work), kept
+    from reuse until both streams are done with it."""
     import torch
-    _DTYPE_CODES.update({torch.float32: QMM_F32, torch.float16: QMM_F16})
-    _torch = torch
-    return torch
-
-
-def _code(t) -> int:
-    return _DTYPE_CODES.get(t.dtype, 99)  # 99: refused by the library as a bad dtype
-
-
-@functools.lru_cache(maxsize=256)
-def _page_bytes(kind: int, page_size: int, n_kv: int, head_dim: int) -> int:
-    return int(load_library().qmm_kv_page_bytes(kind, page_size, n_kv, head_dim))
-
-
-def _rows_arg(x, what: str) -> tuple[int, int, int, int]:
-    """T, heads, head_dim and row stride of [T, heads, head_dim] rows."""
-    shape = x.shape
-    if len(shape) != 3:
-        raise ValueError(f"{what} must be [rows, heads, head_dim], got {tuple(shape)}")
-    T, H, D = shape
-    st, sh, sd = x.stride()
-    if (D > 1 and sd != 1) or (H > 1 and sh != D):
-        raise ValueError(f"the heads of a row of {what} must be packed, got strides {x.stride()}")
-    return T, H, D, st if T > 1 else H * D
-
-
-def _ints(t, count: int, what: str):
-    if t.dtype is not (_torch or _load_torch()).int32:
-        raise TypeError(f"{what} must be int32, got {t.dtype}")
-    if t.numel() != count or not t.is_contiguous():
-        raise ValueError(f"{what} must hold {count} contiguous elements, got {tuple(t.shape)}")
-
-
-def _pages_arg(pages, kind: int, page_size: int, n_kv: int, head_dim: int, what: str) -> int:
-    """Number of pages of a page tensor."""
-    shape = pages.shape
-    if len(shape) != 2 or pages.element_size() != 1 or not pages.is_contiguous():
-        raise TypeError(f"{what} must be a contiguous byte tensor [n_pages, page_bytes]")
-    pb = _page_bytes(kind, page_size, n_kv, head_dim)
-    if pb > 0 and shape[1] != pb:
-        raise ValueError(f"{what} has pages of {shape[1]} bytes, page_size={page_size}, n_kv={n_kv} and "
-                         f"head_dim={head_dim} need {pb}")
-    return shape[0]
-
-
-def _call(name: str, stream, tensors, *args):
-    """Calls a C entry point on the operands' device (made the current one for
-    the call), refusing operands on the host or on different devices; its last
-    argument is the stream, by default that device's current one."""
-    torch = _torch
-    index = tensors[0].get_device()
-    for t in tensors:
-        if t is not None and t.get_device() != index or index < 0:
-            raise ValueError(f"operands must be on one GPU, got {t.device} with {tensors[0].device}")
-    s = torch._C._cuda_getCurrentRawStream(index) if stream is None else int(stream.cuda_stream)
-    fn = _calls.get(name)
-    if fn is None:
-        load_library()
-        fn = _calls[name]
-    before = torch._C._cuda_getDevice()
-    if before == index:
-        status = fn(*args, s)
-    else:
-        with torch.cuda.device(index):
-            status = fn(*args, s)
-    if status:
-        _check(status)
+    if like.device != stream.device:
+        raise ValueError(f"operands on {like.device}, stream on {stream.device}")
+    here = torch.cuda.current_stream(like.device)
+    with torch.cuda.stream(stream):
+        got = fn(*args)
+    for t in got if isinstance(got, tuple) else (got,):
+        if t is not None and not any(t is a for a in args):
+            t.record_stream(here)
+    return got
 
 
 def kv_page_bytes(kind, page_size: int, n_kv: int, head_dim: int) -> int:
-    return _page_bytes(cache_kind_id(kind), page_size, n_kv, head_dim)
+    return int(load_library().qmm_kv_page_bytes(cache_kind_id(kind), page_size, n_kv, head_dim))
 
 
 def kv_pages(kind, n_pages: int, page_size: int, n_kv: int, head_dim: int, device="cuda"):
@@ -715,115 +657,45 @@ def rope_freqs(n_rot: int, base: float = 10000.0, factors=None, factor: float = 
     return out.to(device), float(m.value)
 
 
-def _freqs_arg(freqs) -> int:
-    if freqs.dtype is not _torch.float64 or freqs.dim() != 1 or not freqs.is_contiguous():
-        raise TypeError(f"freqs must be a contiguous float64 vector, got {freqs.dtype} {tuple(freqs.shape)}")
-    return 2 * freqs.numel()
-
-
-def _new(shape, dtype, like, stream):
-    """An operand allocated for the call, of `stream`'s memory if it runs there
-    (the current stream's free memory may still be in use by its pending work),
-    kept from reuse until both streams are done with it."""
-    if stream is None:
-        return like.new_empty(shape) if dtype is like.dtype else like.new_empty(shape, dtype=dtype)
-    with _torch.cuda.stream(stream):
-        t = like.new_empty(shape, dtype=dtype)
-    t.record_stream(_torch.cuda.current_stream(like.device))
-    return t
-
-
-def _out_arg(out, shape, dtype, like, stream) -> tuple:
-    """`out`, allocated if None, and its row stride."""
-    if out is None:
-        return _new(shape, dtype or like.dtype, like, stream), shape[1] * shape[2]
-    T, H, D, stride = _rows_arg(out, "out")
-    if (T, H, D) != shape:
-        raise ValueError(f"out is {tuple(out.shape)}, needs {shape}")
-    return out, stride
-
-
 def rope(x, positions, freqs, layout="half", mscale: float = 1.0, out=None, out_dtype=None, stream=None):
     """x [T, H, head_dim] with the first 2 * len(freqs) elements of each head
     turned by positions [T] int32; out may be x."""
-    T, H, D, xs = _rows_arg(x, "x")
-    _ints(positions, T, "positions")
-    out, ys = _out_arg(out, (T, H, D), out_dtype, x, stream)
-    _call("qmm_rope", stream, (x, positions, freqs, out), freqs.data_ptr(), _freqs_arg(freqs), _layout_id(layout), mscale,
-          positions.data_ptr(), x.data_ptr(), _code(x), xs, out.data_ptr(), _code(out), ys, T, H, D)
-    return out
-
-
-def _kv_args(k, v, slots):
-    T, n_kv, D, ks = _rows_arg(k, "k")
-    Tv, Hv, Dv, vs = _rows_arg(v, "v")
-    if Tv != T or Hv != n_kv or Dv != D:
-        raise ValueError(f"k is {tuple(k.shape)}, v is {tuple(v.shape)}")
-    if k.dtype is not v.dtype:
-        raise TypeError(f"k is {k.dtype}, v is {v.dtype}")
-    _ints(slots, T, "slots")
-    return T, n_kv, D, ks, vs
-
-
-def _cache_args(k_pages, v_pages, k_kind, v_kind, page_size: int, n_kv: int, D: int):
-    kk, vk = CACHE_KINDS.get(k_kind) or cache_kind_id(k_kind), CACHE_KINDS.get(v_kind) or cache_kind_id(v_kind)
-    n = _pages_arg(k_pages, kk, page_size, n_kv, D, "k_pages")
-    if _pages_arg(v_pages, vk, page_size, n_kv, D, "v_pages") != n:
-        raise ValueError(f"k_pages holds {n} pages, v_pages {v_pages.shape[0]}")
-    return kk, vk, k_pages.data_ptr(), v_pages.data_ptr(), n, page_size, n_kv, D
+    fn = (_ops or _load_ops()).rope
+    if stream is not None:
+        return _on(stream, x, fn, x, positions, freqs, layout, mscale, out, out_dtype)
+    return fn(x, positions, freqs, layout, mscale, out, out_dtype)
 
 
 def kv_write(k, v, slots, k_pages, v_pages, k_kind, v_kind, page_size: int, stream=None):
     """Writes the tokens' keys and values [T, n_kv, head_dim] to slots [T] int32."""
-    T, n_kv, D, ks, vs = _kv_args(k, v, slots)
-    cache = _cache_args(k_pages, v_pages, k_kind, v_kind, page_size, n_kv, D)
-    _call("qmm_kv_write", stream, (k, v, slots, k_pages, v_pages), *cache, k.data_ptr(), ks, v.data_ptr(), vs,
-          _code(k), slots.data_ptr(), T)
+    fn = (_ops or _load_ops()).kv_write
+    if stream is not None:
+        return _on(stream, k, fn, k, v, slots, k_pages, v_pages, k_kind, v_kind, page_size)
+    return fn(k, v, slots, k_pages, v_pages, k_kind, v_kind, page_size)
 
 
 def kv_append(q, k, v, positions, slots, k_pages, v_pages, k_kind, v_kind, page_size: int, freqs, layout="half",
               mscale: float = 1.0, out=None, out_dtype=None, stream=None):
     """Rotates q [T, n_q, head_dim] (returned; out may be q) and k, and writes
     k and v to their slots, in one launch."""
-    T, n_kv, D, ks, vs = _kv_args(k, v, slots)
-    Tq, n_q, Dq, qs = _rows_arg(q, "q")
-    if Tq != T or Dq != D:
-        raise ValueError(f"q is {tuple(q.shape)}, k is {tuple(k.shape)}")
-    if q.dtype is not k.dtype:
-        raise TypeError(f"q is {q.dtype}, k is {k.dtype}")
-    _ints(positions, T, "positions")
-    cache = _cache_args(k_pages, v_pages, k_kind, v_kind, page_size, n_kv, D)
-    out, os_ = _out_arg(out, (T, n_q, D), out_dtype, q, stream)
-    _call("qmm_kv_append", stream, (q, k, v, positions, slots, k_pages, v_pages, freqs, out), freqs.data_ptr(),
-          _freqs_arg(freqs), _layout_id(layout), mscale, positions.data_ptr(), q.data_ptr(), qs, n_q, out.data_ptr(),
-          _code(out), os_, *cache, k.data_ptr(), ks, v.data_ptr(), vs, _code(k), slots.data_ptr(), T)
-    return out
+    fn = (_ops or _load_ops()).kv_append
+    if stream is not None:
+        return _on(stream, q, fn, q, k, v, positions, slots, k_pages, v_pages, k_kind, v_kind, page_size, freqs, layout,
+                   mscale, out, out_dtype)
+    return fn(q, k, v, positions, slots, k_pages, v_pages, k_kind, v_kind, page_size, freqs, layout, mscale, out, out_dtype)
 
 
 def kv_read(slots, k_pages, v_pages, k_kind, v_kind, page_size: int, n_kv: int, head_dim: int, dtype=None, k_out=None,
             v_out=None, stream=None):
     """(k, v) [T, n_kv, head_dim] of the tokens at slots [T] int32, f16 by
     default; zeros for skipped slots (outside the cache)."""
-    torch = _torch or _load_torch()
-    T = slots.numel()
-    _ints(slots, T, "slots")
-    shape = (T, n_kv, head_dim)
-    if (k_out is None) != (v_out is None):
-        raise ValueError("k_out and v_out go together")
-    if k_out is None:
-        dtype = dtype or torch.float16
-        k_out, v_out = _new(shape, dtype, slots, stream), _new(shape, dtype, slots, stream)
-    else:
-        for t in (k_out, v_out):
-            if tuple(t.shape) != shape or not t.is_contiguous() or t.dtype is not k_out.dtype:
-                raise ValueError(f"k_out and v_out must be contiguous {shape} of one type")
-    cache = _cache_args(k_pages, v_pages, k_kind, v_kind, page_size, n_kv, head_dim)
-    _call("qmm_kv_read", stream, (slots, k_pages, v_pages, k_out, v_out), *cache, slots.data_ptr(), T, k_out.data_ptr(),
-          v_out.data_ptr(), _code(k_out))
-    return k_out, v_out
+    fn = (_ops or _load_ops()).kv_read
+    if stream is not None:
+        return _on(stream, slots, fn, slots, k_pages, v_pages, k_kind, v_kind, page_size, n_kv, head_dim, dtype, k_out,
+                   v_out)
+    return fn(slots, k_pages, v_pages, k_kind, v_kind, page_size, n_kv, head_dim, dtype, k_out, v_out)
 
 
-@functools.lru_cache(maxsize=1024)
 def qmm_attn_decode_workspace_bytes(B: int, n_q: int, n_kv: int, head_dim: int) -> int:
     return int(load_library().qmm_attn_decode_workspace_bytes(B, n_q, n_kv, head_dim))
 
@@ -835,30 +707,9 @@ def attn_decode(q, k_pages, v_pages, block_table, seq_lens, k_kind, v_kind, page
     seq_lens [B] int32 tokens.  scale defaults to head_dim^-0.5; window > 0
     keeps the last `window` tokens; sinks [n_q] f32 adds a logit without a
     value per head."""
-    torch = _torch or _load_torch()
-    B, n_q, D, qs = _rows_arg(q, "q")
-    _ints(seq_lens, B, "seq_lens")
-    shape = block_table.shape
-    if len(shape) != 2 or shape[0] != B:
-        raise ValueError(f"block_table must be [{B}, max_pages], got {tuple(shape)}")
-    max_pages = shape[1]
-    _ints(block_table, B * max_pages, "block_table")
-    if sinks is not None and (sinks.dtype is not torch.float32 or not sinks.is_contiguous() or sinks.numel() != n_q):
-        raise ValueError(f"sinks must be {n_q} contiguous float32 values")
-    cache = _cache_args(k_pages, v_pages, k_kind, v_kind, page_size, n_kv, D)
-    if out is None:
-        out = _new((B, n_q, D), q.dtype, q, stream)
-    elif tuple(out.shape) != (B, n_q, D) or not out.is_contiguous() or out.dtype is not q.dtype:
-        raise ValueError(f"out must be contiguous {(B, n_q, D)} of q's type")
-    if workspace is None:
-        nbytes = qmm_attn_decode_workspace_bytes(B, n_q, n_kv, D)
-        workspace = _new(max(nbytes, 1), torch.uint8, q, stream)
-    else:
-        nbytes = workspace.numel() * workspace.element_size()
-        if not workspace.is_contiguous():
-            raise ValueError("workspace must be contiguous")
-    _call("qmm_attn_decode", stream, (q, k_pages, v_pages, block_table, seq_lens, sinks, out, workspace), *cache,
-          q.data_ptr(), _code(q), qs, n_q, block_table.data_ptr(), max_pages, seq_lens.data_ptr(), B,
-          D ** -0.5 if scale is None else scale, window, 0 if sinks is None else sinks.data_ptr(), out.data_ptr(),
-          workspace.data_ptr(), nbytes)
-    return out
+    fn = (_ops or _load_ops()).attn_decode
+    if stream is not None:
+        return _on(stream, q, fn, q, k_pages, v_pages, block_table, seq_lens, k_kind, v_kind, page_size, n_kv, scale, window,
+                   sinks, out, workspace)
+    return fn(q, k_pages, v_pages, block_table, seq_lens, k_kind, v_kind, page_size, n_kv, scale, window, sinks, out,
+              workspace)

@@ -22,8 +22,8 @@ LIBRARY = os.path.join(HERE, "libqmm.so")
 # library; not part of the matmul C ABI).
 PROBE_SOURCE = os.path.join(CSRC, "probe", "qmm_stream_read.hip")
 PROBE_LIBRARY = os.path.join(HERE, "libqmm_probe.so")
-# The CPython calls of the entry points made once per layer (host code only).
-CALL_SOURCE = os.path.join(CSRC, "bind", "qmm_call.c")
+# The calls on torch tensors of the entry points made once per layer (host code only).
+CALL_SOURCE = os.path.join(CSRC, "bind", "qmm_call.cpp")
 CALL_MODULE = os.path.join(HERE, "_qmm_call" + sysconfig.get_config_var("EXT_SUFFIX"))
 OBJDIR = os.path.join(ROOT, "_build")
 ARCH = "gfx950"
@@ -94,11 +94,16 @@ def build_probe(cc: str) -> str:
 
 
 def build_call() -> str:
+    from torch.utils import cpp_extension
+    includes = [*cpp_extension.include_paths(), sysconfig.get_paths()["include"], "/opt/rocm/include"]
+    torch_lib = os.path.join(os.path.dirname(includes[0]), "lib")
     tmp = CALL_MODULE + ".tmp"
-    r = subprocess.run(["gcc", "-O2", "-shared", "-fPIC", "-Wall", "-I", sysconfig.get_paths()["include"], CALL_SOURCE, "-o", tmp],
+    r = subprocess.run(["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-Wall",
+                        "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM", *(x for i in includes for x in ("-isystem", i)),
+                        CALL_SOURCE, "-o", tmp, "-L", torch_lib, "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_python"],
                        capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"gcc failed on {CALL_SOURCE}:\n{r.stderr}")
+        raise RuntimeError(f"g++ failed on {CALL_SOURCE}:\n{r.stderr}")
     os.replace(tmp, CALL_MODULE)
     return CALL_MODULE
 

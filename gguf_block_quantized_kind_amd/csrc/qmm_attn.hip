@@ -187,6 +187,9 @@ hipError_t launch_attn_decode(const KvCache &kc, const AttnDecode &d, hipStream_
   QMM_CASE(C_Q4_0, C_Q4_0, launch_q4_q4)
 #undef QMM_CASE
   if (e != hipSuccess) return e;
+  // (A table of at most one split's tokens: the attention kernel has finished
+  // every sequence.)
+  if (a.max_pages * a.page_groups <= kMinGroups) return hipSuccess;
   if (d.f16) launch_join<_Float16>(a, (int)kc.head_dim, s);
   else launch_join<float>(a, (int)kc.head_dim, s);
   return hipGetLastError();

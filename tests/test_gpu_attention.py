@@ -386,6 +386,16 @@ def test_attn_strong_and_tiny_values(kk, vk):
             check(got.cpu().numpy(), *c.want(q, "f16", scale=scale, sinks=sinks), f"{amount} {scale}")
 
 
+@pytest.mark.parametrize("P,wide", [(32, 1), (32, 4), (64, 2), (128, 1), (32, 5)])
+@pytest.mark.parametrize("B", [1, 3, 70])
+def test_attn_small_tables(P, wide, B):
+    """Tables of one split's tokens, and of one page more."""
+    full = P * wide
+    c = Case("Q8_0", "Q8_0", 64, P, 2, ([full, 1, full - 1] * 24)[:B], seed=str(wide), wide=wide)
+    q = c.g.normal(size=(B, 6, 64)).astype(np.float16)
+    check(c.run(dev(q)).cpu().numpy(), *c.want(q, "f16"), "out")
+
+
 def test_attn_lengths_beyond_the_table_and_bad_pages():
     """Lengths are cut to the table, negative ones are empty, pages outside the cache count as absent."""
     c = Case("Q8_0", "Q4_0", 64, 32, 2, [96, 70, 200, 33], wide=7)

@@ -288,3 +288,28 @@ def test_python_checks_before_the_library():
         qmm.kv_pages("Q8_0", 3, 48, 2, 128, device="cpu")
     with pytest.raises(ValueError):
         qmm.rope_freqs(8, factors=[1.0], device="cpu")
+
+
+def test_python_checks_of_other_operands(lib):
+    torch = pytest.importorskip("torch")
+    x = torch.zeros((3, 2, 64), dtype=torch.float16)
+    pos, (f, m) = torch.arange(3, dtype=torch.int32), qmm.rope_freqs(64, device="cpu")
+    for bad, error in [((x.numpy(), pos, f), TypeError), ((x[0], pos, f), ValueError), ((x, pos.long(), f), TypeError),
+                       ((x, pos[:2], f), ValueError), ((x, pos, f.float()), TypeError), ((x, None, f), TypeError),
+                       ((x, pos, f, "other"), qmm.QmmError), ((x, pos, f, "half", "1"), TypeError),
+                       ((x, pos, f), ValueError)]:                      # the last: host tensors
+        with pytest.raises(error):
+            qmm.rope(*bad)
+    kp = torch.zeros((4, qmm.kv_page_bytes("F16", 32, 2, 64)), dtype=torch.uint8)
+    table, lens = torch.zeros((3, 2), dtype=torch.int32), torch.ones(3, dtype=torch.int32)
+    good = [x, kp, kp, table, lens, "F16", "F16", 32, 2]
+    for at, value, error in [(3, table[:2], ValueError), (3, table.long(), TypeError), (4, lens[:2], ValueError),
+                             (1, kp[:, :-1], TypeError), (1, kp[:3], ValueError), (7, 64, ValueError), (8, 3, ValueError),
+                             (8, 2.5, TypeError), (5, "Q6_K", qmm.QmmError), (0, x, ValueError)]:
+        with pytest.raises(error):
+            qmm.attn_decode(*good[:at], value, *good[at + 1:])
+    for kw in (dict(sinks=torch.zeros(3)), dict(out=x[:1]), dict(window="a"), dict(workspace=1)):
+        with pytest.raises((ValueError, TypeError)):
+            qmm.attn_decode(*good, **kw)
+    with pytest.raises(TypeError):
+        qmm._load_ops().rope(x)                                         # too few arguments
