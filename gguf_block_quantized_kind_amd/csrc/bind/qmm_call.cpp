@@ -2,7 +2,7 @@
 // tensors: checks of the operands, sizes from their shapes, allocation of
 // outputs, and the C entry point on the operands' device and its current
 // stream.  In C++ because the host's time is what a small step waits for: the
-// same in Python, with the C call made through ctypes, took 3 to 4 us more a
+// same in Python, with the C call made through ctypes, took 2 to 4 us more a
 // call (one token's rotation 6.3 us, of which the kernel's launch takes 2.7).
 //
 // setup(addresses, check, cache_kind_id, layout_id) sets the library's functions
