@@ -486,7 +486,8 @@ int qmm_kv_read(int k_kind, int v_kind, const void *k_pages, const void *v_pages
  * block_table[b * max_pages + t / page_size] at offset t % page_size.  The new
  * token's own key and value are part of the cache (qmm_kv_append first).  q is
  * [B][n_q][head_dim] f32 or f16 with a row stride, out [B][n_q][head_dim],
- * contiguous, of the same type.  A sequence without tokens (length 0 or
+ * contiguous, of the same type; out may be q itself where q is contiguous, and
+ * overlaps nothing else.  A sequence without tokens (length 0 or
  * below) gives zeros; lengths are cut to max_pages * page_size; tokens whose
  * page number lies outside [0, n_pages) count as absent.
  * Numerics: keys and values are exact (codes as integers, block scales in

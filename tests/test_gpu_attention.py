@@ -370,6 +370,14 @@ def test_attn_strided_q_scale_out_and_workspace():
         c.run(q, workspace=ws[:-1])
 
 
+@pytest.mark.parametrize("dt", ["f16", "f32"])
+def test_attn_into_its_queries(dt):
+    c = Case("Q8_0", "Q4_0", 128, 64, 2, [300, 31, 0, 2000])
+    q = dev(c.g.normal(size=(4, 40, 128)).astype(NP[dt]))
+    want = c.run(q)
+    assert c.run(q, out=q) is q and torch.equal(q, want)
+
+
 @pytest.mark.parametrize("kk,vk", [("F16", "F16"), ("Q8_0", "Q4_0")])
 def test_attn_strong_and_tiny_values(kk, vk):
     """Scores that leave one token all the weight, scores far below zero, tiny and large values, sinks that outweigh
