@@ -612,14 +612,18 @@ def _load_ops():
 
 def _on(stream, like, fn, *args):
     """fn(*args) on `stream`.  What it allocates is of that stream's memory (the
-    current stream's free memory may still be in use by its pending work), kept
-    from reuse until both streams are done with it."""
+    current stream's free memory may still be in use by its pending work);
+    operands and results are kept from reuse until both streams are done with
+    them."""
     import torch
     if like.device != stream.device:
         raise ValueError(f"operands on {like.device}, stream on {stream.device}")
     here = torch.cuda.current_stream(like.device)
     with torch.cuda.stream(stream):
         got = fn(*args)
+    for t in args:
+        if isinstance(t, torch.Tensor):
+            t.record_stream(stream)
     for t in got if isinstance(got, tuple) else (got,):
         if t is not None and not any(t is a for a in args):
             t.record_stream(here)

@@ -551,6 +551,23 @@ def test_outputs_of_a_call_on_another_stream_are_its_own():
     assert torch.equal(got, want)
 
 
+def test_operands_of_a_call_on_another_stream_outlive_it():
+    """An operand freed after the call is not handed out while the other stream has still to read it."""
+    T, H, D = 1000, 9, 128
+    x = dev(wl.rng("stream", "operand").normal(size=(T, H, D)).astype(np.float32))
+    pos, (freqs, m) = dev(np.arange(T, dtype=np.int32)), qmm.rope_freqs(D)
+    want, side = qmm.rope(x, pos, freqs, mscale=m), torch.cuda.Stream()
+    brief = x.clone()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(50_000_000)
+    got = qmm.rope(brief, pos, freqs, mscale=m, stream=side)
+    del brief
+    torch.empty_like(x).fill_(5.0)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+
+
 def test_decode_steps_through_a_layer(oracle_mod):
     """Prompt, then decode steps: q, k, v from a Q4_0 projection (qmm_matmul), append, attention, output projection.
     Each part against its definition on the previous part's actual output."""
