@@ -22,17 +22,30 @@
 //            offset as the accumulator's start value -offset * sum q (Q4_0
 //            beside f32 queries: signed integers, as the values); each
 //            block's product is scaled by the token's f32 block scale.
-//   values   D[element][head] += V^T . P^T.  Codes enter as exact signed
-//            integers in f16; the block scale goes into the weight, p * d,
-//            rounded once to f16.
-// f32 queries are split into two f16 terms (exact to about 2^-22), and so are
-// the weights p and p * d; f16 queries and their weights take one term.
+//   values   D[element][head] += V^T . P^T; the block scale goes into the
+//            weight, p * d.  Beside f16 queries weights are rounded once to
+//            f16 and codes enter as exact signed integers in f16.  Beside f32
+//            queries weights, codes and halves enter as f32, in f32 products:
+//            v_mfma_f32_16x16x4_f32, or up to four heads
+//            v_mfma_f32_4x4x1_16b_f32, which takes the same 64 values against 4
+//            columns instead of 16 in a quarter of the time (the heads then
+//            fill the 16 score columns four times over).
+// f32 queries are split into two f16 terms (exact to about 2^-22).
 //
-// The softmax keeps a running reference R per head instead of the running
-// maximum: R is the maximum of (group maximum of s + exponent of the group's
-// largest value scale) - 14, so that p * d = 2^(s - R) * d reaches 2^14..2^15
-// for the strongest tokens and stays clear of f16's subnormals for tokens down
-// to 2^-28 of them, whatever the size of the values.
+// The softmax keeps a running reference R per head.  Beside f32 queries it is
+// the running maximum.  Beside f16 queries it is the maximum of (maximum of s
+// over eight tokens + exponent of their largest value scale) - 14, so that p * d =
+// 2^(s - R) * d reaches 2^14..2^15 for the strongest token and block: weights
+// down to 2^-28 of it are normal f16 numbers, below that they lose bits, each
+// at most 2^-39 of it (2^-25 against 2^14).  One term so loses what a weak
+// token or a small block contributes to an element that the strong ones leave
+// empty; two f16 terms share the exponent range and lose it too (an element 30
+// below in the exponent: nothing of it was right), which f32 results do not
+// bear.  What the f32 products cost against two f16 terms, 64 sequences of 0 to
+// 8192 tokens, heads of 128: 32 / 8 heads Q8_0 / Q4_0 115 -> 120 us, Q4_0 96 ->
+// 101; 48 windows of 4096, 64 / 8 heads of 64, Q4_0 43 -> 61.  (Four columns
+// instead of 16 for four heads: Q8_0 155 -> 123 us, Q4_0 140 -> 101.  Two products
+// of four columns for eight heads: 159 -> 148 and no change, not kept.)
 //
 // What bounds it: the cache's bytes, read once at the rate of a large copy
 // (5.1 TB/s here) as soon as there are enough of them.  Measured, the attention
@@ -317,6 +330,21 @@ __device__ __forceinline__ constexpr int v_token(int k) {
   return (k & 4) + (p == 1 ? 2 : p == 2 ? 1 : p);
 }
 
+// For f32 products: codes of values as signed bytes (four tokens a word) of tile
+// x, Q8_0's own, Q4_0's times 16 (the nibble, its top bit turned, in the upper
+// half).
+template <int VK>
+__device__ __forceinline__ uint32_t value_codes(const Raw<VK> &r, int x, int i) {
+  if constexpr (VK == C_Q8_0) return r.w[2 * x + i] ^ 0x80808080u;
+  if constexpr (VK == C_Q4_0) return ((x == 0 ? r.w[i] << 4 : r.w[i]) & 0xf0f0f0f0u) ^ 0x80808080u;
+}
+// Value of token k of tile x, in that unit.
+template <int VK>
+__device__ __forceinline__ float value_f32(const Raw<VK> &r, int x, int k) {
+  if constexpr (VK == C_F16) return (float)as_h8(r.w[x])[k];
+  else return (float)(int8_t)(value_codes<VK>(r, x, k >> 2) >> (8 * (k & 3)));
+}
+
 // The query elements of the eight K entries of lane group G, of a block of 32
 // (qmm_kv.h; Q4_0 bytes are taken in the order 0, 2, 1, 3, low and high nibbles
 // of a pair of bytes side by side), as floats.
@@ -352,10 +380,12 @@ __device__ __forceinline__ void store_out(QT *out, floatx4 o, float l, float R, 
   *(q4 *)out = q4{(QT)(o[0] * inv), (QT)(o[1] * inv), (QT)(o[2] * inv), (QT)(o[3] * inv)};
 }
 
-template <int KK, int VK, int NB, typename QT>
+// COLS: 16, or 4 for f32 queries of up to four heads.
+template <int KK, int VK, int NB, typename QT, int COLS>
 __global__ __launch_bounds__(64 * kWaves) void attn_kernel(Args a) {
   constexpr int D = NB * 32;
-  constexpr bool SPLIT = sizeof(QT) == 4;  // two f16 terms
+  constexpr bool SPLIT = sizeof(QT) == 4;  // two f16 terms of the query, f32 weights
+  constexpr float kUnit = SPLIT && VK == C_Q4_0 ? 0.0625f : 1.0f;  // of the accumulators
   constexpr bool SUB = kSubnormalKeys<KK, SPLIT>;
   constexpr int kPitch = D + 4;
   extern __shared__ __attribute__((aligned(16))) float lds[];  // [part][heads][kPitch], then [part][heads][2]
@@ -448,7 +478,7 @@ __global__ __launch_bounds__(64 * kWaves) void attn_kernel(Args a) {
   floatx4 qoff[SUB ? NB : 1];
   float qscale = a.scale2 == 0.0f ? 1.0f : fabsf(a.scale2);
   {
-    const QT *q = (const QT *)a.q + (int64_t)b * a.q_stride + (int64_t)(head0 + min(j, heads - 1)) * D;
+    const QT *q = (const QT *)a.q + (int64_t)b * a.q_stride + (int64_t)(head0 + min(j % COLS, heads - 1)) * D;
     const float sign = a.scale2 > 0.0f ? 1.0f : a.scale2 < 0.0f ? -1.0f : 0.0f;
     float up = sign;
     float v[NB][8];
@@ -496,6 +526,9 @@ __global__ __launch_bounds__(64 * kWaves) void attn_kernel(Args a) {
     }
   }
 
+  // Of 16 columns a lane's accumulators are elements 4G .. 4G + 3 of column j, of
+  // four the elements 4 (j / 4) .. + 3 of column j % 4, over the tokens of the
+  // lane group alone.
   floatx4 acc[NB][2];
 #pragma unroll
   for (int n = 0; n < NB; ++n) acc[n][0] = acc[n][1] = floatx4{0, 0, 0, 0};
@@ -561,14 +594,15 @@ __global__ __launch_bounds__(64 * kWaves) void attn_kernel(Args a) {
       }
     }
 
-    // The reference: per lane (its eight tokens) the largest score and the
-    // exponent of the largest value scale, then over the lanes of the column.
+    // The reference: per lane (its eight tokens) the largest score and (f16
+    // weights) the exponent of the largest value scale, then over the lanes of
+    // the column.
     float top = s[0];
 #pragma unroll
     for (int k = 1; k < 8; ++k) top = fmaxf(top, s[k]);
     top *= qscale;
-    float below = 14.0f;  // 14 - the exponent of the largest value scale
-    if constexpr (VK != C_F16) {
+    float below = SPLIT ? 0.0f : 14.0f;  // 14 - the exponent of the largest value scale
+    if constexpr (VK != C_F16 && !SPLIT) {
       // Magnitudes of halves compare as integers (Q8_0 scales have no sign).
       ushort2v part[4] = {{0, 0}, {0, 0}, {0, 0}, {0, 0}};
 #pragma unroll
@@ -621,34 +655,40 @@ __global__ __launch_bounds__(64 * kWaves) void attn_kernel(Args a) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) sum += p[k];
 
-    half8 ph, pl;
-    if constexpr (VK == C_F16) {
+    if constexpr (SPLIT) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        ph[k] = (_Float16)p[k];
-        if constexpr (SPLIT) pl[k] = (_Float16)(p[k] - (float)ph[k]);
-      }
-    }
+      for (int n = 0; n < NB; ++n) {
 #pragma unroll
-    for (int n = 0; n < NB; ++n) {
-      if constexpr (VK != C_F16) {
+        for (int k = 0; k < 8; ++k) {
+          float w = p[k];
+          if constexpr (VK != C_F16) w = __builtin_fmaf(w, (float)vd[n][k], 0.0f);  // one v_fma_mix
 #pragma unroll
-        for (int k = 0; k < 8; ++k)  // one v_fma_mix each
-          ph[k] = (_Float16)__builtin_fmaf(p[v_token<VK>(k)], (float)vd[n][v_token<VK>(k)], 0.0f);
-        if constexpr (SPLIT) {
-          // The second term is what the first one, as it was rounded, leaves:
-          // the compiler must not recompute that rounding in another way.
-          asm("" : "+v"(ph));
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            pl[k] = (_Float16)__builtin_fmaf(p[v_token<VK>(k)], (float)vd[n][v_token<VK>(k)], -(float)ph[k]);
+          for (int x = 0; x < 2; ++x) {
+            const float v = value_f32<VK>(vr[n], x, k);
+            if constexpr (COLS == 16) {  // K entries: token k of each lane group
+              acc[n][x] = __builtin_amdgcn_mfma_f32_16x16x4f32(v, w, acc[n][x], 0, 0, 0);
+            } else {  // sixteen products of the four lanes that share j / 4 and G
+              acc[n][x] = __builtin_amdgcn_mfma_f32_4x4x1f32(v, w, acc[n][x], 0, 0, 0);
+            }
+          }
         }
       }
+    } else {
+      half8 ph;
+      if constexpr (VK == C_F16) {
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const half8 v = value_operand<VK>(vr[n], x, nb);
-        acc[n][x] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, ph, acc[n][x], 0, 0, 0);
-        if constexpr (SPLIT) acc[n][x] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, pl, acc[n][x], 0, 0, 0);
+        for (int k = 0; k < 8; ++k) ph[k] = (_Float16)p[k];
+      }
+#pragma unroll
+      for (int n = 0; n < NB; ++n) {
+        if constexpr (VK != C_F16) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)  // one v_fma_mix each
+            ph[k] = (_Float16)__builtin_fmaf(p[v_token<VK>(k)], (float)vd[n][v_token<VK>(k)], 0.0f);
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          acc[n][x] = __builtin_amdgcn_mfma_f32_16x16x32_f16(value_operand<VK>(vr[n], x, nb), ph, acc[n][x], 0, 0, 0);
       }
     }
     load_values(next, in_next);
@@ -661,21 +701,30 @@ __global__ __launch_bounds__(64 * kWaves) void attn_kernel(Args a) {
   // The four waves' parts, joined through LDS with their references.  Where the
   // heads are too many for four parts in LDS, waves 2 and 3 first hand theirs
   // to waves 0 and 1.
-  const int parts = lds_parts(a.heads);
-  float *ml = lds + parts * a.heads * kPitch;  // [part][heads][2]
-  auto put_part = [&](int w) {
-    if (j >= heads) return;
-    float *o = lds + (w * a.heads + j) * kPitch + 4 * G;
+  if constexpr (COLS == 4) {
 #pragma unroll
     for (int n = 0; n < NB; ++n)
 #pragma unroll
-      for (int x = 0; x < 2; ++x) *(floatx4 *)(o + n * 32 + x * 16) = acc[n][x];
-    if (G == 0) {
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[n][x][r] = sum_over_groups(acc[n][x][r]);
+  }
+  const int parts = lds_parts(a.heads);
+  float *ml = lds + parts * a.heads * kPitch;  // [part][heads][2]
+  auto put_part = [&](int w) {
+    if (G == 0 && j < heads) {
       ml[(w * a.heads + j) * 2] = R;
       ml[(w * a.heads + j) * 2 + 1] = sum;
     }
+    if (j % COLS >= heads) return;
+    float *o = lds + (w * a.heads + j % COLS) * kPitch + (COLS == 16 ? G : j / 4) * 4;
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+        if (COLS == 16 || G == x) *(floatx4 *)(o + n * 32 + x * 16) = acc[n][x] * kUnit;
   };
-  if (parts == 2) {
+  if (COLS == 16 && parts == 2) {
     if (wave >= 2) put_part(wave - 2);
     __syncthreads();
     if (wave < 2 && j < heads) {
@@ -685,7 +734,8 @@ __global__ __launch_bounds__(64 * kWaves) void attn_kernel(Args a) {
 #pragma unroll
       for (int n = 0; n < NB; ++n)
 #pragma unroll
-        for (int x = 0; x < 2; ++x) acc[n][x] = acc[n][x] * f + *(const floatx4 *)(o + n * 32 + x * 16) * fo;
+        for (int x = 0; x < 2; ++x)
+          acc[n][x] = acc[n][x] * f + *(const floatx4 *)(o + n * 32 + x * 16) * (fo / kUnit);
       sum = sum * f + ml[(wave * a.heads + j) * 2 + 1] * fo;
       R = Rn;
     }
@@ -723,13 +773,13 @@ hipError_t launch_plan(const Args &a, hipStream_t s);
 
 // How many workgroups the GPU holds is looked up once per instantiation (with
 // the most LDS a call uses).
-template <int KK, int VK, int NB, typename QT>
-static hipError_t run(Args &a, hipStream_t s) {
+template <int KK, int VK, int NB, typename QT, int COLS>
+static hipError_t run_cols(Args &a, hipStream_t s) {
   static std::atomic<int> per_cu{0};
   auto lds = [](int heads) { return (unsigned)(lds_parts(heads) * (NB * 32 + 4 + 2) * heads * sizeof(float)); };  // <= 34 KiB
   int n = per_cu.load(std::memory_order_relaxed);
   if (n == 0) {
-    hipError_t e = hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, attn_kernel<KK, VK, NB, QT>, 64 * kWaves,
+    hipError_t e = hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, attn_kernel<KK, VK, NB, QT, COLS>, 64 * kWaves,
                                                                 std::max(lds(8), lds(16)));
     if (e != hipSuccess) return e;
     n = std::max(n, 1);
@@ -743,8 +793,16 @@ static hipError_t run(Args &a, hipStream_t s) {
     const hipError_t e = launch_plan(a, s);
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((attn_kernel<KK, VK, NB, QT>), dim3((unsigned)a.items), dim3(64 * kWaves), lds(a.heads), s, a);
+  hipLaunchKernelGGL((attn_kernel<KK, VK, NB, QT, COLS>), dim3((unsigned)a.items), dim3(64 * kWaves), lds(a.heads), s, a);
   return hipGetLastError();
+}
+
+template <int KK, int VK, int NB, typename QT>
+static hipError_t run(Args &a, hipStream_t s) {
+  if constexpr (sizeof(QT) == 4) {
+    if (a.heads <= 4) return run_cols<KK, VK, NB, QT, 4>(a, s);
+  }
+  return run_cols<KK, VK, NB, QT, 16>(a, s);
 }
 
 template <int KK, int VK, typename QT>

@@ -492,13 +492,20 @@ int qmm_kv_read(int k_kind, int v_kind, const void *k_pages, const void *v_pages
  * page number lies outside [0, n_pages) count as absent.
  * Numerics: keys and values are exact (codes as integers, block scales in
  * f32 or folded into the weight); scores, softmax and sums are f32.  f16 q is
- * exact and the weights are rounded once to f16; f32 q and weights are carried
- * as two f16 terms (relative 2^-21).  With w_t the exact weights,
- *   |out - exact| <= (r + 2 max_t e_t) sum_t w_t |v_t|  (+ f16 out's rounding)
+ * exact and the weights, times the value's block scale, are rounded once to
+ * f16; f32 q is carried as two f16 terms (relative 2^-21), and weights and
+ * their products with the values are f32.  With w_t the exact weights,
+ *   |out - exact| <= (r + 2 max_t e_t) sum_t w_t |v_t| + a  (+ f16 out's rounding)
  * where r = 2^-11 + 2^-18 for f16 and 2^-18 for f32, and e_t = c (scale * sum
  * over 32-element blocks of (sum |q|) (max |k_t|) + max |s| + 40) with c =
- * 2^-17 for f16 and 2^-20 for f32 bounds a score's error.  The order of every sum is fixed: a call repeated gives the
- * same bits.
+ * 2^-17 for f16 and 2^-20 for f32 bounds a score's error.  a is 0 for f32
+ * (weights below 2^-100 of the largest may count as 0); for f16 it is what f16
+ * weights lose far below the strongest, 2^-39 M sum_t |c_t|, with c_t the code
+ * of the value (F16: the value itself) and M the largest product of a weight
+ * and a block scale (F16: 1) of two tokens with the same t / 8: it counts in
+ * elements that are empty in all strong tokens and in blocks far smaller than
+ * the others of their head, where a caller for whom they matter takes f32 q.
+ * The order of every sum is fixed: a call repeated gives the same bits.
  * n_q is a multiple of n_kv.  workspace: qmm_attn_decode_workspace_bytes(B,
  * n_q, n_kv, head_dim) bytes, 16-byte aligned, overwritten (it need not be
  * initialized); calls sharing it must not overlap.  Nothing depends on the

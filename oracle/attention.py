@@ -164,3 +164,15 @@ def attend(q, k, v, scale, sink=None, f16=True):
     e = 2.0 ** -20 * (abs(scale) * (ak @ aq).max() + np.abs(s).max() + 40)
     r = 2.0 ** -18 + (2.0 ** -11 if f16 else 0)
     return w @ v, (r + 2 * e) * (w @ np.abs(v))
+
+
+def f16_floor(v, scales, w):
+    """What f16 weights may lose in each element beyond attend's tolerance: v [n, D] exact values, scales [n, D / 32]
+    of their blocks (None: F16), w [n] exact weights, token 0 of the arrays at a multiple of eight."""
+    n, D = v.shape
+    pad = -n % 8
+    top = np.pad(w, (0, pad)).reshape(-1, 8).max(-1)
+    d = np.ones((n, 1)) if scales is None else np.abs(scales.astype(np.float64))
+    big = np.pad(d.max(-1), (0, pad)).reshape(-1, 8).max(-1)
+    d = np.where(d == 0, 1, d).repeat(D // d.shape[1], -1)
+    return 2.0 ** -39 * (top * big).max() * np.abs(v / d).sum(0)

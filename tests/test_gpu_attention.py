@@ -516,6 +516,73 @@ def test_attn_nonfinite_value_stays_in_its_elements(vk):
     check(got, want, tol, "the other elements")
 
 
+def rewrite_kv(c):
+    """c.k and c.v, changed, into the cache and as the oracle's exact values."""
+    t = [np.arange(n) for n in c.lens]
+    slots = np.concatenate([c.table[b, x // c.P] * c.P + x % c.P for b, x in enumerate(t)]).astype(np.int32)
+    qmm.kv_write(dev(c.k), dev(c.v), dev(slots), c.kp, c.vp, c.kk, c.vk, c.P)
+    c.kx, c.vx = (oa.dequantize(kind, *oa.quantize(kind, x)) for kind, x in ((c.kk, c.k), (c.vk, c.v)))
+
+
+def want_with_floor(c, q, dt):
+    """c.want(q, dt), with what f16 weights may lose (the header's term a)."""
+    out, tol = c.want(q, dt)
+    if dt == "f16":
+        scales = None if c.vk == "F16" else oa.quantize(c.vk, c.v)[1]
+        for b, n in enumerate(c.lens):
+            rows = slice(c.first[b], c.first[b] + n)
+            for h in range(q.shape[1]):
+                g = h // (q.shape[1] // c.n_kv)
+                s = c.kx[rows, g] @ q[b, h].astype(np.float64) * c.D ** -0.5
+                w = np.exp(s - s.max())
+                tol[b, h] += oa.f16_floor(c.vx[rows, g], None if scales is None else scales[rows, g], w / w.sum())
+    return out, tol
+
+
+def lone_score(c, b, t, q, gap):
+    """Sets the key of token t of sequence b so that q scores `gap` (scale D^-0.5)."""
+    c.k[c.first[b] + t, 0] = q * (gap * c.D ** 0.5 / np.dot(q, q))
+
+
+@pytest.mark.parametrize("kk", ["F16", "Q4_0"])
+@pytest.mark.parametrize("vk", KINDS)
+@pytest.mark.parametrize("dt", ["f16", "f32"])
+@pytest.mark.parametrize("D,below,G", [(64, 16, 6), (128, 12, 2), (256, 16, 12), (96, 16, 4)])
+def test_attn_blocks_of_unequal_size(kk, vk, dt, D, below, G):
+    """Every second block of the values 2^-below of the others and nearly zero in the strongest token: the bound holds for
+    each element by its own values."""
+    c = Case(kk, vk, D, 64, 1, [1024, 100])
+    q = c.g.normal(size=(2, 1, D)).astype(np.float32) * (1 - np.arange(G, dtype=np.float32)[:, None] / 64)
+    q = q.astype(NP[dt])
+    blocks = c.v.reshape(-1, D // 32, 32)
+    blocks *= 2.0 ** 9 / np.abs(blocks).max()
+    blocks[:, 1::2] *= np.float32(2.0 ** -below)
+    for b, t in ((0, 700), (1, 31)):
+        lone_score(c, b, t, q[b, 0].astype(np.float32), 14.0)
+        blocks[c.first[b] + t, 1::2] *= np.float32(2.0 ** -9)
+    rewrite_kv(c)
+    check(c.run(dev(q)).cpu().numpy(), *want_with_floor(c, q, dt), f"{kk} {vk} D={D}")
+
+
+@pytest.mark.parametrize("kk", ["F16", "Q8_0"])
+@pytest.mark.parametrize("vk", KINDS)
+@pytest.mark.parametrize("dt,gap,size", [("f16", 20.0, 30000.0), ("f32", 20.0, 1.0), ("f32", 30.0, 1.0), ("f32", 60.0, 0.01)])
+def test_attn_strongest_token_of_zero_value(kk, vk, dt, gap, size):
+    """The token with nearly all the weight has the value 0 in some elements: what the others add there is exact to the
+    bound relative to itself."""
+    c = Case(kk, vk, 64, 32, 1, [500, 40], seed=str(gap))
+    q = c.g.normal(size=(2, 2, 64)).astype(np.float32)
+    q[:, 1] = q[:, 0] * np.float32(0.96875)
+    q = q.astype(NP[dt])
+    c.v = (c.v / np.abs(c.v).max() * size).astype(np.float32)
+    for b, t in ((0, 333), (1, 39)):
+        lone_score(c, b, t, q[b, 0].astype(np.float32), gap)
+        c.v[c.first[b] + t, 0, ::2] = 0
+        c.v[c.first[b] + t, 0, 32:] = 0
+    rewrite_kv(c)
+    check(c.run(dev(q)).cpu().numpy(), *want_with_floor(c, q, dt), f"{kk} {vk} gap={gap}")
+
+
 def test_two_streams_at_once():
     """Calls on two streams, each with its own workspace, and the stream argument with outputs allocated by the call."""
     cases = [Case("Q8_0", "Q4_0", 128, 64, 2, [3000, 100]), Case("F16", "F16", 64, 32, 1, [5000])]
