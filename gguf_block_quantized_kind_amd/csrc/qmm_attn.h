@@ -47,6 +47,13 @@
 // instead of 16 for four heads: Q8_0 155 -> 123 us, Q4_0 140 -> 101.  Two products
 // of four columns for eight heads: 159 -> 148 and no change, not kept.)
 //
+// Sums.  A split may hold any number of tokens, and a running f32 sum of
+// like terms rounds the same way each time.  The weights' sum takes eight at a
+// time and carries what each addition rounds off; the accumulators take at most
+// kAdds groups before they are added to the wave's part in LDS, and keep what that
+// addition rounds off.  So the error does not grow with the length (plain running
+// sums: 1e-3 at a million tokens of a split; no difference in time measured).
+//
 // What bounds it: the cache's bytes, read once at the rate of a large copy
 // (5.1 TB/s here) as soon as there are enough of them.  Measured, the attention
 // kernel alone: one sequence of 131071 tokens, 32 / 8 heads of 128, Q8_0 keys
@@ -148,6 +155,18 @@ __device__ __forceinline__ float sum_over_groups(float v) {
   v = __builtin_bit_cast(float, (uint32_t)a[0]) + __builtin_bit_cast(float, (uint32_t)a[1]);
   auto b = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v), false, false);
   return __builtin_bit_cast(float, (uint32_t)b[0]) + __builtin_bit_cast(float, (uint32_t)b[1]);
+}
+
+// Sums of two values over pairs of lane groups, one swap for both: over groups
+// 2i and 2i + 1, a's in group 2i and b's in 2i + 1; over groups i and i + 2, a's in
+// groups 0 and 1 and b's in 2 and 3.
+__device__ __forceinline__ float sum_of_rows(float u, float v) {
+  auto a = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, u), __builtin_bit_cast(uint32_t, v), false, false);
+  return __builtin_bit_cast(float, (uint32_t)a[0]) + __builtin_bit_cast(float, (uint32_t)a[1]);
+}
+__device__ __forceinline__ float sum_of_halves(float u, float v) {
+  auto a = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, u), __builtin_bit_cast(uint32_t, v), false, false);
+  return __builtin_bit_cast(float, (uint32_t)a[0]) + __builtin_bit_cast(float, (uint32_t)a[1]);
 }
 
 // Inclusive sum over the lanes of a wave, without LDS: within rows of 16, then
@@ -361,9 +380,6 @@ __device__ __forceinline__ void load_q(const QT *q, int G, float (&v)[8]) {
   }
 }
 
-// Parts of a workgroup's join that lie in LDS at once.
-__host__ __device__ inline int lds_parts(int heads) { return heads <= 8 ? kWaves : 2; }
-
 // Four elements of the result: the sums o over the weights' sum l (both on
 // reference R), with the sink's share on the larger of the two references;
 // zeros where nothing was attended.
@@ -532,225 +548,240 @@ __global__ __launch_bounds__(64 * kWaves) void attn_kernel(Args a) {
   floatx4 acc[NB][2];
 #pragma unroll
   for (int n = 0; n < NB; ++n) acc[n][0] = acc[n][1] = floatx4{0, 0, 0, 0};
-  float R = kFloor, sum = 0.0f;
+  float R = kFloor, sum = 0.0f, rest = 0.0f;  // weights' sum: sum + rest
   const Nibbles nb;
 
-  while (g < ge) {
-    // The next group's keys load as soon as this one's are used, its values
-    // likewise (after the last group once more the last: the loads are issued
-    // whatever follows, so that no wait is widened by a branch).
-    advance();
-    const int page_after = table[pi], in_after = kvh * a.page_groups + gi;
-
-    // Products of tokens 8G + k with head j, without the query's scale.
-    float s[8];
+  // This wave's part in LDS, to which the accumulators are added every kAdds
+  // groups; they keep what that addition rounds off.  Of four columns a lane
+  // stores, of the sums over the lane groups, elements 2 (G / 2) and 1 more of its
+  // four, of tile G % 2.
+  constexpr int kAdds = SPLIT ? 32 : 64;
+  constexpr int kOwn = COLS == 16 ? 4 : 2;
+  typedef float own_t __attribute__((ext_vector_type(kOwn)));
+  float *ml = lds + kWaves * a.heads * kPitch;  // [part][heads][2]: reference and sum
+  float *own = lds + (wave * a.heads + j % COLS) * kPitch + (COLS == 16 ? 4 * G : j / 4 * 4 + G / 2 * 2 + G % 2 * 16);
+  const bool stores = j % COLS < heads;
+  float R_part = kFloor;
+  bool started = false;
+  auto add_part = [&] {
+    const float f = __builtin_amdgcn_exp2f(R_part - R);
 #pragma unroll
-    for (int m = 0; m < 2; ++m) {
-      floatx4 t = {0, 0, 0, 0};
+    for (int n = 0; n < NB; ++n) {
+      own_t add[COLS == 16 ? 2 : 1];
+      if constexpr (COLS == 16) {
+        add[0] = acc[n][0] * kUnit, add[1] = acc[n][1] * kUnit;
+      } else {
 #pragma unroll
-      for (int n = 0; n < NB; ++n) {
-        const half8 k = key_operand<KK, SPLIT>(kr[n], m, nb);
-        floatx4 u;
-        if constexpr (KK == C_F16) u = t;
-        else if constexpr (SUB) u = qoff[n];
-        else u = floatx4{0, 0, 0, 0};
-        u = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, qh[n], u, 0, 0, 0);
-        if constexpr (SPLIT) u = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, ql[n], u, 0, 0, 0);
-        if constexpr (KK == C_F16) t = u;
-        else
-#pragma unroll
-          for (int r = 0; r < 4; ++r) t[r] = __builtin_fmaf((float)kd[n][4 * m + r], u[r], t[r]);
-      }
-#pragma unroll
-      for (int r = 0; r < 4; ++r) s[4 * m + r] = t[r];
-    }
-    const bool there_next = usable(page_next);
-    const int next = there_next ? page_next : 0;
-    load_keys(next, in_next);
-
-    // Tokens outside [lo, len) of the first and last group: whatever their
-    // bytes hold, they weigh nothing.
-    const int t0 = g * kv::kGroup;
-    if (t0 < sp.lo || t0 > sp.len - kv::kGroup || !there) {
-      bool in[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int t = t0 + 8 * G + k;
-        in[k] = there && t >= sp.lo && t < sp.len;
-        if (!in[k]) s[k] = -__builtin_inff();
-      }
-#pragma unroll
-      for (int n = 0; n < NB; ++n) {
-        if constexpr (VK == C_F16) {
-#pragma unroll
-          for (int x = 0; x < 2; ++x)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              vr[n].w[x][k] &= (in[2 * k] ? 0xffffu : 0u) | (in[2 * k + 1] ? 0xffff0000u : 0u);
-        } else {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) vd[n][k] = in[k] ? vd[n][k] : (_Float16)0.0f;
+        for (int r = 0; r < 2; ++r) {
+          const float low = sum_of_rows(acc[n][0][r], acc[n][1][r]), high = sum_of_rows(acc[n][0][r + 2], acc[n][1][r + 2]);
+          add[0][r] = sum_of_halves(low, high) * kUnit;
         }
       }
-    }
-
-    // The reference: per lane (its eight tokens) the largest score and (f16
-    // weights) the exponent of the largest value scale, then over the lanes of
-    // the column.
-    float top = s[0];
 #pragma unroll
-    for (int k = 1; k < 8; ++k) top = fmaxf(top, s[k]);
-    top *= qscale;
-    float below = SPLIT ? 0.0f : 14.0f;  // 14 - the exponent of the largest value scale
-    if constexpr (VK != C_F16 && !SPLIT) {
-      // Magnitudes of halves compare as integers (Q8_0 scales have no sign).
-      ushort2v part[4] = {{0, 0}, {0, 0}, {0, 0}, {0, 0}};
+      for (int x = 0; x < (COLS == 16 ? 2 : 1); ++x) {
+        own_t *o = (own_t *)(own + n * 32 + x * 16);
+        own_t left = {};
+        if (!started) {
+          if (stores) *o = add[x];
+        } else if (stores) {
+          const own_t old = *o * f, now = old + add[x];
+          *o = now;
+          left = (add[x] - (now - old)) * (1.0f / kUnit);
+        }
+        if constexpr (COLS == 16) {
+          acc[n][x] = left;
+        } else {
 #pragma unroll
-      for (int n = 0; n < NB; ++n) {
-        const u32x4 w = __builtin_bit_cast(u32x4, vd[n]);
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          part[k] = __builtin_elementwise_max(part[k], as_us2(VK == C_Q4_0 ? w[k] & 0x7fff7fffu : w[k]));
+          for (int k = 0; k < 8; ++k) acc[n][k >> 2][k & 3] = G == ((k & 2) | k >> 2) ? left[k & 1] : 0.0f;
+        }
       }
-      ushort2v most = __builtin_elementwise_max(__builtin_elementwise_max(part[0], part[1]),
-                                                __builtin_elementwise_max(part[2], part[3]));
-      // A NaN scale (a block that held an infinity or NaN) leaves the other
-      // blocks' reference alone.
-      if (__any(max(most[0], most[1]) >= 0x7c00)) {
-        most = ushort2v{0, 0};
-        for (int n = 0; n < NB; ++n)
-          for (int k = 0; k < 8; ++k) {
-            const uint16_t m = __builtin_bit_cast(uint16_t, (_Float16)vd[n][k]) & 0x7fff;
-            if (m < 0x7c00) most[0] = max(most[0], m);
-          }
-      }
-      const half2v big = as_h2(as_u(most));
-      // 2^e <= scale < 2^(e + 1); f16 scales are 0 or at least 2^-24.
-      const float bf = fmaxf(fmaxf((float)big[0], (float)big[1]), 0x1p-24f);
-      below = (float)(127 + 14 - (int)(__builtin_bit_cast(uint32_t, bf) >> 23));
+      __builtin_amdgcn_sched_barrier(0);  // (few blocks at a time: registers)
     }
-    // (Among scores whose f32 neighbours lie further apart than `below` means,
-    // the reference is the score itself: weights up to 1, not 2^14.)
-    top = fabsf(top) < kFar ? top - below : top;
-    top = max_over_groups(top);
-    if (__any(top > R)) {  // rare after the first groups
-      const float Rn = fmaxf(R, top), alpha = __builtin_amdgcn_exp2f(R - Rn);
-      R = Rn;
-      sum *= alpha;
-#pragma unroll
-      for (int n = 0; n < NB; ++n)
-#pragma unroll
-        for (int x = 0; x < 2; ++x) acc[n][x] *= alpha;
-    }
-    float p[8];
-    if (__any(fabsf(R) >= kFar)) {
-      // The score rounded as the reference was: what the product's rounding
-      // leaves, itself large here, must not become a weight.
-#pragma unroll
-      for (int k = 0; k < 8; ++k) p[k] = __builtin_amdgcn_exp2f(kv::in_f32(s[k] * qscale) - R);
-    } else {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) p[k] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[k], qscale, -R));
-    }
-#pragma unroll
-    for (int k = 0; k < 8; ++k) sum += p[k];
+    R_part = R;
+    started = true;
+  };
 
-    if constexpr (SPLIT) {
+  do {
+    const int stop = min(ge, g + kAdds * kWaves);
+    while (g < stop) {
+      // The next group's keys load as soon as this one's are used, its values
+      // likewise (after the last group once more the last: the loads are issued
+      // whatever follows, so that no wait is widened by a branch).
+      advance();
+      const int page_after = table[pi], in_after = kvh * a.page_groups + gi;
+
+      // Products of tokens 8G + k with head j, without the query's scale.
+      float s[8];
 #pragma unroll
-      for (int n = 0; n < NB; ++n) {
+      for (int m = 0; m < 2; ++m) {
+        floatx4 t = {0, 0, 0, 0};
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+          const half8 k = key_operand<KK, SPLIT>(kr[n], m, nb);
+          floatx4 u;
+          if constexpr (KK == C_F16) u = t;
+          else if constexpr (SUB) u = qoff[n];
+          else u = floatx4{0, 0, 0, 0};
+          u = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, qh[n], u, 0, 0, 0);
+          if constexpr (SPLIT) u = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, ql[n], u, 0, 0, 0);
+          if constexpr (KK == C_F16) t = u;
+          else
+#pragma unroll
+            for (int r = 0; r < 4; ++r) t[r] = __builtin_fmaf((float)kd[n][4 * m + r], u[r], t[r]);
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) s[4 * m + r] = t[r];
+      }
+      const bool there_next = usable(page_next);
+      const int next = there_next ? page_next : 0;
+      load_keys(next, in_next);
+
+      // Tokens outside [lo, len) of the first and last group: whatever their
+      // bytes hold, they weigh nothing.
+      const int t0 = g * kv::kGroup;
+      if (t0 < sp.lo || t0 > sp.len - kv::kGroup || !there) {
+        bool in[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          float w = p[k];
-          if constexpr (VK != C_F16) w = __builtin_fmaf(w, (float)vd[n][k], 0.0f);  // one v_fma_mix
+          const int t = t0 + 8 * G + k;
+          in[k] = there && t >= sp.lo && t < sp.len;
+          if (!in[k]) s[k] = -__builtin_inff();
+        }
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const float v = value_f32<VK>(vr[n], x, k);
-            if constexpr (COLS == 16) {  // K entries: token k of each lane group
-              acc[n][x] = __builtin_amdgcn_mfma_f32_16x16x4f32(v, w, acc[n][x], 0, 0, 0);
-            } else {  // sixteen products of the four lanes that share j / 4 and G
-              acc[n][x] = __builtin_amdgcn_mfma_f32_4x4x1f32(v, w, acc[n][x], 0, 0, 0);
+        for (int n = 0; n < NB; ++n) {
+          if constexpr (VK == C_F16) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                vr[n].w[x][k] &= (in[2 * k] ? 0xffffu : 0u) | (in[2 * k + 1] ? 0xffff0000u : 0u);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) vd[n][k] = in[k] ? vd[n][k] : (_Float16)0.0f;
+          }
+        }
+      }
+
+      // The reference: per lane (its eight tokens) the largest score and (f16
+      // weights) the exponent of the largest value scale, then over the lanes of
+      // the column.
+      float top = s[0];
+#pragma unroll
+      for (int k = 1; k < 8; ++k) top = fmaxf(top, s[k]);
+      top *= qscale;
+      float below = SPLIT ? 0.0f : 14.0f;  // 14 - the exponent of the largest value scale
+      if constexpr (VK != C_F16 && !SPLIT) {
+        // Magnitudes of halves compare as integers (Q8_0 scales have no sign).
+        ushort2v part[4] = {{0, 0}, {0, 0}, {0, 0}, {0, 0}};
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+          const u32x4 w = __builtin_bit_cast(u32x4, vd[n]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            part[k] = __builtin_elementwise_max(part[k], as_us2(VK == C_Q4_0 ? w[k] & 0x7fff7fffu : w[k]));
+        }
+        ushort2v most = __builtin_elementwise_max(__builtin_elementwise_max(part[0], part[1]),
+                                                  __builtin_elementwise_max(part[2], part[3]));
+        // A NaN scale (a block that held an infinity or NaN) leaves the other
+        // blocks' reference alone.
+        if (__any(max(most[0], most[1]) >= 0x7c00)) {
+          most = ushort2v{0, 0};
+          for (int n = 0; n < NB; ++n)
+            for (int k = 0; k < 8; ++k) {
+              const uint16_t m = __builtin_bit_cast(uint16_t, (_Float16)vd[n][k]) & 0x7fff;
+              if (m < 0x7c00) most[0] = max(most[0], m);
+            }
+        }
+        const half2v big = as_h2(as_u(most));
+        // 2^e <= scale < 2^(e + 1); f16 scales are 0 or at least 2^-24.
+        const float bf = fmaxf(fmaxf((float)big[0], (float)big[1]), 0x1p-24f);
+        below = (float)(127 + 14 - (int)(__builtin_bit_cast(uint32_t, bf) >> 23));
+      }
+      // (Among scores whose f32 neighbours lie further apart than `below` means,
+      // the reference is the score itself: weights up to 1, not 2^14.)
+      top = fabsf(top) < kFar ? top - below : top;
+      top = max_over_groups(top);
+      if (__any(top > R)) {  // rare after the first groups
+        const float Rn = fmaxf(R, top), alpha = __builtin_amdgcn_exp2f(R - Rn);
+        R = Rn;
+        sum *= alpha;
+        rest *= alpha;
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) acc[n][x] *= alpha;
+      }
+      float p[8];
+      if (__any(fabsf(R) >= kFar)) {
+        // The score rounded as the reference was: what the product's rounding
+        // leaves, itself large here, must not become a weight.
+#pragma unroll
+        for (int k = 0; k < 8; ++k) p[k] = __builtin_amdgcn_exp2f(kv::in_f32(s[k] * qscale) - R);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) p[k] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[k], qscale, -R));
+      }
+      const float eight = ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7])), before = sum;
+      sum += eight;
+      rest += eight - (sum - before);
+
+      if constexpr (SPLIT) {
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            float w = p[k];
+            if constexpr (VK != C_F16) w = __builtin_fmaf(w, (float)vd[n][k], 0.0f);  // one v_fma_mix
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const float v = value_f32<VK>(vr[n], x, k);
+              if constexpr (COLS == 16) {  // K entries: token k of each lane group
+                acc[n][x] = __builtin_amdgcn_mfma_f32_16x16x4f32(v, w, acc[n][x], 0, 0, 0);
+              } else {  // sixteen products of the four lanes that share j / 4 and G
+                acc[n][x] = __builtin_amdgcn_mfma_f32_4x4x1f32(v, w, acc[n][x], 0, 0, 0);
+              }
             }
           }
         }
-      }
-    } else {
-      half8 ph;
-      if constexpr (VK == C_F16) {
+      } else {
+        half8 ph;
+        if constexpr (VK == C_F16) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) ph[k] = (_Float16)p[k];
-      }
-#pragma unroll
-      for (int n = 0; n < NB; ++n) {
-        if constexpr (VK != C_F16) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k)  // one v_fma_mix each
-            ph[k] = (_Float16)__builtin_fmaf(p[v_token<VK>(k)], (float)vd[n][v_token<VK>(k)], 0.0f);
+          for (int k = 0; k < 8; ++k) ph[k] = (_Float16)p[k];
         }
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
-          acc[n][x] = __builtin_amdgcn_mfma_f32_16x16x32_f16(value_operand<VK>(vr[n], x, nb), ph, acc[n][x], 0, 0, 0);
+        for (int n = 0; n < NB; ++n) {
+          if constexpr (VK != C_F16) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)  // one v_fma_mix each
+              ph[k] = (_Float16)__builtin_fmaf(p[v_token<VK>(k)], (float)vd[n][v_token<VK>(k)], 0.0f);
+          }
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+            acc[n][x] = __builtin_amdgcn_mfma_f32_16x16x32_f16(value_operand<VK>(vr[n], x, nb), ph, acc[n][x], 0, 0, 0);
+        }
       }
+      load_values(next, in_next);
+      there = there_next;
+      page_next = page_after, in_next = in_after;
+      g += kWaves;
     }
-    load_values(next, in_next);
-    there = there_next;
-    page_next = page_after, in_next = in_after;
-    g += kWaves;
-  }
-  sum = sum_over_groups(sum);
+    add_part();
+  } while (g < ge);
+  sum = sum_over_groups(sum + rest);
 
-  // The four waves' parts, joined through LDS with their references.  Where the
-  // heads are too many for four parts in LDS, waves 2 and 3 first hand theirs
-  // to waves 0 and 1.
-  if constexpr (COLS == 4) {
-#pragma unroll
-    for (int n = 0; n < NB; ++n)
-#pragma unroll
-      for (int x = 0; x < 2; ++x)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) acc[n][x][r] = sum_over_groups(acc[n][x][r]);
-  }
-  const int parts = lds_parts(a.heads);
-  float *ml = lds + parts * a.heads * kPitch;  // [part][heads][2]
-  auto put_part = [&](int w) {
-    if (G == 0 && j < heads) {
-      ml[(w * a.heads + j) * 2] = R;
-      ml[(w * a.heads + j) * 2 + 1] = sum;
-    }
-    if (j % COLS >= heads) return;
-    float *o = lds + (w * a.heads + j % COLS) * kPitch + (COLS == 16 ? G : j / 4) * 4;
-#pragma unroll
-    for (int n = 0; n < NB; ++n)
-#pragma unroll
-      for (int x = 0; x < 2; ++x)
-        if (COLS == 16 || G == x) *(floatx4 *)(o + n * 32 + x * 16) = acc[n][x] * kUnit;
-  };
-  if (COLS == 16 && parts == 2) {
-    if (wave >= 2) put_part(wave - 2);
-    __syncthreads();
-    if (wave < 2 && j < heads) {
-      const float Ro = ml[(wave * a.heads + j) * 2], Rn = fmaxf(R, Ro);
-      const float f = __builtin_amdgcn_exp2f(R - Rn), fo = __builtin_amdgcn_exp2f(Ro - Rn);
-      const float *o = lds + (wave * a.heads + j) * kPitch + 4 * G;
-#pragma unroll
-      for (int n = 0; n < NB; ++n)
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-          acc[n][x] = acc[n][x] * f + *(const floatx4 *)(o + n * 32 + x * 16) * (fo / kUnit);
-      sum = sum * f + ml[(wave * a.heads + j) * 2 + 1] * fo;
-      R = Rn;
-    }
-    __syncthreads();
-    if (wave < 2) put_part(wave);
-  } else {
-    put_part(wave);
+  // The four waves' parts, joined through LDS with their references.
+  if (G == 0 && j < heads) {
+    ml[(wave * a.heads + j) * 2] = R;
+    ml[(wave * a.heads + j) * 2 + 1] = sum;
   }
   __syncthreads();
   for (int i = threadIdx.x; i < heads * (D / 4); i += 64 * kWaves) {
     const int h = i / (D / 4), d = i % (D / 4) * 4;
     float Rm = kFloor, l = 0.0f;
-    for (int w = 0; w < parts; ++w) Rm = fmaxf(Rm, ml[(w * a.heads + h) * 2]);
+    for (int w = 0; w < kWaves; ++w) Rm = fmaxf(Rm, ml[(w * a.heads + h) * 2]);
     floatx4 o = {0, 0, 0, 0};
-    for (int w = 0; w < parts; ++w) {
+    for (int w = 0; w < kWaves; ++w) {
       const float f = __builtin_amdgcn_exp2f(ml[(w * a.heads + h) * 2] - Rm);
       l = __builtin_fmaf(f, ml[(w * a.heads + h) * 2 + 1], l);
       o += *(const floatx4 *)(lds + (w * a.heads + h) * kPitch + d) * f;
@@ -776,11 +807,13 @@ hipError_t launch_plan(const Args &a, hipStream_t s);
 template <int KK, int VK, int NB, typename QT, int COLS>
 static hipError_t run_cols(Args &a, hipStream_t s) {
   static std::atomic<int> per_cu{0};
-  auto lds = [](int heads) { return (unsigned)(lds_parts(heads) * (NB * 32 + 4 + 2) * heads * sizeof(float)); };  // <= 34 KiB
+  auto *kernel = attn_kernel<KK, VK, NB, QT, COLS>;
+  auto lds = [](int heads) { return (unsigned)(kWaves * (NB * 32 + 4 + 2) * heads * sizeof(float)); };  // <= 66 KiB
   int n = per_cu.load(std::memory_order_relaxed);
   if (n == 0) {
-    hipError_t e = hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, attn_kernel<KK, VK, NB, QT, COLS>, 64 * kWaves,
-                                                                std::max(lds(8), lds(16)));
+    hipError_t e = hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds(COLS));
+    if (e != hipSuccess) return e;
+    e = hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, 64 * kWaves, lds(COLS));
     if (e != hipSuccess) return e;
     n = std::max(n, 1);
     per_cu.store(n, std::memory_order_relaxed);
@@ -793,7 +826,7 @@ static hipError_t run_cols(Args &a, hipStream_t s) {
     const hipError_t e = launch_plan(a, s);
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((attn_kernel<KK, VK, NB, QT, COLS>), dim3((unsigned)a.items), dim3(64 * kWaves), lds(a.heads), s, a);
+  hipLaunchKernelGGL(kernel, dim3((unsigned)a.items), dim3(64 * kWaves), lds(a.heads), s, a);
   return hipGetLastError();
 }
 

@@ -505,7 +505,8 @@ int qmm_kv_read(int k_kind, int v_kind, const void *k_pages, const void *v_pages
  * and a block scale (F16: 1) of two tokens with the same t / 8: it counts in
  * elements that are empty in all strong tokens and in blocks far smaller than
  * the others of their head, where a caller for whom they matter takes f32 q.
- * The order of every sum is fixed: a call repeated gives the same bits.
+ * The bound holds at every length: long sums carry what they round off.  The
+ * order of every sum is fixed: a call repeated gives the same bits.
  * n_q is a multiple of n_kv.  workspace: qmm_attn_decode_workspace_bytes(B,
  * n_q, n_kv, head_dim) bytes, 16-byte aligned, overwritten (it need not be
  * initialized); calls sharing it must not overlap.  Nothing depends on the

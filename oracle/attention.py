@@ -148,16 +148,17 @@ def load(kind, is_v, pages, page_size, slot, n_kv, D):
 
 
 # -- attention ---------------------------------------------------------------
-def attend(q, k, v, scale, sink=None, f16=True):
-    """One query head q [D] over k, v [n, D] (binary64): the output and the
-    tolerance of the documented bound, without the output's rounding."""
+def attend(q, k, v, scale, sink=None, f16=True, counts=None):
+    """One query head q [D] over k, v [n, D] (binary64), token t counts[t] times
+    (None: once): the output and the tolerance of the documented bound, without
+    the output's rounding."""
     n, D = k.shape
     if n == 0:
         return np.zeros(D), np.zeros(D)
     q = q.astype(np.float64)
     s = scale * (k @ q)
     top = s.max() if sink is None else max(s.max(), float(sink))
-    p = np.exp(s - top)
+    p = np.exp(s - top) * (1 if counts is None else counts)
     w = p / (p.sum() + (0 if sink is None else np.exp(float(sink) - top)))
     aq = np.abs(q).reshape(-1, 32).sum(-1)
     ak = np.abs(k).reshape(n, -1, 32).max(-1)

@@ -583,6 +583,39 @@ def test_attn_strongest_token_of_zero_value(kk, vk, dt, gap, size):
     check(c.run(dev(q)).cpu().numpy(), *want_with_floor(c, q, dt), f"{kk} {vk} gap={gap}")
 
 
+@pytest.mark.parametrize("kk,vk", [("F16", "F16"), ("Q8_0", "Q4_0"), ("Q4_0", "Q8_0")])
+@pytest.mark.parametrize("G", [1, 6])
+@pytest.mark.parametrize("dt", ["f16", "f32"])
+def test_attn_long_splits(kk, vk, G, dt):
+    """A million tokens in one split (1024 key heads leave no room for more), of nearly equal weight: every entry of the
+    table names the same page, so that the sums repeat the same few additions, whose roundings all go one way."""
+    n, D, H, P = (1 << 20) + 37, 64, 1024, 32
+    g = wl.rng("attn", f"long{kk}{vk}{G}{dt}")
+    q = (g.normal(size=(1, H, 1, D)) * np.linspace(1.0, 0.9, G)[:, None]).astype(NP[dt]).reshape(1, H * G, D)
+    first = q[0, ::G].astype(np.float64)
+    score = np.full((P, 1), -0.41)
+    score[0] = 0.7
+    k = (score[:, :, None] * first * (D ** 0.5 / (first * first).sum(-1, keepdims=True))).astype(np.float32)
+    v = np.abs(g.normal(size=(P, H, D))).astype(np.float32)
+    kp, vp = qmm.kv_pages(kk, 1, P, H, D), qmm.kv_pages(vk, 1, P, H, D)
+    qmm.kv_write(dev(k), dev(v), dev(np.arange(P, dtype=np.int32)), kp, vp, kk, vk, P)
+    kx, vx = (oa.dequantize(kind, *oa.quantize(kind, x)) for kind, x in ((kk, k), (vk, v)))
+    got = qmm.attn_decode(dev(q), kp, vp, torch.zeros((1, n // P + 1), dtype=torch.int32, device="cuda"),
+                          dev(np.array([n], np.int32)), kk, vk, P, H).cpu().numpy()
+    counts = n // P + (np.arange(P) < n % P)
+    for h in range(0, H * G, 97):
+        w, tol = oa.attend(q[0, h], kx[:, h // G], vx[:, h // G], D ** -0.5, f16=dt == "f16", counts=counts)
+        check(got[0, h], w, tol + half_step(w, dt), f"head {h}")
+
+
+@pytest.mark.parametrize("D", [192, 256])
+@pytest.mark.parametrize("dt", ["f16", "f32"])
+def test_attn_many_heads_of_large_size(D, dt):
+    c = Case("Q8_0", "Q8_0", D, 32, 1, [700, 33])
+    q = c.g.normal(size=(2, 16, D)).astype(NP[dt])
+    check(c.run(dev(q)).cpu().numpy(), *c.want(q, dt), f"D={D}")
+
+
 def test_two_streams_at_once():
     """Calls on two streams, each with its own workspace, and the stream argument with outputs allocated by the call."""
     cases = [Case("Q8_0", "Q4_0", 128, 64, 2, [3000, 100]), Case("F16", "F16", 64, 32, 1, [5000])]
