@@ -25,11 +25,12 @@
 //   values   D[element][head] += V^T . P^T; the block scale goes into the
 //            weight, p * d.  Beside f16 queries weights are rounded once to
 //            f16 and codes enter as exact signed integers in f16.  Beside f32
-//            queries weights, codes and halves enter as f32, in f32 products:
-//            v_mfma_f32_16x16x4_f32, or up to four heads
-//            v_mfma_f32_4x4x1_16b_f32, which takes the same 64 values against 4
-//            columns instead of 16 in a quarter of the time (the heads then
-//            fill the 16 score columns four times over).
+//            queries weights are f32: with codes as three bf16 terms of eight
+//            bits each, which have f32's range (codes are exact in bf16 too);
+//            with F16 values in f32 products, v_mfma_f32_16x16x4_f32, or up to
+//            four heads v_mfma_f32_4x4x1_16b_f32, which takes the same 64 values
+//            against 4 columns instead of 16 in a quarter of the time (the heads
+//            then fill the 16 score columns four times over).
 // f32 queries are split into two f16 terms (exact to about 2^-22).
 //
 // The softmax keeps a running reference R per head.  Beside f32 queries it is
@@ -39,13 +40,14 @@
 // down to 2^-28 of it are normal f16 numbers, below that they lose bits, each
 // at most 2^-39 of it (2^-25 against 2^14).  One term so loses what a weak
 // token or a small block contributes to an element that the strong ones leave
-// empty; two f16 terms share the exponent range and lose it too (an element 30
-// below in the exponent: nothing of it was right), which f32 results do not
-// bear.  What the f32 products cost against two f16 terms, 64 sequences of 0 to
-// 8192 tokens, heads of 128: 32 / 8 heads Q8_0 / Q4_0 115 -> 120 us, Q4_0 96 ->
-// 101; 48 windows of 4096, 64 / 8 heads of 64, Q4_0 43 -> 61.  (Four columns
-// instead of 16 for four heads: Q8_0 155 -> 123 us, Q4_0 140 -> 101.  Two products
-// of four columns for eight heads: 159 -> 148 and no change, not kept.)
+// empty; two f16 terms share the exponent range and lose it too (all of it from
+// e^-30 down), which f32 results do not bear.  What the wider terms cost against
+// two f16 ones, 64 sequences of 0 to 8192 tokens of 8 key heads, f32 queries: 32
+// heads of 128, Q8_0 119 -> 121 us, Q4_0 95 -> 101, F16 197 -> 197; 64 heads of 128,
+// 123 -> 127, 96 -> 106, 202 -> 211; 32 heads of 256, 240 -> 268, 208 -> 271, 386
+// -> 388.  Measured against each other: f32 products of 16 columns for codes, 64
+// heads of 128, Q8_0 158 us, Q4_0 141; four columns for 32 heads of 128 120 and
+// 101, of 256 278 and 292; F16 values with 32 heads of 128 in 16 columns 203.
 //
 // Sums.  A split may hold any number of tokens, and a running f32 sum of
 // like terms rounds the same way each time.  The weights' sum takes eight at a
@@ -92,6 +94,7 @@ using kv::C_Q8_0;
 typedef _Float16 half8 __attribute__((ext_vector_type(8)));
 typedef _Float16 half2v __attribute__((ext_vector_type(2)));
 typedef uint16_t ushort2v __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float floatx4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -264,6 +267,11 @@ __device__ __forceinline__ uint32_t pk_fma(uint32_t a, _Float16 m, _Float16 b) {
   return __builtin_bit_cast(uint32_t, v);
 }
 
+__device__ __forceinline__ uint32_t bits_of(float v) { return __builtin_bit_cast(uint32_t, v); }
+__device__ __forceinline__ uint32_t upper_halves(float a, float b) {  // a's in the low half
+  return __builtin_amdgcn_perm(bits_of(b), bits_of(a), 0x07060302);
+}
+
 // Bytes of one block as a lane reads them.
 template <int KIND> struct Raw { u32x4 w; };  // Q8_0
 template <> struct Raw<C_F16> { u32x4 w[2]; };
@@ -349,19 +357,21 @@ __device__ __forceinline__ constexpr int v_token(int k) {
   return (k & 4) + (p == 1 ? 2 : p == 2 ? 1 : p);
 }
 
-// For f32 products: codes of values as signed bytes (four tokens a word) of tile
-// x, Q8_0's own, Q4_0's times 16 (the nibble, its top bit turned, in the upper
-// half).
+// Value operand of tile x beside f32 queries: codes (Q4_0's times 16) in bf16, in
+// natural order.  A signed byte (Q4_0: the nibble in the upper half, its top bit
+// turned) becomes f32, whose upper half holds it.
 template <int VK>
-__device__ __forceinline__ uint32_t value_codes(const Raw<VK> &r, int x, int i) {
-  if constexpr (VK == C_Q8_0) return r.w[2 * x + i] ^ 0x80808080u;
-  if constexpr (VK == C_Q4_0) return ((x == 0 ? r.w[i] << 4 : r.w[i]) & 0xf0f0f0f0u) ^ 0x80808080u;
-}
-// Value of token k of tile x, in that unit.
-template <int VK>
-__device__ __forceinline__ float value_f32(const Raw<VK> &r, int x, int k) {
-  if constexpr (VK == C_F16) return (float)as_h8(r.w[x])[k];
-  else return (float)(int8_t)(value_codes<VK>(r, x, k >> 2) >> (8 * (k & 3)));
+__device__ __forceinline__ bf16x8 value_bf16(const Raw<VK> &r, int x) {
+  u32x4 u;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    uint32_t c;
+    if constexpr (VK == C_Q8_0) c = r.w[2 * x + i] ^ 0x80808080u;
+    else c = ((x == 0 ? r.w[i] << 4 : r.w[i]) & 0xf0f0f0f0u) ^ 0x80808080u;
+    u[2 * i] = upper_halves((float)(int8_t)c, (float)(int8_t)(c >> 8));
+    u[2 * i + 1] = upper_halves((float)(int8_t)(c >> 16), (float)(int8_t)(c >> 24));
+  }
+  return __builtin_bit_cast(bf16x8, u);
 }
 
 // The query elements of the eight K entries of lane group G, of a block of 32
@@ -396,11 +406,11 @@ __device__ __forceinline__ void store_out(QT *out, floatx4 o, float l, float R, 
   *(q4 *)out = q4{(QT)(o[0] * inv), (QT)(o[1] * inv), (QT)(o[2] * inv), (QT)(o[3] * inv)};
 }
 
-// COLS: 16, or 4 for f32 queries of up to four heads.
+// COLS: 16, or 4 for f32 queries of up to four heads over F16 values.
 template <int KK, int VK, int NB, typename QT, int COLS>
 __global__ __launch_bounds__(64 * kWaves) void attn_kernel(Args a) {
   constexpr int D = NB * 32;
-  constexpr bool SPLIT = sizeof(QT) == 4;  // two f16 terms of the query, f32 weights
+  constexpr bool SPLIT = sizeof(QT) == 4;  // two terms of the query, f32 weights
   constexpr float kUnit = SPLIT && VK == C_Q4_0 ? 0.0625f : 1.0f;  // of the accumulators
   constexpr bool SUB = kSubnormalKeys<KK, SPLIT>;
   constexpr int kPitch = D + 4;
@@ -725,22 +735,43 @@ __global__ __launch_bounds__(64 * kWaves) void attn_kernel(Args a) {
       sum += eight;
       rest += eight - (sum - before);
 
-      if constexpr (SPLIT) {
+      if constexpr (SPLIT && VK == C_F16) {
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            float w = p[k];
-            if constexpr (VK != C_F16) w = __builtin_fmaf(w, (float)vd[n][k], 0.0f);  // one v_fma_mix
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-              const float v = value_f32<VK>(vr[n], x, k);
-              if constexpr (COLS == 16) {  // K entries: token k of each lane group
-                acc[n][x] = __builtin_amdgcn_mfma_f32_16x16x4f32(v, w, acc[n][x], 0, 0, 0);
-              } else {  // sixteen products of the four lanes that share j / 4 and G
-                acc[n][x] = __builtin_amdgcn_mfma_f32_4x4x1f32(v, w, acc[n][x], 0, 0, 0);
-              }
+              const float v = (float)as_h8(vr[n].w[x])[k];
+              if constexpr (COLS == 16)  // K entries: token k of each lane group
+                acc[n][x] = __builtin_amdgcn_mfma_f32_16x16x4f32(v, p[k], acc[n][x], 0, 0, 0);
+              else  // sixteen products of the four lanes that share j / 4 and G
+                acc[n][x] = __builtin_amdgcn_mfma_f32_4x4x1f32(v, p[k], acc[n][x], 0, 0, 0);
             }
+          }
+        }
+      } else if constexpr (SPLIT) {
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+          float w[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) w[k] = __builtin_fmaf(p[k], (float)vd[n][k], 0.0f);  // one v_fma_mix
+          // The weight's 24 bits, eight to a term: each cut off, the rest exact.
+          bf16x8 term[3];
+#pragma unroll
+          for (int t = 0; t < 3; ++t) {
+            u32x4 u;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) u[k] = upper_halves(w[2 * k], w[2 * k + 1]);
+            term[t] = __builtin_bit_cast(bf16x8, u);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) w[k] -= __builtin_bit_cast(float, bits_of(w[k]) & 0xffff0000u);
+          }
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const bf16x8 v = value_bf16<VK>(vr[n], x);
+#pragma unroll
+            for (int t = 2; t >= 0; --t) acc[n][x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, term[t], acc[n][x], 0, 0, 0);
           }
         }
       } else {
@@ -832,7 +863,7 @@ static hipError_t run_cols(Args &a, hipStream_t s) {
 
 template <int KK, int VK, int NB, typename QT>
 static hipError_t run(Args &a, hipStream_t s) {
-  if constexpr (sizeof(QT) == 4) {
+  if constexpr (sizeof(QT) == 4 && VK == C_F16) {
     if (a.heads <= 4) return run_cols<KK, VK, NB, QT, 4>(a, s);
   }
   return run_cols<KK, VK, NB, QT, 16>(a, s);

@@ -493,8 +493,7 @@ int qmm_kv_read(int k_kind, int v_kind, const void *k_pages, const void *v_pages
  * Numerics: keys and values are exact (codes as integers, block scales in
  * f32 or folded into the weight); scores, softmax and sums are f32.  f16 q is
  * exact and the weights, times the value's block scale, are rounded once to
- * f16; f32 q is carried as two f16 terms (relative 2^-21), and weights and
- * their products with the values are f32.  With w_t the exact weights,
+ * f16; f32 q is carried as two f16 terms (relative 2^-21), and weights as f32.  With w_t the exact weights,
  *   |out - exact| <= (r + 2 max_t e_t) sum_t w_t |v_t| + a  (+ f16 out's rounding)
  * where r = 2^-11 + 2^-18 for f16 and 2^-18 for f32, and e_t = c (scale * sum
  * over 32-element blocks of (sum |q|) (max |k_t|) + max |s| + 40) with c =
