@@ -397,7 +397,11 @@ template <typename QT>
 __device__ __forceinline__ void store_out(QT *out, floatx4 o, float l, float R, const float *sinks, int head) {
   float f = 1.0f;
   if (sinks) {
-    const float sink = sinks[head] * 1.44269504f, Rn = fmaxf(R, sink);
+    // (Cut where it would overflow: an infinite sink takes all the weight, like
+    // any other far above the scores.  A NaN stays.)
+    float sink = sinks[head] * 1.44269504f;
+    sink = sink > 3e38f ? 3e38f : sink;
+    const float Rn = fmaxf(R, sink);
     f = __builtin_amdgcn_exp2f(R - Rn);
     l = __builtin_fmaf(l, f, __builtin_amdgcn_exp2f(sink - Rn));
   }

@@ -516,6 +516,20 @@ def test_attn_nonfinite_value_stays_in_its_elements(vk):
     check(got, want, tol, "the other elements")
 
 
+@pytest.mark.parametrize("dt", ["f16", "f32"])
+def test_attn_sinks_at_the_ends_of_their_range(dt):
+    """Infinite sinks and those whose base-2 logarithm overflows take all the weight or none; a NaN is one head's own."""
+    c = Case("Q8_0", "Q4_0", 64, 32, 1, [40, 1, 0, 3000])
+    q = c.g.normal(size=(4, 6, 64)).astype(NP[dt])
+    sinks = np.array([np.inf, 3e38, -np.inf, -3.4e38, np.nan, 1.0], np.float32)
+    got = c.run(dev(q), sinks=dev(sinks)).cpu().numpy()
+    want, tol = c.want(q, dt, sinks=[-1e30, -1e30, -1e30, -1e30, 0.0, 1.0])
+    want[:, :2] = tol[:, :2] = 0
+    assert np.isnan(got[[0, 1, 3], 4]).all()
+    got[:, 4] = want[:, 4] = 0
+    check(got, want, tol, "sinks")
+
+
 def rewrite_kv(c):
     """c.k and c.v, changed, into the cache and as the oracle's exact values."""
     t = [np.arange(n) for n in c.lens]
