@@ -8,6 +8,7 @@ instructions, hidden visibility except for the C ABI.
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -80,7 +81,10 @@ def build(jobs: int = 8, verbose: bool = False) -> str:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIBRARY)
     build_probe(cc)
-    build_call()
+    if importlib.util.find_spec("torch"):  # the C library needs only hipcc
+        build_call(cc)
+    elif verbose:
+        print(f"torch is not installed: {CALL_MODULE} not built")
     return LIBRARY
 
 
@@ -93,9 +97,10 @@ def build_probe(cc: str) -> str:
     return PROBE_LIBRARY
 
 
-def build_call() -> str:
+def build_call(cc: str) -> str:
     from torch.utils import cpp_extension
-    includes = [*cpp_extension.include_paths(), sysconfig.get_paths()["include"], "/opt/rocm/include"]
+    rocm = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(cc))), "include")
+    includes = [*cpp_extension.include_paths(), sysconfig.get_paths()["include"], rocm]
     torch_lib = os.path.join(os.path.dirname(includes[0]), "lib")
     tmp = CALL_MODULE + ".tmp"
     r = subprocess.run(["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-Wall",
