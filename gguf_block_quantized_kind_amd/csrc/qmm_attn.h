@@ -837,28 +837,32 @@ __global__ __launch_bounds__(64 * kWaves) void attn_kernel(Args a) {
 
 hipError_t launch_plan(const Args &a, hipStream_t s);
 
-// How many workgroups the GPU holds is looked up once per instantiation (with
-// the most LDS a call uses).
+// How many workgroups the GPU holds is looked up once per instantiation and
+// device (with the most LDS a call uses).
 template <int KK, int VK, int NB, typename QT, int COLS>
 static hipError_t run_cols(Args &a, hipStream_t s) {
-  static std::atomic<int> per_cu{0};
+  static std::atomic<int> slots[64];
   auto *kernel = attn_kernel<KK, VK, NB, QT, COLS>;
   auto lds = [](int heads) { return (unsigned)(kWaves * (NB * 32 + 4 + 2) * heads * sizeof(float)); };  // <= 66 KiB
-  int n = per_cu.load(std::memory_order_relaxed);
-  if (n == 0) {
-    hipError_t e = hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds(COLS));
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return e;
+  if (dev < 0 || dev >= 64) return hipErrorInvalidDevice;
+  a.slots = slots[dev].load(std::memory_order_relaxed);
+  if (a.slots == 0) {
+    int n = 0;
+    e = hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds(COLS));
     if (e != hipSuccess) return e;
     e = hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, 64 * kWaves, lds(COLS));
     if (e != hipSuccess) return e;
-    n = std::max(n, 1);
-    per_cu.store(n, std::memory_order_relaxed);
+    a.slots = std::min(std::max(n, 1) * device_cus(), kMaxSlots);
+    slots[dev].store(a.slots, std::memory_order_relaxed);
   }
-  a.slots = std::min(n * device_cus(), kMaxSlots);
   // Splits of the longest sequences the page table can hold, and of any batch.
   const int64_t nh = a.n_kv * a.tiles, most = a.max_pages * a.page_groups;
   a.items = std::min(2 * a.slots + a.B * nh, a.B * nh * ((most + kMinGroups - 1) / kMinGroups));
   if (a.B > kLanes) {
-    const hipError_t e = launch_plan(a, s);
+    e = launch_plan(a, s);
     if (e != hipSuccess) return e;
   }
   hipLaunchKernelGGL(kernel, dim3((unsigned)a.items), dim3(64 * kWaves), lds(a.heads), s, a);

@@ -32,6 +32,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "qmm_internal.h"
+
 namespace qmm {
 namespace kv {
 
@@ -272,7 +274,7 @@ inline bool plan_rotate(Rotate &r, int x_bytes, int y_bytes, int64_t &threads) {
                     (uintptr_t)r.x % (v * x_bytes) == 0 && (uintptr_t)r.y % (v * y_bytes) == 0;
   r.chunks = r.D / 2 / (wide ? v : 1);
   // Heads per thread: one until the grid holds eight waves per SIMD.
-  const int64_t one = r.T * r.chunks * r.H, full = (int64_t)256 * 4 * 8 * 64;
+  const int64_t one = r.T * r.chunks * r.H, full = (int64_t)device_cus() * 4 * 8 * 64;
   r.per = (int)(one / full < 1 ? 1 : one / full > r.H ? r.H : one / full);
   r.ranges = (r.H + r.per - 1) / r.per;
   threads = r.T * r.chunks * r.ranges;

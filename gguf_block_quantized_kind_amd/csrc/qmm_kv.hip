@@ -542,7 +542,7 @@ __global__ __launch_bounds__(64 * kWaves) void kv_read_kernel(ReadArgs a) {
 // (32768 tokens of 8 x 128 in Q4_0: two heads a wave write in 72 us and read
 // in 37, one in 82 and 41, four in 77 and 41, all eight in 90 and 47).
 static void split_heads(int64_t T, int64_t n_kv, int &per, int &ranges, int64_t &wgs) {
-  const int64_t one = (T + 7) / 8 * 2 * n_kv, full = 4 * 256 * 4 * 8;
+  const int64_t one = (T + 7) / 8 * 2 * n_kv, full = (int64_t)4 * device_cus() * 4 * 8;
   per = (int)std::min(std::max(one / full, (int64_t)1), n_kv);
   ranges = (int)((n_kv + per - 1) / per);
   wgs = (T + 8 * kWaves - 1) / (8 * kWaves) * 2 * ranges;
