@@ -663,7 +663,8 @@ def rope_freqs(n_rot: int, base: float = 10000.0, factors=None, factor: float = 
 
 def rope(x, positions, freqs, layout="half", mscale: float = 1.0, out=None, out_dtype=None, stream=None):
     """x [T, H, head_dim] with the first 2 * len(freqs) elements of each head
-    turned by positions [T] int32; out may be x."""
+    turned by positions [T] int32; out may be x.  Without out, the result is of
+    out_dtype (x's type if None)."""
     fn = (_ops or _load_ops()).rope
     if stream is not None:
         return _on(stream, x, fn, x, positions, freqs, layout, mscale, out, out_dtype)

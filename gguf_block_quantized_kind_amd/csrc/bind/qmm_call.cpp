@@ -135,6 +135,11 @@ at::Device one_gpu(std::initializer_list<const at::Tensor *> ts) {
       raise(PyExc_ValueError, "operands must be on one GPU, got ", t->device(), " with ", d);
   return d;
 }
+// A type asked for beside a tensor to write into has to be that tensor's.
+void check_out_type(PyObject *out, PyObject *dtype, const char *what) {
+  if (out != Py_None && dtype != Py_None && tensor(out, what).scalar_type() != type_of(dtype))
+    raise(PyExc_TypeError, what, " is ", tensor(out, what).scalar_type(), ", the type asked for is ", type_of(dtype));
+}
 at::Tensor make(const at::Tensor &like, at::IntArrayRef shape, at::ScalarType t) {
   return at::empty(shape, at::TensorOptions().dtype(t).device(like.device()));
 }
@@ -186,6 +191,7 @@ PyObject *rope(PyObject *const *a) {
   const double *f = freqs_of(freqs, n_rot);
   const int layout = layout_of(a[3]);
   const float mscale = (float)number(a[4]);
+  check_out_type(a[5], a[6], "out");
   const at::Device d = one_gpu({&x, &pos, &freqs});
   Out out(a[5], a[6], x, r);
   call(d, p_qmm_rope, f, n_rot, layout, mscale, p, (const void *)x.data_ptr(), code(x.scalar_type()), r.stride,
@@ -231,6 +237,7 @@ PyObject *kv_append(PyObject *const *a) {
   const double *f = freqs_of(freqs, n_rot);
   const int layout = layout_of(a[11]);
   const float mscale = (float)number(a[12]);
+  check_out_type(a[13], a[14], "out");
   const at::Device d = one_gpu({&q, &k, &v, &pos, &slots, &kp, &vp, &freqs});
   Out out(a[13], a[14], q, r);
   call(d, p_qmm_kv_append, f, n_rot, layout, mscale, p, (const void *)q.data_ptr(), r.stride, r.H, out.t.data_ptr(),
@@ -245,6 +252,7 @@ PyObject *kv_read(PyObject *const *a) {
   const int64_t T = slots.numel(), H = integer(a[6]), D = integer(a[7]);
   const int32_t *s = ints_of(slots, T, "slots");
   const Cache c = cache_of(kp, vp, a[3], a[4], a[5], H, D);
+  check_out_type(a[9], a[8], "k_out");
   const at::Device d = one_gpu({&slots, &kp, &vp});
   const bool given = a[9] != Py_None;
   if (given != (a[10] != Py_None)) raise(PyExc_ValueError, "k_out and v_out go together");

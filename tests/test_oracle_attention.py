@@ -313,3 +313,19 @@ def test_python_checks_of_other_operands(lib):
             qmm.attn_decode(*good, **kw)
     with pytest.raises(TypeError):
         qmm._load_ops().rope(x)                                         # too few arguments
+
+
+def test_an_output_tensor_of_another_type_than_asked_for_is_refused(lib):
+    """Not written in its own type without a word."""
+    torch = pytest.importorskip("torch")
+    x = torch.zeros((3, 2, 64), dtype=torch.float16)
+    pos, (f, m) = torch.arange(3, dtype=torch.int32), qmm.rope_freqs(64, device="cpu")
+    kp = torch.zeros((4, qmm.kv_page_bytes("F16", 32, 2, 64)), dtype=torch.uint8)
+    cache = (kp, kp, "F16", "F16", 32)
+    for call in (lambda t: qmm.rope(x, pos, f, out=x, out_dtype=t),
+                 lambda t: qmm.kv_append(x, x, x, pos, pos, *cache, f, out=x, out_dtype=t),
+                 lambda t: qmm.kv_read(pos, *cache, 2, 64, dtype=t, k_out=x, v_out=x)):
+        with pytest.raises(TypeError, match="asked for"):
+            call(torch.float32)
+        with pytest.raises(ValueError, match="on one GPU"):             # host tensors, refused after the types
+            call(torch.float16)
