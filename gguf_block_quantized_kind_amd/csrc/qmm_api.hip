@@ -527,6 +527,9 @@ QMM_EXPORT int qmm_rope_freqs(double *freqs, float *mscale, int64_t n_rot, doubl
   const bool yarn = orig_ctx > 0 && factor > 1.0;
   if (yarn && !(beta_slow > 0.0 && beta_fast > beta_slow))
     return fail(QMM_ERR_BAD_ARG, "YaRN needs beta_fast > beta_slow > 0, got %g and %g", beta_fast, beta_slow);
+  for (int64_t i = 0; factors && i < n_rot / 2; ++i)
+    if (!isfinite(factors[i]) || factors[i] == 0.0f)
+      return fail(QMM_ERR_BAD_ARG, "factors[%lld]=%g is zero or not finite", (long long)i, (double)factors[i]);
   const double n = (double)n_rot;
   double low = 0.0, high = 1.0;
   if (yarn) {

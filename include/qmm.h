@@ -431,8 +431,8 @@ enum qmm_rope_layout { QMM_ROPE_HALF = 0, QMM_ROPE_INTERLEAVED = 1 };
  *                  (weight 1 - ramp) and freqs[i] / factor (ramp).
  * *mscale (if not NULL) becomes 0.1 ln(factor) + 1 for YaRN, else 1.
  * Errors: n_rot <= 0 QMM_ERR_EMPTY_SHAPE; odd n_rot, NULL freqs, base <= 1,
- * factor < 1 (or not finite), negative orig_ctx, or YaRN without
- * beta_fast > beta_slow > 0 QMM_ERR_BAD_ARG. */
+ * factor < 1 (or not finite), negative orig_ctx, YaRN without beta_fast >
+ * beta_slow > 0, or one of factors zero or not finite QMM_ERR_BAD_ARG. */
 int qmm_rope_freqs(double *freqs, float *mscale, int64_t n_rot, double base, const float *factors, double factor,
                    int64_t orig_ctx, double beta_fast, double beta_slow);
 

@@ -329,3 +329,12 @@ def test_an_output_tensor_of_another_type_than_asked_for_is_refused(lib):
             call(torch.float32)
         with pytest.raises(ValueError, match="on one GPU"):             # host tensors, refused after the types
             call(torch.float16)
+
+
+def test_rope_factors_that_leave_no_angle_are_refused(lib):
+    """A zero or non-finite per-pair divisor made infinite or NaN angles, and so NaN rows."""
+    for bad in (0.0, math.inf, -math.inf, math.nan):
+        with pytest.raises(qmm.QmmError, match="factors"):
+            qmm.rope_freqs(8, factors=[1.0, 2.0, bad, 1.0], device="cpu")
+    f, _ = qmm.rope_freqs(8, factors=[1.0, 2.0, -4.0, 1.0], device="cpu")
+    assert np.allclose(f.numpy(), 10000.0 ** (-np.arange(4) / 4) / [1, 2, -4, 1], rtol=1e-14)
