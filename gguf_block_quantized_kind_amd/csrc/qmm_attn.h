@@ -31,23 +31,28 @@
 //            four heads v_mfma_f32_4x4x1_16b_f32, which takes the same 64 values
 //            against 4 columns instead of 16 in a quarter of the time (the heads
 //            then fill the 16 score columns four times over).
-// f32 queries are split into two f16 terms (exact to about 2^-22).
+// f32 queries are split into two f16 terms (exact to about 2^-22 of an element, or
+// 2^-39 of the head's largest).
 //
 // The softmax keeps a running reference R per head.  Beside f32 queries it is
-// the running maximum.  Beside f16 queries it is the maximum of (maximum of s
+// the running maximum - 40, so that the last terms of a weight 2^-100 of the
+// largest, times the smallest scale 2^-24, are still normal.  Beside f16 queries it is the maximum of (maximum of s
 // over eight tokens + exponent of their largest value scale) - 14, so that p * d =
 // 2^(s - R) * d reaches 2^14..2^15 for the strongest token and block: weights
 // down to 2^-28 of it are normal f16 numbers, below that they lose bits, each
 // at most 2^-39 of it (2^-25 against 2^14).  One term so loses what a weak
 // token or a small block contributes to an element that the strong ones leave
 // empty; two f16 terms share the exponent range and lose it too (all of it from
-// e^-30 down), which f32 results do not bear.  What the wider terms cost against
-// two f16 ones, 64 sequences of 0 to 8192 tokens of 8 key heads, f32 queries: 32
-// heads of 128, Q8_0 119 -> 121 us, Q4_0 95 -> 101, F16 197 -> 197; 64 heads of 128,
-// 123 -> 127, 96 -> 106, 202 -> 211; 32 heads of 256, 240 -> 268, 208 -> 271, 386
-// -> 388.  Measured against each other: f32 products of 16 columns for codes, 64
-// heads of 128, Q8_0 158 us, Q4_0 141; four columns for 32 heads of 128 120 and
-// 101, of 256 278 and 292; F16 values with 32 heads of 128 in 16 columns 203.
+// e^-30 down), which f32 results do not bear.  f16 results do: the wider terms
+// would bring them from 2.3e-4 to 2.0e-4 of the exact norm, of which the result's
+// own rounding is 2.0e-4, for 95 -> 102 us (64 ragged sequences) and 32 -> 38 (48
+// windows).  What they cost f32 queries against two f16 terms, 64 sequences of 0
+// to 8192 tokens, 8 key heads: 32 heads of 128, Q8_0 119 -> 121 us, Q4_0 95 -> 101,
+// F16 197 -> 197; 64 heads of 128, 123 -> 127, 96 -> 106, 202 -> 211; 32 heads of
+// 256, 240 -> 268, 208 -> 271, 386 -> 388.  The f32 forms against each other: f32
+// products of 16 columns for codes, 64 heads of 128, Q8_0 158 us, Q4_0 141; of four
+// columns for 32 heads of 128 120 and 101, of 256 278 and 292; F16 values with 32
+// heads of 128 in 16 columns 203.
 //
 // Sums.  A split may hold any number of tokens, and a running f32 sum of
 // like terms rounds the same way each time.  The weights' sum takes eight at a
@@ -56,20 +61,24 @@
 // addition rounds off.  So the error does not grow with the length (plain running
 // sums: 1e-3 at a million tokens of a split; no difference in time measured).
 //
-// What bounds it: the cache's bytes, read once at the rate of a large copy
-// (5.1 TB/s here) as soon as there are enough of them.  Measured, the attention
+// What bounds it: the cache's bytes, read once at the rate of a large read (5.5
+// TB/s here) as soon as there are enough of them.  Measured, the attention
 // kernel alone: one sequence of 131071 tokens, 32 / 8 heads of 128, Q8_0 keys
 // and values (285 MB) 53 us, 5.3 TB/s; 64 sequences of 0 to 8192 tokens, Q8_0
-// and Q4_0 (437 MB) 90 us, 4.9 TB/s; 16 of 0 to 4001, 32 / 32 heads, F16, f32
-// queries (474 MB) 86 us, 5.5 TB/s; 48 windows of 4096, 64 / 8 heads of 64, Q4_0
-// (99 MB) 28 us, 3.5 TB/s, of which about 8 are starts and ends.  Choices that
-// were measured against another:
+// and Q4_0 (437 MB) 91 us, 4.8 TB/s, in Q8_0 with heads of 96 (429 MB) 83 us, of
+// 192 (857 MB) 160 us, of 256 (1.14 GB) 218 us, 5.2 to 5.3 TB/s; 16 of 0 to 4001,
+// 32 / 32 heads, F16, f32 queries (474 MB) 86 us, 5.5 TB/s; 48 windows of 4096,
+// 64 / 8 heads of 64, Q4_0 (99 MB) 29 us, 3.4 TB/s, of which about 8 are starts and
+// ends; 1024 sequences of 0 to 600, Q8_0 (683 MB) 144 us, 4.8 TB/s, after a plan of
+// 5.  Choices that were measured against another:
 //   accumulators in vector registers instead of accumulation registers (which
-//     cost 112 moves a group), one fused multiply-convert per weight: 64
-//     ragged sequences 120 -> 92 us;
+//     cost 112 moves a group at heads of 128), one fused multiply-convert per
+//     weight: 64 ragged sequences 120 -> 92 us.  Heads of 256 spill into
+//     accumulation registers in most kinds and leave one wave per SIMD; a bound
+//     of two waves spills to memory instead (f32 queries, Q8_0: 282 -> 816 us);
 //   keys of the next group loaded as soon as this one's are used, values
-//     likewise; two or three whole groups at once in flight hold so many more
-//     registers that a wave per SIMD is lost: 92 -> 90 and 113 us there;
+//     likewise: 92 us there against 113 with two or three whole groups in flight
+//     at once, whose registers cost a wave per SIMD;
 //   one equal range of the batch's groups per workgroup, in one round, instead
 //     of splits: 92 -> 119 us (all workgroups start and end together, and a
 //     range covers two pairs' ends);
@@ -104,7 +113,11 @@ constexpr float kFar = 0x1p20f;  // scores whose products are rounded by more th
 constexpr int kWaves = 4;
 constexpr int kMinGroups = 4;  // groups per split at least: one per wave
 constexpr int kMaxSlots = 1280;  // most workgroups counted on at once (five on each of 256 compute units)
-constexpr float kOverhead = 8.0f;  // a workgroup's start and end, in groups' time
+// A workgroup's start and end, in groups' time, for the choice between one round
+// of splits and two.  With 2, 8 and 32: 48 windows of 4096, 8 heads of 64 in Q4_0
+// (groups of 2 KB) 39, 33, 33 us; 64 ragged sequences, heads of 128 in Q8_0 and
+// Q4_0 96.4, 95.8, 102.4; heads of 256 in F16 (32 KB) no difference.
+constexpr float kOverhead = 8.0f;
 
 struct Args {
   const uint8_t *kp, *vp;
@@ -289,9 +302,9 @@ __device__ __forceinline__ void load_block(const uint8_t *block, int lane, Raw<K
   }
 }
 
-// Eight bytes of Q8_0, or the nibbles of pairs of Q4_0 bytes, as exact signed integers in f16: the code under the mantissa of
-// 1024 (a high nibble 16 times too high), the offset taken off by one packed
-// operation.
+// Eight bytes of Q8_0, or the nibbles of pairs of Q4_0 bytes, as exact signed
+// integers in f16: the code under the mantissa of 1024 (a high nibble 16 times
+// too high), the offset taken off by one packed operation.
 __device__ __forceinline__ half8 signed_bytes(uint32_t a, uint32_t b) {
   const uint32_t k = 0x64646464;  // 1024 + u
   return as_h8(u32x4{pk_add(__builtin_amdgcn_perm(k, a, 0x04010400), -1152.0f16),
@@ -395,17 +408,18 @@ __device__ __forceinline__ void load_q(const QT *q, int G, float (&v)[8]) {
 // zeros where nothing was attended.
 template <typename QT>
 __device__ __forceinline__ void store_out(QT *out, floatx4 o, float l, float R, const float *sinks, int head) {
-  float f = 1.0f;
+  float root = 1.0f;  // of the sums' factor, which may lie below f32's range
   if (sinks) {
     // (Cut where it would overflow: an infinite sink takes all the weight, like
     // any other far above the scores.  A NaN stays.)
     float sink = sinks[head] * 1.44269504f;
     sink = sink > 3e38f ? 3e38f : sink;
     const float Rn = fmaxf(R, sink);
-    f = __builtin_amdgcn_exp2f(R - Rn);
-    l = __builtin_fmaf(l, f, __builtin_amdgcn_exp2f(sink - Rn));
+    root = __builtin_amdgcn_exp2f(0.5f * (R - Rn));
+    l = __builtin_fmaf(l * root, root, __builtin_amdgcn_exp2f(sink - Rn));
   }
-  const float inv = l > 0.0f || l != l ? f / l : 0.0f;
+  const float inv = l > 0.0f || l != l ? root / l : 0.0f;
+  o *= root;
   typedef QT q4 __attribute__((ext_vector_type(4)));
   *(q4 *)out = q4{(QT)(o[0] * inv), (QT)(o[1] * inv), (QT)(o[2] * inv), (QT)(o[3] * inv)};
 }
@@ -683,7 +697,7 @@ __global__ __launch_bounds__(64 * kWaves) void attn_kernel(Args a) {
 #pragma unroll
       for (int k = 1; k < 8; ++k) top = fmaxf(top, s[k]);
       top *= qscale;
-      float below = SPLIT ? 0.0f : 14.0f;  // 14 - the exponent of the largest value scale
+      float below = SPLIT ? 40.0f : 14.0f;  // f16 weights: 14 - the exponent of the largest value scale
       if constexpr (VK != C_F16 && !SPLIT) {
         // Magnitudes of halves compare as integers (Q8_0 scales have no sign).
         ushort2v part[4] = {{0, 0}, {0, 0}, {0, 0}, {0, 0}};
@@ -712,7 +726,7 @@ __global__ __launch_bounds__(64 * kWaves) void attn_kernel(Args a) {
         below = (float)(127 + 14 - (int)(__builtin_bit_cast(uint32_t, bf) >> 23));
       }
       // (Among scores whose f32 neighbours lie further apart than `below` means,
-      // the reference is the score itself: weights up to 1, not 2^14.)
+      // the reference is the score itself: weights up to 1, not 2^14 or 2^40.)
       top = fabsf(top) < kFar ? top - below : top;
       top = max_over_groups(top);
       if (__any(top > R)) {  // rare after the first groups

@@ -597,6 +597,29 @@ def test_attn_strongest_token_of_zero_value(kk, vk, dt, gap, size):
     check(c.run(dev(q)).cpu().numpy(), *want_with_floor(c, q, dt), f"{kk} {vk} gap={gap}")
 
 
+@pytest.mark.parametrize("vk", KINDS)
+def test_attn_far_weights_of_the_smallest_blocks(vk):
+    """Tokens 2^-98 below the strongest in blocks of the smallest scale, 2^-24, where f32's own range nearly ends."""
+    c = Case("Q8_0", vk, 64, 32, 1, [500, 40])
+    q = c.g.normal(size=(2, 2, 64)).astype(np.float32)
+    q[:, 1] = q[:, 0] * np.float32(0.96875)
+    c.v = (c.v / np.abs(c.v).max() * 4e-6).astype(np.float32)
+    for b, t in ((0, 333), (1, 39)):
+        lone_score(c, b, t, q[b, 0], 68.0)
+        c.v[c.first[b] + t] = 0
+    rewrite_kv(c)
+    check(c.run(dev(q)).cpu().numpy(), *c.want(q, "f32"), vk)
+
+
+@pytest.mark.parametrize("kk,vk", [("F16", "F16"), ("Q4_0", "Q8_0")])
+def test_attn_results_far_below_a_sink(kk, vk):
+    """e^-80 of the values, relative to itself."""
+    c = Case(kk, vk, 64, 32, 1, [70, 3000])
+    q = c.g.normal(size=(2, 2, 64)).astype(np.float32)
+    sinks = np.array([80.0, 75.0], np.float32)
+    check(c.run(dev(q), sinks=dev(sinks)).cpu().numpy(), *c.want(q, "f32", sinks=sinks), "far below")
+
+
 @pytest.mark.parametrize("kk,vk", [("F16", "F16"), ("Q8_0", "Q4_0"), ("Q4_0", "Q8_0")])
 @pytest.mark.parametrize("G", [1, 6])
 @pytest.mark.parametrize("dt", ["f16", "f32"])
