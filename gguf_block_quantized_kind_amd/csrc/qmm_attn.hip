@@ -72,8 +72,11 @@ hipError_t launch_plan(const Args &a, hipStream_t s) {
 // head compute its weights and sums together and read its parts in ways of
 // D / 4 lanes, so that a sequence of a thousand splits costs no chain of a
 // thousand loads.  H = 1 spreads few heads with many splits over the GPU (32
-// heads of 96 splits 5 us), H = 4 makes fewer workgroups of many heads with few
-// splits (48 sequences of 64 heads, 3 splits: 7.5 -> 4.7 us).
+// heads of 96 splits 6 us), H = 4 makes fewer workgroups of many heads with few
+// splits (48 sequences of 64 heads, 3 splits: 7.5 -> 4.7 us).  The change at 1024
+// heads in all, sequences of 4096 with heads of 128, H = 1 and 4: 32 heads 5.4 and
+// 5.9 us, 256 to 768 both 4.2 to 4.6, 1024 4.8 and 4.6, 1536 5.6 and 4.6, 2048 6.2
+// and 4.6.
 template <typename QT, int H>
 __global__ __launch_bounds__(256) void join_kernel(Args a, int D) {
   constexpr int kThreads = 256 / H, kChunk = 1024 / H;

@@ -124,27 +124,35 @@ __device__ __forceinline__ float encode(float x, Step st) {
   return KIND == C_Q8_0 ? fmaxf(q, -127.0f) + 128.0f : fminf(q + 8.0f, 15.0f);
 }
 
-// cos and sin of pos * freq (radians per position), each within about 1e-7.
-// The angle is reduced in 64 bits to an eighth of a turn: a 32-bit angle at
-// position 10^6 would already be off by 0.06.  The rest is the Taylor series
-// on |x| <= pi / 4, whose first omitted terms are below 2e-9.
-__device__ __forceinline__ void rotation(int pos, double freq, float &c, float &s) {
+// A constant in scalar registers (in a loop the compiler would keep it in vector
+// registers, and so waves off the GPU).
+__device__ __forceinline__ double uniform(double v) {
+  asm("" : "+s"(v));
+  return v;
+}
+
+// m cos and m sin of pos * freq (radians per position), computed in 64 bits and
+// rounded once.  (A 32-bit angle at position 10^6 would already be off by 0.06, and
+// a 64-bit product costs what a 32-bit one does here.)  The angle is reduced to an
+// eighth of a turn; there the Taylor series' first omitted terms are below 1e-11.
+__device__ __forceinline__ void rotation(int pos, double freq, float m, float &c, float &s) {
   double t = (double)pos * freq * 0.15915494309189533577;  // turns
   t -= rint(t);
   const double q = rint(4.0 * t);
-  const float x = (float)((t - 0.25 * q) * 6.283185307179586477);
-  const float z = x * x;
-  float sp = __builtin_fmaf(z, 2.7557319e-6f, -1.9841270e-4f);
-  sp = __builtin_fmaf(z, sp, 8.3333333e-3f);
-  sp = __builtin_fmaf(z, sp, -1.6666667e-1f);
-  sp = __builtin_fmaf(z * x, sp, x);
-  float cp = __builtin_fmaf(z, -2.7557319e-7f, 2.4801587e-5f);
-  cp = __builtin_fmaf(z, cp, -1.3888889e-3f);
-  cp = __builtin_fmaf(z, cp, 4.1666667e-2f);
-  cp = __builtin_fmaf(z, cp, -0.5f);
-  cp = __builtin_fmaf(z, cp, 1.0f);
+  const double x = (t - 0.25 * q) * 6.283185307179586477, z = x * x;
+  double sp = __builtin_fma(z, uniform(-1.0 / 39916800), 1.0 / 362880);
+  sp = __builtin_fma(z, sp, uniform(-1.0 / 5040));
+  sp = __builtin_fma(z, sp, uniform(1.0 / 120));
+  sp = __builtin_fma(z, sp, uniform(-1.0 / 6));
+  sp = __builtin_fma(z * x, sp, x);
+  double cp = __builtin_fma(z, uniform(1.0 / 479001600), -1.0 / 3628800);
+  cp = __builtin_fma(z, cp, uniform(1.0 / 40320));
+  cp = __builtin_fma(z, cp, uniform(-1.0 / 720));
+  cp = __builtin_fma(z, cp, uniform(1.0 / 24));
+  cp = __builtin_fma(z, cp, -0.5);
+  cp = __builtin_fma(z, cp, 1.0);
   const int k = (int)q & 3;
-  const float a = (k & 1) ? sp : cp, b = (k & 1) ? cp : sp;
+  const float a = (float)((k & 1 ? sp : cp) * m), b = (float)((k & 1 ? cp : sp) * m);
   c = (k == 1 || k == 2) ? -a : a;
   s = (k & 2) ? -b : b;
 }
@@ -219,11 +227,7 @@ __device__ __forceinline__ void rotate_rows(const Rotate &r, int64_t i) {
   for (int k = 0; k < V; ++k) {
     c[k] = 1.0f;
     s[k] = 0.0f;
-    if (turned) {
-      rotation(r.pos[t], r.rope.freqs[p + k], c[k], s[k]);
-      c[k] *= r.rope.mscale;
-      s[k] *= r.rope.mscale;
-    }
+    if (turned) rotation(r.pos[t], r.rope.freqs[p + k], r.rope.mscale, c[k], s[k]);
   }
   const int h1 = min(r.H, (range + 1) * r.per);
   const T *x = (const T *)r.x + t * r.x_stride;

@@ -321,6 +321,7 @@ __global__ __launch_bounds__(64 * kWaves) void kv_write_kernel(WriteArgs a) {
   const int64_t head_bytes = (int64_t)(a.cache.page_size / kGroup) * group_bytes(kind, NB);
   const uint32_t valid = (uint32_t)__ballot(p.slot >= 0);
   const int half = ROPE ? a.rope.n_rot >> 1 : 0;
+  const uint32_t per_half = ROPE ? (1u << 20) / (uint32_t)half + 1 : 0;
   const bool shifted = p.octet > 8;
 
   for (int pass = 0; pass < 2; ++pass) {
@@ -339,13 +340,12 @@ __global__ __launch_bounds__(64 * kWaves) void kv_write_kernel(WriteArgs a) {
       if (h + 1 < h1) load_rows<T, NB>(next, xp + D, stride, vec, g.mask);
       wave_sync();
       if (ROPE && !is_v) {
+#pragma unroll 1
         for (int i = lane; i < 8 * half; i += 64) {
-          const int t = i / half, q = i - t * half;
+          const int t = (int)(i * per_half >> 20), q = i - t * half;  // i / half: i < 1024
           if (!(g.mask >> t & 1)) continue;
           float c, s;
-          rotation(a.pos[own - 8 + g.first + t], a.rope.freqs[q], c, s);
-          c *= a.rope.mscale;
-          s *= a.rope.mscale;
+          rotation(a.pos[own - 8 + g.first + t], a.rope.freqs[q], a.rope.mscale, c, s);
           float *u = rows + t * pitch + (a.rope.interleaved ? 2 * q : q), *v = u + (a.rope.interleaved ? 1 : half);
           const float xa = *u, xb = *v;
           *u = turned_a(xa, xb, c, s);

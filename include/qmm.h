@@ -440,10 +440,10 @@ int qmm_rope_freqs(double *freqs, float *mscale, int64_t n_rot, double base, con
  * turned by phi = pos[t] * freqs[i] (freqs: n_rot / 2 f64 on the device):
  *   y_a = mscale (x_a cos phi - x_b sin phi)
  *   y_b = mscale (x_a sin phi + x_b cos phi);
- * elements n_rot .. head_dim - 1 are copied.  The angle is reduced in 64
- * bits, so far positions lose nothing; cos, sin and the products are f32
- * (within 2^-21 mscale (|x_a| + |x_b|), before the rounding to f16).  x is [T][H][head_dim] f32 or f16, y
- * f32 or f16, head_dim and n_rot even, n_rot <= head_dim.  y may be x itself
+ * elements n_rot .. head_dim - 1 are copied.  mscale cos and mscale sin are
+ * computed in 64 bits, so far positions lose nothing, and rounded once to f32, as
+ * are the products (within 2^-22 mscale (|x_a| + |x_b|), before the rounding to
+ * f16).  x is [T][H][head_dim] f32 or f16, y f32 or f16, head_dim and n_rot even, n_rot <= head_dim.  y may be x itself
  * (same stride and type); any other overlap is not allowed.
  * Errors: a zero dimension, dtype, then pointers, alignment, strides, layout,
  * n_rot and T * H * head_dim > 2^32 as QMM_ERR_BAD_ARG. */
@@ -492,12 +492,15 @@ int qmm_kv_read(int k_kind, int v_kind, const void *k_pages, const void *v_pages
  * page number lies outside [0, n_pages) count as absent.
  * Numerics: keys and values are exact (codes as integers, block scales in
  * f32 or folded into the weight); scores, softmax and sums are f32.  f16 q is
- * exact and the weights, times the value's block scale, are rounded once to
- * f16; f32 q is carried as two f16 terms (relative 2^-21), and weights as f32.  With w_t the exact weights,
+ * exact (beside quantized keys down to 2^-35 of the head's largest element) and
+ * the weights, times the value's block scale, are rounded once to f16; f32 q is
+ * carried as two f16 terms (2^-21 of an element, or 2^-39 of the head's largest),
+ * and weights as f32.  With w_t the exact weights,
  *   |out - exact| <= (r + 2 max_t e_t) sum_t w_t |v_t| + a  (+ f16 out's rounding)
  * where r = 2^-11 + 2^-18 for f16 and 2^-18 for f32, and e_t = c (scale * sum
- * over 32-element blocks of (sum |q|) (max |k_t|) + max |s| + 40) with c =
- * 2^-17 for f16 and 2^-20 for f32 bounds a score's error.  a is 0 for f32
+ * over 32-element blocks of (sum |q| + 2^-13 max |q| of the whole head) (max
+ * |k_t|) + max |s| + 40) with c = 2^-17 for f16 and 2^-20 for f32 bounds a
+ * score's error.  a is 0 for f32
  * (weights below 2^-100 of the largest may count as 0); for f16 it is what f16
  * weights lose far below the strongest, 2^-39 M sum_t |c_t|, with c_t the code
  * of the value (F16: the value itself) and M the largest product of a weight

@@ -82,6 +82,35 @@ def test_rope_far_positions():
     check(y, want, tol, "far")
 
 
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("D", [8, 2])
+def test_rope_turns_by_the_rounded_cosine_and_sine(layout, D):
+    """The vector (1, 0) turned is mscale (cos, sin), each rounded once to f32: half a step of the value itself, beside
+    the 64-bit angle's |phi| 2^-51 and 2^-35 of the series.  Positions and angles of every size, zeros of both."""
+    g = wl.rng("rope", f"unit{layout}{D}")
+    pos = np.concatenate([np.arange(700), g.integers(-2 ** 31, 2 ** 31, 300)]).astype(np.int32)
+    f = np.exp(g.uniform(np.log(1e-6), np.log(10), D // 2))
+    f[0] = np.pi / 8
+    x = np.zeros((1000, 1, D), np.float32)
+    a = np.arange(D // 2) if layout == "half" else 2 * np.arange(D // 2)
+    x[..., a] = 1
+    m = np.float32(1.2079442)
+    y = qmm.rope(dev(x), dev(pos), dev(f), layout, float(m)).cpu().numpy()
+    want, phi = oa.rope(x, pos, f, layout, float(m)), np.zeros((1000, 1, D))
+    phi[:, 0, a] = phi[:, 0, a + (D // 2 if layout == "half" else 1)] = np.abs(np.outer(pos.astype(float), f))
+    check(y, want, 2.0 ** -24 * np.abs(want) + m * (phi * 2.0 ** -51 + 2.0 ** -35), "unit")
+
+
+@pytest.mark.parametrize("T,H,D,n_rot,layout", [(1, 40, 128, 128, "half"), (130, 2, 256, 64, "interleaved")])
+def test_rope_bound(T, H, D, n_rot, layout):
+    """f32 rows within the header's 2^-22 mscale (|x_a| + |x_b|)."""
+    g = wl.rng("rope", f"bound{T}")
+    x, pos = g.normal(size=(T, H, D)).astype(np.float32), g.integers(0, 1 << 20, T).astype(np.int32)
+    freqs, m = qmm.rope_freqs(n_rot, factor=8.0, orig_ctx=4096)
+    y = qmm.rope(dev(x), dev(pos), freqs, layout, m).cpu().numpy()
+    check(y, oa.rope(x, pos, freqs.cpu().numpy(), layout, m), 2.0 ** -22 * oa.rope_bound(x, n_rot, layout, m), "rope")
+
+
 # -- writing and reading the cache -----------------------------------------------
 def values_for(g, shape, dt):
     """Rows of very different sizes with some far outliers."""
