@@ -20,10 +20,12 @@
 //
 // What bounds it: memory traffic when there is much of it, and a wave's chain of
 // loads and LDS rounds when there is not.  Measured, 32768 tokens of 8 heads of
-// 128 in Q4_0: f32 rows written (306 MB) in 72 us, 4.3 TB/s, read back as f16
-// (172 MB) in 37 us, 4.6 TB/s; 5003 tokens, Q8_0 keys and Q4_0 values, written
-// from f16 (29 MB) in 15 us and read as f32 (49 MB) in 12; one token of 8 heads
-// appended with 32 query heads 5.5 us.  A half wave per block of a token with
+// 128 in Q4_0: f32 rows written (306 MB) in 74 us, 4.2 TB/s, read back as f16
+// (172 MB) in 38 us, 4.5 TB/s; 5003 tokens, Q8_0 keys and Q4_0 values, written
+// from f16 (29 MB) in 15 us and read as f32 (49 MB) in 12; with 32 query heads
+// rotated, one token of 8 heads appended in 5.5 us, 8192 from f32 to Q8_0 (353 MB)
+// in 90, 3.9 TB/s, from f16 to Q4_0 (177 MB) in 67, 2.7 TB/s (each head's keys
+// compute their angles anew).  A half wave per block of a token with
 // byte stores took 420 and 230 us for the first two; windows of 32 tokens per
 // workgroup, synchronized three times, 82 and 51.
 #include <algorithm>

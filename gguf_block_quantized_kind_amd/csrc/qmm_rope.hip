@@ -4,7 +4,7 @@
 // with (a, b) = (i, i + n_rot / 2) or (2i, 2i + 1); elements past n_rot pass.
 // Each element is read and written once, by the thread that holds its pair
 // (so y may be x): the bound is the memory traffic.  8192 tokens of 32 heads of
-// 128, f32 to f16 (201 MB): 38.7 us, 5.2 TB/s, the rate of a large copy; a
+// 128, f32 to f16 (201 MB): 39.4 us, 5.1 TB/s, the rate of a large copy; a
 // thread per pair that finds its own angle took 65.
 #include "qmm_internal.h"
 #include "qmm_kv.h"

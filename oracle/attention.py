@@ -150,8 +150,10 @@ def load(kind, is_v, pages, page_size, slot, n_kv, D):
 # -- attention ---------------------------------------------------------------
 def attend(q, k, v, scale, sink=None, f16=True, counts=None):
     """One query head q [D] over k, v [n, D] (binary64), token t counts[t] times
-    (None: once): the output and the tolerance of the documented bound, without
-    the output's rounding."""
+    (None: once): the output and its tolerance, without the output's rounding: the
+    header's bound without its terms for far smaller elements (f16_floor, and a
+    query's 2^-13 max |q|), f16 queries held to the f32 ones' constant for scores,
+    2^-20 instead of the documented 2^-17."""
     n, D = k.shape
     if n == 0:
         return np.zeros(D), np.zeros(D)
