@@ -12,7 +12,9 @@ it raises instead of falling back to anything else.
 allocate their outputs (and the expert workspace) with torch and call the
 ``qmm_*`` functions; so are ``rope``, ``kv_write``, ``kv_append``, ``kv_read``
 and ``attn_decode``, the operators between a layer's projections, over a paged
-key/value cache of ``kv_pages`` tensors.
+key/value cache of ``kv_pages`` tensors, and what stands around the products:
+``rmsnorm`` and ``rmsnorm_q8`` before them, ``matmul_ep``, ``matmul_packed_ep``
+and ``gemv_q8`` with an epilogue, ``moe_route`` before the experts.
 """
 from __future__ import annotations
 
@@ -81,6 +83,12 @@ def load_library(path: str = LIBRARY) -> ctypes.CDLL:
         "qmm_attn_decode": (I, [I, I, P, P, I64, I64, I64, I64, P, I, I64, I64, P, I64, P, I64, F, I64, P, P, P, SZ,
                                 P]),
         "qmm_attn_decode_workspace_bytes": (SZ, [I64, I64, I64, I64]),
+        "qmm_matmul_ep": (I, [I, P, P, I, P, P, I, I64, I64, I64, I64, P]),
+        "qmm_matmul_packed_ep": (I, [I, P, P, I, P, P, I, I64, I64, I64, I64, P]),
+        "qmm_gemv_q8": (I, [I, P, P, P, P, P, P, I, I64, I64, I64, I64, P]),
+        "qmm_rmsnorm": (I, [P, I, I64, P, I, I64, P, F, P, I64, P, I, I64, I64, I64, I64, P]),
+        "qmm_rmsnorm_q8": (I, [I, P, I, I64, P, I, I64, P, F, P, I64, P, P, P, I64, I64, P]),
+        "qmm_moe_route": (I, [P, I, I64, P, I64, I64, I64, I, I64, I64, I, I, F, P, P, P, P]),
         "qmm_row_bytes": (I64, [I, I64]),
         "qmm_block_geometry": (I, [I, ctypes.POINTER(I), ctypes.POINTER(I)]),
         "qmm_kind_from_name": (I, [ctypes.c_char_p]),
@@ -588,6 +596,33 @@ def _layout_id(layout) -> int:
     return int(layout)
 
 
+ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+ROUTE_SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+class Epilogue(ctypes.Structure):
+    """qmm_epilogue of include/qmm.h, for calls of the C entry points themselves."""
+    _fields_ = [("bias", ctypes.c_void_p), ("mul", ctypes.c_void_p), ("residual", ctypes.c_void_p),
+                ("mul_stride", ctypes.c_int64), ("residual_stride", ctypes.c_int64), ("act", ctypes.c_int),
+                ("mul_dtype", ctypes.c_int), ("residual_dtype", ctypes.c_int)]
+
+
+def _act_id(act) -> int:
+    if isinstance(act, str):
+        if act not in ACTS:
+            raise QmmError(5, f"act {act} is none of {', '.join(ACTS)}")
+        return ACTS[act]
+    return int(act)
+
+
+def _score_id(score) -> int:
+    if isinstance(score, str):
+        if score not in ROUTE_SCORES:
+            raise QmmError(5, f"score {score} is none of {', '.join(ROUTE_SCORES)}")
+        return ROUTE_SCORES[score]
+    return int(score)
+
+
 # Checks, allocation and the C calls on tensors are in the _qmm_call module
 # (built with the library): these calls run once per layer and token, where the
 # host's time is what a small step waits for.
@@ -603,9 +638,11 @@ def _load_ops():
         raise RuntimeError("the _qmm_call module is not built; run __graft_entry__.build() first") from e
     lib = load_library()
     names = ("qmm_rope", "qmm_kv_write", "qmm_kv_append", "qmm_kv_read", "qmm_attn_decode",
-             "qmm_attn_decode_workspace_bytes", "qmm_kv_page_bytes")
+             "qmm_attn_decode_workspace_bytes", "qmm_kv_page_bytes", "qmm_rmsnorm", "qmm_rmsnorm_q8", "qmm_gemv_q8",
+             "qmm_moe_route", "qmm_matmul_ep", "qmm_matmul_packed_ep", "qmm_kind_from_name", "qmm_row_bytes",
+             "qmm_packed_bytes")
     _qmm_call.setup({n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names}, _check, cache_kind_id,
-                    _layout_id)
+                    _layout_id, kind_id, _act_id, _score_id)
     _ops = _qmm_call
     return _ops
 
@@ -624,10 +661,17 @@ def _on(stream, like, fn, *args):
     for t in args:
         if isinstance(t, torch.Tensor):
             t.record_stream(stream)
-    for t in got if isinstance(got, tuple) else (got,):
-        if t is not None and not any(t is a for a in args):
+    for t in _tensors(got):
+        if not any(t is a for a in args):
             t.record_stream(here)
     return got
+
+
+def _tensors(got):
+    """The tensors of a result: one, or tuples of them."""
+    if isinstance(got, tuple):
+        return [t for part in got for t in _tensors(part)]
+    return [] if got is None else [got]
 
 
 def kv_page_bytes(kind, page_size: int, n_kv: int, head_dim: int) -> int:
@@ -718,3 +762,74 @@ def attn_decode(q, k_pages, v_pages, block_table, seq_lens, k_kind, v_kind, page
                    sinks, out, workspace)
     return fn(q, k_pages, v_pages, block_table, seq_lens, k_kind, v_kind, page_size, n_kv, scale, window, sinks, out,
               workspace)
+
+
+# ---------------------------------------------------------------------------
+# What stands around the products: norms, the choice of experts, epilogues.
+# Rows have packed elements and any row stride.
+# ---------------------------------------------------------------------------
+def rmsnorm(x, weight=None, eps: float = 1e-6, residual=None, out=None, out_dtype=None, sum_out=None, stream=None):
+    """x [T, D] or [T, heads, D], each row (of a head) divided by the root of its
+    mean square + eps and multiplied by weight [D] f32.  Without a residual: the
+    normed rows, of out_dtype (x's type if None).  With one: (rows, sum), where
+    sum = x + residual is what is normed, kept in the residual's type; sum_out may
+    be the residual or x itself."""
+    fn = (_ops or _load_ops()).rmsnorm
+    if stream is not None:
+        return _on(stream, x, fn, x, weight, eps, residual, out, out_dtype, sum_out)
+    return fn(x, weight, eps, residual, out, out_dtype, sum_out)
+
+
+def rmsnorm_q8(kind, x, weight=None, eps: float = 1e-6, residual=None, acts=None, sum_out=None, stream=None):
+    """rmsnorm of x [T, D] in 8 bits for products with repacked weights of `kind`:
+    acts = (codes [T, D] int8, scales [T, D / 32] f32, code_sums [T, D / 32] int32),
+    for gemv_q8 (rows t0 .. t1 are the three tensors' rows t0 .. t1); (acts, sum)
+    with a residual."""
+    fn = (_ops or _load_ops()).rmsnorm_q8
+    codes, scales, sums = (None, None, None) if acts is None else acts
+    if stream is not None:
+        return _on(stream, x, fn, kind, x, weight, eps, residual, codes, scales, sums, sum_out)
+    return fn(kind, x, weight, eps, residual, codes, scales, sums, sum_out)
+
+
+def matmul_ep(kind, W, A, N: int | None = None, bias=None, act=None, mul=None, residual=None, out=None, out_dtype=None,
+              stream=None):
+    """act(A . W^T + bias) * mul + residual, [M, N] f32 (or out_dtype, or out's
+    type): bias [N] f32, act one of ACTS, mul and residual [M, N] f32 or f16; out
+    may be mul or residual."""
+    fn = (_ops or _load_ops()).matmul_ep
+    if stream is not None:
+        return _on(stream, A, fn, kind, W, A, N, bias, act, mul, residual, out, out_dtype)
+    return fn(kind, W, A, N, bias, act, mul, residual, out, out_dtype)
+
+
+def matmul_packed_ep(kind, P, A, N: int, bias=None, act=None, mul=None, residual=None, out=None, out_dtype=None,
+                     stream=None):
+    """matmul_ep over repacked weights (qmm_matmul_packed's kinds)."""
+    fn = (_ops or _load_ops()).matmul_packed_ep
+    if stream is not None:
+        return _on(stream, A, fn, kind, P, A, N, bias, act, mul, residual, out, out_dtype)
+    return fn(kind, P, A, N, bias, act, mul, residual, out, out_dtype)
+
+
+def gemv_q8(kind, P, acts, N: int, bias=None, act=None, mul=None, residual=None, out=None, out_dtype=None, stream=None):
+    """matmul_ep over repacked weights with the 8-bit activations of rmsnorm_q8
+    (up to 8 rows; the integer product of gemv_i8)."""
+    fn = (_ops or _load_ops()).gemv_q8
+    codes, scales, sums = acts
+    if stream is not None:
+        return _on(stream, codes, fn, kind, P, codes, scales, sums, N, bias, act, mul, residual, out, out_dtype)
+    return fn(kind, P, codes, scales, sums, N, bias, act, mul, residual, out, out_dtype)
+
+
+def moe_route(logits, topk: int, score="softmax", bias=None, n_group: int = 1, topk_group: int = 1, group_top: int = 1,
+              normalize: bool = True, scale: float = 1.0, slots=None, ids=None, weights=None, stream=None):
+    """(ids [M, topk] int32, weights [M, topk] f32) for moe_ffn from logits [M, E]:
+    the topk largest scores (plus bias [E] f32, which decides but does not weigh)
+    within the topk_group groups of the largest sums of group_top.  Tokens with
+    slots [M] int32 below 0, and rows that run out of experts, get ids of -1."""
+    fn = (_ops or _load_ops()).moe_route
+    if stream is not None:
+        return _on(stream, logits, fn, logits, topk, score, bias, n_group, topk_group, group_top, normalize, scale, slots,
+                   ids, weights)
+    return fn(logits, topk, score, bias, n_group, topk_group, group_top, normalize, scale, slots, ids, weights)

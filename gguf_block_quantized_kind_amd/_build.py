@@ -50,7 +50,7 @@ def compile_flags() -> list[str]:
 # mixes inline assembly with its matrix-core code and keeps the default.)
 # The attention kernels do too: their score products go straight to the VALU.
 VGPR_FORM = ["-mllvm", "-amdgpu-mfma-vgpr-form"]
-FILE_FLAGS = {"qmm_gemm.hip": VGPR_FORM,
+FILE_FLAGS = {"qmm_gemm.hip": VGPR_FORM, "qmm_gemm_ep.hip": VGPR_FORM,
               **{f"qmm_attn_{k}_{v}.hip": VGPR_FORM for k in ("f16", "q8", "q4") for v in ("f16", "q8", "q4")}}
 
 

@@ -5,8 +5,8 @@
 // same in Python, with the C call made through ctypes, took 2 to 4 us more a
 // call (one token's rotation 6.3 us, of which the kernel's launch takes 2.7).
 //
-// setup(addresses, check, cache_kind_id, layout_id) sets the library's functions
-// and what raises for a status or an unknown name.  Every function takes its
+// setup(addresses, check, cache_kind_id, layout_id, kind_id, act_id, score_id) sets
+// the library's functions and what raises for a status or an unknown name.  Every function takes its
 // arguments by position (the package's functions of the same names carry the
 // defaults).  The interpreter lock is released during the C call.
 #define PY_SSIZE_T_CLEAN
@@ -28,11 +28,12 @@ namespace {
 // The library's functions, by their header's types.
 #define EACH_FUNCTION(X) \
   X(qmm_rope) X(qmm_kv_write) X(qmm_kv_append) X(qmm_kv_read) X(qmm_attn_decode) X(qmm_attn_decode_workspace_bytes) \
-  X(qmm_kv_page_bytes)
+  X(qmm_kv_page_bytes) X(qmm_rmsnorm) X(qmm_rmsnorm_q8) X(qmm_gemv_q8) X(qmm_moe_route) X(qmm_matmul_ep)             \
+  X(qmm_matmul_packed_ep) X(qmm_kind_from_name) X(qmm_row_bytes) X(qmm_packed_bytes)
 #define DECLARE(fn) decltype(&::fn) p_##fn = nullptr;
 EACH_FUNCTION(DECLARE)
 #undef DECLARE
-PyObject *g_check, *g_cache_kind_id, *g_layout_id;
+PyObject *g_check, *g_cache_kind_id, *g_layout_id, *g_kind_id, *g_act_id, *g_score_id;
 
 struct Raised {};  // a Python exception is set
 
@@ -327,6 +328,278 @@ PyObject *attn_decode(PyObject *const *a) {
   return a[12] != Py_None ? Py_NewRef(a[12]) : THPVariable_Wrap(std::move(out));
 }
 
+int weight_kind(PyObject *o) {
+  if (PyUnicode_Check(o)) {
+    const char *name = PyUnicode_AsUTF8(o);
+    if (!name) throw Raised{};
+    const int id = p_qmm_kind_from_name(name);
+    if (id >= 0) return id;
+  }
+  return call_id(g_kind_id, o);
+}
+int act_of(PyObject *o) {
+  return o == Py_None || is(o, "none") ? QMM_ACT_NONE
+         : is(o, "silu")               ? QMM_ACT_SILU
+         : is(o, "gelu")               ? QMM_ACT_GELU
+         : is(o, "gelu_tanh")          ? QMM_ACT_GELU_TANH
+         : is(o, "relu")               ? QMM_ACT_RELU
+                                       : call_id(g_act_id, o);
+}
+
+// [T, D] rows, or [T, heads, D] as rows_of.
+Rows any_rows_of(const at::Tensor &x, const char *what) {
+  if (x.dim() != 2) return rows_of(x, what);
+  const int64_t T = x.size(0), D = x.size(1);
+  if (D > 1 && x.stride(1) != 1) raise(PyExc_ValueError, "the rows of ", what, " must be packed, got strides ", x.strides());
+  return Rows{T, 1, D, T > 1 ? x.stride(0) : D};
+}
+const float *floats_of(const at::Tensor &t, int64_t count, const char *what) {
+  if (t.scalar_type() != at::kFloat) raise(PyExc_TypeError, what, " must be float32, got ", t.scalar_type());
+  if (t.numel() != count || !t.is_contiguous())
+    raise(PyExc_ValueError, what, " must hold ", count, " contiguous elements, got ", t.sizes());
+  return (const float *)t.data_ptr();
+}
+void same_shape(const at::Tensor &t, const at::Tensor &like, const char *what) {
+  if (t.sizes() != like.sizes()) raise(PyExc_ValueError, what, " is ", t.sizes(), ", needs ", like.sizes());
+}
+
+// A norm's operands besides its result: x, weight, residual, sum_out.
+struct NormIn {
+  const at::Tensor &x;
+  Rows r;
+  const float *weight = nullptr;
+  float eps;
+  at::Tensor residual, sum;  // undefined without a residual
+  int64_t residual_stride = 0, sum_stride = 0;
+  PyObject *sum_given = nullptr;
+  at::Device device;
+  NormIn(PyObject *px, PyObject *pw, PyObject *pe, PyObject *pr, PyObject *ps)
+      : x(tensor(px, "x")), r(any_rows_of(x, "x")), eps((float)number(pe)), device(one_gpu({&x})) {
+    if (pw != Py_None) {
+      const at::Tensor &w = tensor(pw, "weight");
+      weight = floats_of(w, r.D, "weight");
+      one_gpu({&x, &w});
+    }
+    if (pr == Py_None) {
+      if (ps != Py_None) raise(PyExc_ValueError, "sum_out without a residual");
+      return;
+    }
+    residual = tensor(pr, "residual");
+    same_shape(residual, x, "residual");
+    residual_stride = any_rows_of(residual, "residual").stride;
+    one_gpu({&x, &residual});
+    if (ps != Py_None) {
+      sum_given = ps;
+      sum = tensor(ps, "sum_out");
+      same_shape(sum, x, "sum_out");
+      if (sum.scalar_type() != residual.scalar_type())
+        raise(PyExc_TypeError, "sum_out is ", sum.scalar_type(), ", the residual is ", residual.scalar_type());
+      sum_stride = any_rows_of(sum, "sum_out").stride;
+      one_gpu({&x, &sum});
+    } else {
+      sum = make(x, x.sizes(), residual.scalar_type());
+      sum_stride = r.H * r.D;
+    }
+  }
+  const void *res() const { return residual.defined() ? residual.data_ptr() : nullptr; }
+  int res_code() const { return residual.defined() ? code(residual.scalar_type()) : QMM_F32; }
+  void *sum_ptr() const { return sum.defined() ? sum.data_ptr() : nullptr; }
+  // `y` (a new reference), and the sum with it where there is a residual.
+  PyObject *with_sum(PyObject *y) {
+    if (!y || !sum.defined()) return y;
+    PyObject *s = sum_given ? Py_NewRef(sum_given) : THPVariable_Wrap(std::move(sum));
+    PyObject *both = s ? PyTuple_Pack(2, y, s) : nullptr;
+    Py_DECREF(y);
+    Py_XDECREF(s);
+    return both;
+  }
+};
+
+// x, weight, eps, residual, out, out_dtype, sum_out
+PyObject *rmsnorm(PyObject *const *a) {
+  check_out_type(a[4], a[5], "out");
+  NormIn in(a[0], a[1], a[2], a[3], a[6]);
+  at::Tensor y;
+  int64_t stride = in.r.H * in.r.D;
+  if (a[4] != Py_None) {
+    y = tensor(a[4], "out");
+    same_shape(y, in.x, "out");
+    stride = any_rows_of(y, "out").stride;
+    one_gpu({&in.x, &y});
+  } else {
+    y = make(in.x, in.x.sizes(), a[5] == Py_None ? in.x.scalar_type() : type_of(a[5]));
+  }
+  call(in.device, p_qmm_rmsnorm, (const void *)in.x.data_ptr(), code(in.x.scalar_type()), in.r.stride, in.res(),
+       in.res_code(), in.residual_stride, in.weight, in.eps, in.sum_ptr(), in.sum_stride, y.data_ptr(),
+       code(y.scalar_type()), stride, in.r.T, in.r.H, in.r.D);
+  return in.with_sum(a[4] != Py_None ? Py_NewRef(a[4]) : THPVariable_Wrap(std::move(y)));
+}
+
+// kind, x, weight, eps, residual, codes, scales, code_sums, sum_out
+PyObject *rmsnorm_q8(PyObject *const *a) {
+  const int kind = weight_kind(a[0]);
+  NormIn in(a[1], a[2], a[3], a[4], a[8]);
+  if (in.x.dim() != 2) raise(PyExc_ValueError, "x must be [rows, elements], got ", in.x.sizes());
+  const int64_t T = in.r.T, D = in.r.D, shape[2] = {T, D}, blocks[2] = {T, D / 32};
+  at::Tensor t[3];
+  const char *names[3] = {"codes", "scales", "code_sums"};
+  const at::ScalarType types[3] = {at::kChar, at::kFloat, at::kInt};
+  const bool given = a[5] != Py_None;
+  for (int i = 0; i < 3; ++i) {
+    const at::IntArrayRef want = i == 0 ? shape : blocks;
+    if (given) {
+      t[i] = tensor(a[5 + i], names[i]);
+      if (t[i].scalar_type() != types[i] || t[i].sizes() != want || !t[i].is_contiguous())
+        raise(PyExc_ValueError, names[i], " must be contiguous ", types[i], " ", want, ", got ", t[i].scalar_type(), " ",
+              t[i].sizes());
+      one_gpu({&in.x, &t[i]});
+    } else {
+      t[i] = make(in.x, want, types[i]);
+    }
+  }
+  call(in.device, p_qmm_rmsnorm_q8, kind, (const void *)in.x.data_ptr(), code(in.x.scalar_type()), in.r.stride, in.res(),
+       in.res_code(), in.residual_stride, in.weight, in.eps, in.sum_ptr(), in.sum_stride, (int8_t *)t[0].data_ptr(),
+       (float *)t[1].data_ptr(), (int32_t *)t[2].data_ptr(), T, D);
+  PyObject *o[3], *acts = nullptr;
+  for (int i = 0; i < 3; ++i) o[i] = given ? Py_NewRef(a[5 + i]) : THPVariable_Wrap(std::move(t[i]));
+  if (o[0] && o[1] && o[2]) acts = PyTuple_Pack(3, o[0], o[1], o[2]);
+  for (int i = 0; i < 3; ++i) Py_XDECREF(o[i]);
+  return in.with_sum(acts);
+}
+
+// A product's epilogue and result: bias, act, mul, residual, out, out_dtype.
+struct Ep {
+  qmm_epilogue e{};
+  at::Tensor out;
+  PyObject *given;
+  int64_t stride;
+  Ep(PyObject *const *a, const at::Tensor &x, int64_t M, int64_t N) : given(a[4] == Py_None ? nullptr : a[4]), stride(N) {
+    const int64_t shape[2] = {M, N};
+    e.act = act_of(a[1]);
+    if (a[0] != Py_None) {
+      const at::Tensor &b = tensor(a[0], "bias");
+      e.bias = floats_of(b, N, "bias");
+      one_gpu({&x, &b});
+    }
+    auto rows = [&](PyObject *o, const char *what, int &type, int64_t &stride) -> const at::Tensor & {
+      const at::Tensor &t = tensor(o, what);
+      if (t.sizes() != at::IntArrayRef(shape)) raise(PyExc_ValueError, what, " is ", t.sizes(), ", needs ", at::IntArrayRef(shape));
+      one_gpu({&x, &t});
+      type = code(t.scalar_type());
+      stride = any_rows_of(t, what).stride;
+      return t;
+    };
+    if (a[2] != Py_None) e.mul = rows(a[2], "mul", e.mul_dtype, e.mul_stride).data_ptr();
+    if (a[3] != Py_None) e.residual = rows(a[3], "residual", e.residual_dtype, e.residual_stride).data_ptr();
+    check_out_type(a[4], a[5], "out");
+    int type;
+    if (given) {
+      out = rows(given, "out", type, stride);
+    } else {
+      if (N < 0) raise(PyExc_ValueError, "N=", N, " is not a size");
+      out = make(x, shape, a[5] == Py_None ? at::kFloat : type_of(a[5]));
+    }
+  }
+  PyObject *result() { return given ? Py_NewRef(given) : THPVariable_Wrap(std::move(out)); }
+};
+void bytes_of(const at::Tensor &t, int64_t need, const char *what) {
+  if (t.element_size() != 1) raise(PyExc_TypeError, what, " must be a byte tensor, got ", t.scalar_type());
+  if (!t.is_contiguous() || t.numel() < need)
+    raise(PyExc_ValueError, what, " holds ", t.numel(), " bytes (contiguous: ", t.is_contiguous(), "), needs ", need);
+}
+
+// kind, W, A, N, bias, act, mul, residual, out, out_dtype
+template <bool PACKED>
+PyObject *matmul_with(PyObject *const *a) {
+  const int kind = weight_kind(a[0]);
+  const at::Tensor &W = tensor(a[1], PACKED ? "P" : "W"), &A = tensor(a[2], "A");
+  if ((A.dim() != 1 && A.dim() != 2) || !A.is_contiguous())
+    raise(PyExc_ValueError, "A must be contiguous [M, K] or [K], got ", A.sizes());
+  const int64_t K = A.size(A.dim() - 1), M = A.dim() == 1 ? 1 : A.size(0);
+  const int64_t rb = PACKED ? 0 : p_qmm_row_bytes(kind, K);
+  // (Without N, rows of a kind or length that the library refuses count as one.)
+  const int64_t N = a[3] != Py_None ? integer(a[3]) : rb > 0 ? W.numel() / rb : 1;
+  const int64_t need = PACKED ? p_qmm_packed_bytes(kind, N, K) : rb > 0 && N > 0 && N <= INT32_MAX ? rb * N : 0;
+  bytes_of(W, need, PACKED ? "P" : "W");
+  const at::Device d = one_gpu({&A, &W});
+  Ep ep(a + 4, A, M, N);
+  call(d, PACKED ? p_qmm_matmul_packed_ep : p_qmm_matmul_ep, kind, (const void *)W.data_ptr(), (const void *)A.data_ptr(),
+       code(A.scalar_type()), (const qmm_epilogue *)&ep.e, ep.out.data_ptr(), code(ep.out.scalar_type()), ep.stride, M, N,
+       K);
+  return ep.result();
+}
+PyObject *matmul_ep(PyObject *const *a) { return matmul_with<false>(a); }
+PyObject *matmul_packed_ep(PyObject *const *a) { return matmul_with<true>(a); }
+
+// kind, P, codes, scales, code_sums, N, bias, act, mul, residual, out, out_dtype
+PyObject *gemv_q8(PyObject *const *a) {
+  const int kind = weight_kind(a[0]);
+  const at::Tensor &P = tensor(a[1], "P"), &q = tensor(a[2], "codes"), &d = tensor(a[3], "scales"), &s = tensor(a[4], "code_sums");
+  if (q.dim() != 2 || !q.is_contiguous() || q.scalar_type() != at::kChar)
+    raise(PyExc_ValueError, "codes must be contiguous int8 [M, K], got ", q.scalar_type(), " ", q.sizes());
+  const int64_t M = q.size(0), K = q.size(1), N = integer(a[5]);
+  const float *scales = floats_of(d, M * (K / 32), "scales");
+  const int32_t *sums = ints_of(s, M * (K / 32), "code_sums");
+  bytes_of(P, p_qmm_packed_bytes(kind, N, K), "P");
+  const at::Device dev = one_gpu({&q, &P, &d, &s});
+  Ep ep(a + 6, q, M, N);
+  call(dev, p_qmm_gemv_q8, kind, (const void *)P.data_ptr(), (const int8_t *)q.data_ptr(), scales, sums,
+       (const qmm_epilogue *)&ep.e, ep.out.data_ptr(), code(ep.out.scalar_type()), ep.stride, M, N, K);
+  return ep.result();
+}
+
+// logits, topk, score, bias, n_group, topk_group, group_top, normalize, scale, slots, ids, weights
+PyObject *moe_route(PyObject *const *a) {
+  const at::Tensor &x = tensor(a[0], "logits");
+  if (x.dim() != 2) raise(PyExc_ValueError, "logits must be [tokens, experts], got ", x.sizes());
+  const Rows r = any_rows_of(x, "logits");
+  const int64_t M = r.T, E = r.D, k = integer(a[1]);
+  const int score = is(a[2], "softmax")   ? QMM_ROUTE_SOFTMAX
+                    : is(a[2], "sigmoid") ? QMM_ROUTE_SIGMOID
+                                          : call_id(g_score_id, a[2]);
+  const int64_t n_group = integer(a[4]), topk_group = integer(a[5]), top = integer(a[6]);
+  const int normalize = PyObject_IsTrue(a[7]);
+  if (normalize < 0) throw Raised{};
+  const float scale = (float)number(a[8]);
+  const at::Device d = one_gpu({&x});
+  const float *bias = nullptr;
+  if (a[3] != Py_None) {
+    const at::Tensor &b = tensor(a[3], "bias");
+    bias = floats_of(b, E, "bias");
+    one_gpu({&x, &b});
+  }
+  const int32_t *slots = nullptr;
+  if (a[9] != Py_None) {
+    const at::Tensor &s = tensor(a[9], "slots");
+    slots = ints_of(s, M, "slots");
+    one_gpu({&x, &s});
+  }
+  const bool given = a[10] != Py_None;
+  if (given != (a[11] != Py_None)) raise(PyExc_ValueError, "ids and weights go together");
+  const int64_t shape[2] = {M, k};
+  at::Tensor ids, w;
+  if (given) {
+    ids = tensor(a[10], "ids"), w = tensor(a[11], "weights");
+    for (const at::Tensor *t : {&ids, &w})
+      if (t->sizes() != at::IntArrayRef(shape)) raise(PyExc_ValueError, "ids and weights must be ", at::IntArrayRef(shape));
+    ints_of(ids, M * k, "ids");
+    floats_of(w, M * k, "weights");
+    one_gpu({&x, &ids, &w});
+  } else {
+    if (k < 0) raise(PyExc_ValueError, "topk=", k, " is not a size");
+    ids = make(x, shape, at::kInt), w = make(x, shape, at::kFloat);
+  }
+  call(d, p_qmm_moe_route, (const void *)x.data_ptr(), code(x.scalar_type()), r.stride, bias, M, E, k, score, n_group,
+       topk_group, (int)std::max<int64_t>(std::min<int64_t>(top, 3), 0), normalize, scale, slots, (int32_t *)ids.data_ptr(),
+       (float *)w.data_ptr());
+  if (given) return PyTuple_Pack(2, a[10], a[11]);
+  PyObject *io = THPVariable_Wrap(std::move(ids)), *wo = THPVariable_Wrap(std::move(w));
+  PyObject *both = io && wo ? PyTuple_Pack(2, io, wo) : nullptr;
+  Py_XDECREF(io);
+  Py_XDECREF(wo);
+  return both;
+}
+
 template <PyObject *(*F)(PyObject *const *), int N>
 PyObject *entry(PyObject *, PyObject *const *a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
@@ -341,8 +614,9 @@ PyObject *entry(PyObject *, PyObject *const *a, Py_ssize_t n) {
 }
 
 PyObject *setup(PyObject *, PyObject *args) {
-  PyObject *addresses, *check, *kind, *layout;
-  if (!PyArg_ParseTuple(args, "O!OOO", &PyDict_Type, &addresses, &check, &kind, &layout)) return nullptr;
+  PyObject *addresses, *check, *cache_kind, *layout, *kind, *act, *score;
+  if (!PyArg_ParseTuple(args, "O!OOOOOO", &PyDict_Type, &addresses, &check, &cache_kind, &layout, &kind, &act, &score))
+    return nullptr;
 #define SET(fn)                                                                             \
   {                                                                                         \
     PyObject *o = PyDict_GetItemString(addresses, #fn);                                     \
@@ -352,13 +626,16 @@ PyObject *setup(PyObject *, PyObject *args) {
   }
   EACH_FUNCTION(SET)
 #undef SET
-  g_check = Py_NewRef(check), g_cache_kind_id = Py_NewRef(kind), g_layout_id = Py_NewRef(layout);
+  g_check = Py_NewRef(check), g_cache_kind_id = Py_NewRef(cache_kind), g_layout_id = Py_NewRef(layout);
+  g_kind_id = Py_NewRef(kind), g_act_id = Py_NewRef(act), g_score_id = Py_NewRef(score);
   Py_RETURN_NONE;
 }
 
 #define METHOD(fn, n) {#fn, (PyCFunction)(void (*)(void))entry<fn, n>, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {METHOD(rope, 7),     METHOD(kv_write, 8),     METHOD(kv_append, 15),
-                         METHOD(kv_read, 11), METHOD(attn_decode, 14), {"setup", setup, METH_VARARGS, nullptr},
+                         METHOD(kv_read, 11), METHOD(attn_decode, 14), METHOD(rmsnorm, 7),
+                         METHOD(rmsnorm_q8, 9), METHOD(gemv_q8, 12),   METHOD(moe_route, 12),
+                         METHOD(matmul_ep, 10), METHOD(matmul_packed_ep, 10), {"setup", setup, METH_VARARGS, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_qmm_call", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -661,6 +661,231 @@ QMM_EXPORT int qmm_attn_decode(int k_kind, int v_kind, const void *k_pages, cons
   return hip_status(qmm::launch_attn_decode(c, d, (hipStream_t)stream), "attn_decode launch");
 }
 
+// ---------------------------------------------------------------------------
+// Products with an epilogue, the norm, the choice of experts
+// ---------------------------------------------------------------------------
+namespace {
+
+bool dtype_ok(int dtype) { return dtype == QMM_F32 || dtype == QMM_F16; }
+
+// The types of an epilogue's operands.
+int check_epilogue_types(const qmm_epilogue *ep, int out_dtype) {
+  if (!dtype_ok(out_dtype) || (ep && ep->mul && !dtype_ok(ep->mul_dtype)) ||
+      (ep && ep->residual && !dtype_ok(ep->residual_dtype)))
+    return fail(QMM_ERR_BAD_DTYPE, "the dtype of out, mul or residual is neither QMM_F32 nor QMM_F16");
+  return QMM_OK;
+}
+
+int check_operand(const void *p, int dtype, int64_t stride, int64_t M, int64_t N, const char *what) {
+  int st = check_act(p, dtype, what);
+  if (st) return st;
+  if (stride < N || stride > ((int64_t)1 << 40) / M)
+    return fail(QMM_ERR_BAD_ARG, "the row stride %lld of %s is below its %lld elements or out of range",
+                (long long)stride, what, (long long)N);
+  return QMM_OK;
+}
+
+// The operands of an epilogue, and the launchers' form of it.
+int check_epilogue(const qmm_epilogue *ep, void *out, int out_dtype, int64_t out_stride, int64_t M, int64_t N,
+                   qmm::Epilogue *e) {
+  *e = qmm::Epilogue{};
+  int st = check_operand(out, out_dtype, out_stride, M, N, "out");
+  if (st) return st;
+  e->out = out, e->out_stride = out_stride, e->out_f16 = out_dtype == QMM_F16;
+  if (!ep) return QMM_OK;
+  if (ep->act < QMM_ACT_NONE || ep->act > QMM_ACT_GELU_TANH) return fail(QMM_ERR_BAD_ARG, "act %d is not an activation", ep->act);
+  if (ep->bias && !aligned(ep->bias, 4)) return fail(QMM_ERR_BAD_ARG, "bias is not 4-byte aligned");
+  if (ep->mul && (st = check_operand(ep->mul, ep->mul_dtype, ep->mul_stride, M, N, "mul"))) return st;
+  if (ep->residual && (st = check_operand(ep->residual, ep->residual_dtype, ep->residual_stride, M, N, "residual")))
+    return st;
+  if ((ep->mul == out && (ep->mul_dtype != out_dtype || ep->mul_stride != out_stride)) ||
+      (ep->residual == out && (ep->residual_dtype != out_dtype || ep->residual_stride != out_stride)))
+    return fail(QMM_ERR_BAD_ARG, "out in the place of mul or residual needs its type and stride");
+  e->bias = ep->bias, e->act = ep->act;
+  e->mul = ep->mul, e->mul_stride = ep->mul_stride, e->mul_f16 = ep->mul_dtype == QMM_F16;
+  e->residual = ep->residual, e->residual_stride = ep->residual_stride, e->residual_f16 = ep->residual_dtype == QMM_F16;
+  return QMM_OK;
+}
+
+}  // namespace
+
+QMM_EXPORT int qmm_matmul_ep(int kind, const void *W, const void *A, int a_dtype, const qmm_epilogue *ep, void *out,
+                             int out_dtype, int64_t out_stride, int64_t M, int64_t N, int64_t K, void *stream) {
+  const KindInfo *k;
+  int st = check_shape(kind, M, N, K, &k);
+  if (st) return st;
+  if ((st = check_dtype(a_dtype))) return st;
+  if ((st = check_epilogue_types(ep, out_dtype))) return st;
+  if (!W) return fail(QMM_ERR_BAD_ARG, "W is NULL");
+  if ((st = check_act(A, a_dtype, "A"))) return st;
+  if (M > (int64_t)65535 * 64) return fail(QMM_ERR_BAD_ARG, "M=%lld exceeds the supported range", (long long)M);
+  qmm::Epilogue e;
+  if ((st = check_epilogue(ep, out, out_dtype, out_stride, M, N, &e))) return st;
+  if (M <= QMM_GEMV_MAX_M)
+    return hip_status(qmm::launch_gemv(kind, (const uint8_t *)W, A, a_dtype == QMM_F16, e, (int)M, N, K,
+                                       (hipStream_t)stream),
+                      "matmul_ep launch (GEMV)");
+  return hip_status(qmm::launch_gemm(kind, (const uint8_t *)W, A, a_dtype == QMM_F16, e, M, N, K, (hipStream_t)stream),
+                    "matmul_ep launch (GEMM)");
+}
+
+QMM_EXPORT int qmm_matmul_packed_ep(int kind, const void *P, const void *A, int a_dtype, const qmm_epilogue *ep,
+                                    void *out, int out_dtype, int64_t out_stride, int64_t M, int64_t N, int64_t K,
+                                    void *stream) {
+  int st = check_packed(kind, M, N, K);
+  if (st) return st;
+  if (M > QMM_GEMV_MAX_M && !qmm::gemm_packed_supported(kind))
+    return fail(QMM_ERR_UNSUPPORTED_KIND, "the prefill GEMM over repacked weights does not take kind %d (M > %d)",
+                kind, QMM_GEMV_MAX_M);
+  if ((st = check_dtype(a_dtype))) return st;
+  if ((st = check_epilogue_types(ep, out_dtype))) return st;
+  if (!P) return fail(QMM_ERR_BAD_ARG, "P is NULL");
+  if (!aligned(P, 16)) return fail(QMM_ERR_BAD_ARG, "P is not 16-byte aligned");
+  if ((st = check_act(A, a_dtype, "A"))) return st;
+  if (M * K >= ((int64_t)1 << 31)) return fail(QMM_ERR_BAD_ARG, "M*K=%lld exceeds 2^31-1", (long long)(M * K));
+  // As qmm_matmul_packed: the GEMM's 32-bit byte offsets.
+  if (M > QMM_GEMV_MAX_M &&
+      (qmm::packed_bytes_of(kind, N, K) >= ((int64_t)1 << 31) ||
+       M * K * (a_dtype == QMM_F16 ? 2 : 4) >= ((int64_t)1 << 31) || M >= ((int64_t)1 << 24)))
+    return fail(QMM_ERR_BAD_ARG, "N=%lld, K=%lld, M=%lld exceed the GEMM's 32-bit offsets", (long long)N,
+                (long long)K, (long long)M);
+  qmm::Epilogue e;
+  if ((st = check_epilogue(ep, out, out_dtype, out_stride, M, N, &e))) return st;
+  if (M <= QMM_GEMV_MAX_M)
+    return hip_status(qmm::launch_gemv_packed(kind, (const uint8_t *)P, A, a_dtype == QMM_F16, e, (int)M, N, K,
+                                              (hipStream_t)stream),
+                      "matmul_packed_ep launch (GEMV)");
+  return hip_status(qmm::launch_gemm_packed(kind, (const uint8_t *)P, A, a_dtype == QMM_F16, e, M, N, K,
+                                            (hipStream_t)stream),
+                    "matmul_packed_ep launch (GEMM)");
+}
+
+QMM_EXPORT int qmm_gemv_q8(int kind, const void *P, const int8_t *codes, const float *scales, const int32_t *code_sums,
+                           const qmm_epilogue *ep, void *out, int out_dtype, int64_t out_stride, int64_t M, int64_t N,
+                           int64_t K, void *stream) {
+  int st = check_packed(kind, M, N, K);
+  if (st) return st;
+  if (!qmm::gemv_i8_supported(kind))
+    return fail(QMM_ERR_UNSUPPORTED_KIND,
+                "the int8-activation GEMV takes Q8_0, Q4_0, Q5_0, IQ4_NL or MXFP4 weights, not kind %d", kind);
+  if ((st = check_epilogue_types(ep, out_dtype))) return st;
+  if (!P || !aligned(P, 16)) return fail(QMM_ERR_BAD_ARG, "P is NULL or not 16-byte aligned");
+  if (!codes || !scales || !code_sums || !aligned(codes, 16) || !aligned(scales, 4) || !aligned(code_sums, 4))
+    return fail(QMM_ERR_BAD_ARG, "codes, scales or code_sums is NULL or misaligned");
+  if (M > QMM_GEMV_MAX_M || M * K > (int64_t)QMM_GEMV_I8_MAX_MK)
+    return fail(QMM_ERR_BAD_ARG, "M=%lld, K=%lld exceed %d tokens or M*K of %d", (long long)M, (long long)K,
+                QMM_GEMV_MAX_M, QMM_GEMV_I8_MAX_MK);
+  qmm::Epilogue e;
+  if ((st = check_epilogue(ep, out, out_dtype, out_stride, M, N, &e))) return st;
+  return hip_status(qmm::launch_gemv_q8(kind, (const uint8_t *)P, codes, scales, code_sums, e, (int)M, N, K,
+                                        (hipStream_t)stream),
+                    "gemv_q8 launch");
+}
+
+namespace {
+
+// qmm_rmsnorm and qmm_rmsnorm_q8 (its y in 8 bits) from the dtypes on.
+int rmsnorm_checked(qmm::Norm &n, int x_dtype, int residual_dtype, int y_dtype, void *stream) {
+  if (!dtype_ok(x_dtype) || !dtype_ok(y_dtype) || (n.residual && !dtype_ok(residual_dtype)))
+    return fail(QMM_ERR_BAD_DTYPE, "the dtype of x, residual or y is neither QMM_F32 nor QMM_F16");
+  n.x_f16 = x_dtype == QMM_F16, n.residual_f16 = residual_dtype == QMM_F16, n.y_f16 = y_dtype == QMM_F16;
+  if (n.D > qmm::kNormMaxD || n.H > 65536 || n.T > INT32_MAX || n.T * n.H > INT32_MAX ||
+      n.T * n.H * n.D > ((int64_t)1 << 40))
+    return fail(QMM_ERR_BAD_ARG, "T=%lld, H=%lld, D=%lld exceed the supported range (D up to %lld)", (long long)n.T,
+                (long long)n.H, (long long)n.D, (long long)qmm::kNormMaxD);
+  if (!(n.eps >= 0.0f) || !isfinite(n.eps)) return fail(QMM_ERR_BAD_ARG, "eps=%g is negative or not finite", (double)n.eps);
+  if (n.sum && !n.residual) return fail(QMM_ERR_BAD_ARG, "sum without a residual");
+  const int64_t row = n.H * n.D;
+  int st = check_rows(n.x, x_dtype, n.x_stride, row, n.T, "x");
+  if (st) return st;
+  if (n.residual && (st = check_rows(n.residual, residual_dtype, n.residual_stride, row, n.T, "residual"))) return st;
+  if (n.sum && (st = check_rows(n.sum, residual_dtype, n.sum_stride, row, n.T, "sum"))) return st;
+  if (n.weight && !aligned(n.weight, 4)) return fail(QMM_ERR_BAD_ARG, "weight is not 4-byte aligned");
+  if (!n.q8 && (st = check_rows(n.y, y_dtype, n.y_stride, row, n.T, "y"))) return st;
+  // In place only over the whole operand.
+  auto clash = [](const void *a, int ta, int64_t sa, const void *b, int tb, int64_t sb) {
+    return a && a == b && (ta != tb || sa != sb);
+  };
+  if (clash(n.sum, residual_dtype, n.sum_stride, n.x, x_dtype, n.x_stride) ||
+      clash(n.sum, residual_dtype, n.sum_stride, n.residual, residual_dtype, n.residual_stride) ||
+      clash(n.y, y_dtype, n.y_stride, n.x, x_dtype, n.x_stride) ||
+      clash(n.y, y_dtype, n.y_stride, n.residual, residual_dtype, n.residual_stride))
+    return fail(QMM_ERR_BAD_ARG, "writing in place needs equal types and strides");
+  if (n.sum && n.sum == n.y) return fail(QMM_ERR_BAD_ARG, "sum and y are one buffer");
+  return hip_status(qmm::launch_rmsnorm(n, (hipStream_t)stream), n.q8 ? "rmsnorm_q8 launch" : "rmsnorm launch");
+}
+
+qmm::Norm norm_of(const void *x, int64_t x_stride, const void *residual, int64_t residual_stride, const float *weight,
+                  float eps, void *sum, int64_t sum_stride, int64_t T, int64_t H, int64_t D) {
+  qmm::Norm n{};
+  n.x = x, n.x_stride = x_stride, n.residual = residual, n.residual_stride = residual_stride;
+  n.weight = weight, n.eps = eps, n.sum = sum, n.sum_stride = sum_stride, n.T = T, n.H = H, n.D = D;
+  return n;
+}
+
+}  // namespace
+
+QMM_EXPORT int qmm_rmsnorm(const void *x, int x_dtype, int64_t x_stride, const void *residual, int residual_dtype,
+                           int64_t residual_stride, const float *weight, float eps, void *sum, int64_t sum_stride,
+                           void *y, int y_dtype, int64_t y_stride, int64_t T, int64_t H, int64_t D, void *stream) {
+  if (T <= 0 || H <= 0 || D <= 0)
+    return fail(QMM_ERR_EMPTY_SHAPE, "empty shape: T=%lld H=%lld D=%lld", (long long)T, (long long)H, (long long)D);
+  qmm::Norm n = norm_of(x, x_stride, residual, residual_stride, weight, eps, sum, sum_stride, T, H, D);
+  n.y = y, n.y_stride = y_stride;
+  return rmsnorm_checked(n, x_dtype, residual_dtype, y_dtype, stream);
+}
+
+QMM_EXPORT int qmm_rmsnorm_q8(int kind, const void *x, int x_dtype, int64_t x_stride, const void *residual,
+                              int residual_dtype, int64_t residual_stride, const float *weight, float eps, void *sum,
+                              int64_t sum_stride, int8_t *codes, float *scales, int32_t *code_sums, int64_t T,
+                              int64_t D, void *stream) {
+  if (T <= 0 || D <= 0) return fail(QMM_ERR_EMPTY_SHAPE, "empty shape: T=%lld D=%lld", (long long)T, (long long)D);
+  if (!qmm::gemv_i8_supported(kind))
+    return fail(QMM_ERR_UNSUPPORTED_KIND,
+                "8-bit activations meet Q8_0, Q4_0, Q5_0, IQ4_NL or MXFP4 weights, not kind %d", kind);
+  if (D % 32 != 0) return fail(QMM_ERR_K_NOT_BLOCK_ALIGNED, "D=%lld is not a whole number of 32-element blocks", (long long)D);
+  if (!codes || !scales || !code_sums || !aligned(codes, 16) || !aligned(scales, 4) || !aligned(code_sums, 4)) {
+    // After the dtypes, as everywhere.
+    if (dtype_ok(x_dtype) && (!residual || dtype_ok(residual_dtype)))
+      return fail(QMM_ERR_BAD_ARG, "codes, scales or code_sums is NULL or misaligned");
+  }
+  qmm::Norm n = norm_of(x, x_stride, residual, residual_stride, weight, eps, sum, sum_stride, T, 1, D);
+  n.q8 = kind == QMM_Q8_0 ? 1 : 2;
+  n.codes = codes, n.scales = scales, n.code_sums = code_sums;
+  return rmsnorm_checked(n, x_dtype, residual_dtype, QMM_F32, stream);
+}
+
+QMM_EXPORT int qmm_moe_route(const void *logits, int dtype, int64_t stride, const float *bias, int64_t M, int64_t E,
+                             int64_t topk, int score, int64_t n_group, int64_t topk_group, int group_top,
+                             int normalize, float scale, const int32_t *slots, int32_t *ids, float *weights,
+                             void *stream) {
+  if (M <= 0 || E <= 0 || topk <= 0 || n_group <= 0)
+    return fail(QMM_ERR_EMPTY_SHAPE, "empty shape: M=%lld E=%lld topk=%lld n_group=%lld", (long long)M, (long long)E,
+                (long long)topk, (long long)n_group);
+  int st = check_dtype(dtype);
+  if (st) return st;
+  if (E > qmm::kMoeMaxExperts || topk > 64 || M > INT32_MAX)
+    return fail(QMM_ERR_BAD_ARG, "E=%lld, topk=%lld or M=%lld exceeds the supported range (%lld experts, 64 chosen)",
+                (long long)E, (long long)topk, (long long)M, (long long)qmm::kMoeMaxExperts);
+  if (n_group > 64 || E % n_group != 0 || topk_group < 1 || topk_group > n_group || (group_top != 1 && group_top != 2))
+    return fail(QMM_ERR_BAD_ARG, "n_group=%lld, topk_group=%lld, group_top=%d: up to 64 equal groups of the %lld experts, "
+                "1 to n_group of them kept by their largest 1 or 2", (long long)n_group, (long long)topk_group, group_top,
+                (long long)E);
+  if (topk > topk_group * (E / n_group))
+    return fail(QMM_ERR_BAD_ARG, "topk=%lld is more than the %lld experts of the kept groups", (long long)topk,
+                (long long)(topk_group * (E / n_group)));
+  if (score != QMM_ROUTE_SOFTMAX && score != QMM_ROUTE_SIGMOID) return fail(QMM_ERR_BAD_ARG, "score %d is unknown", score);
+  if (normalize != 0 && normalize != 1) return fail(QMM_ERR_BAD_ARG, "normalize must be 0 or 1");
+  if (!isfinite(scale)) return fail(QMM_ERR_BAD_ARG, "scale is not finite");
+  if ((st = check_rows(logits, dtype, stride, E, M, "logits"))) return st;
+  if ((bias && !aligned(bias, 4)) || (slots && !aligned(slots, 4)) || !ids || !weights || !aligned(ids, 4) ||
+      !aligned(weights, 4))
+    return fail(QMM_ERR_BAD_ARG, "ids or weights is NULL, or bias, slots, ids or weights is misaligned");
+  const qmm::Route r{logits, dtype == QMM_F16, stride, bias, M, E, topk, score == QMM_ROUTE_SIGMOID, n_group,
+                     topk_group, group_top, normalize, scale, slots, ids, weights};
+  return hip_status(qmm::launch_moe_route(r, (hipStream_t)stream), "moe_route launch");
+}
+
 QMM_EXPORT int qmm_dequant(int kind, const void *W, float *out, int64_t n_elems, void *stream) {
   if (n_elems <= 0) return fail(QMM_ERR_EMPTY_SHAPE, "empty shape: n_elems=%lld", (long long)n_elems);
   const KindInfo *k = find_kind(kind);

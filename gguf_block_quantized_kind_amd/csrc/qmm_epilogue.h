@@ -1,0 +1,58 @@
+// qmm_epilogue.h -- what a product does with each sum before it is stored.
+//
+// The product kernels write through QMM_OUT and put().  In their own files
+// QMM_OUT is the f32 result; the *_ep.hip files define QMM_WITH_EPILOGUE and
+// include the same kernels with an Epilogue (qmm_internal.h) in its place:
+//   out[m][n] = act(sum + bias[n]) * mul[m][n] + residual[m][n]
+// in f32, rounded once to out's type.  Every element is read and written by
+// one thread, its operands before its result, so out may be mul or residual.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "qmm.h"
+#include "qmm_internal.h"
+
+namespace qmm {
+
+// f32 activations.  Each is written so that its tail keeps its relative
+// accuracy: v * sigmoid as one quotient (an overflowing exponential gives the
+// limit, -0), gelu through erfc (1 + erf loses everything below -4).
+__device__ __forceinline__ float activated(int act, float v) {
+  switch (act) {
+    case QMM_ACT_RELU: return v < 0.f ? 0.f : v;  // a NaN stays one
+    case QMM_ACT_SILU: return v / (1.0f + expf(-v));
+    case QMM_ACT_GELU: return 0.5f * v * erfcf(v * -0.70710678118654752f);
+    case QMM_ACT_GELU_TANH: {
+      const float u = v + 0.044715f * v * v * v;
+      return v / (1.0f + expf(-1.5957691216057308f * u));  // 2 sqrt(2 / pi)
+    }
+    default: return v;
+  }
+}
+
+__device__ __forceinline__ float element(const void *p, int f16, int64_t i) {
+  return f16 ? (float)static_cast<const _Float16 *>(p)[i] : static_cast<const float *>(p)[i];
+}
+
+__device__ __forceinline__ void put(const Epilogue &e, int64_t m, int64_t n, int64_t, float v) {
+  if (e.bias) v += e.bias[n];
+  v = activated(e.act, v);
+  if (e.mul) v *= element(e.mul, e.mul_f16, m * e.mul_stride + n);
+  if (e.residual) v += element(e.residual, e.residual_f16, m * e.residual_stride + n);
+  if (e.out_f16)
+    static_cast<_Float16 *>(e.out)[m * e.out_stride + n] = (_Float16)v;
+  else
+    static_cast<float *>(e.out)[m * e.out_stride + n] = v;
+}
+__device__ __forceinline__ void put(float *Y, int64_t m, int64_t n, int64_t N, float v) { Y[m * N + n] = v; }
+
+#ifdef QMM_WITH_EPILOGUE
+#define QMM_OUT const Epilogue
+using Out = Epilogue;
+#else
+#define QMM_OUT float *__restrict__
+using Out = float *;
+#endif
+
+}  // namespace qmm

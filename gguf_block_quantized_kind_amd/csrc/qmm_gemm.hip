@@ -25,6 +25,7 @@
 #include <stdlib.h>
 
 #include "qmm_gemm_dec.h"
+#include "qmm_epilogue.h"
 #include "qmm_internal.h"
 
 namespace qmm {
@@ -47,7 +48,7 @@ struct Tile {
 
 template <int KIND, typename AT, int BM, int BN, int BK, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(const uint8_t *__restrict__ W, int64_t row_bytes,
-                                                            const AT *__restrict__ A, float *__restrict__ C,
+                                                            const AT *__restrict__ A, QMM_OUT C,
                                                             int M, int N, int K) {
   constexpr int T = 64 * WM * WN;
   constexpr bool kSplit = sizeof(AT) == 4;
@@ -230,7 +231,7 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(const uint8_t *__res
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const int m = m0 + wm * TM * 16 + 16 * i + rq + q;
-        if (m < M) C[(int64_t)m * N + n] = acc[i][j][q];
+        if (m < M) put(C, m, n, N, acc[i][j][q]);
       }
     }
 }
@@ -239,7 +240,7 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(const uint8_t *__res
 constexpr size_t kMaxLds = 160 * 1024;
 
 template <int KIND, typename AT, int BM, int BN, int BK, int WM, int WN>
-static hipError_t run_as(const uint8_t *W, const void *A, float *C, int64_t M, int64_t N, int64_t K,
+static hipError_t run_as(const uint8_t *W, const void *A, Out C, int64_t M, int64_t N, int64_t K,
                          hipStream_t s) {
   constexpr size_t lds = Tile<BM, BN, BK, sizeof(AT) == 4>::LDS_BYTES;
   if constexpr (lds > kMaxLds) {
@@ -254,7 +255,7 @@ static hipError_t run_as(const uint8_t *W, const void *A, float *C, int64_t M, i
 }
 
 template <int KIND, int BM, int BN, int BK, int WM, int WN>
-static hipError_t run(const uint8_t *W, const void *A, int a_f16, float *C, int64_t M, int64_t N, int64_t K,
+static hipError_t run(const uint8_t *W, const void *A, int a_f16, Out C, int64_t M, int64_t N, int64_t K,
                       hipStream_t s) {
   return a_f16 ? run_as<KIND, _Float16, BM, BN, BK, WM, WN>(W, A, C, M, N, K, s)
                : run_as<KIND, float, BM, BN, BK, WM, WN>(W, A, C, M, N, K, s);
@@ -267,7 +268,7 @@ static hipError_t run(const uint8_t *W, const void *A, int a_f16, float *C, int6
 // stages for f32 A, whose two f16 planes would need 192 KiB of LDS with
 // 128-element stages.
 template <int KIND>
-static hipError_t run_m(const uint8_t *W, const void *A, int a_f16, float *C, int64_t M, int64_t N, int64_t K,
+static hipError_t run_m(const uint8_t *W, const void *A, int a_f16, Out C, int64_t M, int64_t N, int64_t K,
                         hipStream_t s, int cfg) {
 #ifdef QMM_TUNING
   switch (cfg) {
@@ -293,13 +294,13 @@ static hipError_t run_m(const uint8_t *W, const void *A, int a_f16, float *C, in
 
 }  // namespace gm
 
-hipError_t launch_gemm(int kind, const uint8_t *W, const void *A, int a_f16, float *C, int64_t M,
+hipError_t launch_gemm(int kind, const uint8_t *W, const void *A, int a_f16, Out C, int64_t M,
                        int64_t N, int64_t K, hipStream_t s) {
   if (gemm_ks_supported(kind, M, N, K, a_f16)) return launch_gemm_ks(kind, W, A, a_f16, C, M, N, K, s);
   return launch_gemm_lds(kind, W, A, a_f16, C, M, N, K, s);
 }
 
-hipError_t launch_gemm_lds(int kind, const uint8_t *W, const void *A, int a_f16, float *C, int64_t M,
+hipError_t launch_gemm_lds(int kind, const uint8_t *W, const void *A, int a_f16, Out C, int64_t M,
                            int64_t N, int64_t K, hipStream_t s) {
   // Launch shapes are fixed by the rules in run_m.  A tuning build
   // (-DQMM_TUNING) can pick an alternative shape from QMM_GEMM_CFG.

@@ -32,6 +32,7 @@
 #include <type_traits>
 
 #include "qmm_gemm_ks.h"
+#include "qmm_epilogue.h"
 #include "qmm_internal.h"
 
 // The kinds this GEMM serves: the super-block kinds whose decode it does
@@ -115,7 +116,7 @@ struct WRow {
 
 template <int KIND, typename AT, int TM, int TN>
 __global__ __launch_bounds__(64 * kWaves, kWgPerCu) void gemm_ks_kernel(const uint8_t *__restrict__ W, uint32_t row_bytes,
-                                                                  const AT *__restrict__ A, float *__restrict__ C,
+                                                                  const AT *__restrict__ A, QMM_OUT C,
                                                                   int M, int N, int K, int tiles_m) {
   using F = Frag<KIND>;
   using AS = AStage<AT, TM>;
@@ -303,7 +304,7 @@ __global__ __launch_bounds__(64 * kWaves, kWgPerCu) void gemm_ks_kernel(const ui
                         red[(3 * kRedChunk + vl) * 64 + lane];
         const int i = (v >> 2) / TN, j = (v >> 2) % TN;
         const int m = m0 + 16 * i + rq + (v & 3), n = n0 + 16 * j + col;
-        if (m < M && n < N) C[(int64_t)m * N + n] = s;
+        if (m < M && n < N) put(C, m, n, N, s);
       }
     }
   }
@@ -312,7 +313,7 @@ __global__ __launch_bounds__(64 * kWaves, kWgPerCu) void gemm_ks_kernel(const ui
 constexpr size_t kRedLds = (size_t)kWaves * kRedChunk * 64 * sizeof(float);
 
 template <int KIND, typename AT, int TM, int TN>
-static hipError_t run_as(const uint8_t *W, const void *A, float *C, int64_t M, int64_t N, int64_t K, hipStream_t s) {
+static hipError_t run_as(const uint8_t *W, const void *A, Out C, int64_t M, int64_t N, int64_t K, hipStream_t s) {
   constexpr size_t ring = (size_t)kWaves * Stage<KIND, AT, TM, TN>::BYTES;
   constexpr size_t lds = ring > kRedLds ? ring : kRedLds;
   if constexpr (lds > 160 * 1024 / kWgPerCu) {
@@ -329,7 +330,7 @@ static hipError_t run_as(const uint8_t *W, const void *A, float *C, int64_t M, i
 // f32 activations take tiles of half as many tokens: a step of 64 f32 per
 // row is twice the LDS of f16.
 template <int KIND, int TM, int TN>
-static hipError_t run(const uint8_t *W, const void *A, int a_f16, float *C, int64_t M, int64_t N, int64_t K,
+static hipError_t run(const uint8_t *W, const void *A, int a_f16, Out C, int64_t M, int64_t N, int64_t K,
                       hipStream_t s) {
   return a_f16 ? run_as<KIND, _Float16, TM, TN>(W, A, C, M, N, K, s)
                : run_as<KIND, float, TM / 2, TN>(W, A, C, M, N, K, s);
@@ -340,7 +341,7 @@ static hipError_t run(const uint8_t *W, const void *A, int a_f16, float *C, int6
 // would leave the last round of workgroups on the 256 compute units mostly
 // empty and 176-row tiles fit in one round.
 template <int KIND>
-static hipError_t run_m(const uint8_t *W, const void *A, int a_f16, float *C, int64_t M, int64_t N, int64_t K,
+static hipError_t run_m(const uint8_t *W, const void *A, int a_f16, Out C, int64_t M, int64_t N, int64_t K,
                         hipStream_t s, int cfg) {
   // Kinds whose step needs more chunk slots per row take 64-row tiles so
   // that two stages of four waves fit the 160 KiB of LDS.
@@ -361,6 +362,7 @@ static hipError_t run_m(const uint8_t *W, const void *A, int a_f16, float *C, in
 
 }  // namespace gk
 
+#ifndef QMM_WITH_EPILOGUE
 bool gemm_ks_supported(int kind, int64_t M, int64_t N, int64_t K, int a_f16) {
   int64_t row_bytes = -1;
   switch (kind) {
@@ -375,8 +377,9 @@ bool gemm_ks_supported(int kind, int64_t M, int64_t N, int64_t K, int a_f16) {
   return row_bytes > 0 && M * K * (a_f16 ? 2 : 4) < ((int64_t)1 << 31) && N * row_bytes < ((int64_t)1 << 31) &&
          (M + 31) / 32 * ((N + 63) / 64) < ((int64_t)1 << 31);
 }
+#endif
 
-hipError_t launch_gemm_ks(int kind, const uint8_t *W, const void *A, int a_f16, float *C, int64_t M, int64_t N,
+hipError_t launch_gemm_ks(int kind, const uint8_t *W, const void *A, int a_f16, Out C, int64_t M, int64_t N,
                           int64_t K, hipStream_t s) {
 #ifdef QMM_TUNING
   static const int cfg = [] {

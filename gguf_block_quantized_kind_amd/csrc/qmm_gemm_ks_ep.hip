@@ -1,0 +1,3 @@
+// The kernels of qmm_gemm_ks.hip with an epilogue before the store (qmm_epilogue.h).
+#define QMM_WITH_EPILOGUE
+#include "qmm_gemm_ks.hip"

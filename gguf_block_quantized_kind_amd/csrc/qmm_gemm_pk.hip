@@ -27,6 +27,7 @@
 #include <stdlib.h>
 
 #include "qmm_gemm_dec.h"
+#include "qmm_epilogue.h"
 #include "qmm_internal.h"
 
 namespace qmm {
@@ -284,7 +285,7 @@ struct AStage {
 // and scale-row buffers are fixed per unrolled position.
 template <int KIND, typename AT, int TM, int TN, int KQ, int NH>
 __global__ __launch_bounds__(64 * KQ * NH, 1) void gemm_pk_kernel(const uint8_t *__restrict__ P,
-                                                                  const AT *__restrict__ A, float *__restrict__ C,
+                                                                  const AT *__restrict__ A, QMM_OUT C,
                                                                   int M, int N, int K, int tiles_m) {
   using R = Rows<KIND, TN>;
   using AS = AStage<AT, TM>;
@@ -513,14 +514,14 @@ __global__ __launch_bounds__(64 * KQ * NH, 1) void gemm_pk_kernel(const uint8_t 
         for (int q = 1; q < KQ; ++q) sum += red[((q * NH + wh) * kRedChunk + vl) * 64 + lane];
         const int tm = (v >> 2) / TN, tn = (v >> 2) % TN;
         const int m = m0 + 16 * tm + 4 * G + (v & 3), n = n0 + 16 * tn + j;
-        if (m < M && n < N) C[(int64_t)m * N + n] = sum;
+        if (m < M && n < N) put(C, m, n, N, sum);
       }
     }
   }
 }
 
 template <int KIND, typename AT, int TM, int TN, int KQ, int NH>
-static hipError_t run(const uint8_t *P, const void *A, float *C, int64_t M, int64_t N, int64_t K, hipStream_t s) {
+static hipError_t run(const uint8_t *P, const void *A, Out C, int64_t M, int64_t N, int64_t K, hipStream_t s) {
   constexpr int KW = KQ * NH;
   const int64_t tm = (M + 16 * TM - 1) / (16 * TM), tn = (N + 16 * TN * NH - 1) / (16 * TN * NH);
   static_assert((size_t)KQ * kRing * AStage<AT, TM>::BYTES <= 160 * 1024, "one workgroup per compute unit");
@@ -532,7 +533,7 @@ static hipError_t run(const uint8_t *P, const void *A, float *C, int64_t M, int6
 // The k parts must divide the k-block count: four where they do (two for
 // f32 activations, whose staging is twice the size), else two, else one.
 template <int KIND, int TM, int TN, int NH>
-static hipError_t run_any(const uint8_t *P, const void *A, int a_f16, float *C, int64_t M, int64_t N, int64_t K,
+static hipError_t run_any(const uint8_t *P, const void *A, int a_f16, Out C, int64_t M, int64_t N, int64_t K,
                           hipStream_t s) {
   const int64_t nkb = K / 256;
   if (a_f16) {
@@ -545,7 +546,7 @@ static hipError_t run_any(const uint8_t *P, const void *A, int a_f16, float *C, 
 }
 
 template <int KIND>
-static hipError_t run_kind(const uint8_t *P, const void *A, int a_f16, float *C, int64_t M, int64_t N, int64_t K,
+static hipError_t run_kind(const uint8_t *P, const void *A, int a_f16, Out C, int64_t M, int64_t N, int64_t K,
                            hipStream_t s) {
 #ifdef QMM_TUNING
   static const int cfg = [] {
@@ -577,11 +578,13 @@ static hipError_t run_kind(const uint8_t *P, const void *A, int a_f16, float *C,
 
 }  // namespace pk
 
+#ifndef QMM_WITH_EPILOGUE
 bool gemm_packed_supported(int kind) {
   return kind == Q8_0 || kind == Q4_0 || kind == Q5_0 || kind == IQ4_NL || kind == MXFP4 || kind == IQ4_XS;
 }
+#endif
 
-hipError_t launch_gemm_packed(int kind, const uint8_t *P, const void *A, int a_f16, float *C, int64_t M, int64_t N,
+hipError_t launch_gemm_packed(int kind, const uint8_t *P, const void *A, int a_f16, Out C, int64_t M, int64_t N,
                               int64_t K, hipStream_t s) {
   switch (kind) {
     case Q8_0: return pk::run_kind<Q8_0>(P, A, a_f16, C, M, N, K, s);

@@ -6,6 +6,7 @@
 // f32.  A wave-wide reduction ends the row.  Every weight is exact, so with a
 // unit-vector x the result is the decoded weight itself.
 #include "qmm_device.h"
+#include "qmm_epilogue.h"
 #include "qmm_internal.h"
 
 namespace qmm {
@@ -14,7 +15,7 @@ template <typename XT> __device__ __forceinline__ float to_f32(XT v) { return (f
 
 template <int KIND, typename XT>
 __global__ __launch_bounds__(256) void gemv_rows_kernel(const uint8_t *__restrict__ W, int64_t row_bytes,
-                                                        const XT *__restrict__ X, float *__restrict__ Y,
+                                                        const XT *__restrict__ X, QMM_OUT Y,
                                                         int M, int64_t N, int K) {
   const int lane = threadIdx.x & 63;
   const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
@@ -43,12 +44,12 @@ __global__ __launch_bounds__(256) void gemv_rows_kernel(const uint8_t *__restric
   if (lane == 0) {
 #pragma unroll
     for (int m = 0; m < 8; ++m)
-      if (m < M) Y[(int64_t)m * N + row] = acc[m];
+      if (m < M) put(Y, m, row, N, acc[m]);
   }
 }
 
 template <int KIND>
-static hipError_t run_gemv(const uint8_t *W, const void *x, int x_f16, float *y, int M, int64_t N,
+static hipError_t run_gemv(const uint8_t *W, const void *x, int x_f16, Out y, int M, int64_t N,
                            int64_t K, hipStream_t s) {
   const int64_t row_bytes = (K / Geometry<KIND>::elems) * Geometry<KIND>::bytes;
   const dim3 grid((unsigned)((N + 3) / 4)), block(256);
@@ -61,7 +62,7 @@ static hipError_t run_gemv(const uint8_t *W, const void *x, int x_f16, float *y,
   return hipGetLastError();
 }
 
-hipError_t launch_gemv(int kind, const uint8_t *W, const void *x, int x_f16, float *y, int M,
+hipError_t launch_gemv(int kind, const uint8_t *W, const void *x, int x_f16, Out y, int M,
                        int64_t N, int64_t K, hipStream_t s) {
   const hipError_t e = launch_gemv_mfma(kind, W, x, x_f16, y, M, N, K, s);
   if (e != hipErrorNotSupported) return e;

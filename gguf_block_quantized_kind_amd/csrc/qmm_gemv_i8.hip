@@ -30,6 +30,7 @@
 #include <mutex>
 
 #include "qmm.h"
+#include "qmm_epilogue.h"
 #include "qmm_gemv_mfma.h"
 #include "qmm_internal.h"
 
@@ -56,6 +57,7 @@ __device__ __forceinline__ int position_of(int e) {
   }
 }
 
+#ifndef QMM_WITH_EPILOGUE
 // One thread per element, 32 consecutive threads per (token, block): the
 // block maximum and the code sum are reduced across the 32 lanes, so the
 // quantization takes a few steps instead of a 32-element loop per thread.
@@ -85,6 +87,7 @@ __global__ __launch_bounds__(256) void quantize_kernel(const XT *__restrict__ X,
     s[i] = sum;
   }
 }
+#endif
 
 // B operand of step c: the 8 codes of block 2c, then the 8 of block 2c+1.
 // Twice the E2M1 value of each of four 4-bit codes (one per byte), as signed
@@ -147,7 +150,7 @@ __device__ __forceinline__ void block_scales(const typename gv::Rec<KIND>::Packe
 template <int KIND, int S, int PD>
 __global__ __launch_bounds__(64 * S) void gemv_i8_kernel(const uint8_t *__restrict__ P, const int8_t *__restrict__ q,
                                                         const float *__restrict__ dx, const int32_t *__restrict__ sx,
-                                                        float *__restrict__ Y, int M, int64_t N, int K) {
+                                                        QMM_OUT Y, int M, int64_t N, int K) {
   using Rc = gv::Rec<KIND>;
   using Packed = typename Rc::Packed;
   constexpr int kBias = KIND == Q4_0 ? 8 : KIND == Q5_0 ? 16 : 0;
@@ -232,12 +235,12 @@ __global__ __launch_bounds__(64 * S) void gemv_i8_kernel(const uint8_t *__restri
   }
   const int64_t row = tile * 16 + j;
   if (row >= N) return;
-  if (2 * G < M) Y[(int64_t)(2 * G) * N + row] = y0;
-  if (2 * G + 1 < M) Y[(int64_t)(2 * G + 1) * N + row] = y1;
+  if (2 * G < M) put(Y, 2 * G, row, N, y0);
+  if (2 * G + 1 < M) put(Y, 2 * G + 1, row, N, y1);
 }
 
 template <int KIND, int S, int PD>
-hipError_t run(const uint8_t *P, const int8_t *q, const float *d, const int32_t *s, float *y, int M, int64_t N,
+hipError_t run(const uint8_t *P, const int8_t *q, const float *d, const int32_t *s, Out y, int M, int64_t N,
                int64_t K, hipStream_t st) {
   const size_t stage = (size_t)M * (K / 32) * 8;
   const size_t red = (size_t)(S - 1) * 64 * 8;
@@ -250,7 +253,7 @@ hipError_t run(const uint8_t *P, const int8_t *q, const float *d, const int32_t 
 // Launch shape: S waves split K, PD k-blocks in flight.  A tuning build
 // (-DQMM_TUNING) can pick another from QMM_GEMV_I8_CFG.
 template <int KIND>
-hipError_t run_shape(const uint8_t *P, const int8_t *q, const float *d, const int32_t *s, float *y, int M,
+hipError_t run_shape(const uint8_t *P, const int8_t *q, const float *d, const int32_t *s, Out y, int M,
                      int64_t N, int64_t K, hipStream_t st) {
 #ifdef QMM_TUNING
   static const int cfg = [] {
@@ -272,6 +275,7 @@ hipError_t run_shape(const uint8_t *P, const int8_t *q, const float *d, const in
   return run<KIND, 4, 1>(P, q, d, s, y, M, N, K, st);
 }
 
+#ifndef QMM_WITH_EPILOGUE
 size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 
 template <int KIND>
@@ -284,9 +288,26 @@ void quantize(const void *x, int x_f16, int8_t *q, float *d, int32_t *s, int64_t
     hipLaunchKernelGGL((quantize_kernel<KIND, float>), dim3(grid), dim3(256), 0, st, (const float *)x, q, d, s,
                        blocks, nb);
 }
+#endif
 
 }  // namespace i8
 
+// The product over quantized activations: codes [M][K], scales and code sums
+// [M][K/32].
+hipError_t launch_gemv_q8(int kind, const uint8_t *P, const int8_t *q, const float *d, const int32_t *s, Out y, int M,
+                          int64_t N, int64_t K, hipStream_t st) {
+  switch (kind) {
+    case Q8_0: return i8::run_shape<Q8_0>(P, q, d, s, y, M, N, K, st);
+    case Q4_0: return i8::run_shape<Q4_0>(P, q, d, s, y, M, N, K, st);
+    case Q5_0: return i8::run_shape<Q5_0>(P, q, d, s, y, M, N, K, st);
+    case IQ4_NL: return i8::run_shape<IQ4_NL>(P, q, d, s, y, M, N, K, st);
+    case MXFP4: return i8::run_shape<MXFP4>(P, q, d, s, y, M, N, K, st);
+    default: break;
+  }
+  return hipErrorNotSupported;
+}
+
+#ifndef QMM_WITH_EPILOGUE
 bool gemv_i8_supported(int kind) {
   return kind == Q8_0 || kind == Q4_0 || kind == Q5_0 || kind == IQ4_NL || kind == MXFP4;
 }
@@ -347,15 +368,8 @@ hipError_t launch_gemv_i8(int kind, const uint8_t *P, const void *x, int x_f16, 
     i8::quantize<Q4_0>(x, x_f16, q, d, s, blocks, nb, grid, st);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  switch (kind) {
-    case Q8_0: return i8::run_shape<Q8_0>(P, q, d, s, y, M, N, K, st);
-    case Q4_0: return i8::run_shape<Q4_0>(P, q, d, s, y, M, N, K, st);
-    case Q5_0: return i8::run_shape<Q5_0>(P, q, d, s, y, M, N, K, st);
-    case IQ4_NL: return i8::run_shape<IQ4_NL>(P, q, d, s, y, M, N, K, st);
-    case MXFP4: return i8::run_shape<MXFP4>(P, q, d, s, y, M, N, K, st);
-    default: break;
-  }
-  return hipErrorNotSupported;
+  return launch_gemv_q8(kind, P, q, d, s, y, M, N, K, st);
 }
+#endif
 
 }  // namespace qmm

@@ -1,0 +1,3 @@
+// The kernels of qmm_gemv_i8.hip with an epilogue before the store (qmm_epilogue.h).
+#define QMM_WITH_EPILOGUE
+#include "qmm_gemv_i8.hip"

@@ -9,6 +9,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "qmm_epilogue.h"
 #include "qmm_gemv_mfma.h"
 #include "qmm_internal.h"
 
@@ -55,7 +56,7 @@ using Held = typename HeldOf<KIND, PACKED, Dd>::type;
 // qmm_gemv_mfma.h) instead of native rows; row_bytes is then unused.
 template <int KIND, typename XT, int MT, int S, int R, int PD, int OCC, bool ROUTED, bool PACKED>
 __global__ __launch_bounds__(64 * S) __attribute__((amdgpu_waves_per_eu(OCC, 8))) void gemv_mfma_kernel(
-    const uint8_t *__restrict__ W, int64_t row_bytes, const XT *__restrict__ X, float *__restrict__ Y, int M,
+    const uint8_t *__restrict__ W, int64_t row_bytes, const XT *__restrict__ X, QMM_OUT Y, int M,
     int64_t N, int K, MoeRoute rt) {
   using Dd = Dec<KIND>;
   using XS = XSlice<KIND, MT>;
@@ -276,13 +277,13 @@ __global__ __launch_bounds__(64 * S) __attribute__((amdgpu_waves_per_eu(OCC, 8))
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int t = 4 * G + q;
-      if (t < M) Y[(int64_t)(ROUTED ? pair_of(t) : t) * N + row] = acc[r][q];
+      if (t < M) put(Y, ROUTED ? pair_of(t) : t, row, N, acc[r][q]);
     }
   }
 }
 
 template <int KIND, int MT, int S, int R, int PD, int OCC = 1, bool ROUTED = false, bool PACKED = false>
-static hipError_t run(const uint8_t *W, const void *x, int x_f16, float *y, int M, int64_t N, int64_t K,
+static hipError_t run(const uint8_t *W, const void *x, int x_f16, Out y, int M, int64_t N, int64_t K,
                       hipStream_t s, MoeRoute rt = MoeRoute{}, int items = 0) {
   const int64_t row_bytes = (K / Geometry<KIND>::elems) * Geometry<KIND>::bytes;
   const size_t ring = (size_t)S * (PD + 1) * XSlice<KIND, MT>::kFrag * 16 + 16 +
@@ -302,7 +303,7 @@ static hipError_t run(const uint8_t *W, const void *x, int x_f16, float *y, int 
 // Launch shapes, chosen by M: small M keeps many k-blocks in flight per
 // wave; large M shares each staged activation k-block among R tiles.
 template <int KIND>
-static hipError_t run_m(const uint8_t *W, const void *x, int x_f16, float *y, int M, int64_t N, int64_t K,
+static hipError_t run_m(const uint8_t *W, const void *x, int x_f16, Out y, int M, int64_t N, int64_t K,
                         hipStream_t s, int cfg) {
 #ifdef QMM_TUNING
   switch (cfg) {
@@ -337,6 +338,7 @@ static hipError_t run_m(const uint8_t *W, const void *x, int x_f16, float *y, in
   return run<KIND, 8, 2, 2, 2>(W, x, x_f16, y, M, N, K, s);
 }
 
+#ifndef QMM_WITH_EPILOGUE
 template <int KIND, bool PACKED>
 static hipError_t run_routed(const uint8_t *W, const void *x, int x_f16, float *y, int mt, int64_t N, int64_t K,
                              hipStream_t s, const MoeRoute &rt, int items) {
@@ -351,13 +353,14 @@ static hipError_t run_routed(const uint8_t *W, const void *x, int x_f16, float *
   // four 16-row tiles.
   return run<KIND, 16, 1, 4, 1, 1, true, PACKED>(W, x, x_f16, y, 16, N, K, s, rt, items);
 }
+#endif
 
 // Launch shapes over the repacked layout (no staging), for what the kernels
 // of qmm_gemv_t1.hip and qmm_gemv_xs.hip do not take (in default builds:
 // Q2_K, Q3_K and Q5_K at one token).  Fewer waves per tile (two tiles per
 // wave) measured 40-70% slower at one token.
 template <int KIND>
-static hipError_t run_packed(const uint8_t *P, const void *x, int x_f16, float *y, int M, int64_t N, int64_t K,
+static hipError_t run_packed(const uint8_t *P, const void *x, int x_f16, Out y, int M, int64_t N, int64_t K,
                              hipStream_t s, int cfg) {
 #ifdef QMM_TUNING
   switch (cfg) {
@@ -421,6 +424,7 @@ static hipError_t run_packed(const uint8_t *P, const void *x, int x_f16, float *
 
 }  // namespace gv
 
+#ifndef QMM_WITH_EPILOGUE
 bool packed_supported(int kind) {
   switch (kind) {
     case Q4_K: case Q6_K: case IQ4_XS: case Q4_0: case Q5_0: case Q8_0: case IQ4_NL: case MXFP4:
@@ -430,8 +434,9 @@ bool packed_supported(int kind) {
       return false;
   }
 }
+#endif
 
-hipError_t launch_gemv_packed(int kind, const uint8_t *P, const void *x, int x_f16, float *y, int M, int64_t N,
+hipError_t launch_gemv_packed(int kind, const uint8_t *P, const void *x, int x_f16, Out y, int M, int64_t N,
                               int64_t K, hipStream_t s) {
 #ifdef QMM_TUNING
   static const int cfg = [] {
@@ -465,6 +470,7 @@ hipError_t launch_gemv_packed(int kind, const uint8_t *P, const void *x, int x_f
   return hipErrorNotSupported;
 }
 
+#ifndef QMM_WITH_EPILOGUE
 bool moe_mfma_supported(int kind, int64_t K) {
   switch (kind) {
     case Q4_K: case Q6_K: case IQ4_XS: case Q4_0: case Q5_0: case Q8_0: case IQ4_NL: case MXFP4:
@@ -517,10 +523,11 @@ hipError_t launch_moe_mfma(int kind, const uint8_t *W, const void *X, int x_f16,
   }
   return hipErrorNotSupported;
 }
+#endif
 
 // Returns hipErrorNotSupported when the kind has no matrix-core decoder or K
 // is not a whole number of the decoder's k-blocks.
-hipError_t launch_gemv_mfma(int kind, const uint8_t *W, const void *x, int x_f16, float *y, int M,
+hipError_t launch_gemv_mfma(int kind, const uint8_t *W, const void *x, int x_f16, Out y, int M,
                             int64_t N, int64_t K, hipStream_t s) {
   // Activation offsets are 32-bit inside the kernel.
   if ((int64_t)M * K >= ((int64_t)1 << 31)) return hipErrorNotSupported;

@@ -39,6 +39,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "qmm_epilogue.h"
 #include "qmm_gemv_mfma.h"
 #include "qmm_gemv_t1.h"
 #include "qmm_internal.h"
@@ -52,7 +53,7 @@ namespace gv {
 // are skipped), activations row x_per_slot ? i : i / topk, output row i.
 template <int KIND, typename XT, int S, int PD, int OCC, bool PACKED, bool ROUTED>
 __global__ __launch_bounds__(64 * S) __attribute__((amdgpu_waves_per_eu(OCC, 8))) void gemv_t1_kernel(
-    const uint8_t *__restrict__ W, int64_t row_bytes, const XT *__restrict__ X, float *__restrict__ Y, int64_t N,
+    const uint8_t *__restrict__ W, int64_t row_bytes, const XT *__restrict__ X, QMM_OUT Y, int64_t N,
     int K, MoeRoute rt) {
   using Tr = T1<KIND>;
   using Dd = typename Tr::Dd;
@@ -70,13 +71,14 @@ __global__ __launch_bounds__(64 * S) __attribute__((amdgpu_waves_per_eu(OCC, 8))
   const int j = lane & 15, G = lane >> 4;
   const int64_t tile = blockIdx.x;
   const int nkb = K / Dd::KB;
+  [[maybe_unused]] int64_t out_row = 0;
   if constexpr (ROUTED) {
     const int pair = blockIdx.y;
     const int e = pair < rt.pairs ? rt.ids[pair] : -1;
     if (e < 0 || e >= rt.E) return;  // the whole workgroup, before any barrier
     W += (int64_t)e * (PACKED ? (N + 15) / 16 * nkb * kRec : N * row_bytes);
     X += (int64_t)(rt.x_per_slot ? pair : pair / rt.topk) * K;
-    Y += (int64_t)pair * N;
+    out_row = pair;
   }
   const int kb0 = (int)((int64_t)wave * nkb / S), kb1 = (int)((int64_t)(wave + 1) * nkb / S);
   const int kb_last = max(kb1 - 1, 0);
@@ -161,11 +163,11 @@ __global__ __launch_bounds__(64 * S) __attribute__((amdgpu_waves_per_eu(OCC, 8))
     for (int w = 0; w < S - 1; ++w) acc += red[w * 16 + (lane & 15)];
   }
   const int64_t row = tile * 16 + j;
-  if (lane < 16 && row < N) Y[row] = acc;
+  if (lane < 16 && row < N) put(Y, out_row, row, N, acc);
 }
 
 template <int KIND, int S, int PD, int OCC = 1, bool PACKED = true, bool ROUTED = false>
-static hipError_t run_t1(const uint8_t *W, const void *x, int x_f16, float *y, int64_t N, int64_t K, hipStream_t s,
+static hipError_t run_t1(const uint8_t *W, const void *x, int x_f16, Out y, int64_t N, int64_t K, hipStream_t s,
                          const MoeRoute &rt = MoeRoute{}, int items = 1) {
   constexpr int kFrag = T1<KIND>::Dd::NSTEP * 4;
   const size_t lds = std::max<size_t>((size_t)S * (PD + 2) * kFrag * 16, (size_t)(S - 1) * 16 * 4);
@@ -183,7 +185,7 @@ static hipError_t run_t1(const uint8_t *W, const void *x, int x_f16, float *y, i
 }
 
 template <int KIND, bool PACKED>
-static hipError_t run_t1_k(const uint8_t *P, const void *x, int x_f16, float *y, int64_t N, int64_t K, hipStream_t s,
+static hipError_t run_t1_k(const uint8_t *P, const void *x, int x_f16, Out y, int64_t N, int64_t K, hipStream_t s,
                            int cfg) {
 #ifdef QMM_TUNING
   switch (cfg) {
@@ -222,6 +224,7 @@ static hipError_t run_t1_k(const uint8_t *P, const void *x, int x_f16, float *y,
   }
 }
 
+#ifndef QMM_WITH_EPILOGUE
 // Routed pairs: K of three k-blocks (an expert down matrix of 768 columns)
 // takes three waves of one k-block each, else the shapes above.
 template <int KIND, bool PACKED>
@@ -230,9 +233,11 @@ static hipError_t run_t1_routed(const uint8_t *W, const void *x, int x_f16, floa
   if (K == 3 * T1<KIND>::Dd::KB) return run_t1<KIND, 3, 1, 1, PACKED, true>(W, x, x_f16, y, N, K, s, rt, items);
   return run_t1<KIND, 2, PACKED ? 1 : 2, 1, PACKED, true>(W, x, x_f16, y, N, K, s, rt, items);
 }
+#endif
 
 }  // namespace gv
 
+#ifndef QMM_WITH_EPILOGUE
 // Over native rows only the super-block kinds: the step-scaled kinds read
 // native rows through an LDS staging (the matrix-core GEMV's), with which
 // this kernel measured no faster (Q4_0, IQ4_NL, IQ4_XS) or slower (MXFP4
@@ -244,8 +249,9 @@ bool gemv_t1_supported(int kind, bool packed) {
     default: return false;
   }
 }
+#endif
 
-hipError_t launch_gemv_t1(int kind, const uint8_t *W, const void *x, int x_f16, float *y, int64_t N, int64_t K,
+hipError_t launch_gemv_t1(int kind, const uint8_t *W, const void *x, int x_f16, Out y, int64_t N, int64_t K,
                           hipStream_t s, int cfg, bool packed) {
   if (!gemv_t1_supported(kind, packed)) return hipErrorNotSupported;
   switch (kind) {
@@ -268,6 +274,7 @@ hipError_t launch_gemv_t1(int kind, const uint8_t *W, const void *x, int x_f16, 
   return hipErrorNotSupported;
 }
 
+#ifndef QMM_WITH_EPILOGUE
 hipError_t launch_moe_t1(int kind, const uint8_t *W, const void *X, int x_f16, float *Y, int64_t N, int64_t K,
                          const MoeRoute &rt, int items, hipStream_t s, bool packed) {
   if (!gemv_t1_supported(kind, packed)) return hipErrorNotSupported;
@@ -290,5 +297,6 @@ hipError_t launch_moe_t1(int kind, const uint8_t *W, const void *X, int x_f16, f
   }
   return hipErrorNotSupported;
 }
+#endif
 
 }  // namespace qmm

@@ -30,6 +30,7 @@
 #include <atomic>
 #include <type_traits>
 
+#include "qmm_epilogue.h"
 #include "qmm_gemv_mfma.h"
 #include "qmm_internal.h"
 
@@ -51,7 +52,7 @@ constexpr int kWaitLds = 0xC07F;
 // ones).
 template <int KIND, typename XT, int MT, int T, int S, int PD, int XD, bool ROUTED = false, bool PACKED = true>
 __global__ __launch_bounds__(64 * T * S) void gemv_xs_kernel(const uint8_t *__restrict__ P,
-                                                             const XT *__restrict__ X, float *__restrict__ Y,
+                                                             const XT *__restrict__ X, QMM_OUT Y,
                                                              int M, int64_t N, int K, int per_wg, int extra,
                                                              MoeRoute rt, int64_t row_bytes) {
   using Dd = Dec<KIND>;
@@ -233,12 +234,13 @@ __global__ __launch_bounds__(64 * T * S) void gemv_xs_kernel(const uint8_t *__re
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     const int tok = 4 * G + q;
-    if (tok < M) Y[(int64_t)(ROUTED ? order[c0 + tok] : tok) * N + row] = acc[q];
+    if (tok < M) put(Y, ROUTED ? order[c0 + tok] : tok, row, N, acc[q]);
   }
 }
 
 }  // namespace gv
 
+#ifndef QMM_WITH_EPILOGUE
 // Compute units of the current device (looked up once per device).
 int device_cus() {
   static std::atomic<int> cache[64];
@@ -250,11 +252,12 @@ int device_cus() {
   cache[dev].store(n, std::memory_order_relaxed);
   return n;
 }
+#endif
 
 namespace gv {
 
 template <int KIND, int MT, int T, int S, int PD, int XD = 2, bool PACKED = true>
-static hipError_t run_xs(const uint8_t *P, const void *x, int x_f16, float *y, int M, int64_t N, int64_t K,
+static hipError_t run_xs(const uint8_t *P, const void *x, int x_f16, Out y, int M, int64_t N, int64_t K,
                          hipStream_t s, bool spread = true) {
   const int64_t row_bytes = (K / Geometry<KIND>::elems) * Geometry<KIND>::bytes;
   constexpr int kFrag = Dec<KIND>::NSTEP * MT * 4;
@@ -272,6 +275,7 @@ static hipError_t run_xs(const uint8_t *P, const void *x, int x_f16, float *y, i
   return hipGetLastError();
 }
 
+#ifndef QMM_WITH_EPILOGUE
 // Grouped expert products: grid (tile groups of T, work items); T tiles
 // share each staged activation k-block of the item's MT pairs.
 template <int KIND, int MT, int T, int S, int PD, int XD, bool PACKED = true>
@@ -314,9 +318,10 @@ static hipError_t run_xs_routed_m(const uint8_t *P, const void *x, int x_f16, fl
   if (mt == 8) return run_xs_routed<KIND, 8, 8, 1, 1, 1, PACKED>(P, x, x_f16, y, N, K, s, rt, items);
   return run_xs_routed<KIND, 16, 8, 1, 1, 1, PACKED>(P, x, x_f16, y, N, K, s, rt, items);
 }
+#endif
 
 template <int KIND>
-static hipError_t run_xs_m(const uint8_t *P, const void *x, int x_f16, float *y, int M, int64_t N, int64_t K,
+static hipError_t run_xs_m(const uint8_t *P, const void *x, int x_f16, Out y, int M, int64_t N, int64_t K,
                            hipStream_t s, int cfg) {
 #ifdef QMM_TUNING
   switch (cfg) {
@@ -352,6 +357,7 @@ static hipError_t run_xs_m(const uint8_t *P, const void *x, int x_f16, float *y,
 
 }  // namespace gv
 
+#ifndef QMM_WITH_EPILOGUE
 bool xs_native_supported(int kind) {
   return kind == Q4_K || kind == Q6_K || kind == Q5_K || kind == Q2_K || kind == Q3_K;
 }
@@ -377,9 +383,10 @@ hipError_t launch_moe_xs(int kind, const uint8_t *P, const void *X, int x_f16, f
   }
   return hipErrorNotSupported;
 }
+#endif
 
 // 2 to 8 tokens over native rows (the super-block kinds).
-hipError_t launch_gemv_xs_native(int kind, const uint8_t *W, const void *x, int x_f16, float *y, int M, int64_t N,
+hipError_t launch_gemv_xs_native(int kind, const uint8_t *W, const void *x, int x_f16, Out y, int M, int64_t N,
                                  int64_t K, hipStream_t s) {
   switch (kind) {
 #define QMM_CASE(K_)                                                                         \
@@ -394,7 +401,7 @@ hipError_t launch_gemv_xs_native(int kind, const uint8_t *W, const void *x, int 
   return hipErrorNotSupported;
 }
 
-hipError_t launch_gemv_xs(int kind, const uint8_t *P, const void *x, int x_f16, float *y, int M, int64_t N,
+hipError_t launch_gemv_xs(int kind, const uint8_t *P, const void *x, int x_f16, Out y, int M, int64_t N,
                           int64_t K, hipStream_t s, int cfg) {
   switch (kind) {
     case Q4_K: return gv::run_xs_m<Q4_K>(P, x, x_f16, y, M, N, K, s, cfg);

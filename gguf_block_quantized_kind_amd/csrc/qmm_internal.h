@@ -9,6 +9,18 @@
 
 namespace qmm {
 
+// What a product's epilogue does (qmm_epilogue.h; strides in elements).  The
+// launchers that take one in place of the f32 result are the same kernels
+// compiled with it.
+struct Epilogue {
+  const float *bias;
+  const void *mul, *residual;
+  void *out;
+  int64_t mul_stride, residual_stride, out_stride;
+  int act;
+  int mul_f16, residual_f16, out_f16;
+};
+
 // out[i] for i < n_blocks * block_elems.
 hipError_t launch_dequant(int kind, const uint8_t *W, float *out, int64_t n_blocks, hipStream_t s);
 
@@ -71,6 +83,68 @@ hipError_t launch_gemm_lds(int kind, const uint8_t *W, const void *A, int a_f16,
                            int64_t K, hipStream_t s);
 hipError_t launch_gemm(int kind, const uint8_t *W, const void *A, int a_f16, float *C,
                        int64_t M, int64_t N, int64_t K, hipStream_t s);
+
+// The products above with an epilogue.
+hipError_t launch_gemv(int kind, const uint8_t *W, const void *x, int x_f16, Epilogue y, int M, int64_t N, int64_t K,
+                       hipStream_t s);
+hipError_t launch_gemv_mfma(int kind, const uint8_t *W, const void *x, int x_f16, Epilogue y, int M, int64_t N,
+                            int64_t K, hipStream_t s);
+hipError_t launch_gemv_packed(int kind, const uint8_t *P, const void *x, int x_f16, Epilogue y, int M, int64_t N,
+                              int64_t K, hipStream_t s);
+hipError_t launch_gemv_xs(int kind, const uint8_t *P, const void *x, int x_f16, Epilogue y, int M, int64_t N,
+                          int64_t K, hipStream_t s, int cfg = 0);
+hipError_t launch_gemv_xs_native(int kind, const uint8_t *W, const void *x, int x_f16, Epilogue y, int M, int64_t N,
+                                 int64_t K, hipStream_t s);
+hipError_t launch_gemv_t1(int kind, const uint8_t *W, const void *x, int x_f16, Epilogue y, int64_t N, int64_t K,
+                          hipStream_t s, int cfg = 0, bool packed = true);
+hipError_t launch_gemm(int kind, const uint8_t *W, const void *A, int a_f16, Epilogue C, int64_t M, int64_t N,
+                       int64_t K, hipStream_t s);
+hipError_t launch_gemm_ks(int kind, const uint8_t *W, const void *A, int a_f16, Epilogue C, int64_t M, int64_t N,
+                          int64_t K, hipStream_t s);
+hipError_t launch_gemm_lds(int kind, const uint8_t *W, const void *A, int a_f16, Epilogue C, int64_t M, int64_t N,
+                           int64_t K, hipStream_t s);
+hipError_t launch_gemm_packed(int kind, const uint8_t *P, const void *A, int a_f16, Epilogue C, int64_t M, int64_t N,
+                              int64_t K, hipStream_t s);
+// The int8-activation GEMV over activations already quantized (by
+// launch_rmsnorm or launch_gemv_i8's first half).
+hipError_t launch_gemv_q8(int kind, const uint8_t *P, const int8_t *q, const float *d, const int32_t *s, float *y,
+                          int M, int64_t N, int64_t K, hipStream_t st);
+hipError_t launch_gemv_q8(int kind, const uint8_t *P, const int8_t *q, const float *d, const int32_t *s, Epilogue y,
+                          int M, int64_t N, int64_t K, hipStream_t st);
+
+// Root-mean-square norm of [T][H][D] rows with the residual's addition
+// (residual and sum may be NULL), to y, or in 8 bits to codes, scales and code
+// sums (q8: 1 the order of Q8_0 weights, 2 of the other kinds; 0: y).
+struct Norm {
+  const void *x, *residual;
+  void *sum, *y;
+  const float *weight;
+  int64_t x_stride, residual_stride, sum_stride, y_stride, T, H, D;
+  int x_f16, residual_f16, y_f16, q8;
+  float eps;
+  int8_t *codes;
+  float *scales;
+  int32_t *code_sums;
+};
+constexpr int64_t kNormMaxD = 32768;
+hipError_t launch_rmsnorm(const Norm &n, hipStream_t s);
+
+// Choice of experts; see qmm_moe_route in qmm.h.
+struct Route {
+  const void *logits;
+  int f16;
+  int64_t stride;
+  const float *bias;
+  int64_t M, E, topk;
+  int sigmoid;
+  int64_t n_group, topk_group;
+  int group_top, normalize;
+  float scale;
+  const int32_t *slots;
+  int32_t *ids;
+  float *weights;
+};
+hipError_t launch_moe_route(const Route &r, hipStream_t s);
 
 // Routed SiLU-gated expert FFN with a weighted top-k combine; see
 // qmm_moe_ffn in qmm.h.

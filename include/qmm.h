@@ -355,6 +355,113 @@ size_t qmm_gemv_i8_workspace_bytes(int64_t M, int64_t K);
 int qmm_gemv_i8_noalloc(int kind, const void *P, const void *x, int x_dtype, float *y,
                         int64_t M, int64_t N, int64_t K, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Products with an epilogue: what a layer does with a projection's sums before
+ * anything else reads them.  Model semantics beyond the pages, like
+ * qmm_moe_ffn.
+ *   out[m][n] = act(sum_k A[m][k] w[n][k] + bias[n]) * mul[m][n] + residual[m][n]
+ * with act one of
+ *   QMM_ACT_NONE       v
+ *   QMM_ACT_RELU       max(v, 0)
+ *   QMM_ACT_SILU       v / (1 + e^-v)
+ *   QMM_ACT_GELU       v (1 + erf(v / sqrt 2)) / 2
+ *   QMM_ACT_GELU_TANH  v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) / 2
+ * A NULL bias, mul or residual leaves its step out; mul and residual are
+ * [M][N], f32 or f16, with row strides in elements (>= N), bias is [N] f32.  A
+ * gated FFN is act(x . W_gate^T) into g, then mul = g in the product with W_up.
+ * out is f32 or f16 with a row stride; it may be mul or residual itself (same
+ * type and stride), and overlaps nothing else.  The sum is the plain entry
+ * point's, the epilogue is in f32 (activations within 2^-20 relative of their
+ * value at the f32 sum), and the result is rounded once to out's type: an f16
+ * out beyond 65504 is an infinity.
+ * --------------------------------------------------------------------- */
+enum qmm_act { QMM_ACT_NONE = 0, QMM_ACT_RELU = 1, QMM_ACT_SILU = 2, QMM_ACT_GELU = 3, QMM_ACT_GELU_TANH = 4 };
+typedef struct qmm_epilogue {
+    const float *bias;
+    const void *mul;
+    const void *residual;
+    int64_t mul_stride;
+    int64_t residual_stride;
+    int act;
+    int mul_dtype;
+    int residual_dtype;
+} qmm_epilogue;
+
+/* qmm_matmul with an epilogue (ep NULL: none).  Errors as qmm_matmul, with the
+ * dtypes of out, mul and residual beside A's, and then a stride below N, an
+ * unknown act or a misaligned operand as QMM_ERR_BAD_ARG. */
+int qmm_matmul_ep(int kind, const void *W, const void *A, int a_dtype, const qmm_epilogue *ep, void *out,
+                  int out_dtype, int64_t out_stride, int64_t M, int64_t N, int64_t K, void *stream);
+/* qmm_matmul_packed with an epilogue; errors as both. */
+int qmm_matmul_packed_ep(int kind, const void *P, const void *A, int a_dtype, const qmm_epilogue *ep, void *out,
+                         int out_dtype, int64_t out_stride, int64_t M, int64_t N, int64_t K, void *stream);
+
+/* The product of qmm_gemv_i8 over activations that are quantized already (by
+ * qmm_rmsnorm_q8, for this kind of weights), with an epilogue: codes [M][K]
+ * int8, 16-byte aligned, scales and code_sums [M][K / 32].  Kinds, sizes (M <=
+ * QMM_GEMV_MAX_M, M * K <= QMM_GEMV_I8_MAX_MK), numerics and errors as
+ * qmm_gemv_i8 and qmm_matmul_ep.  More rows than M are taken by more calls: row
+ * t's codes start at t * K, its scales and sums at t * K / 32. */
+int qmm_gemv_q8(int kind, const void *P, const int8_t *codes, const float *scales, const int32_t *code_sums,
+                const qmm_epilogue *ep, void *out, int out_dtype, int64_t out_stride, int64_t M, int64_t N, int64_t K,
+                void *stream);
+
+/* Root-mean-square norm of [T][H][D] rows (H packed rows of D elements at t *
+ * stride: the heads of a projection, or H = 1), with the residual's addition:
+ *   h = x + residual, rounded to f32 (residual NULL: x)
+ *   y = h / sqrt(mean(h^2) + eps) * weight    (weight [D] f32, or NULL: 1)
+ * sum (if not NULL) receives h in the residual's type, y is f32 or f16.  Each of
+ * x and residual is f32 or f16.  The mean and y are computed in 64 bits and y is
+ * rounded to f32, then to f16: within 2^-24 relative (f16: 2^-11 + 2^-24, and
+ * 2^-25 absolute below its normal range).  A row of zeros with eps = 0 gives
+ * zeros.  An infinity in a row gives NaN at its place and zeros elsewhere, a NaN
+ * gives a row of NaN.  sum and y may each be x or residual itself (same type and
+ * stride) but not each other; other overlaps are not allowed.
+ * Errors: a zero dimension, dtypes, then QMM_ERR_BAD_ARG: D > 32768, T * H *
+ * D > 2^40 or T * H >= 2^31, eps negative or not finite, sum without residual,
+ * sum equal to y, pointers, alignment to the elements, strides below H * D. */
+int qmm_rmsnorm(const void *x, int x_dtype, int64_t x_stride, const void *residual, int residual_dtype,
+                int64_t residual_stride, const float *weight, float eps, void *sum, int64_t sum_stride, void *y,
+                int y_dtype, int64_t y_stride, int64_t T, int64_t H, int64_t D, void *stream);
+/* qmm_rmsnorm of [T][D] rows with y in 8 bits, as qmm_gemv_i8 quantizes the f32
+ * y (bit for bit; a block with an infinity or NaN gets a NaN for its scale): codes
+ * [T][D] in the lane order of the weights of `kind`, scales and code_sums [T][D /
+ * 32], all contiguous, codes 16-byte aligned.  They overlap no operand.  Errors as
+ * qmm_rmsnorm, with unsupported kinds (those of qmm_gemv_i8) and D not a multiple
+ * of 32 before the dtypes. */
+int qmm_rmsnorm_q8(int kind, const void *x, int x_dtype, int64_t x_stride, const void *residual, int residual_dtype,
+                   int64_t residual_stride, const float *weight, float eps, void *sum, int64_t sum_stride,
+                   int8_t *codes, float *scales, int32_t *code_sums, int64_t T, int64_t D, void *stream);
+
+/* The choice of experts for qmm_moe, qmm_moe_ffn: per token t, from its logits
+ * l_e (f32 or f16, row stride in elements),
+ *   s_e = e^(l_e) / sum_j e^(l_j)   (QMM_ROUTE_SOFTMAX), or
+ *   s_e = 1 / (1 + e^(-l_e))        (QMM_ROUTE_SIGMOID)
+ *   c_e = s_e + bias[e]             (bias [E] f32, or NULL: c_e = s_e)
+ * With n_group > 1 the experts lie in n_group groups of E / n_group; a group's
+ * value is the sum of its group_top (1 or 2) largest c, and only the topk_group
+ * groups of the largest values keep their experts.  The topk largest c that are
+ * left are chosen, in their order; equal ones (groups too) go by the lowest
+ * index.  ids [M][topk] int32 gets their numbers and weights [M][topk] f32 their
+ * s_e, divided by the chosen ones' sum if normalize is 1, times scale.
+ * An expert whose logit or c is NaN or minus infinity is never chosen and has no
+ * part in the softmax; a row that runs out of experts, and every row t with
+ * slots[t] < 0 (slots [M] int32, or NULL: none; the padding tokens of
+ * qmm_kv_append) gets ids of -1, which qmm_moe skips, and weights of 0.
+ * Numerics: the choice is that of 64-bit scores (without a bias, and with
+ * group_top = 1, that of the logits themselves), so neighbours that f32 cannot
+ * tell apart keep their order; weights are within 2^-20 relative, also where
+ * every chosen score vanishes.
+ * Errors: a zero dimension, dtype, then QMM_ERR_BAD_ARG: E > 4096, topk > 64 or
+ * above the topk_group * E / n_group experts that can be left, n_group > 64, E
+ * not a multiple of it, topk_group outside [1, n_group], group_top not 1 or 2, an
+ * unknown score, normalize not 0 or 1, scale not finite, M >= 2^31, pointers,
+ * alignment, a stride below E. */
+enum qmm_route_score { QMM_ROUTE_SOFTMAX = 0, QMM_ROUTE_SIGMOID = 1 };
+int qmm_moe_route(const void *logits, int dtype, int64_t stride, const float *bias, int64_t M, int64_t E,
+                  int64_t topk, int score, int64_t n_group, int64_t topk_group, int group_top, int normalize,
+                  float scale, const int32_t *slots, int32_t *ids, float *weights, void *stream);
+
 /* Dequantize n_elems consecutive elements (whole blocks) of W to f32 on
  * `stream`: the GPU dequantization that redgpu/Vulkore quant_test.cpp checks
  * bit for bit against its CPU references (its dequant_q8_0 / _q5_0 / _q4_k /

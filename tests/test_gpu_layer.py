@@ -1,0 +1,648 @@
+"""What stands around a layer's products on the GPU -- the norm with the residual's
+addition (also in 8 bits), the choice of experts, products with an epilogue --
+against the definitions of oracle/layer.py.
+
+Tolerances (none measured).  Norm: sums exactly; a row 2^-24 of its value from the
+rounding of the 64-bit result to f32 (2^-40 for the 64-bit steps), plus half a step
+of an f16 result; codes, scales and code sums exactly those of the f32 rows.
+Choice of experts: the experts exactly; weights 2^-20.  Products: the plain
+entry points' 1e-3 sum |w||x| + 1e-6 (8 bits: 2e-5) carried through the epilogue
+(oracle/layer.py, epilogue); with sums that are exact, 2^-20 for the activation and
+2^-24 a step.
+"""
+import numpy as np
+import pytest
+
+import workloads as wl
+from oracle import int8, layer
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+import gguf_block_quantized_kind_amd as qmm  # noqa: E402
+
+NP = {"f16": np.float16, "f32": np.float32}
+TT = {"f16": torch.float16, "f32": torch.float32}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    qmm.load_library()
+
+
+def dev(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def host(t):
+    return t.cpu().numpy()
+
+
+def check(got, want, tol, what):
+    got = got.astype(np.float64)
+    assert got.shape == want.shape, what
+    assert np.all(np.isfinite(got)), f"{what}: not finite"
+    err = np.abs(got - want)
+    tol = np.broadcast_to(tol, err.shape)
+    ratio = np.divide(err, tol, out=np.where(err == 0, 0.0, np.inf), where=tol > 0)
+    at = np.unravel_index(np.argmax(ratio), ratio.shape)
+    assert ratio[at] <= 1.0, f"{what}: |err| / tol = {ratio[at]:.3g} at {at}: got {got[at]}, want {want[at]}"
+
+
+def norm_tol(y, dt):
+    """2^-24 of the value, or half the smallest f32; then half a step of f16."""
+    t = 2.0 ** -24 * (1 + 2.0 ** -14) * np.abs(y) + 2.0 ** -150
+    return t * (1 + 2.0 ** -11) + 2.0 ** -11 * np.abs(y) + 2.0 ** -25 if dt == "f16" else t
+
+
+# -- the norm ------------------------------------------------------------------
+SIZES = [1, 7, 8, 31, 64, 65, 128, 255, 512, 1000, 1337, 2048, 2050, 4096, 5003, 8192, 9999, 16384, 16391, 32768]
+
+
+@pytest.mark.parametrize("D", SIZES)
+@pytest.mark.parametrize("xd,rd,yd", [("f32", "f32", "f16"), ("f16", None, "f16"), ("f32", None, "f32"), ("f16", "f32", "f32"),
+                                      ("f32", "f16", "f16"), ("f16", "f16", "f32")])
+def test_rmsnorm(D, xd, rd, yd):
+    """Rows of every size, at odd places (strides above D, a base that is aligned to the element only), what lies
+    between them left alone."""
+    g = wl.rng("norm", f"{D}{xd}{rd}{yd}")
+    T, pad = (5, 3) if D < 20000 else (2, 1)
+    x = (g.normal(size=(T, D + pad)) * np.exp(g.normal(size=(1, D + pad)))).astype(NP[xd])
+    w = g.normal(size=D).astype(np.float32)
+    view = dev(x)[:, 1:1 + D]
+    out = torch.full((T, D + pad), 7.0, dtype=TT[yd], device="cuda")
+    if rd is None:
+        got = qmm.rmsnorm(view, dev(w), 1e-5, out=out[:, 1:1 + D])
+        h, y = layer.rmsnorm(x[:, 1:1 + D], None, w, 1e-5)
+    else:
+        r = (3 * g.normal(size=(T, D + 2))).astype(NP[rd])
+        rbuf = dev(r)
+        got, s = qmm.rmsnorm(view, dev(w), 1e-5, residual=rbuf[:, 2:2 + D], out=out[:, 1:1 + D], sum_out=rbuf[:, 2:2 + D])
+        h, y = layer.rmsnorm(x[:, 1:1 + D], r[:, 2:2 + D], w, 1e-5)
+        assert np.array_equal(host(s), h.astype(NP[rd])) and np.array_equal(host(rbuf[:, :2]), r[:, :2])
+    check(host(got), y, norm_tol(y, yd), f"norm D={D}")
+    assert torch.all(out[:, :1] == 7) and torch.all(out[:, 1 + D:] == 7)
+
+
+@pytest.mark.parametrize("T,H,D", [(1, 1, 4096), (1, 40, 128), (333, 9, 96), (70, 3, 64), (5, 2, 24), (3, 5, 1100)])
+def test_rmsnorm_heads(T, H, D):
+    """The heads of a slice of a projection's output, each normed by itself, in place and out of place."""
+    g = wl.rng("norm", f"heads{T}{H}{D}")
+    x = g.normal(size=(T, H + 3, D)).astype(np.float16)
+    w = g.normal(size=D).astype(np.float32)
+    buf = dev(x)
+    y = qmm.rmsnorm(buf[:, 1:1 + H], dev(w), 1e-6)
+    want = layer.rmsnorm(x[:, 1:1 + H], None, w, 1e-6)[1]
+    check(host(y), want, norm_tol(want, "f16"), "heads")
+    qmm.rmsnorm(buf[:, 1:1 + H], dev(w), 1e-6, out=buf[:, 1:1 + H])
+    assert torch.equal(buf[:, 1:1 + H], y) and np.array_equal(host(buf[:, :1]), x[:, :1])
+    assert np.array_equal(host(buf[:, 1 + H:]), x[:, 1 + H:])
+
+
+def test_rmsnorm_in_place_of_either_operand():
+    g = wl.rng("norm", "places")
+    x, r = (g.normal(size=(6, 3001)).astype(np.float32) for _ in range(2))
+    h, y = layer.rmsnorm(x, r, None, 1e-6)
+    for sum_in_x in (True, False):
+        dx, dr = dev(x), dev(r)
+        got, s = qmm.rmsnorm(dx, None, 1e-6, residual=dr, sum_out=dx if sum_in_x else dr, out=dr if sum_in_x else dx)
+        assert s is (dx if sum_in_x else dr) and got is (dr if sum_in_x else dx)
+        assert np.array_equal(host(s), h)
+        check(host(got), y, norm_tol(y, "f32"), "in place")
+
+
+@pytest.mark.parametrize("scale", [1e38, 1e30, 1e-30, 1e-42])
+def test_rmsnorm_sizes_whose_squares_leave_f32(scale):
+    g = wl.rng("norm", f"far{scale}")
+    x = (np.clip(g.normal(size=(4, 777)), -3, 3) * scale).astype(np.float32)
+    y = layer.rmsnorm(x, eps=0.0)[1]
+    check(host(qmm.rmsnorm(dev(x), None, 0.0)), y, norm_tol(y, "f32"), "far")
+
+
+def test_rmsnorm_zeros_infinities_and_nan():
+    x = np.ones((5, 300), np.float32)
+    x[0] = 0
+    x[1, 7] = np.inf
+    x[2, 9] = np.nan
+    x[3, 299], x[3, 0] = -np.inf, np.inf
+    y = host(qmm.rmsnorm(dev(x), None, 0.0))
+    assert not y[0].any()
+    assert np.isnan(y[1, 7]) and not np.delete(y[1], 7).any()
+    assert np.isnan(y[2]).all()
+    assert np.isnan(y[3, [0, 299]]).all() and not y[3, 1:299].any()
+    assert np.all(y[4] == 1)
+
+
+@pytest.mark.parametrize("kind", ["Q8_0", "Q4_0", "Q5_0", "IQ4_NL", "MXFP4"])
+@pytest.mark.parametrize("T,D", [(1, 32), (3, 256), (8, 4096), (70, 1312), (2, 11008), (2, 32768), (300, 96)])
+@pytest.mark.parametrize("rd", [None, "f16"])
+def test_rmsnorm_q8(kind, T, D, rd):
+    """The bits of the quantizer on the f32 rows (here computed by the f32 form), and the same sums."""
+    g = wl.rng("norm", f"q8{kind}{T}{D}")
+    x = (g.normal(size=(T, D + 1)) * np.exp(0.5 * g.normal(size=(1, D + 1)))).astype(np.float32)
+    x[0, 1:1 + 32] = 0                                      # a block of zeros (without a residual)
+    r = None if rd is None else dev(g.normal(size=(T, D)).astype(NP[rd]))
+    w = dev(g.normal(size=D).astype(np.float32))
+    view = dev(x)[:, 1:]
+    got = qmm.rmsnorm_q8(kind, view, w, 1e-5, residual=r)
+    y = qmm.rmsnorm(view, w, 1e-5, residual=r, out_dtype=torch.float32)
+    if rd is not None:
+        assert torch.equal(got[1], y[1]) and got[1].dtype == TT[rd]
+        got, y = got[0], y[0]
+    codes, d, sums = layer.eight_bits(kind, host(y))
+    assert np.array_equal(host(got[0]), codes) and np.array_equal(host(got[1]), d) and np.array_equal(host(got[2]), sums)
+
+
+def test_rmsnorm_q8_nonfinite_blocks():
+    """An infinity leaves zeros elsewhere in its row; its own block has a NaN for a scale, as every block of a row with a
+    NaN; the other rows are theirs."""
+    x = np.ones((3, 256), np.float32)
+    x[0, 40], x[1, 70] = np.inf, np.nan
+    codes, d, sums = (host(t) for t in qmm.rmsnorm_q8("Q8_0", dev(x), None, 0.0))
+    assert np.isnan(d[0, 1]) and not np.delete(d[0], 1).any() and np.isnan(d[1]).all()
+    assert not codes[:2].any() and not sums[:2].any()
+    assert np.all(codes[2] == 127)
+
+
+# -- the choice of experts -----------------------------------------------------
+def check_route(logits, k, what="", **kw):
+    bias = kw.pop("bias", None)
+    slots = kw.pop("slots", None)
+    want = layer.route(logits if isinstance(logits, np.ndarray) else host(logits), k, bias=bias, slots=slots, **kw)
+    t = dev(logits) if isinstance(logits, np.ndarray) else logits
+    ids, w = qmm.moe_route(t, k, bias=None if bias is None else dev(bias), slots=None if slots is None else dev(slots), **kw)
+    assert np.array_equal(host(ids), want[0]), what
+    check(host(w), want[1], 2.0 ** -20 * np.abs(want[1]) + 2.0 ** -149, what)
+    return ids, w
+
+
+@pytest.mark.parametrize("E,k", [(1, 1), (2, 1), (7, 7), (8, 2), (60, 4), (64, 8), (65, 6), (128, 8), (160, 6), (256, 8),
+                                 (257, 1), (384, 8), (512, 10), (1000, 33), (2048, 64), (4096, 16)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dt", ["f32", "f16"])
+@pytest.mark.parametrize("biased", [False, True])
+def test_route_sizes(E, k, score, dt, biased):
+    g = wl.rng("route", f"{E}{k}{score}{dt}{biased}")
+    M = 37 if E <= 512 else 5
+    l = (3 * g.normal(size=(M, E))).astype(NP[dt])
+    b = (0.3 * g.normal(size=E)).astype(np.float32) if biased else None
+    check_route(l, k, score=score, bias=b, normalize=True, scale=2.5)
+    check_route(l, k, score=score, bias=b, normalize=False)
+
+
+@pytest.mark.parametrize("E,groups,keep", [(256, 8, 4), (64, 4, 1), (60, 6, 6), (128, 64, 3), (160, 8, 3), (24, 3, 2), (64, 64, 9),
+                                           (4096, 2, 1), (512, 16, 5), (96, 8, 2)])
+@pytest.mark.parametrize("top", [1, 2])
+@pytest.mark.parametrize("score,biased", [("softmax", False), ("sigmoid", True), ("softmax", True)])
+def test_route_groups(E, groups, keep, top, score, biased):
+    g = wl.rng("route", f"groups{E}{groups}{top}{score}")
+    l = (2 * g.normal(size=(33 if E < 1000 else 4, E))).astype(np.float32)
+    b = (0.2 * g.normal(size=E)).astype(np.float32) if biased else None
+    k = min(8, E // groups * keep)
+    check_route(l, k, score=score, bias=b, n_group=groups, topk_group=keep, group_top=top)
+
+
+@pytest.mark.parametrize("E", [33, 64, 200, 256, 1024])
+def test_route_ties_go_to_the_lowest(E):
+    """Logits of few values, all alike, and groups of equal values."""
+    g = wl.rng("route", f"ties{E}")
+    for l in (g.integers(-2, 3, (50, E)).astype(np.float32), np.zeros((3, E), np.float16), -np.zeros((2, E), np.float32)):
+        for score in ("softmax", "sigmoid"):
+            check_route(l, 8, score=score)
+            check_route(l, 8, score=score, bias=np.zeros(E, np.float32))
+    l = np.zeros((4, E), np.float32)
+    l[1::2] = -0.0                                          # equal to 0: the order is that of the places
+    l[:, E // 2] = -0.0
+    check_route(l, 4)
+    if E % 8 == 0:
+        check_route(np.tile(g.normal(size=(20, E // 8)).astype(np.float32), (1, 8)), 6, n_group=8, topk_group=3, group_top=2)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups", [(256, 1), (256, 8), (48, 4), (512, 1)])
+def test_route_neighbours_that_f32_cannot_tell_apart(score, E, groups):
+    """Biases that bring every c to within a few 2^-30 of one value: the order is that of the 64-bit sums."""
+    g = wl.rng("route", f"near{score}{E}{groups}")
+    l = np.tile(g.normal(size=(1, E)).astype(np.float32), (40, 1))
+    s = np.exp(l[0].astype(np.float64))
+    s = s / s.sum() if score == "softmax" else 1 / (1 + np.exp(-l[0].astype(np.float64)))
+    b = (1.0 - s).astype(np.float32)
+    l[1:] += (2.0 ** -21 * g.integers(-3, 4, (39, E))).astype(np.float32)
+    check_route(l, 8, score=score, bias=b)
+    if groups > 1:
+        for top in (1, 2):
+            check_route(l, 8, score=score, bias=b, n_group=groups, topk_group=2, group_top=top)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups", [(8, 1), (64, 1), (100, 4), (256, 8)])
+@pytest.mark.parametrize("biased", [False, True])
+def test_route_masks_infinities_and_nan(score, E, groups, biased):
+    g = wl.rng("route", f"masks{score}{E}{groups}")
+    low = np.finfo(np.float32).min
+    l = g.normal(size=(14, E)).astype(np.float32)
+    l[0] = -np.inf                                          # nothing left
+    l[1] = np.nan
+    l[2] = low                                              # a mask of the type's lowest value everywhere
+    l[3, 1:] = low
+    l[4, 3:] = -np.inf                                      # fewer than are asked for
+    l[5, ::2] = np.nan
+    l[6, 1::2] = -np.inf
+    l[7, [1, E - 1]] = np.inf
+    l[8] = np.inf
+    l[9] = np.finfo(np.float32).max
+    l[10] *= 1e30
+    l[11] = -1000 - np.arange(E)                            # scores that vanish
+    l[12] = np.where(np.arange(E) % 3 == 0, low, -np.inf)
+    b = (0.25 * g.integers(-4, 5, E)).astype(np.float32) if biased else None
+    for norm in (True, False):
+        check_route(l, 6, score=score, bias=b, normalize=norm)
+        if groups > 1:
+            for top in (1, 2):
+                check_route(l, 6, score=score, bias=b, n_group=groups, topk_group=2, group_top=top, normalize=norm)
+    if biased:
+        b[::2], b[1], b[3] = -np.inf, np.nan, np.inf
+        check_route(l, 6, score=score, bias=b)
+
+
+@pytest.mark.parametrize("M", [1, 2, 63, 1000, 5000])
+def test_route_padding_strides_and_places(M):
+    g = wl.rng("route", f"pad{M}")
+    buf = g.normal(size=(M, 100)).astype(np.float32)
+    slots = np.where(np.arange(M) % 5 == 4, -1 - np.arange(M), np.arange(M)).astype(np.int32)
+    slots[M - 1] = -1
+    t = dev(buf)[:, 3:63]
+    ids, w = check_route(t, 4, slots=slots)
+    assert (ids[M - 1] == -1).all() and not w[M - 1].any()
+    oi = torch.full((M + 2, 4), 77, dtype=torch.int32, device="cuda")
+    ow = torch.full((M + 2, 4), 77.0, device="cuda")
+    qmm.moe_route(t, 4, slots=dev(slots), ids=oi[1:M + 1], weights=ow[1:M + 1])
+    assert torch.equal(oi[1:M + 1], ids) and torch.equal(ow[1:M + 1], w)
+    assert (oi[[0, M + 1]] == 77).all() and (ow[[0, M + 1]] == 77).all()
+
+
+# -- products with an epilogue ---------------------------------------------------
+KINDS = list(wl.KINDS)
+PACKED_GEMM = ["Q8_0", "Q4_0", "Q5_0", "IQ4_NL", "MXFP4", "IQ4_XS"]
+
+
+def operands(g, M, N, mul, res):
+    """Rows with strides of their own."""
+    out = []
+    for dt in (mul, res):
+        out.append(None if dt is None else (2 * g.normal(size=(M, N + 5))).astype(NP[dt]))
+    return out
+
+
+def run_product(oracle_mod, kind, M, N, K, a="f16", bias=True, act="none", mul=None, res=None, out="f32", packed=False, what=""):
+    g = wl.rng("product", f"{kind}{M}{N}{K}{a}{act}{mul}{res}{out}")
+    W = wl.random_weights(kind, N, K, g)
+    A = wl.activations((M, K), NP[a], g)
+    b = g.normal(size=N).astype(np.float32) if bias else None
+    m, r = operands(g, M, N, mul, res)
+    Y, B = oracle_mod.matmul(kind, W, K, A)
+    size = np.sqrt(np.mean(Y * Y))                          # the products' size goes into A: activations around their bends
+    A = (A / NP[a](size)).astype(NP[a])
+    Y, B = oracle_mod.matmul(kind, W, K, A)
+    want, tol = layer.epilogue(Y, 1e-3 * B + 1e-6, b, act, None if m is None else m[:, 2:2 + N], None if r is None else r[:, 1:1 + N],
+                               out == "f16")
+    buf = torch.full((M, N + 3), 9.0, dtype=TT[out], device="cuda")
+    Wd = dev(W) if not packed else qmm.repack(kind, dev(W), N, K)
+    fn = qmm.matmul_packed_ep if packed else qmm.matmul_ep
+    got = fn(kind, Wd, dev(A), N, bias=None if b is None else dev(b), act=act, mul=None if m is None else dev(m)[:, 2:2 + N],
+             residual=None if r is None else dev(r)[:, 1:1 + N], out=buf[:, 1:1 + N])
+    check(host(got), want, tol, what or f"{kind} M={M} N={N} K={K}")
+    assert (buf[:, 0] == 9).all() and (buf[:, 1 + N:] == 9).all()
+    return got
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("M,N,K", [(1, 100, 512), (3, 77, 1024), (8, 333, 768), (9, 64, 512), (33, 200, 512), (130, 129, 1024)])
+@pytest.mark.parametrize("a", ["f16", "f32"])
+def test_product_kinds(oracle_mod, kind, M, N, K, a):
+    run_product(oracle_mod, kind, M, N, K, a, act="silu", mul="f16", res="f32", out="f32")
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("M,N,K", [(1, 100, 512), (2, 4200, 256), (5, 77, 1024), (8, 333, 768), (9, 64, 512), (70, 200, 1024),
+                                   (131, 129, 1280)])
+def test_product_packed_kinds(oracle_mod, kind, M, N, K):
+    if M > 8 and kind not in PACKED_GEMM:
+        with pytest.raises(qmm.QmmError):
+            run_product(oracle_mod, kind, M, N, K, packed=True)
+        return
+    run_product(oracle_mod, kind, M, N, K, "f16" if M % 2 else "f32", act="gelu", res="f16", out="f16", packed=True)
+
+
+@pytest.mark.parametrize("kind", ["Q8_0", "Q4_0", "Q5_0", "IQ4_NL", "MXFP4"])
+@pytest.mark.parametrize("M,K", [(1, 32), (5, 1312), (20, 96), (70, 1312)])
+def test_product_odd_k(oracle_mod, kind, M, K):
+    """K that is not whole 256-element k-blocks."""
+    run_product(oracle_mod, kind, M, 61, K, act="relu", mul="f32", out="f16")
+
+
+@pytest.mark.parametrize("act", layer.ACTS)
+@pytest.mark.parametrize("mul,res,out", [(None, None, "f32"), ("f16", "f32", "f16"), ("f32", "f16", "f32")])
+@pytest.mark.parametrize("M", [1, 8, 40])
+def test_product_epilogues(oracle_mod, act, mul, res, out, M):
+    run_product(oracle_mod, "Q4_K", M, 90, 512, act=act, mul=mul, res=res, out=out, bias=mul is None)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 4096, 4096), (1, 14400, 512), (8, 4096, 14336), (6, 130, 14336), (7, 16, 8192), (300, 1000, 2048),
+                                   (515, 4100, 512)])
+@pytest.mark.parametrize("kind", ["Q4_K", "Q6_K", "Q8_0"])
+def test_product_larger(oracle_mod, kind, M, N, K):
+    run_product(oracle_mod, kind, M, N, K, res="f32")
+
+
+def exact_product(M, N, K, seed):
+    """Q8_0 weights of scale 2^-6 with small codes and small whole activations: every sum is exact in f32, and every
+    weight in f16."""
+    g = wl.rng("product", f"exact{seed}")
+    W = np.zeros((N, K // 32, 34), np.uint8)
+    W[..., :2] = np.frombuffer(np.float16(2.0 ** -6).tobytes(), np.uint8)
+    q = g.integers(-3, 4, (N, K // 32, 32)).astype(np.int8)
+    W[..., 2:] = q.view(np.uint8)
+    A = g.integers(-2, 3, (M, K)).astype(np.float16)
+    return W.reshape(-1), A, A.astype(np.float64) @ q.reshape(N, K).T.astype(np.float64) * 2.0 ** -6
+
+
+@pytest.mark.parametrize("act", layer.ACTS)
+@pytest.mark.parametrize("M,packed", [(1, False), (1, True), (5, False), (5, True), (70, False), (70, True)])
+def test_product_epilogue_on_exact_sums(act, M, packed):
+    """The epilogue alone: nothing of the product's own error hides it.  Sums from far below to far above 0."""
+    N, K = 130, 512
+    W, A, Y = exact_product(M, N, K, f"{act}{M}")
+    g = wl.rng("product", f"exactops{act}{M}")
+    b = (np.linspace(-12, 12, N)).astype(np.float32)
+    b[0], b[1], b[2] = -200.0, 200.0, -88.0
+    m, r = g.normal(size=(M, N)).astype(np.float16), g.normal(size=(M, N)).astype(np.float32)
+    Wd = qmm.repack("Q8_0", dev(W), N, K) if packed else dev(W)
+    fn = qmm.matmul_packed_ep if packed else qmm.matmul_ep
+    for mul, res, out in ((None, None, "f32"), (None, None, "f16"), (m, r, "f32"), (None, r, "f16"), (m, None, "f16")):
+        want, tol = layer.epilogue(Y, 0.0, b, act, mul, res, out == "f16")
+        got = fn("Q8_0", Wd, dev(A), N, bias=dev(b), act=act, mul=None if mul is None else dev(mul),
+                 residual=None if res is None else dev(res), out_dtype=TT[out])
+        check(host(got), want, tol, f"{act} {out}")
+
+
+@pytest.mark.parametrize("M", [1, 4, 8, 50])
+@pytest.mark.parametrize("dt", ["f16", "f32"])
+def test_product_into_its_operands(oracle_mod, M, dt):
+    """out in the place of the residual (the residual stream itself) and of mul, with its stride."""
+    N, K = 200, 512
+    W, A, Y = exact_product(M, N, K, f"place{M}{dt}")
+    g = wl.rng("product", f"place{M}{dt}")
+    buf = g.normal(size=(M, N + 7)).astype(NP[dt])
+    for what in ("residual", "mul"):
+        t = dev(buf)
+        view = t[:, 3:3 + N]
+        got = qmm.matmul_ep("Q8_0", dev(W), dev(A), N, out=view, **{what: view})
+        assert got is view
+        want, tol = layer.epilogue(Y, 0.0, **{what: buf[:, 3:3 + N]}, f16=dt == "f16")
+        check(host(got), want, tol, what)
+        assert np.array_equal(host(t[:, :3]), buf[:, :3]) and np.array_equal(host(t[:, 3 + N:]), buf[:, 3 + N:])
+
+
+def test_product_f16_overflow_and_activations_of_far_sums():
+    """A result beyond f16 is an infinity; far sums meet the activations' limits."""
+    W, A, Y = exact_product(2, 64, 256, "far")
+    b = np.concatenate([np.full(16, 1e6), np.full(16, -1e6), np.full(16, 1e30), np.full(16, -1e30)]).astype(np.float32)
+    for act in layer.ACTS:
+        y = host(qmm.matmul_ep("Q8_0", dev(W), dev(A), 64, bias=dev(b), act=act, out_dtype=torch.float16))
+        assert np.all(np.isposinf(y[:, :16])) and np.all(np.isposinf(y[:, 32:48]))
+        low = y[:, 16:32], y[:, 48:]
+        assert all(np.all(np.isneginf(v)) if act == "none" else np.all(v == 0) for v in low), act
+
+
+@pytest.mark.parametrize("kind", ["Q8_0", "Q4_0", "Q5_0", "IQ4_NL", "MXFP4"])
+@pytest.mark.parametrize("M,N,K", [(1, 100, 256), (3, 4100, 512), (8, 130, 4096), (1, 16, 262144), (5, 5000, 1024)])
+def test_gemv_q8(oracle_mod, kind, M, N, K):
+    """The product with 8-bit activations, through an epilogue, against the exact product with the values they stand
+    for; and without one the numbers of gemv_i8 on the f32 rows."""
+    g = wl.rng("q8", f"{kind}{M}{N}{K}")
+    W = wl.random_weights(kind, N, K, g)
+    P = qmm.repack(kind, dev(W), N, K)
+    x = wl.activations((M, min(K, 32768)), np.float32, g)
+    if K > 32768:                                           # beyond a norm's rows: quantized rows put together
+        parts = [qmm.rmsnorm_q8(kind, dev(np.roll(x, i, 1)), None) for i in range(K // 32768)]
+        rows = [qmm.rmsnorm(dev(np.roll(x, i, 1)), None) for i in range(K // 32768)]
+        acts = tuple(torch.cat(t, 1) for t in zip(*parts))
+        y = torch.cat(rows, 1)
+    else:
+        acts, y = qmm.rmsnorm_q8(kind, dev(x), None), qmm.rmsnorm(dev(x), None)
+    Y, B = oracle_mod.matmul(kind, W, K, int8.rebuilt(host(y)))
+    tol = (2e-5 + max(K - 32768, 0) * 2.0 ** -31) * B + 1e-6
+    check(host(qmm.gemv_q8(kind, P, acts, N)), Y, tol, "plain")
+    scale = float(np.sqrt(np.mean(Y * Y)))
+    b, r = (scale * g.normal(size=N)).astype(np.float32), (scale * g.normal(size=(M, N))).astype(np.float32)
+    want, t2 = layer.epilogue(Y, tol, b, "gelu_tanh", None, r, False)
+    got = qmm.gemv_q8(kind, P, acts, N, bias=dev(b), act="gelu_tanh", residual=dev(r))
+    check(host(got), want, t2, "epilogue")
+
+
+def test_gemv_q8_rows_of_a_larger_norm(oracle_mod):
+    """A norm of more rows than one product takes: its rows go in by slices."""
+    g = wl.rng("q8", "slices")
+    N, K, T = 50, 512, 21
+    W = wl.random_weights("Q8_0", N, K, g)
+    P = qmm.repack("Q8_0", dev(W), N, K)
+    x = wl.activations((T, K), np.float32, g)
+    acts = qmm.rmsnorm_q8("Q8_0", dev(x), None)
+    out = torch.empty((T, N), device="cuda")
+    for t in range(0, T, 8):
+        qmm.gemv_q8("Q8_0", P, tuple(a[t:t + 8] for a in acts), N, out=out[t:t + 8])
+    Y, B = oracle_mod.matmul("Q8_0", W, K, int8.rebuilt(host(qmm.rmsnorm(dev(x), None))))
+    check(host(out), Y, 2e-5 * B + 1e-6, "slices")
+
+
+# -- together --------------------------------------------------------------------
+class Layer:
+    """What a step does after the attention, in the order of a layer: the output projection into the residual stream,
+    the norm, the choice of experts, the experts, the next norm in 8 bits, and a gated dense FFN."""
+
+    def __init__(self, seed, D=512, F=768, E=16, N_ff=256):
+        g = wl.rng("layer", seed)
+        self.D, self.F, self.E, self.N_ff = D, F, E, N_ff
+        self.np = {n: wl.random_weights(k, rows, cols, g) for n, k, rows, cols in
+                   (("o", "Q4_K", D, D), ("router", "Q8_0", E, D), ("gate", "Q8_0", F, D), ("up", "Q8_0", F, D),
+                    ("down", "Q6_K", D, F), ("gu", "Q4_K", E * 2 * N_ff, D), ("d", "Q4_K", E * D, N_ff))}
+        self.W = {n: dev(w) for n, w in self.np.items()}
+        for n in ("gate", "up"):
+            self.W[n] = qmm.repack("Q8_0", self.W[n], F, D)
+        self.w = [dev((1 + 0.1 * g.normal(size=D)).astype(np.float32)) for _ in range(2)]
+        self.bias = dev((0.05 * g.normal(size=E)).astype(np.float32))
+
+    def step(self, x, stream_h, slots):
+        """x [M, D] f16 (the attention's result), stream_h [M, D] f32, rewritten."""
+        h = qmm.matmul_ep("Q4_K", self.W["o"], x, self.D, residual=stream_h, out=stream_h)
+        y = qmm.rmsnorm(h, self.w[0], 1e-5, out_dtype=torch.float16)
+        logits = qmm.matmul("Q8_0", self.W["router"], y, self.E)
+        ids, w = qmm.moe_route(logits, 4, "sigmoid", self.bias, n_group=4, topk_group=2, group_top=2, scale=1.5, slots=slots)
+        ffn = qmm.moe_ffn("Q4_K", self.W["gu"], self.W["d"], self.E, ids, w, y, self.N_ff)
+        acts, h = qmm.rmsnorm_q8("Q8_0", ffn, self.w[1], 1e-5, residual=h, sum_out=h)
+        gate = qmm.gemv_q8("Q8_0", self.W["gate"], acts, self.F, act="silu", out_dtype=torch.float32)
+        up = qmm.gemv_q8("Q8_0", self.W["up"], acts, self.F, mul=gate, out_dtype=torch.float16)
+        return qmm.matmul_ep("Q6_K", self.W["down"], up, self.D, residual=h, out=h), ids, w, logits, y, ffn
+
+
+def test_a_layer_step_against_the_definitions(oracle_mod):
+    """Each operator's result in the run against its definition on that run's own operands."""
+    L, M = Layer("step"), 5
+    g = wl.rng("layer", "inputs")
+    x = g.normal(size=(M, L.D)).astype(np.float16)
+    x = (x / np.float16(8)).astype(np.float16)
+    h0 = g.normal(size=(M, L.D)).astype(np.float32)
+    slots = np.array([3, 9, -1, 4, 7], np.int32)
+    st = dev(h0)
+    out, ids, w, logits, y, ffn = L.step(dev(x), st, dev(slots))
+    Y, B = oracle_mod.matmul("Q4_K", L.np["o"], L.D, x)
+    h1, tol = layer.epilogue(Y, 1e-3 * B + 1e-6, residual=h0)
+    h1r = dev(h0)
+    qmm.matmul_ep("Q4_K", L.W["o"], dev(x), L.D, residual=h1r, out=h1r)
+    check(host(h1r), h1, tol, "projection")
+    want = layer.rmsnorm(host(h1r), None, host(L.w[0]), 1e-5)[1]
+    check(host(y), want, norm_tol(want, "f16"), "norm")
+    wi, ww = layer.route(host(logits), 4, "sigmoid", host(L.bias), 4, 2, 2, True, 1.5, slots)
+    assert np.array_equal(host(ids), wi)
+    check(host(w), ww, 2.0 ** -20 * ww, "weights")
+    fy, ft = oracle_mod.moe_ffn("Q4_K", L.np["gu"], L.np["d"], L.E, L.N_ff, L.D, wi, host(w), host(y))
+    check(host(ffn), fy, ft + 1e-30, "experts")
+    assert not host(ffn)[2].any()                           # the padding token reached none
+    h2, n2 = layer.rmsnorm(host(ffn), host(h1r), host(L.w[1]), 1e-5)
+    q = int8.rebuilt(host(qmm.rmsnorm(dev(h2), L.w[1], 1e-5)))
+    G, GB = oracle_mod.matmul("Q8_0", L.np["gate"], L.D, q)
+    U, UB = oracle_mod.matmul("Q8_0", L.np["up"], L.D, q)
+    gate, gt = layer.epilogue(G, 2e-5 * GB + 1e-6, act="silu")
+    up, ut = layer.epilogue(U, 2e-5 * UB + 1e-6, mul=gate, f16=True)
+    ut = ut + np.abs(U) * gt * (1 + 2.0 ** -10)
+    down, DB = oracle_mod.matmul("Q6_K", L.np["down"], L.F, up)
+    _, du = oracle_mod.matmul("Q6_K", L.np["down"], L.F, ut)
+    want, tol = layer.epilogue(down, 1e-3 * (DB + du) + 1e-6 + du, residual=h2)
+    check(host(out), want, tol, "out")
+
+
+def test_captured_layer_replays_with_other_inputs():
+    """One capture, replayed with other inputs, against the eager step; the program's own work between the replays."""
+    L, M = Layer("graph"), 3
+    g = wl.rng("layer", "graphs")
+    x, h, slots = (torch.empty((M, L.D), dtype=torch.float16, device="cuda"), torch.empty((M, L.D), device="cuda"),
+                   torch.empty(M, dtype=torch.int32, device="cuda"))
+
+    def fill(i):
+        gi = wl.rng("layer", f"graph{i}")
+        x.copy_(dev((gi.normal(size=(M, L.D)) / 8).astype(np.float16)))
+        h.copy_(dev(gi.normal(size=(M, L.D)).astype(np.float32)))
+        slots.copy_(dev(np.array([i, -1 if i % 2 else 2, 5], np.int32)))
+
+    fill(0)
+    L.step(x, h, slots)                                     # everything is loaded before the capture
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            got = L.step(x, h, slots)
+    for i in range(1, 5):
+        fill(i)
+        want = [t.clone() for t in L.step(x, h, slots)]
+        torch.cuda.synchronize()
+        fill(i)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b), i
+
+
+def test_two_streams_at_once():
+    """Calls on two streams, none with a workspace: each as if alone."""
+    L = Layer("streams")
+    g = wl.rng("layer", "streams")
+    ins = [((g.normal(size=(m, L.D)) / 8).astype(np.float16), g.normal(size=(m, L.D)).astype(np.float32)) for m in (2, 7)]
+    alone = [L.step(dev(x), dev(h), None) for x, h in ins]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(3):
+        both = []
+        held = [(dev(x), dev(h)) for x, h in ins]
+        torch.cuda.synchronize()
+        for s, (x, h) in zip(streams, held):
+            with torch.cuda.stream(s):
+                both.append(L.step(x, h, None))
+        torch.cuda.synchronize()
+        for a, b in zip(alone, both):
+            assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+def test_calls_on_a_stream_given(oracle_mod):
+    """stream=: results of that stream's memory, the same numbers."""
+    g = wl.rng("layer", "given")
+    s = torch.cuda.Stream()
+    x, r = dev(g.normal(size=(4, 512)).astype(np.float32)), dev(g.normal(size=(4, 512)).astype(np.float32))
+    W = dev(wl.random_weights("Q8_0", 96, 512, g))
+    P = qmm.repack("Q8_0", W, 96, 512)
+    torch.cuda.synchronize()
+    for fn in (lambda **k: qmm.rmsnorm(x, None, residual=r, **k), lambda **k: qmm.rmsnorm_q8("Q8_0", x, None, residual=r, **k)[0],
+               lambda **k: qmm.matmul_ep("Q8_0", W, x, 96, act="silu", **k), lambda **k: qmm.matmul_packed_ep("Q8_0", P, x, 96, **k),
+               lambda **k: qmm.moe_route(x, 5, **k), lambda **k: qmm.gemv_q8("Q8_0", P, qmm.rmsnorm_q8("Q8_0", x, None), 96, **k)):
+        a = fn()
+        torch.cuda.synchronize()
+        b = fn(stream=s)
+        torch.cuda.synchronize()
+        a, b = (t if isinstance(t, tuple) else (t,) for t in (a, b))
+        assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+def test_python_refusals_on_the_gpu():
+    z = lambda *s, t=torch.float32: torch.zeros(s, dtype=t, device="cuda")  # noqa: E731
+    u8 = z(96 * 544, t=torch.uint8)
+    with pytest.raises(TypeError, match="weight must be float32"):
+        qmm.rmsnorm(z(2, 64), z(64, t=torch.float16))
+    with pytest.raises(ValueError, match="weight must hold 64"):
+        qmm.rmsnorm(z(2, 64), z(65))
+    with pytest.raises(ValueError, match="residual is"):
+        qmm.rmsnorm(z(2, 64), None, residual=z(2, 65))
+    with pytest.raises(TypeError, match="sum_out is"):
+        qmm.rmsnorm(z(2, 64), None, residual=z(2, 64), sum_out=z(2, 64, t=torch.float16))
+    with pytest.raises(ValueError, match="without a residual"):
+        qmm.rmsnorm(z(2, 64), None, sum_out=z(2, 64))
+    with pytest.raises(ValueError, match="packed"):
+        qmm.rmsnorm(z(64, 2).t(), None)
+    with pytest.raises(qmm.QmmError):
+        qmm.rmsnorm(z(2, 64, t=torch.float64), None)
+    with pytest.raises(qmm.QmmError, match="D="):
+        qmm.rmsnorm_q8("Q8_0", z(2, 40), None)
+    with pytest.raises(qmm.QmmError):
+        qmm.rmsnorm_q8("Q4_K", z(2, 64), None)
+    with pytest.raises(ValueError, match="codes must be"):
+        qmm.rmsnorm_q8("Q8_0", z(2, 64), None, acts=(z(2, 64), z(2, 2), z(2, 2, t=torch.int32)))
+    with pytest.raises(qmm.QmmError):
+        qmm.moe_route(z(2, 8), 9)
+    with pytest.raises(ValueError, match="bias must hold 8"):
+        qmm.moe_route(z(2, 8), 2, bias=z(7))
+    with pytest.raises(TypeError, match="slots must be int32"):
+        qmm.moe_route(z(2, 8), 2, slots=z(2, t=torch.int64))
+    with pytest.raises(ValueError, match="ids and weights must be"):
+        qmm.moe_route(z(2, 8), 2, ids=z(2, 3, t=torch.int32), weights=z(2, 3))
+    with pytest.raises(ValueError, match="go together"):
+        qmm.moe_route(z(2, 8), 2, weights=z(2, 2))
+    with pytest.raises(ValueError, match="mul is"):
+        qmm.matmul_ep("Q8_0", u8, z(2, 512), 96, mul=z(2, 95))
+    with pytest.raises(ValueError, match="bias must hold 96"):
+        qmm.matmul_ep("Q8_0", u8, z(2, 512), 96, bias=z(97))
+    with pytest.raises(qmm.QmmError, match="act"):
+        qmm.matmul_ep("Q8_0", u8, z(2, 512), 96, act="tanh")
+    with pytest.raises(TypeError, match="type asked for"):
+        qmm.matmul_ep("Q8_0", u8, z(2, 512), 96, out=z(2, 96), out_dtype=torch.float16)
+    with pytest.raises(qmm.QmmError):
+        qmm.matmul_ep("Q8_0", u8, z(2, 512), 96, out=z(2, 96, t=torch.float64))
+    with pytest.raises(qmm.QmmError):
+        qmm.matmul_ep("Q8_0", u8, z(2, 500))                # no whole blocks, no N
+    with pytest.raises(ValueError, match="A must be"):
+        qmm.matmul_ep("Q8_0", u8, z(2, 1024)[:, :512], 96)
+    with pytest.raises(ValueError, match="scales must hold"):
+        qmm.gemv_q8("Q8_0", u8, (z(2, 512, t=torch.int8), z(2, 15), z(2, 16, t=torch.int32)), 96)
+    assert torch.cuda.is_available()
+    torch.cuda.synchronize()
