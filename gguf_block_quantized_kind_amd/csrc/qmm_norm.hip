@@ -82,25 +82,41 @@ __global__ __launch_bounds__(R > 256 ? R : 256) void rmsnorm_kernel(const Norm n
   float h[NP][V], w[NP][V];
 #pragma unroll
   for (int i = 0; i < NP; ++i) load8(n.x, n.x_f16, t * n.x_stride + head + V * (r + i * R), D - V * (r + i * R), h[i]);
+  // (Four pieces a thread leave no registers for residual and weight beside
+  // them: a piece's residual is added as it comes, the weight is loaded with the
+  // factor known.)
+  constexpr bool kLate = NP >= 4;
   if (n.residual) {
-    float a[NP][V];
+    float a[kLate ? 1 : NP][V];
 #pragma unroll
-    for (int i = 0; i < NP; ++i)
-      load8(n.residual, n.residual_f16, t * n.residual_stride + head + V * (r + i * R), D - V * (r + i * R), a[i]);
+    for (int i = 0; i < NP; ++i) {
+      float(&b)[V] = a[kLate ? 0 : i];
+      load8(n.residual, n.residual_f16, t * n.residual_stride + head + V * (r + i * R), D - V * (r + i * R), b);
+      if constexpr (kLate) {
 #pragma unroll
-    for (int i = 0; i < NP; ++i)
+        for (int e = 0; e < V; ++e) h[i][e] += b[e];
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    if constexpr (!kLate) {
 #pragma unroll
-      for (int e = 0; e < V; ++e) h[i][e] += a[i][e];
-  }
+      for (int i = 0; i < NP; ++i)
 #pragma unroll
-  for (int i = 0; i < NP; ++i) {
-    if (n.weight) {
-      load8(n.weight, 0, V * (r + i * R), D - V * (r + i * R), w[i]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < V; ++e) w[i][e] = 1.f;
+        for (int e = 0; e < V; ++e) h[i][e] += a[i][e];
     }
   }
+  auto weights = [&]() {
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      if (n.weight) {
+        load8(n.weight, 0, V * (r + i * R), D - V * (r + i * R), w[i]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) w[i][e] = 1.f;
+      }
+    }
+  };
+  if constexpr (!kLate) weights();
   double ss = 0.0;
 #pragma unroll
   for (int i = 0; i < NP; ++i)
@@ -118,6 +134,7 @@ __global__ __launch_bounds__(R > 256 ? R : 256) void rmsnorm_kernel(const Norm n
   }
   const double m = ss / (double)D + (double)n.eps;
   const double f = m > 0.0 ? rsqrt(m) : m == 0.0 ? 0.0 : m;  // a row of zeros without eps stays one; NaN stays
+  if constexpr (kLate) weights();
   if (!live) return;
   if (n.sum) {
 #pragma unroll

@@ -1,9 +1,26 @@
 // qmm_route.hip -- the choice of experts: scores, groups, the topk largest, and
 // their weights.
 //
-// One wave takes one token.  The values that decide are held in 64 bits: a
-// score plus a bias, and sums of scores, lie closer together than f32 tells
-// apart in every few thousand tokens.
+// The choice is that of 64-bit scores, since a score plus a bias, or two sums
+// of scores, lie closer together than f32 tells apart in every few thousand
+// tokens.  Nearly all of the work is done in f32 all the same: f32 values
+// bring out topk + 2 candidates, whose scores are computed in 64 bits (their
+// weights need those anyway), and whose order is corrected where neighbours lie
+// within the f32 values' error.  Where that leaves a doubt about which experts
+// belong among the candidates (rows of many equal scores, sums of groups within
+// 2^-19), the row is done again in 64 bits throughout.
+//
+// Candidates.  L = 16 or 64 lanes take a row, each up to EPL experts in
+// registers.  An expert's key is a 32-bit whole number: its value's bits, made
+// to order as the values do, with the lowest BITS replaced by the complement of
+// its number, so keys differ, equal values go by the lowest number, and the
+// key names its expert.  The next smaller key after x is x + max over keys of
+// (key - x) in 32-bit wrap-around arithmetic (keys below x wrap to the top of the
+// range, the nearest one highest): one subtraction and half a max3 an expert and
+// a round, no compares, no removal.
+//
+// Bound.  16384 tokens of 256 experts are 17.9 MB; the arithmetic is about 30
+// instructions an expert, the selection two thirds of them.
 #include <math.h>
 
 #include "qmm_internal.h"
@@ -15,7 +32,16 @@ __device__ __forceinline__ double shfl_xor(double v, int m) {
   const int2 a = __builtin_bit_cast(int2, v);
   return __builtin_bit_cast(double, int2{__shfl_xor(a.x, m), __shfl_xor(a.y, m)});
 }
+__device__ __forceinline__ double shfl(double v, int lane) {
+  const int2 a = __builtin_bit_cast(int2, v);
+  return __builtin_bit_cast(double, int2{__shfl(a.x, lane), __shfl(a.y, lane)});
+}
 
+template <bool F16>
+__device__ __forceinline__ float logit_of(const Route &r, int64_t at) {
+  if constexpr (F16) return (float)static_cast<const _Float16 *>(r.logits)[at];
+  else return static_cast<const float *>(r.logits)[at];
+}
 __device__ __forceinline__ float logit(const Route &r, int64_t row, int e) {
   return r.f16 ? (float)static_cast<const _Float16 *>(r.logits)[row * r.stride + e]
                : static_cast<const float *>(r.logits)[row * r.stride + e];
@@ -23,11 +49,85 @@ __device__ __forceinline__ float logit(const Route &r, int64_t row, int e) {
 
 // e^(l - m), also where both are infinite.
 __device__ __forceinline__ double above(float l, float m) { return l == m ? 1.0 : exp((double)l - (double)m); }
+__device__ __forceinline__ double sigmoid(float l) {
+  const double t = exp(-fabs((double)l));
+  return (l >= 0.f ? 1.0 : t) / (1.0 + t);
+}
 
-__global__ __launch_bounds__(64) void route_kernel(const Route r) {
-  extern __shared__ double pick[];  // [E]
-  const int lane = threadIdx.x;
-  const int64_t row = blockIdx.x;
+// Orders this wave's LDS accesses.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// Reductions over the L = 16 or 64 lanes of a row, the result on each of them.
+// Within a DPP row of 16: neighbours, pairs (quad_perm), the two quads (half
+// mirror), the two halves (mirror); its four through scalars.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, true);  // every source lane is there
+}
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) { return __uint_as_float(dpp<CTRL>(__float_as_uint(v))); }
+template <int CTRL>
+__device__ __forceinline__ double dpp(double v) {
+  const uint2 a = __builtin_bit_cast(uint2, v);
+  return __builtin_bit_cast(double, uint2{dpp<CTRL>(a.x), dpp<CTRL>(a.y)});
+}
+__device__ __forceinline__ uint32_t lane_of(uint32_t v, int i) { return __builtin_amdgcn_readlane(v, i); }
+__device__ __forceinline__ float lane_of(float v, int i) { return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), i)); }
+__device__ __forceinline__ double lane_of(double v, int i) {
+  const uint2 a = __builtin_bit_cast(uint2, v);
+  return __builtin_bit_cast(double, uint2{(uint32_t)__builtin_amdgcn_readlane(a.x, i), (uint32_t)__builtin_amdgcn_readlane(a.y, i)});
+}
+template <int L, typename T, typename F>
+__device__ __forceinline__ T reduce(T v, F f) {
+  v = f(v, dpp<0xB1>(v));
+  v = f(v, dpp<0x4E>(v));
+  v = f(v, dpp<0x141>(v));
+  v = f(v, dpp<0x140>(v));
+  if constexpr (L == 64) v = f(f(lane_of(v, 0), lane_of(v, 16)), f(lane_of(v, 32), lane_of(v, 48)));
+  return v;
+}
+template <int L>
+__device__ __forceinline__ float row_max(float v) { return reduce<L>(v, [](float a, float b) { return fmaxf(a, b); }); }
+template <int L>
+__device__ __forceinline__ float row_min(float v) { return reduce<L>(v, [](float a, float b) { return fminf(a, b); }); }
+template <int L>
+__device__ __forceinline__ uint32_t row_max(uint32_t v) { return reduce<L>(v, [](uint32_t a, uint32_t b) { return max(a, b); }); }
+template <int L>
+__device__ __forceinline__ double row_sum(double v) { return reduce<L>(v, [](double a, double b) { return a + b; }); }
+
+// Weight of a chosen expert with logit l (id < 0: none) on each of the L lanes
+// of a row: normalized relative to the largest chosen logit, so that it stays
+// right where the scores themselves vanish.  The exponentials are in 64 bits (a
+// difference of logits has no rounding there), the quotients in f32.
+template <int L>
+__device__ __forceinline__ float weight_of(const Route &r, int id, float l, float top, double total) {
+  double w = 0.0, below = 1.0;  // numerator, denominator
+  float sum = 1.f;
+  if (r.sigmoid) {
+    const double t = exp(-fabs((double)l));
+    below = 1.0 + t;
+    w = l >= 0.f ? 1.0 : t;
+    if (r.normalize) {
+      const float lead = row_max<L>(id >= 0 ? l : -INFINITY);
+      if (lead < 0.f) w = above(l, lead);
+    }
+  } else {
+    if (r.normalize) top = row_max<L>(id >= 0 ? l : -INFINITY);
+    else below = total;
+    w = above(l, top);
+  }
+  const float share = id >= 0 ? (float)w / (float)below : 0.f;
+  if (r.normalize) sum = (float)row_sum<L>((double)share);
+  return id >= 0 ? share / sum : 0.f;
+}
+
+// A row by one wave, in 64 bits throughout; pick: this wave's LDS [E].
+__device__ __forceinline__ void route_row(const Route &r, int64_t row, double *pick) {
+  const int lane = threadIdx.x & 63;
   const int E = (int)r.E, k = (int)r.topk;
   int id = -1;  // lane i: the expert of slot i
   double total = 0.0;
@@ -36,28 +136,27 @@ __global__ __launch_bounds__(64) void route_kernel(const Route r) {
     // The largest logit and the sum of the exponentials.
     if (!r.sigmoid) {
       for (int e = lane; e < E; e += 64) top = fmaxf(top, logit(r, row, e));  // fmaxf passes a NaN by
-#pragma unroll
-      for (int m = 32; m >= 1; m >>= 1) top = fmaxf(top, __shfl_xor(top, m));
+      top = row_max<64>(top);
       for (int e = lane; e < E; e += 64) {
         const float l = logit(r, row, e);
         if (l > -INFINITY) total += above(l, top);
       }
-#pragma unroll
-      for (int m = 32; m >= 1; m >>= 1) total += shfl_xor(total, m);
+      total = row_sum<64>(total);
     }
     // Without a bias or sums the logits decide as their scores would.
     const bool plain = !r.bias && (r.n_group == 1 || r.group_top == 1);
+    wave_sync();  // an earlier row's reads
     for (int e = lane; e < E; e += 64) {
       const float l = logit(r, row, e);
       double c = -INFINITY;
       if (l > -INFINITY) {
         if (plain) c = l;
-        else c = (r.sigmoid ? 1.0 / (1.0 + exp(-(double)l)) : above(l, top) / total) + (r.bias ? (double)r.bias[e] : 0.0);
+        else c = (r.sigmoid ? sigmoid(l) : above(l, top) / total) + (r.bias ? (double)r.bias[e] : 0.0);
         if (c != c) c = -INFINITY;
       }
       pick[e] = c;
     }
-    __syncthreads();
+    wave_sync();
     if (r.n_group > 1) {
       const int size = E / (int)r.n_group;
       double best = -INFINITY;  // lane g: its group's value
@@ -72,13 +171,12 @@ __global__ __launch_bounds__(64) void route_kernel(const Route r) {
       }
       int before = 0;
       for (int g = 0; g < (int)r.n_group; ++g) {
-        const int2 v = __builtin_bit_cast(int2, best);
-        const double other = __builtin_bit_cast(double, int2{__shfl(v.x, g), __shfl(v.y, g)});
+        const double other = shfl(best, g);
         if (other > best || (other == best && g < lane)) ++before;
       }
       if (lane < r.n_group && before >= r.topk_group)
         for (int i = 0; i < size; ++i) pick[lane * size + i] = -INFINITY;
-      __syncthreads();
+      wave_sync();
     }
     for (int j = 0; j < k; ++j) {
       double c = -INFINITY;
@@ -94,39 +192,323 @@ __global__ __launch_bounds__(64) void route_kernel(const Route r) {
       if (c == -INFINITY) break;
       if (lane == j) id = at;
       if (lane == 0) pick[at] = -INFINITY;
-      __syncthreads();
+      wave_sync();
     }
   }
-  // Weights of the chosen, normalized relative to the largest chosen logit, so
-  // that they stay right where the scores themselves vanish.
-  double w = 0.0;
-  const float l = id >= 0 ? logit(r, row, id) : -INFINITY;
-  if (r.normalize) {
-    float lead = l;
-#pragma unroll
-    for (int m = 32; m >= 1; m >>= 1) lead = fmaxf(lead, __shfl_xor(lead, m));
-    if (id >= 0) {
-      if (!r.sigmoid) w = above(l, lead);
-      else if (l >= 0.f) w = 1.0 / (1.0 + exp(-(double)l));
-      else w = (lead < 0.f ? above(l, lead) : exp((double)l)) / (1.0 + exp((double)l));
-    }
-    double sum = w;
-#pragma unroll
-    for (int m = 32; m >= 1; m >>= 1) sum += shfl_xor(sum, m);
-    if (id >= 0) w /= sum;
-  } else if (id >= 0) {
-    w = r.sigmoid ? 1.0 / (1.0 + exp(-(double)l)) : above(l, top) / total;
-  }
+  const float w = weight_of<64>(r, id, id >= 0 ? logit(r, row, id) : -INFINITY, top, total);
   if (lane < k) {
     r.ids[row * k + lane] = id;
-    r.weights[row * k + lane] = (float)(w * (double)r.scale);
+    r.weights[row * k + lane] = w * r.scale;
   }
+}
+
+// Any number of experts and groups.
+__global__ __launch_bounds__(64) void route_any_kernel(const Route r) {
+  extern __shared__ double lds[];
+  const int64_t row = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+  if (row < r.M) route_row(r, row, lds);
+}
+
+// What a row's experts are ranked by, and whether the sum of the exponentials
+// is needed: the logits (no bias, no sums of two), without or with that sum
+// (for weights that are not normalized); the sigmoid + bias; the softmax + bias.
+enum Mode { kLogit, kLogitSum, kSigmoid, kSoftmax };
+
+// Bits of a float made to order as the floats (neither NaN nor -0).
+__device__ __forceinline__ uint32_t ordered(float v) {
+  const uint32_t u = __float_as_uint(v);
+  return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float unordered(uint32_t k) {
+  return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+}
+
+constexpr uint32_t kNone = 0x00800000u;  // ordered(the lowest finite float)
+
+constexpr int log2_of(int v) { return v <= 1 ? 0 : 1 + log2_of(v / 2); }
+constexpr int kWaves = 4;
+
+// What f32 values may be off by beside their truncation in the keys: sigmoids
+// and softmax shares are within 2^-22, the sum with a bias half a step more.
+__device__ __forceinline__ float slack(int mode, float v) {
+  return mode == kSigmoid || mode == kSoftmax ? 0x1p-21f + 0x1p-23f * fabsf(v) : 0.f;
+}
+
+// L lanes a row, EPL experts a lane.  The lanes are dealt out to the groups
+// evenly (n_group divides L), and within a group's lanes its experts go in
+// units of UNIT neighbours (one load), the lanes side by side.
+// A call with its groups dealt out: experts of a group, and the logarithm of the
+// lanes that share it.
+struct Split : Route {
+  int size, log_per;
+};
+
+template <int L, int EPL, int MODE, bool F16>
+__global__ __launch_bounds__(64 * kWaves) void route_kernel(const Split r) {
+  constexpr int BITS = log2_of(L * EPL);
+  constexpr uint32_t kLow = (1u << BITS) - 1;
+  constexpr int UNIT = EPL < 4 ? EPL : 4, NU = EPL / UNIT;
+  extern __shared__ double lds[];
+  const int lane = threadIdx.x & 63, q = lane % L;
+  const int64_t first = (((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * kWaves + (threadIdx.x >> 6)) * (64 / L);
+  if (first >= r.M) return;  // the whole wave
+  const int64_t row = first + lane / L;
+  const bool there = row < r.M;
+  const int k = (int)r.topk, G = (int)r.n_group;
+  const bool live = there && (!r.slots || r.slots[row] >= 0);
+  const int size = r.size, log_per = r.log_per, per = 1 << log_per;  // experts and lanes of a group
+  const int g = q >> log_per, sub = q & (per - 1);
+
+  // Logits and biases; experts that are not there read as -inf.  Where the
+  // experts fill every lane (the same for all rows) the loads go out together
+  // under no lane's condition, rows that are skipped reading the last row's.
+  float l[EPL], b[EPL];
+  constexpr bool kBias = MODE == kSigmoid || MODE == kSoftmax;
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) b[i] = 0.f;
+  if (size == NU * UNIT * per) {
+    const int64_t base = min(row, r.M - 1) * r.stride + g * size + sub * UNIT;
+    if constexpr (F16) {
+      _Float16 h[NU][UNIT];
+#pragma unroll
+      for (int u = 0; u < NU; ++u)
+        __builtin_memcpy(h[u], static_cast<const _Float16 *>(r.logits) + base + u * per * UNIT, sizeof h[u]);
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) l[i] = (float)h[i / UNIT][i % UNIT];
+    } else {
+#pragma unroll
+      for (int u = 0; u < NU; ++u)
+        __builtin_memcpy(&l[u * UNIT], static_cast<const float *>(r.logits) + base + u * per * UNIT, UNIT * sizeof(float));
+    }
+    if (kBias && r.bias) {
+#pragma unroll
+      for (int u = 0; u < NU; ++u)
+        __builtin_memcpy(&b[u * UNIT], r.bias + g * size + (u * per + sub) * UNIT, UNIT * sizeof(float));
+    }
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) l[i] = live ? l[i] : -INFINITY;
+  } else {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      const int at = (i / UNIT * per + sub) * UNIT + i % UNIT;  // within the group
+      const bool is = live && at < size;
+      const int e = is ? g * size + at : 0;
+      const int64_t from = (is ? row : 0) * r.stride + e;
+      l[i] = logit_of<F16>(r, from);
+      if (kBias && r.bias) b[i] = r.bias[e];
+      l[i] = is ? l[i] : -INFINITY;
+    }
+  }
+
+  // The largest logit and the sum of the exponentials.
+  float top = -INFINITY;
+  double total = 0.0;
+  if constexpr (MODE == kLogitSum || MODE == kSoftmax) {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) top = fmaxf(top, l[i]);
+    top = row_max<L>(top);
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      if (!(l[i] > -INFINITY)) continue;
+      if constexpr (MODE == kSoftmax) total += above(l[i], top);  // decides: 64 bits
+      else total += l[i] == top ? 1.0 : (double)expf(l[i] - top);
+    }
+    total = row_sum<L>(total);
+  }
+
+  // Values in f32.
+  float c[EPL];
+  const float share = MODE == kSoftmax ? (float)(1.0 / total) : 0.f;
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    const float v = l[i];
+    float s;
+    if constexpr (MODE == kSigmoid) s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v * -1.44269504f)) + b[i];
+    else if constexpr (MODE == kSoftmax) s = (v == top ? 1.0f : __builtin_amdgcn_exp2f((v - top) * 1.44269504f)) * share + b[i];
+    else s = v + 0.0f;  // -0 ranks as 0
+    c[i] = v > -INFINITY && s > -INFINITY ? s : -INFINITY;  // NaN of either: never chosen
+  }
+
+  bool doubt = false;
+  if (G > 1) {
+    // The group's value, on each of its lanes.
+    float a = -INFINITY, b2 = -INFINITY;  // the two largest
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      b2 = __builtin_amdgcn_fmed3f(a, b2, c[i]);
+      a = __builtin_amdgcn_fmed3f(a, c[i], INFINITY);
+    }
+    auto join = [&](float oa, float ob) {
+      b2 = fmaxf(fminf(a, oa), fmaxf(b2, ob));
+      a = fmaxf(a, oa);
+    };
+    if (per >= 2) join(dpp<0xB1>(a), dpp<0xB1>(b2));
+    if (per >= 4) join(dpp<0x4E>(a), dpp<0x4E>(b2));
+    if (per >= 8) join(dpp<0x141>(a), dpp<0x141>(b2));
+    if (per >= 16) join(dpp<0x140>(a), dpp<0x140>(b2));
+    if (per >= 32) join(__shfl_xor(a, 16), __shfl_xor(b2, 16));
+    const float value = r.group_top == 2 && b2 > -INFINITY ? a + b2 : a;
+    // Groups before this one.
+    int before = 0;
+    if constexpr (L == 16) {
+      // The same lane of every other group, by turns of the row.
+      const int mine = g << log_per;  // lanes below belong to earlier groups
+      auto seen = [&](float other, int n) {
+        const bool earlier = ((q - n) & 15) < mine;
+        before += (int)(other > value) | ((int)(other == value) & (int)earlier);
+      };
+#define QMM_TURN(n) \
+  if ((n & (per - 1)) == 0) seen(dpp<0x120 + n>(value), n);
+      QMM_TURN(1) QMM_TURN(2) QMM_TURN(3) QMM_TURN(4) QMM_TURN(5) QMM_TURN(6) QMM_TURN(7) QMM_TURN(8) QMM_TURN(9)
+      QMM_TURN(10) QMM_TURN(11) QMM_TURN(12) QMM_TURN(13) QMM_TURN(14) QMM_TURN(15)
+#undef QMM_TURN
+    } else {
+      for (int h = 0; h < G; ++h) {
+        const float other = lane_of(value, h * per);
+        before += other > value || (other == value && h < g);
+      }
+    }
+    const bool kept = before < (int)r.topk_group;
+    if constexpr (MODE == kSigmoid || MODE == kSoftmax) {
+      // How far the kept ones are above the others.
+      const float in = row_min<L>(kept ? value : INFINITY), out = row_max<L>(kept ? -INFINITY : value);
+      // What the sums round off goes by their terms.
+      const float terms = row_max<L>(a > -INFINITY ? fabsf(a) + (b2 > -INFINITY ? fabsf(b2) : 0.f) : 0.f);
+      if (out > -INFINITY) doubt = !(in - out > 0x1p-19f + 0x1p-21f * terms);
+    }
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) c[i] = kept ? c[i] : -INFINITY;
+  }
+
+  // (Experts that are out have the keys of -inf, below kNone.)
+  uint32_t key[EPL], best = 0;
+#pragma unroll
+  for (int u = 0; u < NU; ++u) {
+    const uint32_t low = kLow - (uint32_t)(g * size + (u * per + sub) * UNIT);
+#pragma unroll
+    for (int x = 0; x < UNIT; ++x) {
+      const int i = u * UNIT + x;
+      key[i] = (ordered(c[i]) & ~kLow) | ((low - x) & kLow);
+      best = max(best, key[i]);
+    }
+  }
+  // Candidates: lane j gets the j-th largest key.
+  uint32_t x = row_max<L>(best), mine = q == 0 ? x : 0u;
+  for (int j = 1; j < k + 2; ++j) {
+    uint32_t d = 0;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) d = max(d, key[i] - x);
+    d = row_max<L>(d);
+    x = x + d < x ? x + d : 0u;  // none below: 0, and it stays
+    mine = q == j ? x : mine;
+  }
+
+  // Order and completeness within the values' error.
+  const int id0 = mine >= kNone ? (int)(kLow - (mine & kLow)) : -1;
+  const uint32_t cell = mine & ~kLow;
+  const uint32_t next = __shfl_down(mine, 1), over = __shfl_down(mine, 2);
+  const float v = unordered(cell);
+  bool close = false, open = false;
+  // f16 logits fill no more bits than the keys keep.
+  if constexpr (!((MODE == kLogit || MODE == kLogitSum) && F16)) {
+    auto near = [&](uint32_t other) {
+      if (other < kNone) return false;
+      const float w = unordered(other | kLow);  // its cell's upper end
+      return !(v - w > 2.0f * slack(MODE, v));
+    };
+    if (id0 >= 0 && q < k) close = near(next);
+    if (id0 >= 0 && q == k - 1) open = near(over);
+  }
+  doubt = doubt || open;
+
+  // The candidates' scores in 64 bits.
+  const float cl = id0 >= 0 ? logit_of<F16>(r, row * r.stride + id0) : -INFINITY;
+  int slot = q;
+  if (__any(close)) {
+    double exact = -INFINITY;
+    if (id0 >= 0) {
+      if constexpr (MODE == kSigmoid) exact = sigmoid(cl) + (r.bias ? (double)r.bias[id0] : 0.0);
+      else if constexpr (MODE == kSoftmax) exact = above(cl, top) / total + (r.bias ? (double)r.bias[id0] : 0.0);
+      else exact = cl;
+    }
+    int before = 0;
+    for (int j = 0; j < k + 2; ++j) {
+      const double o = shfl(exact, lane - q + j);
+      const int oi = __shfl(id0, lane - q + j);
+      before += oi >= 0 && (o > exact || (o == exact && oi < id0));
+    }
+    if (id0 >= 0) slot = before;
+  }
+  const int id = slot < k ? id0 : -1;
+  const float w = weight_of<L>(r, id, cl, top, total);
+  if (there && q < k + 2 && slot < k) {
+    r.ids[row * k + slot] = id;
+    r.weights[row * k + slot] = w * r.scale;
+  }
+  // Rows in doubt again, one at a time.
+  uint64_t again = __ballot(doubt && live);
+  while (again) {
+    const int at = __builtin_ctzll(again);
+    again &= L == 64 ? 0ull : ~(((1ull << (L % 64)) - 1) << (at / L * L));
+    route_row(r, first + at / L, lds + (threadIdx.x >> 6) * r.E);
+  }
+}
+
+constexpr int64_t kGridX = 1 << 20;
+
+template <int L, int EPL, int MODE>
+void launch(const Split &r, dim3 grid, size_t lds, hipStream_t s) {
+  if (r.f16) hipLaunchKernelGGL((route_kernel<L, EPL, MODE, true>), grid, dim3(64 * kWaves), lds, s, r);
+  else hipLaunchKernelGGL((route_kernel<L, EPL, MODE, false>), grid, dim3(64 * kWaves), lds, s, r);
+}
+
+template <int L, int EPL>
+hipError_t run(const Route &call, int mode, hipStream_t s) {
+  Split r;
+  static_cast<Route &>(r) = call;
+  r.size = (int)(r.E / r.n_group), r.log_per = __builtin_ctz((unsigned)(L / r.n_group));
+  const int64_t per = kWaves * (64 / L), groups = (r.M + per - 1) / per, wide = groups < kGridX ? groups : kGridX;
+  const dim3 grid((unsigned)wide, (unsigned)((groups + wide - 1) / wide));
+  const size_t lds = (size_t)kWaves * r.E * sizeof(double);
+  switch (mode) {
+    case kLogit: launch<L, EPL, kLogit>(r, grid, lds, s); break;
+    case kLogitSum: launch<L, EPL, kLogitSum>(r, grid, lds, s); break;
+    case kSigmoid: launch<L, EPL, kSigmoid>(r, grid, lds, s); break;
+    default: launch<L, EPL, kSoftmax>(r, grid, lds, s); break;
+  }
+  return hipGetLastError();
 }
 
 }  // namespace route
 
 hipError_t launch_moe_route(const Route &r, hipStream_t s) {
-  hipLaunchKernelGGL(route::route_kernel, dim3((unsigned)r.M), dim3(64), (size_t)r.E * sizeof(double), s, r);
+  using namespace route;
+  const bool plain = !r.bias && (r.n_group == 1 || r.group_top == 1);
+  const int mode = plain ? (r.sigmoid || r.normalize ? kLogit : kLogitSum) : r.sigmoid ? kSigmoid : kSoftmax;
+  // Experts of a lane, in whole units, where L lanes share a row (0: they cannot:
+  // groups that do not divide them, more candidates than lanes).
+  auto fit = [&](int64_t L, int64_t unit) -> int64_t {
+    if (L % r.n_group != 0 || r.topk + 2 > L) return 0;
+    const int64_t size = r.E / r.n_group, step = L / r.n_group * unit;
+    return (size + step - 1) / step * unit;
+  };
+  // Many rows: 16 lanes each, four rows a wave.  Few: a wave each, whose
+  // selection takes fewer steps in a row.
+  if (const int64_t n = fit(16, 4); n && r.M > 2048) {
+    if (n <= 4) return run<16, 4>(r, mode, s);
+    if (n <= 8) return run<16, 8>(r, mode, s);
+    if (n <= 16) return run<16, 16>(r, mode, s);
+  }
+  if (const int64_t n = fit(64, 4)) {
+    if (fit(64, 1) == 1) return run<64, 1>(r, mode, s);
+    if (fit(64, 2) == 2) return run<64, 2>(r, mode, s);
+    if (n <= 4) return run<64, 4>(r, mode, s);
+    if (n <= 8) return run<64, 8>(r, mode, s);
+    if (n <= 16) return run<64, 16>(r, mode, s);
+  }
+  const int64_t wide = r.M < kGridX ? r.M : kGridX;
+  hipLaunchKernelGGL(route_any_kernel, dim3((unsigned)wide, (unsigned)((r.M + wide - 1) / wide)), dim3(64),
+                     (size_t)r.E * sizeof(double), s, r);
   return hipGetLastError();
 }
 
