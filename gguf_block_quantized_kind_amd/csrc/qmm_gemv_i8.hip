@@ -272,6 +272,10 @@ hipError_t run_shape(const uint8_t *P, const int8_t *q, const float *d, const in
 #endif
   // Measured at 4096 and 14336 rows: more waves per tile when tiles are few.
   if (N <= 4096) return run<KIND, 16, 1>(P, q, d, s, y, M, N, K, st);
+#ifdef QMM_WITH_EPILOGUE
+  // 8192 x 4096, seven tokens: Q8_0 10.4 -> 9.8 us, Q4_0 8.5 -> 8.1.
+  if (N <= 8192) return run<KIND, 8, 1>(P, q, d, s, y, M, N, K, st);
+#endif
   return run<KIND, 4, 1>(P, q, d, s, y, M, N, K, st);
 }
 

@@ -332,6 +332,21 @@ static hipError_t run_m(const uint8_t *W, const void *x, int x_f16, Out y, int M
       return run<KIND, 1, 4, 1, 1>(W, x, x_f16, y, M, N, K, s);
     }
   }
+#ifdef QMM_WITH_EPILOGUE
+  // The products with an epilogue split K further where there are few tiles: at
+  // most one a compute unit eight waves, at most two four.  Eight tokens, 4096 x
+  // 14336: Q8_0 57.0 -> 22.6 us, Q4_0 50.8 -> 18.9; 4096 x 4096: 19.1 -> 10.1, 17.2
+  // -> 9.5; 8192 x 4096: 21.3 -> 15.3, 17.5 -> 13.3 (14336 x 4096 takes 25.7 in the
+  // shape for many tiles, 28.1 with four waves).
+  if (M > 1 && (N + 15) / 16 <= device_cus()) {
+    if (M <= 4) return run<KIND, 4, 8, 1, 1>(W, x, x_f16, y, M, N, K, s);
+    return run<KIND, 8, 8, 1, 1>(W, x, x_f16, y, M, N, K, s);
+  }
+  if (M > 1 && (N + 15) / 16 <= 2 * device_cus()) {
+    if (M <= 4) return run<KIND, 4, 4, 1, 1>(W, x, x_f16, y, M, N, K, s);
+    return run<KIND, 8, 4, 1, 1>(W, x, x_f16, y, M, N, K, s);
+  }
+#endif
   if (M <= 1) return run<KIND, 1, 2, 1, 2>(W, x, x_f16, y, M, N, K, s);
   if (M <= 2) return run<KIND, 2, 2, 1, 2>(W, x, x_f16, y, M, N, K, s);
   if (M <= 4) return run<KIND, 4, 2, 2, 2>(W, x, x_f16, y, M, N, K, s);

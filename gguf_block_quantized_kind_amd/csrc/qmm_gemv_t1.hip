@@ -206,6 +206,20 @@ static hipError_t run_t1_k(const uint8_t *P, const void *x, int x_f16, Out y, in
 #else
   (void)cfg;
 #endif
+#ifdef QMM_WITH_EPILOGUE
+  // The products with an epilogue split K further where there are few tiles (at
+  // most one a compute unit): the super-block kinds over eight waves with two
+  // k-blocks in flight, 4096 x 14336 Q4_K 14.1 -> 10.4 us, 1024 x 4096 5.3 -> 4.6
+  // (Q6_K 17.0 -> 16.8, 6.2 -> 5.8).  The step-scaled kinds, which start from
+  // eight waves, take four where there are many tiles: 11008 x 4096 Q4_0 8.1 ->
+  // 7.3 us, Q8_0 11.8 -> 11.7, 14336 x 4096 9.2 -> 8.6, 14.7 -> 14.2.
+  const bool few = (N + 15) / 16 <= device_cus();
+  if constexpr (Dec<KIND>::STEP_SCALE) {
+    if (!few && KIND != MXFP4) return run_t1<KIND, 4, 1, 1, true>(P, x, x_f16, y, N, K, s);
+  } else {
+    if (few) return run_t1<KIND, 8, 2, 1, PACKED>(P, x, x_f16, y, N, K, s);
+  }
+#endif
   if constexpr (Dec<KIND>::STEP_SCALE) {
     // The step-scaled kinds (records only) decode with more VALU per byte:
     // more waves per tile, one k-block in flight each; MXFP4 at four waves

@@ -275,6 +275,33 @@ static hipError_t run_xs(const uint8_t *P, const void *x, int x_f16, Out y, int 
   return hipGetLastError();
 }
 
+#ifdef QMM_WITH_EPILOGUE
+// Launch shapes of the products with an epilogue: where there are few tiles the
+// waves of a workgroup split K instead of sharing activations, so that a compute
+// unit has as many weight loads in flight as elsewhere.  One tile a compute unit:
+// 16 waves of K (8 above 16 k-blocks, whose k-blocks in flight fill the unit
+// already); two: two tiles of four.  Eight tokens, 4096 x 14336: Q4_K 30.0 ->
+// 17.3 us, Q6_K 53.0 -> 22.8, repacked Q8_0 27.0 -> 17.9; 4096 x 4096: 12.2 ->
+// 9.1, 19.6 -> 11.7, 10.9 -> 8.7; 8192 x 4096: 12.4 -> 10.6, 19.6 -> 15.4, 12.4 ->
+// 11.6.  (With 688 tiles the shape for many is the fastest: Q6_K 11008 x 4096
+// 21.5 us, 26.9 with two tiles of four.)
+template <int KIND, int MT, bool PACKED>
+static hipError_t run_xs_mt(const uint8_t *P, const void *x, int x_f16, Out y, int M, int64_t N, int64_t K,
+                            hipStream_t s) {
+  const int64_t tiles = (N + 15) / 16, nkb = K / Dec<KIND>::KB;
+  if (tiles <= device_cus() && nkb > 16) return run_xs<KIND, MT, 1, 8, 1, 1, PACKED>(P, x, x_f16, y, M, N, K, s);
+  if (tiles <= device_cus() && nkb > 4) return run_xs<KIND, MT, 1, 16, 1, 1, PACKED>(P, x, x_f16, y, M, N, K, s);
+  if (tiles <= 2 * device_cus() && nkb > 4) return run_xs<KIND, MT, 2, 4, 1, 1, PACKED>(P, x, x_f16, y, M, N, K, s);
+  return run_xs<KIND, MT, 4, 2, 1, 1, PACKED>(P, x, x_f16, y, M, N, K, s);
+}
+#else
+template <int KIND, int MT, bool PACKED>
+static hipError_t run_xs_mt(const uint8_t *P, const void *x, int x_f16, Out y, int M, int64_t N, int64_t K,
+                            hipStream_t s) {
+  return run_xs<KIND, MT, 4, 2, 1, 1, PACKED>(P, x, x_f16, y, M, N, K, s);
+}
+#endif
+
 #ifndef QMM_WITH_EPILOGUE
 // Grouped expert products: grid (tile groups of T, work items); T tiles
 // share each staged activation k-block of the item's MT pairs.
@@ -350,9 +377,9 @@ static hipError_t run_xs_m(const uint8_t *P, const void *x, int x_f16, Out y, in
 #else
   (void)cfg;
 #endif
-  if (M <= 2) return run_xs<KIND, 2, 4, 2, 1, 1>(P, x, x_f16, y, M, N, K, s);
-  if (M <= 4) return run_xs<KIND, 4, 4, 2, 1, 1>(P, x, x_f16, y, M, N, K, s);
-  return run_xs<KIND, 8, 4, 2, 1, 1>(P, x, x_f16, y, M, N, K, s);
+  if (M <= 2) return run_xs_mt<KIND, 2, true>(P, x, x_f16, y, M, N, K, s);
+  if (M <= 4) return run_xs_mt<KIND, 4, true>(P, x, x_f16, y, M, N, K, s);
+  return run_xs_mt<KIND, 8, true>(P, x, x_f16, y, M, N, K, s);
 }
 
 }  // namespace gv
@@ -389,11 +416,11 @@ hipError_t launch_moe_xs(int kind, const uint8_t *P, const void *X, int x_f16, f
 hipError_t launch_gemv_xs_native(int kind, const uint8_t *W, const void *x, int x_f16, Out y, int M, int64_t N,
                                  int64_t K, hipStream_t s) {
   switch (kind) {
-#define QMM_CASE(K_)                                                                         \
-  case K_:                                                                                   \
-    if (M <= 2) return gv::run_xs<K_, 2, 4, 2, 1, 1, false>(W, x, x_f16, y, M, N, K, s);     \
-    if (M <= 4) return gv::run_xs<K_, 4, 4, 2, 1, 1, false>(W, x, x_f16, y, M, N, K, s);     \
-    return gv::run_xs<K_, 8, 4, 2, 1, 1, false>(W, x, x_f16, y, M, N, K, s);
+#define QMM_CASE(K_)                                                              \
+  case K_:                                                                        \
+    if (M <= 2) return gv::run_xs_mt<K_, 2, false>(W, x, x_f16, y, M, N, K, s);   \
+    if (M <= 4) return gv::run_xs_mt<K_, 4, false>(W, x, x_f16, y, M, N, K, s);   \
+    return gv::run_xs_mt<K_, 8, false>(W, x, x_f16, y, M, N, K, s);
     QMM_CASE(Q4_K) QMM_CASE(Q6_K) QMM_CASE(Q2_K) QMM_CASE(Q3_K) QMM_CASE(Q5_K)
 #undef QMM_CASE
     default: break;
