@@ -83,8 +83,9 @@ def load_library(path: str = LIBRARY) -> ctypes.CDLL:
         "qmm_attn_decode": (I, [I, I, P, P, I64, I64, I64, I64, P, I, I64, I64, P, I64, P, I64, F, I64, P, P, P, SZ,
                                 P]),
         "qmm_attn_decode_workspace_bytes": (SZ, [I64, I64, I64, I64]),
-        "qmm_matmul_ep": (I, [I, P, P, I, P, P, I, I64, I64, I64, I64, P]),
-        "qmm_matmul_packed_ep": (I, [I, P, P, I, P, P, I, I64, I64, I64, I64, P]),
+        "qmm_matmul_ep": (I, [I, P, P, I, P, P, I, I64, I64, I64, I64, P, SZ, P]),
+        "qmm_matmul_packed_ep": (I, [I, P, P, I, P, P, I, I64, I64, I64, I64, P, SZ, P]),
+        "qmm_matmul_ep_workspace_bytes": (SZ, [I, I, I64, I64, I64, I]),
         "qmm_gemv_q8": (I, [I, P, P, P, P, P, P, I, I64, I64, I64, I64, P]),
         "qmm_rmsnorm": (I, [P, I, I64, P, I, I64, P, F, P, I64, P, I, I64, I64, I64, I64, P]),
         "qmm_rmsnorm_q8": (I, [I, P, I, I64, P, I, I64, P, F, P, I64, P, P, P, I64, I64, P]),
@@ -639,8 +640,8 @@ def _load_ops():
     lib = load_library()
     names = ("qmm_rope", "qmm_kv_write", "qmm_kv_append", "qmm_kv_read", "qmm_attn_decode",
              "qmm_attn_decode_workspace_bytes", "qmm_kv_page_bytes", "qmm_rmsnorm", "qmm_rmsnorm_q8", "qmm_gemv_q8",
-             "qmm_moe_route", "qmm_matmul_ep", "qmm_matmul_packed_ep", "qmm_kind_from_name", "qmm_row_bytes",
-             "qmm_packed_bytes")
+             "qmm_moe_route", "qmm_matmul_ep", "qmm_matmul_packed_ep", "qmm_matmul_ep_workspace_bytes",
+             "qmm_kind_from_name", "qmm_row_bytes", "qmm_packed_bytes")
     _qmm_call.setup({n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names}, _check, cache_kind_id,
                     _layout_id, kind_id, _act_id, _score_id)
     _ops = _qmm_call
@@ -792,24 +793,31 @@ def rmsnorm_q8(kind, x, weight=None, eps: float = 1e-6, residual=None, acts=None
     return fn(kind, x, weight, eps, residual, codes, scales, sums, sum_out)
 
 
+def qmm_matmul_ep_workspace_bytes(kind, M: int, N: int, K: int, dtype, packed: bool = False) -> int:
+    import torch
+    code = {torch.float32: QMM_F32, torch.float16: QMM_F16}.get(dtype, 99)
+    return int(load_library().qmm_matmul_ep_workspace_bytes(kind_id(kind), int(packed), M, N, K, code))
+
+
 def matmul_ep(kind, W, A, N: int | None = None, bias=None, act=None, mul=None, residual=None, out=None, out_dtype=None,
-              stream=None):
+              stream=None, workspace=None):
     """act(A . W^T + bias) * mul + residual, [M, N] f32 (or out_dtype, or out's
     type): bias [N] f32, act one of ACTS, mul and residual [M, N] f32 or f16; out
-    may be mul or residual."""
+    may be mul or residual.  workspace: qmm_matmul_ep_workspace_bytes bytes
+    (allocated if None; many tokens only)."""
     fn = (_ops or _load_ops()).matmul_ep
     if stream is not None:
-        return _on(stream, A, fn, kind, W, A, N, bias, act, mul, residual, out, out_dtype)
-    return fn(kind, W, A, N, bias, act, mul, residual, out, out_dtype)
+        return _on(stream, A, fn, kind, W, A, N, bias, act, mul, residual, out, out_dtype, workspace)
+    return fn(kind, W, A, N, bias, act, mul, residual, out, out_dtype, workspace)
 
 
 def matmul_packed_ep(kind, P, A, N: int, bias=None, act=None, mul=None, residual=None, out=None, out_dtype=None,
-                     stream=None):
-    """matmul_ep over repacked weights (qmm_matmul_packed's kinds)."""
+                     stream=None, workspace=None):
+    """matmul_ep over repacked weights, any kind and number of tokens."""
     fn = (_ops or _load_ops()).matmul_packed_ep
     if stream is not None:
-        return _on(stream, A, fn, kind, P, A, N, bias, act, mul, residual, out, out_dtype)
-    return fn(kind, P, A, N, bias, act, mul, residual, out, out_dtype)
+        return _on(stream, A, fn, kind, P, A, N, bias, act, mul, residual, out, out_dtype, workspace)
+    return fn(kind, P, A, N, bias, act, mul, residual, out, out_dtype, workspace)
 
 
 def gemv_q8(kind, P, acts, N: int, bias=None, act=None, mul=None, residual=None, out=None, out_dtype=None, stream=None):

@@ -29,7 +29,7 @@ namespace {
 #define EACH_FUNCTION(X) \
   X(qmm_rope) X(qmm_kv_write) X(qmm_kv_append) X(qmm_kv_read) X(qmm_attn_decode) X(qmm_attn_decode_workspace_bytes) \
   X(qmm_kv_page_bytes) X(qmm_rmsnorm) X(qmm_rmsnorm_q8) X(qmm_gemv_q8) X(qmm_moe_route) X(qmm_matmul_ep)             \
-  X(qmm_matmul_packed_ep) X(qmm_kind_from_name) X(qmm_row_bytes) X(qmm_packed_bytes)
+  X(qmm_matmul_packed_ep) X(qmm_matmul_ep_workspace_bytes) X(qmm_kind_from_name) X(qmm_row_bytes) X(qmm_packed_bytes)
 #define DECLARE(fn) decltype(&::fn) p_##fn = nullptr;
 EACH_FUNCTION(DECLARE)
 #undef DECLARE
@@ -508,7 +508,25 @@ void bytes_of(const at::Tensor &t, int64_t need, const char *what) {
     raise(PyExc_ValueError, what, " holds ", t.numel(), " bytes (contiguous: ", t.is_contiguous(), "), needs ", need);
 }
 
-// kind, W, A, N, bias, act, mul, residual, out, out_dtype
+// A workspace of `bytes` (0: none is used): `o`, or one made for the call.
+struct Workspace {
+  at::Tensor t;
+  size_t bytes = 0;
+  Workspace(PyObject *o, const at::Tensor &like, size_t need) {
+    if (o != Py_None) {
+      t = tensor(o, "workspace");
+      if (!t.is_contiguous()) raise(PyExc_ValueError, "workspace must be contiguous");
+      one_gpu({&like, &t});
+      bytes = t.nbytes();
+    } else if (need) {
+      t = make(like, {(int64_t)need}, at::kByte);
+      bytes = need;
+    }
+  }
+  void *ptr() const { return t.defined() ? t.data_ptr() : nullptr; }
+};
+
+// kind, W, A, N, bias, act, mul, residual, out, out_dtype, workspace
 template <bool PACKED>
 PyObject *matmul_with(PyObject *const *a) {
   const int kind = weight_kind(a[0]);
@@ -523,9 +541,16 @@ PyObject *matmul_with(PyObject *const *a) {
   bytes_of(W, need, PACKED ? "P" : "W");
   const at::Device d = one_gpu({&A, &W});
   Ep ep(a + 4, A, M, N);
+  const int type = code(A.scalar_type());
+  size_t bytes = 0;
+  if (a[10] == Py_None && M > QMM_GEMV_MAX_M) {
+    const c10::DeviceGuard guard(d);
+    bytes = p_qmm_matmul_ep_workspace_bytes(kind, PACKED, M, N, K, type);
+  }
+  const Workspace work(a[10], A, bytes);
   call(d, PACKED ? p_qmm_matmul_packed_ep : p_qmm_matmul_ep, kind, (const void *)W.data_ptr(), (const void *)A.data_ptr(),
-       code(A.scalar_type()), (const qmm_epilogue *)&ep.e, ep.out.data_ptr(), code(ep.out.scalar_type()), ep.stride, M, N,
-       K);
+       type, (const qmm_epilogue *)&ep.e, ep.out.data_ptr(), code(ep.out.scalar_type()), ep.stride, M, N, K, work.ptr(),
+       work.bytes);
   return ep.result();
 }
 PyObject *matmul_ep(PyObject *const *a) { return matmul_with<false>(a); }
@@ -635,7 +660,7 @@ PyObject *setup(PyObject *, PyObject *args) {
 PyMethodDef methods[] = {METHOD(rope, 7),     METHOD(kv_write, 8),     METHOD(kv_append, 15),
                          METHOD(kv_read, 11), METHOD(attn_decode, 14), METHOD(rmsnorm, 7),
                          METHOD(rmsnorm_q8, 9), METHOD(gemv_q8, 12),   METHOD(moe_route, 12),
-                         METHOD(matmul_ep, 10), METHOD(matmul_packed_ep, 10), {"setup", setup, METH_VARARGS, nullptr},
+                         METHOD(matmul_ep, 11), METHOD(matmul_packed_ep, 11), {"setup", setup, METH_VARARGS, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_qmm_call", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -709,55 +709,83 @@ int check_epilogue(const qmm_epilogue *ep, void *out, int out_dtype, int64_t out
 
 }  // namespace
 
+namespace {
+
+// What both products share after the shape checks.
+int matmul_ep_checked(int kind, const void *W, bool packed, const void *A, int a_dtype, const qmm_epilogue *ep, void *out,
+                      int out_dtype, int64_t out_stride, int64_t M, int64_t N, int64_t K, void *workspace,
+                      size_t workspace_bytes, void *stream) {
+  const char *what = packed ? "P" : "W";
+  int st = check_dtype(a_dtype);
+  if (st) return st;
+  if ((st = check_epilogue_types(ep, out_dtype))) return st;
+  if (!W) return fail(QMM_ERR_BAD_ARG, "%s is NULL", what);
+  if (packed && !aligned(W, 16)) return fail(QMM_ERR_BAD_ARG, "P is not 16-byte aligned");
+  if ((st = check_act(A, a_dtype, "A"))) return st;
+  // (More than eight tokens are loaded in pieces of 16 bytes, some straight into
+  // LDS.)
+  if (M > QMM_GEMV_MAX_M && !aligned(A, 16)) return fail(QMM_ERR_BAD_ARG, "A of more than %d tokens is not 16-byte aligned", QMM_GEMV_MAX_M);
+  const int a_f16 = a_dtype == QMM_F16;
+  // Limits of the GEMMs that decode as they multiply (qmm_matmul,
+  // qmm_matmul_packed: 32-bit offsets), and of tiles and offsets over decoded
+  // weights.
+  const bool gemv = M <= QMM_GEMV_MAX_M;
+  const qmm::Way way = gemv ? qmm::Way::kGemv : qmm::way_of(kind, packed, M, N, K, a_f16);
+  if (M > (int64_t)65535 * 64 || (packed && M * K >= ((int64_t)1 << 31)) ||
+      (packed && way == qmm::Way::kGemm &&
+       (qmm::packed_bytes_of(kind, N, K) >= ((int64_t)1 << 31) || M * K * (a_f16 ? 2 : 4) >= ((int64_t)1 << 31))) ||
+      (way == qmm::Way::kDecoded && (K > (int64_t)1 << 20 || (M + 63) / 64 * ((N + 63) / 64) >= (int64_t)1 << 24)))
+    return fail(QMM_ERR_BAD_ARG, "M=%lld, N=%lld, K=%lld exceed the supported range", (long long)M, (long long)N,
+                (long long)K);
+  qmm::Epilogue e;
+  if ((st = check_epilogue(ep, out, out_dtype, out_stride, M, N, &e))) return st;
+  const size_t need = qmm::gemm_w16_workspace_bytes(kind, packed, M, N, K, a_f16);
+  if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 256)))
+    return fail(QMM_ERR_WORKSPACE, "workspace needs %zu bytes (256-byte aligned), got %zu", need,
+                workspace ? workspace_bytes : (size_t)0);
+  const uint8_t *w = (const uint8_t *)W;
+  hipStream_t s = (hipStream_t)stream;
+  hipError_t r;
+  if (gemv)
+    r = packed ? qmm::launch_gemv_packed(kind, w, A, a_f16, e, (int)M, N, K, s)
+               : qmm::launch_gemv(kind, w, A, a_f16, e, (int)M, N, K, s);
+  else if (way == qmm::Way::kGemv)
+    r = qmm::launch_gemv_many(kind, w, packed, A, a_f16, e, (int)M, N, K, s);
+  else if (way == qmm::Way::kDecoded)
+    r = qmm::launch_gemm_w16(kind, w, packed, A, a_f16, e, M, N, K, workspace, s);
+  else
+    r = packed ? qmm::launch_gemm_packed(kind, w, A, a_f16, e, M, N, K, s)
+               : qmm::launch_gemm(kind, w, A, a_f16, e, M, N, K, s);
+  return hip_status(r, packed ? "matmul_packed_ep launch" : "matmul_ep launch");
+}
+
+}  // namespace
+
+QMM_EXPORT size_t qmm_matmul_ep_workspace_bytes(int kind, int packed, int64_t M, int64_t N, int64_t K, int a_dtype) {
+  const KindInfo *k = find_kind(kind);
+  if (!k || M <= 0 || N <= 0 || K <= 0 || K > (int64_t)1 << 30 || N > INT32_MAX || M > (int64_t)65535 * 64 ||
+      K % (packed ? 256 : k->block_elems) != 0 || !dtype_ok(a_dtype))
+    return 0;
+  return qmm::gemm_w16_workspace_bytes(kind, packed != 0, M, N, K, a_dtype == QMM_F16);
+}
+
 QMM_EXPORT int qmm_matmul_ep(int kind, const void *W, const void *A, int a_dtype, const qmm_epilogue *ep, void *out,
-                             int out_dtype, int64_t out_stride, int64_t M, int64_t N, int64_t K, void *stream) {
+                             int out_dtype, int64_t out_stride, int64_t M, int64_t N, int64_t K, void *workspace,
+                             size_t workspace_bytes, void *stream) {
   const KindInfo *k;
   int st = check_shape(kind, M, N, K, &k);
   if (st) return st;
-  if ((st = check_dtype(a_dtype))) return st;
-  if ((st = check_epilogue_types(ep, out_dtype))) return st;
-  if (!W) return fail(QMM_ERR_BAD_ARG, "W is NULL");
-  if ((st = check_act(A, a_dtype, "A"))) return st;
-  if (M > (int64_t)65535 * 64) return fail(QMM_ERR_BAD_ARG, "M=%lld exceeds the supported range", (long long)M);
-  qmm::Epilogue e;
-  if ((st = check_epilogue(ep, out, out_dtype, out_stride, M, N, &e))) return st;
-  if (M <= QMM_GEMV_MAX_M)
-    return hip_status(qmm::launch_gemv(kind, (const uint8_t *)W, A, a_dtype == QMM_F16, e, (int)M, N, K,
-                                       (hipStream_t)stream),
-                      "matmul_ep launch (GEMV)");
-  return hip_status(qmm::launch_gemm(kind, (const uint8_t *)W, A, a_dtype == QMM_F16, e, M, N, K, (hipStream_t)stream),
-                    "matmul_ep launch (GEMM)");
+  return matmul_ep_checked(kind, W, false, A, a_dtype, ep, out, out_dtype, out_stride, M, N, K, workspace, workspace_bytes,
+                           stream);
 }
 
 QMM_EXPORT int qmm_matmul_packed_ep(int kind, const void *P, const void *A, int a_dtype, const qmm_epilogue *ep,
                                     void *out, int out_dtype, int64_t out_stride, int64_t M, int64_t N, int64_t K,
-                                    void *stream) {
+                                    void *workspace, size_t workspace_bytes, void *stream) {
   int st = check_packed(kind, M, N, K);
   if (st) return st;
-  if (M > QMM_GEMV_MAX_M && !qmm::gemm_packed_supported(kind))
-    return fail(QMM_ERR_UNSUPPORTED_KIND, "the prefill GEMM over repacked weights does not take kind %d (M > %d)",
-                kind, QMM_GEMV_MAX_M);
-  if ((st = check_dtype(a_dtype))) return st;
-  if ((st = check_epilogue_types(ep, out_dtype))) return st;
-  if (!P) return fail(QMM_ERR_BAD_ARG, "P is NULL");
-  if (!aligned(P, 16)) return fail(QMM_ERR_BAD_ARG, "P is not 16-byte aligned");
-  if ((st = check_act(A, a_dtype, "A"))) return st;
-  if (M * K >= ((int64_t)1 << 31)) return fail(QMM_ERR_BAD_ARG, "M*K=%lld exceeds 2^31-1", (long long)(M * K));
-  // As qmm_matmul_packed: the GEMM's 32-bit byte offsets.
-  if (M > QMM_GEMV_MAX_M &&
-      (qmm::packed_bytes_of(kind, N, K) >= ((int64_t)1 << 31) ||
-       M * K * (a_dtype == QMM_F16 ? 2 : 4) >= ((int64_t)1 << 31) || M >= ((int64_t)1 << 24)))
-    return fail(QMM_ERR_BAD_ARG, "N=%lld, K=%lld, M=%lld exceed the GEMM's 32-bit offsets", (long long)N,
-                (long long)K, (long long)M);
-  qmm::Epilogue e;
-  if ((st = check_epilogue(ep, out, out_dtype, out_stride, M, N, &e))) return st;
-  if (M <= QMM_GEMV_MAX_M)
-    return hip_status(qmm::launch_gemv_packed(kind, (const uint8_t *)P, A, a_dtype == QMM_F16, e, (int)M, N, K,
-                                              (hipStream_t)stream),
-                      "matmul_packed_ep launch (GEMV)");
-  return hip_status(qmm::launch_gemm_packed(kind, (const uint8_t *)P, A, a_dtype == QMM_F16, e, M, N, K,
-                                            (hipStream_t)stream),
-                    "matmul_packed_ep launch (GEMM)");
+  return matmul_ep_checked(kind, P, true, A, a_dtype, ep, out, out_dtype, out_stride, M, N, K, workspace, workspace_bytes,
+                           stream);
 }
 
 QMM_EXPORT int qmm_gemv_q8(int kind, const void *P, const int8_t *codes, const float *scales, const int32_t *code_sums,

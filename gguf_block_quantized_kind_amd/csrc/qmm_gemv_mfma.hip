@@ -91,6 +91,14 @@ __global__ __launch_bounds__(64 * S) __attribute__((amdgpu_waves_per_eu(OCC, 8))
     // Expert e's rows (repacked: its records, N padded to whole tiles).
     W += (int64_t)e * (PACKED ? (N + 15) / 16 * 16 : N) * row_bytes;
   }
+#ifdef QMM_WITH_EPILOGUE
+  // More than MT tokens: a row of workgroups for every MT of them.
+  const int64_t tok0 = (int64_t)blockIdx.y * MT;
+  X += tok0 * K;
+  M = min(MT, M - (int)tok0);
+#else
+  constexpr int64_t tok0 = 0;
+#endif
   // Pair of token slot t of this item.
   auto pair_of = [&](int t) { return order != nullptr ? order[c0 + t] : c0 + t; };
   const int64_t row0 = (int64_t)(ROUTED ? blockIdx.y : blockIdx.x) * (16 * R);
@@ -277,7 +285,7 @@ __global__ __launch_bounds__(64 * S) __attribute__((amdgpu_waves_per_eu(OCC, 8))
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int t = 4 * G + q;
-      if (t < M) put(Y, ROUTED ? pair_of(t) : t, row, N, acc[r][q]);
+      if (t < M) put(Y, ROUTED ? pair_of(t) : tok0 + t, row, N, acc[r][q]);
     }
   }
 }
@@ -290,7 +298,7 @@ static hipError_t run(const uint8_t *W, const void *x, int x_f16, Out y, int M, 
                       (Dec<KIND>::CHUNKED && !PACKED ? (size_t)S * 16 * Chunks<Dec<KIND>>::RS : 0);
   const size_t lds = std::max<size_t>(ring, (size_t)(S - 1) * R * 64 * sizeof(floatx4));
   const unsigned tiles = (unsigned)((N + 16 * R - 1) / (16 * R));
-  const dim3 grid = ROUTED ? dim3((unsigned)items, tiles) : dim3(tiles), block(64 * S);
+  const dim3 grid = ROUTED ? dim3((unsigned)items, tiles) : dim3(tiles, (unsigned)((M + MT - 1) / MT)), block(64 * S);
   if (x_f16)
     hipLaunchKernelGGL((gemv_mfma_kernel<KIND, _Float16, MT, S, R, PD, OCC, ROUTED, PACKED>), grid, block, lds, s, W,
                        row_bytes, (const _Float16 *)x, y, M, N, (int)K, rt);
@@ -352,6 +360,21 @@ static hipError_t run_m(const uint8_t *W, const void *x, int x_f16, Out y, int M
   if (M <= 4) return run<KIND, 4, 2, 2, 2>(W, x, x_f16, y, M, N, K, s);
   return run<KIND, 8, 2, 2, 2>(W, x, x_f16, y, M, N, K, s);
 }
+
+#ifdef QMM_WITH_EPILOGUE
+// More than eight tokens over native rows, sixteen at a time, by the number of
+// tiles of all of them: 16 tokens, 4096 x 4096 Q4_0 10.0 us with four waves of K
+// (17.3 with two over two tiles), 32 tokens 13.7 with four over two tiles (14.6
+// over one), 64 tokens 21.2 with two over two tiles (25.2 with four).
+template <int KIND>
+static hipError_t run_many(const uint8_t *W, const void *x, int x_f16, Out y, int M, int64_t N, int64_t K,
+                           hipStream_t s) {
+  const int64_t tiles = (N + 15) / 16 * ((M + 15) / 16);
+  if (tiles <= device_cus()) return run<KIND, 16, 4, 1, 1>(W, x, x_f16, y, M, N, K, s);
+  if (tiles <= 2 * device_cus()) return run<KIND, 16, 4, 2, 1>(W, x, x_f16, y, M, N, K, s);
+  return run<KIND, 16, 2, 2, 1>(W, x, x_f16, y, M, N, K, s);
+}
+#endif
 
 #ifndef QMM_WITH_EPILOGUE
 template <int KIND, bool PACKED>
@@ -583,5 +606,19 @@ hipError_t launch_gemv_mfma(int kind, const uint8_t *W, const void *x, int x_f16
   }
   return hipErrorNotSupported;
 }
+
+#ifdef QMM_WITH_EPILOGUE
+hipError_t launch_gemv_many(int kind, const uint8_t *W, bool packed, const void *x, int x_f16, Epilogue y, int M,
+                            int64_t N, int64_t K, hipStream_t s) {
+  if (packed || xs_native_supported(kind)) return launch_gemv_xs_many(kind, W, packed, x, x_f16, y, M, N, K, s);
+  switch (kind) {
+#define QMM_CASE(K_) \
+  case K_: return gv::run_many<K_>(W, x, x_f16, y, M, N, K, s);
+    QMM_CASE(Q4_0) QMM_CASE(Q5_0) QMM_CASE(Q8_0) QMM_CASE(IQ4_NL) QMM_CASE(MXFP4) QMM_CASE(IQ4_XS)
+#undef QMM_CASE
+    default: return hipErrorNotSupported;
+  }
+}
+#endif
 
 }  // namespace qmm

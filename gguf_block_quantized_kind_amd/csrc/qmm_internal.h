@@ -105,6 +105,21 @@ hipError_t launch_gemm_lds(int kind, const uint8_t *W, const void *A, int a_f16,
                            int64_t K, hipStream_t s);
 hipError_t launch_gemm_packed(int kind, const uint8_t *P, const void *A, int a_f16, Epilogue C, int64_t M, int64_t N,
                               int64_t K, hipStream_t s);
+// Sixteen tokens at a time by the GEMVs' kernels, K a multiple of 256.
+hipError_t launch_gemv_xs_many(int kind, const uint8_t *W, bool packed, const void *x, int x_f16, Epilogue y, int M,
+                               int64_t N, int64_t K, hipStream_t s);
+hipError_t launch_gemv_many(int kind, const uint8_t *W, bool packed, const void *x, int x_f16, Epilogue y, int M,
+                            int64_t N, int64_t K, hipStream_t s);
+// How a product with an epilogue of more than eight tokens runs (the rules are in
+// qmm_gemm_w16.hip): by the GEMVs' kernels, by the GEMMs that decode as they
+// multiply, or over weights decoded once to f16 into a workspace of
+// gemm_w16_workspace_bytes bytes (256-byte aligned; 0 for the other ways).  W
+// native rows or (packed) records of any kind.
+enum class Way { kGemv, kGemm, kDecoded };
+Way way_of(int kind, bool packed, int64_t M, int64_t N, int64_t K, int a_f16);
+size_t gemm_w16_workspace_bytes(int kind, bool packed, int64_t M, int64_t N, int64_t K, int a_f16);
+hipError_t launch_gemm_w16(int kind, const uint8_t *W, bool packed, const void *A, int a_f16, Epilogue C, int64_t M,
+                           int64_t N, int64_t K, void *ws, hipStream_t s);
 // The int8-activation GEMV over activations already quantized (by
 // launch_rmsnorm or launch_gemv_i8's first half).
 hipError_t launch_gemv_q8(int kind, const uint8_t *P, const int8_t *q, const float *d, const int32_t *s, float *y,

@@ -387,14 +387,28 @@ typedef struct qmm_epilogue {
     int residual_dtype;
 } qmm_epilogue;
 
-/* qmm_matmul with an epilogue (ep NULL: none).  Errors as qmm_matmul, with the
- * dtypes of out, mul and residual beside A's, and then a stride below N, an
- * unknown act or a misaligned operand as QMM_ERR_BAD_ARG. */
+/* qmm_matmul with an epilogue (ep NULL: none).  A of more than QMM_GEMV_MAX_M tokens
+ * is 16-byte aligned.  Up to some tens of tokens the sum is the GEMV's (f32 A
+ * rounded once to f16, weights exact), above the GEMM's (weights rounded once to
+ * f16, f32 A in two f16 parts).  Some sizes decode the weights once into the
+ * workspace, to f16 as the GEMM rounds them, with f32 activations' two parts beside
+ * them, and multiply from there: qmm_matmul_ep_workspace_bytes gives its size, 0
+ * where none is used.  It is device memory, 256-byte aligned, overwritten; calls
+ * sharing it must not overlap.  Errors as qmm_matmul, with the dtypes of out, mul
+ * and residual beside A's, a stride below N, an unknown act or a misaligned operand
+ * as QMM_ERR_BAD_ARG, and last a short workspace as QMM_ERR_WORKSPACE. */
 int qmm_matmul_ep(int kind, const void *W, const void *A, int a_dtype, const qmm_epilogue *ep, void *out,
-                  int out_dtype, int64_t out_stride, int64_t M, int64_t N, int64_t K, void *stream);
-/* qmm_matmul_packed with an epilogue; errors as both. */
+                  int out_dtype, int64_t out_stride, int64_t M, int64_t N, int64_t K, void *workspace,
+                  size_t workspace_bytes, void *stream);
+/* qmm_matmul_packed with an epilogue and that workspace, at any M for every kind
+ * (those that qmm_matmul_packed's GEMM does not take go through the workspace);
+ * errors as both. */
 int qmm_matmul_packed_ep(int kind, const void *P, const void *A, int a_dtype, const qmm_epilogue *ep, void *out,
-                         int out_dtype, int64_t out_stride, int64_t M, int64_t N, int64_t K, void *stream);
+                         int out_dtype, int64_t out_stride, int64_t M, int64_t N, int64_t K, void *workspace,
+                         size_t workspace_bytes, void *stream);
+/* Bytes of workspace of qmm_matmul_ep (packed 0) and qmm_matmul_packed_ep (packed
+ * 1) on the current device; 0 also for shapes, kinds and dtypes that they refuse. */
+size_t qmm_matmul_ep_workspace_bytes(int kind, int packed, int64_t M, int64_t N, int64_t K, int a_dtype);
 
 /* The product of qmm_gemv_i8 over activations that are quantized already (by
  * qmm_rmsnorm_q8, for this kind of weights), with an epilogue: codes [M][K]

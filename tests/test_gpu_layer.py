@@ -285,7 +285,6 @@ def test_route_padding_strides_and_places(M):
 
 # -- products with an epilogue ---------------------------------------------------
 KINDS = list(wl.KINDS)
-PACKED_GEMM = ["Q8_0", "Q4_0", "Q5_0", "IQ4_NL", "MXFP4", "IQ4_XS"]
 
 
 def operands(g, M, N, mul, res):
@@ -329,10 +328,6 @@ def test_product_kinds(oracle_mod, kind, M, N, K, a):
 @pytest.mark.parametrize("M,N,K", [(1, 100, 512), (2, 4200, 256), (5, 77, 1024), (8, 333, 768), (9, 64, 512), (70, 200, 1024),
                                    (131, 129, 1280)])
 def test_product_packed_kinds(oracle_mod, kind, M, N, K):
-    if M > 8 and kind not in PACKED_GEMM:
-        with pytest.raises(qmm.QmmError):
-            run_product(oracle_mod, kind, M, N, K, packed=True)
-        return
     run_product(oracle_mod, kind, M, N, K, "f16" if M % 2 else "f32", act="gelu", res="f16", out="f16", packed=True)
 
 
@@ -357,6 +352,38 @@ def test_product_larger(oracle_mod, kind, M, N, K):
     run_product(oracle_mod, kind, M, N, K, res="f32")
 
 
+@pytest.mark.parametrize("a", ["f16", "f32"])
+@pytest.mark.parametrize("kind,packed,M,N,K,decoded", [
+    ("Q6_K", False, 257, 14400, 256, True), ("Q6_K", False, 100, 8200, 256, True), ("Q4_K", False, 2049, 4100, 256, True),
+    ("Q4_0", False, 300, 8000, 96, True), ("Q8_0", False, 70, 61, 32, True), ("Q5_0", False, 1030, 1000, 160, True),
+    ("MXFP4", False, 999, 2000, 512, True), ("IQ4_XS", False, 800, 4000, 256, True), ("Q5_K", True, 200, 8200, 256, True),
+    ("Q3_K", True, 129, 8200, 512, True), ("Q6_K", True, 70, 16500, 256, True), ("Q8_0", True, 600, 3000, 512, True),
+    ("IQ4_NL", True, 600, 2990, 256, True), ("Q2_K", True, 70, 16400, 256, True), ("Q4_K", True, 70, 16400, 512, True),
+    ("Q4_K", False, 130, 4100, 512, False), ("Q8_0", True, 400, 4100, 256, False), ("Q2_K", False, 65, 8200, 256, "f32")])
+def test_product_ways(oracle_mod, kind, packed, M, N, K, a, decoded):
+    """Weights decoded once (in every tile and stage size, from rows and from records) and as they are multiplied."""
+    assert (qmm.qmm_matmul_ep_workspace_bytes(kind, M, N, K, TT[a], packed) > 0) == (decoded in (True, a))
+    run_product(oracle_mod, kind, M, N, K, a, act="silu", mul="f16", res="f32", out="f16" if M % 2 else "f32", packed=packed)
+
+
+def test_product_workspace_of_the_caller(oracle_mod):
+    """A workspace of the caller's, with what lies behind it left alone; a short one is refused."""
+    M, N, K = 300, 8000, 96
+    g = wl.rng("product", "workspace")
+    W, A = dev(wl.random_weights("Q4_0", N, K, g)), dev(wl.activations((M, K), np.float32, g))
+    need = qmm.qmm_matmul_ep_workspace_bytes("Q4_0", M, N, K, torch.float32)
+    assert need == -(-N * K * 2 // 256) * 256 + M * K * 4
+    buf = torch.full((need + 256,), 77, dtype=torch.uint8, device="cuda")
+    got = qmm.matmul_ep("Q4_0", W, A, N, workspace=buf[:need])
+    assert torch.equal(got, qmm.matmul_ep("Q4_0", W, A, N)) and (buf[need:] == 77).all()
+    with pytest.raises(qmm.QmmError, match="workspace"):
+        qmm.matmul_ep("Q4_0", W, A, N, workspace=buf[:need - 1])
+    with pytest.raises(qmm.QmmError, match="workspace"):
+        qmm.matmul_ep("Q4_0", W, A, N, workspace=buf[1:])
+    with pytest.raises(qmm.QmmError, match="16-byte"):
+        qmm.matmul_ep("Q4_0", W, torch.cat((A.reshape(-1), A.new_zeros(1)))[1:].reshape(M, K), N)
+
+
 def exact_product(M, N, K, seed):
     """Q8_0 weights of scale 2^-6 with small codes and small whole activations: every sum is exact in f32, and every
     weight in f16."""
@@ -370,10 +397,11 @@ def exact_product(M, N, K, seed):
 
 
 @pytest.mark.parametrize("act", layer.ACTS)
-@pytest.mark.parametrize("M,packed", [(1, False), (1, True), (5, False), (5, True), (70, False), (70, True)])
-def test_product_epilogue_on_exact_sums(act, M, packed):
+@pytest.mark.parametrize("M,packed,N,K", [(1, False, 130, 512), (1, True, 130, 512), (5, False, 130, 512), (5, True, 130, 512),
+                                          (70, False, 130, 512), (70, True, 130, 512), (33, False, 130, 96), (300, False, 8190, 96),
+                                          (40, False, 16403, 256), (40, True, 16403, 256), (1029, False, 8197, 64)])
+def test_product_epilogue_on_exact_sums(act, M, packed, N, K):
     """The epilogue alone: nothing of the product's own error hides it.  Sums from far below to far above 0."""
-    N, K = 130, 512
     W, A, Y = exact_product(M, N, K, f"{act}{M}")
     g = wl.rng("product", f"exactops{act}{M}")
     b = (np.linspace(-12, 12, N)).astype(np.float32)

@@ -99,7 +99,7 @@ def product(fn, **kw):
     a.update(kw)
     e = None if a["ep"] is None else ctypes.byref(a["ep"])
     return fn(a["kind"], a["W"], a["A"], a["dt"], e, a["out"], a["odt"], a["N"] if a["os"] is None else a["os"], a["M"],
-              a["N"], a["K"], None)
+              a["N"], a["K"], a.get("ws"), a.get("wsb", 0), None)
 
 
 @pytest.mark.parametrize("packed", [False, True])
@@ -119,13 +119,23 @@ def test_product_refusals_in_order(lib, packed):
                 dict(ep=ep(residual=FAKE, residual_stride=0)), dict(ep=ep(residual=FAKE, residual_stride=16, residual_dtype=1)),
                 dict(ep=ep(residual=FAKE, residual_stride=17)), dict(N=1 << 31)):
         assert product(f, **bad) == ARG, bad
+    assert product(f, M=65535 * 64 + 1) == ARG
+    assert product(f, M=9, A=FAKE + 8) == ARG               # more than eight tokens: whole 16-byte pieces
     if packed:
         assert product(f, W=FAKE + 8) == ARG
-        assert product(f, kind=12, M=9) == KIND             # as qmm_matmul_packed
         assert product(f, kind=8, M=1 << 21, K=1024) == ARG
-        assert product(f, kind=8, M=16, N=(1 << 31) // 272 + 16) == ARG
-    else:
-        assert product(f, M=65535 * 64 + 1) == ARG
+        assert product(f, kind=8, M=100, N=(1 << 31) // 272 + 16) == WS  # beyond the GEMM over records: decoded once
+    # The workspace last, where one is used: many tokens, or records that no GEMM multiplies directly.
+    big = dict(kind=12, M=4096, N=4096, K=4096)
+    need = lib.qmm_matmul_ep_workspace_bytes(12, int(packed), 4096, 4096, 4096, 1)
+    assert need == 4096 * 4096 * 2
+    assert lib.qmm_matmul_ep_workspace_bytes(12, int(packed), 4096, 4096, 4096, 0) == need + 4096 * 4096 * 4
+    assert product(f, **big) == WS and product(f, ws=FAKE, wsb=need - 1, **big) == WS
+    assert product(f, ws=FAKE + 128, wsb=need, **big) == WS and product(f, out=None, **big) == ARG
+    for bad in ((12, 9, 0, 16, 256, 1), (12, 9, 16, 16, 257, 1), (3, 4096, 4096, 4096, 4096, 1), (12, 4096, 4096, 4096, 4096, 7),
+                (12, 8, 4096, 4096, 1, 1), (12, 65535 * 64 + 1, 4096, 4096, 256, 1)):
+        k, M, N, K, _, dt = bad
+        assert lib.qmm_matmul_ep_workspace_bytes(k, int(packed), M, N, bad[4], dt) == 0, bad
 
 
 def test_gemv_q8_refusals_in_order(lib):
