@@ -15,18 +15,32 @@
 
 namespace qmm {
 
+// v / (1 + exp(-x)), to about 4 steps of f32 relative, by the hardware's 2^t and
+// reciprocal (one step each).  A GEMM's epilogue overlaps with nothing, so its
+// instructions count: silu(product) * factor, 8192 tokens, 8192 x 4096 Q4_K 573 ->
+// 556 us, 2048 tokens, 14336 x 4096 294 -> 286, against expf and a division.
+// -x log2(e) in two parts, as the rounding of its product alone would be |x| steps
+// of the result; a quarter of the sum, so that its reciprocal is never subnormal:
+// v / 4 loses nothing that silu(v) has.  Past the clamp the exponential is 0 or
+// infinite anyway, which leaves v and -0.
+__device__ __forceinline__ float times_sigmoid(float v, float x) {
+  constexpr float kHi = -1.44269502162933349609375f, kLo = -1.92596299112661746887e-8f, kLn2 = 0.69314718055994531f;
+  x = __builtin_amdgcn_fmed3f(x, -256.f, 256.f);  // a NaN is still one in v
+  const float t = x * kHi;
+  const float rest = fmaf(x, kLo, fmaf(x, kHi, -t));
+  const float quarter = __builtin_amdgcn_exp2f(t) * fmaf(rest, 0.25f * kLn2, 0.25f);
+  return 0.25f * v * __builtin_amdgcn_rcpf(0.25f + quarter);
+}
+
 // f32 activations.  Each is written so that its tail keeps its relative
-// accuracy: v * sigmoid as one quotient (an overflowing exponential gives the
-// limit, -0), gelu through erfc (1 + erf loses everything below -4).
+// accuracy: gelu through erfc (1 + erf loses everything below -4), its tanh form as
+// a sigmoid: (1 + tanh(u)) / 2 = 1 / (1 + exp(-2 u)).
 __device__ __forceinline__ float activated(int act, float v) {
   switch (act) {
     case QMM_ACT_RELU: return v < 0.f ? 0.f : v;  // a NaN stays one
-    case QMM_ACT_SILU: return v / (1.0f + expf(-v));
+    case QMM_ACT_SILU: return times_sigmoid(v, v);
     case QMM_ACT_GELU: return 0.5f * v * erfcf(v * -0.70710678118654752f);
-    case QMM_ACT_GELU_TANH: {
-      const float u = v + 0.044715f * v * v * v;
-      return v / (1.0f + expf(-1.5957691216057308f * u));  // 2 sqrt(2 / pi)
-    }
+    case QMM_ACT_GELU_TANH: return times_sigmoid(v, 1.5957691216057308f * (v + 0.044715f * v * v * v));  // 2 sqrt(2 / pi)
     default: return v;
   }
 }

@@ -21,8 +21,16 @@
 // through LDS and takes eight columns a thread, whole rows a wave.
 //
 // Workgroups are numbered so that each XCD (workgroup i runs on XCD i mod 8)
-// takes a contiguous range of tiles, tokens fastest: the token tiles of one
-// weight tile read it through one L2.
+// takes a contiguous range of tiles, eight token tiles after one another for a
+// weight tile, then the next weight tile: the 32 that an XCD works on at a time read
+// 8 + 4 operand tiles through its L2 (8192 tokens, 8192 x 4096 Q4_K, no
+// activation: 497 us; all token tiles after one another 535).
+//
+// Bound (2048 tokens, 8192 x 4096: 118 us in one round of tiles): the matrix
+// instructions fill 58% of its cycles, at the 1.6 to 1.9 GHz that the power leaves
+// (activations of zeros take 20% less time, a library's f16 product 12% less).
+// Measured and left: five rings, fewer waves with 128 x 128 each, 32 x 32 matrix
+// tiles and 256 x 224 tiles all took as long or longer.
 #include "qmm_device.h"
 #include "qmm_epilogue.h"
 #include "qmm_internal.h"
@@ -108,6 +116,7 @@ __global__ __launch_bounds__(256) void split_kernel(const float *__restrict__ A,
 constexpr int kRsrcWord3 = 0x00020000;  // buffer descriptor word 3 (raw 32-bit data)
 constexpr int vmcnt_imm(int n) { return (n & 15) | ((n >> 4) << 14) | 0x0F70; }
 constexpr int kRing = 4;
+constexpr int kGroup = 8;  // token tiles that share weight tiles, one after another
 
 __device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t r, uint8_t *lds, int voff, int soff) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)lds, 16, voff, soff, 0, 0);
@@ -180,10 +189,10 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void gemm_kernel(const _Float16 *_
                                                                int M, int N, int K, int planes, int tiles_m) {
   constexpr int BM = 16 * WM * TM, BN = 16 * WN * TN, NW = WM * WN;
   constexpr int RB = BK * 2, CPR = RB / 16, RPL = 64 / CPR;  // bytes and chunks of a row, rows of a wave's load
+  constexpr int kLoadsA = BM / RPL / NW, kLoadsW = BN / RPL / NW, kLoads = kLoadsA + kLoadsW;  // a wave's, a stage
   constexpr int kBytes = (BM + BN) * RB;                     // of a ring
-  constexpr int kLoads = (BM + BN) / RPL / NW;               // a wave's loads of a stage
   constexpr int KS = BK / 32;
-  static_assert((BM + BN) / RPL % NW == 0 && BM % RPL == 0, "loads split evenly, each of one operand");
+  static_assert(BM % (RPL * NW) == 0 && BN % (RPL * NW) == 0, "as many loads of either operand for every wave");
   // Where chunk c of row r lies: c ^ key(r), so that a fragment read's 16 rows
   // fall on all banks.
   auto key = [](int r) { return CPR >= 8 ? r & 7 : (r >> 1) & 3; };
@@ -197,31 +206,36 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void gemm_kernel(const _Float16 *_
   const int T = gridDim.x, L = blockIdx.x;
   const int xcd = L & 7, jx = L >> 3, q8 = T >> 3, r8 = T & 7;
   const int V = xcd < r8 ? xcd * (q8 + 1) + jx : r8 * (q8 + 1) + (xcd - r8) * q8 + jx;
-  const int m0 = V % tiles_m * BM, n0 = V / tiles_m * BN;
+  const int wide = kGroup * ((N + BN - 1) / BN), g0 = V / wide * kGroup, tall = min(kGroup, tiles_m - g0);
+  const int m0 = (g0 + V % wide % tall) * BM, n0 = V % wide / tall * BN;
 
   // Loads: RPL rows each, lane l row l / CPR's chunk at position l % CPR.
   // Offsets are from the tile's first row; rows past the end read the last one.
   int voff[kLoads];
 #pragma unroll
   for (int i = 0; i < kLoads; ++i) {
-    const int r = (wave * kLoads + i) * RPL + lane / CPR;  // of the BM + BN rows
+    const bool ofA = i < kLoadsA;
+    const int r = (ofA ? wave * kLoadsA + i : wave * kLoadsW + i - kLoadsA) * RPL + lane / CPR;
     const int chunk = lane % CPR ^ key(r);
-    const int row = r < BM ? min(r, M - 1 - m0) : min(r - BM, N - 1 - n0);
-    voff[i] = row * K * 2 + chunk * 16;
+    voff[i] = min(r, ofA ? M - 1 - m0 : N - 1 - n0) * K * 2 + chunk * 16;
   }
-  const int nst1 = K / BK, nst = nst1 * planes;
-  auto load = [&](int t, int u) {
-    t = min(t, nst - 1);
-    const int plane = t >= nst1, k = (t - (plane ? nst1 : 0)) * RB;
-    const __amdgpu_buffer_rsrc_t ars = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<_Float16 *>(A + ((int64_t)plane * M + m0) * K), 0, 0x7FFFFFFF, kRsrcWord3);
-    const __amdgpu_buffer_rsrc_t wrs =
-        __builtin_amdgcn_make_buffer_rsrc(const_cast<_Float16 *>(W + (int64_t)n0 * K), 0, 0x7FFFFFFF, kRsrcWord3);
+  const int nst = K / BK * planes;
+  // The next load's plane and bytes into its rows; past the last stage it stays there.
+  const _Float16 *plane = A + (int64_t)m0 * K;
+  int at = 0, left = planes - 1;
+  const __amdgpu_buffer_rsrc_t wrs =
+      __builtin_amdgcn_make_buffer_rsrc(const_cast<_Float16 *>(W + (int64_t)n0 * K), 0, 0x7FFFFFFF, kRsrcWord3);
+  auto load = [&](int u) {
+    const __amdgpu_buffer_rsrc_t ars = __builtin_amdgcn_make_buffer_rsrc(const_cast<_Float16 *>(plane), 0, 0x7FFFFFFF, kRsrcWord3);
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      const int x = wave * kLoads + i;
-      dma16(x < BM / RPL ? ars : wrs, ring(u) + 1024 * x, voff[i], k);
+      const bool ofA = i < kLoadsA;
+      dma16(ofA ? ars : wrs, ring(u) + 1024 * (ofA ? wave * kLoadsA + i : BM / RPL + wave * kLoadsW + i - kLoadsA), voff[i], at);
     }
+    const bool end = at + RB == 2 * K, more = end && left > 0;
+    at = more ? 0 : end ? at : at + RB;
+    plane += more ? (int64_t)M * K : 0;
+    left -= more;
   };
 
   int frag[KS];
@@ -258,7 +272,7 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void gemm_kernel(const _Float16 *_
   // Stage t at ring u = t mod 4: its fragments are in registers p.
   auto stage = [&](int t, int u, int p) {
     arrive(1);                       // stage t + 1 is there; every wave has multiplied stage t - 1
-    load(t + 3, (u + 3) % kRing);    // over stage t - 1
+    load((u + 3) % kRing);           // stage t + 3, over stage t - 1
     read((u + 1) % kRing, p ^ 1);
 #pragma unroll
     for (int h = 0; h < KS; ++h)
@@ -267,16 +281,20 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void gemm_kernel(const _Float16 *_
 #pragma unroll
         for (int n = 0; n < TN; ++n)
           acc[i][n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w[p][h][n], a[p][h][i], acc[i][n], 0, 0, 0);
-    // A fragment read after every few products.
+    // Products first, as both waves of a SIMD come here at once; then a fragment read
+    // after every few, the loads between them.
+    constexpr int kReads = KS * (TM + TN), kBetween = TM * TN / (TM + TN) > 0 ? TM * TN / (TM + TN) : 1;
+    __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
 #pragma unroll
-    for (int i = 0; i < KS * (TM + TN); ++i) {
+    for (int i = 0; i < kReads; ++i) {
       __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(0x008, TM * TN / (TM + TN) > 0 ? TM * TN / (TM + TN) : 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x008, kBetween, 0);
+      if ((i + 1) * kLoads / kReads > i * kLoads / kReads) __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
     }
   };
 
 #pragma unroll
-  for (int s = 0; s < kRing - 1; ++s) load(s, s);
+  for (int s = 0; s < kRing - 1; ++s) load(s);
   arrive(2);
   read(0, 0);
   int t = 0;
@@ -291,37 +309,33 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void gemm_kernel(const _Float16 *_
   __builtin_amdgcn_s_waitcnt(0);
   __syncthreads();
 
-  // The tile through LDS, 16 tokens of every wave (and kCols columns of each) at
-  // a time, so that rows are read and written whole: 16-byte chunk c of row r
-  // (four columns) lies at chunk c ^ (r mod 16), which spreads a wave's writes of
-  // 16 rows over the banks.  Four rings in turn: the barrier before a pass's reads
-  // also ends the reads of three passes before.
-  constexpr int kRows = 16 * WM, kParts = (kRows * BN * 4 + kBytes - 1) / kBytes;
-  constexpr int TP = TN / kParts, kCols = 16 * TP, kWide = WN * kCols;  // a pass's tiles and columns of a wave, of all
-  static_assert(TN % kParts == 0 && kWide % 64 == 0, "whole tiles a pass, whole swizzles a row");
+  // The tile through LDS, 16 tokens of every wave at a time, so that rows are read
+  // and written whole: 16-byte chunk c of row r (four columns) lies at chunk c ^
+  // (r mod 16), which spreads a wave's writes of 16 rows over the banks.  Four rings
+  // in turn: the barrier before a pass's reads also ends the reads of three passes
+  // before.
+  static_assert(16 * WM * BN * 4 <= kBytes && BN % 64 == 0, "a pass fits a ring, whole swizzles a row");
 #pragma unroll 1
-  for (int pass = 0; pass < TM * kParts; ++pass) {
-    const int i = pass / kParts, part = pass % kParts;
+  for (int pass = 0; pass < TM; ++pass) {
     uint8_t *buf = ring(pass % kRing);
     // (Registers are named, not indexed: one branch a pass of this loop.)
 #pragma unroll
-    for (int k = 0; k < TM * kParts; ++k) {
+    for (int k = 0; k < TM; ++k) {
       if (k != pass) continue;
 #pragma unroll
-      for (int n = 0; n < TP; ++n) {
-        const int c = (wn * TP + n) * 4 + G;
-        *reinterpret_cast<floatx4 *>(buf + (wm * 16 + j) * kWide * 4 + 16 * (c ^ j)) = acc[k / kParts][k % kParts * TP + n];
+      for (int n = 0; n < TN; ++n) {
+        const int c = (wn * TN + n) * 4 + G;
+        *reinterpret_cast<floatx4 *>(buf + (wm * 16 + j) * BN * 4 + 16 * (c ^ j)) = acc[k][n];
       }
     }
     __syncthreads();
 #pragma unroll 1
-    for (int x = threadIdx.x; x < kRows * kWide / 8; x += 64 * NW) {
-      const int row = x / (kWide / 8), c = x % (kWide / 8) * 2;
-      const int m = m0 + (row / 16 * TM + i) * 16 + row % 16;
-      const int n = n0 + (4 * c / kCols * TN + part * TP) * 16 + 4 * c % kCols;
+    for (int x = threadIdx.x; x < 16 * WM * BN / 8; x += 64 * NW) {
+      const int row = x / (BN / 8), c = x % (BN / 8) * 2;
+      const int m = m0 + (row / 16 * TM + pass) * 16 + row % 16, n = n0 + 4 * c;
       if (m >= M || n >= N) continue;
-      const floatx4 lo = *reinterpret_cast<const floatx4 *>(buf + row * kWide * 4 + 16 * (c ^ (row & 15)));
-      const floatx4 hi = *reinterpret_cast<const floatx4 *>(buf + row * kWide * 4 + 16 * ((c + 1) ^ (row & 15)));
+      const floatx4 lo = *reinterpret_cast<const floatx4 *>(buf + row * BN * 4 + 16 * (c ^ (row & 15)));
+      const floatx4 hi = *reinterpret_cast<const floatx4 *>(buf + row * BN * 4 + 16 * ((c + 1) ^ (row & 15)));
       float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
       put8(C, m, n, N, v);
     }
