@@ -6,9 +6,10 @@
 // tokens.  Nearly all of the work is done in f32 all the same: f32 values
 // bring out topk + 2 candidates, whose scores are computed in 64 bits (their
 // weights need those anyway), and whose order is corrected where neighbours lie
-// within the f32 values' error.  Where that leaves a doubt about which experts
-// belong among the candidates (rows of many equal scores, sums of groups within
-// 2^-19), the row is done again in 64 bits throughout.
+// within the f32 values' error.  Groups whose f32 sums lie within 2^-19 are told
+// apart by the 64-bit scores of their largest experts.  Where a doubt is left about
+// which experts belong among the candidates (rows of many equal scores), the row is
+// done again in 64 bits throughout.
 //
 // Candidates.  L = 16 or 64 lanes take a row, each up to EPL experts in
 // registers.  An expert's key is a 32-bit whole number: its value's bits, made
@@ -19,8 +20,10 @@
 // range, the nearest one highest): one subtraction and half a max3 an expert and
 // a round, no compares, no removal.
 //
-// Bound.  16384 tokens of 256 experts are 17.9 MB; the arithmetic is about 30
-// instructions an expert, the selection two thirds of them.
+// Bound.  16384 tokens of 256 experts (eight groups, a bias) are 17.9 MB, 3.5 us of
+// memory time; the kernel takes 11.2 us, 5 of them the launch and one wave's chain
+// of dependent steps (2049 tokens take 6.7), the rest the arithmetic: 950 instructions
+// a wave of four rows, a third of them the selection's rounds.
 #include <math.h>
 
 #include "qmm_internal.h"
@@ -243,6 +246,57 @@ struct Split : Route {
   int size, log_per;
 };
 
+// An expert's score with its bias, in 64 bits.
+template <int MODE>
+__device__ __forceinline__ double score(const Route &r, float l, int e, float top, double total) {
+  return (MODE == kSigmoid ? sigmoid(l) : above(l, top) / total) + (r.bias ? (double)r.bias[e] : 0.0);
+}
+
+// The two largest values over the `per` lanes of a group, from each lane's.
+__device__ __forceinline__ float larger(float a, float b) { return fmaxf(a, b); }
+__device__ __forceinline__ double larger(double a, double b) { return a > b ? a : b; }
+__device__ __forceinline__ float smaller(float a, float b) { return fminf(a, b); }
+__device__ __forceinline__ double smaller(double a, double b) { return a > b ? b : a; }
+__device__ __forceinline__ float from(float v, int by) { return __shfl_xor(v, by); }
+__device__ __forceinline__ double from(double v, int by) { return shfl_xor(v, by); }
+template <int L, typename T>
+__device__ __forceinline__ void join_groups(int per, T &a, T &b) {
+  auto join = [&](T oa, T ob) {
+    b = larger(smaller(a, oa), larger(b, ob));
+    a = larger(a, oa);
+  };
+  if (per >= 2) join(dpp<0xB1>(a), dpp<0xB1>(b));
+  if (per >= 4) join(dpp<0x4E>(a), dpp<0x4E>(b));
+  if (per >= 8) join(dpp<0x141>(a), dpp<0x141>(b));
+  if (per >= 16) join(dpp<0x140>(a), dpp<0x140>(b));
+  if (L == 64 && per >= 32) join(from(a, 16), from(b, 16));
+}
+
+// Groups of larger values than this lane's, or of equal ones and before it.
+template <int L, typename T>
+__device__ __forceinline__ int groups_before(T value, int q, int g, int log_per, int G) {
+  int before = 0;
+  if constexpr (L == 16) {
+    // The same lane of every other group, by turns of the row.
+    const int per = 1 << log_per, mine = g << log_per;  // lanes below belong to earlier groups
+    auto seen = [&](T other, int n) {
+      const bool earlier = ((q - n) & 15) < mine;
+      before += (int)(other > value) | ((int)(other == value) & (int)earlier);
+    };
+#define QMM_TURN(n) \
+  if ((n & (per - 1)) == 0) seen(dpp<0x120 + n>(value), n);
+    QMM_TURN(1) QMM_TURN(2) QMM_TURN(3) QMM_TURN(4) QMM_TURN(5) QMM_TURN(6) QMM_TURN(7) QMM_TURN(8) QMM_TURN(9)
+    QMM_TURN(10) QMM_TURN(11) QMM_TURN(12) QMM_TURN(13) QMM_TURN(14) QMM_TURN(15)
+#undef QMM_TURN
+  } else {
+    for (int h = 0; h < G; ++h) {
+      const T other = lane_of(value, h << log_per);
+      before += other > value || (other == value && h < g);
+    }
+  }
+  return before;
+}
+
 template <int L, int EPL, int MODE, bool F16>
 __global__ __launch_bounds__(64 * kWaves) void route_kernel(const Split r) {
   constexpr int BITS = log2_of(L * EPL);
@@ -329,7 +383,6 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(const Split r) {
     c[i] = v > -INFINITY && s > -INFINITY ? s : -INFINITY;  // NaN of either: never chosen
   }
 
-  bool doubt = false;
   if (G > 1) {
     // The group's value, on each of its lanes.
     float a = -INFINITY, b2 = -INFINITY;  // the two largest
@@ -338,43 +391,38 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(const Split r) {
       b2 = __builtin_amdgcn_fmed3f(a, b2, c[i]);
       a = __builtin_amdgcn_fmed3f(a, c[i], INFINITY);
     }
-    auto join = [&](float oa, float ob) {
-      b2 = fmaxf(fminf(a, oa), fmaxf(b2, ob));
-      a = fmaxf(a, oa);
-    };
-    if (per >= 2) join(dpp<0xB1>(a), dpp<0xB1>(b2));
-    if (per >= 4) join(dpp<0x4E>(a), dpp<0x4E>(b2));
-    if (per >= 8) join(dpp<0x141>(a), dpp<0x141>(b2));
-    if (per >= 16) join(dpp<0x140>(a), dpp<0x140>(b2));
-    if (per >= 32) join(__shfl_xor(a, 16), __shfl_xor(b2, 16));
+    join_groups<L>(per, a, b2);
     const float value = r.group_top == 2 && b2 > -INFINITY ? a + b2 : a;
-    // Groups before this one.
-    int before = 0;
-    if constexpr (L == 16) {
-      // The same lane of every other group, by turns of the row.
-      const int mine = g << log_per;  // lanes below belong to earlier groups
-      auto seen = [&](float other, int n) {
-        const bool earlier = ((q - n) & 15) < mine;
-        before += (int)(other > value) | ((int)(other == value) & (int)earlier);
-      };
-#define QMM_TURN(n) \
-  if ((n & (per - 1)) == 0) seen(dpp<0x120 + n>(value), n);
-      QMM_TURN(1) QMM_TURN(2) QMM_TURN(3) QMM_TURN(4) QMM_TURN(5) QMM_TURN(6) QMM_TURN(7) QMM_TURN(8) QMM_TURN(9)
-      QMM_TURN(10) QMM_TURN(11) QMM_TURN(12) QMM_TURN(13) QMM_TURN(14) QMM_TURN(15)
-#undef QMM_TURN
-    } else {
-      for (int h = 0; h < G; ++h) {
-        const float other = lane_of(value, h * per);
-        before += other > value || (other == value && h < g);
-      }
-    }
-    const bool kept = before < (int)r.topk_group;
+    bool kept = groups_before<L>(value, q, g, log_per, G) < (int)r.topk_group;
     if constexpr (MODE == kSigmoid || MODE == kSoftmax) {
       // How far the kept ones are above the others.
       const float in = row_min<L>(kept ? value : INFINITY), out = row_max<L>(kept ? -INFINITY : value);
       // What the sums round off goes by their terms.
       const float terms = row_max<L>(a > -INFINITY ? fabsf(a) + (b2 > -INFINITY ? fabsf(b2) : 0.f) : 0.f);
-      if (out > -INFINITY) doubt = !(in - out > 0x1p-19f + 0x1p-21f * terms);
+      const bool near = out > -INFINITY && !(in - out > 0x1p-19f + 0x1p-21f * terms);
+      if (__any(near)) {
+        // The groups by 64-bit values, of the experts that may be among their two
+        // (or one) largest.  One row of every few thousand, but the call waits for it:
+        // 16384 tokens of 256 experts 11.2 us, 20 with such rows done again as a whole.
+        const float least = r.group_top == 2 ? b2 : a;
+        uint32_t in_question = 0;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+          if (c[i] > -INFINITY && !(c[i] < least - slack(MODE, least) - slack(MODE, c[i]))) in_question |= 1u << i;
+        double da = -INFINITY, db = -INFINITY;
+        while (__any(in_question != 0)) {
+          if (in_question) {
+            const int i = __builtin_ctz(in_question);
+            in_question &= in_question - 1;
+            const int e = g * size + (i / UNIT * per + sub) * UNIT + i % UNIT;
+            const double v = score<MODE>(r, logit_of<F16>(r, row * r.stride + e), e, top, total);
+            if (v > da) db = da, da = v;
+            else if (v > db) db = v;
+          }
+        }
+        join_groups<L>(per, da, db);
+        kept = groups_before<L>(r.group_top == 2 && db > -INFINITY ? da + db : da, q, g, log_per, G) < (int)r.topk_group;
+      }
     }
 #pragma unroll
     for (int i = 0; i < EPL; ++i) c[i] = kept ? c[i] : -INFINITY;
@@ -419,7 +467,6 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(const Split r) {
     if (id0 >= 0 && q < k) close = near(next);
     if (id0 >= 0 && q == k - 1) open = near(over);
   }
-  doubt = doubt || open;
 
   // The candidates' scores in 64 bits.
   const float cl = id0 >= 0 ? logit_of<F16>(r, row * r.stride + id0) : -INFINITY;
@@ -427,8 +474,7 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(const Split r) {
   if (__any(close)) {
     double exact = -INFINITY;
     if (id0 >= 0) {
-      if constexpr (MODE == kSigmoid) exact = sigmoid(cl) + (r.bias ? (double)r.bias[id0] : 0.0);
-      else if constexpr (MODE == kSoftmax) exact = above(cl, top) / total + (r.bias ? (double)r.bias[id0] : 0.0);
+      if constexpr (kBias) exact = score<MODE>(r, cl, id0, top, total);
       else exact = cl;
     }
     int before = 0;
@@ -446,7 +492,7 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(const Split r) {
     r.weights[row * k + slot] = w * r.scale;
   }
   // Rows in doubt again, one at a time.
-  uint64_t again = __ballot(doubt && live);
+  uint64_t again = __ballot(open && live);
   while (again) {
     const int at = __builtin_ctzll(again);
     again &= L == 64 ? 0ull : ~(((1ull << (L % 64)) - 1) << (at / L * L));
