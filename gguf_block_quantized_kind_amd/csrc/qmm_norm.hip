@@ -18,6 +18,7 @@
 // to f16: 470 MB, 84 us; a large copy's rate); few rows by the launch and one
 // workgroup's chain of load, sum, factor and store (3.4 us, 4.0 to 8 bits).
 #include "qmm_internal.h"
+#include "qmm_lanes.h"
 
 namespace qmm {
 namespace norm {
@@ -30,8 +31,9 @@ constexpr int V = 8;  // elements of a piece
 constexpr int64_t kGridX = 1 << 20;
 
 // Elements [at, at + 8) of a row of D (those past its end read as 0).
-__device__ __forceinline__ void load8(const void *p, int f16, int64_t at, int left, float (&v)[V]) {
-  if (left >= V) {
+// full: the same on all lanes, and then left is not looked at.
+__device__ __forceinline__ void load8(const void *p, int f16, int64_t at, bool full, int left, float (&v)[V]) {
+  if (full || left >= V) {
     if (f16) {
       half8 h;
       __builtin_memcpy(&h, static_cast<const _Float16 *>(p) + at, sizeof h);
@@ -47,8 +49,8 @@ __device__ __forceinline__ void load8(const void *p, int f16, int64_t at, int le
   }
 }
 
-__device__ __forceinline__ void store8(void *p, int f16, int64_t at, int left, const float (&v)[V]) {
-  if (left >= V) {
+__device__ __forceinline__ void store8(void *p, int f16, int64_t at, bool full, int left, const float (&v)[V]) {
+  if (full || left >= V) {
     if (f16) {
       half8 h;
 #pragma unroll
@@ -67,25 +69,29 @@ __device__ __forceinline__ void store8(void *p, int f16, int64_t at, int left, c
   }
 }
 
-__device__ __forceinline__ double shfl_xor(double v, int m, int width) {
-  const int2 a = __builtin_bit_cast(int2, v);
-  return __builtin_bit_cast(double, int2{__shfl_xor(a.x, m, width), __shfl_xor(a.y, m, width)});
-}
+// A call and what divides a row's number into a token and a head (by 0: a division).
+struct Split : Norm {
+  uint32_t by;
+  int shift;
+};
 
 // R threads a row (8 to 64: 256 / R rows a workgroup; above: the workgroup's
 // one row), NP pieces a thread, Q8: to 8 bits.
 template <int R, int NP, bool Q8>
-__global__ __launch_bounds__(R > 256 ? R : 256) void rmsnorm_kernel(const Norm n) {
+__global__ __launch_bounds__(R > 256 ? R : 256) void rmsnorm_kernel(const Split n) {
   constexpr int kThreads = R > 256 ? R : 256;
   const int r = threadIdx.x % R;
   const int64_t row = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * (kThreads / R) + threadIdx.x / R;
   const int D = (int)n.D;
   const bool live = row < n.T * n.H;
-  const int64_t t = live ? row / n.H : 0, head = live ? (row - t * n.H) * D : 0;
+  const int64_t at = live ? row : 0;
+  const int64_t t = n.by ? (int64_t)((uint64_t)(uint32_t)at * n.by >> n.shift) : at / n.H;
+  const int64_t head = (at - t * n.H) * D;
 
+  const bool full = D == V * R * NP;
   float h[NP][V], w[NP][V];
 #pragma unroll
-  for (int i = 0; i < NP; ++i) load8(n.x, n.x_f16, t * n.x_stride + head + V * (r + i * R), D - V * (r + i * R), h[i]);
+  for (int i = 0; i < NP; ++i) load8(n.x, n.x_f16, t * n.x_stride + head + V * (r + i * R), full, D - V * (r + i * R), h[i]);
   // (Four pieces a thread leave no registers for residual and weight beside
   // them: a piece's residual is added as it comes, the weight is loaded with the
   // factor known.)
@@ -95,7 +101,7 @@ __global__ __launch_bounds__(R > 256 ? R : 256) void rmsnorm_kernel(const Norm n
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
       float(&b)[V] = a[kLate ? 0 : i];
-      load8(n.residual, n.residual_f16, t * n.residual_stride + head + V * (r + i * R), D - V * (r + i * R), b);
+      load8(n.residual, n.residual_f16, t * n.residual_stride + head + V * (r + i * R), full, D - V * (r + i * R), b);
       if constexpr (kLate) {
 #pragma unroll
         for (int e = 0; e < V; ++e) h[i][e] += b[e];
@@ -113,7 +119,7 @@ __global__ __launch_bounds__(R > 256 ? R : 256) void rmsnorm_kernel(const Norm n
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
       if (n.weight) {
-        load8(n.weight, 0, V * (r + i * R), D - V * (r + i * R), w[i]);
+        load8(n.weight, 0, V * (r + i * R), full, D - V * (r + i * R), w[i]);
       } else {
 #pragma unroll
         for (int e = 0; e < V; ++e) w[i][e] = 1.f;
@@ -126,8 +132,7 @@ __global__ __launch_bounds__(R > 256 ? R : 256) void rmsnorm_kernel(const Norm n
   for (int i = 0; i < NP; ++i)
 #pragma unroll
     for (int e = 0; e < V; ++e) ss = fma((double)h[i][e], (double)h[i][e], ss);
-#pragma unroll
-  for (int m = (R < 64 ? R : 64) / 2; m >= 1; m >>= 1) ss += shfl_xor(ss, m, 64);
+  ss = reduce<(R < 64 ? R : 64)>(ss, [](double a, double b) { return a + b; });
   if constexpr (R > 64) {
     __shared__ double part[R / 64];
     if (threadIdx.x % 64 == 0) part[threadIdx.x / 64] = ss;
@@ -143,7 +148,7 @@ __global__ __launch_bounds__(R > 256 ? R : 256) void rmsnorm_kernel(const Norm n
   if (n.sum) {
 #pragma unroll
     for (int i = 0; i < NP; ++i)
-      store8(n.sum, n.residual_f16, t * n.sum_stride + head + V * (r + i * R), D - V * (r + i * R), h[i]);
+      store8(n.sum, n.residual_f16, t * n.sum_stride + head + V * (r + i * R), full, D - V * (r + i * R), h[i]);
   }
 #pragma unroll
   for (int i = 0; i < NP; ++i)
@@ -152,7 +157,7 @@ __global__ __launch_bounds__(R > 256 ? R : 256) void rmsnorm_kernel(const Norm n
   if constexpr (!Q8) {
 #pragma unroll
     for (int i = 0; i < NP; ++i)
-      store8(n.y, n.y_f16, t * n.y_stride + head + V * (r + i * R), D - V * (r + i * R), h[i]);
+      store8(n.y, n.y_f16, t * n.y_stride + head + V * (r + i * R), full, D - V * (r + i * R), h[i]);
   } else {
     // A block is the pieces of four neighbouring threads (D is a multiple of
     // 32, so they are all there or none is).
@@ -164,8 +169,8 @@ __global__ __launch_bounds__(R > 256 ? R : 256) void rmsnorm_kernel(const Norm n
       uint32_t top = 0;
 #pragma unroll
       for (int e = 0; e < V; ++e) top = max(top, __float_as_uint(h[i][e]) & 0x7FFFFFFFu);
-      top = max(top, (uint32_t)__shfl_xor((int)top, 1, 64));
-      top = max(top, (uint32_t)__shfl_xor((int)top, 2, 64));
+      top = max(top, dpp<0xB1>(top));
+      top = max(top, dpp<0x4E>(top));
       const float amax = top >= 0x7F800000u ? __builtin_nanf("") : __uint_as_float(top);
       const float d = amax / 127.0f;
       int c[V], sum = 0;
@@ -175,8 +180,8 @@ __global__ __launch_bounds__(R > 256 ? R : 256) void rmsnorm_kernel(const Norm n
         c[e] = (int)__builtin_rintf(q);
         sum += c[e];
       }
-      sum += __shfl_xor(sum, 1, 64);
-      sum += __shfl_xor(sum, 2, 64);
+      sum += (int)dpp<0xB1>((uint32_t)sum);
+      sum += (int)dpp<0x4E>((uint32_t)sum);
       if (V * p >= D) continue;
       uint32_t b[2];
 #pragma unroll
@@ -204,9 +209,18 @@ __global__ __launch_bounds__(R > 256 ? R : 256) void rmsnorm_kernel(const Norm n
 }
 
 template <int R, int NP>
-hipError_t run(const Norm &n, hipStream_t s) {
+hipError_t run(const Norm &call, hipStream_t s) {
   constexpr int kThreads = R > 256 ? R : 256;
-  const int64_t rows = n.T * n.H, per = kThreads / R;
+  const int64_t rows = call.T * call.H, per = kThreads / R;
+  // row / H = row * by >> shift for rows below 2^31, with by = 2^shift / H rounded up
+  // beyond an exact one: by H is less than 2^shift + 2^(shift - 31) (H <= 2^(shift - 31)).
+  Split n;
+  static_cast<Norm &>(n) = call;
+  n.by = 0, n.shift = 31;
+  if (rows < (int64_t)1 << 31) {
+    while ((int64_t)1 << (n.shift - 31) < n.H) ++n.shift;
+    n.by = (uint32_t)(((uint64_t)1 << n.shift) / (uint64_t)n.H + 1);
+  }
   const int64_t groups = (rows + per - 1) / per, wide = groups < kGridX ? groups : kGridX;
   const dim3 grid((unsigned)wide, (unsigned)((groups + wide - 1) / wide)), block(kThreads);
   if (n.q8) hipLaunchKernelGGL((rmsnorm_kernel<R, NP, true>), grid, block, 0, s, n);

@@ -27,14 +27,11 @@
 #include <math.h>
 
 #include "qmm_internal.h"
+#include "qmm_lanes.h"
 
 namespace qmm {
 namespace route {
 
-__device__ __forceinline__ double shfl_xor(double v, int m) {
-  const int2 a = __builtin_bit_cast(int2, v);
-  return __builtin_bit_cast(double, int2{__shfl_xor(a.x, m), __shfl_xor(a.y, m)});
-}
 __device__ __forceinline__ double shfl(double v, int lane) {
   const int2 a = __builtin_bit_cast(int2, v);
   return __builtin_bit_cast(double, int2{__shfl(a.x, lane), __shfl(a.y, lane)});
@@ -64,35 +61,6 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// Reductions over the L = 16 or 64 lanes of a row, the result on each of them.
-// Within a DPP row of 16: neighbours, pairs (quad_perm), the two quads (half
-// mirror), the two halves (mirror); its four through scalars.
-template <int CTRL>
-__device__ __forceinline__ uint32_t dpp(uint32_t v) {
-  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, true);  // every source lane is there
-}
-template <int CTRL>
-__device__ __forceinline__ float dpp(float v) { return __uint_as_float(dpp<CTRL>(__float_as_uint(v))); }
-template <int CTRL>
-__device__ __forceinline__ double dpp(double v) {
-  const uint2 a = __builtin_bit_cast(uint2, v);
-  return __builtin_bit_cast(double, uint2{dpp<CTRL>(a.x), dpp<CTRL>(a.y)});
-}
-__device__ __forceinline__ uint32_t lane_of(uint32_t v, int i) { return __builtin_amdgcn_readlane(v, i); }
-__device__ __forceinline__ float lane_of(float v, int i) { return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), i)); }
-__device__ __forceinline__ double lane_of(double v, int i) {
-  const uint2 a = __builtin_bit_cast(uint2, v);
-  return __builtin_bit_cast(double, uint2{(uint32_t)__builtin_amdgcn_readlane(a.x, i), (uint32_t)__builtin_amdgcn_readlane(a.y, i)});
-}
-template <int L, typename T, typename F>
-__device__ __forceinline__ T reduce(T v, F f) {
-  v = f(v, dpp<0xB1>(v));
-  v = f(v, dpp<0x4E>(v));
-  v = f(v, dpp<0x141>(v));
-  v = f(v, dpp<0x140>(v));
-  if constexpr (L == 64) v = f(f(lane_of(v, 0), lane_of(v, 16)), f(lane_of(v, 32), lane_of(v, 48)));
-  return v;
-}
 template <int L>
 __device__ __forceinline__ float row_max(float v) { return reduce<L>(v, [](float a, float b) { return fmaxf(a, b); }); }
 template <int L>
@@ -257,8 +225,6 @@ __device__ __forceinline__ float larger(float a, float b) { return fmaxf(a, b); 
 __device__ __forceinline__ double larger(double a, double b) { return a > b ? a : b; }
 __device__ __forceinline__ float smaller(float a, float b) { return fminf(a, b); }
 __device__ __forceinline__ double smaller(double a, double b) { return a > b ? b : a; }
-__device__ __forceinline__ float from(float v, int by) { return __shfl_xor(v, by); }
-__device__ __forceinline__ double from(double v, int by) { return shfl_xor(v, by); }
 template <int L, typename T>
 __device__ __forceinline__ void join_groups(int per, T &a, T &b) {
   auto join = [&](T oa, T ob) {
@@ -269,7 +235,7 @@ __device__ __forceinline__ void join_groups(int per, T &a, T &b) {
   if (per >= 4) join(dpp<0x4E>(a), dpp<0x4E>(b));
   if (per >= 8) join(dpp<0x141>(a), dpp<0x141>(b));
   if (per >= 16) join(dpp<0x140>(a), dpp<0x140>(b));
-  if (L == 64 && per >= 32) join(from(a, 16), from(b, 16));
+  if (L == 64 && per >= 32) join(shfl_xor(a, 16), shfl_xor(b, 16));
 }
 
 // Groups of larger values than this lane's, or of equal ones and before it.
