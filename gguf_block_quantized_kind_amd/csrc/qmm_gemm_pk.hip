@@ -467,6 +467,29 @@ __global__ __launch_bounds__(64 * KQ * NH, 1) void gemm_pk_kernel(const uint8_t 
     frags((u + 1) % kRing, 0, a0hi, a0lo);
   };
 
+  // Stage u of that last k-block, which starts at stage t.  Its first stage issues
+  // the only loads that are left, and the waits count no others: weight loads
+  // whose values nothing uses are dropped by the compiler, and a wait that counted
+  // them would let the next stage's activations be read before they are in LDS.
+  auto last = [&](int u, int t) {
+    if (u == 0) load(t + kRing - 1, kRing - 1, 0);
+    __builtin_amdgcn_sched_barrier(0);
+    products(u, 0, 0, a0hi, a0lo);
+    frags(u, 1, a1hi, a1lo);
+    products(u, 0, 1, a1hi, a1lo);
+    if (u == kRing - 1) return;
+    __builtin_amdgcn_sched_barrier(0);
+    constexpr int kNewer[kRing - 1] = {count(2) + count(3), count(3), 0};
+    switch (u) {
+      case 0: __builtin_amdgcn_s_waitcnt(vmcnt_imm(kNewer[0])); break;
+      case 1: __builtin_amdgcn_s_waitcnt(vmcnt_imm(kNewer[1])); break;
+      default: __builtin_amdgcn_s_waitcnt(vmcnt_imm(kNewer[2])); break;
+    }
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    frags(u + 1, 0, a0hi, a0lo);
+  };
+
   // Prologue: stages 0 .. kRing - 2 in flight, stage 0's first fragments.
 #pragma unroll
   for (int s = 0; s < kRing - 1; ++s) load(s, s, 0);
@@ -481,7 +504,7 @@ __global__ __launch_bounds__(64 * KQ * NH, 1) void gemm_pk_kernel(const uint8_t 
   }
   if (t < nst) {
 #pragma unroll
-    for (int u = 0; u < kRing; ++u) stage(t + u, u, 0);
+    for (int u = 0; u < kRing; ++u) last(u, t);
   }
   // The last direct-to-LDS loads may still be landing: wait for every
   // memory operation of this wave before the LDS is reused below.

@@ -416,6 +416,21 @@ def test_product_epilogue_on_exact_sums(act, M, packed, N, K):
         check(host(got), want, tol, f"{act} {out}")
 
 
+@pytest.mark.parametrize("K", [256, 512, 768, 1024, 1280, 2560, 5120])
+@pytest.mark.parametrize("a", ["f16", "f32"])
+@pytest.mark.parametrize("M,N", [(40, 16403), (300, 4101)])
+def test_packed_products_whose_k_parts_have_an_odd_number_of_blocks(M, N, a, K):
+    """Exact sums, so a single activation read before it has arrived shows; the plain product and the one with an
+    epilogue."""
+    W, A, Y = exact_product(M, N, K, f"odd{M}{K}")
+    P, A = qmm.repack("Q8_0", dev(W), N, K), dev(A).to(TT[a])
+    for _ in range(3):
+        C = torch.empty(M, N, device="cuda")
+        qmm.qmm_matmul_packed("Q8_0", P, A, C, M, N, K)
+        assert np.array_equal(host(C), Y)
+        assert np.array_equal(host(qmm.matmul_packed_ep("Q8_0", P, A, N)), Y)
+
+
 @pytest.mark.parametrize("M", [1, 4, 8, 50])
 @pytest.mark.parametrize("dt", ["f16", "f32"])
 def test_product_into_its_operands(oracle_mod, M, dt):
