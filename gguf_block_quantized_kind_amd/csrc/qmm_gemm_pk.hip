@@ -523,6 +523,12 @@ __global__ __launch_bounds__(64 * KQ * NH, 1) void gemm_pk_kernel(const uint8_t 
   static_assert(kRedChunk % VS == 0 && NV % kRedChunk == 0, "reduction rounds");
 #pragma unroll
   for (int c0 = 0; c0 < NV; c0 += kRedChunk) {
+    decltype(operands(C, 0, 0)) around[kRedChunk / VS];
+#pragma unroll
+    for (int r = 0; r < kRedChunk / VS; ++r) {
+      const int v = c0 + wq + VS * r, m = m0 + 16 * ((v >> 2) / TN) + 4 * G + (v & 3), n = n0 + 16 * ((v >> 2) % TN) + j;
+      if (v < NV && m < M && n < N) around[r] = operands(C, m, n);
+    }
     if (c0) __syncthreads();
 #pragma unroll
     for (int v = c0; v < c0 + kRedChunk && v < NV; ++v)
@@ -537,7 +543,7 @@ __global__ __launch_bounds__(64 * KQ * NH, 1) void gemm_pk_kernel(const uint8_t 
         for (int q = 1; q < KQ; ++q) sum += red[((q * NH + wh) * kRedChunk + vl) * 64 + lane];
         const int tm = (v >> 2) / TN, tn = (v >> 2) % TN;
         const int m = m0 + 16 * tm + 4 * G + (v & 3), n = n0 + 16 * tn + j;
-        if (m < M && n < N) put(C, m, n, N, sum);
+        if (m < M && n < N) put(C, m, n, N, sum, around[r]);
       }
     }
   }

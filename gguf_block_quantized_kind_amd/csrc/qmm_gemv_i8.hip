@@ -218,6 +218,12 @@ __global__ __launch_bounds__(64 * S) void gemv_i8_kernel(const uint8_t *__restri
   }
   // Tokens 2G and 2G+1 of row j: both block parities.
   float y0 = acc[0] + acc[1], y1 = acc[2] + acc[3];
+  const int64_t row = tile * 16 + j;
+  decltype(operands(Y, 0, 0)) around0{}, around1{};
+  if (wave == 0 && row < N) {
+    if (2 * G < M) around0 = operands(Y, 2 * G, row);
+    if (2 * G + 1 < M) around1 = operands(Y, 2 * G + 1, row);
+  }
   if constexpr (S > 1) {
     __syncthreads();  // every wave is done with the staged scales
     float *red = reinterpret_cast<float *>(lds);
@@ -233,10 +239,9 @@ __global__ __launch_bounds__(64 * S) void gemv_i8_kernel(const uint8_t *__restri
       y1 += red[(w * 64 + lane) * 2 + 1];
     }
   }
-  const int64_t row = tile * 16 + j;
   if (row >= N) return;
-  if (2 * G < M) put(Y, 2 * G, row, N, y0);
-  if (2 * G + 1 < M) put(Y, 2 * G + 1, row, N, y1);
+  if (2 * G < M) put(Y, 2 * G, row, N, y0, around0);
+  if (2 * G + 1 < M) put(Y, 2 * G + 1, row, N, y1, around1);
 }
 
 template <int KIND, int S, int PD>

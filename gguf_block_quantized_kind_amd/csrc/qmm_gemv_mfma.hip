@@ -263,6 +263,15 @@ __global__ __launch_bounds__(64 * S) __attribute__((amdgpu_waves_per_eu(OCC, 8))
     }
   }
 
+  // Lane (j, G) holds D[token 4G + q][row j] of each tile.
+  decltype(operands(Y, 0, 0)) around[R][4] = {};
+  if (!ROUTED && wave == 0) {
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (row0 + 16 * r + j < N && 4 * G + q < M) around[r][q] = operands(Y, tok0 + 4 * G + q, row0 + 16 * r + j);
+  }
   if constexpr (S > 1) {
     __syncthreads();  // every wave is done with its ring
     floatx4 *red = reinterpret_cast<floatx4 *>(lds);
@@ -277,7 +286,6 @@ __global__ __launch_bounds__(64 * S) __attribute__((amdgpu_waves_per_eu(OCC, 8))
 #pragma unroll
       for (int r = 0; r < R; ++r) acc[r] += red[(w * R + r) * 64 + lane];
   }
-  // Lane (j, G) holds D[token 4G + q][row j] of each tile.
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     const int64_t row = row0 + 16 * r + j;
@@ -285,7 +293,7 @@ __global__ __launch_bounds__(64 * S) __attribute__((amdgpu_waves_per_eu(OCC, 8))
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int t = 4 * G + q;
-      if (t < M) put(Y, ROUTED ? pair_of(t) : tok0 + t, row, N, acc[r][q]);
+      if (t < M) put(Y, ROUTED ? pair_of(t) : tok0 + t, row, N, acc[r][q], around[r][q]);
     }
   }
 }

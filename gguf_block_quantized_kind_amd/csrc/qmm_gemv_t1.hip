@@ -150,6 +150,10 @@ __global__ __launch_bounds__(64 * S) __attribute__((amdgpu_waves_per_eu(OCC, 8))
   for (int d = 0; d < NS - 1; ++d)
     if (d < cnt - full) consume(d);
 
+  const int64_t row = tile * 16 + j;
+  const bool mine = wave == 0 && lane < 16 && row < N;
+  decltype(operands(Y, 0, 0)) around{};
+  if (mine) around = operands(Y, out_row, row);
   // Row j's sum is spread over the four lane groups, then over the S waves.
   acc += __shfl_xor(acc, 16);
   acc += __shfl_xor(acc, 32);
@@ -162,8 +166,7 @@ __global__ __launch_bounds__(64 * S) __attribute__((amdgpu_waves_per_eu(OCC, 8))
 #pragma unroll
     for (int w = 0; w < S - 1; ++w) acc += red[w * 16 + (lane & 15)];
   }
-  const int64_t row = tile * 16 + j;
-  if (lane < 16 && row < N) put(Y, out_row, row, N, acc);
+  if (mine) put(Y, out_row, row, N, acc, around);
 }
 
 template <int KIND, int S, int PD, int OCC = 1, bool PACKED = true, bool ROUTED = false>

@@ -226,6 +226,12 @@ __global__ __launch_bounds__(64 * T * S) void gemv_xs_kernel(const uint8_t *__re
   for (int u = 0; u < U - 1; ++u)
     if (u < rounds - full) round(full + u, u);
 
+  decltype(operands(Y, 0, 0)) around[4] = {};
+  if (!ROUTED && kp == 0 && owner && tile * 16 + j < N) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (4 * G + q < M) around[q] = operands(Y, tok0 + 4 * G + q, tile * 16 + j);
+  }
   if constexpr (S > 1) {
     __syncthreads();  // every wave is done with the rings
     floatx4 *red = reinterpret_cast<floatx4 *>(lds);
@@ -242,7 +248,7 @@ __global__ __launch_bounds__(64 * T * S) void gemv_xs_kernel(const uint8_t *__re
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     const int tok = 4 * G + q;
-    if (tok < M) put(Y, ROUTED ? order[c0 + tok] : tok0 + tok, row, N, acc[q]);
+    if (tok < M) put(Y, ROUTED ? order[c0 + tok] : tok0 + tok, row, N, acc[q], around[q]);
   }
 }
 
@@ -286,21 +292,17 @@ static hipError_t run_xs(const uint8_t *P, const void *x, int x_f16, Out y, int 
 }
 
 #ifdef QMM_WITH_EPILOGUE
-// Launch shapes of the products with an epilogue: where there are few tiles the
-// waves of a workgroup split K instead of sharing activations, so that a compute
-// unit has as many weight loads in flight as elsewhere.  One tile a compute unit:
-// 16 waves of K (8 above 16 k-blocks, whose k-blocks in flight fill the unit
-// already); two: two tiles of four.  Eight tokens, 4096 x 14336: Q4_K 30.0 ->
-// 17.3 us, Q6_K 53.0 -> 22.8, repacked Q8_0 27.0 -> 17.9; 4096 x 4096: 12.2 ->
-// 9.1, 19.6 -> 11.7, 10.9 -> 8.7; 8192 x 4096: 12.4 -> 10.6, 19.6 -> 15.4, 12.4 ->
-// 11.6.  (With 688 tiles the shape for many is the fastest: Q6_K 11008 x 4096
-// 21.5 us, 26.9 with two tiles of four.)
+// Launch shapes of the products with an epilogue: where there are few tiles K is
+// split over a workgroup's waves (qmm_gemv_xk.hip); up to two a compute unit, two
+// tiles of four waves.  Eight tokens, 8192 x 4096: Q4_K 12.4 -> 11.3 us; with 688
+// tiles the shape for many is the fastest, Q6_K 11008 x 4096 21.5 us, 26.9 with two
+// tiles of four.
 template <int KIND, int MT, bool PACKED>
 static hipError_t run_xs_mt(const uint8_t *P, const void *x, int x_f16, Out y, int M, int64_t N, int64_t K,
                             hipStream_t s) {
+  const hipError_t e = launch_gemv_xk(KIND, P, PACKED, x, x_f16, y, M, N, K, s);
+  if (e != hipErrorNotSupported) return e;
   const int64_t tiles = (N + 15) / 16, nkb = K / Dec<KIND>::KB;
-  if (tiles <= device_cus() && nkb > 16) return run_xs<KIND, MT, 1, 8, 1, 1, PACKED>(P, x, x_f16, y, M, N, K, s);
-  if (tiles <= device_cus() && nkb > 4) return run_xs<KIND, MT, 1, 16, 1, 1, PACKED>(P, x, x_f16, y, M, N, K, s);
   if (tiles <= 2 * device_cus() && nkb > 4) return run_xs<KIND, MT, 2, 4, 1, 1, PACKED>(P, x, x_f16, y, M, N, K, s);
   return run_xs<KIND, MT, 4, 2, 1, 1, PACKED>(P, x, x_f16, y, M, N, K, s);
 }
