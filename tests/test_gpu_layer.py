@@ -416,6 +416,64 @@ def test_product_epilogue_on_exact_sums(act, M, packed, N, K):
         check(host(got), want, tol, f"{act} {out}")
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("M,N,K", [(2, 100, 1280), (4, 77, 2304), (7, 333, 1536), (8, 50, 8448), (3, 4200, 1536), (5, 9000, 1280)])
+@pytest.mark.parametrize("a,packed", [("f16", False), ("f32", False), ("f16", True), ("f32", True)])
+def test_product_of_few_tokens_over_more_k_blocks(oracle_mod, kind, M, N, K, a, packed):
+    run_product(oracle_mod, kind, M, N, K, a, act="silu", mul="f16", res="f32", out="f16" if M % 2 else "f32", packed=packed)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("offset", [1, 2, 6, 15])
+@pytest.mark.parametrize("M,N,K", [(1, 70, 512), (4, 70, 512), (2, 70, 1280), (8, 4131, 1280), (20, 70, 1280), (90, 70, 512)])
+def test_weights_at_any_address(kind, offset, M, N, K):
+    """The same bytes elsewhere, and other bytes around them: the same results."""
+    g = wl.rng("product", f"address{kind}{offset}{M}")
+    W, A = dev(wl.random_weights(kind, N, K, g)).reshape(-1), dev(wl.activations((M, K), np.float16, g))
+    want = qmm.matmul_ep(kind, W, A, N, act="silu")
+    for fill in (0, 255):
+        buf = torch.full((W.numel() + 32,), fill, dtype=torch.uint8, device="cuda")
+        buf[offset:offset + W.numel()] = W
+        assert torch.equal(qmm.matmul_ep(kind, buf[offset:offset + W.numel()], A, N, act="silu"), want)
+
+
+def far_rows(rows, cols, stride, dt):
+    """[rows, cols] with rows `stride` elements apart."""
+    buf = torch.zeros((rows - 1) * stride + cols, dtype=TT[dt], device="cuda")
+    return buf.as_strided((rows, cols), (stride, 1))
+
+
+def test_offsets_past_32_bits():
+    """Rows whose last one begins beyond 2^31 elements: the results of packed rows."""
+    far = (1 << 31) + 8
+    x, w = torch.randn(2, 96, device="cuda"), torch.randn(96, device="cuda")
+    xs, rs, ys, ss = (far_rows(2, 96, far, dt) for dt in ("f16", "f16", "f16", "f16"))
+    xs.copy_(x)
+    rs.copy_(x.flip(0))
+    y, s = qmm.rmsnorm(xs, w, 1e-6, residual=rs, out=ys, sum_out=ss)
+    y1, s1 = qmm.rmsnorm(xs.contiguous(), w, 1e-6, residual=rs.contiguous())
+    assert torch.equal(ys, y1) and torch.equal(ss, s1) and y is ys and s is ss
+    del rs, ss
+    a, b = qmm.moe_route(xs, 4), qmm.moe_route(xs.contiguous(), 4)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    del xs, ys
+    torch.cuda.empty_cache()
+    g = wl.rng("product", "far")
+    for M in (2, 300):
+        N, K = 96, 512
+        stride = far // (M - 1) + 8
+        W, A = dev(wl.random_weights("Q4_K", N, K, g)), dev(wl.activations((M, K), np.float16, g))
+        mul, res = torch.randn(M, N, device="cuda").half(), torch.randn(M, N, device="cuda").half()
+        want = qmm.matmul_ep("Q4_K", W, A, N, act="silu", mul=mul, residual=res, out_dtype=torch.float16)
+        far_mul, out = far_rows(M, N, stride, "f16"), far_rows(M, N, stride, "f16")
+        far_mul.copy_(mul)
+        out.copy_(res)
+        qmm.matmul_ep("Q4_K", W, A, N, act="silu", mul=far_mul, residual=out, out=out)
+        assert torch.equal(out, want), M
+        del far_mul, out
+        torch.cuda.empty_cache()
+
+
 @pytest.mark.parametrize("K", [256, 512, 768, 1024, 1280, 2560, 5120])
 @pytest.mark.parametrize("a", ["f16", "f32"])
 @pytest.mark.parametrize("M,N", [(40, 16403), (300, 4101)])
