@@ -107,9 +107,11 @@ struct Granules {
   }
 };
 
-// Fragments of a step in LDS, four more than there are: steps would fall on the
-// same banks.
-constexpr int step_of(int MT) { return MT * 4 + 4; }
+// Fragments in LDS: a group's tokens side by side, so that a read of them is one run;
+// groups MT + 1 apart and steps two more than their groups take, so that a write's
+// groups, steps and halves fall on different banks in each decoder's order.
+constexpr int group_of(int MT) { return MT + 1; }
+constexpr int step_of(int MT) { return 4 * group_of(MT) + 2; }
 template <int KIND, int MT, bool PACKED>
 constexpr int wave_bytes() {
   return Dec<KIND>::NSTEP * step_of(MT) * 16 + (PACKED ? 0 : Granules<Dec<KIND>>::kBytes);
@@ -136,8 +138,8 @@ __global__ __launch_bounds__(64 * S) void gemv_xk_kernel(const uint8_t *__restri
   auto bit = [&](int by) { return lane / (by / 4) & 1; };
   const int g2 = bit(Dd::x_off(0, 1, 0)) | bit(Dd::x_off(0, 2, 0)) << 1;
   const int st = bit(Dd::x_off(1, 0, 0)) | bit(Dd::x_off(2, 0, 0)) << 1 | bit(Dd::x_off(4, 0, 0)) << 2;
-  uint8_t *to = own + (st * kStep + g2) * 16 + 8 * bit(Dd::x_off(0, 0, 1));
-  const u32x4 *from = reinterpret_cast<const u32x4 *>(own) + j % MT * 4 + G;
+  uint8_t *to = own + (st * kStep + g2 * group_of(MT)) * 16 + 8 * bit(Dd::x_off(0, 0, 1));
+  const u32x4 *from = reinterpret_cast<const u32x4 *>(own) + G * group_of(MT) + j % MT;
 
   typename std::conditional<PACKED, typename Rec<KIND>::Packed, typename Granules<Dd>::Held>::type raw[2];
   Granules<Dd> gran;
@@ -164,7 +166,7 @@ __global__ __launch_bounds__(64 * S) void gemv_xk_kernel(const uint8_t *__restri
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
       const half2v p0 = {(_Float16)x[i][0], (_Float16)x[i][2]}, p1 = {(_Float16)x[i][1], (_Float16)x[i][3]};
-      *reinterpret_cast<u32x2 *>(to + 64 * i) = u32x2{as_u(p0), as_u(p1)};
+      *reinterpret_cast<u32x2 *>(to + 16 * i) = u32x2{as_u(p0), as_u(p1)};
     }
     if constexpr (!PACKED) gran.store(rows, lane, raw[slot]);
     const int next = min(kb + 1, kb1 - 1);
@@ -275,9 +277,9 @@ static hipError_t run_xk_x(const uint8_t *P, const void *x, int x_f16, const Epi
 //
 // Up to a tile a compute unit: eight waves of K, sixteen up to 32 k-blocks where a
 // wave stays within 128 registers (f16 activations, Q4_K 4096 x 4096 7.4 with eight,
-// 6.8).  4096 x 14336 native Q6_K 23.4 -> 19.3, Q4_K 17.6 -> 14.4, Q5_K 21.6 -> 18.1,
-// repacked Q4_0 13.7 -> 12.0, Q8_0 19.1 -> 17.9; 4096 x 4096 native Q6_K 11.3 -> 9.2,
-// Q4_K 8.9 -> 6.8, Q5_K 10.4 -> 8.4, repacked Q8_0 8.5 -> 7.4, Q4_0 7.3 -> 6.2.
+// 6.7).  4096 x 14336 native Q6_K 23.4 -> 19.1, Q4_K 17.6 -> 13.6, Q5_K 21.6 -> 16.9,
+// repacked Q4_0 13.7 -> 12.1, Q8_0 19.1 -> 18.0; 4096 x 4096 native Q6_K 11.3 -> 9.2,
+// Q4_K 8.9 -> 6.7, Q5_K 10.4 -> 8.1, repacked Q8_0 8.5 -> 7.4, Q4_0 7.3 -> 6.1.
 //
 // More tiles: four waves of K for the native kinds whose fields lie between words.
 // Q6_K 14336 x 4096 23.7 -> 22.2, 32768 x 4096 44.1 -> 40.3; Q3_K 8192 x 4096 13.0 ->

@@ -69,7 +69,7 @@ __device__ __forceinline__ void store8(void *p, int f16, int64_t at, bool full, 
   }
 }
 
-// A call and what divides a row's number into a token and a head (by 0: a division).
+// A call and what divides a row's number into a token and a head.
 struct Split : Norm {
   uint32_t by;
   int shift;
@@ -85,7 +85,7 @@ __global__ __launch_bounds__(R > 256 ? R : 256) void rmsnorm_kernel(const Split 
   const int D = (int)n.D;
   const bool live = row < n.T * n.H;
   const int64_t at = live ? row : 0;
-  const int64_t t = n.by ? (int64_t)((uint64_t)(uint32_t)at * n.by >> n.shift) : at / n.H;
+  const int64_t t = (int64_t)((uint64_t)(uint32_t)at * n.by >> n.shift);
   const int64_t head = (at - t * n.H) * D;
 
   const bool full = D == V * R * NP;
@@ -212,15 +212,14 @@ template <int R, int NP>
 hipError_t run(const Norm &call, hipStream_t s) {
   constexpr int kThreads = R > 256 ? R : 256;
   const int64_t rows = call.T * call.H, per = kThreads / R;
-  // row / H = row * by >> shift for rows below 2^31, with by = 2^shift / H rounded up
-  // beyond an exact one: by H is less than 2^shift + 2^(shift - 31) (H <= 2^(shift - 31)).
+  // row / H = row * by >> shift for rows below 2^31 (there are no more), with by =
+  // 2^shift / H rounded up, beyond an exact one too: by H is at most 2^shift + 2^(shift -
+  // 31), as H is at most 2^(shift - 31).
   Split n;
   static_cast<Norm &>(n) = call;
-  n.by = 0, n.shift = 31;
-  if (rows < (int64_t)1 << 31) {
-    while ((int64_t)1 << (n.shift - 31) < n.H) ++n.shift;
-    n.by = (uint32_t)(((uint64_t)1 << n.shift) / (uint64_t)n.H + 1);
-  }
+  n.shift = 31;
+  while ((int64_t)1 << (n.shift - 31) < n.H) ++n.shift;
+  n.by = (uint32_t)(((uint64_t)1 << n.shift) / (uint64_t)n.H + 1);
   const int64_t groups = (rows + per - 1) / per, wide = groups < kGridX ? groups : kGridX;
   const dim3 grid((unsigned)wide, (unsigned)((groups + wide - 1) / wide)), block(kThreads);
   if (n.q8) hipLaunchKernelGGL((rmsnorm_kernel<R, NP, true>), grid, block, 0, s, n);
