@@ -147,6 +147,31 @@ at::Tensor make(const at::Tensor &like, at::IntArrayRef shape, at::ScalarType t)
   return at::Tensor(at::detail::empty_cuda(shape, t, like.device(), std::nullopt));
 }
 
+// Tensors that are used together in one allocation, each at a multiple of 256 bytes
+// (0.2 us less a tensor than one each).
+template <int N>
+void make_together(at::Tensor (&t)[N], const at::Tensor &like, const at::IntArrayRef (&shapes)[N],
+                   const at::ScalarType (&types)[N]) {
+  int64_t at_byte[N], bytes = 0;
+  for (int i = 0; i < N; ++i) {
+    int64_t n = (int64_t)c10::elementSize(types[i]);
+    for (const int64_t size : shapes[i]) {
+      if (size < 0 || (size > 0 && n > INT64_MAX / 4 / size)) raise(PyExc_ValueError, "no tensor is of ", shapes[i]);
+      n *= size;
+    }
+    at_byte[i] = bytes;
+    bytes += (n + 255) / 256 * 256;
+  }
+  const at::Tensor all = make(like, {bytes}, at::kByte);
+  for (int i = 0; i < N; ++i) {
+    t[i] = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(),
+                                                    c10::scalarTypeToTypeMeta(types[i]));
+    c10::TensorImpl *const impl = t[i].unsafeGetTensorImpl();
+    impl->set_storage_offset(at_byte[i] / (int64_t)c10::elementSize(types[i]));
+    impl->set_sizes_contiguous(shapes[i]);
+  }
+}
+
 // Calls fn(args..., the device's current stream) with that device current.
 template <typename F, typename... A>
 void call(at::Device d, F fn, A... args) {
@@ -447,17 +472,14 @@ PyObject *rmsnorm_q8(PyObject *const *a) {
   const char *names[3] = {"codes", "scales", "code_sums"};
   const at::ScalarType types[3] = {at::kChar, at::kFloat, at::kInt};
   const bool given = a[5] != Py_None;
-  for (int i = 0; i < 3; ++i) {
-    const at::IntArrayRef want = i == 0 ? shape : blocks;
-    if (given) {
-      t[i] = tensor(a[5 + i], names[i]);
-      if (t[i].scalar_type() != types[i] || t[i].sizes() != want || !t[i].is_contiguous())
-        raise(PyExc_ValueError, names[i], " must be contiguous ", types[i], " ", want, ", got ", t[i].scalar_type(), " ",
-              t[i].sizes());
-      one_gpu({&in.x, &t[i]});
-    } else {
-      t[i] = make(in.x, want, types[i]);
-    }
+  const at::IntArrayRef want[3] = {shape, blocks, blocks};
+  if (!given) make_together(t, in.x, want, types);
+  for (int i = 0; given && i < 3; ++i) {
+    t[i] = tensor(a[5 + i], names[i]);
+    if (t[i].scalar_type() != types[i] || t[i].sizes() != want[i] || !t[i].is_contiguous())
+      raise(PyExc_ValueError, names[i], " must be contiguous ", types[i], " ", want[i], ", got ", t[i].scalar_type(), " ",
+            t[i].sizes());
+    one_gpu({&in.x, &t[i]});
   }
   call(in.device, p_qmm_rmsnorm_q8, kind, (const void *)in.x.data_ptr(), code(in.x.scalar_type()), in.r.stride, in.res(),
        in.res_code(), in.residual_stride, in.weight, in.eps, in.sum_ptr(), in.sum_stride, (int8_t *)t[0].data_ptr(),
@@ -614,7 +636,9 @@ PyObject *moe_route(PyObject *const *a) {
     one_gpu({&x, &ids, &w});
   } else {
     if (k < 0) raise(PyExc_ValueError, "topk=", k, " is not a size");
-    ids = make(x, shape, at::kInt), w = make(x, shape, at::kFloat);
+    at::Tensor t[2];
+    make_together(t, x, {at::IntArrayRef(shape), at::IntArrayRef(shape)}, {at::kInt, at::kFloat});
+    ids = std::move(t[0]), w = std::move(t[1]);
   }
   call(d, p_qmm_moe_route, (const void *)x.data_ptr(), code(x.scalar_type()), r.stride, bias, M, E, k, score, n_group,
        topk_group, (int)std::max<int64_t>(std::min<int64_t>(top, 3), 0), normalize, scale, slots, (int32_t *)ids.data_ptr(),
