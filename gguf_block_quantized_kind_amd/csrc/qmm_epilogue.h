@@ -32,6 +32,30 @@ __device__ __forceinline__ float times_sigmoid(float v, float x) {
   return 0.25f * v * __builtin_amdgcn_rcpf(0.25f + quarter);
 }
 
+// v erfc(-v / sqrt(2)) / 2 within 2^-20 relative.  With y = |v| and t = 1 / (1 + 0.33 y),
+// erfc(y / sqrt(2)) exp(y^2 / 2) / t is a polynomial of degree 9 in t to 2e-8 on 0 <= y
+// <= 14.5 (a least squares fit of the function's values with weights raised where
+// the relative error was largest), where the exponential leaves f32's range; 3e-7 as it
+// is evaluated, 6.5e-7 with 2^x and the reciprocal each a step off.  The square is
+// taken in two parts, as its rounding alone would be y^2 / 2 steps of the result.
+// Against erfcf: gelu(product) * factor, 8192 tokens, 8192 x 4096 Q4_K 596 -> 560 us,
+// 2048 tokens, 14336 x 4096 309 -> 292; 499 tokens with a bias, 4096 x 4096 repacked Q8_0
+// 35.2 -> 33.6.
+__device__ __forceinline__ float gelu(float v) {
+  constexpr float kC[10] = {-0.0219160002f, 0.0707042441f, -0.00149240822f, -0.226902843f, 0.213063121f,
+                            0.00304379361f, 0.207221866f, 0.229145855f, 0.263853908f, 0.263278455f};
+  constexpr float kHi = -0.7213475108146667f, kLo = -9.629815167500055e-9f, kLn2 = 0.69314718055994531f;  // -log2(e) / 2
+  const float y = fminf(fabsf(v), 14.5f);  // a NaN is still one in v
+  const float t = __builtin_amdgcn_rcpf(fmaf(0.33f, y, 1.0f));
+  float q = kC[0];
+#pragma unroll
+  for (int i = 1; i < 10; ++i) q = fmaf(q, t, kC[i]);
+  const float s = y * y, x = s * kHi;
+  const float rest = fmaf(fmaf(y, y, -s), kHi, fmaf(s, kLo, fmaf(s, kHi, -x)));
+  const float tail = 0.5f * q * t * (__builtin_amdgcn_exp2f(x) * fmaf(rest, kLn2, 1.0f));
+  return v * (v < 0.f ? tail : 1.0f - tail);
+}
+
 // f32 activations.  Each is written so that its tail keeps its relative
 // accuracy: gelu through erfc (1 + erf loses everything below -4), its tanh form as
 // a sigmoid: (1 + tanh(u)) / 2 = 1 / (1 + exp(-2 u)).
@@ -39,7 +63,7 @@ __device__ __forceinline__ float activated(int act, float v) {
   switch (act) {
     case QMM_ACT_RELU: return v < 0.f ? 0.f : v;  // a NaN stays one
     case QMM_ACT_SILU: return times_sigmoid(v, v);
-    case QMM_ACT_GELU: return 0.5f * v * erfcf(v * -0.70710678118654752f);
+    case QMM_ACT_GELU: return gelu(v);
     case QMM_ACT_GELU_TANH: return times_sigmoid(v, 1.5957691216057308f * (v + 0.044715f * v * v * v));  // 2 sqrt(2 / pi)
     default: return v;
   }
