@@ -587,6 +587,16 @@ hipError_t launch_gemv_mfma(int kind, const uint8_t *W, const void *x, int x_f16
 #else
   constexpr int cfg = 0;
 #endif
+#ifdef QMM_WITH_EPILOGUE
+  // One token over native rows that begin between words, or few and long ones of
+  // the same kinds, by granules: 2638 x 13056 Q6_K 22.0 -> 13.6 us, Q3_K 18.5 -> 12.2;
+  // 4096 x 14336 17.5 -> 16.3, 14.6 -> 13.4 (4096 x 4096 7.0 -> 8.1, even).
+  if (M == 1 && (kind == Q6_K || kind == Q3_K) && K % 256 == 0 &&
+      (K / 256 % 2 != 0 || ((N + 15) / 16 <= device_cus() && K / 256 > 32))) {
+    const hipError_t e = launch_gemv_xk(kind, W, false, x, x_f16, y, M, N, K, s);
+    if (e != hipErrorNotSupported) return e;
+  }
+#endif
   // One token: the single-token decoders; two to eight tokens of a
   // super-block kind: the staged-activation kernel.
   if (M == 1 && K % 256 == 0 && gemv_t1_supported(kind, false) && (cfg == 0 || cfg >= 200))

@@ -1,4 +1,4 @@
-// qmm_gemv_xk.hip -- products of 2 to 8 tokens with an epilogue where there are few
+// qmm_gemv_xk.hip -- products of up to 8 tokens with an epilogue where there are few
 // tiles of 16 weight rows: a workgroup a tile, its S waves split K.
 //
 // A wave does its k-blocks without the others: the tokens' activations of a

@@ -105,7 +105,7 @@ hipError_t launch_gemm_lds(int kind, const uint8_t *W, const void *A, int a_f16,
                            int64_t K, hipStream_t s);
 hipError_t launch_gemm_packed(int kind, const uint8_t *P, const void *A, int a_f16, Epilogue C, int64_t M, int64_t N,
                               int64_t K, hipStream_t s);
-// 2 to 8 tokens where K is split over a workgroup's waves (hipErrorNotSupported:
+// Up to 8 tokens where K is split over a workgroup's waves (hipErrorNotSupported:
 // elsewhere).
 hipError_t launch_gemv_xk(int kind, const uint8_t *W, bool packed, const void *x, int x_f16, const Epilogue &y, int M,
                           int64_t N, int64_t K, hipStream_t s);

@@ -417,7 +417,7 @@ def test_product_epilogue_on_exact_sums(act, M, packed, N, K):
 
 
 @pytest.mark.parametrize("kind", KINDS)
-@pytest.mark.parametrize("M,N,K", [(2, 100, 1280), (4, 77, 2304), (7, 333, 1536), (8, 50, 8448), (3, 4200, 1536), (5, 9000, 1280)])
+@pytest.mark.parametrize("M,N,K", [(1, 100, 1280), (1, 77, 8704), (2, 100, 1280), (4, 77, 2304), (7, 333, 1536), (8, 50, 8448), (3, 4200, 1536), (5, 9000, 1280)])
 @pytest.mark.parametrize("a,packed", [("f16", False), ("f32", False), ("f16", True), ("f32", True)])
 def test_product_of_few_tokens_over_more_k_blocks(oracle_mod, kind, M, N, K, a, packed):
     run_product(oracle_mod, kind, M, N, K, a, act="silu", mul="f16", res="f32", out="f16" if M % 2 else "f32", packed=packed)
@@ -425,7 +425,7 @@ def test_product_of_few_tokens_over_more_k_blocks(oracle_mod, kind, M, N, K, a, 
 
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("offset", [1, 2, 6, 15])
-@pytest.mark.parametrize("M,N,K", [(1, 70, 512), (4, 70, 512), (2, 70, 1280), (8, 4131, 1280), (20, 70, 1280), (90, 70, 512)])
+@pytest.mark.parametrize("M,N,K", [(1, 70, 512), (1, 70, 1280), (4, 70, 512), (2, 70, 1280), (8, 4131, 1280), (20, 70, 1280), (90, 70, 512)])
 def test_weights_at_any_address(kind, offset, M, N, K):
     """The same bytes elsewhere, and other bytes around them: the same results."""
     g = wl.rng("product", f"address{kind}{offset}{M}")
