@@ -15,24 +15,43 @@
 
 namespace qmm {
 
-// v / (1 + exp(-x)), to about 4 steps of f32 relative, by the hardware's 2^t and
-// reciprocal (one step each).  A GEMM's epilogue overlaps with nothing, so its
-// instructions count: silu(product) * factor, 8192 tokens, 8192 x 4096 Q4_K 573 ->
-// 556 us, 2048 tokens, 14336 x 4096 294 -> 286, against expf and a division.
-// -x log2(e) in two parts, as the rounding of its product alone would be |x| steps
-// of the result; a quarter of the sum, so that its reciprocal is never subnormal:
-// v / 4 loses nothing that silu(v) has.  Past the clamp the exponential is 0 or
-// infinite anyway, which leaves v and -0.
-__device__ __forceinline__ float times_sigmoid(float v, float x) {
-  constexpr float kHi = -1.44269502162933349609375f, kLo = -1.92596299112661746887e-8f, kLn2 = 0.69314718055994531f;
-  x = __builtin_amdgcn_fmed3f(x, -256.f, 256.f);  // a NaN is still one in v
-  const float t = x * kHi;
-  const float rest = fmaf(x, kLo, fmaf(x, kHi, -t));
-  const float quarter = __builtin_amdgcn_exp2f(t) * fmaf(rest, 0.25f * kLn2, 0.25f);
-  return 0.25f * v * __builtin_amdgcn_rcpf(0.25f + quarter);
+// v / (1 + exp(-x)) for an x of v's sign, where t + rest = -|x| log2(e) / 2: within 7 steps of
+// f32 relative (2^-20 is eight), by the hardware's 2^t and reciprocal (one step each).
+// With e = 2^(t + rest) it is v / (1 + e^2) above 0 and v e^2 / (1 + e^2) below: e^2 never
+// overflows, and below 0 it is multiplied in by halves, so that what underflows is the result
+// alone.  (One exponential of -x overflows at -88.72, where silu is still 2.6e-37.)  t is
+// rounded to f32; what that leaves out goes into rest, as it alone would be |x| steps of the
+// result.  A GEMM's epilogue overlaps with nothing, so its instructions count: silu(product)
+// * factor, 8192 tokens, 8192 x 4096 Q4_K 568 us (561 with that one exponential, 546 without
+// an activation), 2048 tokens, 14336 x 4096 293 (290, 283).
+__device__ __forceinline__ float times_sigmoid(float v, float t, float rest) {
+  constexpr float kLn2 = 0.69314718055994531f;
+  const float e = __builtin_amdgcn_exp2f(t) * fmaf(rest, kLn2, 1.0f);
+  const float r = v * __builtin_amdgcn_rcpf(fmaf(e, e, 1.0f)), below = v < 0.f ? e : 1.0f;
+  return r * below * below;  // a NaN in v stays one
 }
 
-// v erfc(-v / sqrt(2)) / 2 within 2^-20 relative.  With y = |v| and t = 1 / (1 + 0.33 y),
+__device__ __forceinline__ float silu(float v) {
+  constexpr float kHi = -0.72134751081466674805f, kLo = -9.629815167500055e-9f;  // -log2(e) / 2
+  const float y = fminf(fabsf(v), 250.f);  // past it e is 0
+  const float t = y * kHi;
+  return times_sigmoid(v, t, fmaf(y, kLo, fmaf(y, kHi, -t)));
+}
+
+// v (1 + tanh(u)) / 2 = v / (1 + exp(-2 u)), 2 u = 2 sqrt(2 / pi) (v + 0.044715 v^3).  In 64
+// bits up to t: 2 u is a number of up to 88 where the result leaves f32's normal range, and
+// each rounding of it to f32 would be up to 88 steps of the result (in all 12 times 2^-20 at
+// -9; 8192 tokens as above 571 us, 563 in f32).
+__device__ __forceinline__ float gelu_tanh(float v) {
+  constexpr double kV = -1.1511040990721626, kV3 = kV * 0.044715;  // -log2(e) sqrt(2 / pi)
+  const double y = (double)fminf(fabsf(v), 16.f);  // past it e is 0
+  const double u = y * fma(kV3 * y, y, kV);
+  const float t = (float)u;
+  return times_sigmoid(v, t, (float)(u - (double)t));
+}
+
+// v erfc(-v / sqrt(2)) / 2 within 2^-20 relative (from -13.2 down, where it leaves f32's
+// normal range, 2^-126 absolute).  With y = |v| and t = 1 / (1 + 0.33 y),
 // erfc(y / sqrt(2)) exp(y^2 / 2) / t is a polynomial of degree 9 in t to 2e-8 on 0 <= y
 // <= 14.5 (a least squares fit of the function's values with weights raised where
 // the relative error was largest), where the exponential leaves f32's range; 3e-7 as it
@@ -52,19 +71,20 @@ __device__ __forceinline__ float gelu(float v) {
   for (int i = 1; i < 10; ++i) q = fmaf(q, t, kC[i]);
   const float s = y * y, x = s * kHi;
   const float rest = fmaf(fmaf(y, y, -s), kHi, fmaf(s, kLo, fmaf(s, kHi, -x)));
-  const float tail = 0.5f * q * t * (__builtin_amdgcn_exp2f(x) * fmaf(rest, kLn2, 1.0f));
-  return v * (v < 0.f ? tail : 1.0f - tail);
+  // (y comes in before the exponential, whose product with the rest alone is subnormal earlier.)
+  const float tail = y * (0.5f * q * t) * (__builtin_amdgcn_exp2f(x) * fmaf(rest, kLn2, 1.0f));
+  return v < 0.f ? -tail : v - tail;
 }
 
 // f32 activations.  Each is written so that its tail keeps its relative
-// accuracy: gelu through erfc (1 + erf loses everything below -4), its tanh form as
-// a sigmoid: (1 + tanh(u)) / 2 = 1 / (1 + exp(-2 u)).
+// accuracy: gelu through erfc (1 + erf loses everything below -4), silu and gelu's tanh form
+// through e^x below 0.
 __device__ __forceinline__ float activated(int act, float v) {
   switch (act) {
     case QMM_ACT_RELU: return v < 0.f ? 0.f : v;  // a NaN stays one
-    case QMM_ACT_SILU: return times_sigmoid(v, v);
+    case QMM_ACT_SILU: return silu(v);
     case QMM_ACT_GELU: return gelu(v);
-    case QMM_ACT_GELU_TANH: return times_sigmoid(v, 1.5957691216057308f * (v + 0.044715f * v * v * v));  // 2 sqrt(2 / pi)
+    case QMM_ACT_GELU_TANH: return gelu_tanh(v);
     default: return v;
   }
 }

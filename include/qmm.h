@@ -372,8 +372,9 @@ int qmm_gemv_i8_noalloc(int kind, const void *P, const void *x, int x_dtype, flo
  * out is f32 or f16 with a row stride; it may be mul or residual itself (same
  * type and stride), and overlaps nothing else.  The sum is held to the plain entry
  * points' accuracy, the epilogue is in f32 (activations within 2^-20 relative of
- * their value at the f32 sum), and the result is rounded once to out's type: an
- * f16 out beyond 65504 is an infinity.
+ * their value at the f32 sum with its bias, or within 2^-126 where that value is
+ * below f32's normal range), and the result is rounded once to out's type: an f16
+ * out beyond 65504 is an infinity.
  * --------------------------------------------------------------------- */
 enum qmm_act { QMM_ACT_NONE = 0, QMM_ACT_RELU = 1, QMM_ACT_SILU = 2, QMM_ACT_GELU = 3, QMM_ACT_GELU_TANH = 4 };
 typedef struct qmm_epilogue {

@@ -1,0 +1,73 @@
+"""What stands around a layer's products on the GPU, at the edges of its numerics and of its sizes, against the
+definitions of oracle/layer.py.
+
+Activations: 2^-20 of the value, or 2^-126 (where the value leaves f32's normal range), as include/qmm.h states it, on
+sums whose f32 value is known exactly.
+"""
+import numpy as np
+import pytest
+
+import workloads as wl
+from oracle import layer
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+import gguf_block_quantized_kind_amd as qmm  # noqa: E402
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    qmm.load_library()
+
+
+def dev(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def host(t):
+    return t.cpu().numpy()
+
+
+# -- activations -----------------------------------------------------------------
+def far_and_near(n, g):
+    """n numbers of f32: tails down to where each activation leaves f32's normal range and past it, what lies between,
+    and far ones."""
+    parts = [(-104, -87), (-92, -88), (-15, -12.5), (-14, -3), (-11, -9), (-3, 3), (3, 14), (14, 92)]
+    special = [0.0, -0.0, 1e-40, -1e-40, 2.0 ** -126, -88.722839, -88.72284, -91.85, 88.722839, 1e30, -1e30, 3e38, -3e38]
+    each = -(-(n - len(special)) // len(parts))
+    v = np.concatenate([special] + [g.uniform(a, b, each) for a, b in parts])[:n].astype(np.float32)
+    return g.permutation(v)
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("kind,packed,M,N,K", [
+    ("Q4_K", False, 1, 4099, 256), ("Q6_K", False, 8, 4099, 1536), ("Q8_0", True, 1, 4099, 256), ("Q8_0", True, 5, 9001, 256),
+    ("Q4_0", False, 3, 4099, 96), ("Q4_K", False, 33, 4099, 256), ("Q4_K", False, 130, 4099, 256), ("Q8_0", False, 64, 8203, 64),
+    ("Q8_0", True, 300, 4099, 256), ("Q8_0", False, 70, 4099, 64), ("Q6_K", True, 70, 16403, 256)])
+def test_activations_of_known_sums(act, kind, packed, M, N, K):
+    """Activations of zeros: the sum is the bias itself, through every kernel that ends in an epilogue."""
+    g = wl.rng("edges", f"{act}{kind}{M}{N}")
+    b = far_and_near(N, g)
+    W = dev(wl.random_weights(kind, N, K, g))
+    W = qmm.repack(kind, W, N, K) if packed else W
+    fn = qmm.matmul_packed_ep if packed else qmm.matmul_ep
+    got = host(fn(kind, W, torch.zeros((M, K), dtype=torch.float16, device="cuda"), N, bias=dev(b), act=act)).astype(np.float64)
+    want = layer.activation(act, b)
+    ratio = np.abs(got - want) / (2.0 ** -20 * np.abs(want) + 2.0 ** -126)
+    at = np.unravel_index(np.argmax(ratio), ratio.shape)
+    assert ratio[at] <= 1.0, f"{ratio[at]:.3g} of the bound at {b[at[1]]}: got {got[at]}, want {want[at[1]]}"
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+def test_activations_of_known_sums_behind_the_integer_product(act):
+    g = wl.rng("edges", f"q8{act}")
+    N, K = 5003, 512
+    b = far_and_near(N, g)
+    P = qmm.repack("Q4_0", dev(wl.random_weights("Q4_0", N, K, g)), N, K)
+    acts = qmm.rmsnorm_q8("Q4_0", torch.zeros((3, K), device="cuda"), None, 0.0)
+    got = host(qmm.gemv_q8("Q4_0", P, acts, N, bias=dev(b), act=act)).astype(np.float64)
+    want = layer.activation(act, b)
+    assert np.all(np.abs(got - want) <= 2.0 ** -20 * np.abs(want) + 2.0 ** -126)
