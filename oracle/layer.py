@@ -15,6 +15,8 @@ import numpy as np
 from . import int8
 
 ACTS = ("none", "relu", "silu", "gelu", "gelu_tanh")
+# Where an activation has its only minimum (between two rising parts), to 1e-9.
+LOWEST = {"silu": -1.278464543, "gelu": -0.751791524, "gelu_tanh": -0.752461422}
 # Bounds of |act'|: of silu 1.0998 (near 2.4), of both gelus 1.129 (near 1.41).
 SLOPE = {"none": 1.0, "relu": 1.0, "silu": 1.1, "gelu": 1.13, "gelu_tanh": 1.13}
 
@@ -69,14 +71,27 @@ def activation(act, v):
     raise KeyError(act)
 
 
+def moved(act, u, err):
+    """How far act(v) can be from act(u) for v within err of u.  Between its minimum and either side an activation only
+    falls or rises, so the farthest are the ends or the minimum."""
+    y = activation(act, u)
+    far = np.maximum(np.abs(activation(act, u - err) - y), np.abs(activation(act, u + err) - y))
+    if act in LOWEST:
+        low = LOWEST[act]
+        far = np.where(np.abs(u - low) <= err + 1e-9, np.maximum(far, np.abs(activation(act, low) - y)), far)
+    return far
+
+
 def epilogue(v, err, bias=None, act="none", mul=None, residual=None, f16=False):
     """(out, tol) for sums v that are known to `err`: the epilogue in binary64, and what the sums' error and f32 steps
-    (2^-24 relative each, 2^-20 for the activation) make of it, beside the result's own rounding."""
+    (2^-24 relative each, for the activation 2^-20 or 2^-126 absolute) make of it, beside the result's own rounding."""
     b = 0.0 if bias is None else np.asarray(bias, dtype=np.float64)
     u = v + b
     err = err + 2.0 ** -24 * np.abs(u)
     y = activation(act, u)
-    tol = SLOPE[act or "none"] * err + (2.0 ** -20 * np.abs(y) if act not in ("none", None, "relu") else 0.0)
+    tol = moved(act, u, err)
+    if act not in ("none", None, "relu"):
+        tol = tol + 2.0 ** -20 * (np.abs(y) + tol) + 2.0 ** -126
     if mul is not None:
         m = np.asarray(mul).astype(np.float64)
         y, tol = y * m, tol * np.abs(m)

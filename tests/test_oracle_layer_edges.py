@@ -1,0 +1,49 @@
+"""The edges of what stands around a layer's products, without a GPU: what the tolerances of the definitions let pass,
+and calls of the library that end before it reaches one."""
+import math
+
+import numpy as np
+import pytest
+
+from oracle import layer
+
+
+# -- tolerances ------------------------------------------------------------------
+def test_how_far_an_activation_moves():
+    """Against a fine grid of the sums within reach, the minimum among them."""
+    for act in layer.ACTS:
+        for u, err in ((-1.3, 0.2), (-0.75, 1e-3), (-0.7518, 1e-9), (-6.0, 0.5), (2.0, 0.25), (0.0, 3.0), (-88.0, 1.0)):
+            grid = u + err * np.linspace(-1, 1, 20001)
+            far = np.abs(layer.activation(act, grid) - layer.activation(act, u)).max()
+            got = float(layer.moved(act, np.array(u), err))
+            assert far * (1 - 1e-12) <= got <= far * (1 + 1e-3) + 1e-18, (act, u, got, far)
+    for act, low in layer.LOWEST.items():
+        x = low + np.array([-1e-4, 0.0, 1e-4])
+        assert np.argmin(layer.activation(act, x)) == 1, act
+
+
+@pytest.mark.parametrize("act,where", [("silu", (-103.0, -5.0)), ("gelu", (-13.0, -3.0)), ("gelu_tanh", (-10.0, -3.0))])
+def test_tails_that_are_lost_are_outside_the_tolerance(act, where):
+    """Mistakes planted in the result: a tail of zeros, one off by a thousandth, and the tail of an exponential that
+    overflows; sums known to their rounding alone, the result in f32."""
+    v = np.linspace(*where, 1001)
+    want, tol = layer.epilogue(v, 0.0, act=act)
+    far = np.abs(want) > 2.0 ** -125
+    assert np.any(far) and np.all(np.abs(want[far]) > tol[far])
+    # (A rounding of the sum moves a tail by up to |v| (silu) or v^2 (gelu) steps; a thousandth is far beyond.)
+    clear = np.abs(want) > 2.0 ** -114                      # a thousandth of it is a normal number
+    assert np.any(clear) and np.all(np.abs(1e-3 * want[clear]) > tol[clear])
+    assert np.all(np.abs(want * (1 + 2.0 ** -21) - want) <= tol)
+    if act == "silu":
+        over = (v < -88.73) & far
+        assert np.any(over) and np.all(np.abs(want[over]) > tol[over])
+
+
+def test_tolerance_covers_sums_that_lie_across_the_minimum():
+    g = np.random.default_rng(7)
+    for act in ("silu", "gelu", "gelu_tanh"):
+        u = g.uniform(-3, 1, 4000)
+        err = np.exp(g.uniform(math.log(1e-7), math.log(2.0), 4000))
+        want, tol = layer.epilogue(u, err, act=act)
+        off = u + err * g.uniform(-1, 1, 4000)
+        assert np.all(np.abs(layer.activation(act, off) - want) <= tol)
