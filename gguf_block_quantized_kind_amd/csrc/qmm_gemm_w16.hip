@@ -385,8 +385,10 @@ Way way_of(int kind, bool packed, int64_t M, int64_t N, int64_t K, int a_f16) {
     // f16: 512 tokens, 4096 x 4096 Q8_0 26.6 (decoded 43.6), 768 tokens 49.4 (43.5);
     // 512 tokens, 14336 x 4096 Q4_0 101 (86).  f32 takes two products: 256 tokens
     // 60 (46), unless its tiles of 64 x 128 just fill the units: 512 tokens 62 (70).
+    // Records of 2^31 bytes and more are beyond that GEMM's offsets.
     const int64_t wide = (M + 63) / 64 * ((N + 127) / 128);
-    decoded = M > 512 || t >= 1792 || (!a_f16 && !(2 * wide > device_cus() && wide <= device_cus()));
+    decoded = packed_bytes_of(kind, N, K) >= (int64_t)1 << 31 || M > 512 || t >= 1792 ||
+              (!a_f16 && !(2 * wide > device_cus() && wide <= device_cus()));
   } else {
     switch (kind) {
       // 64 tokens, 4096 x 4096 115 (33); 128 tokens, 14336 x 4096 66 (58).

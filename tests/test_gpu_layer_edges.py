@@ -71,3 +71,24 @@ def test_activations_of_known_sums_behind_the_integer_product(act):
     got = host(qmm.gemv_q8("Q4_0", P, acts, N, bias=dev(b), act=act)).astype(np.float64)
     want = layer.activation(act, b)
     assert np.all(np.abs(got - want) <= 2.0 ** -20 * np.abs(want) + 2.0 ** -126)
+
+
+# -- sizes -----------------------------------------------------------------------
+def test_packed_weights_of_more_than_2_31_bytes():
+    """Few tokens over records beyond 32-bit offsets, against the same rows taken a few at a time: sums that are exact
+    in f32, so the ways give the same bits."""
+    N, K = 100352, 20480
+    assert qmm.qmm_packed_bytes("Q8_0", N, K) >= 1 << 31
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+    W = torch.randint(-3, 4, (N, K // 32, 34), generator=g, device="cuda", dtype=torch.int8).view(torch.uint8)
+    W[..., 0], W[..., 1] = 0, 0x24                          # 2^-6 in f16
+    P = qmm.repack("Q8_0", W.reshape(-1), N, K)
+    A = torch.randint(-2, 3, (64, K), generator=g, device="cuda").half()
+    for M in (9, 64):
+        out = qmm.matmul_packed_ep("Q8_0", P, A[:M], N)
+        for n in (0, 50000, N - 1040):
+            part = qmm.matmul_ep("Q8_0", W[n:n + 1040].reshape(-1), A[:M], 1040)
+            assert torch.equal(out[:, n:n + 1040], part), (M, n)
+    del W, P, out
+    torch.cuda.empty_cache()

@@ -47,3 +47,34 @@ def test_tolerance_covers_sums_that_lie_across_the_minimum():
         want, tol = layer.epilogue(u, err, act=act)
         off = u + err * g.uniform(-1, 1, 4000)
         assert np.all(np.abs(layer.activation(act, off) - want) <= tol)
+
+
+# -- the library's answers about sizes ---------------------------------------------
+OK, EMPTY, KIND, KALIGN, DTYPE, ARG, HIP, WS = range(8)
+FAKE = 0x1000  # never dereferenced: every call below is refused first
+
+
+@pytest.fixture(scope="module")
+def lib():
+    import os
+
+    import gguf_block_quantized_kind_amd as qmm
+    if not os.path.exists(qmm.LIBRARY):
+        import gguf_block_quantized_kind_amd._build as b
+        b.build()
+    return qmm.load_library()
+
+
+def product(lib, packed, kind, M, N, K, dt=1, ws=None, wsb=0):
+    fn = lib.qmm_matmul_packed_ep if packed else lib.qmm_matmul_ep
+    return fn(kind, FAKE, FAKE, dt, None, FAKE, 0, N, M, N, K, ws, wsb, None)
+
+
+@pytest.mark.parametrize("kind,N,K", [(8, 100352, 20480), (2, 65536, 65536), (20, 131072, 32768)])
+def test_weights_beyond_32_bits_at_any_number_of_tokens(lib, kind, N, K):
+    """Records of 2^31 bytes and more are beyond the GEMM over records: decoded once, whether the tokens are few or many.
+    (Every call ends at the missing workspace.)"""
+    for M in (9, 16, 17, 64, 65, 100, 512, 513, 600, 2000):
+        for dt in (0, 1):
+            assert lib.qmm_matmul_ep_workspace_bytes(kind, 1, M, N, K, dt) >= 2 * N * K, (M, dt)
+            assert product(lib, True, kind, M, N, K, dt) == WS, (M, dt)
