@@ -711,6 +711,17 @@ int check_epilogue(const qmm_epilogue *ep, void *out, int out_dtype, int64_t out
 
 namespace {
 
+// The way of a product, within the limits of the GEMMs that decode as they
+// multiply (qmm_matmul, qmm_matmul_packed: 32-bit offsets), and of tiles and
+// offsets over decoded weights.
+bool ep_fits(int kind, bool packed, int64_t M, int64_t N, int64_t K, int a_f16, qmm::Way *way) {
+  if (M > (int64_t)65535 * 64 || (packed && M * K >= ((int64_t)1 << 31))) return false;
+  *way = M <= QMM_GEMV_MAX_M ? qmm::Way::kGemv : qmm::way_of(kind, packed, M, N, K, a_f16);
+  if (*way == qmm::Way::kDecoded) return K <= (int64_t)1 << 20 && (M + 63) / 64 * ((N + 63) / 64) < (int64_t)1 << 24;
+  return *way != qmm::Way::kGemm || !packed ||
+         (qmm::packed_bytes_of(kind, N, K) < ((int64_t)1 << 31) && M * K * (a_f16 ? 2 : 4) < ((int64_t)1 << 31));
+}
+
 // What both products share after the shape checks.
 int matmul_ep_checked(int kind, const void *W, bool packed, const void *A, int a_dtype, const qmm_epilogue *ep, void *out,
                       int out_dtype, int64_t out_stride, int64_t M, int64_t N, int64_t K, void *workspace,
@@ -726,15 +737,8 @@ int matmul_ep_checked(int kind, const void *W, bool packed, const void *A, int a
   // LDS.)
   if (M > QMM_GEMV_MAX_M && !aligned(A, 16)) return fail(QMM_ERR_BAD_ARG, "A of more than %d tokens is not 16-byte aligned", QMM_GEMV_MAX_M);
   const int a_f16 = a_dtype == QMM_F16;
-  // Limits of the GEMMs that decode as they multiply (qmm_matmul,
-  // qmm_matmul_packed: 32-bit offsets), and of tiles and offsets over decoded
-  // weights.
-  const bool gemv = M <= QMM_GEMV_MAX_M;
-  const qmm::Way way = gemv ? qmm::Way::kGemv : qmm::way_of(kind, packed, M, N, K, a_f16);
-  if (M > (int64_t)65535 * 64 || (packed && M * K >= ((int64_t)1 << 31)) ||
-      (packed && way == qmm::Way::kGemm &&
-       (qmm::packed_bytes_of(kind, N, K) >= ((int64_t)1 << 31) || M * K * (a_f16 ? 2 : 4) >= ((int64_t)1 << 31))) ||
-      (way == qmm::Way::kDecoded && (K > (int64_t)1 << 20 || (M + 63) / 64 * ((N + 63) / 64) >= (int64_t)1 << 24)))
+  qmm::Way way;
+  if (!ep_fits(kind, packed, M, N, K, a_f16, &way))
     return fail(QMM_ERR_BAD_ARG, "M=%lld, N=%lld, K=%lld exceed the supported range", (long long)M, (long long)N,
                 (long long)K);
   qmm::Epilogue e;
@@ -746,7 +750,7 @@ int matmul_ep_checked(int kind, const void *W, bool packed, const void *A, int a
   const uint8_t *w = (const uint8_t *)W;
   hipStream_t s = (hipStream_t)stream;
   hipError_t r;
-  if (gemv)
+  if (M <= QMM_GEMV_MAX_M)
     r = packed ? qmm::launch_gemv_packed(kind, w, A, a_f16, e, (int)M, N, K, s)
                : qmm::launch_gemv(kind, w, A, a_f16, e, (int)M, N, K, s);
   else if (way == qmm::Way::kGemv)
@@ -763,10 +767,14 @@ int matmul_ep_checked(int kind, const void *W, bool packed, const void *A, int a
 
 QMM_EXPORT size_t qmm_matmul_ep_workspace_bytes(int kind, int packed, int64_t M, int64_t N, int64_t K, int a_dtype) {
   const KindInfo *k = find_kind(kind);
-  if (!k || M <= 0 || N <= 0 || K <= 0 || K > (int64_t)1 << 30 || N > INT32_MAX || M > (int64_t)65535 * 64 ||
-      K % (packed ? 256 : k->block_elems) != 0 || !dtype_ok(a_dtype))
+  if (!k || M <= 0 || N <= 0 || K <= 0 || K > (int64_t)1 << 30 || N > INT32_MAX ||
+      K % (packed ? 256 : k->block_elems) != 0 || !dtype_ok(a_dtype) ||
+      (packed && qmm::packed_bytes_of(kind, N, K) > ((int64_t)1 << 40)))
     return 0;
-  return qmm::gemm_w16_workspace_bytes(kind, packed != 0, M, N, K, a_dtype == QMM_F16);
+  const int a_f16 = a_dtype == QMM_F16;
+  qmm::Way way;
+  if (!ep_fits(kind, packed != 0, M, N, K, a_f16, &way)) return 0;
+  return qmm::gemm_w16_workspace_bytes(kind, packed != 0, M, N, K, a_f16);
 }
 
 QMM_EXPORT int qmm_matmul_ep(int kind, const void *W, const void *A, int a_dtype, const qmm_epilogue *ep, void *out,

@@ -402,8 +402,8 @@ int qmm_matmul_ep(int kind, const void *W, const void *A, int a_dtype, const qmm
                   int out_dtype, int64_t out_stride, int64_t M, int64_t N, int64_t K, void *workspace,
                   size_t workspace_bytes, void *stream);
 /* qmm_matmul_packed with an epilogue and that workspace, at any M for every kind
- * (those that qmm_matmul_packed's GEMM does not take go through the workspace);
- * errors as both. */
+ * (those that qmm_matmul_packed's GEMM does not take, and records of 2^31 bytes and
+ * more, go through the workspace: K up to 2^20 there); errors as both. */
 int qmm_matmul_packed_ep(int kind, const void *P, const void *A, int a_dtype, const qmm_epilogue *ep, void *out,
                          int out_dtype, int64_t out_stride, int64_t M, int64_t N, int64_t K, void *workspace,
                          size_t workspace_bytes, void *stream);

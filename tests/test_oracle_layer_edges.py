@@ -78,3 +78,15 @@ def test_weights_beyond_32_bits_at_any_number_of_tokens(lib, kind, N, K):
         for dt in (0, 1):
             assert lib.qmm_matmul_ep_workspace_bytes(kind, 1, M, N, K, dt) >= 2 * N * K, (M, dt)
             assert product(lib, True, kind, M, N, K, dt) == WS, (M, dt)
+
+
+@pytest.mark.parametrize("packed,kind,M,N,K", [
+    (1, 8, 1 << 21, 64, 1024),                               # M K of 2^31
+    (1, 12, 9, 16, 1 << 21), (1, 14, 100, 4096, 1 << 21),    # decoded weights of more than 2^20 columns
+    (1, 8, 9, 16, (1 << 30) + 256), (0, 8, 9, 16, (1 << 30) + 32), (0, 8, 100, (1 << 31), 32), (1, 8, 100, (1 << 31), 256),
+    (1, 8, 100, 1 << 28, 1 << 20),                           # 2^40 bytes of records
+    (1, 12, 1 << 21, 1 << 21, 256), (0, 14, 65535 * 64 + 1, 64, 256), (1, 3, 100, 8192, 256), (0, 12, 100, 8192, 288)])
+def test_no_workspace_for_what_is_refused(lib, packed, kind, M, N, K):
+    for dt in (0, 1):
+        assert product(lib, packed, kind, M, N, K, dt) not in (OK, WS, HIP)
+        assert lib.qmm_matmul_ep_workspace_bytes(kind, packed, M, N, K, dt) == 0, dt
