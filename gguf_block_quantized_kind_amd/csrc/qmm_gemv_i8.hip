@@ -76,7 +76,7 @@ __global__ __launch_bounds__(256) void quantize_kernel(const XT *__restrict__ X,
   for (int m = 16; m >= 1; m >>= 1) amax = fmaxf(amax, __shfl_xor(amax, m, 32));
   const float db = (float)((double)amax / 127.0);
   const float r = db > 0.f ? (float)((double)v / (double)db) : 0.f;
-  const int c = (int)__builtin_rintf(r);
+  const int c = max(-127, min(127, (int)__builtin_rintf(r)));  // beyond it only where db is subnormal
   int sum = c;
 #pragma unroll
   for (int m = 16; m >= 1; m >>= 1) sum += __shfl_xor(sum, m, 32);

@@ -177,7 +177,7 @@ __global__ __launch_bounds__(R > 256 ? R : 256) void rmsnorm_kernel(const Split 
 #pragma unroll
       for (int e = 0; e < V; ++e) {
         const float q = d > 0.f ? h[i][e] / d : 0.f;
-        c[e] = (int)__builtin_rintf(q);
+        c[e] = max(-127, min(127, (int)__builtin_rintf(q)));  // beyond it only where d is subnormal
         sum += c[e];
       }
       sum += (int)dpp<0xB1>((uint32_t)sum);

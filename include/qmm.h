@@ -307,7 +307,8 @@ int qmm_moe_packed(int kind, const void *P, int64_t E, const int32_t *ids, int64
  * f16, [M][K], finite) is first quantized into `workspace`, per token and
  * 32-element block: amax = max |x|, d = amax / 127 and x / d each rounded to
  * f32 (correctly rounded), then q = x / d rounded to the nearest integer,
- * ties to even (|q| <= 127); an all-zero block has d = 0.  Then
+ * ties to even (|q| <= 127: cut there where a subnormal d makes x / d larger); a
+ * block with d = 0 has q = 0.  Then
  *   y[t][n] = sum over blocks b of d_w[n][b] d[t][b] (sum_i w_i q_i)
  * with each block's integer dot product exact (Q4_0 as code - 8, Q5_0 as
  * code - 16, IQ4_NL as the table value, MXFP4 as twice its E2M1 value with

@@ -13,8 +13,9 @@ for it, so the plainest reading is taken:
 * per token and 32-element block (the weight block of Q8_0, Q4_0, Q5_0,
   IQ4_NL and MXFP4, whose values are integers up to the block scale),
   amax = max |x|, the scale d = amax / 127 rounded to f32, and each code
-  q = x / d rounded to f32, then to the nearest integer, ties to even;
-  an all-zero block has d = 0 and q = 0;
+  q = x / d rounded to f32, then to the nearest integer, ties to even, at most
+  127 either way (a subnormal d has few bits, so x / d can be beyond it);
+  a block with d = 0 has q = 0;
 * the product is y[t][n] = sum over blocks of d_w d_x (sum_i w_i q_i) with
   the weights' own integer codes, i.e. the exact product of W with the
   rebuilt activations d_x * q.
@@ -50,7 +51,7 @@ def quantize(X) -> tuple[np.ndarray, np.ndarray]:
     with np.errstate(divide="ignore", invalid="ignore"):
         r = (xb / d[:, :, None]).astype(np.float32)            # one f32 rounding
     q = np.where(d[:, :, None] > 0, np.rint(r), 0.0)           # ties to even
-    assert np.all(np.abs(q) <= 127)
+    q = np.clip(q, -127.0, 127.0)                              # beyond it only where d is subnormal
     return q.astype(np.int8).reshape(M, K), d
 
 

@@ -92,3 +92,48 @@ def test_packed_weights_of_more_than_2_31_bytes():
             assert torch.equal(out[:, n:n + 1040], part), (M, n)
     del W, P, out
     torch.cuda.empty_cache()
+
+
+# -- eight bits ------------------------------------------------------------------
+def subnormal_rows(g, T, D):
+    """f32 rows whose blocks have largest magnitudes of 1 to 20000 times the smallest f32, both signs."""
+    top = np.exp(g.uniform(0, np.log(20000), (T, D // 32, 1)))
+    n = np.rint(g.uniform(-1, 1, (T, D // 32, 32)) * top)
+    n[:, :, 5] = np.rint(np.where(g.random((T, D // 32)) < 0.5, -1, 1) * top[:, :, 0])
+    n[0, 0, :4] = [190, -190, 100, 63]
+    n[0, 0, 4:] = 0
+    return (n.reshape(T, D) * 2.0 ** -149).astype(np.float32)
+
+
+@pytest.mark.parametrize("kind", ["Q8_0", "Q4_0"])
+def test_eight_bits_of_subnormal_rows(kind):
+    """The norm's 8 bits are those of its f32 rows where these are subnormal: codes, scales and code sums."""
+    g = wl.rng("edges", f"subnormal{kind}")
+    T, D = 7, 1312
+    w = subnormal_rows(g, 1, D)[0]                           # h / sqrt(mean h^2) = 1, -1: the rows are the weight
+    x = np.where(g.random((T, D)) < 0.5, -3.0, 3.0).astype(np.float32)
+    y = host(qmm.rmsnorm(dev(x), dev(w), 0.0))
+    assert np.array_equal(np.abs(y), np.broadcast_to(np.abs(w), y.shape))
+    codes, d, sums = layer.eight_bits(kind, y)
+    got = qmm.rmsnorm_q8(kind, dev(x), dev(w), 0.0)
+    assert np.array_equal(host(got[1]), d) and np.array_equal(host(got[0]), codes) and np.array_equal(host(got[2]), sums)
+
+
+@pytest.mark.parametrize("kind", ["Q8_0", "Q5_0"])
+def test_integer_product_of_subnormal_activations(kind):
+    """The workspace of the quantizing product: the oracle's codes, scales and code sums."""
+    g = wl.rng("edges", f"subnormal i8 {kind}")
+    M, N, K = 5, 32, 1024
+    X = subnormal_rows(g, M, K)
+    P = qmm.repack(kind, dev(wl.random_weights(kind, N, K, g)), N, K)
+    ws = torch.empty(qmm.qmm_gemv_i8_workspace_bytes(M, K), dtype=torch.uint8, device="cuda")
+    y = torch.empty((M, N), device="cuda")
+    qmm.qmm_gemv_i8(kind, P, dev(X), y, M, N, K, ws)
+    raw = host(ws)
+    at = [0]
+    for n in (M * K, M * K // 8):
+        at.append((at[-1] + n + 255) // 256 * 256)
+    codes, d, sums = layer.eight_bits(kind, X)
+    assert np.array_equal(raw[at[1]:at[1] + M * K // 8].view(np.float32).reshape(M, K // 32), d)
+    assert np.array_equal(raw[:M * K].view(np.int8).reshape(M, K), codes)
+    assert np.array_equal(raw[at[2]:at[2] + M * K // 8].view(np.int32).reshape(M, K // 32), sums)

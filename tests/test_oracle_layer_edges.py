@@ -90,3 +90,22 @@ def test_no_workspace_for_what_is_refused(lib, packed, kind, M, N, K):
     for dt in (0, 1):
         assert product(lib, packed, kind, M, N, K, dt) not in (OK, WS, HIP)
         assert lib.qmm_matmul_ep_workspace_bytes(kind, packed, M, N, K, dt) == 0, dt
+
+
+# -- eight bits ------------------------------------------------------------------
+def test_eight_bits_of_subnormal_blocks():
+    """Where the scale has few bits left the quotient of the largest can be beyond 127: its code is cut there, with its
+    sign, and the code sum is that of the codes."""
+    from oracle import int8
+    unit = np.float32(2.0 ** -149)
+    y = np.zeros((1, 64), np.float32)
+    y[0, :4] = np.array([190, -190, 100, 63], np.float32) * unit     # d = 190 / 127 rounds to one unit
+    y[0, 32:35] = np.array([-63, 40, 5], np.float32) * unit          # d rounds to none
+    q, d = int8.quantize(y)
+    assert d.tolist() == [[float(unit), 0.0]]
+    assert q[0, :4].tolist() == [127, -127, 100, 63] and not q[0, 4:].any()
+    assert layer.eight_bits("Q8_0", y)[2].tolist() == [[163, 0]]
+    for n in range(1, 127 * 127 + 2000, 37):                          # every other scale: codes within half a step of 127
+        q, d = int8.quantize(np.full((1, 32), n, np.float32) * unit)
+        k = round(float(d[0, 0]) / 2.0 ** -149)
+        assert k == int(np.rint(np.float32(n) / np.float32(127))) and np.all(q == (min(127, round(n / k)) if k else 0))
