@@ -785,7 +785,8 @@ def rmsnorm_q8(kind, x, weight=None, eps: float = 1e-6, residual=None, acts=None
     """rmsnorm of x [T, D] in 8 bits for products with repacked weights of `kind`:
     acts = (codes [T, D] int8, scales [T, D / 32] f32, code_sums [T, D / 32] int32),
     for gemv_q8 (rows t0 .. t1 are the three tensors' rows t0 .. t1); (acts, sum)
-    with a residual."""
+    with a residual.  The three that a call makes are parts of one allocation, which
+    lives as long as any of them."""
     fn = (_ops or _load_ops()).rmsnorm_q8
     codes, scales, sums = (None, None, None) if acts is None else acts
     if stream is not None:
@@ -835,7 +836,9 @@ def moe_route(logits, topk: int, score="softmax", bias=None, n_group: int = 1, t
     """(ids [M, topk] int32, weights [M, topk] f32) for moe_ffn from logits [M, E]:
     the topk largest scores (plus bias [E] f32, which decides but does not weigh)
     within the topk_group groups of the largest sums of group_top.  Tokens with
-    slots [M] int32 below 0, and rows that run out of experts, get ids of -1."""
+    slots [M] int32 below 0, and rows that run out of experts, get ids of -1.  ids and
+    weights that a call makes are parts of one allocation, which lives as long as
+    either."""
     fn = (_ops or _load_ops()).moe_route
     if stream is not None:
         return _on(stream, logits, fn, logits, topk, score, bias, n_group, topk_group, group_top, normalize, scale, slots,

@@ -13,6 +13,7 @@
 #include <ATen/ATen.h>
 #include <ATen/hip/EmptyTensor.h>
 #include <c10/core/DeviceGuard.h>
+#include <c10/core/impl/TorchDispatchModeTLS.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
@@ -142,13 +143,21 @@ void check_out_type(PyObject *out, PyObject *dtype, const char *what) {
   if (out != Py_None && dtype != Py_None && tensor(out, what).scalar_type() != type_of(dtype))
     raise(PyExc_TypeError, what, " is ", tensor(out, what).scalar_type(), ", the type asked for is ", type_of(dtype));
 }
-// A tensor beside `like`, which is on a GPU (0.13 us less each than through the dispatcher).
+// Whether someone looks at new tensors: a mode that watches or replaces torch's
+// operators, or torch's filling of new memory.
+bool watched() {
+  return c10::impl::dispatch_mode_enabled() ||
+         (at::globalContext().deterministicAlgorithms() && at::globalContext().deterministicFillUninitializedMemory());
+}
+// A tensor beside `like`, which is on a GPU (0.13 us less each than through the dispatcher,
+// where nobody looks).
 at::Tensor make(const at::Tensor &like, at::IntArrayRef shape, at::ScalarType t) {
+  if (watched()) return at::empty(shape, at::TensorOptions().dtype(t).device(like.device()));
   return at::Tensor(at::detail::empty_cuda(shape, t, like.device(), std::nullopt));
 }
 
 // Tensors that are used together in one allocation, each at a multiple of 256 bytes
-// (0.2 us less a tensor than one each).
+// (0.2 us less a tensor than one each; one each where someone looks).
 template <int N>
 void make_together(at::Tensor (&t)[N], const at::Tensor &like, const at::IntArrayRef (&shapes)[N],
                    const at::ScalarType (&types)[N]) {
@@ -161,6 +170,10 @@ void make_together(at::Tensor (&t)[N], const at::Tensor &like, const at::IntArra
     }
     at_byte[i] = bytes;
     bytes += (n + 255) / 256 * 256;
+  }
+  if (watched()) {
+    for (int i = 0; i < N; ++i) t[i] = make(like, shapes[i], types[i]);
+    return;
   }
   const at::Tensor all = make(like, {bytes}, at::kByte);
   for (int i = 0; i < N; ++i) {

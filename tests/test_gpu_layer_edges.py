@@ -137,3 +137,68 @@ def test_integer_product_of_subnormal_activations(kind):
     assert np.array_equal(raw[at[1]:at[1] + M * K // 8].view(np.float32).reshape(M, K // 32), d)
     assert np.array_equal(raw[:M * K].view(np.int8).reshape(M, K), codes)
     assert np.array_equal(raw[at[2]:at[2] + M * K // 8].view(np.int32).reshape(M, K // 32), sums)
+
+
+# -- the outputs' tensors ----------------------------------------------------------
+def calls():
+    """One call of every function that makes its outputs itself, as (name, function, how many tensors it makes)."""
+    g = wl.rng("edges", "calls")
+    x = dev(g.normal(size=(3, 256)).astype(np.float32))
+    W = dev(wl.random_weights("Q8_0", 64, 256, g))
+    P = qmm.repack("Q8_0", W, 64, 256)
+    acts = qmm.rmsnorm_q8("Q8_0", x, None)
+    heads, pos = x.view(3, 4, 64), dev(np.arange(3, dtype=np.int32))
+    freqs = torch.ones(32, dtype=torch.float64, device="cuda")
+    pages = torch.zeros((2, qmm.kv_page_bytes("F16", 32, 4, 64)), dtype=torch.uint8, device="cuda")
+    table, lens = dev(np.zeros((3, 1), np.int32)), dev(np.array([1, 2, 3], np.int32))
+    return [("rmsnorm", lambda: qmm.rmsnorm(x, None), 1), ("rmsnorm with a residual", lambda: qmm.rmsnorm(x, None, residual=x), 2),
+            ("rmsnorm_q8", lambda: qmm.rmsnorm_q8("Q8_0", x, None), 3), ("moe_route", lambda: qmm.moe_route(x, 4), 2),
+            ("matmul_ep", lambda: qmm.matmul_ep("Q8_0", W, x, 64), 1), ("matmul_packed_ep", lambda: qmm.matmul_packed_ep("Q8_0", P, x, 64), 1),
+            ("gemv_q8", lambda: qmm.gemv_q8("Q8_0", P, acts, 64), 1), ("rope", lambda: qmm.rope(heads, pos, freqs), 1),
+            ("kv_read", lambda: qmm.kv_read(pos, pages, pages, "F16", "F16", 32, 4, 64), 2),
+            ("attn_decode", lambda: qmm.attn_decode(heads, pages, pages, table, lens, "F16", "F16", 32, 4), 2)]
+
+
+def tensors(got):
+    return [t for part in got for t in tensors(part)] if isinstance(got, tuple) else [got]
+
+
+def test_dispatch_modes_see_the_outputs():
+    """A mode that watches torch's operators sees every tensor that a call makes, and may replace it."""
+    from torch.utils._python_dispatch import TorchDispatchMode
+
+    class Watch(TorchDispatchMode):
+        def __init__(self):
+            super().__init__()
+            self.made = []
+
+        def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+            out = func(*args, **(kwargs or {}))
+            self.made.append((func.name().split(".")[0], out))
+            return out
+
+    for name, call, n in calls():
+        want = tensors(call())
+        with Watch() as w:
+            got = tensors(call())
+        made = [t for f, t in w.made if f == "aten::empty"]
+        assert len(made) == n, (name, w.made)
+        assert all(any(t is m for m in made) for t in got), name
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), name
+
+
+def test_deterministic_fill_reaches_the_outputs():
+    """With torch's filling of new memory on, the tensors are made by the operator that fills them; the results stay."""
+    from torch.profiler import ProfilerActivity, profile
+    assert torch.utils.deterministic.fill_uninitialized_memory
+    for name, call, n in calls():
+        want = tensors(call())
+        torch.use_deterministic_algorithms(True)
+        try:
+            with profile(activities=[ProfilerActivity.CPU]) as p:
+                got = tensors(call())
+        finally:
+            torch.use_deterministic_algorithms(False)
+        fills = sum(e.count for e in p.key_averages() if e.key == "aten::empty")
+        assert fills >= n, (name, [e.key for e in p.key_averages()])
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), name
