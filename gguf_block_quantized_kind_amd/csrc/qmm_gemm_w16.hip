@@ -363,7 +363,12 @@ size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 }  // namespace w16
 
 // The crossings below were measured at 4096 x 4096, 14336 x 4096 and 4096 x 14336
-// (rows x K); times in us.
+// (rows x K); times in us.  Over 64, 256 and 1024 rows of 2048 and 7168 (64 to 4096
+// tokens; Q8_0 and Q4_K as rows and as records, Q6_K) they are within a tenth of the
+// fastest way at nine sizes of ten.  The others lie beside a crossing: f16 up to 1.5
+// times (4096 tokens, 64 x 2048 Q8_0 17.2, decoded 12.1; 2048 tokens, 256 x 7168 Q4_K
+// 43.3, decoded 28.0), f32 up to 1.9 (512 tokens, 1024 x 2048 repacked 26.5, by the
+// GEMV's kernels 13.6, which round f32 activations to f16).
 Way way_of(int kind, bool packed, int64_t M, int64_t N, int64_t K, int a_f16) {
   // Sixteen tokens at a time while the tiles of all of them are few: the GEMMs'
   // tiles of 64 tokens leave most compute units without work.  16 tokens, 4096 x

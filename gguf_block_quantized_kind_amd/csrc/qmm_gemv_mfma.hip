@@ -588,9 +588,13 @@ hipError_t launch_gemv_mfma(int kind, const uint8_t *W, const void *x, int x_f16
   constexpr int cfg = 0;
 #endif
 #ifdef QMM_WITH_EPILOGUE
-  // One token over native rows that begin between words, or few and long ones of
-  // the same kinds, by granules: 2638 x 13056 Q6_K 22.0 -> 13.6 us, Q3_K 18.5 -> 12.2;
-  // 4096 x 14336 17.5 -> 16.3, 14.6 -> 13.4 (4096 x 4096 7.0 -> 8.1, even).
+  // One token over native rows that begin between words (an odd number of k-blocks), or
+  // few and long ones of the same kinds, by granules.  Timed at 256 to 32768 rows of 5
+  // to 51 k-blocks: Q6_K as fast at 512 tiles of five, elsewhere 1.0 to 1.8 times as fast
+  // (4096 x 4352 8.2, 8.2 us; 14336 x 4352 24.6 -> 18.2, 2638 x 13056 22.0 -> 13.6, 32768 x
+  // 13056 126 -> 80); Q3_K up to two tiles a compute unit 1.2 to 1.7 (2638 x 13056 18.5 ->
+  // 12.2), beyond them the shape below is taken.  Long rows of an even number: 4096 x
+  // 14336 17.5 -> 16.3, 14.6 -> 13.4 (4096 x 4096 7.0 -> 8.1, even).
   if (M == 1 && (kind == Q6_K || kind == Q3_K) && K % 256 == 0 &&
       (K / 256 % 2 != 0 || ((N + 15) / 16 <= device_cus() && K / 256 > 32))) {
     const hipError_t e = launch_gemv_xk(kind, W, false, x, x_f16, y, M, N, K, s);

@@ -390,15 +390,19 @@ typedef struct qmm_epilogue {
 } qmm_epilogue;
 
 /* qmm_matmul with an epilogue (ep NULL: none).  A of more than QMM_GEMV_MAX_M tokens
- * is 16-byte aligned.  Up to some tens of tokens the sum is the GEMV's (f32 A
- * rounded once to f16, weights exact), above the GEMM's (weights rounded once to
- * f16, f32 A in two f16 parts).  Some sizes decode the weights once into the
- * workspace, to f16 as the GEMM rounds them, with f32 activations' two parts beside
- * them, and multiply from there: qmm_matmul_ep_workspace_bytes gives its size, 0
- * where none is used.  It is device memory, 256-byte aligned, overwritten; calls
- * sharing it must not overlap.  Errors as qmm_matmul, with the dtypes of out, mul
- * and residual beside A's, a stride below N, an unknown act or a misaligned operand
- * as QMM_ERR_BAD_ARG, and last a short workspace as QMM_ERR_WORKSPACE. */
+ * is 16-byte aligned.  The sum is the GEMV's (f32 A rounded once to f16, weights
+ * exact) up to QMM_GEMV_MAX_M tokens, and beyond them while the 16 x 16 tiles of
+ * [M][N] are few: K a multiple of 256 up to 2^20 and at most seven tiles a compute
+ * unit (four over native IQ4_XS rows), on 256 units 112 tokens at N = 4096 and 7168
+ * at N = 64.  Otherwise it is the GEMM's (weights rounded once to f16, f32 A in two
+ * f16 parts, as qmm_matmul takes any M above QMM_GEMV_MAX_M).  Some of these sizes
+ * decode the weights once into the workspace, to f16 as the GEMM rounds them, with
+ * f32 activations' two parts beside them, and multiply from there:
+ * qmm_matmul_ep_workspace_bytes gives its size, 0 where none is used.  It is device
+ * memory, 256-byte aligned, overwritten; calls sharing it must not overlap.  Errors as
+ * qmm_matmul, with the dtypes of out, mul and residual beside A's, a stride below N,
+ * an unknown act or a misaligned operand as QMM_ERR_BAD_ARG, and last a short
+ * workspace as QMM_ERR_WORKSPACE. */
 int qmm_matmul_ep(int kind, const void *W, const void *A, int a_dtype, const qmm_epilogue *ep, void *out,
                   int out_dtype, int64_t out_stride, int64_t M, int64_t N, int64_t K, void *workspace,
                   size_t workspace_bytes, void *stream);
@@ -433,8 +437,8 @@ int qmm_gemv_q8(int kind, const void *P, const int8_t *codes, const float *scale
  * zeros.  An infinity in a row gives NaN at its place and zeros elsewhere, a NaN
  * gives a row of NaN.  sum and y may each be x or residual itself (same type and
  * stride) but not each other; other overlaps are not allowed.
- * Errors: a zero dimension, dtypes, then QMM_ERR_BAD_ARG: D > 32768, T * H *
- * D > 2^40 or T * H >= 2^31, eps negative or not finite, sum without residual,
+ * Errors: a zero dimension, dtypes, then QMM_ERR_BAD_ARG: D > 32768, H > 65536, T *
+ * H * D > 2^40 or T * H >= 2^31, eps negative or not finite, sum without residual,
  * sum equal to y, pointers, alignment to the elements, strides below H * D. */
 int qmm_rmsnorm(const void *x, int x_dtype, int64_t x_stride, const void *residual, int residual_dtype,
                 int64_t residual_stride, const float *weight, float eps, void *sum, int64_t sum_stride, void *y,

@@ -109,3 +109,15 @@ def test_eight_bits_of_subnormal_blocks():
         q, d = int8.quantize(np.full((1, 32), n, np.float32) * unit)
         k = round(float(d[0, 0]) / 2.0 ** -149)
         assert k == int(np.rint(np.float32(n) / np.float32(127))) and np.all(q == (min(127, round(n / k)) if k else 0))
+
+
+def test_norm_refuses_more_heads_than_it_names(lib):
+    f = lambda H: lib.qmm_rmsnorm(FAKE, 0, 4 * H, None, 0, 0, None, 1e-6, None, 0, FAKE + 2, 0, 4 * H, 1, H, 4, None)  # noqa: E731
+    assert f(65536) == f(65537) == ARG                       # y is misaligned: refused either way, by their own words
+    import gguf_block_quantized_kind_amd as qmm
+    f(65536)
+    assert b"aligned" in lib.qmm_last_error()
+    f(65537)
+    assert b"H=65537" in lib.qmm_last_error()
+    assert "H > 65536" in open(__import__("os").path.join(__import__("os").path.dirname(__import__("os").path.dirname(qmm.__file__)),
+                                                          "include", "qmm.h")).read()
