@@ -57,9 +57,9 @@ __device__ __forceinline__ float gelu_tanh(float v) {
 // the relative error was largest), where the exponential leaves f32's range; 3e-7 as it
 // is evaluated, 6.5e-7 with 2^x and the reciprocal each a step off.  The square is
 // taken in two parts, as its rounding alone would be y^2 / 2 steps of the result.
-// Against erfcf: gelu(product) * factor, 8192 tokens, 8192 x 4096 Q4_K 596 -> 560 us,
-// 2048 tokens, 14336 x 4096 309 -> 292; 499 tokens with a bias, 4096 x 4096 repacked Q8_0
-// 35.2 -> 33.6.
+// gelu(product) * factor, 8192 tokens, 8192 x 4096 Q4_K 581 us (546 without an activation;
+// erfcf took 6% longer), 2048 tokens, 14336 x 4096 299 (283); 499 tokens with a bias, 4096 x
+// 4096 repacked Q8_0 33.4 (32.8).
 __device__ __forceinline__ float gelu(float v) {
   constexpr float kC[10] = {-0.0219160002f, 0.0707042441f, -0.00149240822f, -0.226902843f, 0.213063121f,
                             0.00304379361f, 0.207221866f, 0.229145855f, 0.263853908f, 0.263278455f};

@@ -286,7 +286,10 @@ static hipError_t run_xk_x(const uint8_t *P, const void *x, int x_f16, const Epi
 // 12.4, 5120 x 5120 13.8 -> 12.9, 14336 x 4096 even.  (Repacked Q6_K 8192 x 4096 10.8
 // -> 11.4, Q8_0 11.6 -> 12.2.)
 //
-// Bound: 4096 x 14336 Q6_K is 48 MB, 9.4 us at a copy's rate; launch, first loads and
+// (All with operands from memory; where they stay in the 256 MB behind L2 the first takes
+// 15.6.)
+//
+// Bound: 4096 x 14336 Q6_K is 48 MB, 8.7 us at a large read's rate; launch, first loads and
 // the sums' meeting take 6 us of any call, the decoding 270 instructions a wave and
 // k-block.
 hipError_t launch_gemv_xk(int kind, const uint8_t *W, bool packed, const void *x, int x_f16, const Epilogue &y, int M, int64_t N,
