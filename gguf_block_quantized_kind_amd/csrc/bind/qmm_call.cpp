@@ -152,7 +152,13 @@ bool watched() {
 // A tensor beside `like`, which is on a GPU (0.13 us less each than through the dispatcher,
 // where nobody looks).
 at::Tensor make(const at::Tensor &like, at::IntArrayRef shape, at::ScalarType t) {
-  if (watched()) return at::empty(shape, at::TensorOptions().dtype(t).device(like.device()));
+  if (watched()) {
+    at::Tensor made = at::empty(shape, at::TensorOptions().dtype(t).device(like.device()));
+    if (made.device() != like.device() || made.scalar_type() != t || made.sizes() != shape || !made.is_contiguous())
+      raise(PyExc_TypeError, "a new tensor of ", shape, " ", t, " on ", like.device(), " came back as ", made.sizes(), " ",
+            made.scalar_type(), " on ", made.device());
+    return made;
+  }
   return at::Tensor(at::detail::empty_cuda(shape, t, like.device(), std::nullopt));
 }
 

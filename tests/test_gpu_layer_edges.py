@@ -202,3 +202,26 @@ def test_deterministic_fill_reaches_the_outputs():
         fills = sum(e.count for e in p.key_averages() if e.key == "aten::empty")
         assert fills >= n, (name, [e.key for e in p.key_averages()])
         assert all(torch.equal(a, b) for a, b in zip(got, want)), name
+
+
+def test_outputs_that_a_mode_replaces_are_looked_at():
+    """A mode that answers with a tensor the kernels cannot write to (on the host, of another type or shape) ends the
+    call; what the caller gives is looked at as before."""
+    from torch.utils._python_dispatch import TorchDispatchMode
+
+    class Replace(TorchDispatchMode):
+        def __init__(self, change):
+            super().__init__()
+            self.change = change
+
+        def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+            out = func(*args, **(kwargs or {}))
+            return self.change(out) if func.name().startswith("aten::empty") else out
+
+    changes = [lambda t: torch.zeros(t.shape, dtype=t.dtype), lambda t: t.double(), lambda t: t.reshape(-1)[:1],
+               lambda t: torch.zeros((*t.shape, 2), dtype=t.dtype, device=t.device)[..., 0]]
+    for name, call, _ in calls():
+        for i, change in enumerate(changes):
+            with Replace(change), pytest.raises(TypeError, match="new tensor"):
+                call()
+    torch.cuda.synchronize()
