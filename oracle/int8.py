@@ -52,6 +52,7 @@ def quantize(X) -> tuple[np.ndarray, np.ndarray]:
         r = (xb / d[:, :, None]).astype(np.float32)            # one f32 rounding
     q = np.where(d[:, :, None] > 0, np.rint(r), 0.0)           # ties to even
     q = np.clip(q, -127.0, 127.0)                              # beyond it only where d is subnormal
+    assert not np.any(np.isnan(q))                             # X is finite
     return q.astype(np.int8).reshape(M, K), d
 
 
